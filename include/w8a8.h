@@ -383,6 +383,163 @@ W8A8_API w8a8_status w8a8_fp8_kv_decode_attention(
     void* out, int out_dtype, void* workspace, size_t workspace_bytes, w8a8_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * A serving step over a 4-bit paged KV cache
+ *
+ * Four operators in the order a step calls them: block tables and slots of
+ * the step's tokens, the new keys and values into the cache, attention of
+ * the new tokens over the cache, and (for drafted tokens) their
+ * verification.  No counterpart on the source pages; they stand beside the
+ * fp8 cache and its attention above.  All are asynchronous, allocate
+ * nothing and can be captured in a CUDA graph.
+ *
+ * The cache holds K and V in 4 bits: groups of 16 consecutive dims of one
+ * head of one token share an e4m3 scale s, and an element stands for
+ * code * s * g with g the tensor's fp32 scale (k_scale, v_scale).  Codes are
+ * W8A8_KV4_E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and negatives) or W8A8_KV4_INT4
+ * (-7..7, two's complement).  An element takes 0.5625 bytes.
+ *
+ * Layout: [num_blocks, num_kv_heads, block_size / 16] records of 16 tokens,
+ * each of 18 * head_dim bytes: K codes [16, head_dim / 2] (even dim in the
+ * low half of a byte), K scales [16, head_dim / 16], V codes, V scales.
+ * block_size is a multiple of 16, head_dim is 64 or 128, the base is 16-byte
+ * aligned.  Token t of a block of slot numbers block * block_size + t.
+ * ---------------------------------------------------------------------- */
+enum { W8A8_KV4_E2M1 = 0, W8A8_KV4_INT4 = 1 };
+
+/* Bytes of a cache (0 for sizes outside the limits). */
+W8A8_API size_t w8a8_kv4_cache_bytes(int64_t num_blocks, int64_t num_kv_heads, int64_t block_size,
+                                     int64_t head_dim);
+
+/* Writes keys and values of `tokens` tokens at their slots.  With
+ * a = max |x| over a group (NaN ignored) and M the largest code (6 or 7):
+ *   s = e4m3(min(max(a / (M * g), 2^-9), 448)),  code = round(x / (s * g)),
+ * both divisions correctly rounded in fp32, rounding half to even, codes
+ * saturating; a NaN element becomes code 0.
+ *   k, v     [tokens, num_kv_heads, head_dim] bf16 or fp16 (dtype), a head's
+ *            dims consecutive, token and head strides in elements: views of
+ *            a merged projection's output are fine.
+ *   slots    int64 [tokens]; a slot outside the cache is skipped.  No slot
+ *            twice in a call.
+ *   k_scale, v_scale  fp32 [1], positive and finite.
+ * Alignment: k and v need 2 bytes; 16-byte aligned bases and strides take
+ * the vectorised path.  Limits: 1 <= tokens, num_kv_heads, num_blocks;
+ * tokens * num_kv_heads * head_dim < 2^40. */
+W8A8_API w8a8_status w8a8_kv4_cache_write(const void* k, const void* v, int dtype, int64_t tokens,
+                                          int64_t num_kv_heads, int64_t head_dim, int64_t k_token_stride,
+                                          int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                                          void* cache, int64_t num_blocks, int64_t block_size,
+                                          const int64_t* slots, const float* k_scale, const float* v_scale,
+                                          int kind, w8a8_stream_t stream);
+
+/* The inverse: k, v = round16((code * s) * g) of the tokens at `slots`, zeros
+ * for a slot outside the cache.  Arguments as above, k and v written. */
+W8A8_API w8a8_status w8a8_kv4_cache_read(const void* cache, int64_t num_blocks, int64_t block_size,
+                                         const int64_t* slots, const float* k_scale, const float* v_scale,
+                                         int kind, void* k, void* v, int dtype, int64_t tokens,
+                                         int64_t num_kv_heads, int64_t head_dim, int64_t k_token_stride,
+                                         int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                                         w8a8_stream_t stream);
+
+/* Block tables, slots and positions of a step's tokens, built on the GPU.
+ * Request b holds context_lens[b] tokens and adds new_lens[b] (negative
+ * numbers count as 0).  Its new blocks, need_b = ceil((context + new) /
+ * block_size) - ceil(context / block_size) of them, come from the end of the
+ * free list in request order: with before_b the needs of the requests in
+ * front of it, entry ceil(context / block_size) + i of its table becomes
+ * free_blocks[free_count - 1 - before_b - i].  A request whose tokens would
+ * not fit max_blocks blocks is refused and needs nothing; one whose need
+ * goes past free_count (before_b + need_b > free_count, need_b > 0) is
+ * refused too, and so is then every later one that needs a block.
+ *   free_count    int32 [1] on the device, at most free_capacity ids.
+ *   block_table   int32 [batch, max_blocks]; only new entries are written.
+ *   query_start   int32 [batch + 1], prefix sums of new_lens (refused
+ *                 requests' tokens keep their place in the packed order).
+ *   seq_lens      int32 [batch], context + new, 0 for a refused request.
+ *   slots, positions  int64 / int32 [tokens]: block * block_size + offset,
+ *                 or -1 for tokens of refused requests, of context blocks
+ *                 whose entry is negative, and past the last new token
+ *                 (padding of a captured step); context + i, or 0 for
+ *                 padding.  tokens must hold every new token: blocks are
+ *                 entered by their first token.
+ *   free_left     int32 [1], the balance: free_count less the needs of
+ *                 every request up to the last admitted one.  Refused requests
+ *                 among them count as waiting for their blocks, so that a
+ *                 negative number says how many blocks the list was short.
+ *   free_count_out  int32 [1] or NULL: the number of ids that are still free,
+ *                 free_blocks[0 .. free_count_out - 1] (the next call's
+ *                 free_count).  Neither may alias free_count.
+ * The inputs are not changed, so a call can be repeated.  Limits:
+ * 1 <= batch <= 16384, the sum of new_lens below 2^31. */
+W8A8_API w8a8_status w8a8_build_block_tables(const int32_t* context_lens, const int32_t* new_lens,
+                                             int64_t batch, const int32_t* free_blocks,
+                                             const int32_t* free_count, int64_t free_capacity,
+                                             int32_t* block_table, int64_t max_blocks, int64_t block_size,
+                                             int32_t* query_start, int32_t* seq_lens, int64_t* slots,
+                                             int32_t* positions, int64_t tokens, int32_t* free_left,
+                                             int32_t* free_count_out, w8a8_stream_t stream);
+
+/* Attention of new tokens over the cache (their own K and V already in it).
+ * Request b's new tokens are rows query_start[b] .. query_start[b + 1] - 1 of
+ * q; row i of its n sees the tokens t <= seq_lens[b] - n + i:
+ *   s_t = sm_scale * sum_d q[i,h,d] K[t,d],  out[i,h,:] = sum_t softmax(s)_t V[t,:]
+ * for every query head h, KV head h / (num_q_heads / num_kv_heads).  A row
+ * that sees no token gives zeros.
+ *   q, out      [tokens, num_q_heads, head_dim] bf16 / fp16, a head's dims
+ *               consecutive, token and head strides in elements.
+ *   block_table int32 [batch, max_blocks]; tokens of a block whose id is
+ *               outside [0, num_blocks) are not attended to.
+ *   seq_lens    int32 [batch], clamped to [0, max_blocks * block_size].
+ *   query_start int32 [batch + 1], clamped to [0, tokens]; NULL: one token
+ *               a request (tokens = batch).
+ *   max_query_len  the largest n (rows of a request past it are not
+ *               written).
+ *   workspace   w8a8_kv4_attention_workspace_size() bytes, 16-byte aligned,
+ *               zero-filled before its first use; every call leaves its
+ *               counters zero again.  Calls that may overlap on the GPU
+ *               need workspaces of their own.
+ * Scores, softmax statistics and sums are fp32; the softmax weights enter the
+ * second product as f16 (11 bits).  Limits: num_q_heads a multiple of
+ * num_kv_heads with a quotient of at most 64; max_blocks * block_size < 2^31;
+ * batch and head counts <= 65535.  The workspace size is 0 for sizes outside
+ * the limits. */
+W8A8_API size_t w8a8_kv4_attention_workspace_size(int64_t batch, int64_t max_query_len, int64_t num_q_heads,
+                                                  int64_t num_kv_heads, int64_t head_dim);
+
+W8A8_API w8a8_status w8a8_kv4_attention(
+    const void* q, int q_dtype, int64_t tokens, int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
+    int64_t q_token_stride, int64_t q_head_stride, const void* cache, int64_t num_blocks, int64_t block_size,
+    const int32_t* block_table, int64_t max_blocks, const int32_t* seq_lens, const int32_t* query_start,
+    int64_t batch, int64_t max_query_len, const float* k_scale, const float* v_scale, float sm_scale, int kind,
+    void* out, int out_dtype, int64_t out_token_stride, int64_t out_head_stride, void* workspace,
+    size_t workspace_bytes, w8a8_stream_t stream);
+
+/* Verification of drafted tokens.  Request b drafted n tokens x_i (rows
+ * draft_start[b] + i of draft_tokens, draft_probs and uniform); the target's
+ * probabilities p_0 .. p_n are rows draft_start[b] + b + i of target_probs.
+ * Token i is kept while uniform_i * q_i(x_i) < p_i(x_i).  At the first token j
+ * not kept a replacement is drawn from max(p_j - q_j, 0) (from p_j if that is
+ * zero everywhere), with all kept an extra token from p_n: the lowest v whose
+ * running sum exceeds sample_uniform[b] times the total.
+ *   target_probs, draft_probs  fp32, bf16 or fp16 (one dtype), rows of vocab
+ *                numbers, leading dimensions in elements.  They need not sum
+ *                to 1; negative numbers and NaN count as 0.  draft_probs NULL:
+ *                the draft gave its tokens alone (q(x) = 1 at the token).
+ *   draft_tokens int32 [rows]; one outside [0, vocab) is not kept.
+ *   draft_start  int32 [batch + 1], clamped to [0, rows]; at most max_drafts
+ *                tokens of a request are looked at.
+ *   uniform      fp32 [rows], sample_uniform fp32 [batch], in [0, 1).
+ *   out_tokens   int32 [batch, max_drafts + 1]: kept tokens, the drawn one
+ *                (-1 if no token has any probability), then -1.
+ *   num_accepted int32 [batch], the number kept.
+ * Comparisons and sums are made in 64 bits. */
+W8A8_API w8a8_status w8a8_verify_drafts(const void* target_probs, const void* draft_probs, int dtype,
+                                        int64_t vocab, int64_t target_ld, int64_t draft_ld,
+                                        const int32_t* draft_tokens, const int32_t* draft_start, int64_t batch,
+                                        int64_t rows, const float* uniform, const float* sample_uniform,
+                                        int32_t* out_tokens, int64_t max_drafts, int32_t* num_accepted,
+                                        w8a8_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Scaled matmul without a caller-provided workspace
  *
  * No counterpart on the source pages: this entry point exists for callers

@@ -16,6 +16,7 @@ E4M3, INT8, BF16, FP16, FP32, INT32 = 0, 1, 2, 3, 4, 5
 PER_TENSOR, PER_ROW = 0, 1
 DYNAMIC, STATIC = 0, 1
 REDUCE_AUTO, REDUCE_GLOBAL, REDUCE_CLUSTER = 0, 1, 2
+KV4_KINDS = {"e2m1": 0, "int4": 1}
 ROUTES = {"auto": 0, "one_kernel": 1, "two_step": 2}
 
 STATUS_NAMES = {
@@ -50,6 +51,13 @@ EXPORTS = (
     "w8a8_quant_scaled_mm",
     "w8a8_fp8_kv_attention_workspace_size",
     "w8a8_fp8_kv_decode_attention",
+    "w8a8_kv4_cache_bytes",
+    "w8a8_kv4_cache_write",
+    "w8a8_kv4_cache_read",
+    "w8a8_build_block_tables",
+    "w8a8_kv4_attention_workspace_size",
+    "w8a8_kv4_attention",
+    "w8a8_verify_drafts",
 )
 
 
@@ -127,6 +135,21 @@ def load(build_if_needed: bool = True):
         lib.w8a8_fp8_kv_decode_attention.restype = I
         lib.w8a8_fp8_kv_decode_attention.argtypes = [P, I, I64, I64, I64, I64, P, P, I64, P, I64, I64, I64,
                                                      P, P, P, ctypes.c_float, P, I, P, SZ, P]
+        lib.w8a8_kv4_cache_bytes.restype = SZ
+        lib.w8a8_kv4_cache_bytes.argtypes = [I64, I64, I64, I64]
+        lib.w8a8_kv4_cache_write.restype = I
+        lib.w8a8_kv4_cache_write.argtypes = [P, P, I, I64, I64, I64, I64, I64, I64, I64, P, I64, I64, P, P, P, I, P]
+        lib.w8a8_kv4_cache_read.restype = I
+        lib.w8a8_kv4_cache_read.argtypes = [P, I64, I64, P, P, P, I, P, P, I, I64, I64, I64, I64, I64, I64, I64, P]
+        lib.w8a8_build_block_tables.restype = I
+        lib.w8a8_build_block_tables.argtypes = [P, P, I64, P, P, I64, P, I64, I64, P, P, P, P, I64, P, P, P]
+        lib.w8a8_kv4_attention_workspace_size.restype = SZ
+        lib.w8a8_kv4_attention_workspace_size.argtypes = [I64, I64, I64, I64, I64]
+        lib.w8a8_kv4_attention.restype = I
+        lib.w8a8_kv4_attention.argtypes = [P, I, I64, I64, I64, I64, I64, I64, P, I64, I64, P, I64, P, P, I64, I64,
+                                           P, P, ctypes.c_float, I, P, I, I64, I64, P, SZ, P]
+        lib.w8a8_verify_drafts.restype = I
+        lib.w8a8_verify_drafts.argtypes = [P, P, I, I64, I64, I64, P, P, I64, I64, P, P, P, I64, P, P]
         lib.w8a8_device_status.restype = I
         lib.w8a8_device_status.argtypes = [ctypes.POINTER(ctypes.c_int)]
         _lib = lib

@@ -29,6 +29,8 @@ __all__ = [
     "scaled_quant", "scaled_dequant", "scaled_mm", "mm_workspace_size",
     "quant_workspace_size", "pick_config", "device_status", "Workspace", "quant_scaled_mm",
     "expand_shard_scales", "requant_shards", "fp8_kv_decode_attention", "attention_workspace_size",
+    "kv4_cache_shape", "kv4_cache_write", "kv4_cache_read", "build_block_tables", "kv4_attention",
+    "kv4_attention_workspace_size", "verify_drafts",
     "W8A8Error", "MmConfig",
 ]
 
@@ -378,3 +380,221 @@ def fp8_kv_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
         _ptr(q), _fkind(q), batch, hq, hkv, d, _ptr(k_cache), _ptr(v_cache), max_seq, bt, bsz, maxb, nblk,
         _ptr(seq_lens), _ptr(k_scale), _ptr(v_scale), float(sm_scale), _ptr(out), _fkind(out),
         _ptr(wbuf), wbuf.numel(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- a serving step over a 4-bit paged KV cache
+
+
+def kv4_cache_shape(num_blocks: int, num_kv_heads: int, block_size: int, head_dim: int) -> tuple:
+    """Shape of a 4-bit cache, a contiguous uint8 tensor: [num_blocks,
+    num_kv_heads, block_size / 16, 18 * head_dim], one record of 16 tokens'
+    keys and values (codes and group scales) in the last dimension."""
+    if _lib.load().w8a8_kv4_cache_bytes(num_blocks, num_kv_heads, block_size, head_dim) == 0:
+        raise ValueError("block_size must be a multiple of 16, head_dim 64 or 128, counts >= 1")
+    return (num_blocks, num_kv_heads, block_size // 16, 18 * head_dim)
+
+
+def _kv4_cache(cache: torch.Tensor) -> tuple:
+    """(num_blocks, num_kv_heads, block_size, head_dim) of a cache tensor."""
+    if cache.dtype != torch.uint8 or cache.dim() != 4 or not cache.is_contiguous() or cache.shape[3] % 18:
+        raise ValueError("the cache must be a contiguous uint8 tensor of kv4_cache_shape()")
+    nb, h, records, nbytes = cache.shape
+    return nb, h, 16 * records, nbytes // 18
+
+
+def _kv4_kind(kind: str) -> int:
+    if kind not in _lib.KV4_KINDS:
+        raise ValueError(f"kind must be one of {sorted(_lib.KV4_KINDS)}")
+    return _lib.KV4_KINDS[kind]
+
+
+def _ints(name: str, t: torch.Tensor, n: int | None, dtype=torch.int32) -> None:
+    if t.dtype != dtype or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.numel() != n):
+        size = "" if n is None else f" of {n} entries"
+        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} vector{size}")
+
+
+def _one_scale(*ts: torch.Tensor) -> None:
+    for t in ts:
+        if t.dtype != torch.float32 or t.numel() != 1:
+            raise ValueError("k_scale and v_scale must be float32 tensors of one element")
+
+
+def _heads(name: str, t: torch.Tensor, shape: tuple) -> tuple:
+    """Token and head strides of a [tokens, heads, head_dim] tensor."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    if t.stride(2) != 1 and t.shape[2] > 1:
+        raise ValueError(f"the dims of a head of {name} must be consecutive (stride(2) == 1)")
+    return t.stride(0), t.stride(1)
+
+
+def _kv4_tokens(k, v, cache, slots, k_scale, v_scale, kind) -> tuple:
+    _cuda(k, v, cache, slots, k_scale, v_scale)
+    nb, h, bs, d = _kv4_cache(cache)
+    if k.dim() != 3:
+        raise ValueError("k and v must be [tokens, num_kv_heads, head_dim]")
+    shape = (k.shape[0], h, d)
+    ks, vs = _heads("k", k, shape), _heads("v", v, shape)
+    if v.dtype != k.dtype:
+        raise TypeError("k and v must have the same element type")
+    _ints("slots", slots, shape[0], torch.int64)
+    _one_scale(k_scale, v_scale)
+    return nb, bs, (_fkind(k), *shape, *ks, *vs), _kv4_kind(kind)
+
+
+def kv4_cache_write(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor,
+                    k_scale: torch.Tensor, v_scale: torch.Tensor, kind: str = "e2m1", stream=None) -> None:
+    """Quantise new keys and values to 4 bits and write them at their slots.
+
+    k, v: [tokens, num_kv_heads, head_dim] bf16 / fp16, any token and head
+    strides.  cache: uint8 of kv4_cache_shape().  slots: int64 [tokens]
+    (block * block_size + offset; one outside the cache is skipped).
+    k_scale, v_scale: float32 [1], the tensors' scales: with absmax / (6 * 448)
+    (e2m1) or absmax / (7 * 448) (int4) of the values met, no group saturates.
+    kind: "e2m1" or "int4"."""
+    nb, bs, sizes, kd = _kv4_tokens(k, v, cache, slots, k_scale, v_scale, kind)
+    if k.shape[0] == 0:
+        return
+    check(_lib.load().w8a8_kv4_cache_write(_ptr(k), _ptr(v), *sizes, _ptr(cache), nb, bs, _ptr(slots), _ptr(k_scale),
+                                           _ptr(v_scale), kd, _stream(stream)))
+
+
+def kv4_cache_read(cache: torch.Tensor, slots: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                   k: torch.Tensor, v: torch.Tensor, kind: str = "e2m1", stream=None) -> None:
+    """The values that the tokens at `slots` stand for, into k and v (bf16 /
+    fp16 [tokens, num_kv_heads, head_dim]); zeros for a slot outside the
+    cache.  Arguments as for kv4_cache_write."""
+    nb, bs, sizes, kd = _kv4_tokens(k, v, cache, slots, k_scale, v_scale, kind)
+    if k.shape[0] == 0:
+        return
+    check(_lib.load().w8a8_kv4_cache_read(_ptr(cache), nb, bs, _ptr(slots), _ptr(k_scale), _ptr(v_scale), kd,
+                                          _ptr(k), _ptr(v), *sizes, _stream(stream)))
+
+
+def build_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_blocks: torch.Tensor,
+                       free_count: torch.Tensor, block_table: torch.Tensor, block_size: int,
+                       query_start: torch.Tensor, seq_lens: torch.Tensor, slots: torch.Tensor,
+                       positions: torch.Tensor, free_left: torch.Tensor, free_count_out: torch.Tensor | None = None,
+                       stream=None) -> None:
+    """Block tables, slots and positions of a step's tokens, on the GPU.
+
+    context_lens, new_lens: int32 [batch], the tokens each request holds and
+    adds.  free_blocks: int32 ids, of which the first free_count[0] (int32
+    [1]) are free; blocks are taken from the end, in request order.
+    Written: the new entries of block_table (int32 [batch, max_blocks]),
+    query_start (int32 [batch + 1]), seq_lens (int32 [batch]; 0 for a request
+    that its table or the free list has no room for), slots (int64) and
+    positions (int32) of the packed tokens (-1 and 0 past the last one, -1 for
+    a refused request's), free_left (int32 [1], the balance: free_count less
+    the needs up to the last admitted request, negative by the blocks that the
+    list was short) and free_count_out (int32 [1], optional: the ids still
+    free, the next call's free_count)."""
+    _cuda(context_lens, new_lens, free_blocks, free_count, block_table, query_start, seq_lens, slots, positions,
+          free_left, free_count_out)
+    if block_table.dim() != 2 or block_table.dtype != torch.int32 or not block_table.is_contiguous():
+        raise ValueError("block_table must be a contiguous int32 [batch, max_blocks] tensor")
+    batch, max_blocks = block_table.shape
+    _ints("context_lens", context_lens, batch)
+    _ints("new_lens", new_lens, batch)
+    _ints("free_blocks", free_blocks, None)
+    _ints("free_count", free_count, 1)
+    _ints("query_start", query_start, batch + 1)
+    _ints("seq_lens", seq_lens, batch)
+    _ints("slots", slots, None, torch.int64)
+    _ints("positions", positions, slots.numel())
+    _ints("free_left", free_left, 1)
+    if free_count_out is not None:
+        _ints("free_count_out", free_count_out, 1)
+    check(_lib.load().w8a8_build_block_tables(
+        _ptr(context_lens), _ptr(new_lens), batch, _ptr(free_blocks), _ptr(free_count), free_blocks.numel(),
+        _ptr(block_table), max_blocks, block_size, _ptr(query_start), _ptr(seq_lens), _ptr(slots), _ptr(positions),
+        slots.numel(), _ptr(free_left), _ptr(free_count_out), _stream(stream)))
+
+
+def kv4_attention_workspace_size(batch: int, max_query_len: int, num_q_heads: int, num_kv_heads: int,
+                                 head_dim: int) -> int:
+    return int(_lib.load().w8a8_kv4_attention_workspace_size(batch, max_query_len, num_q_heads, num_kv_heads, head_dim))
+
+
+def kv4_attention(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor,
+                  k_scale: torch.Tensor, v_scale: torch.Tensor, out: torch.Tensor,
+                  query_start: torch.Tensor | None = None, max_query_len: int = 1, sm_scale: float | None = None,
+                  kind: str = "e2m1", workspace=None, stream=None) -> None:
+    """Attention of new tokens over a 4-bit paged cache that holds their keys
+    and values already.
+
+    q, out: [tokens, num_q_heads, head_dim] bf16 / fp16, any token and head
+    strides.  seq_lens: int32 [batch], lengths with the new tokens.
+    block_table: int32 [batch, max_blocks].  query_start: int32 [batch + 1],
+    the first row of each request in q, with max_query_len the most rows of
+    one; None: one row a request.  Row i of a request's n sees its tokens
+    t <= seq_len - n + i; a row that sees none gives zeros.  sm_scale defaults
+    to 1 / sqrt(head_dim)."""
+    _cuda(q, cache, seq_lens, block_table, k_scale, v_scale, out, query_start)
+    lib = _lib.load()
+    nb, hkv, bs, d = _kv4_cache(cache)
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError("q must be [tokens, num_q_heads, head_dim] with the cache's head_dim")
+    tokens, hq = q.shape[0], q.shape[1]
+    qs, os_ = _heads("q", q, tuple(q.shape)), _heads("out", out, tuple(q.shape))
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
+        raise ValueError("block_table must be a contiguous int32 [batch, max_blocks] tensor")
+    batch, max_blocks = block_table.shape
+    _ints("seq_lens", seq_lens, batch)
+    if query_start is not None:
+        _ints("query_start", query_start, batch + 1)
+    _one_scale(k_scale, v_scale)
+    kd = _kv4_kind(kind)
+    if tokens == 0:
+        return
+    need = lib.w8a8_kv4_attention_workspace_size(batch, max_query_len, hq, hkv, d)
+    if isinstance(workspace, Workspace):
+        wbuf = workspace.ensure(need).buf
+    elif workspace is None:
+        wbuf = _default_workspace(q.device, need, "kv4_attention").buf
+    else:
+        wbuf = workspace
+    if sm_scale is None:
+        sm_scale = 1.0 / float(d) ** 0.5
+    check(lib.w8a8_kv4_attention(
+        _ptr(q), _fkind(q), tokens, hq, hkv, d, *qs, _ptr(cache), nb, bs, _ptr(block_table), max_blocks,
+        _ptr(seq_lens), _ptr(query_start), batch, max_query_len, _ptr(k_scale), _ptr(v_scale), float(sm_scale), kd,
+        _ptr(out), _fkind(out), *os_, _ptr(wbuf), wbuf.numel() * wbuf.element_size(), _stream(stream)))
+
+
+def verify_drafts(target_probs: torch.Tensor, draft_probs: torch.Tensor | None, draft_tokens: torch.Tensor,
+                  draft_start: torch.Tensor, uniform: torch.Tensor, sample_uniform: torch.Tensor,
+                  out_tokens: torch.Tensor, num_accepted: torch.Tensor, stream=None) -> None:
+    """Accept drafted tokens against the target's probabilities, and draw the
+    token after the last accepted one.
+
+    target_probs: [rows + batch, vocab] fp32 / bf16 / fp16, rows contiguous:
+    n + 1 rows for a request of n drafts.  draft_probs: [rows, vocab] of the
+    same type, or None for a draft that gave its tokens alone.  draft_tokens:
+    int32 [rows]; draft_start: int32 [batch + 1], the first drafted row of
+    each request.  uniform: float32 [rows] and sample_uniform: float32 [batch],
+    random numbers in [0, 1).  Written: out_tokens, int32 [batch,
+    max_drafts + 1] (accepted tokens, the drawn one, then -1), and
+    num_accepted, int32 [batch]."""
+    _cuda(target_probs, draft_probs, draft_tokens, draft_start, uniform, sample_uniform, out_tokens, num_accepted)
+    if out_tokens.dtype != torch.int32 or out_tokens.dim() != 2 or not out_tokens.is_contiguous():
+        raise ValueError("out_tokens must be a contiguous int32 [batch, max_drafts + 1] tensor")
+    batch, rows = out_tokens.shape[0], draft_tokens.numel()
+    vocab = target_probs.shape[1] if target_probs.dim() == 2 else 0
+    if target_probs.dim() != 2 or target_probs.shape[0] != rows + batch:
+        raise ValueError("target_probs must be [rows + batch, vocab]")
+    if draft_probs is not None and tuple(draft_probs.shape) != (rows, vocab):
+        raise ValueError("draft_probs must be [rows, vocab]")
+    if draft_probs is not None and draft_probs.dtype != target_probs.dtype:
+        raise TypeError("target_probs and draft_probs must have the same element type")
+    _ints("draft_tokens", draft_tokens, rows)
+    _ints("draft_start", draft_start, batch + 1)
+    _ints("uniform", uniform, rows, torch.float32)
+    _ints("sample_uniform", sample_uniform, batch, torch.float32)
+    _ints("num_accepted", num_accepted, batch)
+    check(_lib.load().w8a8_verify_drafts(
+        _ptr(target_probs), _ptr(draft_probs), FP32 if target_probs.dtype == torch.float32 else _fkind(target_probs),
+        vocab, _ld(target_probs), vocab if draft_probs is None else _ld(draft_probs), _ptr(draft_tokens),
+        _ptr(draft_start), batch, rows, _ptr(uniform), _ptr(sample_uniform), _ptr(out_tokens),
+        out_tokens.shape[1] - 1, _ptr(num_accepted), _stream(stream)))

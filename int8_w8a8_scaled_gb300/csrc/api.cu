@@ -12,6 +12,7 @@
 #include <algorithm>
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 #include <atomic>
 #include <mutex>
 #include <string>
@@ -954,6 +955,285 @@ w8a8_status w8a8_fp8_kv_decode_attention(const void* q, int q_dtype, int64_t bat
   cudaError_t e = w8a8::launch_fp8kv_attention(p, tma ? &mk : nullptr, tma ? &mv : nullptr,
                                                reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "fp8 KV attention launch");
+  return ok();
+}
+
+namespace {
+
+w8a8_status kv4_sizes(int64_t num_blocks, int64_t num_kv_heads, int64_t block_size, int64_t head_dim, int kind) {
+  if (kind != W8A8_KV4_E2M1 && kind != W8A8_KV4_INT4) return fail(W8A8_ERR_INVALID_ARG, "kind must be KV4_E2M1 or KV4_INT4");
+  if (num_blocks < 1 || num_kv_heads < 1 || block_size < 1)
+    return fail(W8A8_ERR_INVALID_ARG, "num_blocks, num_kv_heads and block_size must be >= 1");
+  if (head_dim != 64 && head_dim != 128) return fail(W8A8_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (block_size % 16 != 0) return fail(W8A8_ERR_UNSUPPORTED, "block_size must be a multiple of 16");
+  if (num_kv_heads > 65535 || block_size > (1 << 20) || num_blocks >= (1LL << 31))
+    return fail(W8A8_ERR_UNSUPPORTED, "cache sizes out of range");
+  return W8A8_OK;
+}
+
+w8a8_status kv4_cache_call(bool write, const void* k, const void* v, int dtype, int64_t tokens, int64_t num_kv_heads,
+                           int64_t head_dim, int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                           int64_t v_head_stride, const void* cache, int64_t num_blocks, int64_t block_size,
+                           const int64_t* slots, const float* k_scale, const float* v_scale, int kind,
+                           w8a8_stream_t stream) {
+  if (!k || !v || !cache || !slots || !k_scale || !v_scale) return fail(W8A8_ERR_INVALID_ARG, "null pointer argument");
+  if (dtype != W8A8_BF16 && dtype != W8A8_FP16) return fail(W8A8_ERR_INVALID_ARG, "k and v must be BF16 or FP16");
+  w8a8_status st = kv4_sizes(num_blocks, num_kv_heads, block_size, head_dim, kind);
+  if (st != W8A8_OK) return st;
+  if (tokens < 1) return fail(W8A8_ERR_INVALID_ARG, "tokens must be >= 1");
+  if (tokens >= (1LL << 40) / (num_kv_heads * head_dim)) return fail(W8A8_ERR_UNSUPPORTED, "too many tokens");
+  if (k_token_stride < 0 || k_head_stride < 0 || v_token_stride < 0 || v_head_stride < 0)
+    return fail(W8A8_ERR_INVALID_ARG, "strides must not be negative");
+  if (!write && ((tokens > 1 && (k_token_stride < head_dim || v_token_stride < head_dim)) ||
+                 (num_kv_heads > 1 && (k_head_stride < head_dim || v_head_stride < head_dim))))
+    return fail(W8A8_ERR_INVALID_ARG, "strides of an output must be at least head_dim");
+  if (!aligned(cache, 16)) return fail(W8A8_ERR_MISALIGNED, "the cache must be 16-byte aligned");
+  if (!aligned(k, 2) || !aligned(v, 2) || !aligned(slots, 8) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+    return fail(W8A8_ERR_MISALIGNED, "misaligned k, v, slots or scale pointer");
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != W8A8_OK) return st;
+  w8a8::Kv4CacheArgs a{};
+  if (write) {
+    a.k = k;
+    a.v = v;
+  } else {
+    a.k_out = const_cast<void*>(k);
+    a.v_out = const_cast<void*>(v);
+  }
+  a.k_token_stride = k_token_stride;
+  a.k_head_stride = k_head_stride;
+  a.v_token_stride = v_token_stride;
+  a.v_head_stride = v_head_stride;
+  a.fp16 = dtype == W8A8_FP16;
+  a.vec = aligned(k, 16) && aligned(v, 16) && (k_token_stride | k_head_stride | v_token_stride | v_head_stride) % 8 == 0;
+  a.cache = const_cast<void*>(cache);
+  a.num_blocks = num_blocks;
+  a.block_size = static_cast<int>(block_size);
+  a.heads = static_cast<int>(num_kv_heads);
+  a.head_dim = static_cast<int>(head_dim);
+  a.slots = slots;
+  a.tokens = tokens;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.kind = kind;
+  cudaError_t e = w8a8::launch_kv4_cache(a, write, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, write ? "KV cache write launch" : "KV cache read launch");
+  return ok();
+}
+
+}  // namespace
+
+size_t w8a8_kv4_cache_bytes(int64_t num_blocks, int64_t num_kv_heads, int64_t block_size, int64_t head_dim) {
+  if (kv4_sizes(num_blocks, num_kv_heads, block_size, head_dim, W8A8_KV4_E2M1) != W8A8_OK) return 0;
+  const size_t record = 18 * static_cast<size_t>(head_dim) * static_cast<size_t>(block_size / 16) *
+                        static_cast<size_t>(num_kv_heads);  // below 2^45
+  if (record > (size_t(1) << 62) / static_cast<size_t>(num_blocks)) return 0;
+  t_last_error.clear();
+  return record * static_cast<size_t>(num_blocks);
+}
+
+w8a8_status w8a8_kv4_cache_write(const void* k, const void* v, int dtype, int64_t tokens, int64_t num_kv_heads,
+                                 int64_t head_dim, int64_t k_token_stride, int64_t k_head_stride,
+                                 int64_t v_token_stride, int64_t v_head_stride, void* cache, int64_t num_blocks,
+                                 int64_t block_size, const int64_t* slots, const float* k_scale, const float* v_scale,
+                                 int kind, w8a8_stream_t stream) {
+  return kv4_cache_call(true, k, v, dtype, tokens, num_kv_heads, head_dim, k_token_stride, k_head_stride,
+                        v_token_stride, v_head_stride, cache, num_blocks, block_size, slots, k_scale, v_scale, kind,
+                        stream);
+}
+
+w8a8_status w8a8_kv4_cache_read(const void* cache, int64_t num_blocks, int64_t block_size, const int64_t* slots,
+                                const float* k_scale, const float* v_scale, int kind, void* k, void* v, int dtype,
+                                int64_t tokens, int64_t num_kv_heads, int64_t head_dim, int64_t k_token_stride,
+                                int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                                w8a8_stream_t stream) {
+  return kv4_cache_call(false, k, v, dtype, tokens, num_kv_heads, head_dim, k_token_stride, k_head_stride,
+                        v_token_stride, v_head_stride, cache, num_blocks, block_size, slots, k_scale, v_scale, kind,
+                        stream);
+}
+
+w8a8_status w8a8_build_block_tables(const int32_t* context_lens, const int32_t* new_lens, int64_t batch,
+                                    const int32_t* free_blocks, const int32_t* free_count, int64_t free_capacity,
+                                    int32_t* block_table, int64_t max_blocks, int64_t block_size,
+                                    int32_t* query_start, int32_t* seq_lens, int64_t* slots, int32_t* positions,
+                                    int64_t tokens, int32_t* free_left, int32_t* free_count_out,
+                                    w8a8_stream_t stream) {
+  if (!context_lens || !new_lens || (!free_blocks && free_capacity > 0) || !free_count || !block_table || !query_start || !seq_lens ||
+      !slots || !positions || !free_left)
+    return fail(W8A8_ERR_INVALID_ARG, "null pointer argument");
+  if (batch < 1 || max_blocks < 1 || block_size < 1 || tokens < 1 || free_capacity < 0)
+    return fail(W8A8_ERR_INVALID_ARG, "batch, max_blocks, block_size and tokens must be >= 1, free_capacity >= 0");
+  if (batch > w8a8::kMaxTableBatch) return fail(W8A8_ERR_UNSUPPORTED, "batch must be at most %d", w8a8::kMaxTableBatch);
+  if (block_size > (1 << 20) || max_blocks >= (1LL << 31) / block_size || tokens >= (1LL << 31) ||
+      free_capacity >= (1LL << 31))
+    return fail(W8A8_ERR_UNSUPPORTED, "max_blocks * block_size, tokens and free_capacity must be below 2^31");
+  if (free_left == free_count || free_count_out == free_count || free_left == free_count_out)
+    return fail(W8A8_ERR_INVALID_ARG, "free_count, free_left and free_count_out must be different words");
+  for (const void* ptr : {static_cast<const void*>(context_lens), static_cast<const void*>(new_lens),
+                          static_cast<const void*>(free_blocks), static_cast<const void*>(free_count),
+                          static_cast<const void*>(block_table), static_cast<const void*>(query_start),
+                          static_cast<const void*>(seq_lens), static_cast<const void*>(positions),
+                          static_cast<const void*>(free_left), static_cast<const void*>(free_count_out)})
+    if (!aligned(ptr, 4)) return fail(W8A8_ERR_MISALIGNED, "int32 arrays must be 4-byte aligned");
+  if (!aligned(slots, 8)) return fail(W8A8_ERR_MISALIGNED, "slots must be 8-byte aligned");
+  w8a8_status st;
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != W8A8_OK) return st;
+  w8a8::BlockTableArgs a{};
+  a.context_lens = context_lens;
+  a.new_lens = new_lens;
+  a.batch = static_cast<int>(batch);
+  a.free_blocks = free_blocks;
+  a.free_count = free_count;
+  a.free_capacity = static_cast<int>(free_capacity);
+  a.block_table = block_table;
+  a.max_blocks = static_cast<int>(max_blocks);
+  a.block_size = static_cast<int>(block_size);
+  a.query_start = query_start;
+  a.seq_lens = seq_lens;
+  a.slots = slots;
+  a.positions = positions;
+  a.tokens = tokens;
+  a.free_left = free_left;
+  a.free_count_out = free_count_out;
+  cudaError_t e = w8a8::launch_block_tables(a, dev.sms, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "block table launch");
+  return ok();
+}
+
+namespace {
+
+// Sizes of an attention call over the 4-bit cache.
+w8a8_status kv4_attention_sizes(int64_t batch, int64_t max_query_len, int64_t num_q_heads, int64_t num_kv_heads,
+                                int64_t head_dim) {
+  if (batch < 1 || max_query_len < 1 || num_q_heads < 1 || num_kv_heads < 1)
+    return fail(W8A8_ERR_INVALID_ARG, "batch, max_query_len and head counts must be >= 1");
+  if (head_dim != 64 && head_dim != 128) return fail(W8A8_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (batch > 65535 || num_q_heads > 65535 || max_query_len >= (1LL << 31) / num_q_heads)
+    return fail(W8A8_ERR_UNSUPPORTED, "batch, head counts or max_query_len out of range");
+  if (num_q_heads % num_kv_heads != 0)
+    return fail(W8A8_ERR_INVALID_ARG, "num_q_heads must be a multiple of num_kv_heads");
+  if (num_q_heads / num_kv_heads > 64) return fail(W8A8_ERR_UNSUPPORTED, "num_q_heads / num_kv_heads must be at most 64");
+  return W8A8_OK;
+}
+
+}  // namespace
+
+size_t w8a8_kv4_attention_workspace_size(int64_t batch, int64_t max_query_len, int64_t num_q_heads,
+                                         int64_t num_kv_heads, int64_t head_dim) {
+  if (kv4_attention_sizes(batch, max_query_len, num_q_heads, num_kv_heads, head_dim) != W8A8_OK) return 0;
+  t_last_error.clear();
+  return w8a8::kv4_attention_workspace(static_cast<int>(num_q_heads / num_kv_heads), max_query_len,
+                                       static_cast<int>(head_dim), sms_or_default());
+}
+
+w8a8_status w8a8_kv4_attention(const void* q, int q_dtype, int64_t tokens, int64_t num_q_heads, int64_t num_kv_heads,
+                               int64_t head_dim, int64_t q_token_stride, int64_t q_head_stride, const void* cache,
+                               int64_t num_blocks, int64_t block_size, const int32_t* block_table, int64_t max_blocks,
+                               const int32_t* seq_lens, const int32_t* query_start, int64_t batch,
+                               int64_t max_query_len, const float* k_scale, const float* v_scale, float sm_scale,
+                               int kind, void* out, int out_dtype, int64_t out_token_stride, int64_t out_head_stride,
+                               void* workspace, size_t workspace_bytes, w8a8_stream_t stream) {
+  if (!q || !cache || !block_table || !seq_lens || !k_scale || !v_scale || !out)
+    return fail(W8A8_ERR_INVALID_ARG, "null pointer argument");
+  if ((q_dtype != W8A8_BF16 && q_dtype != W8A8_FP16) || (out_dtype != W8A8_BF16 && out_dtype != W8A8_FP16))
+    return fail(W8A8_ERR_INVALID_ARG, "q and out must be BF16 or FP16");
+  w8a8_status st = kv4_sizes(num_blocks, num_kv_heads, block_size, head_dim, kind);
+  if (st != W8A8_OK) return st;
+  if ((st = kv4_attention_sizes(batch, max_query_len, num_q_heads, num_kv_heads, head_dim)) != W8A8_OK) return st;
+  if (tokens < 1 || max_blocks < 1) return fail(W8A8_ERR_INVALID_ARG, "tokens and max_blocks must be >= 1");
+  if (!query_start && (tokens != batch || max_query_len != 1))
+    return fail(W8A8_ERR_INVALID_ARG, "without query_start a request has one token: tokens = batch, max_query_len = 1");
+  if (tokens >= (1LL << 31) || max_blocks >= (1LL << 31) / block_size)
+    return fail(W8A8_ERR_UNSUPPORTED, "tokens and max_blocks * block_size must be below 2^31");
+  if (q_token_stride < 0 || q_head_stride < 0 || (tokens > 1 && out_token_stride < head_dim) ||
+      (num_q_heads > 1 && out_head_stride < head_dim))
+    return fail(W8A8_ERR_INVALID_ARG, "strides of q must not be negative, those of out at least head_dim");
+  if (!aligned(cache, 16)) return fail(W8A8_ERR_MISALIGNED, "the cache must be 16-byte aligned");
+  if (!aligned(seq_lens, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(block_table, 4) ||
+      !aligned(query_start, 4) || !aligned(q, 2) || !aligned(out, 2))
+    return fail(W8A8_ERR_MISALIGNED, "misaligned q, out, scale, length, start or block table pointer");
+  const size_t need = w8a8::kv4_attention_workspace(static_cast<int>(num_q_heads / num_kv_heads), max_query_len,
+                                                    static_cast<int>(head_dim), sms_or_default());
+  if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+    return fail(W8A8_ERR_WORKSPACE, "workspace must be 16-byte aligned and hold %zu bytes", need);
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != W8A8_OK) return st;
+  w8a8::Kv4AttnParams p{};
+  p.q = q;
+  p.q_token_stride = q_token_stride;
+  p.q_head_stride = q_head_stride;
+  p.q_fp16 = q_dtype == W8A8_FP16;
+  p.q_vec = aligned(q, 16) && (q_token_stride | q_head_stride) % 8 == 0;
+  p.cache = cache;
+  p.num_blocks = num_blocks;
+  p.block_table = block_table;
+  p.max_blocks = static_cast<int>(max_blocks);
+  p.block_size = static_cast<int>(block_size);
+  p.seq_lens = seq_lens;
+  p.query_start = query_start;
+  p.tokens = static_cast<int>(tokens);
+  p.max_query_len = static_cast<int>(max_query_len);
+  p.batch = static_cast<int>(batch);
+  p.num_q_heads = static_cast<int>(num_q_heads);
+  p.num_kv_heads = static_cast<int>(num_kv_heads);
+  p.head_dim = static_cast<int>(head_dim);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.sm_scale = sm_scale;
+  p.kind = kind;
+  p.out = out;
+  p.out_token_stride = out_token_stride;
+  p.out_head_stride = out_head_stride;
+  p.out_fp16 = out_dtype == W8A8_FP16;
+  p.out_vec = aligned(out, 16) && (out_token_stride | out_head_stride) % 8 == 0;
+  cudaError_t e = w8a8::launch_kv4_attention(p, dev.sms, workspace, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "4-bit KV attention launch");
+  return ok();
+}
+
+w8a8_status w8a8_verify_drafts(const void* target_probs, const void* draft_probs, int dtype, int64_t vocab,
+                               int64_t target_ld, int64_t draft_ld, const int32_t* draft_tokens,
+                               const int32_t* draft_start, int64_t batch, int64_t rows, const float* uniform,
+                               const float* sample_uniform, int32_t* out_tokens, int64_t max_drafts,
+                               int32_t* num_accepted, w8a8_stream_t stream) {
+  if (!target_probs || !draft_start || !sample_uniform || !out_tokens || !num_accepted)
+    return fail(W8A8_ERR_INVALID_ARG, "null pointer argument");
+  if (rows > 0 && (!draft_tokens || !uniform)) return fail(W8A8_ERR_INVALID_ARG, "null pointer argument");
+  if (dtype != W8A8_FP32 && dtype != W8A8_BF16 && dtype != W8A8_FP16)
+    return fail(W8A8_ERR_INVALID_ARG, "probabilities must be FP32, BF16 or FP16");
+  if (batch < 1 || vocab < 1 || rows < 0 || max_drafts < 0)
+    return fail(W8A8_ERR_INVALID_ARG, "batch and vocab must be >= 1, rows and max_drafts >= 0");
+  if (target_ld < vocab || (draft_probs && rows > 0 && draft_ld < vocab))
+    return fail(W8A8_ERR_INVALID_ARG, "leading dimensions must be at least vocab");
+  if (batch > 65535 || vocab >= (1LL << 30) || rows >= (1LL << 30) || max_drafts >= (1LL << 20))
+    return fail(W8A8_ERR_UNSUPPORTED, "batch, vocab, rows or max_drafts out of range");
+  const size_t elem = dtype == W8A8_FP32 ? 4 : 2;
+  if (!aligned(target_probs, elem) || !aligned(draft_probs, elem) || !aligned(draft_tokens, 4) ||
+      !aligned(draft_start, 4) || !aligned(uniform, 4) || !aligned(sample_uniform, 4) || !aligned(out_tokens, 4) ||
+      !aligned(num_accepted, 4))
+    return fail(W8A8_ERR_MISALIGNED, "misaligned pointer");
+  w8a8_status st;
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != W8A8_OK) return st;
+  w8a8::VerifyArgs a{};
+  a.target = target_probs;
+  a.draft = rows > 0 ? draft_probs : nullptr;
+  a.dtype = dtype;
+  a.vocab = static_cast<int>(vocab);
+  a.target_ld = target_ld;
+  a.draft_ld = draft_ld;
+  a.draft_tokens = draft_tokens;
+  a.draft_start = draft_start;
+  a.batch = static_cast<int>(batch);
+  a.rows = static_cast<int>(rows);
+  a.uniform = uniform;
+  a.sample_uniform = sample_uniform;
+  a.out_tokens = out_tokens;
+  a.max_drafts = static_cast<int>(max_drafts);
+  a.num_accepted = num_accepted;
+  cudaError_t e = w8a8::launch_verify(a, dev.sms, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "draft verification launch");
   return ok();
 }
 

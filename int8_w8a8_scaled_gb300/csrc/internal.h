@@ -143,6 +143,94 @@ cudaError_t launch_fp8kv_attention(const AttnParams& p, const CUtensorMap* tmap_
 // Reads and clears the attention kernels' status word (call after a sync).
 cudaError_t read_clear_attn_status(int* flags);
 
+// The 4-bit KV cache (kv4.cuh has its layout): writing and reading tokens at
+// their slots (kv4_cache.cu).
+struct Kv4CacheArgs {
+  const void* k;  // write: [tokens, heads, head_dim] of 16-bit values
+  const void* v;
+  void* k_out;    // read: the same shape
+  void* v_out;
+  long long k_token_stride, k_head_stride, v_token_stride, v_head_stride;  // elements
+  int fp16;       // the 16-bit values are fp16, else bf16
+  int vec;        // every group of 16 values is 16-byte aligned
+  void* cache;
+  long long num_blocks;
+  int block_size;          // a multiple of 16
+  int heads, head_dim;
+  const int64_t* slots;    // [tokens]; outside the cache: skipped (read: zeros)
+  long long tokens;
+  const float* k_scale;    // [1]
+  const float* v_scale;    // [1]
+  int kind;                // W8A8_KV4_*
+};
+cudaError_t launch_kv4_cache(const Kv4CacheArgs& a, bool write, cudaStream_t stream);
+
+// Block tables, slots and positions of a step's tokens (kv4_cache.cu).
+struct BlockTableArgs {
+  const int* context_lens;  // [batch]
+  const int* new_lens;      // [batch]
+  int batch;
+  const int* free_blocks;   // [free_capacity]
+  const int* free_count;    // [1]
+  int free_capacity;
+  int* block_table;         // [batch, max_blocks]
+  int max_blocks, block_size;
+  int* query_start;         // [batch + 1]
+  int* seq_lens;            // [batch]
+  int64_t* slots;           // [tokens]
+  int* positions;           // [tokens]
+  long long tokens;
+  int* free_left;           // [1]
+  int* free_count_out;      // [1] or null
+};
+constexpr int kMaxTableBatch = 16384;  // two words of shared memory a request
+cudaError_t launch_block_tables(const BlockTableArgs& a, int num_sms, cudaStream_t stream);
+
+// Attention over the 4-bit cache (kv4_attention.cu).
+struct Kv4AttnParams {
+  const void* q;        // [tokens, num_q_heads, head_dim] of 16-bit values
+  long long q_token_stride, q_head_stride;  // elements
+  int q_fp16;
+  int q_vec;            // q rows are 16-byte aligned
+  const void* cache;
+  long long num_blocks;
+  const int* block_table;  // [batch, max_blocks]; entries outside the cache are skipped
+  int max_blocks, block_size;
+  const int* seq_lens;     // [batch], clamped to [0, max_blocks * block_size]
+  const int* query_start;  // [batch + 1], or null: one token a request
+  int tokens, max_query_len;
+  int batch, num_q_heads, num_kv_heads, head_dim;
+  const float* k_scale;    // [1]
+  const float* v_scale;    // [1]
+  float sm_scale;
+  int kind;
+  void* out;               // as q
+  long long out_token_stride, out_head_stride;
+  int out_fp16;
+  int out_vec;
+};
+// Workspace bytes of a call with `share` query heads to a KV head.
+size_t kv4_attention_workspace(int share, long long max_query_len, int head_dim, int num_sms);
+cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int num_sms, void* workspace, cudaStream_t stream);
+
+// Verification of drafted tokens (verify.cu).
+struct VerifyArgs {
+  const void* target;       // [rows + batch, vocab]
+  const void* draft;        // [rows, vocab], or null: the draft gave its tokens alone
+  int dtype;                // W8A8_FP32 / BF16 / FP16
+  int vocab;
+  long long target_ld, draft_ld;
+  const int* draft_tokens;  // [rows]
+  const int* draft_start;   // [batch + 1]
+  int batch, rows;
+  const float* uniform;         // [rows]
+  const float* sample_uniform;  // [batch]
+  int* out_tokens;          // [batch, max_drafts + 1]
+  int max_drafts;
+  int* num_accepted;        // [batch]
+};
+cudaError_t launch_verify(const VerifyArgs& a, int num_sms, cudaStream_t stream);
+
 // Quantiser / dequantiser launchers.
 struct QuantArgs {
   const void* x;

@@ -1,0 +1,67 @@
+// kv4.cuh -- the 4-bit KV cache: its layout, and the arithmetic of its codes.
+//
+// A cache is [num_blocks, num_kv_heads, block_size / 16] records of 16
+// tokens, 18 * head_dim bytes each:
+//   key codes    16 rows of head_dim / 2 bytes (two codes a byte, even dim low)
+//   key scales   16 rows of head_dim / 16 bytes (one e4m3 scale for 16 dims)
+//   value codes, value scales   the same
+// One block and head's records are consecutive, so that any run of records is
+// one untiled bulk copy, whose offsets are multiples of 16 bytes.
+//
+// An element stands for code * group scale * g, with g the tensor's fp32
+// scale, one for K and one for V.  Codes are e2m1 (0, .5, 1, 1.5, 2, 3, 4, 6
+// and their negatives) or int4 (two's complement, -7..7).  code * group scale
+// has at most 3 + 4 significant bits and lies in [2^-10, 7 * 448]: an exact
+// f16 number, so a matrix product over f16 operands sees the cache without
+// a rounding, and g is applied in fp32 to its result.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+namespace w8a8 {
+namespace {  // each translation unit keeps its own copy
+
+constexpr int kKv4Tokens = 16;  // tokens of a record
+constexpr int kKv4Group = 16;   // dims that share a scale
+
+// Byte offsets within a record.
+__host__ __device__ constexpr int kv4_record_bytes(int d) { return 18 * d; }
+__host__ __device__ constexpr int kv4_codes_at(int d, int which) { return which ? 9 * d : 0; }
+__host__ __device__ constexpr int kv4_scales_at(int d, int which) { return which ? 17 * d : 8 * d; }
+
+// The record of token `off` of a block, for one head.
+__device__ __forceinline__ size_t kv4_record_of(long long block, int head, int heads, int block_size, int off) {
+  return (static_cast<size_t>(block) * heads + head) * (block_size / kKv4Tokens) + off / kKv4Tokens;
+}
+
+__host__ __device__ constexpr float kv4_largest(int kind) { return kind == W8A8_KV4_E2M1 ? 6.f : 7.f; }
+
+// The 8 codes of a word as 4 f16x2 values (h[i] = codes 2i, 2i + 1), exactly.
+template <int KIND>
+__device__ __forceinline__ void kv4_decode8(uint32_t w, uint32_t (&h)[4]) {
+  if (KIND == W8A8_KV4_E2M1) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int lo = static_cast<int>(w << (28 - 8 * i)) >> 28, hi = static_cast<int>(w << (24 - 8 * i)) >> 28;
+      const __half2 v = __halves2half2(__int2half_rn(lo), __int2half_rn(hi));
+      h[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  }
+}
+
+__device__ __forceinline__ float e4m3_to_float(uint8_t s) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(s)));
+  return __low2float(*reinterpret_cast<const __half2*>(&h));
+}
+
+}  // namespace
+}  // namespace w8a8
