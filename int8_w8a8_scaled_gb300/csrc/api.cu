@@ -1256,6 +1256,9 @@ w8a8_status w8a8_device_status(int* flags) {
   e = read_clear_attn_status(&qf);
   if (e != cudaSuccess) return cuda_fail(e, "device status read");
   *flags |= qf;
+  e = read_clear_kv4_status(&qf);
+  if (e != cudaSuccess) return cuda_fail(e, "device status read");
+  *flags |= qf;
   return ok();
 }
 

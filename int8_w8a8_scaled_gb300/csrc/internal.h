@@ -208,10 +208,19 @@ struct Kv4AttnParams {
   long long out_token_stride, out_head_stride;
   int out_fp16;
   int out_vec;
+  // set by the launcher
+  int share;            // num_q_heads / num_kv_heads
+  int only;             // which requests a launch takes (request_of)
+  unsigned* counters;   // parts of a cut unit that have arrived, left zero
+  float* partial;       // [CTAs][2] partial results
 };
 // Workspace bytes of a call with `share` query heads to a KV head.
 size_t kv4_attention_workspace(int share, long long max_query_len, int head_dim, int num_sms);
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int num_sms, void* workspace, cudaStream_t stream);
+// Requests of more rows than the few-rows kernel takes (kv4_prompt.cu).
+cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, cudaStream_t stream);
+// Reads and clears the kernels' status word (call after a sync).
+cudaError_t read_clear_kv4_status(int* flags);
 
 // Verification of drafted tokens (verify.cu).
 struct VerifyArgs {

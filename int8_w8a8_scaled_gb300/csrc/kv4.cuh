@@ -38,23 +38,50 @@ __device__ __forceinline__ size_t kv4_record_of(long long block, int head, int h
 
 __host__ __device__ constexpr float kv4_largest(int kind) { return kind == W8A8_KV4_E2M1 ? 6.f : 7.f; }
 
-// The 8 codes of a word as 4 f16x2 values (h[i] = codes 2i, 2i + 1), exactly.
+// A pair of group scales as kv4_decode8 takes them: the scales, and for int4
+// also -72 times them (4 + 4 significant bits: exact).
+struct Kv4Scale {
+  __half2 s, bias;
+};
 template <int KIND>
-__device__ __forceinline__ void kv4_decode8(uint32_t w, uint32_t (&h)[4]) {
+__device__ __forceinline__ Kv4Scale kv4_scale(__half2 s) {
+  return {s, KIND == W8A8_KV4_INT4 ? __hmul2(s, __float2half2_rn(-72.f)) : s};
+}
+
+// The 8 codes of a word times a pair of scales, as 4 f16x2 values: h[i] =
+// (code 2i * low scale, code 2i + 1 * high scale), exactly.
+template <int KIND>
+__device__ __forceinline__ void kv4_decode8(uint32_t w, const Kv4Scale& sc, uint32_t (&h)[4]) {
   if (KIND == W8A8_KV4_E2M1) {
+    uint32_t c[4];
     asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
         "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
         "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
         : "r"(w));
-  } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int lo = static_cast<int>(w << (28 - 8 * i)) >> 28, hi = static_cast<int>(w << (24 - 8 * i)) >> 28;
-      const __half2 v = __halves2half2(__int2half_rn(lo), __int2half_rn(hi));
+      const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&c[i]), sc.s);
+      h[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  } else {
+    // a nibble n in bits 4..7 of the f16 64 (whose steps are 1/16 there), its
+    // sign bit flipped, is 72 + n; s (72 + n) - 72 s is one exact FMA
+    const uint32_t up = w << 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t r = (__byte_perm(up, w, 0x4400u + 0x1111u * i) & 0x00F000F0u) ^ 0x54805480u;
+      const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&r), sc.s, sc.bias);
       h[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
   }
+}
+
+// Two e4m3 bytes as f16x2.
+__device__ __forceinline__ __half2 e4m3x2_to_half2(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+  return *reinterpret_cast<const __half2*>(&h);
 }
 
 __device__ __forceinline__ float e4m3_to_float(uint8_t s) {

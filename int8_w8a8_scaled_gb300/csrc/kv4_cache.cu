@@ -139,8 +139,9 @@ __global__ void __launch_bounds__(kCacheThreads) kv4_read_kernel(const Kv4CacheA
         *reinterpret_cast<const uint2*>(rec + kv4_codes_at(p.head_dim, which) + row * (p.head_dim / 2) + grp * 8);
     const float s = e4m3_to_float(rec[kv4_scales_at(p.head_dim, which) + row * groups + grp]);
     uint32_t h[2][4];
-    kv4_decode8<KIND>(codes.x, h[0]);
-    kv4_decode8<KIND>(codes.y, h[1]);
+    const Kv4Scale one = kv4_scale<KIND>(__float2half2_rn(1.f));
+    kv4_decode8<KIND>(codes.x, one, h[0]);
+    kv4_decode8<KIND>(codes.y, one, h[1]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&h[j / 4][j % 4]));
