@@ -211,6 +211,8 @@ struct Kv4AttnParams {
   // set by the launcher
   int share;            // num_q_heads / num_kv_heads
   int only;             // which requests a launch takes (request_of)
+  int per_block;        // records of a block
+  int block_shift;      // its logarithm, -1 if it is no power of two
   unsigned* counters;   // parts of a cut unit that have arrived, left zero
   float* partial;       // [CTAs][2] partial results
 };

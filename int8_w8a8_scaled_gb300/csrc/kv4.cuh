@@ -48,8 +48,28 @@ __device__ __forceinline__ Kv4Scale kv4_scale(__half2 s) {
   return {s, KIND == W8A8_KV4_INT4 ? __hmul2(s, __float2half2_rn(-72.f)) : s};
 }
 
+// (x & mask) ^ flip in one instruction (two immediates would make it two).
+__device__ __forceinline__ uint32_t and_xor(uint32_t x, uint32_t mask, uint32_t flip) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(y) : "r"(x), "r"(mask), "r"(flip));
+  return y;
+}
+
+// Where the two codes of f16x2 value i of a decoded word sit in it.  An e2m1
+// conversion takes a byte; int4's arithmetic takes nibbles 16 bits apart.
+template <int KIND>
+__host__ __device__ constexpr int kv4_low(int i) {
+  return KIND == W8A8_KV4_E2M1 ? 2 * i : i;
+}
+template <int KIND>
+__host__ __device__ constexpr int kv4_high(int i) {
+  return KIND == W8A8_KV4_E2M1 ? 2 * i + 1 : i + 4;
+}
+
 // The 8 codes of a word times a pair of scales, as 4 f16x2 values: h[i] =
-// (code 2i * low scale, code 2i + 1 * high scale), exactly.
+// (code kv4_low(i) * low scale, code kv4_high(i) * high scale), exactly.
+// Four conversions and four products for e2m1; for int4 three shifts, four
+// logical operations and four FMAs.
 template <int KIND>
 __device__ __forceinline__ void kv4_decode8(uint32_t w, const Kv4Scale& sc, uint32_t (&h)[4]) {
   if (KIND == W8A8_KV4_E2M1) {
@@ -67,14 +87,30 @@ __device__ __forceinline__ void kv4_decode8(uint32_t w, const Kv4Scale& sc, uint
   } else {
     // a nibble n in bits 4..7 of the f16 64 (whose steps are 1/16 there), its
     // sign bit flipped, is 72 + n; s (72 + n) - 72 s is one exact FMA
-    const uint32_t up = w << 4;
+    const uint32_t at[4] = {w << 4, w, w >> 4, w >> 8};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t r = (__byte_perm(up, w, 0x4400u + 0x1111u * i) & 0x00F000F0u) ^ 0x54805480u;
+      const uint32_t r = and_xor(at[i], 0x00F000F0u, 0x54805480u);
       const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&r), sc.s, sc.bias);
       h[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
   }
+}
+
+// A word for kv4_decode8 whose value i pairs code 4 q + i of `a` (low) with
+// the same of `b`, q = 0 or 1; for e2m1 the codes come in the order kv4_pair_dim.
+template <int KIND>
+__device__ __forceinline__ uint32_t kv4_interleave(uint32_t a, uint32_t b, int q) {
+  if (KIND == W8A8_KV4_E2M1) {
+    constexpr uint32_t kLow = 0x0F0F0F0Fu;
+    return q == 0 ? (a & kLow) | ((b << 4) & ~kLow) : ((a >> 4) & kLow) | (b & ~kLow);
+  }
+  return __byte_perm(a, b, q == 0 ? 0x5410 : 0x7632);
+}
+// The code (of 8) that value i of kv4_interleave(.., q) holds.
+template <int KIND>
+__host__ __device__ constexpr int kv4_pair_dim(int q, int i) {
+  return KIND == W8A8_KV4_E2M1 ? 2 * i + q : 4 * q + i;
 }
 
 // Two e4m3 bytes as f16x2.

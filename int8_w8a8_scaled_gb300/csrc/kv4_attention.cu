@@ -7,7 +7,7 @@
 // ---- Work
 // A unit is one request and KV head: its n new tokens times the G query heads
 // that share the KV head are `rows` rows over the same tokens, taken 16 at a
-// time (a tile: one record of the cache).  All units' tiles in a row, request
+// time (a tile: one record of the cache).  All units' steps of kStep tiles in a row, request
 // by request and head by head, are cut into equal runs, one for each CTA, so
 // that ragged lengths load the SMs evenly.  A unit that lies in one run is
 // written out by its CTA.  One that is cut leaves a partial result (maximum,
@@ -23,16 +23,20 @@
 //   scores  S^T[16 tokens x 8 rows] = K[16 x D] . q^T[D x 8]
 //   output  O^T[D x 8 rows] += V^T[D x 16 tokens] . P^T[16 x 8]
 // with f16 operands (the decoded cache is exact in f16, the query after
-// scaling by a power of two) and fp32 sums.  The weights p = 2^(s - m) <= 1
-// enter the second product as f16(p 2^15), 11 bits, and the sum that divides
-// the result is taken over the rounded weights, so that the rounding's common
-// part cancels.
+// scaling by a power of two) and fp32 sums.  The weights p = 2^(s - m)
+// enter the second product as f16(p 2^7), 11 bits, and the sum that divides
+// the result is taken over the rounded weights (by one more MMA, whose A is
+// ones), so that the rounding's common part cancels.  The maximum m is raised
+// only when a score passes it by more than 8 (2^15 then, f16's last power of
+// two): the state is rescaled once or twice a unit, not at every new maximum.
 //
-// A producer warp copies tiles ahead into a ring (one untiled bulk copy each;
-// lane l looks after slot l: block table, wait, copy); eight warps take the
-// tiles in turn, each with a softmax state of its own, joined in shared memory
-// at the end of a unit.  While they join, the producer is filling the ring
-// with the next unit's tiles.
+// Eight warps take the steps of a run in turn (a step: kStep tiles, decoded
+// together so that one's latencies hide behind the other's), each with a softmax
+// state of its own, joined in shared memory at the end of a unit.  A warp
+// copies its next step's records (untiled bulk copies) as soon as it has read
+// a slot of its ring, across the ends of units, so that the copies go on
+// while the states are joined.  A producer warp in place of that cost a
+// fifth of the issue slots in polling, and its registers.
 //
 // Registers (lane = 4 g + t).  The dot product does not depend on the order
 // of the dims, nor the sum over tokens on theirs, so both are permuted to
@@ -40,9 +44,9 @@
 //   K: lane (g, t) holds dims [D/4 t, D/4 (t + 1)) of the tokens in rows g
 //      and g + 8; k-block j takes dims D/4 t + 4 j .. + 3 of every lane.
 //   V: lane (g, t) holds dims [D/8 g, D/8 (g + 1)) of four tokens, those of
-//      rows 2t, 2t + 1, 2t + 8, 2t + 9; m-tile i takes dims D/8 g + 2 i (row
-//      g) and + 2 i + 1 (row g + 8).  The codes of two tokens are interleaved
-//      nibble by nibble, which makes each byte one operand register.
+//      rows 2t, 2t + 1, 2t + 8, 2t + 9; m-tile i takes two of the dims (rows g
+//      and g + 8).  The codes of two tokens are interleaved, which makes two
+//      codes of one dim one operand register.
 //   Row 2j of the tile is token j, row 2j + 1 token 4 + (j ^ 1), rows 8.. the
 //      same + 8: the K reads are then free of bank conflicts (V's two-way).
 #include <algorithm>
@@ -55,15 +59,15 @@ namespace w8a8 {
 
 namespace {
 
-constexpr float kPScale = 32768.f;
 constexpr float kLog2e = 1.4426950408889634f;
 
-constexpr int kWarps = 8;                        // warps that compute
-constexpr int kThreads = 32 * (kWarps + 1);      // and the producer
-constexpr int kComputeThreads = 32 * kWarps;
-constexpr int kSlots = 32;                       // ring slots, one for each lane of the producer
-constexpr int kMinRun = kWarps;                  // tiles of a CTA's run: one a warp at least
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStep = 2;                         // tiles of a step
+constexpr int kRing = 2;                         // steps in a warp's ring
+constexpr int kMinRun = kWarps;                  // steps of a CTA's run: one a warp at least
 constexpr int kSmallRows = 16;
+constexpr float kHeadroom = 8.f;
 constexpr int kMaxCounters = 1024;               // CTAs that may leave a unit open
 constexpr size_t kCounterBytes = kMaxCounters * sizeof(unsigned);
 
@@ -76,7 +80,7 @@ inline int few_rows_ctas(int nt, int num_sms) { return std::min(kMaxCounters, (n
 struct Request {
   int first, n;  // its rows in q
   int len;       // tokens
-  int tiles;     // 0: nothing to do here
+  int steps;     // steps of a unit; 0: nothing to do here
 };
 
 // `only` 1: requests of up to kSmallRows rows, 0: larger ones, -1: all.
@@ -91,15 +95,16 @@ __device__ __forceinline__ Request request_of(const Kv4AttnParams& p, int b, int
   const long long room = static_cast<long long>(p.max_blocks) * p.block_size;
   r.len = static_cast<int>(min(static_cast<long long>(max(__ldg(p.seq_lens + b), 0)), room));
   const bool small = static_cast<long long>(r.n) * p.share <= kSmallRows;
-  // an empty request has one tile, with no token in it, to write its zeros
-  r.tiles = r.n > 0 && (only < 0 || small == (only > 0)) ? max(1, (r.len + kKv4Tokens - 1) / kKv4Tokens) : 0;
+  // an empty request has one step, with no token in it, to write its zeros
+  constexpr int kTokens = kStep * kKv4Tokens;
+  r.steps = r.n > 0 && (only < 0 || small == (only > 0)) ? max(1, (r.len + kTokens - 1) / kTokens) : 0;
   return r;
 }
 
 // Where a CTA's run begins.
 struct Start {
-  long long total;  // tiles of all units
-  long long before; // tiles in front of request b
+  long long total;  // steps of all units
+  long long before; // steps in front of request b
   int b;
 };
 
@@ -127,13 +132,6 @@ __device__ __forceinline__ float ex2_fast(float x) {
 }
 
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
-
-__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kComputeThreads) : "memory"); }
-
-__device__ __forceinline__ float load16(const void* p, int fp16, size_t i) {
-  if (fp16) return __half2float(static_cast<const __half*>(p)[i]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
 
 // 4 consecutive outputs.
 __device__ __forceinline__ void store4(const Kv4AttnParams& p, size_t at, const float (&y)[4]) {
@@ -163,10 +161,11 @@ template <int D, int NT>
 struct Small {
   static constexpr int kRows = 8 * NT;
   static constexpr int kTile = kv4_record_bytes(D);
-  static constexpr int kRing = kSlots * kTile;
+  static constexpr int kSlot = kStep * kTile;
+  static constexpr int kRingBytes = kWarps * kRing * kSlot;
   static constexpr int kOStride = D + 4;                   // a row's o in shared memory
   static constexpr int kJoin = kWarps * kRows * kOStride * 4;
-  static constexpr int kSmem = kRing + kJoin;
+  static constexpr int kSmem = kRingBytes + kJoin;
   static constexpr int kPart = kRows * (D + 4);            // floats of a partial result: o, then m, l of each row
 };
 
@@ -176,22 +175,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
   constexpr int KW = D / 32;   // words of K codes a lane holds of a token
   constexpr int MT = D / 16;   // m-tiles of the output product, k-blocks of the scores'
   extern __shared__ __align__(128) uint8_t smem[];
-  float* s_o = reinterpret_cast<float*>(smem + C::kRing);
-  __shared__ uint64_t s_full[kSlots], s_empty[kSlots];
+  float* s_o = reinterpret_cast<float*>(smem + C::kRingBytes);
+  __shared__ uint64_t s_full[kWarps][kRing];
   __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
-  __shared__ long long s_scan[kWarps + 1];
+  __shared__ long long s_scan[kWarps];
   __shared__ Start s_start;
   __shared__ int s_last;
-  __shared__ uint8_t s_live[kSlots];  // the slot's tile lies in the cache
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
-  if (tid < kSlots) {
-    mbar_init(smem_addr(&s_full[tid]), 1);
-    mbar_init(smem_addr(&s_empty[tid]), 1);
-  }
   if (tid == 0) {
+    for (int i = 0; i < kWarps * kRing; ++i) mbar_init(smem_addr(&s_full[0][0] + i), kStep);
     fence_barrier_init();
-    s_start.b = p.batch;
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -202,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
     const int per = (p.batch + kThreads - 1) / kThreads;
     const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += static_cast<long long>(request_of(p, b, p.only).tiles) * hkv;
+    for (int b = b0; b < b1; ++b) mine += static_cast<long long>(request_of(p, b, p.only).steps) * hkv;
     long long run = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -213,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
     __syncthreads();
     long long total = 0;
     run -= mine;
-    for (int w = 0; w <= kWarps; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
       if (w < warp) run += s_scan[w];
       total += s_scan[w];
     }
@@ -221,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
     const long long r0 = share * blockIdx.x;
     if (r0 >= run && r0 < run + mine) {
       for (int b = b0; b < b1; ++b) {
-        const long long w = static_cast<long long>(request_of(p, b, p.only).tiles) * hkv;
+        const long long w = static_cast<long long>(request_of(p, b, p.only).steps) * hkv;
         if (r0 < run + w) {
           s_start.b = b;
           s_start.before = run;
@@ -239,83 +233,80 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
   if (r0 >= r1) return;
   int b = s_start.b;
   Request rq = request_of(p, b, p.only);
-  int kvh = static_cast<int>((r0 - s_start.before) / rq.tiles);
-  int tile = static_cast<int>((r0 - s_start.before) % rq.tiles);
-  const int run_tiles = static_cast<int>(min(r1 - r0, 0x7fffffffLL));
+  int kvh = static_cast<int>((r0 - s_start.before) / rq.steps);
+  int step = static_cast<int>((r0 - s_start.before) % rq.steps);
+  const int run_steps = static_cast<int>(min(r1 - r0, 0x7fffffffLL));
 
-  if (warp == kWarps) {
-    // ---- producer: lane l fills slot l with tiles l, l + 32, ...; the lanes
-    // poll, so that none waits for a slot that is not its own
-    const int per_block = p.block_size / kKv4Tokens;
-    const uint64_t pol = policy_evict_first();
-    const uint32_t full = smem_addr(&s_full[lane]), empty = smem_addr(&s_empty[lane]);
-    const uint32_t dst = smem_addr(smem) + lane * C::kTile;
-    uint32_t use = 0, idle = 0;
-    uint64_t since = 0;
-    int f = lane;
-    long long rec = -1;
-    tile += lane;
-    bool fresh = true;  // the next tile's place in the cache is not known yet
-    while (__any_sync(0xffffffffu, f < run_tiles)) {
-      bool moved = false;
-      if (f < run_tiles) {
-        if (fresh) {
-          while (tile >= rq.tiles) {
-            tile -= rq.tiles;
-            if (++kvh == hkv) {
-              kvh = 0;
-              do rq = request_of(p, ++b, p.only);
-              while (rq.tiles == 0);
-            }
+  // ---- the warp's steps: warp, warp + 8, ... of the run.  The fetching end is
+  // up to kRing steps ahead of the computing one.
+  const uint64_t pol = policy_evict_first();
+  const uint32_t full0 = smem_addr(&s_full[warp][0]);
+  uint8_t* const ring = smem + warp * kRing * C::kSlot;
+  // The places of a batch of 16 steps are looked up at once: lane 2 k + u has
+  // record u of the batch's step k, and copies it when its turn comes.
+  constexpr int kBatch = 32 / kStep;
+  int fb = b, fkvh = kvh, fpos = 0, fetched = 0;  // fpos: the position in the run that fstep stands for
+  long long fstep = step;
+  Request frq = rq;
+  const uint8_t* src = nullptr;  // this lane's record
+  uint32_t found = 0u;           // the lanes whose record lies in the cache
+  uint32_t live_bits = 0u;       // the same of the steps in the ring
+  auto fetch = [&] {
+    if (warp + kWarps * fetched >= run_steps) return;
+    if (fetched % kBatch == 0) {
+      const int want = warp + kWarps * (fetched + lane / kStep);
+      bool in = want < run_steps;
+      if (in) {
+        fstep += want - fpos;
+        fpos = want;
+        while (fstep >= frq.steps) {
+          fstep -= frq.steps;
+          if (++fkvh == hkv) {
+            fkvh = 0;
+            do frq = request_of(p, ++fb, p.only);
+            while (frq.steps == 0);
           }
-          rec = -1;
-          if (tile * kKv4Tokens < rq.len) {
-            const int blk = __ldg(p.block_table + static_cast<size_t>(b) * p.max_blocks + tile / per_block);
-            if (blk >= 0 && blk < p.num_blocks)
-              rec = (static_cast<long long>(blk) * hkv + kvh) * per_block + tile % per_block;
-          }
-          fresh = false;
         }
-        if (use == 0 || mbar_test_wait(empty, (use - 1) & 1)) {
-          s_live[lane] = rec >= 0;
-          if (rec >= 0) {
-            mbar_arrive_expect_tx(full, C::kTile);
-            bulk_load_hint(dst, static_cast<const uint8_t*>(p.cache) + rec * C::kTile, C::kTile, full, pol);
-          } else {
-            mbar_arrive(full);
-          }
-          ++use;
-          f += kSlots;
-          tile += kSlots;
-          fresh = moved = true;
+        const int tile = static_cast<int>(fstep) * kStep + lane % kStep;
+        in = tile < (frq.len + kKv4Tokens - 1) / kKv4Tokens;
+        if (in) {
+          const int page = p.block_shift >= 0 ? tile >> p.block_shift : tile / p.per_block;
+          const int blk = __ldg(p.block_table + static_cast<size_t>(fb) * p.max_blocks + page);
+          in = blk >= 0 && blk < p.num_blocks;
+          src = static_cast<const uint8_t*>(p.cache) +
+                ((static_cast<long long>(blk) * hkv + fkvh) * p.per_block + (tile - page * p.per_block)) * C::kTile;
         }
       }
-      if (__any_sync(0xffffffffu, moved)) {
-        idle = 0;
-      } else if ((++idle & 255u) == 0u) {  // bounded, like every wait
-        const uint64_t now = global_timer_ns();
-        if (idle == 256u) since = now;
-        else if (now - since > W8A8_WAIT_NS) {
-          atomicOr(&g_device_status, 1);
-          break;
-        }
+      found = __ballot_sync(0xffffffffu, in);
+    }
+    const int turn = fetched % kBatch, slot = fetched % kRing;
+    const uint32_t live = (found >> (kStep * turn)) & 3u;
+    live_bits = (live_bits & ~(3u << (kStep * slot))) | (live << (kStep * slot));
+    if (lane / kStep == turn) {
+      const uint32_t full = full0 + 8 * slot;
+      fence_proxy_async_shared();  // the reads of the slot's last step before the copies that overwrite it
+      if (live >> (lane % kStep) & 1u) {
+        mbar_arrive_expect_tx(full, C::kTile);
+        bulk_load_hint(smem_addr(ring + slot * C::kSlot + (lane % kStep) * C::kTile), src, C::kTile, full, pol);
+      } else {
+        mbar_arrive(full);
       }
     }
-    // the slot's last copy has landed before the CTA's shared memory is released
-    if (use > 0) mbar_wait(full, (use - 1) & 1);
-    return;
-  }
+    ++fetched;
+  };
+#pragma unroll
+  for (int i = 0; i < kRing; ++i) fetch();
 
-  // ---- the warps that compute
   const int g = lane >> 2, t = lane & 3;
   const int tk = (g >> 1) + (g & 1 ? 4 - (g >> 1) + ((g >> 1) ^ 1) : 0);  // token of row g
   const int tv[4] = {t, 4 + (t ^ 1), 8 + t, 12 + (t ^ 1)};                // tokens of rows 2t, 2t + 1, 2t + 8, 2t + 9
   const float kscale = __ldg(p.k_scale), vscale = __ldg(p.v_scale);
   bool ok = true;
-  int f = 0;  // tiles of the run in front of this unit
+  int done = 0;  // steps this warp has computed
+  int f = 0;  // steps of the run in front of this unit
   long long at = r0;
-  while (f < run_tiles) {
-    const int seg = min(rq.tiles - tile, run_tiles - f);  // this unit's tiles in the run
+  while (f < run_steps) {
+    const int seg = min(rq.steps - step, run_steps - f);  // this unit's steps in the run
     const int rows = rq.n * p.share;
 
     // the query: dims D/4 t .. of row g (and 8 + g), scaled by 2^e so that the largest lies in [2^14, 2^15)
@@ -362,15 +353,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
       // 2^e as a float: qmax in [2^x, 2^(x + 1)) has x + 127 in its exponent bits
       int e = 0;
       if (qmax > 0.f && qmax <= 3.0e38f) e = min(100, max(-100, 14 + 127 - static_cast<int>(__float_as_uint(qmax) >> 23)));
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
       cs = p.sm_scale * kscale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      // the scale's sign goes to the query: the largest product is the largest score
+      const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), cs);
+      cs = fabsf(cs);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-          const float2 v = p.q_fp16 ? __half22float2(*reinterpret_cast<const __half2*>(&raw[nt][j]))
-                                    : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[nt][j]));
-          qf[nt][j / 2][j & 1] = as_u32(__floats2half2_rn(v.x * up, v.y * up));
+        for (int w = 0; w < KW; ++w) {
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 x = p.q_fp16 ? __half22float2(*reinterpret_cast<const __half2*>(&raw[nt][4 * w + j]))
+                                      : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[nt][4 * w + j]));
+            v[2 * j] = x.x * up;
+            v[2 * j + 1] = x.y * up;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            qf[nt][2 * w + j / 2][j & 1] = as_u32(__floats2half2_rn(v[kv4_low<KIND>(j)], v[kv4_high<KIND>(j)]));
         }
     }
     // the last token that the columns 2t, 2t + 1 see
@@ -384,80 +385,90 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
       }
     const int all_seen = rq.len - rq.n;  // tokens up to this one are seen by every row
 
-    float m[NT][2], l[NT][2], o[NT][MT][4];
+    // products that may pass the running maximum before it is raised: weights
+    // then reach 2^kHeadroom, and come out times 2^(15 - kHeadroom) for f16
+    const float room = fminf(kHeadroom / cs, 1e38f);
+    float m[NT][2], l[NT][4], o[NT][MT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = 0.f;
+      l[nt][0] = l[nt][1] = l[nt][2] = l[nt][3] = 0.f;
 #pragma unroll
       for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
     }
 
-    // tiles f + x of the run, x < seg, with (f + x) % kWarps == warp
+    // steps f + x of the run, x < seg, with (f + x) % kWarps == warp
     for (int x = (warp - f % kWarps + kWarps) % kWarps; x < seg; x += kWarps) {
-      const int slot = (f + x) % kSlots;
-      const uint32_t parity = ((f + x) / kSlots) & 1;
-      if (ok) ok = mbar_wait(smem_addr(&s_full[slot]), parity);
-      const int t0 = (tile + x) * kKv4Tokens;
-      if (ok && s_live[slot]) {
-        const uint8_t* rec = smem + slot * C::kTile;
+      const int slot = done % kRing;
+      if (ok) ok = mbar_wait(full0 + 8 * slot, (done / kRing) & 1);
+      const uint32_t live = ok ? (live_bits >> (kStep * slot)) & 3u : 0u;
+      const int t0 = (step + x) * kStep * kKv4Tokens;
+      const uint8_t* rec0 = ring + slot * C::kSlot;
+      if (live) {
         // scores
-        float sp[NT][4];
+        float sp[kStep][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) sp[nt][0] = sp[nt][1] = sp[nt][2] = sp[nt][3] = 0.f;
-        uint32_t kw[2][KW];
-        Kv4Scale ks[2][D / 64];
+        for (int u = 0; u < kStep; ++u) {
+          const uint8_t* rec = rec0 + u * C::kTile;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int row = tk + 8 * r;
-          if (D == 128) {
-            const uint4 v = *reinterpret_cast<const uint4*>(rec + row * (D / 2) + 16 * t);
-            kw[r][0] = v.x;
-            kw[r][1] = v.y;
-            kw[r][KW - 2] = v.z;
-            kw[r][KW - 1] = v.w;
-            const __half2 s = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(rec + kv4_scales_at(D, 0) + row * (D / 16) + 2 * t));
-            ks[r][0] = kv4_scale<KIND>(__low2half2(s));
-            ks[r][D / 64 - 1] = kv4_scale<KIND>(__high2half2(s));
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(rec + row * (D / 2) + 8 * t);
-            kw[r][0] = v.x;
-            kw[r][1] = v.y;
-            const __half2 s = e4m3x2_to_half2(rec[kv4_scales_at(D, 0) + row * (D / 16) + t]);
-            ks[r][0] = kv4_scale<KIND>(__low2half2(s));
+          for (int nt = 0; nt < NT; ++nt) sp[u][nt][0] = sp[u][nt][1] = sp[u][nt][2] = sp[u][nt][3] = 0.f;
+          uint32_t kw[2][KW];
+          Kv4Scale ks[2][D / 64];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int row = tk + 8 * r;
+            if (D == 128) {
+              const uint4 v = *reinterpret_cast<const uint4*>(rec + row * (D / 2) + 16 * t);
+              kw[r][0] = v.x;
+              kw[r][1] = v.y;
+              kw[r][KW - 2] = v.z;
+              kw[r][KW - 1] = v.w;
+              const __half2 s = e4m3x2_to_half2(
+                  *reinterpret_cast<const uint16_t*>(rec + kv4_scales_at(D, 0) + row * (D / 16) + 2 * t));
+              ks[r][0] = kv4_scale<KIND>(__low2half2(s));
+              ks[r][D / 64 - 1] = kv4_scale<KIND>(__high2half2(s));
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(rec + row * (D / 2) + 8 * t);
+              kw[r][0] = v.x;
+              kw[r][1] = v.y;
+              const __half2 s = e4m3x2_to_half2(rec[kv4_scales_at(D, 0) + row * (D / 16) + t]);
+              ks[r][0] = kv4_scale<KIND>(__low2half2(s));
+            }
           }
-        }
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          uint32_t a[2][4];
-          kv4_decode8<KIND>(kw[0][w], ks[0][w / 2], a[0]);
-          kv4_decode8<KIND>(kw[1][w], ks[1][w / 2], a[1]);
+          for (int w = 0; w < KW; ++w) {
+            uint32_t a[2][4];
+            kv4_decode8<KIND>(kw[0][w], ks[0][w / 2], a[0]);
+            kv4_decode8<KIND>(kw[1][w], ks[1][w / 2], a[1]);
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816(sp[nt], a[0][2 * j], a[1][2 * j], a[0][2 * j + 1], a[1][2 * j + 1], qf[nt][2 * w + j][0],
-                       qf[nt][2 * w + j][1]);
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816(sp[u][nt], a[0][2 * j], a[1][2 * j], a[0][2 * j + 1], a[1][2 * j + 1], qf[nt][2 * w + j][0],
+                         qf[nt][2 * w + j][1]);
+          }
         }
         // softmax weights
-        const bool edge = t0 + kKv4Tokens - 1 > all_seen;
-        uint32_t pb[NT][2];
+        const bool edge = t0 + kStep * kKv4Tokens - 1 > all_seen || live != 3u;
+        uint32_t pb[kStep][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float s[4], mx[2] = {-INFINITY, -INFINITY};
+          float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            s[k] = sp[nt][k] * cs;
-            if (edge && t0 + tk + 8 * (k >> 1) > lim[nt][k & 1]) s[k] = -INFINITY;
-            mx[k & 1] = fmaxf(mx[k & 1], s[k]);
-          }
-          if (__any_sync(0xffffffffu, mx[0] > m[nt][0] || mx[1] > m[nt][1])) {
+          for (int u = 0; u < kStep; ++u)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float& s = sp[u][nt][k];
+              if (edge && (t0 + u * kKv4Tokens + tk + 8 * (k >> 1) > lim[nt][k & 1] || !(live >> u & 1u))) s = -INFINITY;
+              mx[k & 1] = fmaxf(mx[k & 1], s);
+            }
+          if (__any_sync(0xffffffffu, mx[0] > m[nt][0] + room || mx[1] > m[nt][1] + room)) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
 #pragma unroll
               for (int off = 4; off < 32; off <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], off));
               const float mn = fmaxf(m[nt][c], mx[c]);
-              const float alpha = mn == -INFINITY ? 1.f : ex2_fast(m[nt][c] - mn);
+              const float alpha = m[nt][c] == -INFINITY ? 0.f : ex2_fast((m[nt][c] - mn) * cs);
               m[nt][c] = mn;
               l[nt][c] *= alpha;
 #pragma unroll
@@ -467,52 +478,64 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
               }
             }
           }
-          float w[4];
+          const float b0 = fmaf(-m[nt][0], cs, 15.f - kHeadroom), b1 = fmaf(-m[nt][1], cs, 15.f - kHeadroom);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = m[nt][k & 1] == -INFINITY ? 0.f : ex2_fast(s[k] - m[nt][k & 1]) * kPScale;
-          const __half2 h01 = __floats2half2_rn(w[0], w[1]), h23 = __floats2half2_rn(w[2], w[3]);
-          const float2 f01 = __half22float2(h01), f23 = __half22float2(h23);
-          l[nt][0] += f01.x + f23.x;
-          l[nt][1] += f01.y + f23.y;
-          pb[nt][0] = movmatrix_t(as_u32(h01));
-          pb[nt][1] = movmatrix_t(as_u32(h23));
+          for (int u = 0; u < kStep; ++u) {
+            float w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              w[k] = ex2_fast(fmaf(sp[u][nt][k], cs, k & 1 ? b1 : b0));
+              if (edge && sp[u][nt][k] == -INFINITY) w[k] = 0.f;
+            }
+            pb[u][nt][0] = movmatrix_t(as_u32(__floats2half2_rn(w[0], w[1])));
+            pb[u][nt][1] = movmatrix_t(as_u32(__floats2half2_rn(w[2], w[3])));
+            // the sum of the rounded weights, as one more row of ones
+            constexpr uint32_t kOnes = 0x3C003C00u;
+            mma16816(l[nt], kOnes, kOnes, kOnes, kOnes, pb[u][nt][0], pb[u][nt][1]);
+          }
         }
         // output
-        uint32_t vw[4][D / 64], vs[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint8_t* row = rec + kv4_codes_at(D, 1) + tv[r] * (D / 2);
-          if (D == 128) {
-            const uint2 v = *reinterpret_cast<const uint2*>(row + 8 * g);
-            vw[r][0] = v.x;
-            vw[r][D / 64 - 1] = v.y;
-            vs[r] = rec[kv4_scales_at(D, 1) + tv[r] * (D / 16) + g];
-          } else {
-            vw[r][0] = *reinterpret_cast<const uint32_t*>(row + 4 * g);
-            vs[r] = rec[kv4_scales_at(D, 1) + tv[r] * (D / 16) + (g >> 1)];
+        for (int u = 0; u < kStep; ++u) {
+          const uint8_t* rec = rec0 + u * C::kTile;
+          const bool tail = t0 + (u + 1) * kKv4Tokens > rq.len || !(live >> u & 1u);
+          uint32_t vw[4][D / 64], vs[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const uint8_t* row = rec + kv4_codes_at(D, 1) + tv[r] * (D / 2);
+            if (D == 128) {
+              const uint2 v = *reinterpret_cast<const uint2*>(row + 8 * g);
+              vw[r][0] = v.x;
+              vw[r][D / 64 - 1] = v.y;
+              vs[r] = rec[kv4_scales_at(D, 1) + tv[r] * (D / 16) + g];
+            } else {
+              vw[r][0] = *reinterpret_cast<const uint32_t*>(row + 4 * g);
+              vs[r] = rec[kv4_scales_at(D, 1) + tv[r] * (D / 16) + (g >> 1)];
+            }
+            // where there is no token the scale may be anything, a NaN too: the weights there are 0
+            if (tail && (t0 + u * kKv4Tokens + tv[r] >= rq.len || !(live >> u & 1u))) vs[r] = 0u;
           }
-          // past the end the scale may be anything, a NaN too: the weights there are 0
-          if (t0 + kKv4Tokens > rq.len && t0 + tv[r] >= rq.len) vs[r] = 0u;
-        }
-        const Kv4Scale s01 = kv4_scale<KIND>(e4m3x2_to_half2(vs[0] | (vs[1] << 8)));
-        const Kv4Scale s23 = kv4_scale<KIND>(e4m3x2_to_half2(vs[2] | (vs[3] << 8)));
+          const Kv4Scale s01 = kv4_scale<KIND>(e4m3x2_to_half2(vs[0] | (vs[1] << 8)));
+          const Kv4Scale s23 = kv4_scale<KIND>(e4m3x2_to_half2(vs[2] | (vs[3] << 8)));
 #pragma unroll
-        for (int w = 0; w < D / 64; ++w) {
-          constexpr uint32_t kLow = 0x0F0F0F0Fu;
-          uint32_t e01[4], e23[4], d01[4], d23[4];  // even and odd dims of the token pairs
-          kv4_decode8<KIND>((vw[0][w] & kLow) | ((vw[1][w] << 4) & ~kLow), s01, e01);
-          kv4_decode8<KIND>((vw[2][w] & kLow) | ((vw[3][w] << 4) & ~kLow), s23, e23);
-          kv4_decode8<KIND>(((vw[0][w] >> 4) & kLow) | (vw[1][w] & ~kLow), s01, d01);
-          kv4_decode8<KIND>(((vw[2][w] >> 4) & kLow) | (vw[3][w] & ~kLow), s23, d23);
+          for (int w = 0; w < D / 64; ++w) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+            for (int q = 0; q < 2; ++q) {
+              uint32_t h01[4], h23[4];
+              kv4_decode8<KIND>(kv4_interleave<KIND>(vw[0][w], vw[1][w], q), s01, h01);
+              kv4_decode8<KIND>(kv4_interleave<KIND>(vw[2][w], vw[3][w], q), s23, h23);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816(o[nt][4 * w + i], e01[i], d01[i], e23[i], d23[i], pb[nt][0], pb[nt][1]);
+              for (int i = 0; i < 4; i += 2)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma16816(o[nt][4 * w + 2 * q + i / 2], h01[i], h01[i + 1], h23[i], h23[i + 1], pb[u][nt][0], pb[u][nt][1]);
+            }
+          }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&s_empty[slot]));
+      __syncwarp();  // every lane has read the slot
+      ++done;
+      fetch();
     }
 
     // ---- join the warps' states
@@ -520,24 +543,28 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], off);
         const int col = 8 * nt + 2 * t + c;
         if (g == 0) {
-          s_m[warp][col] = m[nt][c];
+          // in the log2 domain (a zero scale must not meet an infinity)
+          s_m[warp][col] = m[nt][c] == -INFINITY ? -INFINITY : m[nt][c] * cs;
           s_l[warp][col] = l[nt][c];
         }
         float* dst = s_o + (warp * C::kRows + col) * C::kOStride + (D / 8) * g;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(o[nt][i][c], o[nt][i][2 + c]);
+        for (int i = 0; i < MT; ++i) {
+          // m-tile i: values 2 (i % 2), + 1 of interleaved word i / 2
+          const int w = i / 4, q = i / 2 % 2, v = 2 * (i % 2);
+          dst[8 * w + kv4_pair_dim<KIND>(q, v)] = o[nt][i][c];
+          dst[8 * w + kv4_pair_dim<KIND>(q, v + 1)] = o[nt][i][2 + c];
+        }
       }
-    compute_sync();
-    const bool whole = tile == 0 && seg == rq.tiles;
-    const long long unit = at - tile;  // the unit's first tile
+    __syncthreads();
+    const bool whole = step == 0 && seg == rq.steps;
+    const long long unit = at - step;  // the unit's first step
     const long long c0 = unit / share;
-    const int parts = static_cast<int>((unit + rq.tiles - 1) / share - c0) + 1;
+    const int parts = static_cast<int>((unit + rq.steps - 1) / share - c0) + 1;
     float* part = p.partial + (2 * static_cast<size_t>(blockIdx.x) + (c0 == blockIdx.x ? 1 : 0)) * C::kPart;
-    for (int item = tid; item < C::kRows * (D / 4); item += kComputeThreads) {
+    for (int item = tid; item < C::kRows * (D / 4); item += kThreads) {
       const int col = item / (D / 4), d = 4 * (item % (D / 4));
       if (col >= rows) continue;
       float mm = s_m[0][col];
@@ -568,16 +595,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
     }
     if (!whole) {
       __threadfence();
-      compute_sync();
+      __syncthreads();
       if (tid == 0) {
         const unsigned old = atomicAdd(p.counters + c0, 1u);
         s_last = old == static_cast<unsigned>(parts) - 1u;
         if (s_last) p.counters[c0] = 0u;
       }
-      compute_sync();
+      __syncthreads();
       if (s_last) {
         __threadfence();
-        for (int item = tid; item < C::kRows * (D / 4); item += kComputeThreads) {
+        for (int item = tid; item < C::kRows * (D / 4); item += kThreads) {
           const int col = item / (D / 4), d = 4 * (item % (D / 4));
           if (col >= rows) continue;
           const float* src = p.partial + 2 * static_cast<size_t>(c0) * C::kPart + col * (D + 4);
@@ -607,19 +634,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
         }
       }
     } else {
-      compute_sync();  // the joined states have been read
+      __syncthreads();  // the joined states have been read
     }
 
     // ---- the next unit
     f += seg;
     at += seg;
-    tile = 0;
-    if (f < run_tiles && ++kvh == hkv) {
+    step = 0;
+    if (f < run_steps && ++kvh == hkv) {
       kvh = 0;
       do rq = request_of(p, ++b, p.only);
-      while (rq.tiles == 0);
+      while (rq.steps == 0);
     }
   }
+  // a wait gave up (flagged in the device status): the copies still in flight
+  // land before the CTA's shared memory is released
+  if (!ok)
+    for (int i = max(0, fetched - kRing); i < fetched; ++i) mbar_wait(full0 + 8 * (i % kRing), (i / kRing) & 1);
 }
 
 template <typename... Params, typename... Args>
@@ -646,7 +677,7 @@ cudaError_t launch_few(const Kv4AttnParams& p, int num_sms, cudaStream_t stream)
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Small<D, NT>::kSmem);
   if (e != cudaSuccess) return e;
   const long long most = static_cast<long long>(p.batch) * p.num_kv_heads *
-                         ((static_cast<long long>(p.max_blocks) * p.block_size + kKv4Tokens - 1) / kKv4Tokens);
+                         ((static_cast<long long>(p.max_blocks) * p.per_block + kStep - 1) / kStep);
   const long long ctas = std::min<long long>((most + kMinRun - 1) / kMinRun, few_rows_ctas(NT, num_sms));
   return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), Small<D, NT>::kSmem, stream, p);
 }
@@ -681,6 +712,10 @@ cudaError_t launch_kv4_attention(const Kv4AttnParams& args, int num_sms, void* w
   p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes);
   p.share = p.num_q_heads / p.num_kv_heads;
   p.only = -1;
+  p.per_block = p.block_size / kKv4Tokens;
+  p.block_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if ((1 << i) == p.per_block) p.block_shift = i;
   if (static_cast<long long>(p.share) * p.max_query_len > kSmallRows) return launch_kv4_prompt(p, stream);
   if (p.head_dim == 64)
     return p.kind == W8A8_KV4_E2M1 ? launch_kind<W8A8_KV4_E2M1, 64>(p, num_sms, stream)

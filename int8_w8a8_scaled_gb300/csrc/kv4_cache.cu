@@ -142,10 +142,16 @@ __global__ void __launch_bounds__(kCacheThreads) kv4_read_kernel(const Kv4CacheA
     const Kv4Scale one = kv4_scale<KIND>(__float2half2_rn(1.f));
     kv4_decode8<KIND>(codes.x, one, h[0]);
     kv4_decode8<KIND>(codes.y, one, h[1]);
+    float y[16];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&h[j / 4][j % 4]));
-      const float a = c.x * s * g, b = c.y * s * g;
+      y[8 * (j / 4) + kv4_low<KIND>(j % 4)] = c.x * s * g;
+      y[8 * (j / 4) + kv4_high<KIND>(j % 4)] = c.y * s * g;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float a = y[2 * j], b = y[2 * j + 1];
       if (p.fp16) {
         const __half2 y = __floats2half2_rn(a, b);
         out[j] = *reinterpret_cast<const uint32_t*>(&y);

@@ -25,9 +25,9 @@ __device__ __forceinline__ float load16(const void* p, int fp16, size_t i) {
 template <int KIND>
 __device__ __forceinline__ float code_value(const uint8_t* row, const uint8_t* scales, int d) {
   uint32_t h[4];
-  kv4_decode8<KIND>(row[d / 2], kv4_scale<KIND>(e4m3x2_to_half2(scales[d / kKv4Group] * 0x101u)), h);
+  kv4_decode8<KIND>(row[d / 2] >> (4 * (d & 1)), kv4_scale<KIND>(e4m3x2_to_half2(scales[d / kKv4Group] * 0x101u)), h);
   const __half2 v = *reinterpret_cast<const __half2*>(&h[0]);
-  return d & 1 ? __high2float(v) : __low2float(v);
+  return __low2float(v);
 }
 
 template <int KIND>
