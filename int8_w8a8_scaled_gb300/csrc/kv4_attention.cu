@@ -6,15 +6,19 @@
 //
 // ---- Work
 // A unit is one request and KV head: its n new tokens times the G query heads
-// that share the KV head are `rows` rows over the same tokens, taken 16 at a
-// time (a tile: one record of the cache).  All units' steps of kStep tiles in a row, request
-// by request and head by head, are cut into equal runs, one for each CTA, so
-// that ragged lengths load the SMs evenly.  A unit that lies in one run is
-// written out by its CTA.  One that is cut leaves a partial result (maximum,
-// sum, unnormalised output of each row) in the workspace from each CTA, and
-// the last of them to arrive joins the parts, in their order.  Every CTA
-// makes the sum over the requests' lengths that finds its run itself, so the
-// split follows the lengths on the device and one launch does it all.
+// that share the KV head are `rows` rows over the same tokens, taken in steps
+// of kStep tiles (a tile: the 16 tokens of one record).  All units' steps in a
+// row, request by request and head by head, are cut into equal runs, one for
+// each warp of the grid, so that ragged lengths load the SMs evenly.  A warp
+// goes through its run alone: no barrier, no other warp's data.  A unit that
+// lies in one run is written out by its warp; one that is cut leaves a piece
+// (maximum, sum, unnormalised output of each row) with each of its warps.  At
+// the end the CTA joins its warps' pieces; a unit that goes on in other CTAs
+// leaves a part in the workspace, and the last CTA to arrive joins the parts.
+// Pieces and parts are joined in the order of their tokens, so the result does
+// not depend on timing.  Every CTA makes the sum over the requests' lengths
+// that finds its run itself: the split follows the lengths on the device, and
+// one launch does it all.
 //
 // ---- Few rows (up to 16): mma.sync
 // Bound by the cache's bytes, 18 head_dim a tile, as long as the decoding
@@ -30,13 +34,12 @@
 // only when a score passes it by more than 8 (2^15 then, f16's last power of
 // two): the state is rescaled once or twice a unit, not at every new maximum.
 //
-// Eight warps take the steps of a run in turn (a step: kStep tiles, decoded
-// together so that one's latencies hide behind the other's), each with a softmax
-// state of its own, joined in shared memory at the end of a unit.  A warp
-// copies its next step's records (untiled bulk copies) as soon as it has read
-// a slot of its ring, across the ends of units, so that the copies go on
-// while the states are joined.  A producer warp in place of that cost a
-// fifth of the issue slots in polling, and its registers.
+// A warp copies its next step's records (untiled bulk copies) as soon as it
+// has read a slot of its ring, across the ends of units.  (A producer warp in
+// place of that cost a fifth of the issue slots in polling, and its
+// registers; units shared by a CTA's warps and joined one by one cost 10 us
+// of barriers and cold loads each.)  The two tiles of a step are decoded
+// together, so that one's latencies hide behind the other's.
 //
 // Registers (lane = 4 g + t).  The dot product does not depend on the order
 // of the dims, nor the sum over tokens on theirs, so both are permuted to
@@ -65,7 +68,6 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 2;                         // tiles of a step
 constexpr int kRing = 2;                         // steps in a warp's ring
-constexpr int kMinRun = kWarps;                  // steps of a CTA's run: one a warp at least
 constexpr int kSmallRows = 16;
 constexpr float kHeadroom = 8.f;
 constexpr int kMaxCounters = 1024;               // CTAs that may leave a unit open
@@ -101,11 +103,16 @@ __device__ __forceinline__ Request request_of(const Kv4AttnParams& p, int b, int
   return r;
 }
 
-// Where a CTA's run begins.
+// Where a warp's run begins: the request, and the steps in front of it.
 struct Start {
-  long long total;  // steps of all units
-  long long before; // steps in front of request b
+  long long before;
   int b;
+};
+
+// A cut unit's share of one run.
+struct Piece {
+  long long unit;  // the unit's first step; -1: no piece
+  int b, kvh;
 };
 
 // ------------------------------------------------------------------ pieces
@@ -133,16 +140,21 @@ __device__ __forceinline__ float ex2_fast(float x) {
 
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
+// The first output element of a unit's row.
+__device__ __forceinline__ size_t out_at(const Kv4AttnParams& p, const Request& rq, int kvh, int row) {
+  return (rq.first + row / p.share) * p.out_token_stride + (kvh * p.share + row % p.share) * p.out_head_stride;
+}
+
 // 4 consecutive outputs.
-__device__ __forceinline__ void store4(const Kv4AttnParams& p, size_t at, const float (&y)[4]) {
+__device__ __forceinline__ void store4(const Kv4AttnParams& p, size_t at, float a, float b, float c, float d) {
   uint32_t w[2];
   if (p.out_fp16) {
-    w[0] = as_u32(__floats2half2_rn(y[0], y[1]));
-    w[1] = as_u32(__floats2half2_rn(y[2], y[3]));
+    w[0] = as_u32(__floats2half2_rn(a, b));
+    w[1] = as_u32(__floats2half2_rn(c, d));
   } else {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(y[0], y[1]), b = __floats2bfloat162_rn(y[2], y[3]);
-    w[0] = *reinterpret_cast<const uint32_t*>(&a);
-    w[1] = *reinterpret_cast<const uint32_t*>(&b);
+    const __nv_bfloat162 x = __floats2bfloat162_rn(a, b), y = __floats2bfloat162_rn(c, d);
+    w[0] = *reinterpret_cast<const uint32_t*>(&x);
+    w[1] = *reinterpret_cast<const uint32_t*>(&y);
   }
   uint16_t* dst = static_cast<uint16_t*>(p.out) + at;
   if (p.out_vec) {
@@ -155,6 +167,23 @@ __device__ __forceinline__ void store4(const Kv4AttnParams& p, size_t at, const 
   }
 }
 
+// Softmax states of one row and 4 dims, joined one by one.
+struct Joined {
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void add(float2 ml, float4 v) {
+    const float mn = fmaxf(m, ml.x);
+    const float a = m == -INFINITY ? 0.f : ex2_fast(m - mn), c = ml.x == -INFINITY ? 0.f : ex2_fast(ml.x - mn);
+    m = mn;
+    l = fmaf(a, l, c * ml.y);
+    o = make_float4(fmaf(a, o.x, c * v.x), fmaf(a, o.y, c * v.y), fmaf(a, o.z, c * v.z), fmaf(a, o.w, c * v.w));
+  }
+  __device__ __forceinline__ void store(const Kv4AttnParams& p, size_t at, float vscale) const {
+    const float inv = l > 0.f ? vscale / l : 0.f;
+    store4(p, at, o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  }
+};
+
 // ------------------------------------------------------------------ few rows
 
 template <int D, int NT>
@@ -163,10 +192,10 @@ struct Small {
   static constexpr int kTile = kv4_record_bytes(D);
   static constexpr int kSlot = kStep * kTile;
   static constexpr int kRingBytes = kWarps * kRing * kSlot;
-  static constexpr int kOStride = D + 4;                   // a row's o in shared memory
-  static constexpr int kJoin = kWarps * kRows * kOStride * 4;
-  static constexpr int kSmem = kRingBytes + kJoin;
-  static constexpr int kPart = kRows * (D + 4);            // floats of a partial result: o, then m, l of each row
+  static constexpr int kOStride = D + 4;                   // a row of a piece
+  static constexpr int kPiece = kRows * kOStride;          // floats: o, m, l of each row
+  static constexpr int kSmem = kRingBytes + kWarps * kPiece * 4;
+  static_assert(kPiece * 4 <= kRing * kSlot, "a warp's ring holds its last piece");
 };
 
 template <int KIND, int D, int NT>
@@ -175,23 +204,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
   constexpr int KW = D / 32;   // words of K codes a lane holds of a token
   constexpr int MT = D / 16;   // m-tiles of the output product, k-blocks of the scores'
   extern __shared__ __align__(128) uint8_t smem[];
-  float* s_o = reinterpret_cast<float*>(smem + C::kRingBytes);
+  float* const heads = reinterpret_cast<float*>(smem + C::kRingBytes);  // [kWarps] pieces of units begun in front of a run
   __shared__ uint64_t s_full[kWarps][kRing];
-  __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
   __shared__ long long s_scan[kWarps];
-  __shared__ Start s_start;
-  __shared__ int s_last;
+  __shared__ Start s_start[kWarps];
+  __shared__ Piece s_piece[2 * kWarps];  // in the order of their tokens
+  __shared__ int s_last[2];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
   if (tid == 0) {
     for (int i = 0; i < kWarps * kRing; ++i) mbar_init(smem_addr(&s_full[0][0] + i), kStep);
     fence_barrier_init();
   }
+  if (tid < 2 * kWarps) s_piece[tid].unit = -1;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // ---- this CTA's run of tiles
+  // ---- the runs
   const int hkv = p.num_kv_heads;
+  long long total = 0, share;
   {
     const int per = (p.batch + kThreads - 1) / kThreads;
     const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
@@ -205,43 +236,43 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
     }
     if (lane == 31) s_scan[warp] = run;
     __syncthreads();
-    long long total = 0;
     run -= mine;
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) run += s_scan[w];
       total += s_scan[w];
     }
-    const long long share = max(static_cast<long long>(kMinRun), (total + gridDim.x - 1) / gridDim.x);
-    const long long r0 = share * blockIdx.x;
-    if (r0 >= run && r0 < run + mine) {
+    share = (total + static_cast<long long>(gridDim.x) * kWarps - 1) / (static_cast<long long>(gridDim.x) * kWarps);
+    for (int w = 0; w < kWarps && mine > 0; ++w) {
+      const long long at = share * (static_cast<long long>(blockIdx.x) * kWarps + w);
+      if (at < run || at >= run + mine) continue;
+      long long before = run;
       for (int b = b0; b < b1; ++b) {
-        const long long w = static_cast<long long>(request_of(p, b, p.only).steps) * hkv;
-        if (r0 < run + w) {
-          s_start.b = b;
-          s_start.before = run;
+        const long long steps = static_cast<long long>(request_of(p, b, p.only).steps) * hkv;
+        if (at < before + steps) {
+          s_start[w].b = b;
+          s_start[w].before = before;
           break;
         }
-        run += w;
+        before += steps;
       }
     }
-    if (tid == 0) s_start.total = total;
   }
   __syncthreads();
-  const long long total = s_start.total;
-  const long long share = max(static_cast<long long>(kMinRun), (total + gridDim.x - 1) / gridDim.x);
-  const long long r0 = share * blockIdx.x, r1 = min(total, r0 + share);
-  if (r0 >= r1) return;
-  int b = s_start.b;
-  Request rq = request_of(p, b, p.only);
-  int kvh = static_cast<int>((r0 - s_start.before) / rq.steps);
-  int step = static_cast<int>((r0 - s_start.before) % rq.steps);
-  const int run_steps = static_cast<int>(min(r1 - r0, 0x7fffffffLL));
-
-  // ---- the warp's steps: warp, warp + 8, ... of the run.  The fetching end is
-  // up to kRing steps ahead of the computing one.
-  const uint64_t pol = policy_evict_first();
+  if (share * kWarps * blockIdx.x >= total) return;
+  const long long r0 = share * (static_cast<long long>(blockIdx.x) * kWarps + warp), r1 = min(total, r0 + share);
+  const int run_steps = static_cast<int>(max(0LL, min(r1 - r0, 0x7fffffffLL)));
+  const float kscale = __ldg(p.k_scale), vscale = __ldg(p.v_scale);
   const uint32_t full0 = smem_addr(&s_full[warp][0]);
   uint8_t* const ring = smem + warp * kRing * C::kSlot;
+  bool ok = true;
+  if (run_steps > 0) {
+  int b = s_start[warp].b;
+  Request rq = request_of(p, b, p.only);
+  int kvh = static_cast<int>((r0 - s_start[warp].before) / rq.steps);
+  int step = static_cast<int>((r0 - s_start[warp].before) % rq.steps);
+
+  // ---- fetching, up to kRing steps ahead of the computation
+  const uint64_t pol = policy_evict_first();
   // The places of a batch of 16 steps are looked up at once: lane 2 k + u has
   // record u of the batch's step k, and copies it when its turn comes.
   constexpr int kBatch = 32 / kStep;
@@ -252,9 +283,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
   uint32_t found = 0u;           // the lanes whose record lies in the cache
   uint32_t live_bits = 0u;       // the same of the steps in the ring
   auto fetch = [&] {
-    if (warp + kWarps * fetched >= run_steps) return;
+    if (fetched >= run_steps) return;
     if (fetched % kBatch == 0) {
-      const int want = warp + kWarps * (fetched + lane / kStep);
+      const int want = fetched + lane / kStep;
       bool in = want < run_steps;
       if (in) {
         fstep += want - fpos;
@@ -300,13 +331,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
   const int g = lane >> 2, t = lane & 3;
   const int tk = (g >> 1) + (g & 1 ? 4 - (g >> 1) + ((g >> 1) ^ 1) : 0);  // token of row g
   const int tv[4] = {t, 4 + (t ^ 1), 8 + t, 12 + (t ^ 1)};                // tokens of rows 2t, 2t + 1, 2t + 8, 2t + 9
-  const float kscale = __ldg(p.k_scale), vscale = __ldg(p.v_scale);
-  bool ok = true;
-  int done = 0;  // steps this warp has computed
-  int f = 0;  // steps of the run in front of this unit
-  long long at = r0;
-  while (f < run_steps) {
-    const int seg = min(rq.steps - step, run_steps - f);  // this unit's steps in the run
+  int done = 0;  // steps computed
+  while (done < run_steps) {
+    const int seg = min(rq.steps - step, run_steps - done);  // this unit's steps in the run
     const int rows = rq.n * p.share;
 
     // the query: dims D/4 t .. of row g (and 8 + g), scaled by 2^e so that the largest lies in [2^14, 2^15)
@@ -397,8 +424,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
       for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
     }
 
-    // steps f + x of the run, x < seg, with (f + x) % kWarps == warp
-    for (int x = (warp - f % kWarps + kWarps) % kWarps; x < seg; x += kWarps) {
+    for (int x = 0; x < seg; ++x) {
       const int slot = done % kRing;
       if (ok) ok = mbar_wait(full0 + 8 * slot, (done / kRing) & 1);
       const uint32_t live = ok ? (live_bits >> (kStep * slot)) & 3u : 0u;
@@ -538,110 +564,46 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
       fetch();
     }
 
-    // ---- join the warps' states
+    // ---- the unit's end, or the run's: lane (g, t) has dims D/8 g .. of the columns 2t, 2t + 1
+    const bool ends = step + seg == rq.steps;
+    const bool last = done == run_steps;
+    const bool whole = step == 0 && ends;
+    if (!whole && last) __syncwarp();  // the ring's last slot has been read: it takes the piece
+    float* piece = last ? reinterpret_cast<float*>(ring) : heads + warp * C::kPiece;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int col = 8 * nt + 2 * t + c;
-        if (g == 0) {
-          // in the log2 domain (a zero scale must not meet an infinity)
-          s_m[warp][col] = m[nt][c] == -INFINITY ? -INFINITY : m[nt][c] * cs;
-          s_l[warp][col] = l[nt][c];
-        }
-        float* dst = s_o + (warp * C::kRows + col) * C::kOStride + (D / 8) * g;
+        float y[D / 8];
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           // m-tile i: values 2 (i % 2), + 1 of interleaved word i / 2
           const int w = i / 4, q = i / 2 % 2, v = 2 * (i % 2);
-          dst[8 * w + kv4_pair_dim<KIND>(q, v)] = o[nt][i][c];
-          dst[8 * w + kv4_pair_dim<KIND>(q, v + 1)] = o[nt][i][2 + c];
+          y[8 * w + kv4_pair_dim<KIND>(q, v)] = o[nt][i][c];
+          y[8 * w + kv4_pair_dim<KIND>(q, v + 1)] = o[nt][i][2 + c];
+        }
+        if (col >= rows) continue;
+        if (whole) {
+          const float inv = l[nt][c] > 0.f ? vscale / l[nt][c] : 0.f;
+          const size_t at = out_at(p, rq, kvh, col) + (D / 8) * g;
+#pragma unroll
+          for (int i = 0; i < D / 8; i += 4) store4(p, at + i, y[i] * inv, y[i + 1] * inv, y[i + 2] * inv, y[i + 3] * inv);
+        } else {
+          float* dst = piece + col * C::kOStride + (D / 8) * g;
+#pragma unroll
+          for (int i = 0; i < D / 8; i += 4) *reinterpret_cast<float4*>(dst + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+          // m in the log2 domain (a zero scale must not meet an infinity)
+          if (g == 0)
+            *reinterpret_cast<float2*>(piece + col * C::kOStride + D) =
+                make_float2(m[nt][c] == -INFINITY ? -INFINITY : m[nt][c] * cs, l[nt][c]);
         }
       }
-    __syncthreads();
-    const bool whole = step == 0 && seg == rq.steps;
-    const long long unit = at - step;  // the unit's first step
-    const long long c0 = unit / share;
-    const int parts = static_cast<int>((unit + rq.steps - 1) / share - c0) + 1;
-    float* part = p.partial + (2 * static_cast<size_t>(blockIdx.x) + (c0 == blockIdx.x ? 1 : 0)) * C::kPart;
-    for (int item = tid; item < C::kRows * (D / 4); item += kThreads) {
-      const int col = item / (D / 4), d = 4 * (item % (D / 4));
-      if (col >= rows) continue;
-      float mm = s_m[0][col];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][col]);
-      float ll = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-      if (mm != -INFINITY) {
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float a = ex2_fast(s_m[w][col] - mm);
-          const float4 v = *reinterpret_cast<const float4*>(s_o + (w * C::kRows + col) * C::kOStride + d);
-          ll = fmaf(a, s_l[w][col], ll);
-          y[0] = fmaf(a, v.x, y[0]);
-          y[1] = fmaf(a, v.y, y[1]);
-          y[2] = fmaf(a, v.z, y[2]);
-          y[3] = fmaf(a, v.w, y[3]);
-        }
-      }
-      if (whole) {
-        const float inv = ll > 0.f ? vscale / ll : 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] *= inv;
-        store4(p, (rq.first + col / p.share) * p.out_token_stride + (kvh * p.share + col % p.share) * p.out_head_stride + d, y);
-      } else {
-        __stcg(reinterpret_cast<float4*>(part + col * (D + 4) + d), make_float4(y[0], y[1], y[2], y[3]));
-        if (d == 0) __stcg(reinterpret_cast<float2*>(part + col * (D + 4) + D), make_float2(mm, ll));
-      }
-    }
-    if (!whole) {
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const unsigned old = atomicAdd(p.counters + c0, 1u);
-        s_last = old == static_cast<unsigned>(parts) - 1u;
-        if (s_last) p.counters[c0] = 0u;
-      }
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        for (int item = tid; item < C::kRows * (D / 4); item += kThreads) {
-          const int col = item / (D / 4), d = 4 * (item % (D / 4));
-          if (col >= rows) continue;
-          const float* src = p.partial + 2 * static_cast<size_t>(c0) * C::kPart + col * (D + 4);
-          // part 0 is the second place of CTA c0, part j the first of CTA c0 + j
-          float mm = -INFINITY;
-#pragma unroll 8
-          for (int j = 0; j < parts; ++j) mm = fmaxf(mm, __ldcg(src + (j ? 2 * j : 1) * static_cast<size_t>(C::kPart) + D));
-          float ll = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-          if (mm != -INFINITY) {
-#pragma unroll 8
-            for (int j = 0; j < parts; ++j) {
-              const float* q = src + (j ? 2 * j : 1) * static_cast<size_t>(C::kPart);
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(q + D));
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(q + d));
-              const float a = ex2_fast(ml.x - mm);
-              ll = fmaf(a, ml.y, ll);
-              y[0] = fmaf(a, v.x, y[0]);
-              y[1] = fmaf(a, v.y, y[1]);
-              y[2] = fmaf(a, v.z, y[2]);
-              y[3] = fmaf(a, v.w, y[3]);
-            }
-          }
-          const float inv = ll > 0.f ? vscale / ll : 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] *= inv;
-          store4(p, (rq.first + col / p.share) * p.out_token_stride + (kvh * p.share + col % p.share) * p.out_head_stride + d, y);
-        }
-      }
-    } else {
-      __syncthreads();  // the joined states have been read
-    }
+    if (!whole && lane == 0) s_piece[2 * warp + last] = {r0 + done - seg - step, b, kvh};
 
     // ---- the next unit
-    f += seg;
-    at += seg;
     step = 0;
-    if (f < run_steps && ++kvh == hkv) {
+    if (!last && ++kvh == hkv) {
       kvh = 0;
       do rq = request_of(p, ++b, p.only);
       while (rq.steps == 0);
@@ -651,6 +613,92 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
   // land before the CTA's shared memory is released
   if (!ok)
     for (int i = max(0, fetched - kRing); i < fetched; ++i) mbar_wait(full0 + 8 * (i % kRing), (i / kRing) & 1);
+  }
+  __syncthreads();
+
+  // ---- join the warps' pieces
+  const long long cta_share = share * kWarps;
+  int part_b[2] = {-1, -1}, part_kvh[2];  // units that go on in other CTAs: the one begun before this CTA, the one begun here
+  long long part_unit[2];
+  for (int i = 0; i < 2 * kWarps;) {
+    const Piece first = s_piece[i];
+    if (first.unit < 0) {
+      ++i;
+      continue;
+    }
+    int end = i + 1;  // the unit's pieces: i .. end - 1, with gaps
+    for (int k = i + 1; k < 2 * kWarps; ++k) {
+      if (s_piece[k].unit == first.unit) end = k + 1;
+      else if (s_piece[k].unit >= 0) break;
+    }
+    const Request rq = request_of(p, first.b, p.only);
+    const int rows = rq.n * p.share;
+    const long long c0 = first.unit / cta_share, c1 = (first.unit + rq.steps - 1) / cta_share;
+    const bool whole = c0 == c1;
+    const int which = c0 == blockIdx.x;
+    float* part = p.partial + (2 * static_cast<size_t>(blockIdx.x) + which) * C::kPiece;
+    for (int item = tid; item < C::kRows * (D / 4); item += kThreads) {
+      const int col = item / (D / 4), d = 4 * (item % (D / 4));
+      if (col >= rows) continue;
+      Joined sum;
+      for (int k = i; k < end; ++k) {
+        if (s_piece[k].unit < 0) continue;
+        const float* src = (k & 1 ? reinterpret_cast<const float*>(smem + (k / 2) * kRing * C::kSlot) : heads + (k / 2) * C::kPiece) +
+                           col * C::kOStride;
+        sum.add(*reinterpret_cast<const float2*>(src + D), *reinterpret_cast<const float4*>(src + d));
+      }
+      if (whole) {
+        sum.store(p, out_at(p, rq, first.kvh, col) + d, vscale);
+      } else {
+        __stcg(reinterpret_cast<float4*>(part + col * C::kOStride + d), sum.o);
+        if (d == 0) __stcg(reinterpret_cast<float2*>(part + col * C::kOStride + D), make_float2(sum.m, sum.l));
+      }
+    }
+    if (!whole) {
+      part_b[which] = first.b;
+      part_kvh[which] = first.kvh;
+      part_unit[which] = first.unit;
+    }
+    i = end;
+  }
+  if (part_b[0] < 0 && part_b[1] < 0) return;
+
+  // ---- join the CTAs' parts of a unit, in the last CTA to arrive
+  __threadfence();
+  __syncthreads();
+  if (tid < 2) {
+    s_last[tid] = 0;
+    const int pb = tid ? part_b[1] : part_b[0];
+    if (pb >= 0) {
+      const long long unit = tid ? part_unit[1] : part_unit[0];
+      const long long c0 = unit / cta_share, c1 = (unit + request_of(p, pb, p.only).steps - 1) / cta_share;
+      s_last[tid] = atomicAdd(p.counters + c0, 1u) == static_cast<unsigned>(c1 - c0);
+      if (s_last[tid]) p.counters[c0] = 0u;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    if (part_b[which] < 0 || !s_last[which]) continue;
+    __threadfence();
+    const Request rq = request_of(p, part_b[which], p.only);
+    const int rows = rq.n * p.share;
+    const long long c0 = part_unit[which] / cta_share;
+    const int parts = static_cast<int>((part_unit[which] + rq.steps - 1) / cta_share - c0) + 1;
+    for (int item = tid; item < C::kRows * (D / 4); item += kThreads) {
+      const int col = item / (D / 4), d = 4 * (item % (D / 4));
+      if (col >= rows) continue;
+      // part 0 is the second place of CTA c0, part k the first of CTA c0 + k
+      const float* src = p.partial + 2 * static_cast<size_t>(c0) * C::kPiece + col * C::kOStride;
+      Joined sum;
+#pragma unroll 8
+      for (int k = 0; k < parts; ++k) {
+        const float* s = src + (k ? 2 * k : 1) * static_cast<size_t>(C::kPiece);
+        sum.add(__ldcg(reinterpret_cast<const float2*>(s + D)), __ldcg(reinterpret_cast<const float4*>(s + d)));
+      }
+      sum.store(p, out_at(p, rq, part_kvh[which], col) + d, vscale);
+    }
+  }
 }
 
 template <typename... Params, typename... Args>
@@ -678,7 +726,7 @@ cudaError_t launch_few(const Kv4AttnParams& p, int num_sms, cudaStream_t stream)
   if (e != cudaSuccess) return e;
   const long long most = static_cast<long long>(p.batch) * p.num_kv_heads *
                          ((static_cast<long long>(p.max_blocks) * p.per_block + kStep - 1) / kStep);
-  const long long ctas = std::min<long long>((most + kMinRun - 1) / kMinRun, few_rows_ctas(NT, num_sms));
+  const long long ctas = std::min<long long>((most + kWarps - 1) / kWarps, few_rows_ctas(NT, num_sms));
   return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), Small<D, NT>::kSmem, stream, p);
 }
 
