@@ -70,6 +70,7 @@ constexpr int kStep = 2;                         // tiles of a step
 constexpr int kRing = 2;                         // steps in a warp's ring
 constexpr int kSmallRows = 16;
 constexpr float kHeadroom = 8.f;
+constexpr float kNoScore = -1e30f;               // below any product, and finite
 constexpr int kMaxCounters = 1024;               // CTAs that may leave a unit open
 constexpr size_t kCounterBytes = kMaxCounters * sizeof(unsigned);
 
@@ -119,8 +120,7 @@ struct Piece {
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -383,7 +383,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
       cs = p.sm_scale * kscale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
       // the scale's sign goes to the query: the largest product is the largest score
       const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), cs);
-      cs = fabsf(cs);
+      // (no zero, so that a masked score's infinity stays one)
+      cs = fmaxf(fabsf(cs), 1e-37f);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -418,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
     float m[NT][2], l[NT][4], o[NT][MT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = kNoScore;
       l[nt][0] = l[nt][1] = l[nt][2] = l[nt][3] = 0.f;
 #pragma unroll
       for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
@@ -476,6 +477,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
         }
         // softmax weights
         const bool edge = t0 + kStep * kKv4Tokens - 1 > all_seen || live != 3u;
+        if (edge) {
+          asm volatile("");  // a branch, not a select for every score of every step
+#pragma unroll
+          for (int u = 0; u < kStep; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (t0 + u * kKv4Tokens + tk + 8 * (k >> 1) > lim[nt][k & 1] || !(live >> u & 1u)) sp[u][nt][k] = -INFINITY;
+        }
         uint32_t pb[kStep][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -483,18 +494,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
 #pragma unroll
           for (int u = 0; u < kStep; ++u)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float& s = sp[u][nt][k];
-              if (edge && (t0 + u * kKv4Tokens + tk + 8 * (k >> 1) > lim[nt][k & 1] || !(live >> u & 1u))) s = -INFINITY;
-              mx[k & 1] = fmaxf(mx[k & 1], s);
-            }
+            for (int k = 0; k < 4; ++k) mx[k & 1] = fmaxf(mx[k & 1], sp[u][nt][k]);
           if (__any_sync(0xffffffffu, mx[0] > m[nt][0] + room || mx[1] > m[nt][1] + room)) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
 #pragma unroll
               for (int off = 4; off < 32; off <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], off));
               const float mn = fmaxf(m[nt][c], mx[c]);
-              const float alpha = m[nt][c] == -INFINITY ? 0.f : ex2_fast((m[nt][c] - mn) * cs);
+              const float alpha = ex2_fast((m[nt][c] - mn) * cs);
               m[nt][c] = mn;
               l[nt][c] *= alpha;
 #pragma unroll
@@ -509,10 +516,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
           for (int u = 0; u < kStep; ++u) {
             float w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              w[k] = ex2_fast(fmaf(sp[u][nt][k], cs, k & 1 ? b1 : b0));
-              if (edge && sp[u][nt][k] == -INFINITY) w[k] = 0.f;
-            }
+            for (int k = 0; k < 4; ++k) w[k] = ex2_fast(fmaf(sp[u][nt][k], cs, k & 1 ? b1 : b0));
             pb[u][nt][0] = movmatrix_t(as_u32(__floats2half2_rn(w[0], w[1])));
             pb[u][nt][1] = movmatrix_t(as_u32(__floats2half2_rn(w[2], w[3])));
             // the sum of the rounded weights, as one more row of ones
@@ -538,11 +542,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
               vw[r][0] = *reinterpret_cast<const uint32_t*>(row + 4 * g);
               vs[r] = rec[kv4_scales_at(D, 1) + tv[r] * (D / 16) + (g >> 1)];
             }
-            // where there is no token the scale may be anything, a NaN too: the weights there are 0
-            if (tail && (t0 + u * kKv4Tokens + tv[r] >= rq.len || !(live >> u & 1u))) vs[r] = 0u;
           }
-          const Kv4Scale s01 = kv4_scale<KIND>(e4m3x2_to_half2(vs[0] | (vs[1] << 8)));
-          const Kv4Scale s23 = kv4_scale<KIND>(e4m3x2_to_half2(vs[2] | (vs[3] << 8)));
+          if (tail) {
+            // where there is no token the scale may be anything, a NaN too: the weights there are 0
+            asm volatile("");
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (t0 + u * kKv4Tokens + tv[r] >= rq.len || !(live >> u & 1u)) vs[r] = 0u;
+          }
+          const Kv4Scale s01 = kv4_scale<KIND>(e4m3x2_to_half2(__byte_perm(vs[0], vs[1], 0x0040)));
+          const Kv4Scale s23 = kv4_scale<KIND>(e4m3x2_to_half2(__byte_perm(vs[2], vs[3], 0x0040)));
 #pragma unroll
           for (int w = 0; w < D / 64; ++w) {
 #pragma unroll
@@ -593,10 +602,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
           float* dst = piece + col * C::kOStride + (D / 8) * g;
 #pragma unroll
           for (int i = 0; i < D / 8; i += 4) *reinterpret_cast<float4*>(dst + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-          // m in the log2 domain (a zero scale must not meet an infinity)
-          if (g == 0)
+          if (g == 0)  // m in the log2 domain
             *reinterpret_cast<float2*>(piece + col * C::kOStride + D) =
-                make_float2(m[nt][c] == -INFINITY ? -INFINITY : m[nt][c] * cs, l[nt][c]);
+                make_float2(l[nt][c] > 0.f ? m[nt][c] * cs : -INFINITY, l[nt][c]);
         }
       }
     if (!whole && lane == 0) s_piece[2 * warp + last] = {r0 + done - seg - step, b, kvh};
