@@ -106,14 +106,14 @@ __device__ __forceinline__ Request request_of(const Kv4AttnParams& p, int b, int
 
 // Where a warp's run begins: the request, and the steps in front of it.
 struct Start {
-  long long before;
-  int b;
+  int b, before;
 };
 
 // A cut unit's share of one run.
 struct Piece {
-  long long unit;  // the unit's first step; -1: no piece
-  int b, kvh;
+  int unit;  // the unit's first step; -1: no piece
+  int steps; // the unit's
+  int first, n, kvh;
 };
 
 // ------------------------------------------------------------------ pieces
@@ -141,8 +141,8 @@ __device__ __forceinline__ float ex2_fast(float x) {
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
 // The first output element of a unit's row.
-__device__ __forceinline__ size_t out_at(const Kv4AttnParams& p, const Request& rq, int kvh, int row) {
-  return (rq.first + row / p.share) * p.out_token_stride + (kvh * p.share + row % p.share) * p.out_head_stride;
+__device__ __forceinline__ size_t out_at(const Kv4AttnParams& p, int first, int kvh, int row) {
+  return (first + row / p.share) * p.out_token_stride + (kvh * p.share + row % p.share) * p.out_head_stride;
 }
 
 // 4 consecutive outputs.
@@ -167,16 +167,15 @@ __device__ __forceinline__ void store4(const Kv4AttnParams& p, size_t at, float 
   }
 }
 
-// Softmax states of one row and 4 dims, joined one by one.
+// Softmax states of one row and 4 dims, joined: m their largest maximum,
+// known first.
 struct Joined {
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   __device__ __forceinline__ void add(float2 ml, float4 v) {
-    const float mn = fmaxf(m, ml.x);
-    const float a = m == -INFINITY ? 0.f : ex2_fast(m - mn), c = ml.x == -INFINITY ? 0.f : ex2_fast(ml.x - mn);
-    m = mn;
-    l = fmaf(a, l, c * ml.y);
-    o = make_float4(fmaf(a, o.x, c * v.x), fmaf(a, o.y, c * v.y), fmaf(a, o.z, c * v.z), fmaf(a, o.w, c * v.w));
+    const float a = ml.x == -INFINITY ? 0.f : ex2_fast(ml.x - m);
+    l = fmaf(a, ml.y, l);
+    o = make_float4(fmaf(a, v.x, o.x), fmaf(a, v.y, o.y), fmaf(a, v.z, o.z), fmaf(a, v.w, o.w));
   }
   __device__ __forceinline__ void store(const Kv4AttnParams& p, size_t at, float vscale) const {
     const float inv = l > 0.f ? vscale / l : 0.f;
@@ -206,13 +205,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
   extern __shared__ __align__(128) uint8_t smem[];
   float* const heads = reinterpret_cast<float*>(smem + C::kRingBytes);  // [kWarps] pieces of units begun in front of a run
   __shared__ uint64_t s_full[kWarps][kRing];
-  __shared__ long long s_scan[kWarps];
+  __shared__ int s_scan[kWarps];
   __shared__ Start s_start[kWarps];
   __shared__ Piece s_piece[2 * kWarps];  // in the order of their tokens
   __shared__ int s_last[2];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
   if (tid == 0) {
+#pragma unroll 1
     for (int i = 0; i < kWarps * kRing; ++i) mbar_init(smem_addr(&s_full[0][0] + i), kStep);
     fence_barrier_init();
   }
@@ -220,47 +220,54 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // ---- the runs
-  const int hkv = p.num_kv_heads;
-  long long total = 0, share;
+  // ---- the runs (all units' steps are fewer than 2^31, the launcher sees to it)
+  const int hkv = p.num_kv_heads, workers = static_cast<int>(gridDim.x) * kWarps;
+  int total = 0, share;
   {
     const int per = (p.batch + kThreads - 1) / kThreads;
     const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += static_cast<long long>(request_of(p, b, p.only).steps) * hkv;
-    long long run = mine;
-#pragma unroll
+    int mine = 0;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) mine += request_of(p, b, p.only).steps * hkv;
+    int run = mine;
+#pragma unroll 1
     for (int off = 1; off < 32; off <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, run, off);
+      const int o = __shfl_up_sync(0xffffffffu, run, off);
       if (lane >= off) run += o;
     }
     if (lane == 31) s_scan[warp] = run;
     __syncthreads();
     run -= mine;
+#pragma unroll 1
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) run += s_scan[w];
       total += s_scan[w];
     }
-    share = (total + static_cast<long long>(gridDim.x) * kWarps - 1) / (static_cast<long long>(gridDim.x) * kWarps);
-    for (int w = 0; w < kWarps && mine > 0; ++w) {
-      const long long at = share * (static_cast<long long>(blockIdx.x) * kWarps + w);
-      if (at < run || at >= run + mine) continue;
-      long long before = run;
-      for (int b = b0; b < b1; ++b) {
-        const long long steps = static_cast<long long>(request_of(p, b, p.only).steps) * hkv;
-        if (at < before + steps) {
-          s_start[w].b = b;
-          s_start[w].before = before;
-          break;
+    share = static_cast<int>((static_cast<unsigned>(total) + workers - 1u) / workers);
+    // the runs of this CTA's warps that begin in the thread's requests
+    if (mine > 0) {
+#pragma unroll 1
+      for (int w = 0; w < kWarps; ++w) {
+        const long long at = static_cast<long long>(share) * (blockIdx.x * kWarps + w);
+        if (at < run || at >= static_cast<long long>(run) + mine) continue;
+        int before = run;
+#pragma unroll 1
+        for (int b = b0; b < b1; ++b) {
+          const int steps = request_of(p, b, p.only).steps * hkv;
+          if (at < before + steps) {
+            s_start[w] = {b, before};
+            break;
+          }
+          before += steps;
         }
-        before += steps;
       }
     }
   }
   __syncthreads();
-  if (share * kWarps * blockIdx.x >= total) return;
-  const long long r0 = share * (static_cast<long long>(blockIdx.x) * kWarps + warp), r1 = min(total, r0 + share);
-  const int run_steps = static_cast<int>(max(0LL, min(r1 - r0, 0x7fffffffLL)));
+  const int cta_share = share * kWarps;  // at most total + workers
+  if (static_cast<long long>(cta_share) * blockIdx.x >= total) return;
+  const int r0 = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(share) * (blockIdx.x * kWarps + warp)));
+  const int run_steps = min(total - r0, share);
   const float kscale = __ldg(p.k_scale), vscale = __ldg(p.v_scale);
   const uint32_t full0 = smem_addr(&s_full[warp][0]);
   uint8_t* const ring = smem + warp * kRing * C::kSlot;
@@ -268,8 +275,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
   if (run_steps > 0) {
   int b = s_start[warp].b;
   Request rq = request_of(p, b, p.only);
-  int kvh = static_cast<int>((r0 - s_start[warp].before) / rq.steps);
-  int step = static_cast<int>((r0 - s_start[warp].before) % rq.steps);
+  int kvh = (r0 - s_start[warp].before) / rq.steps;
+  int step = (r0 - s_start[warp].before) - kvh * rq.steps;
 
   // ---- fetching, up to kRing steps ahead of the computation
   const uint64_t pol = policy_evict_first();
@@ -277,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
   // record u of the batch's step k, and copies it when its turn comes.
   constexpr int kBatch = 32 / kStep;
   int fb = b, fkvh = kvh, fpos = 0, fetched = 0;  // fpos: the position in the run that fstep stands for
-  long long fstep = step;
+  int fstep = step;
   Request frq = rq;
   const uint8_t* src = nullptr;  // this lane's record
   uint32_t found = 0u;           // the lanes whose record lies in the cache
@@ -298,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
             while (frq.steps == 0);
           }
         }
-        const int tile = static_cast<int>(fstep) * kStep + lane % kStep;
+        const int tile = fstep * kStep + lane % kStep;
         in = tile < (frq.len + kKv4Tokens - 1) / kKv4Tokens;
         if (in) {
           const int page = p.block_shift >= 0 ? tile >> p.block_shift : tile / p.per_block;
@@ -325,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
     }
     ++fetched;
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < kRing; ++i) fetch();
 
   const int g = lane >> 2, t = lane & 3;
@@ -595,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
         if (col >= rows) continue;
         if (whole) {
           const float inv = l[nt][c] > 0.f ? vscale / l[nt][c] : 0.f;
-          const size_t at = out_at(p, rq, kvh, col) + (D / 8) * g;
+          const size_t at = out_at(p, rq.first, kvh, col) + (D / 8) * g;
 #pragma unroll
           for (int i = 0; i < D / 8; i += 4) store4(p, at + i, y[i] * inv, y[i + 1] * inv, y[i + 2] * inv, y[i + 3] * inv);
         } else {
@@ -607,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
                 make_float2(l[nt][c] > 0.f ? m[nt][c] * cs : -INFINITY, l[nt][c]);
         }
       }
-    if (!whole && lane == 0) s_piece[2 * warp + last] = {r0 + done - seg - step, b, kvh};
+    if (!whole && lane == 0) s_piece[2 * warp + last] = {r0 + done - seg - step, rq.steps, rq.first, rq.n, kvh};
 
     // ---- the next unit
     step = 0;
@@ -625,86 +632,93 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
   __syncthreads();
 
   // ---- join the warps' pieces
-  const long long cta_share = share * kWarps;
-  int part_b[2] = {-1, -1}, part_kvh[2];  // units that go on in other CTAs: the one begun before this CTA, the one begun here
-  long long part_unit[2];
+  auto piece_at = [&](int k) {
+    return k & 1 ? reinterpret_cast<const float*>(smem + (k / 2) * kRing * C::kSlot) : heads + (k / 2) * C::kPiece;
+  };
+  Piece open0, open1;  // units that go on in other CTAs: the one begun in front of this CTA, the one begun here
+  open0.unit = open1.unit = -1;
   for (int i = 0; i < 2 * kWarps;) {
-    const Piece first = s_piece[i];
-    if (first.unit < 0) {
+    const Piece u = s_piece[i];
+    if (u.unit < 0) {
       ++i;
       continue;
     }
-    int end = i + 1;  // the unit's pieces: i .. end - 1, with gaps
-    for (int k = i + 1; k < 2 * kWarps; ++k) {
-      if (s_piece[k].unit == first.unit) end = k + 1;
-      else if (s_piece[k].unit >= 0) break;
+    uint32_t mine = 0u;  // the unit's pieces
+    int next = 2 * kWarps;
+#pragma unroll 1
+    for (int k = i; k < next; ++k) {
+      const int unit = s_piece[k].unit;
+      if (unit == u.unit) mine |= 1u << k;
+      else if (unit >= 0) next = k;
     }
-    const Request rq = request_of(p, first.b, p.only);
-    const int rows = rq.n * p.share;
-    const long long c0 = first.unit / cta_share, c1 = (first.unit + rq.steps - 1) / cta_share;
-    const bool whole = c0 == c1;
-    const int which = c0 == blockIdx.x;
-    float* part = p.partial + (2 * static_cast<size_t>(blockIdx.x) + which) * C::kPiece;
-    for (int item = tid; item < C::kRows * (D / 4); item += kThreads) {
+    const int rows = u.n * p.share;
+    const int c0 = u.unit / cta_share, c1 = (u.unit + u.steps - 1) / cta_share;
+    const bool whole = c0 == c1, begun = c0 == static_cast<int>(blockIdx.x);
+    float* part = p.partial + (2 * static_cast<size_t>(blockIdx.x) + begun) * C::kPiece;
+    for (int item = tid; item < rows * (D / 4); item += kThreads) {
       const int col = item / (D / 4), d = 4 * (item % (D / 4));
-      if (col >= rows) continue;
       Joined sum;
-      for (int k = i; k < end; ++k) {
-        if (s_piece[k].unit < 0) continue;
-        const float* src = (k & 1 ? reinterpret_cast<const float*>(smem + (k / 2) * kRing * C::kSlot) : heads + (k / 2) * C::kPiece) +
-                           col * C::kOStride;
-        sum.add(*reinterpret_cast<const float2*>(src + D), *reinterpret_cast<const float4*>(src + d));
+      float2 ml[2 * kWarps];
+#pragma unroll
+      for (int k = 0; k < 2 * kWarps; ++k) {
+        ml[k] = mine >> k & 1u ? *reinterpret_cast<const float2*>(piece_at(k) + col * C::kOStride + D)
+                               : make_float2(-INFINITY, 0.f);
+        sum.m = fmaxf(sum.m, ml[k].x);
       }
+#pragma unroll
+      for (int k = 0; k < 2 * kWarps; ++k)
+        if (mine >> k & 1u) sum.add(ml[k], *reinterpret_cast<const float4*>(piece_at(k) + col * C::kOStride + d));
       if (whole) {
-        sum.store(p, out_at(p, rq, first.kvh, col) + d, vscale);
+        sum.store(p, out_at(p, u.first, u.kvh, col) + d, vscale);
       } else {
         __stcg(reinterpret_cast<float4*>(part + col * C::kOStride + d), sum.o);
         if (d == 0) __stcg(reinterpret_cast<float2*>(part + col * C::kOStride + D), make_float2(sum.m, sum.l));
       }
     }
     if (!whole) {
-      part_b[which] = first.b;
-      part_kvh[which] = first.kvh;
-      part_unit[which] = first.unit;
+      if (begun) open1 = u;
+      else open0 = u;
     }
-    i = end;
+    i = next;
   }
-  if (part_b[0] < 0 && part_b[1] < 0) return;
+  if (open0.unit < 0 && open1.unit < 0) return;
 
   // ---- join the CTAs' parts of a unit, in the last CTA to arrive
-  __threadfence();
   __syncthreads();
   if (tid < 2) {
+    const Piece u = tid ? open1 : open0;
     s_last[tid] = 0;
-    const int pb = tid ? part_b[1] : part_b[0];
-    if (pb >= 0) {
-      const long long unit = tid ? part_unit[1] : part_unit[0];
-      const long long c0 = unit / cta_share, c1 = (unit + request_of(p, pb, p.only).steps - 1) / cta_share;
+    if (u.unit >= 0) {
+      const int c0 = u.unit / cta_share, c1 = (u.unit + u.steps - 1) / cta_share;
+      __threadfence();  // the CTA's stores, seen through the barrier, before the arrival
       s_last[tid] = atomicAdd(p.counters + c0, 1u) == static_cast<unsigned>(c1 - c0);
-      if (s_last[tid]) p.counters[c0] = 0u;
+      if (s_last[tid]) {
+        p.counters[c0] = 0u;
+        __threadfence();
+      }
     }
   }
   __syncthreads();
-#pragma unroll
+#pragma unroll 1
   for (int which = 0; which < 2; ++which) {
-    if (part_b[which] < 0 || !s_last[which]) continue;
-    __threadfence();
-    const Request rq = request_of(p, part_b[which], p.only);
-    const int rows = rq.n * p.share;
-    const long long c0 = part_unit[which] / cta_share;
-    const int parts = static_cast<int>((part_unit[which] + rq.steps - 1) / cta_share - c0) + 1;
-    for (int item = tid; item < C::kRows * (D / 4); item += kThreads) {
+    if (!s_last[which]) continue;
+    const Piece u = which ? open1 : open0;
+    const int rows = u.n * p.share;
+    const int c0 = u.unit / cta_share, parts = (u.unit + u.steps - 1) / cta_share - c0 + 1;
+    for (int item = tid; item < rows * (D / 4); item += kThreads) {
       const int col = item / (D / 4), d = 4 * (item % (D / 4));
-      if (col >= rows) continue;
       // part 0 is the second place of CTA c0, part k the first of CTA c0 + k
       const float* src = p.partial + 2 * static_cast<size_t>(c0) * C::kPiece + col * C::kOStride;
       Joined sum;
 #pragma unroll 8
+      for (int k = 0; k < parts; ++k)
+        sum.m = fmaxf(sum.m, __ldcg(src + (k ? 2 * k : 1) * static_cast<size_t>(C::kPiece) + D));
+#pragma unroll 4
       for (int k = 0; k < parts; ++k) {
         const float* s = src + (k ? 2 * k : 1) * static_cast<size_t>(C::kPiece);
         sum.add(__ldcg(reinterpret_cast<const float2*>(s + D)), __ldcg(reinterpret_cast<const float4*>(s + d)));
       }
-      sum.store(p, out_at(p, rq, part_kvh[which], col) + d, vscale);
+      sum.store(p, out_at(p, u.first, u.kvh, col) + d, vscale);
     }
   }
 }

@@ -85,7 +85,7 @@ ATTEND = dict(q=FAKE, qd=w8.BF16, tokens=4, hq=8, hkv=2, d=128, qt=1024, qh=128,
     (dict(start=None), INVALID), (dict(start=None, most=1, tokens=3), INVALID), (dict(ot=64), INVALID), (dict(oh=64), INVALID),
     (dict(qt=-1), INVALID), (dict(d=32), UNSUPPORTED), (dict(bs=8), UNSUPPORTED), (dict(hq=130), UNSUPPORTED),
     (dict(batch=65536), UNSUPPORTED), (dict(mb=1 << 27), UNSUPPORTED), (dict(tokens=1 << 31), UNSUPPORTED),
-    (dict(most=1 << 30), UNSUPPORTED), (dict(cache=ODD), MISALIGNED), (dict(q=ODD), MISALIGNED), (dict(table=ODD), MISALIGNED),
+    (dict(batch=1 << 13, mb=1 << 16), UNSUPPORTED), (dict(most=1 << 30), UNSUPPORTED), (dict(cache=ODD), MISALIGNED), (dict(q=ODD), MISALIGNED), (dict(table=ODD), MISALIGNED),
     (dict(start=ODD), MISALIGNED), (dict(ws=None), WORKSPACE), (dict(wsb=8), WORKSPACE), (dict(ws=ODD), WORKSPACE),
 ])
 def test_attention_refuses(kw, status):
