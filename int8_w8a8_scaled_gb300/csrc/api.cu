@@ -1113,6 +1113,8 @@ w8a8_status kv4_attention_sizes(int64_t batch, int64_t max_query_len, int64_t nu
     return fail(W8A8_ERR_UNSUPPORTED, "batch, head counts or max_query_len out of range");
   if (num_q_heads % num_kv_heads != 0)
     return fail(W8A8_ERR_INVALID_ARG, "num_q_heads must be a multiple of num_kv_heads");
+  if (max_query_len * num_q_heads >= (1LL << 31) / batch)
+    return fail(W8A8_ERR_UNSUPPORTED, "batch * max_query_len * num_q_heads must be below 2^31");
   if (num_q_heads / num_kv_heads > 64) return fail(W8A8_ERR_UNSUPPORTED, "num_q_heads / num_kv_heads must be at most 64");
   return W8A8_OK;
 }

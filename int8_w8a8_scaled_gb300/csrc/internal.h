@@ -210,7 +210,6 @@ struct Kv4AttnParams {
   int out_vec;
   // set by the launcher
   int share;            // num_q_heads / num_kv_heads
-  int only;             // which requests a launch takes (request_of)
   int per_block;        // records of a block
   int block_shift;      // its logarithm, -1 if it is no power of two
   unsigned* counters;   // parts of a cut unit that have arrived, left zero
@@ -220,7 +219,9 @@ struct Kv4AttnParams {
 size_t kv4_attention_workspace(int share, long long max_query_len, int head_dim, int num_sms);
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int num_sms, void* workspace, cudaStream_t stream);
 // Requests of more rows than the few-rows kernel takes (kv4_prompt.cu).
-cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, cudaStream_t stream);
+cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, int num_sms, cudaStream_t stream);
+size_t kv4_prompt_workspace(int head_dim, int num_sms);
+cudaError_t read_clear_kv4_prompt_status(int* flags);
 // Reads and clears the kernels' status word (call after a sync).
 cudaError_t read_clear_kv4_status(int* flags);
 

@@ -69,8 +69,8 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 2;                         // tiles of a step
 constexpr int kRing = 2;                         // steps in a warp's ring
 constexpr int kSmallRows = 16;
-constexpr float kHeadroom = 8.f;
-constexpr float kNoScore = -1e30f;               // below any product, and finite
+constexpr float kHeadroom = 2.f;
+constexpr float kNoScore = -1e25f;               // below any product, and finite
 constexpr int kMaxCounters = 1024;               // CTAs that may leave a unit open
 constexpr size_t kCounterBytes = kMaxCounters * sizeof(unsigned);
 
@@ -86,8 +86,7 @@ struct Request {
   int steps;     // steps of a unit; 0: nothing to do here
 };
 
-// `only` 1: requests of up to kSmallRows rows, 0: larger ones, -1: all.
-__device__ __forceinline__ Request request_of(const Kv4AttnParams& p, int b, int only) {
+__device__ __forceinline__ Request request_of(const Kv4AttnParams& p, int b) {
   Request r;
   r.first = b;
   r.n = 1;
@@ -97,10 +96,9 @@ __device__ __forceinline__ Request request_of(const Kv4AttnParams& p, int b, int
   }
   const long long room = static_cast<long long>(p.max_blocks) * p.block_size;
   r.len = static_cast<int>(min(static_cast<long long>(max(__ldg(p.seq_lens + b), 0)), room));
-  const bool small = static_cast<long long>(r.n) * p.share <= kSmallRows;
   // an empty request has one step, with no token in it, to write its zeros
   constexpr int kTokens = kStep * kKv4Tokens;
-  r.steps = r.n > 0 && (only < 0 || small == (only > 0)) ? max(1, (r.len + kTokens - 1) / kTokens) : 0;
+  r.steps = r.n > 0 ? max(1, (r.len + kTokens - 1) / kTokens) : 0;
   return r;
 }
 
@@ -228,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
     const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
     int mine = 0;
 #pragma unroll 1
-    for (int b = b0; b < b1; ++b) mine += request_of(p, b, p.only).steps * hkv;
+    for (int b = b0; b < b1; ++b) mine += request_of(p, b).steps * hkv;
     int run = mine;
 #pragma unroll 1
     for (int off = 1; off < 32; off <<= 1) {
@@ -253,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
         int before = run;
 #pragma unroll 1
         for (int b = b0; b < b1; ++b) {
-          const int steps = request_of(p, b, p.only).steps * hkv;
+          const int steps = request_of(p, b).steps * hkv;
           if (at < before + steps) {
             s_start[w] = {b, before};
             break;
@@ -274,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
   bool ok = true;
   if (run_steps > 0) {
   int b = s_start[warp].b;
-  Request rq = request_of(p, b, p.only);
+  Request rq = request_of(p, b);
   int kvh = (r0 - s_start[warp].before) / rq.steps;
   int step = (r0 - s_start[warp].before) - kvh * rq.steps;
 
@@ -301,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
           fstep -= frq.steps;
           if (++fkvh == hkv) {
             fkvh = 0;
-            do frq = request_of(p, ++fb, p.only);
+            do frq = request_of(p, ++fb);
             while (frq.steps == 0);
           }
         }
@@ -434,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
 
     for (int x = 0; x < seg; ++x) {
       const int slot = done % kRing;
-      if (ok) ok = mbar_wait(full0 + 8 * slot, (done / kRing) & 1);
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(full0 + 8 * slot, (done / kRing) & 1));
       const uint32_t live = ok ? (live_bits >> (kStep * slot)) & 3u : 0u;
       const int t0 = (step + x) * kStep * kKv4Tokens;
       const uint8_t* rec0 = ring + slot * C::kSlot;
@@ -620,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
     step = 0;
     if (!last && ++kvh == hkv) {
       kvh = 0;
-      do rq = request_of(p, ++b, p.only);
+      do rq = request_of(p, ++b);
       while (rq.steps == 0);
     }
   }
@@ -762,6 +760,7 @@ cudaError_t launch_kind(const Kv4AttnParams& p, int num_sms, cudaStream_t stream
 }  // namespace
 
 size_t kv4_attention_workspace(int share, long long max_query_len, int head_dim, int num_sms) {
+  if (share * max_query_len > kSmallRows) return kv4_prompt_workspace(head_dim, num_sms);
   const int nt = share * max_query_len <= 8 ? 1 : 2;
   return kCounterBytes + static_cast<size_t>(few_rows_ctas(nt, num_sms)) * 2 * 8 * nt * (head_dim + 4) * sizeof(float);
 }
@@ -773,6 +772,9 @@ cudaError_t read_clear_kv4_status(int* flags) {
   const int zero = 0;
   e = cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int));
   *flags = v;
+  if (e != cudaSuccess) return e;
+  e = read_clear_kv4_prompt_status(&v);
+  *flags |= v;
   return e;
 }
 
@@ -781,12 +783,11 @@ cudaError_t launch_kv4_attention(const Kv4AttnParams& args, int num_sms, void* w
   p.counters = static_cast<unsigned*>(workspace);
   p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes);
   p.share = p.num_q_heads / p.num_kv_heads;
-  p.only = -1;
   p.per_block = p.block_size / kKv4Tokens;
   p.block_shift = -1;
   for (int i = 0; i < 31; ++i)
     if ((1 << i) == p.per_block) p.block_shift = i;
-  if (static_cast<long long>(p.share) * p.max_query_len > kSmallRows) return launch_kv4_prompt(p, stream);
+  if (static_cast<long long>(p.share) * p.max_query_len > kSmallRows) return launch_kv4_prompt(p, num_sms, stream);
   if (p.head_dim == 64)
     return p.kind == W8A8_KV4_E2M1 ? launch_kind<W8A8_KV4_E2M1, 64>(p, num_sms, stream)
                                    : launch_kind<W8A8_KV4_INT4, 64>(p, num_sms, stream);

@@ -1,114 +1,800 @@
 // kv4_prompt.cu -- attention over the 4-bit KV cache, many rows a request
-// (sm_103a).
+// (prompts, prompt chunks, long drafts; sm_103a).
 //
-// Row i of the n new rows of a request of length L sees its tokens
-// t <= L - n + i:  out = sum_t softmax(sm_scale q . K_t) V_t, with the cache
-// decoded as it is read.  A row that sees nothing gives zeros.
+// The rows of a request and KV head are its n new tokens times the G query
+// heads that share the KV head (row r: token r / G, head r % G), so that each
+// decoded K and V serves all of them.  Both products run on the 5th-generation
+// tensor cores with f16 operands and fp32 accumulators in TMEM:
+//   S[128 rows x 128 tokens] = Q[128 x D] . K^T     (Q, K in shared memory)
+//   O[128 rows x D]         += P[128 x 128] . V     (P in TMEM, over S; V in
+//                                                    shared memory as it lies,
+//                                                    dims contiguous)
+// The decoded cache is exact in f16; a row of Q is scaled by a power of two
+// before its conversion; the weights are f16(2^(s - m + 7)), with the maximum
+// m raised (and O rescaled) only when a score passes it by 2^8.
 //
-// One CTA takes one row and one query head, 128 tokens at a time: a thread
-// scores a token, the block shares the running maximum and sum, and a thread
-// then sums a dim over the tokens.
+// One CTA to an SM, 13 warps: two softmax warpgroups (a thread owns a row of
+// its 128-row tile), four warps that decode K and V into swizzled tiles two
+// deep, one that issues the MMAs.  While one warpgroup is at its softmax the
+// tensor cores work for the other.  With more than 128 rows the warpgroups
+// take 128 rows each of the same tokens; with fewer both take the same rows,
+// and the token tiles in turn, and their states are joined at the end.
+//
+// Per 128 tokens and 256 rows the MMAs take 4 x 512 cycles (at 8192 flops a
+// cycle); the softmax issues about 2 x 600 instructions on each of the SM's
+// four schedulers and the decoding 350, so the MMAs bound a long prompt.
+//
+// A unit is one request, KV head and 256 rows; its work is the token tiles up
+// to the last one that its last row sees.  All units' tiles in a row are cut
+// into equal runs, one for each CTA; a cut unit leaves a part in the workspace
+// from each of its CTAs, joined by the last to arrive, in their order.
+#include <algorithm>
+
 #include "internal.h"
 #include "kv4.cuh"
+#include "sm103_ptx.cuh"
 
 namespace w8a8 {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kTileRows = 128, kTileTokens = 128;
+constexpr int kUnitRows = 2 * kTileRows;
+constexpr int kSoftmaxThreads = 256;                   // warps 0-3: slot 0, 4-7: slot 1
+constexpr int kDecodeThreads = 128;                    // warps 8-11
+constexpr int kThreads = kSoftmaxThreads + kDecodeThreads + 32;  // and warp 12: the MMAs
+constexpr int kStages = 2;
+constexpr int kRecords = kTileTokens / kKv4Tokens;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kHeadroom = 2.f;
+constexpr float kNoScore = -1e25f;
+constexpr int kMaxCounters = 1024;
+constexpr size_t kCounterBytes = kMaxCounters * sizeof(unsigned);
+constexpr uint32_t kTmemCols = 512;
 
-__device__ __forceinline__ float load16(const void* p, int fp16, size_t i) {
-  if (fp16) return __half2float(static_cast<const __half*>(p)[i]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
+template <int D>
+struct Big {
+  static constexpr int kHalves = D / 64;                        // 128-byte column blocks of a row
+  static constexpr int kBlockBytes = 128 * 128;                 // 128 rows x 128 bytes
+  static constexpr int kTileBytes = kHalves * kBlockBytes;      // a Q, K or V tile
+  static constexpr int kQ = 0, kK = 2 * kTileBytes, kV = kK + kStages * kTileBytes;
+  static constexpr int kSmem = kV + kStages * kTileBytes + 1024;  // + alignment
+  static constexpr int kPart = kUnitRows * (D + 2);             // floats: o [D / 4][256][4], m [256], l [256]
+  static constexpr int kPieces = kTileTokens * D / 2 / 16 / kDecodeThreads;  // 16-byte pieces of K a thread decodes
+};
 
-template <int KIND>
-__device__ __forceinline__ float code_value(const uint8_t* row, const uint8_t* scales, int d) {
-  uint32_t h[4];
-  kv4_decode8<KIND>(row[d / 2] >> (4 * (d & 1)), kv4_scale<KIND>(e4m3x2_to_half2(scales[d / kKv4Group] * 0x101u)), h);
-  const __half2 v = *reinterpret_cast<const __half2*>(&h[0]);
-  return __low2float(v);
-}
+struct Request {
+  int first, n, len, rows;
+};
 
-template <int KIND>
-__global__ void __launch_bounds__(kThreads) kv4_prompt_kernel(const Kv4AttnParams p) {
-  __shared__ float s_q[128], s_p[kThreads];
-  __shared__ float s_red[kThreads / 32];
-  __shared__ long long s_rec[kThreads];
-  const int h = blockIdx.x % p.num_q_heads, i = blockIdx.x / p.num_q_heads, b = blockIdx.y, tid = threadIdx.x;
-  const int first = p.query_start ? min(max(__ldg(p.query_start + b), 0), p.tokens) : b;
-  const int n = p.query_start ? min(max(__ldg(p.query_start + b + 1) - first, 0), min(p.tokens - first, p.max_query_len)) : 1;
-  if (i >= n) return;
-  const int kvh = h / (p.num_q_heads / p.num_kv_heads), d = p.head_dim;
+__device__ __forceinline__ Request request_of(const Kv4AttnParams& p, int b) {
+  Request r;
+  r.first = b;
+  r.n = 1;
+  if (p.query_start) {
+    r.first = min(max(__ldg(p.query_start + b), 0), p.tokens);
+    r.n = min(max(__ldg(p.query_start + b + 1) - r.first, 0), min(p.tokens - r.first, p.max_query_len));
+  }
   const long long room = static_cast<long long>(p.max_blocks) * p.block_size;
-  const int len = static_cast<int>(min(static_cast<long long>(max(__ldg(p.seq_lens + b), 0)), room));
-  const int seen = max(0, len - n + i + 1);
-  if (tid < d) s_q[tid] = load16(p.q, p.q_fp16, static_cast<size_t>(first + i) * p.q_token_stride + h * p.q_head_stride + tid);
-  const float cs = p.sm_scale * __ldg(p.k_scale) * 1.4426950408889634f;
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (int t0 = 0; t0 < seen; t0 += kThreads) {
-    __syncthreads();
-    const int t = t0 + tid;
-    float s = -INFINITY;
-    s_rec[tid] = -1;
-    if (t < seen) {
-      const int blk = __ldg(p.block_table + static_cast<size_t>(b) * p.max_blocks + t / p.block_size);
-      if (blk >= 0 && blk < p.num_blocks) {
-        const int off = t % p.block_size;
-        const size_t rec = kv4_record_of(blk, kvh, p.num_kv_heads, p.block_size, off) * kv4_record_bytes(d);
-        s_rec[tid] = static_cast<long long>(rec);
-        const uint8_t* base = static_cast<const uint8_t*>(p.cache) + rec;
-        const int row = off % kKv4Tokens;
-        s = 0.f;
-        for (int j = 0; j < d; ++j)
-          s += s_q[j] * code_value<KIND>(base + row * (d / 2), base + kv4_scales_at(d, 0) + row * (d / 16), j);
-        s *= cs;
-      }
+  r.len = static_cast<int>(min(static_cast<long long>(max(__ldg(p.seq_lens + b), 0)), room));
+  r.rows = r.n * p.share;
+  return r;
+}
+
+// Token tiles of row block `rt` of a request: up to the last token that its
+// last row sees, at least one (to write the zeros of rows that see none); 0
+// past its rows.
+__device__ __forceinline__ int tiles_of(const Kv4AttnParams& p, const Request& r, int rt) {
+  if (rt * kUnitRows >= r.rows) return 0;
+  const int last = min(r.rows, (rt + 1) * kUnitRows) - 1;
+  const int seen = min(r.len, max(0, r.len - r.n + last / p.share + 1));
+  return max(1, (seen + kTileTokens - 1) / kTileTokens);
+}
+
+// A place in the row of all units' tiles.
+struct Cursor {
+  int b, rt, kvh;
+  Request rq;
+  int tiles;  // of the unit
+  int tile;   // the next one
+  __device__ __forceinline__ void next_unit(const Kv4AttnParams& p) {
+    tile = 0;
+    if (++kvh < p.num_kv_heads) return;
+    kvh = 0;
+    ++rt;
+    while ((tiles = tiles_of(p, rq, rt)) == 0) {
+      rt = 0;
+      rq = request_of(p, ++b);
     }
-    float mx = s;
-    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    if (tid % 32 == 0) s_red[tid / 32] = mx;
+  }
+};
+
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+
+__device__ __forceinline__ float ex2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory"); }
+
+// The same, and whether `ok` holds in all of them.
+__device__ __forceinline__ bool softmax_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(ok)), "n"(kSoftmaxThreads)
+      : "memory");
+  return r != 0u;
+}
+
+// Whether a warp's wait ended well: the same answer in every lane, since what
+// follows is done by the whole warp.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
+__device__ __forceinline__ float2 to_float2(uint32_t two, int fp16) {
+  return fp16 ? __half22float2(*reinterpret_cast<const __half2*>(&two))
+              : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&two));
+}
+
+// 8 16-bit values at `src` (null: zeros).
+__device__ __forceinline__ uint4 load8(const uint16_t* src, int vec) {
+  if (!src) return make_uint4(0u, 0u, 0u, 0u);
+  if (vec) return __ldg(reinterpret_cast<const uint4*>(src));
+  uint32_t u[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+    u[x] = static_cast<uint32_t>(__ldg(src + 2 * x)) | (static_cast<uint32_t>(__ldg(src + 2 * x + 1)) << 16);
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// 8 consecutive outputs.
+__device__ __forceinline__ void store8(const Kv4AttnParams& p, size_t at, const float (&y)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (p.out_fp16) {
+      w[i] = as_u32(__floats2half2_rn(y[2 * i], y[2 * i + 1]));
+    } else {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+  }
+  uint16_t* dst = static_cast<uint16_t*>(p.out) + at;
+  if (p.out_vec) {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      dst[2 * i] = static_cast<uint16_t>(w[i]);
+      dst[2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
+    }
+  }
+}
+
+__device__ __forceinline__ size_t out_at(const Kv4AttnParams& p, int first, int kvh, int row) {
+  return (first + row / p.share) * p.out_token_stride + (kvh * p.share + row % p.share) * p.out_head_stride;
+}
+
+// A unit that goes on in other CTAs.
+struct Open {
+  int first, rows, row0, kvh;
+  long long unit;  // its first tile; -1: none
+  int tiles;
+};
+
+template <int KIND, int D>
+__global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnParams p) {
+  using C = Big<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t s_kfull[kStages], s_kempty[kStages], s_vfull[kStages], s_vempty[kStages];
+  __shared__ uint64_t s_qfull, s_sfull[2], s_pfull[2], s_pvdone[2];
+  __shared__ uint32_t s_tmem;
+  __shared__ long long s_scan[kThreads / 32], s_before;
+  __shared__ int s_item, s_last[2];
+  __shared__ float s_ml[2][kTileRows];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_addr(&s_kfull[i]), kDecodeThreads / 32);
+      mbar_init(smem_addr(&s_vfull[i]), kDecodeThreads / 32);
+      mbar_init(smem_addr(&s_kempty[i]), 1);
+      mbar_init(smem_addr(&s_vempty[i]), 1);
+    }
+    mbar_init(smem_addr(&s_qfull), kSoftmaxThreads / 32);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&s_sfull[i]), 1);
+      mbar_init(smem_addr(&s_pfull[i]), 4);
+      mbar_init(smem_addr(&s_pvdone[i]), 1);
+    }
+    fence_barrier_init();
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // TMEM only now: a kernel in front may still need it
+  if (warp == 12) {
+    tmem_alloc(smem_addr(&s_tmem), kTmemCols);
+    tmem_relinquish();
+  }
+
+  // ---- this CTA's run; an item is one request and row block, all KV heads
+  const int blocks_max = (p.share * p.max_query_len + kUnitRows - 1) / kUnitRows;
+  const int items = p.batch * blocks_max;  // below 2^31, the launcher sees to it
+  long long total = 0, share;
+  {
+    const int per = (items + kThreads - 1) / kThreads;
+    const int i0 = min(items, tid * per), i1 = min(items, i0 + per);
+    long long mine = 0;
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i)
+      mine += static_cast<long long>(tiles_of(p, request_of(p, i / blocks_max), i % blocks_max)) * p.num_kv_heads;
+    long long run = mine;
+#pragma unroll 1
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, run, off);
+      if (lane >= off) run += o;
+    }
+    if (lane == 31) s_scan[warp] = run;
     __syncthreads();
-    mx = m;
-    for (int w = 0; w < kThreads / 32; ++w) mx = fmaxf(mx, s_red[w]);
-    const float alpha = mx == -INFINITY ? 1.f : exp2f(m - mx);
-    m = mx;
-    const float w = s == -INFINITY ? 0.f : exp2f(s - mx);
-    s_p[tid] = w;
-    l = l * alpha + w;
-    o *= alpha;
-    __syncthreads();
-    if (tid < d) {
-      for (int j = 0; j < kThreads && t0 + j < seen; ++j) {
-        if (s_rec[j] < 0) continue;
-        const uint8_t* base = static_cast<const uint8_t*>(p.cache) + s_rec[j];
-        const int row = (t0 + j) % p.block_size % kKv4Tokens;
-        o += s_p[j] * code_value<KIND>(base + kv4_codes_at(d, 1) + row * (d / 2),
-                                       base + kv4_scales_at(d, 1) + row * (d / 16), tid);
+    run -= mine;
+#pragma unroll 1
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) run += s_scan[w];
+      total += s_scan[w];
+    }
+    share = max(1LL, (total + gridDim.x - 1) / gridDim.x);
+    const long long at = share * blockIdx.x;
+    if (at >= run && at < run + mine) {
+#pragma unroll 1
+      for (int i = i0; i < i1; ++i) {
+        const long long w = static_cast<long long>(tiles_of(p, request_of(p, i / blocks_max), i % blocks_max)) * p.num_kv_heads;
+        if (at < run + w) {
+          s_item = i;
+          s_before = run;
+          break;
+        }
+        run += w;
       }
     }
   }
-  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+  tc_fence_before();
   __syncthreads();
-  if (tid % 32 == 0) s_red[tid / 32] = l;
-  __syncthreads();
-  l = 0.f;
-  for (int w = 0; w < kThreads / 32; ++w) l += s_red[w];
-  if (tid < d) {
-    const float y = l > 0.f ? o / l * __ldg(p.v_scale) : 0.f;
-    const size_t at = static_cast<size_t>(first + i) * p.out_token_stride + h * p.out_head_stride + tid;
-    if (p.out_fp16) static_cast<__half*>(p.out)[at] = __float2half_rn(y);
-    else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const long long r0 = share * blockIdx.x;
+  const int run_tiles = static_cast<int>(max(0LL, min(total - r0, min(share, 0x7fffffffLL))));
+  Cursor at;
+  if (run_tiles > 0) {
+    at.b = s_item / blocks_max;
+    at.rt = s_item % blocks_max;
+    at.rq = request_of(p, at.b);
+    at.tiles = tiles_of(p, at.rq, at.rt);
+    at.kvh = static_cast<int>((r0 - s_before) / at.tiles);
+    at.tile = static_cast<int>((r0 - s_before) % at.tiles);
   }
+  bool ok = true;
+  Open open0, open1;  // the unit begun in front of this CTA, the one begun here
+  open0.unit = open1.unit = -1;
+
+  if (run_tiles == 0) {
+    // nothing to do
+  } else if (warp >= 8 && warp < 12) {
+    // ================= decoding: thread (token, piece) of each 16-byte piece of codes
+    const int dt = tid - kSoftmaxThreads;
+    constexpr int kPerRow = D / 32;                       // pieces of a token's row
+    constexpr int kStride = kDecodeThreads / kPerRow;     // tokens between a thread's pieces
+    const int piece = dt % kPerRow, token0 = dt / kPerRow;
+    uint4 raw[2][C::kPieces];
+    uint32_t sc[2][C::kPieces];
+    auto load = [&](const Cursor& c) {
+      // lane x looks record x of the tile up
+      const int tile = c.tile * kRecords + lane;
+      long long rec = -1;
+      if (lane < kRecords && tile < (c.rq.len + kKv4Tokens - 1) / kKv4Tokens) {
+        const int page = p.block_shift >= 0 ? tile >> p.block_shift : tile / p.per_block;
+        const int blk = __ldg(p.block_table + static_cast<size_t>(c.b) * p.max_blocks + page);
+        if (blk >= 0 && blk < p.num_blocks)
+          rec = (static_cast<long long>(blk) * p.num_kv_heads + c.kvh) * p.per_block + (tile - page * p.per_block);
+      }
+#pragma unroll
+      for (int x = 0; x < C::kPieces; ++x) {
+        const int token = token0 + x * kStride, row = token % kKv4Tokens;
+        const long long r = __shfl_sync(0xffffffffu, rec, token / kKv4Tokens);
+        // what is not a token of the request becomes zeros, whatever the cache holds there
+        const bool real = r >= 0 && c.tile * kTileTokens + token < c.rq.len;
+        const uint8_t* base = static_cast<const uint8_t*>(p.cache) + (real ? r : 0) * kv4_record_bytes(D);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          raw[w][x] = make_uint4(0u, 0u, 0u, 0u);
+          sc[w][x] = 0u;
+          if (real) {
+            raw[w][x] = __ldg(reinterpret_cast<const uint4*>(base + kv4_codes_at(D, w) + row * (D / 2) + 16 * piece));
+            sc[w][x] = __ldg(reinterpret_cast<const uint16_t*>(base + kv4_scales_at(D, w) + row * (D / 16) + 2 * piece));
+          }
+        }
+      }
+    };
+    load(at);
+    for (int j = 0; j < run_tiles && ok; ++j) {
+      const int stage = j % kStages;
+      const uint32_t phase = (j / kStages) & 1;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const uint32_t empty = smem_addr(w ? &s_vempty[stage] : &s_kempty[stage]);
+        if (j >= kStages && ok) ok = warp_wait(empty, phase ^ 1u);
+        if (!ok) break;
+        uint8_t* const tile = smem + (w ? C::kV : C::kK) + stage * C::kTileBytes;
+#pragma unroll
+        for (int x = 0; x < C::kPieces; ++x) {
+          const int token = token0 + x * kStride;
+          const __half2 s = e4m3x2_to_half2(sc[w][x]);
+          Kv4Scale s0 = kv4_scale<KIND>(__low2half2(s)), s1 = kv4_scale<KIND>(__high2half2(s));
+          uint32_t word[4] = {raw[w][x].x, raw[w][x].y, raw[w][x].z, raw[w][x].w};
+          // the second block's lanes store their words in another order: the
+          // eight lanes of a store then meet eight different bank groups
+          const bool turn = D == 128 && piece >= 2;
+          if (turn) {
+            uint32_t t0 = word[0], t1 = word[1];
+            word[0] = word[2];
+            word[1] = word[3];
+            word[2] = t0;
+            word[3] = t1;
+            const Kv4Scale ts = s0;
+            s0 = s1;
+            s1 = ts;
+          }
+          uint8_t* const row = tile + (D == 128 ? piece / 2 : 0) * C::kBlockBytes + token * 128;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t h[4];
+            kv4_decode8<KIND>(word[i], i < 2 ? s0 : s1, h);
+            const int chunk = (piece % 2) * 4 + (turn ? i ^ 2 : i);
+            *reinterpret_cast<uint4*>(row + ((chunk ^ (token & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        }
+        fence_proxy_async_shared();  // the stores before the tensor cores' reads
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(w ? &s_vfull[stage] : &s_kfull[stage]));
+      }
+      if (j + 1 < run_tiles) {
+        if (++at.tile == at.tiles) at.next_unit(p);
+        load(at);
+      }
+    }
+  } else if (warp == 12) {
+    // ================= MMAs, all by one lane
+    if (lane == 0) {
+      constexpr uint32_t kIdescS = make_idesc(kTileRows, kTileTokens, 0);
+      constexpr uint32_t kIdescO = make_idesc(kTileRows, D, 0) | (1u << 16);  // V: dims contiguous
+      const uint32_t base = smem_addr(smem);
+      uint32_t pcount[2] = {0u, 0u};  // weight tiles taken, each slot
+      int done = 0, units = 0;
+      while (done < run_tiles && ok) {
+        const int nt = min(at.tiles - at.tile, run_tiles - done);
+        const bool pair = at.rq.rows - at.rt * kUnitRows > kTileRows;
+        const int ahead = pair ? 1 : 2;
+        ok = mbar_wait(smem_addr(&s_qfull), units & 1);
+        tc_fence_after();
+        auto scores = [&](int j, int slot) {
+          const int stage = (done + j) % kStages;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk / 4) * C::kBlockBytes;
+            const uint64_t da = smem_desc_sw128(base + C::kQ + (pair ? slot : 0) * C::kTileBytes + off) + 2 * (kk % 4);
+            const uint64_t db = smem_desc_sw128(base + C::kK + stage * C::kTileBytes + off) + 2 * (kk % 4);
+            mma_f16(tmem + slot * kTileTokens, da, db, kIdescS, kk > 0);
+          }
+          mma_commit(smem_addr(&s_sfull[slot]));
+        };
+        auto wait_k = [&](int j) {
+          if (ok) ok = mbar_wait(smem_addr(&s_kfull[(done + j) % kStages]), ((done + j) / kStages) & 1);
+          tc_fence_after();
+        };
+        for (int j = 0; j < ahead && j < nt && ok; ++j) {
+          wait_k(j);
+          for (int slot = 0; slot < 2; ++slot)
+            if (ok && (pair || slot == (j & 1))) scores(j, slot);
+          mma_commit(smem_addr(&s_kempty[(done + j) % kStages]));
+        }
+        for (int j = 0; j < nt && ok; ++j) {
+          const int stage = (done + j) % kStages;
+          const bool more = j + ahead < nt;
+          ok = mbar_wait(smem_addr(&s_vfull[stage]), ((done + j) / kStages) & 1);
+          for (int slot = 0; slot < 2 && ok; ++slot) {
+            if (!pair && slot != (j & 1)) continue;
+            ok = mbar_wait(smem_addr(&s_pfull[slot]), pcount[slot] & 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kTileTokens / 16; ++kk) {
+              const uint64_t db = smem_desc_mn_sw128(base + C::kV + stage * C::kTileBytes + kk * 2048, C::kBlockBytes);
+              mma_f16_ts(tmem + 2 * kTileTokens + slot * D, tmem + slot * kTileTokens + 8 * kk, db, kIdescO,
+                         kk > 0 || j >= (pair ? 1 : 2));
+            }
+            mma_commit(smem_addr(&s_pvdone[slot]));
+            if (more) {
+              if (pair ? slot == 0 : true) wait_k(j + ahead);
+              // the scores overwrite the weights
+              if (ok) ok = mbar_wait(smem_addr(&s_pvdone[slot]), pcount[slot] & 1);
+              if (ok) scores(j + ahead, slot);
+            }
+            ++pcount[slot];
+          }
+          mma_commit(smem_addr(&s_vempty[stage]));
+          if (more) mma_commit(smem_addr(&s_kempty[(done + j + ahead) % kStages]));
+        }
+        done += nt;
+        ++units;
+        at.tile += nt;
+        if (done < run_tiles) at.next_unit(p);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ================= softmax: thread = row of slot `slot`
+    const int slot = warp / 4, row = tid % kTileRows;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp % 4) << 21);  // this warp's 32 TMEM lanes
+    const uint32_t s_cols = lanes + slot * kTileTokens, o_cols = lanes + 2 * kTileTokens + slot * D;
+    const float kscale = __ldg(p.k_scale), vscale = __ldg(p.v_scale);
+    uint32_t count = 0u;  // tiles of this slot
+    int done = 0;
+    while (done < run_tiles) {
+      const int nt = min(at.tiles - at.tile, run_tiles - done);
+      const Request rq = at.rq;
+      const int row0 = at.rt * kUnitRows;
+      const bool pair = rq.rows - row0 > kTileRows;
+      const int my = row0 + (pair ? slot * kTileRows : 0) + row;  // the request's row
+      const bool real = my < rq.rows;
+
+      // ---- the query row, scaled by 2^e so that its largest element lies in [2^14, 2^15)
+      float cs = 0.f;
+      if (pair || slot == 0) {
+        const uint16_t* src = real ? static_cast<const uint16_t*>(p.q) + (rq.first + my / p.share) * p.q_token_stride +
+                                         (at.kvh * p.share + my % p.share) * p.q_head_stride
+                                   : nullptr;
+        float qmax = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 w = load8(src ? src + 8 * c : nullptr, p.q_vec);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 v = to_float2(u[i], p.q_fp16);
+            qmax = fmaxf(qmax, fmaxf(fabsf(v.x), fabsf(v.y)));
+          }
+        }
+        int e = 0;
+        if (qmax > 0.f && qmax <= 3.0e38f) e = min(100, max(-100, 14 + 127 - static_cast<int>(__float_as_uint(qmax) >> 23)));
+        cs = p.sm_scale * kscale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        // the scale's sign goes to the query: the largest product is the largest score
+        const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), cs);
+        cs = fmaxf(fabsf(cs), 1e-37f);
+        uint8_t* const dst = smem + C::kQ + slot * C::kTileBytes + row * 128;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 w = load8(src ? src + 8 * c : nullptr, p.q_vec);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 x = to_float2(u[i], p.q_fp16);
+            v[2 * i] = x.x * up;
+            v[2 * i + 1] = x.y * up;
+          }
+          uint32_t h[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] = as_u32(__floats2half2_rn(v[kv4_low<KIND>(i)], v[kv4_high<KIND>(i)]));
+          *reinterpret_cast<uint4*>(dst + (c / 8) * C::kBlockBytes + (((c % 8) ^ (row & 7)) << 4)) =
+              make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        if (!pair) s_ml[0][row] = cs;  // both slots take these rows
+        fence_proxy_async_shared();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&s_qfull));
+      if (!pair) {
+        softmax_sync();
+        cs = s_ml[0][row];
+        softmax_sync();
+      }
+      const int lim = real ? rq.len - rq.n + my / p.share : rq.len - 1;  // the last token seen
+      const float room = fminf(kHeadroom / cs, 1e38f);
+      float m = kNoScore, l = 0.f;
+      int mine = 0;  // tiles of this slot in the unit
+
+      // ---- its tiles
+      for (int j = pair ? 0 : slot; j < nt; j += pair ? 1 : 2) {
+        const int t0 = (at.tile + j) * kTileTokens;
+        // records that lie outside the cache: lane x looks record x up
+        bool gone = false;
+        {
+          const int tile = (at.tile + j) * kRecords + lane;
+          if (lane < kRecords && tile < (rq.len + kKv4Tokens - 1) / kKv4Tokens) {
+            const int page = p.block_shift >= 0 ? tile >> p.block_shift : tile / p.per_block;
+            const int blk = __ldg(p.block_table + static_cast<size_t>(at.b) * p.max_blocks + page);
+            gone = blk < 0 || blk >= p.num_blocks;
+          }
+        }
+        const uint32_t holes = __ballot_sync(0xffffffffu, gone);
+        const bool edge = __any_sync(0xffffffffu, t0 + kTileTokens - 1 > lim) || holes;
+        if (ok) ok = warp_wait(smem_addr(&s_sfull[slot]), count & 1);
+        if (!ok) break;
+        tc_fence_after();
+        // the maximum first, then the weights: 128 columns at once would not fit the registers
+        auto load_scores = [&](int c, uint32_t (&s)[32]) {
+          tmem_ld32(s_cols + 32 * c, s);
+          tmem_ld_wait();
+          if (edge) {
+            asm volatile("");
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (t0 + 32 * c + i > lim || (holes >> (2 * c + i / 16) & 1u)) s[i] = __float_as_uint(-INFINITY);
+          }
+        };
+        float mx = kNoScore;
+#pragma unroll
+        for (int c = 0; c < kTileTokens / 32; ++c) {
+          uint32_t s[32];
+          load_scores(c, s);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(s[i]));
+        }
+        if (__any_sync(0xffffffffu, mx > m + room)) {
+          const float mn = fmaxf(m, mx);
+          const float alpha = ex2_fast((m - mn) * cs);
+          m = mn;
+          l *= alpha;
+          if (mine > 0) {
+            if (ok) ok = warp_wait(smem_addr(&s_pvdone[slot]), (count - 1) & 1);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(o_cols + 32 * c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(o_cols + 32 * c, o);
+            }
+            tmem_st_wait();
+          }
+        }
+        const float bias = fmaf(-m, cs, 15.f - kHeadroom);
+        float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < kTileTokens / 32; ++c) {
+          uint32_t s[32], w[16];
+          load_scores(c, s);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float a = ex2_fast(fmaf(__uint_as_float(s[i]), cs, bias));
+            const float b = ex2_fast(fmaf(__uint_as_float(s[i + 1]), cs, bias));
+            sum0 += a;
+            sum1 += b;
+            w[i / 2] = as_u32(__floats2half2_rn(a, b));
+          }
+          tmem_st16(s_cols + 16 * c, w);  // over scores that have been read
+        }
+        l += sum0 + sum1;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&s_pfull[slot]));
+        ++count;
+        ++mine;
+      }
+
+      // ---- the unit's end
+      if (mine > 0 && ok) ok = warp_wait(smem_addr(&s_pvdone[slot]), (count - 1) & 1);
+      tc_fence_after();
+      const bool whole = at.tile == 0 && nt == at.tiles;
+      const long long unit = r0 + done - at.tile;
+      const bool begun = unit / share == blockIdx.x;
+      float a0 = 1.f, a1 = 0.f;  // this slot's factor, the other's
+      float ms = l > 0.f ? m * cs : -INFINITY;
+      if (!pair) {
+        if (slot == 1) {
+          s_ml[0][row] = ms;
+          s_ml[1][row] = l;
+          tc_fence_before();
+        }
+        softmax_sync();
+        tc_fence_after();
+        if (slot == 0) {
+          const float m1 = s_ml[0][row], l1 = s_ml[1][row];
+          const float mn = fmaxf(ms, m1);
+          a0 = l > 0.f ? ex2_fast(ms - mn) : 0.f;
+          a1 = l1 > 0.f ? ex2_fast(m1 - mn) : 0.f;
+          ms = mn;
+          l = a0 * l + a1 * l1;
+        }
+      }
+      if (ok && (pair || slot == 0)) {
+        const float inv = l > 0.f ? vscale / l : 0.f;
+        const size_t to = real ? out_at(p, rq.first, at.kvh, my) : 0;
+        float* part = p.partial + (2 * static_cast<size_t>(blockIdx.x) + begun) * C::kPart;
+        const int prow = my - row0;
+        const bool both = !pair && nt > 1;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(o_cols + 32 * c, o);
+          tmem_ld_wait();
+          float y[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(o[i]) * a0;
+          if (both) {
+            tmem_ld32(o_cols + D + 32 * c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = fmaf(__uint_as_float(o[i]), a1, y[i]);
+          }
+          if (!(l > 0.f)) {  // nothing seen: the accumulators are not meant
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = 0.f;
+          }
+          if (whole) {
+            if (real) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                float z[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  z[kv4_low<KIND>(i)] = y[8 * q + 2 * i] * inv;
+                  z[kv4_high<KIND>(i)] = y[8 * q + 2 * i + 1] * inv;
+                }
+                store8(p, to + 32 * c + 8 * q, z);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              __stcg(reinterpret_cast<float4*>(part) + (8 * c + q) * kUnitRows + prow,
+                     make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]));
+          }
+        }
+        if (!whole) {
+          __stcg(part + kUnitRows * D + prow, ms);
+          __stcg(part + kUnitRows * (D + 1) + prow, l);
+        }
+      }
+      tc_fence_before();
+      ok = softmax_all(ok);  // slot 1's accumulators have been read; all go on, or none
+      if (!whole) {
+        const Open u = {rq.first, rq.rows, row0, at.kvh, unit, at.tiles};
+        if (begun) open1 = u;
+        else open0 = u;
+      }
+      if (!ok) break;
+      done += nt;
+      at.tile += nt;
+      if (done < run_tiles) at.next_unit(p);
+    }
+  }
+
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  if (tid >= kSoftmaxThreads || (open0.unit < 0 && open1.unit < 0)) return;
+
+  // ---- join the CTAs' parts of a unit, in the last CTA to arrive
+  if (tid < 2) {
+    const Open u = tid ? open1 : open0;
+    s_last[tid] = 0;
+    if (u.unit >= 0) {
+      const long long c0 = u.unit / share, c1 = (u.unit + u.tiles - 1) / share;
+      __threadfence();  // the CTA's stores, seen through the barrier, before the arrival
+      s_last[tid] = atomicAdd(p.counters + c0, 1u) == static_cast<unsigned>(c1 - c0);
+      if (s_last[tid]) {
+        p.counters[c0] = 0u;
+        __threadfence();
+      }
+    }
+  }
+  softmax_sync();
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    if (!s_last[which]) continue;
+    const Open u = which ? open1 : open0;
+    const int my = u.row0 + tid;
+    if (my >= u.rows) continue;
+    const long long c0 = u.unit / share;
+    const int parts = static_cast<int>((u.unit + u.tiles - 1) / share - c0) + 1;
+    // part 0 is the second place of CTA c0, part k the first of CTA c0 + k
+    const float* src = p.partial + 2 * static_cast<size_t>(c0) * C::kPart;
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k)
+      m = fmaxf(m, __ldcg(src + (k ? 2 * k : 1) * static_cast<size_t>(C::kPart) + kUnitRows * D + tid));
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+      const float* s = src + (k ? 2 * k : 1) * static_cast<size_t>(C::kPart) + kUnitRows * D + tid;
+      const float lk = __ldcg(s + kUnitRows);
+      if (lk > 0.f) l = fmaf(ex2_fast(__ldcg(s) - m), lk, l);
+    }
+    const float inv = l > 0.f ? __ldg(p.v_scale) / l : 0.f;
+    const size_t to = out_at(p, u.first, u.kvh, my);
+#pragma unroll 1
+    for (int q = 0; q < D / 8; ++q) {
+      float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int k = 0; k < parts; ++k) {
+        const float* s = src + (k ? 2 * k : 1) * static_cast<size_t>(C::kPart);
+        const float mk = __ldcg(s + kUnitRows * D + tid);
+        const float a = mk == -INFINITY ? 0.f : ex2_fast(mk - m) * inv;
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(s) + (2 * q) * kUnitRows + tid);
+        const float4 w = __ldcg(reinterpret_cast<const float4*>(s) + (2 * q + 1) * kUnitRows + tid);
+        y[0] = fmaf(a, v.x, y[0]);
+        y[1] = fmaf(a, v.y, y[1]);
+        y[2] = fmaf(a, v.z, y[2]);
+        y[3] = fmaf(a, v.w, y[3]);
+        y[4] = fmaf(a, w.x, y[4]);
+        y[5] = fmaf(a, w.y, y[5]);
+        y[6] = fmaf(a, w.z, y[6]);
+        y[7] = fmaf(a, w.w, y[7]);
+      }
+      float z[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        z[kv4_low<KIND>(i)] = y[2 * i];
+        z[kv4_high<KIND>(i)] = y[2 * i + 1];
+      }
+      store8(p, to + 8 * q, z);
+    }
+  }
+}
+
+template <int KIND, int D>
+cudaError_t launch_t(const Kv4AttnParams& p, int num_sms, cudaStream_t stream) {
+  auto kern = kv4_prompt_kernel<KIND, D>;
+  // the attribute is per function and device; setting it again is harmless
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Big<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min(num_sms, kMaxCounters)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Big<D>::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, kern, p)) != cudaSuccess) return e;
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, cudaStream_t stream) {
-  const dim3 grid(p.num_q_heads * p.max_query_len, p.batch);
-  if (p.kind == W8A8_KV4_E2M1) kv4_prompt_kernel<W8A8_KV4_E2M1><<<grid, kThreads, 0, stream>>>(p);
-  else kv4_prompt_kernel<W8A8_KV4_INT4><<<grid, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+size_t kv4_prompt_workspace(int head_dim, int num_sms) {
+  return kCounterBytes + static_cast<size_t>(std::min(num_sms, kMaxCounters)) * 2 * kUnitRows * (head_dim + 2) * sizeof(float);
+}
+
+cudaError_t read_clear_kv4_prompt_status(int* flags) {
+  int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_device_status, sizeof(int));
+  if (e != cudaSuccess) return e;
+  const int zero = 0;
+  e = cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int));
+  *flags = v;
+  return e;
+}
+
+cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, int num_sms, cudaStream_t stream) {
+  if (p.head_dim == 64)
+    return p.kind == W8A8_KV4_E2M1 ? launch_t<W8A8_KV4_E2M1, 64>(p, num_sms, stream)
+                                   : launch_t<W8A8_KV4_INT4, 64>(p, num_sms, stream);
+  return p.kind == W8A8_KV4_E2M1 ? launch_t<W8A8_KV4_E2M1, 128>(p, num_sms, stream)
+                                 : launch_t<W8A8_KV4_INT4, 128>(p, num_sms, stream);
 }
 
 }  // namespace w8a8
