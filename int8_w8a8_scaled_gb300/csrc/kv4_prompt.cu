@@ -142,6 +142,10 @@ __device__ __forceinline__ float2 to_float2(uint32_t two, int fp16) {
               : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&two));
 }
 
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
 // 8 16-bit values at `src` (null: zeros).
 __device__ __forceinline__ uint4 load8(const uint16_t* src, int vec) {
   if (!src) return make_uint4(0u, 0u, 0u, 0u);
@@ -291,82 +295,80 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     constexpr int kPerRow = D / 32;                       // pieces of a token's row
     constexpr int kStride = kDecodeThreads / kPerRow;     // tokens between a thread's pieces
     const int piece = dt % kPerRow, token0 = dt / kPerRow;
-    uint4 raw[2][C::kPieces];
-    uint32_t sc[2][C::kPieces];
-    auto load = [&](const Cursor& c) {
-      // lane x looks record x of the tile up
-      const int tile = c.tile * kRecords + lane;
-      long long rec = -1;
-      if (lane < kRecords && tile < (c.rq.len + kKv4Tokens - 1) / kKv4Tokens) {
-        const int page = p.block_shift >= 0 ? tile >> p.block_shift : tile / p.per_block;
-        const int blk = __ldg(p.block_table + static_cast<size_t>(c.b) * p.max_blocks + page);
-        if (blk >= 0 && blk < p.num_blocks)
-          rec = (static_cast<long long>(blk) * p.num_kv_heads + c.kvh) * p.per_block + (tile - page * p.per_block);
-      }
+    const uint32_t base = smem_addr(smem);
+    // the places of the tile's records, lane x: record x
+    auto look_up = [&]() -> long long {
+      const int tile = at.tile * kRecords + lane;
+      if (lane >= kRecords || tile >= (at.rq.len + kKv4Tokens - 1) / kKv4Tokens) return -1;
+      const int page = p.block_shift >= 0 ? tile >> p.block_shift : tile / p.per_block;
+      const int blk = __ldg(p.block_table + static_cast<size_t>(at.b) * p.max_blocks + page);
+      if (blk < 0 || blk >= p.num_blocks) return -1;
+      return (static_cast<long long>(blk) * p.num_kv_heads + at.kvh) * p.per_block + (tile - page * p.per_block);
+    };
+    // half h of the run: the keys (even) or values (odd) of tile h / 2
+    uint4 raw[C::kPieces];
+    uint32_t sc[C::kPieces];
+    long long rec = look_up();
+    auto load = [&](int w) {
 #pragma unroll
       for (int x = 0; x < C::kPieces; ++x) {
         const int token = token0 + x * kStride, row = token % kKv4Tokens;
         const long long r = __shfl_sync(0xffffffffu, rec, token / kKv4Tokens);
         // what is not a token of the request becomes zeros, whatever the cache holds there
-        const bool real = r >= 0 && c.tile * kTileTokens + token < c.rq.len;
-        const uint8_t* base = static_cast<const uint8_t*>(p.cache) + (real ? r : 0) * kv4_record_bytes(D);
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          raw[w][x] = make_uint4(0u, 0u, 0u, 0u);
-          sc[w][x] = 0u;
-          if (real) {
-            raw[w][x] = __ldg(reinterpret_cast<const uint4*>(base + kv4_codes_at(D, w) + row * (D / 2) + 16 * piece));
-            sc[w][x] = __ldg(reinterpret_cast<const uint16_t*>(base + kv4_scales_at(D, w) + row * (D / 16) + 2 * piece));
-          }
+        raw[x] = make_uint4(0u, 0u, 0u, 0u);
+        sc[x] = 0u;
+        if (r >= 0 && at.tile * kTileTokens + token < at.rq.len) {
+          const uint8_t* src = static_cast<const uint8_t*>(p.cache) + r * kv4_record_bytes(D) + (w ? kv4_codes_at(D, 1) : 0);
+          raw[x] = __ldg(reinterpret_cast<const uint4*>(src + row * (D / 2) + 16 * piece));
+          sc[x] = __ldg(reinterpret_cast<const uint16_t*>(src + kv4_scales_at(D, 0) + row * (D / 16) + 2 * piece));
         }
       }
     };
-    load(at);
-    for (int j = 0; j < run_tiles && ok; ++j) {
-      const int stage = j % kStages;
-      const uint32_t phase = (j / kStages) & 1;
+    static_assert(kv4_scales_at(D, 1) - kv4_codes_at(D, 1) == kv4_scales_at(D, 0), "the halves of a record are alike");
+    load(0);
+#pragma unroll 1
+    for (int h = 0; h < 2 * run_tiles; ++h) {
+      const int j = h / 2, w = h & 1, stage = j % kStages;
+      uint4 now[C::kPieces];
+      uint32_t sn[C::kPieces];
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const uint32_t empty = smem_addr(w ? &s_vempty[stage] : &s_kempty[stage]);
-        if (j >= kStages && ok) ok = warp_wait(empty, phase ^ 1u);
-        if (!ok) break;
-        uint8_t* const tile = smem + (w ? C::kV : C::kK) + stage * C::kTileBytes;
-#pragma unroll
-        for (int x = 0; x < C::kPieces; ++x) {
-          const int token = token0 + x * kStride;
-          const __half2 s = e4m3x2_to_half2(sc[w][x]);
-          Kv4Scale s0 = kv4_scale<KIND>(__low2half2(s)), s1 = kv4_scale<KIND>(__high2half2(s));
-          uint32_t word[4] = {raw[w][x].x, raw[w][x].y, raw[w][x].z, raw[w][x].w};
-          // the second block's lanes store their words in another order: the
-          // eight lanes of a store then meet eight different bank groups
-          const bool turn = D == 128 && piece >= 2;
-          if (turn) {
-            uint32_t t0 = word[0], t1 = word[1];
-            word[0] = word[2];
-            word[1] = word[3];
-            word[2] = t0;
-            word[3] = t1;
-            const Kv4Scale ts = s0;
-            s0 = s1;
-            s1 = ts;
-          }
-          uint8_t* const row = tile + (D == 128 ? piece / 2 : 0) * C::kBlockBytes + token * 128;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t h[4];
-            kv4_decode8<KIND>(word[i], i < 2 ? s0 : s1, h);
-            const int chunk = (piece % 2) * 4 + (turn ? i ^ 2 : i);
-            *reinterpret_cast<uint4*>(row + ((chunk ^ (token & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-          }
+      for (int x = 0; x < C::kPieces; ++x) {
+        now[x] = raw[x];
+        sn[x] = sc[x];
+      }
+      if (h + 1 < 2 * run_tiles) {
+        if (w) {
+          if (++at.tile == at.tiles) at.next_unit(p);
+          rec = look_up();
         }
-        fence_proxy_async_shared();  // the stores before the tensor cores' reads
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(w ? &s_vfull[stage] : &s_kfull[stage]));
+        load(w ^ 1);
       }
-      if (j + 1 < run_tiles) {
-        if (++at.tile == at.tiles) at.next_unit(p);
-        load(at);
+      if (j >= kStages) ok = warp_wait(smem_addr(w ? &s_vempty[stage] : &s_kempty[stage]), ((j / kStages) & 1) ^ 1u);
+      if (!ok) break;
+      const uint32_t tile = base + (w ? C::kV : C::kK) + stage * C::kTileBytes;
+#pragma unroll
+      for (int x = 0; x < C::kPieces; ++x) {
+        const int token = token0 + x * kStride;
+        const __half2 s = e4m3x2_to_half2(sn[x]);
+        // the second block's lanes store their words in another order: the
+        // eight lanes of a store then meet eight different bank groups
+        const bool turn = D == 128 && piece >= 2;
+        const Kv4Scale s0 = kv4_scale<KIND>(turn ? __high2half2(s) : __low2half2(s));
+        const Kv4Scale s1 = kv4_scale<KIND>(turn ? __low2half2(s) : __high2half2(s));
+        const uint32_t word[4] = {turn ? now[x].z : now[x].x, turn ? now[x].w : now[x].y, turn ? now[x].x : now[x].z,
+                                  turn ? now[x].y : now[x].w};
+        const uint32_t row = tile + (D == 128 ? piece / 2 : 0) * C::kBlockBytes + token * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t v[4];
+          kv4_decode8<KIND>(word[i], i < 2 ? s0 : s1, v);
+          const int chunk = (piece % 2) * 4 + (turn ? i ^ 2 : i);
+          st_shared_v4(row + ((chunk ^ (token & 7)) << 4), v[0], v[1], v[2], v[3]);
+        }
       }
+      fence_proxy_async_shared();  // the stores before the tensor cores' reads
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(w ? &s_vfull[stage] : &s_kfull[stage]));
     }
   } else if (warp == 12) {
     // ================= MMAs, all by one lane
@@ -476,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         // the scale's sign goes to the query: the largest product is the largest score
         const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), cs);
         cs = fmaxf(fabsf(cs), 1e-37f);
-        uint8_t* const dst = smem + C::kQ + slot * C::kTileBytes + row * 128;
+        const uint32_t dst = smem_addr(smem) + C::kQ + slot * C::kTileBytes + row * 128;
 #pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
           const uint4 w = load8(src ? src + 8 * c : nullptr, p.q_vec);
@@ -491,8 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           uint32_t h[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) h[i] = as_u32(__floats2half2_rn(v[kv4_low<KIND>(i)], v[kv4_high<KIND>(i)]));
-          *reinterpret_cast<uint4*>(dst + (c / 8) * C::kBlockBytes + (((c % 8) ^ (row & 7)) << 4)) =
-              make_uint4(h[0], h[1], h[2], h[3]);
+          st_shared_v4(dst + (c / 8) * C::kBlockBytes + (((c % 8) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
         }
         if (!pair) s_ml[0][row] = cs;  // both slots take these rows
         fence_proxy_async_shared();
@@ -539,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           }
         };
         float mx = kNoScore;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < kTileTokens / 32; ++c) {
           uint32_t s[32];
           load_scores(c, s);
@@ -568,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         }
         const float bias = fmaf(-m, cs, 15.f - kHeadroom);
         float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < kTileTokens / 32; ++c) {
           uint32_t s[32], w[16];
           load_scores(c, s);
