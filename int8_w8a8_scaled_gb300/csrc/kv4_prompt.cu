@@ -13,7 +13,7 @@
 // before its conversion; the weights are f16(2^(s - m + 7)), with the maximum
 // m raised (and O rescaled) only when a score passes it by 2^8.
 //
-// One CTA to an SM, 13 warps: two softmax warpgroups (a thread owns a row of
+// One CTA to an SM, 14 warps: two softmax warpgroups (a thread owns a row of
 // its 128-row tile), four warps that decode K and V into swizzled tiles two
 // deep, one that issues the MMAs.  While one warpgroup is at its softmax the
 // tensor cores work for the other.  With more than 128 rows the warpgroups
@@ -42,7 +42,8 @@ constexpr int kTileRows = 128, kTileTokens = 128;
 constexpr int kUnitRows = 2 * kTileRows;
 constexpr int kSoftmaxThreads = 256;                   // warps 0-3: slot 0, 4-7: slot 1
 constexpr int kDecodeThreads = 128;                    // warps 8-11
-constexpr int kThreads = kSoftmaxThreads + kDecodeThreads + 32;  // and warp 12: the MMAs
+constexpr int kThreads = kSoftmaxThreads + kDecodeThreads + 64;  // and warp 12: the MMAs, 13: the copies
+constexpr int kRaw = 3;                                // halves (K or V of a tile) of codes in flight
 constexpr int kStages = 2;
 constexpr int kRecords = kTileTokens / kKv4Tokens;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -58,7 +59,8 @@ struct Big {
   static constexpr int kBlockBytes = 128 * 128;                 // 128 rows x 128 bytes
   static constexpr int kTileBytes = kHalves * kBlockBytes;      // a Q, K or V tile
   static constexpr int kQ = 0, kK = 2 * kTileBytes, kV = kK + kStages * kTileBytes;
-  static constexpr int kSmem = kV + kStages * kTileBytes + 1024;  // + alignment
+  static constexpr int kHalf = kv4_record_bytes(D) / 2;         // K or V of a record, codes and scales
+  static constexpr int kCodes = kV + kStages * kTileBytes, kSmem = kCodes + kRaw * kRecords * kHalf + 1024;  // + alignment
   static constexpr int kPart = kUnitRows * (D + 2);             // floats: o [D / 4][256][4], m [256], l [256]
   static constexpr int kPieces = kTileTokens * D / 2 / 16 / kDecodeThreads;  // 16-byte pieces of K a thread decodes
 };
@@ -198,11 +200,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t s_kfull[kStages], s_kempty[kStages], s_vfull[kStages], s_vempty[kStages];
+  __shared__ uint64_t s_rfull[kRaw], s_rempty[kRaw];
+  __shared__ uint8_t s_live[kRaw];  // which of a half's records lie in the cache
   __shared__ uint64_t s_qfull, s_sfull[2], s_pfull[2], s_pvdone[2];
   __shared__ uint32_t s_tmem;
   __shared__ long long s_scan[kThreads / 32], s_before;
   __shared__ int s_item, s_last[2];
-  __shared__ float s_ml[2][kTileRows];
+  __shared__ float s_ml[2][kTileRows], s_cs[2][kTileRows];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
   if (tid == 0) {
@@ -211,6 +215,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       mbar_init(smem_addr(&s_vfull[i]), kDecodeThreads / 32);
       mbar_init(smem_addr(&s_kempty[i]), 1);
       mbar_init(smem_addr(&s_vempty[i]), 1);
+    }
+    for (int i = 0; i < kRaw; ++i) {
+      mbar_init(smem_addr(&s_rfull[i]), kRecords);
+      mbar_init(smem_addr(&s_rempty[i]), kDecodeThreads / 32);
     }
     mbar_init(smem_addr(&s_qfull), kSoftmaxThreads / 32);
     for (int i = 0; i < 2; ++i) {
@@ -296,7 +304,58 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     constexpr int kStride = kDecodeThreads / kPerRow;     // tokens between a thread's pieces
     const int piece = dt % kPerRow, token0 = dt / kPerRow;
     const uint32_t base = smem_addr(smem);
-    // the places of the tile's records, lane x: record x
+    // the second block's lanes store their words in another order: the eight
+    // lanes of a store then meet eight different bank groups
+    const bool turn = D == 128 && piece >= 2;
+    // half h of the run: the keys (even) or values (odd) of tile h / 2
+#pragma unroll 1
+    for (int h = 0; h < 2 * run_tiles; ++h) {
+      const int j = h / 2, w = h & 1, stage = j % kStages, slot = h % kRaw;
+      if (!(ok = warp_wait(smem_addr(&s_rfull[slot]), (h / kRaw) & 1))) break;
+      const uint8_t* half = smem + C::kCodes + slot * kRecords * C::kHalf;
+      const uint32_t live = s_live[slot];
+      const int end = at.rq.len - at.tile * kTileTokens;
+      uint4 raw[C::kPieces];
+      uint32_t sc[C::kPieces];
+#pragma unroll
+      for (int x = 0; x < C::kPieces; ++x) {
+        const int token = token0 + x * kStride, row = token % kKv4Tokens;
+        const uint8_t* rec = half + token / kKv4Tokens * C::kHalf;
+        raw[x] = *reinterpret_cast<const uint4*>(rec + row * (D / 2) + 16 * piece);
+        // what is not a token of the request becomes zeros, whatever the cache holds there
+        sc[x] = token < end && (live >> (token / kKv4Tokens) & 1u)
+                    ? *reinterpret_cast<const uint16_t*>(rec + kv4_scales_at(D, 0) + row * (D / 16) + 2 * piece)
+                    : 0u;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&s_rempty[slot]));
+      if (j >= kStages) ok = warp_wait(smem_addr(w ? &s_vempty[stage] : &s_kempty[stage]), ((j / kStages) & 1) ^ 1u);
+      if (!ok) break;
+      const uint32_t tile = base + (w ? C::kV : C::kK) + stage * C::kTileBytes + (D == 128 ? piece / 2 : 0) * C::kBlockBytes;
+#pragma unroll
+      for (int x = 0; x < C::kPieces; ++x) {
+        const int token = token0 + x * kStride;
+        const __half2 s = e4m3x2_to_half2(sc[x]);
+        const Kv4Scale s0 = kv4_scale<KIND>(turn ? __high2half2(s) : __low2half2(s));
+        const Kv4Scale s1 = kv4_scale<KIND>(turn ? __low2half2(s) : __high2half2(s));
+        const uint32_t word[4] = {turn ? raw[x].z : raw[x].x, turn ? raw[x].w : raw[x].y, turn ? raw[x].x : raw[x].z,
+                                  turn ? raw[x].y : raw[x].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t v[4];
+          kv4_decode8<KIND>(word[i], i < 2 ? s0 : s1, v);
+          const int chunk = (piece % 2) * 4 + (turn ? i ^ 2 : i);
+          st_shared_v4(tile + token * 128 + ((chunk ^ (token & 7)) << 4), v[0], v[1], v[2], v[3]);
+        }
+      }
+      fence_proxy_async_shared();  // the stores before the tensor cores' reads
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(w ? &s_vfull[stage] : &s_kfull[stage]));
+      if (w && h + 1 < 2 * run_tiles && ++at.tile == at.tiles) at.next_unit(p);
+    }
+  } else if (warp == 13) {
+    // ================= copies: lane x has record x of the tile
+    const uint32_t codes = smem_addr(smem) + C::kCodes + lane * C::kHalf;
     auto look_up = [&]() -> long long {
       const int tile = at.tile * kRecords + lane;
       if (lane >= kRecords || tile >= (at.rq.len + kKv4Tokens - 1) / kKv4Tokens) return -1;
@@ -305,71 +364,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       if (blk < 0 || blk >= p.num_blocks) return -1;
       return (static_cast<long long>(blk) * p.num_kv_heads + at.kvh) * p.per_block + (tile - page * p.per_block);
     };
-    // half h of the run: the keys (even) or values (odd) of tile h / 2
-    uint4 raw[C::kPieces];
-    uint32_t sc[C::kPieces];
-    long long rec = look_up();
-    auto load = [&](int w) {
-#pragma unroll
-      for (int x = 0; x < C::kPieces; ++x) {
-        const int token = token0 + x * kStride, row = token % kKv4Tokens;
-        const long long r = __shfl_sync(0xffffffffu, rec, token / kKv4Tokens);
-        // what is not a token of the request becomes zeros, whatever the cache holds there
-        raw[x] = make_uint4(0u, 0u, 0u, 0u);
-        sc[x] = 0u;
-        if (r >= 0 && at.tile * kTileTokens + token < at.rq.len) {
-          const uint8_t* src = static_cast<const uint8_t*>(p.cache) + r * kv4_record_bytes(D) + (w ? kv4_codes_at(D, 1) : 0);
-          raw[x] = __ldg(reinterpret_cast<const uint4*>(src + row * (D / 2) + 16 * piece));
-          sc[x] = __ldg(reinterpret_cast<const uint16_t*>(src + kv4_scales_at(D, 0) + row * (D / 16) + 2 * piece));
-        }
-      }
-    };
-    static_assert(kv4_scales_at(D, 1) - kv4_codes_at(D, 1) == kv4_scales_at(D, 0), "the halves of a record are alike");
-    load(0);
+    long long next = look_up(), rec = -1;
 #pragma unroll 1
     for (int h = 0; h < 2 * run_tiles; ++h) {
-      const int j = h / 2, w = h & 1, stage = j % kStages;
-      uint4 now[C::kPieces];
-      uint32_t sn[C::kPieces];
-#pragma unroll
-      for (int x = 0; x < C::kPieces; ++x) {
-        now[x] = raw[x];
-        sn[x] = sc[x];
-      }
-      if (h + 1 < 2 * run_tiles) {
-        if (w) {
+      const int slot = h % kRaw;
+      if (!(h & 1)) {
+        rec = next;
+        if (h + 2 < 2 * run_tiles) {  // the next tile's places, while this one's are copied
           if (++at.tile == at.tiles) at.next_unit(p);
-          rec = look_up();
-        }
-        load(w ^ 1);
-      }
-      if (j >= kStages) ok = warp_wait(smem_addr(w ? &s_vempty[stage] : &s_kempty[stage]), ((j / kStages) & 1) ^ 1u);
-      if (!ok) break;
-      const uint32_t tile = base + (w ? C::kV : C::kK) + stage * C::kTileBytes;
-#pragma unroll
-      for (int x = 0; x < C::kPieces; ++x) {
-        const int token = token0 + x * kStride;
-        const __half2 s = e4m3x2_to_half2(sn[x]);
-        // the second block's lanes store their words in another order: the
-        // eight lanes of a store then meet eight different bank groups
-        const bool turn = D == 128 && piece >= 2;
-        const Kv4Scale s0 = kv4_scale<KIND>(turn ? __high2half2(s) : __low2half2(s));
-        const Kv4Scale s1 = kv4_scale<KIND>(turn ? __low2half2(s) : __high2half2(s));
-        const uint32_t word[4] = {turn ? now[x].z : now[x].x, turn ? now[x].w : now[x].y, turn ? now[x].x : now[x].z,
-                                  turn ? now[x].y : now[x].w};
-        const uint32_t row = tile + (D == 128 ? piece / 2 : 0) * C::kBlockBytes + token * 128;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t v[4];
-          kv4_decode8<KIND>(word[i], i < 2 ? s0 : s1, v);
-          const int chunk = (piece % 2) * 4 + (turn ? i ^ 2 : i);
-          st_shared_v4(row + ((chunk ^ (token & 7)) << 4), v[0], v[1], v[2], v[3]);
+          next = look_up();
         }
       }
-      fence_proxy_async_shared();  // the stores before the tensor cores' reads
+      if (h >= kRaw && !(ok = warp_wait(smem_addr(&s_rempty[slot]), ((h / kRaw) & 1) ^ 1u))) break;
+      const uint32_t live = __ballot_sync(0xffffffffu, rec >= 0);
+      if (lane == 0) s_live[slot] = static_cast<uint8_t>(live);
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(w ? &s_vfull[stage] : &s_kfull[stage]));
+      if (lane < kRecords) {
+        const uint32_t full = smem_addr(&s_rfull[slot]);
+        fence_proxy_async_shared();  // the reads of the slot's last half before the copies over it
+        if (rec >= 0) {
+          mbar_arrive_expect_tx(full, C::kHalf);
+          bulk_load(codes + slot * kRecords * C::kHalf,
+                    static_cast<const uint8_t*>(p.cache) + rec * kv4_record_bytes(D) + (h & 1) * C::kHalf, C::kHalf, full);
+        } else {
+          mbar_arrive(full);
+        }
+      }
     }
+    // a wait gave up: the copies in flight land before shared memory is released
+    if (!ok)
+      for (int i = 0; i < kRaw; ++i) mbar_wait(smem_addr(&s_rfull[i]), 0), mbar_wait(smem_addr(&s_rfull[i]), 1);
   } else if (warp == 12) {
     // ================= MMAs, all by one lane
     if (lane == 0) {
@@ -455,56 +479,59 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       const int my = row0 + (pair ? slot * kTileRows : 0) + row;  // the request's row
       const bool real = my < rq.rows;
 
-      // ---- the query row, scaled by 2^e so that its largest element lies in [2^14, 2^15)
-      float cs = 0.f;
+      // ---- the warp's 32 query rows, a 16-byte piece for each lane, scaled by
+      // 2^e so that a row's largest element lies in [2^14, 2^15)
       if (pair || slot == 0) {
-        const uint16_t* src = real ? static_cast<const uint16_t*>(p.q) + (rq.first + my / p.share) * p.q_token_stride +
-                                         (at.kvh * p.share + my % p.share) * p.q_head_stride
-                                   : nullptr;
-        float qmax = 0.f;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 w = load8(src ? src + 8 * c : nullptr, p.q_vec);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        constexpr int kPerRow = D / 8, kAtOnce = 32 / kPerRow;  // pieces of a row, rows of one load
+        const int c = lane % kPerRow, wrow = 32 * (warp % 4) + lane / kPerRow;
+        const float to_log2 = p.sm_scale * kscale * kLog2e;
+        const uint32_t dst = smem_addr(smem) + C::kQ + slot * C::kTileBytes + (c / 8) * C::kBlockBytes;
+        constexpr int kBatch = 4;  // loads in flight
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32 / kAtOnce; i0 += kBatch) {
+        uint4 raw[kBatch];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 v = to_float2(u[i], p.q_fp16);
-            qmax = fmaxf(qmax, fmaxf(fabsf(v.x), fabsf(v.y)));
-          }
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = my - row + wrow + (i0 + i) * kAtOnce;
+          raw[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < rq.rows)
+            raw[i] = load8(static_cast<const uint16_t*>(p.q) + (rq.first + r / p.share) * p.q_token_stride +
+                               (at.kvh * p.share + r % p.share) * p.q_head_stride + 8 * c,
+                           p.q_vec);
         }
-        int e = 0;
-        if (qmax > 0.f && qmax <= 3.0e38f) e = min(100, max(-100, 14 + 127 - static_cast<int>(__float_as_uint(qmax) >> 23)));
-        cs = p.sm_scale * kscale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        // the scale's sign goes to the query: the largest product is the largest score
-        const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), cs);
-        cs = fmaxf(fabsf(cs), 1e-37f);
-        const uint32_t dst = smem_addr(smem) + C::kQ + slot * C::kTileBytes + row * 128;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 w = load8(src ? src + 8 * c : nullptr, p.q_vec);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-          float v[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 x = to_float2(u[i], p.q_fp16);
-            v[2 * i] = x.x * up;
-            v[2 * i + 1] = x.y * up;
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = wrow + (i0 + i) * kAtOnce;
+          const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+          float v[8], qmax = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 x = to_float2(u[k], p.q_fp16);
+            v[2 * k] = x.x;
+            v[2 * k + 1] = x.y;
+            qmax = fmaxf(qmax, fmaxf(fabsf(x.x), fabsf(x.y)));
           }
+#pragma unroll
+          for (int off = 1; off < kPerRow; off <<= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, off));
+          int e = 0;
+          if (qmax > 0.f && qmax <= 3.0e38f) e = min(100, max(-100, 14 + 127 - static_cast<int>(__float_as_uint(qmax) >> 23)));
+          const float down = to_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          // the scale's sign goes to the query: the largest product is the largest score
+          const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), down);
+          if (c == 0) s_cs[slot][r] = fmaxf(fabsf(down), 1e-37f);
           uint32_t h[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) h[i] = as_u32(__floats2half2_rn(v[kv4_low<KIND>(i)], v[kv4_high<KIND>(i)]));
-          st_shared_v4(dst + (c / 8) * C::kBlockBytes + (((c % 8) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+          for (int k = 0; k < 4; ++k)
+            h[k] = as_u32(__floats2half2_rn(v[kv4_low<KIND>(k)] * up, v[kv4_high<KIND>(k)] * up));
+          st_shared_v4(dst + r * 128 + (((c % 8) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
         }
-        if (!pair) s_ml[0][row] = cs;  // both slots take these rows
+        }
         fence_proxy_async_shared();
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&s_qfull));
-      if (!pair) {
-        softmax_sync();
-        cs = s_ml[0][row];
-        softmax_sync();
-      }
+      if (!pair) softmax_sync();
+      const float cs = s_cs[pair ? slot : 0][row];
       const int lim = real ? rq.len - rq.n + my / p.share : rq.len - 1;  // the last token seen
       const float room = fminf(kHeadroom / cs, 1e38f);
       float m = kNoScore, l = 0.f;
@@ -529,23 +556,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         if (!ok) break;
         tc_fence_after();
         // the maximum first, then the weights: 128 columns at once would not fit the registers
-        auto load_scores = [&](int c, uint32_t (&s)[32]) {
-          tmem_ld32(s_cols + 32 * c, s);
-          tmem_ld_wait();
-          if (edge) {
-            asm volatile("");
+        if (edge) {
+          // what a row does not see, written back as -infinity: rare, and apart
+          // from the loops below, whose code has to stay in the instruction cache
+#pragma unroll 1
+          for (int c = 0; c < kTileTokens / 16; ++c) {
+            uint32_t s[16];
+            tmem_ld16(s_cols + 16 * c, s);
+            tmem_ld_wait();
+            tmem_loaded(s);
+            const int seen = holes >> c & 1u ? 0 : lim + 1 - t0 - 16 * c;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (t0 + 32 * c + i > lim || (holes >> (2 * c + i / 16) & 1u)) s[i] = __float_as_uint(-INFINITY);
+            for (int i = 0; i < 16; ++i)
+              if (i >= seen) s[i] = __float_as_uint(-INFINITY);
+            tmem_st16(s_cols + 16 * c, s);
           }
-        };
+          tmem_st_wait();
+        }
         float mx = kNoScore;
 #pragma unroll 1
-        for (int c = 0; c < kTileTokens / 32; ++c) {
-          uint32_t s[32];
-          load_scores(c, s);
+        for (int c = 0; c < kTileTokens / 32; c += 2) {
+          uint32_t s[2][32];
+          tmem_ld32(s_cols + 32 * c, s[0]);
+          tmem_ld32(s_cols + 32 * c + 32, s[1]);
+          tmem_ld_wait();
+          tmem_loaded(s[0]);
+          tmem_loaded(s[1]);
+          float x[4] = {mx, mx, mx, mx};
 #pragma unroll
-          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(s[i]));
+          for (int i = 0; i < 32; i += 4)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              x[k] = fmaxf(x[k], fmaxf(__uint_as_float(s[0][i + k]), __uint_as_float(s[1][i + k])));
+          mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
         }
         if (__any_sync(0xffffffffu, mx > m + room)) {
           const float mn = fmaxf(m, mx);
@@ -556,31 +599,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             if (ok) ok = warp_wait(smem_addr(&s_pvdone[slot]), (count - 1) & 1);
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(o_cols + 32 * c, o);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(o_cols + 16 * c, o);
               tmem_ld_wait();
+              tmem_loaded(o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st32(o_cols + 32 * c, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st16(o_cols + 16 * c, o);
             }
             tmem_st_wait();
           }
         }
         const float bias = fmaf(-m, cs, 15.f - kHeadroom);
         float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll 1
-        for (int c = 0; c < kTileTokens / 32; ++c) {
-          uint32_t s[32], w[16];
-          load_scores(c, s);
+        auto weights = [&](const uint32_t (&s)[16], uint32_t* w) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
+          for (int i = 0; i < 16; i += 2) {
             const float a = ex2_fast(fmaf(__uint_as_float(s[i]), cs, bias));
             const float b = ex2_fast(fmaf(__uint_as_float(s[i + 1]), cs, bias));
             sum0 += a;
             sum1 += b;
             w[i / 2] = as_u32(__floats2half2_rn(a, b));
           }
+        };
+        uint32_t sa[16], sb[16], w[16];  // the next columns are on their way while these are worked on
+        tmem_ld16(s_cols, sa);
+#pragma unroll 1
+        for (int c = 0; c < kTileTokens / 32; ++c) {
+          tmem_ld_wait();
+          tmem_loaded(sa);
+          tmem_ld16(s_cols + 32 * c + 16, sb);
+          weights(sa, w);
+          tmem_ld_wait();
+          tmem_loaded(sb);
+          if (c + 1 < kTileTokens / 32) tmem_ld16(s_cols + 32 * c + 32, sa);
+          weights(sb, w + 8);
           tmem_st16(s_cols + 16 * c, w);  // over scores that have been read
         }
         l += sum0 + sum1;
@@ -628,12 +682,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           uint32_t o[32];
           tmem_ld32(o_cols + 32 * c, o);
           tmem_ld_wait();
+          tmem_loaded(o);
           float y[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(o[i]) * a0;
           if (both) {
             tmem_ld32(o_cols + D + 32 * c, o);
             tmem_ld_wait();
+            tmem_loaded(o);
 #pragma unroll
             for (int i = 0; i < 32; ++i) y[i] = fmaf(__uint_as_float(o[i]), a1, y[i]);
           }
