@@ -148,6 +148,9 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// A value that all lanes share, known as such to the compiler.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // 8 16-bit values at `src` (null: zeros).
 __device__ __forceinline__ uint4 load8(const uint16_t* src, int vec) {
   if (!src) return make_uint4(0u, 0u, 0u, 0u);
@@ -395,74 +398,77 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     if (!ok)
       for (int i = 0; i < kRaw; ++i) mbar_wait(smem_addr(&s_rfull[i]), 0), mbar_wait(smem_addr(&s_rfull[i]), 1);
   } else if (warp == 12) {
-    // ================= MMAs, all by one lane
-    if (lane == 0) {
-      constexpr uint32_t kIdescS = make_idesc(kTileRows, kTileTokens, 0);
-      constexpr uint32_t kIdescO = make_idesc(kTileRows, D, 0) | (1u << 16);  // V: dims contiguous
-      const uint32_t base = smem_addr(smem);
-      uint32_t pcount[2] = {0u, 0u};  // weight tiles taken, each slot
-      int done = 0, units = 0;
-      while (done < run_tiles && ok) {
-        const int nt = min(at.tiles - at.tile, run_tiles - done);
-        const bool pair = at.rq.rows - at.rt * kUnitRows > kTileRows;
-        const int ahead = pair ? 1 : 2;
-        ok = mbar_wait(smem_addr(&s_qfull), units & 1);
-        tc_fence_after();
-        auto scores = [&](int j, int slot) {
-          const int stage = (done + j) % kStages;
+    // ================= MMAs: the warp runs converged on uniform values, one lane issues
+    const uint32_t leader = elect_one();
+    constexpr uint32_t kIdescS = make_idesc(kTileRows, kTileTokens, 0);
+    constexpr uint32_t kIdescO = make_idesc(kTileRows, D, 0) | (1u << 16);  // V: dims contiguous
+    const uint32_t tm = uniform(tmem);
+    const uint64_t dq = smem_desc_sw128(smem_addr(smem) + C::kQ), dk = smem_desc_sw128(smem_addr(smem) + C::kK);
+    const uint64_t dv = smem_desc_mn_sw128(smem_addr(smem) + C::kV, C::kBlockBytes);
+    const int all = uniform(run_tiles);
+    uint32_t pcount[2] = {0u, 0u};  // weight tiles taken, each slot
+    int done = 0, units = 0;
+    auto scores = [&](int tile, int slot, int q) {
+      const int stage = tile % kStages;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk / 4) * C::kBlockBytes;
-            const uint64_t da = smem_desc_sw128(base + C::kQ + (pair ? slot : 0) * C::kTileBytes + off) + 2 * (kk % 4);
-            const uint64_t db = smem_desc_sw128(base + C::kK + stage * C::kTileBytes + off) + 2 * (kk % 4);
-            mma_f16(tmem + slot * kTileTokens, da, db, kIdescS, kk > 0);
-          }
-          mma_commit(smem_addr(&s_sfull[slot]));
-        };
-        auto wait_k = [&](int j) {
-          if (ok) ok = mbar_wait(smem_addr(&s_kfull[(done + j) % kStages]), ((done + j) / kStages) & 1);
-          tc_fence_after();
-        };
-        for (int j = 0; j < ahead && j < nt && ok; ++j) {
-          wait_k(j);
-          for (int slot = 0; slot < 2; ++slot)
-            if (ok && (pair || slot == (j & 1))) scores(j, slot);
-          mma_commit(smem_addr(&s_kempty[(done + j) % kStages]));
-        }
-        for (int j = 0; j < nt && ok; ++j) {
-          const int stage = (done + j) % kStages;
-          const bool more = j + ahead < nt;
-          ok = mbar_wait(smem_addr(&s_vfull[stage]), ((done + j) / kStages) & 1);
-          for (int slot = 0; slot < 2 && ok; ++slot) {
-            if (!pair && slot != (j & 1)) continue;
-            ok = mbar_wait(smem_addr(&s_pfull[slot]), pcount[slot] & 1);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < kTileTokens / 16; ++kk) {
-              const uint64_t db = smem_desc_mn_sw128(base + C::kV + stage * C::kTileBytes + kk * 2048, C::kBlockBytes);
-              mma_f16_ts(tmem + 2 * kTileTokens + slot * D, tmem + slot * kTileTokens + 8 * kk, db, kIdescO,
-                         kk > 0 || j >= (pair ? 1 : 2));
-            }
-            mma_commit(smem_addr(&s_pvdone[slot]));
-            if (more) {
-              if (pair ? slot == 0 : true) wait_k(j + ahead);
-              // the scores overwrite the weights
-              if (ok) ok = mbar_wait(smem_addr(&s_pvdone[slot]), pcount[slot] & 1);
-              if (ok) scores(j + ahead, slot);
-            }
-            ++pcount[slot];
-          }
-          mma_commit(smem_addr(&s_vempty[stage]));
-          if (more) mma_commit(smem_addr(&s_kempty[(done + j + ahead) % kStages]));
-        }
-        done += nt;
-        ++units;
-        at.tile += nt;
-        if (done < run_tiles) at.next_unit(p);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk / 4) * (C::kBlockBytes >> 4) + 2 * (kk % 4);
+        mma_f16_by(leader, tm + slot * kTileTokens, dq + q * (C::kTileBytes >> 4) + off,
+                   dk + stage * (C::kTileBytes >> 4) + off, kIdescS, kk > 0);
       }
+      mma_commit_by(leader, smem_addr(&s_sfull[slot]));
+    };
+    auto wait_k = [&](int tile) {
+      if (ok) ok = warp_wait(smem_addr(&s_kfull[tile % kStages]), (tile / kStages) & 1);
+      tc_fence_after();
+    };
+#pragma unroll 1
+    while (done < all && ok) {
+      const int nt = uniform(min(at.tiles - at.tile, all - done));
+      const bool pair = uniform(at.rq.rows - at.rt * kUnitRows > kTileRows);
+      const int ahead = pair ? 1 : 2;
+      ok = warp_wait(smem_addr(&s_qfull), units & 1);
+      tc_fence_after();
+#pragma unroll 1
+      for (int j = 0; j < ahead && j < nt && ok; ++j) {
+        wait_k(done + j);
+        if (!ok) break;
+#pragma unroll 1
+        for (int slot = pair ? 0 : j; slot < (pair ? 2 : j + 1); ++slot) scores(done + j, slot, pair ? slot : 0);
+        mma_commit_by(leader, smem_addr(&s_kempty[(done + j) % kStages]));
+      }
+#pragma unroll 1
+      for (int j = 0; j < nt && ok; ++j) {
+        const int stage = (done + j) % kStages;
+        const bool more = j + ahead < nt;
+        ok = warp_wait(smem_addr(&s_vfull[stage]), ((done + j) / kStages) & 1);
+#pragma unroll 1
+        for (int slot = pair ? 0 : j & 1, end = pair ? 2 : slot + 1; slot < end && ok; ++slot) {
+          const uint32_t parity = (slot ? pcount[1] : pcount[0]) & 1u;
+          if (slot) ++pcount[1];
+          else ++pcount[0];
+          if (!(ok = warp_wait(smem_addr(&s_pfull[slot]), parity))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kTileTokens / 16; ++kk)
+            mma_f16_ts_by(leader, tm + 2 * kTileTokens + slot * D, tm + slot * kTileTokens + 8 * kk,
+                          dv + stage * (C::kTileBytes >> 4) + kk * (2048 >> 4), kIdescO, kk > 0 || j >= ahead);
+          mma_commit_by(leader, smem_addr(&s_pvdone[slot]));
+          if (more) {
+            if (slot == 0 || !pair) wait_k(done + j + ahead);
+            // the scores overwrite the weights
+            if (ok) ok = warp_wait(smem_addr(&s_pvdone[slot]), parity);
+            if (ok) scores(done + j + ahead, slot, pair ? slot : 0);
+          }
+        }
+        mma_commit_by(leader, smem_addr(&s_vempty[stage]));
+        if (more) mma_commit_by(leader, smem_addr(&s_kempty[(done + j + ahead) % kStages]));
+      }
+      done += nt;
+      ++units;
+      at.tile += nt;
+      if (done < all) at.next_unit(p);
     }
-    __syncwarp();
   } else {
     // ================= softmax: thread = row of slot `slot`
     const int slot = warp / 4, row = tid % kTileRows;
