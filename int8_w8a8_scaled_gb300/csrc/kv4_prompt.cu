@@ -40,9 +40,11 @@ namespace {
 
 constexpr int kTileRows = 128, kTileTokens = 128;
 constexpr int kUnitRows = 2 * kTileRows;
-constexpr int kSoftmaxThreads = 256;                   // warps 0-3: slot 0, 4-7: slot 1
-constexpr int kDecodeThreads = 128;                    // warps 8-11
-constexpr int kThreads = kSoftmaxThreads + kDecodeThreads + 64;  // and warp 12: the MMAs, 13: the copies
+constexpr int kSoftmaxThreads = 512;                   // two slots of 8 warps, two threads to a row
+constexpr int kSlotThreads = kSoftmaxThreads / 2;
+constexpr int kDecodeThreads = 128;
+constexpr int kDecodeWarp = kSoftmaxThreads / 32, kMmaWarp = kDecodeWarp + kDecodeThreads / 32, kCopyWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kCopyWarp + 1);
 constexpr int kRaw = 3;                                // halves (K or V of a tile) of codes in flight
 constexpr int kStages = 2;
 constexpr int kRecords = kTileTokens / kKv4Tokens;
@@ -119,9 +121,37 @@ __device__ __forceinline__ float ex2_fast(float x) {
   return y;
 }
 
+// Two fp32 numbers in one register pair, and their arithmetic.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory"); }
 
-// The same, and whether `ok` holds in all of them.
+// The 8 warps of a slot, the two warps that share 32 rows.
+__device__ __forceinline__ void slot_sync(int slot) {
+  asm volatile("bar.sync %0, %1;" ::"r"(2 + slot), "n"(kSlotThreads) : "memory");
+}
+__device__ __forceinline__ void rows_sync(int slot, int quarter) {
+  asm volatile("bar.sync %0, 64;" ::"r"(4 + 4 * slot + quarter) : "memory");
+}
+
+// All softmax warps, and whether `ok` holds in all of them.
 __device__ __forceinline__ bool softmax_all(bool ok) {
   uint32_t r;
   asm volatile(
@@ -209,7 +239,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   __shared__ uint32_t s_tmem;
   __shared__ long long s_scan[kThreads / 32], s_before;
   __shared__ int s_item, s_last[2];
-  __shared__ float s_ml[2][kTileRows], s_cs[2][kTileRows];
+  __shared__ Open s_open[2];  // the unit begun in front of this CTA, the one begun here
+  __shared__ float s_cs[2][kTileRows];         // scale of each row's scores
+  __shared__ float s_mx[2][2][2][kTileRows];   // largest score: tile's parity, slot, half of the tokens
+  // at a unit's end, when nobody reads the last scores any more: sums by slot and half, and slot 1's maximum
+  float (&s_l)[2][2][kTileRows] = s_mx[0];
+  float (&s_m)[kTileRows] = s_mx[1][0][0];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
   if (tid == 0) {
@@ -226,15 +261,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     mbar_init(smem_addr(&s_qfull), kSoftmaxThreads / 32);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&s_sfull[i]), 1);
-      mbar_init(smem_addr(&s_pfull[i]), 4);
+      mbar_init(smem_addr(&s_pfull[i]), kSlotThreads / 32);
       mbar_init(smem_addr(&s_pvdone[i]), 1);
     }
     fence_barrier_init();
   }
+  if (tid < 2) s_open[tid].unit = -1;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // TMEM only now: a kernel in front may still need it
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     tmem_alloc(smem_addr(&s_tmem), kTmemCols);
     tmem_relinquish();
   }
@@ -295,12 +331,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     at.tile = static_cast<int>((r0 - s_before) % at.tiles);
   }
   bool ok = true;
-  Open open0, open1;  // the unit begun in front of this CTA, the one begun here
-  open0.unit = open1.unit = -1;
 
   if (run_tiles == 0) {
     // nothing to do
-  } else if (warp >= 8 && warp < 12) {
+  } else if (warp >= kDecodeWarp && warp < kMmaWarp) {
     // ================= decoding: thread (token, piece) of each 16-byte piece of codes
     const int dt = tid - kSoftmaxThreads;
     constexpr int kPerRow = D / 32;                       // pieces of a token's row
@@ -356,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       if (lane == 0) mbar_arrive(smem_addr(w ? &s_vfull[stage] : &s_kfull[stage]));
       if (w && h + 1 < 2 * run_tiles && ++at.tile == at.tiles) at.next_unit(p);
     }
-  } else if (warp == 13) {
+  } else if (warp == kCopyWarp) {
     // ================= copies: lane x has record x of the tile
     const uint32_t codes = smem_addr(smem) + C::kCodes + lane * C::kHalf;
     auto look_up = [&]() -> long long {
@@ -397,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     // a wait gave up: the copies in flight land before shared memory is released
     if (!ok)
       for (int i = 0; i < kRaw; ++i) mbar_wait(smem_addr(&s_rfull[i]), 0), mbar_wait(smem_addr(&s_rfull[i]), 1);
-  } else if (warp == 12) {
+  } else if (warp == kMmaWarp) {
     // ================= MMAs: the warp runs converged on uniform values, one lane issues
     const uint32_t leader = elect_one();
     constexpr uint32_t kIdescS = make_idesc(kTileRows, kTileTokens, 0);
@@ -451,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kTileTokens / 16; ++kk)
-            mma_f16_ts_by(leader, tm + 2 * kTileTokens + slot * D, tm + slot * kTileTokens + 8 * kk,
+            mma_f16_ts_by(leader, tm + 2 * kTileTokens + slot * D, tm + slot * kTileTokens + 64 * (kk / 4) + 8 * (kk % 4),
                           dv + stage * (C::kTileBytes >> 4) + kk * (2048 >> 4), kIdescO, kk > 0 || j >= ahead);
           mma_commit_by(leader, smem_addr(&s_pvdone[slot]));
           if (more) {
@@ -470,73 +504,75 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       if (done < all) at.next_unit(p);
     }
   } else {
-    // ================= softmax: thread = row of slot `slot`
-    const int slot = warp / 4, row = tid % kTileRows;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp % 4) << 21);  // this warp's 32 TMEM lanes
-    const uint32_t s_cols = lanes + slot * kTileTokens, o_cols = lanes + 2 * kTileTokens + slot * D;
-    const float kscale = __ldg(p.k_scale), vscale = __ldg(p.v_scale);
+    // ================= softmax: thread = row of slot `slot` and half of its tokens (or dims)
+    const int slot = warp / 8, half = warp / 4 % 2, quarter = warp % 4, row = 32 * quarter + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter) << 21);  // this warp's 32 TMEM lanes
+    const uint32_t s_cols = lanes + slot * kTileTokens, o_cols = lanes + 2 * kTileTokens + slot * D + half * (D / 2);
+    const float vscale = __ldg(p.v_scale), to_log2 = p.sm_scale * __ldg(p.k_scale) * kLog2e;
     uint32_t count = 0u;  // tiles of this slot
     int done = 0;
+#pragma unroll 1
     while (done < run_tiles) {
       const int nt = min(at.tiles - at.tile, run_tiles - done);
       const Request rq = at.rq;
       const int row0 = at.rt * kUnitRows;
       const bool pair = rq.rows - row0 > kTileRows;
-      const int my = row0 + (pair ? slot * kTileRows : 0) + row;  // the request's row
+      const int top = row0 + (pair ? slot * kTileRows : 0);  // the request's row in this slot's row 0
+      const int my = top + row;
       const bool real = my < rq.rows;
 
-      // ---- the warp's 32 query rows, a 16-byte piece for each lane, scaled by
+      // ---- the warp's 16 query rows, a 16-byte piece for each lane, scaled by
       // 2^e so that a row's largest element lies in [2^14, 2^15)
       if (pair || slot == 0) {
         constexpr int kPerRow = D / 8, kAtOnce = 32 / kPerRow;  // pieces of a row, rows of one load
-        const int c = lane % kPerRow, wrow = 32 * (warp % 4) + lane / kPerRow;
-        const float to_log2 = p.sm_scale * kscale * kLog2e;
+        constexpr int kBatch = 4;                               // loads in flight
+        const int c = lane % kPerRow, wrow = 16 * (warp % 8) + lane / kPerRow;
         const uint32_t dst = smem_addr(smem) + C::kQ + slot * C::kTileBytes + (c / 8) * C::kBlockBytes;
-        constexpr int kBatch = 4;  // loads in flight
 #pragma unroll 1
-        for (int i0 = 0; i0 < 32 / kAtOnce; i0 += kBatch) {
-        uint4 raw[kBatch];
+        for (int i0 = 0; i0 < 16 / kAtOnce; i0 += kBatch) {
+          uint4 raw[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int r = my - row + wrow + (i0 + i) * kAtOnce;
-          raw[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < rq.rows)
-            raw[i] = load8(static_cast<const uint16_t*>(p.q) + (rq.first + r / p.share) * p.q_token_stride +
-                               (at.kvh * p.share + r % p.share) * p.q_head_stride + 8 * c,
-                           p.q_vec);
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int r = wrow + (i0 + i) * kAtOnce;
-          const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-          float v[8], qmax = 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 x = to_float2(u[k], p.q_fp16);
-            v[2 * k] = x.x;
-            v[2 * k + 1] = x.y;
-            qmax = fmaxf(qmax, fmaxf(fabsf(x.x), fabsf(x.y)));
+          for (int i = 0; i < kBatch; ++i) {
+            const int r = top + wrow + (i0 + i) * kAtOnce;
+            raw[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < rq.rows)
+              raw[i] = load8(static_cast<const uint16_t*>(p.q) + (rq.first + r / p.share) * p.q_token_stride +
+                                 (at.kvh * p.share + r % p.share) * p.q_head_stride + 8 * c,
+                             p.q_vec);
           }
 #pragma unroll
-          for (int off = 1; off < kPerRow; off <<= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, off));
-          int e = 0;
-          if (qmax > 0.f && qmax <= 3.0e38f) e = min(100, max(-100, 14 + 127 - static_cast<int>(__float_as_uint(qmax) >> 23)));
-          const float down = to_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-          // the scale's sign goes to the query: the largest product is the largest score
-          const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), down);
-          if (c == 0) s_cs[slot][r] = fmaxf(fabsf(down), 1e-37f);
-          uint32_t h[4];
+          for (int i = 0; i < kBatch; ++i) {
+            const int r = wrow + (i0 + i) * kAtOnce;
+            const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            float v[8], qmax = 0.f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            h[k] = as_u32(__floats2half2_rn(v[kv4_low<KIND>(k)] * up, v[kv4_high<KIND>(k)] * up));
-          st_shared_v4(dst + r * 128 + (((c % 8) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-        }
+            for (int k = 0; k < 4; ++k) {
+              const float2 x = to_float2(u[k], p.q_fp16);
+              v[2 * k] = x.x;
+              v[2 * k + 1] = x.y;
+              qmax = fmaxf(qmax, fmaxf(fabsf(x.x), fabsf(x.y)));
+            }
+#pragma unroll
+            for (int off = 1; off < kPerRow; off <<= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, off));
+            int e = 0;
+            if (qmax > 0.f && qmax <= 3.0e38f) e = min(100, max(-100, 14 + 127 - static_cast<int>(__float_as_uint(qmax) >> 23)));
+            const float down = to_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            // the scale's sign goes to the query: the largest product is the largest score
+            const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), down);
+            if (c == 0) s_cs[slot][r] = fmaxf(fabsf(down), 1e-37f);
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              h[k] = as_u32(__floats2half2_rn(v[kv4_low<KIND>(k)] * up, v[kv4_high<KIND>(k)] * up));
+            st_shared_v4(dst + r * 128 + (((c % 8) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+          }
         }
         fence_proxy_async_shared();
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&s_qfull));
-      if (!pair) softmax_sync();
+      if (pair) slot_sync(slot);
+      else softmax_sync();
       const float cs = s_cs[pair ? slot : 0][row];
       const int lim = real ? rq.len - rq.n + my / p.share : rq.len - 1;  // the last token seen
       const float room = fminf(kHeadroom / cs, 1e38f);
@@ -544,8 +580,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       int mine = 0;  // tiles of this slot in the unit
 
       // ---- its tiles
+#pragma unroll 1
       for (int j = pair ? 0 : slot; j < nt; j += pair ? 1 : 2) {
-        const int t0 = (at.tile + j) * kTileTokens;
+        const int t0 = (at.tile + j) * kTileTokens + half * 64;  // this thread's 64 tokens
         // records that lie outside the cache: lane x looks record x up
         bool gone = false;
         {
@@ -556,46 +593,43 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             gone = blk < 0 || blk >= p.num_blocks;
           }
         }
-        const uint32_t holes = __ballot_sync(0xffffffffu, gone);
-        const bool edge = __any_sync(0xffffffffu, t0 + kTileTokens - 1 > lim) || holes;
+        const uint32_t holes = __ballot_sync(0xffffffffu, gone) >> (4 * half);
+        const bool edge = __any_sync(0xffffffffu, t0 + 63 > lim) || (holes & 15u);
+        // (a wait that gave up ends no loop here: the barriers below want every warp)
         if (ok) ok = warp_wait(smem_addr(&s_sfull[slot]), count & 1);
-        if (!ok) break;
         tc_fence_after();
-        // the maximum first, then the weights: 128 columns at once would not fit the registers
+        const uint32_t cols = s_cols + half * 64;
         if (edge) {
           // what a row does not see, written back as -infinity: rare, and apart
           // from the loops below, whose code has to stay in the instruction cache
 #pragma unroll 1
-          for (int c = 0; c < kTileTokens / 16; ++c) {
+          for (int c = 0; c < 4; ++c) {
             uint32_t s[16];
-            tmem_ld16(s_cols + 16 * c, s);
+            tmem_ld16(cols + 16 * c, s);
             tmem_ld_wait();
             tmem_loaded(s);
             const int seen = holes >> c & 1u ? 0 : lim + 1 - t0 - 16 * c;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               if (i >= seen) s[i] = __float_as_uint(-INFINITY);
-            tmem_st16(s_cols + 16 * c, s);
+            tmem_st16(cols + 16 * c, s);
           }
           tmem_st_wait();
         }
+        // the maximum first, found by the load itself, then the weights
         float mx = kNoScore;
 #pragma unroll 1
-        for (int c = 0; c < kTileTokens / 32; c += 2) {
-          uint32_t s[2][32];
-          tmem_ld32(s_cols + 32 * c, s[0]);
-          tmem_ld32(s_cols + 32 * c + 32, s[1]);
+        for (int c = 0; c < 2; ++c) {
+          uint32_t s[32], big;
+          tmem_ld32_max(cols + 32 * c, s, big);
           tmem_ld_wait();
-          tmem_loaded(s[0]);
-          tmem_loaded(s[1]);
-          float x[4] = {mx, mx, mx, mx};
-#pragma unroll
-          for (int i = 0; i < 32; i += 4)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              x[k] = fmaxf(x[k], fmaxf(__uint_as_float(s[0][i + k]), __uint_as_float(s[1][i + k])));
-          mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+          tmem_loaded(s);
+          asm volatile("" : "+r"(big));
+          mx = fmaxf(mx, __uint_as_float(big));
         }
+        s_mx[count & 1][slot][half][row] = mx;
+        rows_sync(slot, quarter);
+        mx = fmaxf(mx, s_mx[count & 1][slot][half ^ 1][row]);
         if (__any_sync(0xffffffffu, mx > m + room)) {
           const float mn = fmaxf(m, mx);
           const float alpha = ex2_fast((m - mn) * cs);
@@ -605,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             if (ok) ok = warp_wait(smem_addr(&s_pvdone[slot]), (count - 1) & 1);
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
+            for (int c = 0; c < D / 32; ++c) {
               uint32_t o[16];
               tmem_ld16(o_cols + 16 * c, o);
               tmem_ld_wait();
@@ -617,33 +651,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             tmem_st_wait();
           }
         }
+        // the tokens' weights, over this half's scores as they are read
         const float bias = fmaf(-m, cs, 15.f - kHeadroom);
-        float sum0 = 0.f, sum1 = 0.f;
+        const uint64_t cs2 = pack2(cs, cs), bias2 = pack2(bias, bias);
+        uint64_t sum = 0;
         auto weights = [&](const uint32_t (&s)[16], uint32_t* w) {
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const float a = ex2_fast(fmaf(__uint_as_float(s[i]), cs, bias));
-            const float b = ex2_fast(fmaf(__uint_as_float(s[i + 1]), cs, bias));
-            sum0 += a;
-            sum1 += b;
+            float a, b;
+            unpack2(fma2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), cs2, bias2), a, b);
+            a = ex2_fast(a);
+            b = ex2_fast(b);
+            sum = add2(sum, pack2(a, b));
             w[i / 2] = as_u32(__floats2half2_rn(a, b));
           }
         };
-        uint32_t sa[16], sb[16], w[16];  // the next columns are on their way while these are worked on
-        tmem_ld16(s_cols, sa);
+        uint32_t sx[16], sy[16], w[16];  // the next columns are on their way while these are worked on
+        tmem_ld16(cols, sx);
 #pragma unroll 1
-        for (int c = 0; c < kTileTokens / 32; ++c) {
+        for (int c = 0; c < 2; ++c) {
           tmem_ld_wait();
-          tmem_loaded(sa);
-          tmem_ld16(s_cols + 32 * c + 16, sb);
-          weights(sa, w);
+          tmem_loaded(sx);
+          tmem_ld16(cols + 32 * c + 16, sy);
+          weights(sx, w);
           tmem_ld_wait();
-          tmem_loaded(sb);
-          if (c + 1 < kTileTokens / 32) tmem_ld16(s_cols + 32 * c + 32, sa);
-          weights(sb, w + 8);
-          tmem_st16(s_cols + 16 * c, w);  // over scores that have been read
+          tmem_loaded(sy);
+          if (c == 0) tmem_ld16(cols + 32, sx);
+          weights(sy, w + 8);
+          tmem_st16(cols + 16 * c, w);
         }
-        l += sum0 + sum1;
+        {
+          float a, b;
+          unpack2(sum, a, b);
+          l += a + b;
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -654,87 +695,73 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
 
       // ---- the unit's end
       if (mine > 0 && ok) ok = warp_wait(smem_addr(&s_pvdone[slot]), (count - 1) & 1);
-      tc_fence_after();
       const bool whole = at.tile == 0 && nt == at.tiles;
       const long long unit = r0 + done - at.tile;
       const bool begun = unit / share == blockIdx.x;
+      s_l[slot][half][row] = l;
+      if (half == 0 && slot == 1) s_m[row] = m * cs;
+      tc_fence_before();
+      ok = softmax_all(ok);
+      tc_fence_after();
       float a0 = 1.f, a1 = 0.f;  // this slot's factor, the other's
+      l = s_l[slot][0][row] + s_l[slot][1][row];
       float ms = l > 0.f ? m * cs : -INFINITY;
-      if (!pair) {
-        if (slot == 1) {
-          s_ml[0][row] = ms;
-          s_ml[1][row] = l;
-          tc_fence_before();
-        }
-        softmax_sync();
-        tc_fence_after();
-        if (slot == 0) {
-          const float m1 = s_ml[0][row], l1 = s_ml[1][row];
-          const float mn = fmaxf(ms, m1);
-          a0 = l > 0.f ? ex2_fast(ms - mn) : 0.f;
-          a1 = l1 > 0.f ? ex2_fast(m1 - mn) : 0.f;
-          ms = mn;
-          l = a0 * l + a1 * l1;
-        }
+      if (!pair && slot == 0) {
+        const float l1 = s_l[1][0][row] + s_l[1][1][row], m1 = l1 > 0.f ? s_m[row] : -INFINITY;
+        const float mn = fmaxf(ms, m1);
+        a0 = l > 0.f ? ex2_fast(ms - mn) : 0.f;
+        a1 = l1 > 0.f ? ex2_fast(m1 - mn) : 0.f;
+        ms = mn;
+        l = a0 * l + a1 * l1;
       }
       if (ok && (pair || slot == 0)) {
         const float inv = l > 0.f ? vscale / l : 0.f;
-        const size_t to = real ? out_at(p, rq.first, at.kvh, my) : 0;
+        const size_t to = real ? out_at(p, rq.first, at.kvh, my) + half * (D / 2) : 0;
         float* part = p.partial + (2 * static_cast<size_t>(blockIdx.x) + begun) * C::kPart;
         const int prow = my - row0;
         const bool both = !pair && nt > 1;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(o_cols + 32 * c, o);
+          uint32_t o[16];
+          float y[16];
+          tmem_ld16(o_cols + 16 * c, o);
           tmem_ld_wait();
           tmem_loaded(o);
-          float y[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(o[i]) * a0;
+          for (int i = 0; i < 16; ++i) y[i] = l > 0.f ? __uint_as_float(o[i]) * a0 : 0.f;
           if (both) {
-            tmem_ld32(o_cols + D + 32 * c, o);
+            tmem_ld16(o_cols + D + 16 * c, o);
             tmem_ld_wait();
             tmem_loaded(o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = fmaf(__uint_as_float(o[i]), a1, y[i]);
+            for (int i = 0; i < 16; ++i) y[i] = l > 0.f ? fmaf(__uint_as_float(o[i]), a1, y[i]) : 0.f;
           }
-          if (!(l > 0.f)) {  // nothing seen: the accumulators are not meant
+          if (!whole) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = 0.f;
-          }
-          if (whole) {
-            if (real) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                float z[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  z[kv4_low<KIND>(i)] = y[8 * q + 2 * i] * inv;
-                  z[kv4_high<KIND>(i)] = y[8 * q + 2 * i + 1] * inv;
-                }
-                store8(p, to + 32 * c + 8 * q, z);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              __stcg(reinterpret_cast<float4*>(part) + (8 * c + q) * kUnitRows + prow,
+            for (int q = 0; q < 4; ++q)
+              __stcg(reinterpret_cast<float4*>(part) + (half * (D / 8) + 4 * c + q) * kUnitRows + prow,
                      make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]));
+          } else if (real) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              float z[8];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                z[kv4_low<KIND>(i)] = y[8 * q + 2 * i] * inv;
+                z[kv4_high<KIND>(i)] = y[8 * q + 2 * i + 1] * inv;
+              }
+              store8(p, to + 16 * c + 8 * q, z);
+            }
           }
         }
-        if (!whole) {
+        if (!whole && half == 0) {
           __stcg(part + kUnitRows * D + prow, ms);
           __stcg(part + kUnitRows * (D + 1) + prow, l);
         }
       }
       tc_fence_before();
-      ok = softmax_all(ok);  // slot 1's accumulators have been read; all go on, or none
-      if (!whole) {
-        const Open u = {rq.first, rq.rows, row0, at.kvh, unit, at.tiles};
-        if (begun) open1 = u;
-        else open0 = u;
-      }
+      ok = softmax_all(ok);  // the accumulators and states have been read; all go on, or none
+      if (!whole && tid == 0) s_open[begun] = {rq.first, rq.rows, row0, at.kvh, unit, at.tiles};
       if (!ok) break;
       done += nt;
       at.tile += nt;
@@ -743,15 +770,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   }
 
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-  if (tid >= kSoftmaxThreads || (open0.unit < 0 && open1.unit < 0)) return;
+  if (tid >= kSoftmaxThreads || (s_open[0].unit < 0 && s_open[1].unit < 0)) return;
 
   // ---- join the CTAs' parts of a unit, in the last CTA to arrive
   if (tid < 2) {
-    const Open u = tid ? open1 : open0;
+    const Open u = s_open[tid];
     s_last[tid] = 0;
     if (u.unit >= 0) {
       const long long c0 = u.unit / share, c1 = (u.unit + u.tiles - 1) / share;
@@ -767,8 +794,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     if (!s_last[which]) continue;
-    const Open u = which ? open1 : open0;
-    const int my = u.row0 + tid;
+    const Open u = s_open[which];
+    const int row = tid % kUnitRows, my = u.row0 + row;
     if (my >= u.rows) continue;
     const long long c0 = u.unit / share;
     const int parts = static_cast<int>((u.unit + u.tiles - 1) / share - c0) + 1;
@@ -777,25 +804,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     float m = -INFINITY, l = 0.f;
 #pragma unroll 4
     for (int k = 0; k < parts; ++k)
-      m = fmaxf(m, __ldcg(src + (k ? 2 * k : 1) * static_cast<size_t>(C::kPart) + kUnitRows * D + tid));
+      m = fmaxf(m, __ldcg(src + (k ? 2 * k : 1) * static_cast<size_t>(C::kPart) + kUnitRows * D + row));
 #pragma unroll 4
     for (int k = 0; k < parts; ++k) {
-      const float* s = src + (k ? 2 * k : 1) * static_cast<size_t>(C::kPart) + kUnitRows * D + tid;
+      const float* s = src + (k ? 2 * k : 1) * static_cast<size_t>(C::kPart) + kUnitRows * D + row;
       const float lk = __ldcg(s + kUnitRows);
       if (lk > 0.f) l = fmaf(ex2_fast(__ldcg(s) - m), lk, l);
     }
     const float inv = l > 0.f ? __ldg(p.v_scale) / l : 0.f;
     const size_t to = out_at(p, u.first, u.kvh, my);
 #pragma unroll 1
-    for (int q = 0; q < D / 8; ++q) {
+    for (int q = tid / kUnitRows; q < D / 8; q += kSoftmaxThreads / kUnitRows) {
       float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 2
       for (int k = 0; k < parts; ++k) {
         const float* s = src + (k ? 2 * k : 1) * static_cast<size_t>(C::kPart);
-        const float mk = __ldcg(s + kUnitRows * D + tid);
+        const float mk = __ldcg(s + kUnitRows * D + row);
         const float a = mk == -INFINITY ? 0.f : ex2_fast(mk - m) * inv;
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(s) + (2 * q) * kUnitRows + tid);
-        const float4 w = __ldcg(reinterpret_cast<const float4*>(s) + (2 * q + 1) * kUnitRows + tid);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(s) + (2 * q) * kUnitRows + row);
+        const float4 w = __ldcg(reinterpret_cast<const float4*>(s) + (2 * q + 1) * kUnitRows + row);
         y[0] = fmaf(a, v.x, y[0]);
         y[1] = fmaf(a, v.y, y[1]);
         y[2] = fmaf(a, v.z, y[2]);
