@@ -151,18 +151,6 @@ __device__ __forceinline__ void rows_sync(int slot, int quarter) {
   asm volatile("bar.sync %0, 64;" ::"r"(4 + 4 * slot + quarter) : "memory");
 }
 
-// All softmax warps, and whether `ok` holds in all of them.
-__device__ __forceinline__ bool softmax_all(bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(ok)), "n"(kSoftmaxThreads)
-      : "memory");
-  return r != 0u;
-}
-
 // Whether a warp's wait ended well: the same answer in every lane, since what
 // follows is done by the whole warp.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
@@ -227,6 +215,12 @@ struct Open {
   int tiles;
 };
 
+// A unit whose results are still to be written.
+struct Ended {
+  int first, rows, row0, kvh, tiles;
+  bool whole, begun, pair, both;
+};
+
 template <int KIND, int D>
 __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnParams p) {
   using C = Big<D>;
@@ -242,9 +236,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   __shared__ Open s_open[2];  // the unit begun in front of this CTA, the one begun here
   __shared__ float s_cs[2][kTileRows];         // scale of each row's scores
   __shared__ float s_mx[2][2][2][kTileRows];   // largest score: tile's parity, slot, half of the tokens
-  // at a unit's end, when nobody reads the last scores any more: sums by slot and half, and slot 1's maximum
-  float (&s_l)[2][2][kTileRows] = s_mx[0];
-  float (&s_m)[kTileRows] = s_mx[1][0][0];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
   if (tid == 0) {
@@ -467,6 +458,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       for (int j = 0; j < ahead && j < nt && ok; ++j) {
         wait_k(done + j);
         if (!ok) break;
+        for (int slot = pair ? 0 : j; slot < (pair ? 2 : j + 1) && ok; ++slot) {
+          const uint32_t c = slot ? pcount[1] : pcount[0];
+          if (c > 0) ok = warp_wait(smem_addr(&s_pvdone[slot]), (c - 1) & 1);
+        }
+        if (!ok) break;
 #pragma unroll 1
         for (int slot = pair ? 0 : j; slot < (pair ? 2 : j + 1); ++slot) scores(done + j, slot, pair ? slot : 0);
         mma_commit_by(leader, smem_addr(&s_kempty[(done + j) % kStages]));
@@ -511,9 +507,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     const float vscale = __ldg(p.v_scale), to_log2 = p.sm_scale * __ldg(p.k_scale) * kLog2e;
     uint32_t count = 0u;  // tiles of this slot
     int done = 0;
+    // the unit before, whose results are written when the next one's query is on its way
+    Ended old;
+    old.tiles = 0;
+    float m = kNoScore, l = 0.f, cs = 0.f;
+    int mine = 0;  // tiles of this slot in the unit
 #pragma unroll 1
-    while (done < run_tiles) {
-      const int nt = min(at.tiles - at.tile, run_tiles - done);
+    while (true) {
+      const bool more = done < run_tiles;
+      const int nt = more ? min(at.tiles - at.tile, run_tiles - done) : 0;
       const Request rq = at.rq;
       const int row0 = at.rt * kUnitRows;
       const bool pair = rq.rows - row0 > kTileRows;
@@ -521,9 +523,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       const int my = top + row;
       const bool real = my < rq.rows;
 
+      if (old.tiles > 0 && !old.pair) softmax_sync();  // both slots' last scores are there: the query may go
       // ---- the warp's 16 query rows, a 16-byte piece for each lane, scaled by
       // 2^e so that a row's largest element lies in [2^14, 2^15)
-      if (pair || slot == 0) {
+      if (more && (pair || slot == 0)) {
         constexpr int kPerRow = D / 8, kAtOnce = 32 / kPerRow;  // pieces of a row, rows of one load
         constexpr int kBatch = 4;                               // loads in flight
         const int c = lane % kPerRow, wrow = 16 * (warp % 8) + lane / kPerRow;
@@ -570,14 +573,89 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         fence_proxy_async_shared();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&s_qfull));
+      if (more && lane == 0) mbar_arrive(smem_addr(&s_qfull));
+
+      // ---- the results of the unit before
+      if (old.tiles > 0) {
+        if (mine > 0 && ok) ok = warp_wait(smem_addr(&s_pvdone[slot]), (count - 1) & 1);
+        // sums by slot and half, and slot 1's maximum, where nobody reads scores any
+        // more (with pairs the buffer that the next tile does not write to)
+        float (&s_l)[2][2][kTileRows] = s_mx[old.pair ? (count + 1) & 1 : 0];
+        float (&s_m)[kTileRows] = s_mx[1][0][0];
+        s_l[slot][half][row] = l;
+        if (!old.pair && half == 0 && slot == 1) s_m[row] = m * cs;
+        tc_fence_before();
+        if (old.pair) rows_sync(slot, quarter);
+        else softmax_sync();
+        tc_fence_after();
+        float a0 = 1.f, a1 = 0.f;  // this slot's factor, the other's
+        l = s_l[slot][0][row] + s_l[slot][1][row];
+        float ms = l > 0.f ? m * cs : -INFINITY;
+        if (!old.pair && slot == 0) {
+          const float l1 = s_l[1][0][row] + s_l[1][1][row], m1 = l1 > 0.f ? s_m[row] : -INFINITY;
+          const float mn = fmaxf(ms, m1);
+          a0 = l > 0.f ? ex2_fast(ms - mn) : 0.f;
+          a1 = l1 > 0.f ? ex2_fast(m1 - mn) : 0.f;
+          ms = mn;
+          l = a0 * l + a1 * l1;
+        }
+        if (old.pair || slot == 0) {
+          const float inv = l > 0.f ? vscale / l : 0.f;
+          const int prow = row + (old.pair ? slot * kTileRows : 0), r = old.row0 + prow;
+          const bool real_row = r < old.rows;
+          const size_t to = real_row ? out_at(p, old.first, old.kvh, r) + half * (D / 2) : 0;
+          float* part = p.partial + (2 * static_cast<size_t>(blockIdx.x) + old.begun) * C::kPart;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[16];
+            float y[16];
+            tmem_ld16(o_cols + 16 * c, o);
+            tmem_ld_wait();
+            tmem_loaded(o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = l > 0.f ? __uint_as_float(o[i]) * a0 : 0.f;
+            if (old.both) {
+              tmem_ld16(o_cols + D + 16 * c, o);
+              tmem_ld_wait();
+              tmem_loaded(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) y[i] = l > 0.f ? fmaf(__uint_as_float(o[i]), a1, y[i]) : 0.f;
+            }
+            if (!old.whole) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                __stcg(reinterpret_cast<float4*>(part) + (half * (D / 8) + 4 * c + q) * kUnitRows + prow,
+                       make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]));
+            } else if (real_row) {
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                float z[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  z[kv4_low<KIND>(i)] = y[8 * q + 2 * i] * inv;
+                  z[kv4_high<KIND>(i)] = y[8 * q + 2 * i + 1] * inv;
+                }
+                store8(p, to + 16 * c + 8 * q, z);
+              }
+            }
+          }
+          if (!old.whole && half == 0) {
+            __stcg(part + kUnitRows * D + prow, ms);
+            __stcg(part + kUnitRows * (D + 1) + prow, l);
+          }
+        }
+        tc_fence_before();
+        if (!old.pair) softmax_sync();  // slot 1's accumulators and the states have been read
+      }
+      if (!more) break;
       if (pair) slot_sync(slot);
       else softmax_sync();
-      const float cs = s_cs[pair ? slot : 0][row];
+      cs = s_cs[pair ? slot : 0][row];
       const int lim = real ? rq.len - rq.n + my / p.share : rq.len - 1;  // the last token seen
       const float room = fminf(kHeadroom / cs, 1e38f);
-      float m = kNoScore, l = 0.f;
-      int mine = 0;  // tiles of this slot in the unit
+      m = kNoScore;
+      l = 0.f;
+      mine = 0;
 
       // ---- its tiles
 #pragma unroll 1
@@ -693,76 +771,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         ++mine;
       }
 
-      // ---- the unit's end
-      if (mine > 0 && ok) ok = warp_wait(smem_addr(&s_pvdone[slot]), (count - 1) & 1);
-      const bool whole = at.tile == 0 && nt == at.tiles;
+      // ---- its end
       const long long unit = r0 + done - at.tile;
-      const bool begun = unit / share == blockIdx.x;
-      s_l[slot][half][row] = l;
-      if (half == 0 && slot == 1) s_m[row] = m * cs;
-      tc_fence_before();
-      ok = softmax_all(ok);
-      tc_fence_after();
-      float a0 = 1.f, a1 = 0.f;  // this slot's factor, the other's
-      l = s_l[slot][0][row] + s_l[slot][1][row];
-      float ms = l > 0.f ? m * cs : -INFINITY;
-      if (!pair && slot == 0) {
-        const float l1 = s_l[1][0][row] + s_l[1][1][row], m1 = l1 > 0.f ? s_m[row] : -INFINITY;
-        const float mn = fmaxf(ms, m1);
-        a0 = l > 0.f ? ex2_fast(ms - mn) : 0.f;
-        a1 = l1 > 0.f ? ex2_fast(m1 - mn) : 0.f;
-        ms = mn;
-        l = a0 * l + a1 * l1;
-      }
-      if (ok && (pair || slot == 0)) {
-        const float inv = l > 0.f ? vscale / l : 0.f;
-        const size_t to = real ? out_at(p, rq.first, at.kvh, my) + half * (D / 2) : 0;
-        float* part = p.partial + (2 * static_cast<size_t>(blockIdx.x) + begun) * C::kPart;
-        const int prow = my - row0;
-        const bool both = !pair && nt > 1;
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[16];
-          float y[16];
-          tmem_ld16(o_cols + 16 * c, o);
-          tmem_ld_wait();
-          tmem_loaded(o);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) y[i] = l > 0.f ? __uint_as_float(o[i]) * a0 : 0.f;
-          if (both) {
-            tmem_ld16(o_cols + D + 16 * c, o);
-            tmem_ld_wait();
-            tmem_loaded(o);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = l > 0.f ? fmaf(__uint_as_float(o[i]), a1, y[i]) : 0.f;
-          }
-          if (!whole) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              __stcg(reinterpret_cast<float4*>(part) + (half * (D / 8) + 4 * c + q) * kUnitRows + prow,
-                     make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]));
-          } else if (real) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              float z[8];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                z[kv4_low<KIND>(i)] = y[8 * q + 2 * i] * inv;
-                z[kv4_high<KIND>(i)] = y[8 * q + 2 * i + 1] * inv;
-              }
-              store8(p, to + 16 * c + 8 * q, z);
-            }
-          }
-        }
-        if (!whole && half == 0) {
-          __stcg(part + kUnitRows * D + prow, ms);
-          __stcg(part + kUnitRows * (D + 1) + prow, l);
-        }
-      }
-      tc_fence_before();
-      ok = softmax_all(ok);  // the accumulators and states have been read; all go on, or none
-      if (!whole && tid == 0) s_open[begun] = {rq.first, rq.rows, row0, at.kvh, unit, at.tiles};
-      if (!ok) break;
+      old.whole = at.tile == 0 && nt == at.tiles;
+      old.begun = unit / share == blockIdx.x;
+      old.pair = pair;
+      old.both = !pair && nt > 1;
+      old.first = rq.first;
+      old.rows = rq.rows;
+      old.row0 = row0;
+      old.kvh = at.kvh;
+      old.tiles = nt;
+      if (!old.whole && tid == 0) s_open[old.begun] = {rq.first, rq.rows, row0, at.kvh, unit, at.tiles};
       done += nt;
       at.tile += nt;
       if (done < run_tiles) at.next_unit(p);
