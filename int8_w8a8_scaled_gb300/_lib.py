@@ -87,6 +87,8 @@ def library_path() -> str:
 def load(build_if_needed: bool = True):
     """Load (building first if needed) and return the ctypes library."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -17,6 +17,7 @@ semantics" section of "Enable scaled FP8 (e4m3fn) KV cache on ROCm".
 from __future__ import annotations
 
 import ctypes
+import functools
 import threading
 
 import torch
@@ -73,12 +74,18 @@ def _cuda(*ts):
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+    return t.data_ptr() if t is not None else None
+
+
+def _raw_stream(device_index: int) -> int:
+    """The device's current stream, without making a Stream object of it."""
+    return torch._C._cuda_getCurrentRawStream(device_index)
 
 
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 class Workspace:
@@ -109,7 +116,10 @@ _default_ws: dict = {}
 def _default_workspace(device: torch.device, nbytes: int, kind: str) -> Workspace:
     """Per (device, stream, kind) scratch; the matmul's buffer is never shared
     with the quantiser (whose absmax word would land on a counter)."""
-    key = (kind, device.index, torch.cuda.current_stream(device).cuda_stream)
+    key = (kind, device.index, _raw_stream(device.index))
+    ws = _default_ws.get(key)
+    if ws is not None and ws.buf.numel() >= nbytes:
+        return ws
     with _ws_lock:
         ws = _default_ws.get(key)
         if ws is None:
@@ -409,7 +419,7 @@ def _kv4_kind(kind: str) -> int:
 
 
 def _ints(name: str, t: torch.Tensor, n: int | None, dtype=torch.int32) -> None:
-    if t.dtype != dtype or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.numel() != n):
+    if t.dtype is not dtype or t.ndim != 1 or not t.is_contiguous() or (n is not None and t.numel() != n):
         size = "" if n is None else f" of {n} entries"
         raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} vector{size}")
 
@@ -517,6 +527,12 @@ def kv4_attention_workspace_size(batch: int, max_query_len: int, num_q_heads: in
     return int(_lib.load().w8a8_kv4_attention_workspace_size(batch, max_query_len, num_q_heads, num_kv_heads, head_dim))
 
 
+@functools.lru_cache(maxsize=4096)
+def _kv4_attention_need(device_index: int, *sizes: int) -> int:
+    """The same, looked up once for a device and sizes (it depends on nothing else)."""
+    return kv4_attention_workspace_size(*sizes)
+
+
 def kv4_attention(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor,
                   k_scale: torch.Tensor, v_scale: torch.Tensor, out: torch.Tensor,
                   query_start: torch.Tensor | None = None, max_query_len: int = 1, sm_scale: float | None = None,
@@ -548,7 +564,7 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, 
     kd = _kv4_kind(kind)
     if tokens == 0:
         return
-    need = lib.w8a8_kv4_attention_workspace_size(batch, max_query_len, hq, hkv, d)
+    need = _kv4_attention_need(q.device.index, batch, max_query_len, hq, hkv, d)
     if isinstance(workspace, Workspace):
         wbuf = workspace.ensure(need).buf
     elif workspace is None:
