@@ -240,6 +240,7 @@ struct VerifyArgs {
   int* out_tokens;          // [batch, max_drafts + 1]
   int max_drafts;
   int* num_accepted;        // [batch]
+  int cluster;              // CTAs to a row (set by the launcher)
 };
 cudaError_t launch_verify(const VerifyArgs& a, int num_sms, cudaStream_t stream);
 
