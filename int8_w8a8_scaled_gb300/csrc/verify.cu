@@ -94,26 +94,32 @@ struct Pair {
   }
 };
 
-// Sum of the tokens [v0, v1) over a warp, in every lane.
-template <int DT, bool kVec>
+// Sum of the tokens [v0, v1) over a warp, in every lane.  kQ: less a second
+// row.
+template <int DT, bool kVec, bool kQ>
 __device__ __forceinline__ double warp_sum(const Weights& w, int v0, int v1, int lane) {
   Pair sum;
   if (kVec) {
     int v = v0 + 4 * lane;
-#pragma unroll 4
+#pragma unroll 2
     for (; v + 4 <= v1; v += kStride) {
       float p[4], q[4] = {0.f, 0.f, 0.f, 0.f};
       prob4<DT>(w.p, w.p_at + v, p);
-      if (w.q) prob4<DT>(w.q, w.q_at + v, q);
+      if (kQ) prob4<DT>(w.q, w.q_at + v, q);
+      if (!kQ && static_cast<unsigned>(w.hole - v) < 4u) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sum.add_difference(v + k == w.hole ? 0.f : p[k], q[k]);
+        for (int k = 0; k < 4; ++k)
+          if (v + k == w.hole) p[k] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum.add_difference(p[k], q[k]);
     }
     for (int k = v; k < min(v1, v + 4); ++k)  // the row's end
-      sum.add_difference(k == w.hole ? 0.f : prob<DT>(w.p, w.p_at + k), w.q ? prob<DT>(w.q, w.q_at + k) : 0.f);
+      sum.add_difference(k == w.hole ? 0.f : prob<DT>(w.p, w.p_at + k), kQ ? prob<DT>(w.q, w.q_at + k) : 0.f);
   } else {
 #pragma unroll 4
     for (int v = v0 + lane; v < v1; v += 32)
-      sum.add_difference(v == w.hole ? 0.f : prob<DT>(w.p, w.p_at + v), w.q ? prob<DT>(w.q, w.q_at + v) : 0.f);
+      sum.add_difference(v == w.hole ? 0.f : prob<DT>(w.p, w.p_at + v), kQ ? prob<DT>(w.q, w.q_at + v) : 0.f);
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1)
@@ -123,9 +129,10 @@ __device__ __forceinline__ double warp_sum(const Weights& w, int v0, int v1, int
 }
 
 template <int DT, bool kVec>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a) {
   __shared__ double s_sum[kWarps];
-  __shared__ int s_kept;
+  __shared__ double s_before, s_goal;
+  __shared__ int s_kept, s_owner;  // s_owner: the piece that holds the draw
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int rank = static_cast<int>(cluster_ctarank()), b = static_cast<int>(cluster_id_x());
   const int first = min(max(__ldg(a.draft_start + b), 0), a.rows);
@@ -171,73 +178,87 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
   const int per = ((a.vocab + pieces - 1) / pieces + kStride - 1) / kStride * kStride;
   const int v0 = static_cast<int>(min(static_cast<long long>(a.vocab), static_cast<long long>(mine) * per));
   const int v1 = min(a.vocab, v0 + per);
-  int owner;                // the piece that holds the draw
-  double before, goal;
+  constexpr int kLanePieces = kMaxCluster * kWarps / 32;
   for (int round = 0;; ++round) {
-    const double sum = warp_sum<DT, kVec>(w, v0, v1, lane);
+    const double sum = w.q ? warp_sum<DT, kVec, true>(w, v0, v1, lane) : warp_sum<DT, kVec, false>(w, v0, v1, lane);
     if (lane == 0) s_sum[warp] = sum;
     cluster_sync();
-    // every warp looks at all pieces: lane l at pieces 4 l .. 4 l + 3
-    double piece[kMaxCluster * kWarps / 32], run = 0.0;
+    // one warp of each CTA looks at all pieces: lane l at pieces 4 l .. 4 l + 3
+    if (warp == 0) {
+      double piece[kLanePieces], run = 0.0;
 #pragma unroll
-    for (int k = 0; k < kMaxCluster * kWarps / 32; ++k) {
-      const int i = lane * (kMaxCluster * kWarps / 32) + k;
-      piece[k] = 0.0;
-      if (i < pieces) {
-        const uint32_t at = mapa_shared(smem_addr(&s_sum[i % kWarps]), i / kWarps);
-        const uint32_t lo = ld_dsmem_u32(at), hi = ld_dsmem_u32(at + 4);
-        piece[k] = __hiloint2double(static_cast<int>(hi), static_cast<int>(lo));
-      }
-      run += piece[k];
-    }
-    double upto = run;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const double o = __shfl_up_sync(0xffffffffu, upto, off);
-      if (lane >= off) upto += o;
-    }
-    const double total = __shfl_sync(0xffffffffu, upto, 31);
-    goal = u * total;
-    // the first piece that passes the goal; with none (a rounding) the last of any weight
-    double c = upto - run, c_first = 0.0, c_last = 0.0;
-    int i_first = 1 << 20, i_last = -1;
-#pragma unroll
-    for (int k = 0; k < kMaxCluster * kWarps / 32; ++k) {
-      const int i = lane * (kMaxCluster * kWarps / 32) + k;
-      if (piece[k] > 0.0) {
-        if (c + piece[k] > goal && i < i_first) {
-          i_first = i;
-          c_first = c;
+      for (int k = 0; k < kLanePieces; ++k) {
+        const int i = lane * kLanePieces + k;
+        piece[k] = 0.0;
+        if (i < pieces) {
+          const uint32_t at = mapa_shared(smem_addr(&s_sum[i % kWarps]), i / kWarps);
+          const uint32_t lo = ld_dsmem_u32(at), hi = ld_dsmem_u32(at + 4);
+          piece[k] = __hiloint2double(static_cast<int>(hi), static_cast<int>(lo));
         }
-        i_last = i;
-        c_last = c;
+        run += piece[k];
       }
-      c += piece[k];
+      double upto = run;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const double o = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += o;
+      }
+      const double goal = u * __shfl_sync(0xffffffffu, upto, 31);
+      // the first piece that passes the goal; with none (a rounding) the last of any weight
+      double c = upto - run, c_first = 0.0, c_last = 0.0;
+      int i_first = 1 << 20, i_last = -1;
+#pragma unroll
+      for (int k = 0; k < kLanePieces; ++k) {
+        const int i = lane * kLanePieces + k;
+        if (piece[k] > 0.0) {
+          if (c + piece[k] > goal && i < i_first) {
+            i_first = i;
+            c_first = c;
+          }
+          i_last = i;
+          c_last = c;
+        }
+        c += piece[k];
+      }
+      const int lowest = __reduce_min_sync(0xffffffffu, i_first), highest = __reduce_max_sync(0xffffffffu, i_last);
+      const int owner = lowest < (1 << 20) ? lowest : highest;
+      if (lane == max(owner, 0) / kLanePieces) {
+        s_owner = owner;
+        s_before = lowest < (1 << 20) ? c_first : c_last;
+        s_goal = goal;
+      }
     }
-    const int lowest = __reduce_min_sync(0xffffffffu, i_first), highest = __reduce_max_sync(0xffffffffu, i_last);
-    owner = lowest < (1 << 20) ? lowest : highest;
-    const int from = max(owner, 0) / (kMaxCluster * kWarps / 32);
-    before = __shfl_sync(0xffffffffu, lowest < (1 << 20) ? c_first : c_last, from);
     cluster_sync();  // the sums have been read: they may change, and CTAs may end
-    if (owner >= 0 || round == 1) break;
+    if (s_owner >= 0 || round == 1) break;
     w.q = nullptr;
     w.hole = -1;
   }
+  const int owner = s_owner;
   if (owner < 0) {  // no token has any probability
     if (rank == 0 && tid == 0) out[kept] = -1;
     return;
   }
   if (owner != mine) return;
-  // ---- the walk through the piece
-  double c = before;
-  int last = -1;
+  // ---- the walk through the piece: over 128 tokens at a time, then within them
+  const double goal = s_goal;
+  double c = s_before;
+  int best = -1;
   for (int v = v0; v < v1; v += kStride) {
+    const int end = min(v1, v + kStride);
+    const double sum = w.q ? warp_sum<DT, kVec, true>(w, v, end, lane) : warp_sum<DT, kVec, false>(w, v, end, lane);
+    const bool late = end == v1;  // with nothing found (a rounding): the last token of any weight
+    if (!(sum > 0.0) || (!(c + sum > goal) && !late)) {
+      if (sum > 0.0) best = -2 - v;  // it may still be in here
+      c += sum;
+      if (!late || best == -1) continue;
+    }
+    const int from = sum > 0.0 ? v : -2 - best;
     double x[4], run = 0.0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int t = v + 4 * lane + k;
+      const int t = from + 4 * lane + k;
       x[k] = 0.0;
-      if (t < v1 && t != w.hole) {
+      if (t < min(v1, from + kStride) && t != w.hole) {
         const float p = prob<DT>(w.p, w.p_at + t);
         x[k] = w.q ? fmax(static_cast<double>(p) - static_cast<double>(prob<DT>(w.q, w.q_at + t)), 0.0) : p;
       }
@@ -254,21 +275,17 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       at += x[k];
-      const int t = v + 4 * lane + k;
+      const int t = from + 4 * lane + k;
       if (x[k] > 0.0) {
         if (at > goal && found == (1 << 30)) found = t;
         some = t;
       }
     }
     found = __reduce_min_sync(0xffffffffu, found);
-    last = max(last, __reduce_max_sync(0xffffffffu, some));
-    if (found < (1 << 30)) {
-      last = found;
-      break;
-    }
-    c += __shfl_sync(0xffffffffu, upto, 31);
+    best = found < (1 << 30) && from == v ? found : __reduce_max_sync(0xffffffffu, some);
+    break;
   }
-  if (lane == 0) out[kept] = last;
+  if (lane == 0) out[kept] = best;
 }
 
 template <int DT, bool kVec>
