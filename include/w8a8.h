@@ -422,8 +422,8 @@ W8A8_API size_t w8a8_kv4_cache_bytes(int64_t num_blocks, int64_t num_kv_heads, i
  *            twice in a call.
  *   k_scale, v_scale  fp32 [1], positive and finite.
  * Alignment: k and v need 2 bytes; 16-byte aligned bases and strides take
- * the vectorised path.  Limits: 1 <= tokens, num_kv_heads, num_blocks;
- * tokens * num_kv_heads * head_dim < 2^40. */
+ * the vectorised path.  Limits: 1 <= tokens < 2^31, num_kv_heads and
+ * num_blocks >= 1, tokens * num_kv_heads * head_dim < 2^40. */
 W8A8_API w8a8_status w8a8_kv4_cache_write(const void* k, const void* v, int dtype, int64_t tokens,
                                           int64_t num_kv_heads, int64_t head_dim, int64_t k_token_stride,
                                           int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,

@@ -981,7 +981,7 @@ w8a8_status kv4_cache_call(bool write, const void* k, const void* v, int dtype, 
   w8a8_status st = kv4_sizes(num_blocks, num_kv_heads, block_size, head_dim, kind);
   if (st != W8A8_OK) return st;
   if (tokens < 1) return fail(W8A8_ERR_INVALID_ARG, "tokens must be >= 1");
-  if (tokens >= (1LL << 40) / (num_kv_heads * head_dim)) return fail(W8A8_ERR_UNSUPPORTED, "too many tokens");
+  if (tokens >= (1LL << 31) || tokens >= (1LL << 40) / (num_kv_heads * head_dim)) return fail(W8A8_ERR_UNSUPPORTED, "too many tokens");
   if (k_token_stride < 0 || k_head_stride < 0 || v_token_stride < 0 || v_head_stride < 0)
     return fail(W8A8_ERR_INVALID_ARG, "strides must not be negative");
   if (!write && ((tokens > 1 && (k_token_stride < head_dim || v_token_stride < head_dim)) ||

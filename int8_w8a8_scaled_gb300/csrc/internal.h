@@ -162,6 +162,7 @@ struct Kv4CacheArgs {
   const float* k_scale;    // [1]
   const float* v_scale;    // [1]
   int kind;                // W8A8_KV4_*
+  int block_shift;         // log2 of block_size, -1 if it is no power of two (set by the launcher)
 };
 cudaError_t launch_kv4_cache(const Kv4CacheArgs& a, bool write, cudaStream_t stream);
 

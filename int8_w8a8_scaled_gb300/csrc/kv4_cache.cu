@@ -1,5 +1,7 @@
 // kv4_cache.cu -- writing and reading the 4-bit KV cache, and the block
 // tables, slots and positions of a serving step's tokens (sm_103a).
+#include <algorithm>
+
 #include "internal.h"
 #include "kv4.cuh"
 #include "quant_math.cuh"
@@ -15,16 +17,26 @@ namespace {
 // with M the largest code, codes = nearest(x / (s g)), ties to even; a NaN
 // becomes code 0 and an infinity the largest code.  Both divisions are
 // correctly rounded in fp32, as the 8-bit quantiser's are.
+//
+// Bound by the bytes, 2 + 0.5625 an element, once an element takes about ten
+// instructions.  So: a block's threads are laid out (groups of a token) x
+// (tokens), and nothing is divided to find one's place; a group is looked
+// through for NaN by its maximum (max.NaN) and mended apart; the quotient's
+// guard against overflow is left out where the group's scale bounds it.
 
 constexpr int kCacheThreads = 256;
 
-// 8 quotients -> a word of codes.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// 8 quotients (no NaN) -> a word of codes.
 template <int KIND>
-__device__ __forceinline__ uint32_t kv4_encode8(float (&y)[8]) {
+__device__ __forceinline__ uint32_t kv4_encode8(const float* y) {
   uint32_t w = 0u;
   if (KIND == W8A8_KV4_E2M1) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = y[i] != y[i] ? 0.f : y[i];
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
@@ -32,146 +44,169 @@ __device__ __forceinline__ uint32_t kv4_encode8(float (&y)[8]) {
         : "=r"(w)
         : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
   } else {
+    // adding 1.5 * 2^23 rounds to the nearest whole number, half to even, and
+    // leaves its two's complement in the low bits
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      int c;
-      asm("cvt.rni.s32.f32 %0, %1;" : "=r"(c) : "f"(y[i]));  // half to even, NaN -> 0, saturating
-      w |= static_cast<uint32_t>(max(-7, min(7, c)) & 15) << (4 * i);
-    }
+    for (int i = 0; i < 8; ++i)
+      w |= (__float_as_uint(__fadd_rn(fminf(fmaxf(y[i], -7.f), 7.f), 12582912.f)) & 15u) << (4 * i);
   }
   return w;
 }
 
-template <int KIND>
+template <int KIND, bool kBounded>
 __device__ __forceinline__ uint2 kv4_encode16(const float (&x)[16], float sg) {
-  float r, lo[8], hi[8];
+  float r, y[16];
   const bool ok = recip_ok(sg, &r);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo[i] = div_by<false>(x[i], sg, r, ok);
-    hi[i] = div_by<false>(x[8 + i], sg, r, ok);
-  }
-  return make_uint2(kv4_encode8<KIND>(lo), kv4_encode8<KIND>(hi));
+  for (int i = 0; i < 16; ++i) y[i] = div_by<kBounded>(x[i], sg, r, ok);
+  return make_uint2(kv4_encode8<KIND>(y), kv4_encode8<KIND>(y + 8));
 }
 
-template <int KIND>
-__global__ void __launch_bounds__(kCacheThreads) kv4_write_kernel(const Kv4CacheArgs p) {
-  const int groups = p.head_dim / kKv4Group;
-  const long long per_token = 2LL * p.heads * groups;
-  const long long i = static_cast<long long>(blockIdx.x) * kCacheThreads + threadIdx.x;
-  if (i >= p.tokens * per_token) return;
-  const long long token = i / per_token;
-  int r = static_cast<int>(i % per_token);
-  const int which = r / (p.heads * groups);
-  r -= which * p.heads * groups;
-  const int head = r / groups, grp = r % groups;
-  const long long slot = __ldg(p.slots + token);
-  if (slot < 0 || slot / p.block_size >= p.num_blocks) return;
-  const float g = __ldg(which ? p.v_scale : p.k_scale);
-  const uint16_t* src = static_cast<const uint16_t*>(which ? p.v : p.k) +
-                        token * (which ? p.v_token_stride : p.k_token_stride) +
-                        head * (which ? p.v_head_stride : p.k_head_stride) + grp * kKv4Group;
-  uint4 raw[2];
-  if (p.vec) {
-    raw[0] = __ldg(reinterpret_cast<const uint4*>(src));
-    raw[1] = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+// A token's record for one head, and its row in it; false: no such slot.
+__device__ __forceinline__ bool kv4_place(const Kv4CacheArgs& p, long long slot, int head, int record_bytes,
+                                          size_t* record, int* row) {
+  if (slot < 0) return false;
+  long long block;
+  int off;
+  if (p.block_shift >= 0) {
+    block = slot >> p.block_shift;
+    off = static_cast<int>(slot) & (p.block_size - 1);
+  } else if (slot < (1LL << 32)) {
+    block = static_cast<unsigned>(slot) / static_cast<unsigned>(p.block_size);
+    off = static_cast<int>(static_cast<unsigned>(slot) - static_cast<unsigned>(block) * static_cast<unsigned>(p.block_size));
   } else {
-    uint32_t u[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      u[j] = static_cast<uint32_t>(__ldg(src + 2 * j)) | (static_cast<uint32_t>(__ldg(src + 2 * j + 1)) << 16);
-    raw[0] = make_uint4(u[0], u[1], u[2], u[3]);
-    raw[1] = make_uint4(u[4], u[5], u[6], u[7]);
+    block = slot / p.block_size;
+    off = static_cast<int>(slot - block * p.block_size);
   }
-  float x[16];
-  {
-    float lo[8], hi[8];
-    if (p.fp16) {
-      unpack8<1>(raw[0], lo);
-      unpack8<1>(raw[1], hi);
+  if (block >= p.num_blocks) return false;
+  *row = off % kKv4Tokens;
+  *record = kv4_record_of(block, head, p.heads, p.block_size, off) * record_bytes;
+  return true;
+}
+
+template <int KIND, int D>
+__global__ void __launch_bounds__(kCacheThreads) kv4_write_kernel(const Kv4CacheArgs p) {
+  constexpr int kGroups = D / kKv4Group;
+  const long long token = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  if (token >= p.tokens) return;
+  const long long slot = __ldg(p.slots + token);
+  const int per_half = p.heads * kGroups;
+  for (int i = threadIdx.x; i < 2 * per_half; i += blockDim.x) {
+    const int which = i >= per_half, r = i - (which ? per_half : 0);
+    const int head = r / kGroups, grp = r % kGroups;
+    size_t record;
+    int row;
+    if (!kv4_place(p, slot, head, kv4_record_bytes(D), &record, &row)) return;
+    const float g = __ldg(which ? p.v_scale : p.k_scale);
+    const uint16_t* src = static_cast<const uint16_t*>(which ? p.v : p.k) +
+                          token * (which ? p.v_token_stride : p.k_token_stride) +
+                          head * (which ? p.v_head_stride : p.k_head_stride) + grp * kKv4Group;
+    uint4 raw[2];
+    if (p.vec) {
+      raw[0] = __ldg(reinterpret_cast<const uint4*>(src));
+      raw[1] = __ldg(reinterpret_cast<const uint4*>(src) + 1);
     } else {
-      unpack8<0>(raw[0], lo);
-      unpack8<0>(raw[1], hi);
-    }
+      uint32_t u[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      x[j] = lo[j];
-      x[8 + j] = hi[j];
+      for (int j = 0; j < 8; ++j)
+        u[j] = static_cast<uint32_t>(__ldg(src + 2 * j)) | (static_cast<uint32_t>(__ldg(src + 2 * j + 1)) << 16);
+      raw[0] = make_uint4(u[0], u[1], u[2], u[3]);
+      raw[1] = make_uint4(u[4], u[5], u[6], u[7]);
     }
+    float x[16];
+    {
+      float lo[8], hi[8];
+      if (p.fp16) {
+        unpack8<1>(raw[0], lo);
+        unpack8<1>(raw[1], hi);
+      } else {
+        unpack8<0>(raw[0], lo);
+        unpack8<0>(raw[1], hi);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[j] = lo[j];
+        x[8 + j] = hi[j];
+      }
+    }
+    float a = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) a = max_nan(a, fabsf(x[j]));
+    if (a != a) {
+      a = 0.f;
+      for (int j = 0; j < 16; ++j) {
+        x[j] = x[j] != x[j] ? 0.f : x[j];
+        a = fmaxf(a, fabsf(x[j]));
+      }
+    }
+    const float ratio = __fdiv_rn(a, __fmul_rn(kv4_largest(KIND), g));
+    const uint32_t scale = e4m3x2(fminf(fmaxf(ratio, 0.001953125f), 448.f), 0.f) & 0xFFu;
+    const float sg = __fmul_rn(e4m3_to_float(static_cast<uint8_t>(scale)), g);
+    // with its scale not cut off no quotient passes the largest code by more than a rounding
+    const uint2 codes = ratio <= 448.f ? kv4_encode16<KIND, true>(x, sg) : kv4_encode16<KIND, false>(x, sg);
+    uint8_t* rec = static_cast<uint8_t*>(p.cache) + record;
+    *reinterpret_cast<uint2*>(rec + kv4_codes_at(D, which) + row * (D / 2) + grp * 8) = codes;
+    rec[kv4_scales_at(D, which) + row * kGroups + grp] = static_cast<uint8_t>(scale);
   }
-  float a = 0.f;
-#pragma unroll
-  for (int j = 0; j < 16; ++j) a = fmaxf(a, fabsf(x[j]));  // fmaxf drops a NaN
-  const float ratio = __fdiv_rn(a, __fmul_rn(kv4_largest(KIND), g));
-  const uint32_t scale = e4m3x2(fminf(fmaxf(ratio, 0.001953125f), 448.f), 0.f) & 0xFFu;
-  const uint2 codes = kv4_encode16<KIND>(x, __fmul_rn(e4m3_to_float(static_cast<uint8_t>(scale)), g));
-  const int off = static_cast<int>(slot % p.block_size), row = off % kKv4Tokens;
-  uint8_t* rec = static_cast<uint8_t*>(p.cache) +
-                 kv4_record_of(slot / p.block_size, head, p.heads, p.block_size, off) * kv4_record_bytes(p.head_dim);
-  *reinterpret_cast<uint2*>(rec + kv4_codes_at(p.head_dim, which) + row * (p.head_dim / 2) + grp * 8) = codes;
-  rec[kv4_scales_at(p.head_dim, which) + row * groups + grp] = static_cast<uint8_t>(scale);
 }
 
 // ------------------------------------------------------------------ cache read
 //
 // The inverse: round16(code * s * g), zeros for a token without a slot.
 
-template <int KIND>
+template <int KIND, int D>
 __global__ void __launch_bounds__(kCacheThreads) kv4_read_kernel(const Kv4CacheArgs p) {
-  const int groups = p.head_dim / kKv4Group;
-  const long long per_token = 2LL * p.heads * groups;
-  const long long i = static_cast<long long>(blockIdx.x) * kCacheThreads + threadIdx.x;
-  if (i >= p.tokens * per_token) return;
-  const long long token = i / per_token;
-  int r = static_cast<int>(i % per_token);
-  const int which = r / (p.heads * groups);
-  r -= which * p.heads * groups;
-  const int head = r / groups, grp = r % groups;
+  constexpr int kGroups = D / kKv4Group;
+  const long long token = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  if (token >= p.tokens) return;
   const long long slot = __ldg(p.slots + token);
-  uint32_t out[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-  if (slot >= 0 && slot / p.block_size < p.num_blocks) {
-    const float g = __ldg(which ? p.v_scale : p.k_scale);
-    const int off = static_cast<int>(slot % p.block_size), row = off % kKv4Tokens;
-    const uint8_t* rec =
-        static_cast<const uint8_t*>(p.cache) +
-        kv4_record_of(slot / p.block_size, head, p.heads, p.block_size, off) * kv4_record_bytes(p.head_dim);
-    const uint2 codes =
-        *reinterpret_cast<const uint2*>(rec + kv4_codes_at(p.head_dim, which) + row * (p.head_dim / 2) + grp * 8);
-    const float s = e4m3_to_float(rec[kv4_scales_at(p.head_dim, which) + row * groups + grp]);
-    uint32_t h[2][4];
-    const Kv4Scale one = kv4_scale<KIND>(__float2half2_rn(1.f));
-    kv4_decode8<KIND>(codes.x, one, h[0]);
-    kv4_decode8<KIND>(codes.y, one, h[1]);
-    float y[16];
+  const int per_half = p.heads * kGroups;
+  for (int i = threadIdx.x; i < 2 * per_half; i += blockDim.x) {
+    const int which = i >= per_half, r = i - (which ? per_half : 0);
+    const int head = r / kGroups, grp = r % kGroups;
+    uint32_t out[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    size_t record;
+    int row;
+    if (kv4_place(p, slot, head, kv4_record_bytes(D), &record, &row)) {
+      const float g = __ldg(which ? p.v_scale : p.k_scale);
+      const uint8_t* rec = static_cast<const uint8_t*>(p.cache) + record;
+      const uint2 codes = *reinterpret_cast<const uint2*>(rec + kv4_codes_at(D, which) + row * (D / 2) + grp * 8);
+      // code * s is an exact f16 number
+      const Kv4Scale s = kv4_scale<KIND>(
+          __half2half2(__low2half(e4m3x2_to_half2(rec[kv4_scales_at(D, which) + row * kGroups + grp]))));
+      uint32_t h[2][4];
+      kv4_decode8<KIND>(codes.x, s, h[0]);
+      kv4_decode8<KIND>(codes.y, s, h[1]);
+      float y[16];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&h[j / 4][j % 4]));
-      y[8 * (j / 4) + kv4_low<KIND>(j % 4)] = c.x * s * g;
-      y[8 * (j / 4) + kv4_high<KIND>(j % 4)] = c.y * s * g;
-    }
+      for (int j = 0; j < 8; ++j) {
+        const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&h[j / 4][j % 4]));
+        y[8 * (j / 4) + kv4_low<KIND>(j % 4)] = c.x * g;
+        y[8 * (j / 4) + kv4_high<KIND>(j % 4)] = c.y * g;
+      }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = y[2 * j], b = y[2 * j + 1];
-      if (p.fp16) {
-        const __half2 y = __floats2half2_rn(a, b);
-        out[j] = *reinterpret_cast<const uint32_t*>(&y);
-      } else {
-        const __nv_bfloat162 y = __floats2bfloat162_rn(a, b);
-        out[j] = *reinterpret_cast<const uint32_t*>(&y);
+      for (int j = 0; j < 8; ++j) {
+        if (p.fp16) {
+          const __half2 v = __floats2half2_rn(y[2 * j], y[2 * j + 1]);
+          out[j] = *reinterpret_cast<const uint32_t*>(&v);
+        } else {
+          const __nv_bfloat162 v = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
+          out[j] = *reinterpret_cast<const uint32_t*>(&v);
+        }
       }
     }
-  }
-  uint16_t* dst = static_cast<uint16_t*>(which ? p.v_out : p.k_out) +
-                  token * (which ? p.v_token_stride : p.k_token_stride) +
-                  head * (which ? p.v_head_stride : p.k_head_stride) + grp * kKv4Group;
-  if (p.vec) {
-    reinterpret_cast<uint4*>(dst)[0] = make_uint4(out[0], out[1], out[2], out[3]);
-    reinterpret_cast<uint4*>(dst)[1] = make_uint4(out[4], out[5], out[6], out[7]);
-  } else {
+    uint16_t* dst = static_cast<uint16_t*>(which ? p.v_out : p.k_out) +
+                    token * (which ? p.v_token_stride : p.k_token_stride) +
+                    head * (which ? p.v_head_stride : p.k_head_stride) + grp * kKv4Group;
+    if (p.vec) {
+      reinterpret_cast<uint4*>(dst)[0] = make_uint4(out[0], out[1], out[2], out[3]);
+      reinterpret_cast<uint4*>(dst)[1] = make_uint4(out[4], out[5], out[6], out[7]);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      dst[2 * j] = static_cast<uint16_t>(out[j]);
-      dst[2 * j + 1] = static_cast<uint16_t>(out[j] >> 16);
+      for (int j = 0; j < 8; ++j) {
+        dst[2 * j] = static_cast<uint16_t>(out[j]);
+        dst[2 * j + 1] = static_cast<uint16_t>(out[j] >> 16);
+      }
     }
   }
 }
@@ -296,17 +331,30 @@ __global__ void __launch_bounds__(kTableThreads) block_table_kernel(const BlockT
 
 }  // namespace
 
-cudaError_t launch_kv4_cache(const Kv4CacheArgs& a, bool write, cudaStream_t stream) {
-  const long long n = a.tokens * 2 * a.heads * (a.head_dim / kKv4Group);
-  const unsigned grid = static_cast<unsigned>((n + kCacheThreads - 1) / kCacheThreads);
-  if (write) {
-    if (a.kind == W8A8_KV4_E2M1) kv4_write_kernel<W8A8_KV4_E2M1><<<grid, kCacheThreads, 0, stream>>>(a);
-    else kv4_write_kernel<W8A8_KV4_INT4><<<grid, kCacheThreads, 0, stream>>>(a);
-  } else {
-    if (a.kind == W8A8_KV4_E2M1) kv4_read_kernel<W8A8_KV4_E2M1><<<grid, kCacheThreads, 0, stream>>>(a);
-    else kv4_read_kernel<W8A8_KV4_INT4><<<grid, kCacheThreads, 0, stream>>>(a);
-  }
+namespace {
+
+template <int KIND, int D>
+cudaError_t launch_cache_t(const Kv4CacheArgs& a, bool write, cudaStream_t stream) {
+  const int per_token = 2 * a.heads * (D / kKv4Group);
+  const dim3 block(std::min(per_token, kCacheThreads), std::max(1, kCacheThreads / per_token));
+  const unsigned grid = static_cast<unsigned>((a.tokens + block.y - 1) / block.y);
+  if (write) kv4_write_kernel<KIND, D><<<grid, block, 0, stream>>>(a);
+  else kv4_read_kernel<KIND, D><<<grid, block, 0, stream>>>(a);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_cache(const Kv4CacheArgs& args, bool write, cudaStream_t stream) {
+  Kv4CacheArgs a = args;
+  a.block_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if ((1 << i) == a.block_size) a.block_shift = i;
+  if (a.head_dim == 64)
+    return a.kind == W8A8_KV4_E2M1 ? launch_cache_t<W8A8_KV4_E2M1, 64>(a, write, stream)
+                                   : launch_cache_t<W8A8_KV4_INT4, 64>(a, write, stream);
+  return a.kind == W8A8_KV4_E2M1 ? launch_cache_t<W8A8_KV4_E2M1, 128>(a, write, stream)
+                                 : launch_cache_t<W8A8_KV4_INT4, 128>(a, write, stream);
 }
 
 cudaError_t launch_block_tables(const BlockTableArgs& a, int num_sms, cudaStream_t stream) {

@@ -9,8 +9,9 @@
 // distribution whatever the draft was.
 //
 // Bound by the bytes of one target and one draft row for each request.  A row
-// is shared by a cluster of CTAs (8 for a few requests: one CTA alone draws
-// about 100 GB/s), whose warps sum consecutive pieces.  The piece that holds
+// is shared by a cluster of CTAs (8 for a few requests: one SM alone draws
+// about 100 GB/s; one where there are as many requests as SMs), whose warps
+// sum consecutive pieces.  The piece that holds
 // the draw follows from all pieces' sums, exchanged through distributed
 // shared memory; its warp reads it once more (from L2) and walks it.
 //
@@ -31,7 +32,7 @@ namespace w8a8 {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kStride = 128;  // tokens a warp takes at once: 4 of each lane
@@ -89,8 +90,9 @@ struct Pair {
   }
   // + max(p - q, 0)
   __device__ __forceinline__ void add_difference(float p, float q) {
+    q = fminf(p, q);
     const float d = __fsub_rn(p, q);
-    if (d > 0.f) add(d, __fsub_rn(__fsub_rn(p, d), q));
+    add(d, __fsub_rn(__fsub_rn(p, d), q));
   }
 };
 
@@ -101,7 +103,7 @@ __device__ __forceinline__ double warp_sum(const Weights& w, int v0, int v1, int
   Pair sum;
   if (kVec) {
     int v = v0 + 4 * lane;
-#pragma unroll 2
+#pragma unroll 4
     for (; v + 4 <= v1; v += kStride) {
       float p[4], q[4] = {0.f, 0.f, 0.f, 0.f};
       prob4<DT>(w.p, w.p_at + v, p);
@@ -129,7 +131,7 @@ __device__ __forceinline__ double warp_sum(const Weights& w, int v0, int v1, int
 }
 
 template <int DT, bool kVec>
-__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) verify_kernel(const VerifyArgs a) {
   __shared__ double s_sum[kWarps];
   __shared__ double s_before, s_goal;
   __shared__ int s_kept, s_owner;  // s_owner: the piece that holds the draw
@@ -318,10 +320,10 @@ cudaError_t launch_dt(const VerifyArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_verify(const VerifyArgs& args, int num_sms, cudaStream_t stream) {
   VerifyArgs a = args;
-  // as many CTAs to a row as are resident at once (four of 512 threads to an
-  // SM), while a warp keeps 128 tokens
+  // as many CTAs to a row as there are SMs for, while a warp keeps 128 tokens
+  // (128 rows of 131072: one CTA each; 4 CTAs of 512 threads each took twice as long)
   a.cluster = kMaxCluster;
-  while (a.cluster > 1 && (static_cast<long long>(a.batch) * a.cluster > 4LL * num_sms ||
+  while (a.cluster > 1 && (static_cast<long long>(a.batch) * a.cluster > num_sms ||
                            a.vocab < a.cluster * kWarps * kStride))
     a.cluster /= 2;
   switch (a.dtype) {
