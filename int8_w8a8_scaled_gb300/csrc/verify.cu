@@ -13,7 +13,7 @@
 // about 100 GB/s; one where there are as many requests as SMs), whose warps
 // sum consecutive pieces.  The piece that holds
 // the draw follows from all pieces' sums, exchanged through distributed
-// shared memory; its warp reads it once more (from L2) and walks it.
+// shared memory; its CTA reads it once more (from L2) and narrows it down.
 //
 // Sums and comparisons have to be good to about 48 bits: a 32-bit running sum
 // over 10^5 weights is off by more than most of them.  A GB300 SM adds two
@@ -103,18 +103,36 @@ __device__ __forceinline__ double warp_sum(const Weights& w, int v0, int v1, int
   Pair sum;
   if (kVec) {
     int v = v0 + 4 * lane;
-#pragma unroll 4
+    auto take = [&](int at, const float (&p)[4], const float (&q)[4]) {
+      float x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = p[k];
+      if (!kQ && static_cast<unsigned>(w.hole - at) < 4u) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (at + k == w.hole) x[k] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum.add_difference(x[k], q[k]);
+    };
+    // four loads of each row in flight (a loop left after any of its loads would not have them)
+    constexpr int kAhead = 4;
+    for (; v + (kAhead - 1) * kStride + 4 <= v1; v += kAhead * kStride) {
+      float p[kAhead][4], q[kAhead][4];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        prob4<DT>(w.p, w.p_at + v + i * kStride, p[i]);
+        q[i][0] = q[i][1] = q[i][2] = q[i][3] = 0.f;
+        if (kQ) prob4<DT>(w.q, w.q_at + v + i * kStride, q[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) take(v + i * kStride, p[i], q[i]);
+    }
     for (; v + 4 <= v1; v += kStride) {
       float p[4], q[4] = {0.f, 0.f, 0.f, 0.f};
       prob4<DT>(w.p, w.p_at + v, p);
       if (kQ) prob4<DT>(w.q, w.q_at + v, q);
-      if (!kQ && static_cast<unsigned>(w.hole - v) < 4u) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (v + k == w.hole) p[k] = 0.f;
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) sum.add_difference(p[k], q[k]);
+      take(v, p, q);
     }
     for (int k = v; k < min(v1, v + 4); ++k)  // the row's end
       sum.add_difference(k == w.hole ? 0.f : prob<DT>(w.p, w.p_at + k), kQ ? prob<DT>(w.q, w.q_at + k) : 0.f);
@@ -176,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const VerifyArgs a)
   w.hole = kept < n && !a.draft ? __ldg(a.draft_tokens + first + kept) : -1;
   const double u = __ldg(a.sample_uniform + b);
   // ---- the pieces' sums; a second time over the target alone if nothing is left of it
+  static_assert(kWarps == 32, "a warp looks at one sum in each lane");
   const int pieces = a.cluster * kWarps, mine = rank * kWarps + warp;
   const int per = ((a.vocab + pieces - 1) / pieces + kStride - 1) / kStride * kStride;
   const int v0 = static_cast<int>(min(static_cast<long long>(a.vocab), static_cast<long long>(mine) * per));
@@ -240,54 +259,68 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const VerifyArgs a)
     if (rank == 0 && tid == 0) out[kept] = -1;
     return;
   }
-  if (owner != mine) return;
-  // ---- the walk through the piece: over 128 tokens at a time, then within them
+  if (owner / kWarps != rank) return;
+  // ---- the owner's CTA narrows the piece down to 128 tokens, its warps summing
+  // a 32nd of what is left each time
   const double goal = s_goal;
+  int lo = static_cast<int>(min(static_cast<long long>(a.vocab), static_cast<long long>(owner) * per));
+  int hi = min(a.vocab, lo + per);
   double c = s_before;
-  int best = -1;
-  for (int v = v0; v < v1; v += kStride) {
-    const int end = min(v1, v + kStride);
-    const double sum = w.q ? warp_sum<DT, kVec, true>(w, v, end, lane) : warp_sum<DT, kVec, false>(w, v, end, lane);
-    const bool late = end == v1;  // with nothing found (a rounding): the last token of any weight
-    if (!(sum > 0.0) || (!(c + sum > goal) && !late)) {
-      if (sum > 0.0) best = -2 - v;  // it may still be in here
-      c += sum;
-      if (!late || best == -1) continue;
-    }
-    const int from = sum > 0.0 ? v : -2 - best;
-    double x[4], run = 0.0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int t = from + 4 * lane + k;
-      x[k] = 0.0;
-      if (t < min(v1, from + kStride) && t != w.hole) {
-        const float p = prob<DT>(w.p, w.p_at + t);
-        x[k] = w.q ? fmax(static_cast<double>(p) - static_cast<double>(prob<DT>(w.q, w.q_at + t)), 0.0) : p;
-      }
-      run += x[k];
-    }
-    double upto = run;
+  while (hi - lo > kStride) {
+    const int part = ((hi - lo + kWarps - 1) / kWarps + kStride - 1) / kStride * kStride;
+    const int p0 = static_cast<int>(min(static_cast<long long>(hi), lo + static_cast<long long>(warp) * part)), p1 = min(hi, p0 + part);
+    const double sum = w.q ? warp_sum<DT, kVec, true>(w, p0, p1, lane) : warp_sum<DT, kVec, false>(w, p0, p1, lane);
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    // every warp for itself: the first part that passes the goal, or the last of any weight
+    const double mine_sum = s_sum[lane];
+    double upto = mine_sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const double o = __shfl_up_sync(0xffffffffu, upto, off);
       if (lane >= off) upto += o;
     }
-    double at = c + (upto - run);
-    int found = 1 << 30, some = -1;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      at += x[k];
-      const int t = from + 4 * lane + k;
-      if (x[k] > 0.0) {
-        if (at > goal && found == (1 << 30)) found = t;
-        some = t;
-      }
-    }
-    found = __reduce_min_sync(0xffffffffu, found);
-    best = found < (1 << 30) && from == v ? found : __reduce_max_sync(0xffffffffu, some);
-    break;
+    const uint32_t any = __ballot_sync(0xffffffffu, mine_sum > 0.0);
+    const uint32_t passes = __ballot_sync(0xffffffffu, mine_sum > 0.0 && c + upto > goal);
+    const int pick = passes ? __ffs(passes) - 1 : any ? 31 - __clz(any) : 0;
+    const double front = __shfl_sync(0xffffffffu, upto - mine_sum, pick);
+    c += front;
+    lo = static_cast<int>(min(static_cast<long long>(hi), lo + static_cast<long long>(pick) * part));
+    hi = min(hi, lo + part);
+    __syncthreads();  // the sums have been read
   }
-  if (lane == 0) out[kept] = best;
+  if (warp != 0) return;
+  double x[4], run = 0.0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int t = lo + 4 * lane + k;
+    x[k] = 0.0;
+    if (t < hi && t != w.hole) {
+      const float p = prob<DT>(w.p, w.p_at + t);
+      x[k] = w.q ? fmax(static_cast<double>(p) - static_cast<double>(prob<DT>(w.q, w.q_at + t)), 0.0) : p;
+    }
+    run += x[k];
+  }
+  double upto = run;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const double o = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += o;
+  }
+  double at = c + (upto - run);
+  int found = 1 << 30, some = -1;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    at += x[k];
+    const int t = lo + 4 * lane + k;
+    if (x[k] > 0.0) {
+      if (at > goal && found == (1 << 30)) found = t;
+      some = t;
+    }
+  }
+  found = __reduce_min_sync(0xffffffffu, found);
+  some = __reduce_max_sync(0xffffffffu, some);  // nothing passes (a rounding): the last of any weight
+  if (lane == 0) out[kept] = found < (1 << 30) ? found : some;
 }
 
 template <int DT, bool kVec>
