@@ -406,9 +406,13 @@ def kv4_cache_shape(num_blocks: int, num_kv_heads: int, block_size: int, head_di
 
 def _kv4_cache(cache: torch.Tensor) -> tuple:
     """(num_blocks, num_kv_heads, block_size, head_dim) of a cache tensor."""
-    if cache.dtype != torch.uint8 or cache.dim() != 4 or not cache.is_contiguous() or cache.shape[3] % 18:
-        raise ValueError("the cache must be a contiguous uint8 tensor of kv4_cache_shape()")
+    if cache.dtype is not torch.uint8 or cache.ndim != 4 or not cache.is_contiguous():
+        raise ValueError("the cache must be a contiguous uint8 CUDA tensor of kv4_cache_shape()")
     nb, h, records, nbytes = cache.shape
+    if nbytes % 18:
+        raise ValueError("the cache must be a contiguous uint8 CUDA tensor of kv4_cache_shape()")
+    if not cache.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors")
     return nb, h, 16 * records, nbytes // 18
 
 
@@ -418,39 +422,53 @@ def _kv4_kind(kind: str) -> int:
     return _lib.KV4_KINDS[kind]
 
 
-def _ints(name: str, t: torch.Tensor, n: int | None, dtype=torch.int32) -> None:
-    if t.dtype is not dtype or t.ndim != 1 or not t.is_contiguous() or (n is not None and t.numel() != n):
-        size = "" if n is None else f" of {n} entries"
-        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} vector{size}")
+def _vectors(checks, dtype) -> None:
+    """Refuses what is not a contiguous CUDA tensor of `dtype` with n elements,
+    for (name, tensor, n) in `checks`."""
+    for name, t, n in checks:
+        if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} vector of {n} entries")
+        if not t.is_cuda:
+            raise ValueError("all tensors must be CUDA tensors")
+
+
+def _stream_on(t: torch.Tensor, stream):
+    """The given stream, or the current one of the tensor's device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 def _one_scale(*ts: torch.Tensor) -> None:
     for t in ts:
-        if t.dtype != torch.float32 or t.numel() != 1:
+        if t.dtype is not torch.float32 or t.numel() != 1:
             raise ValueError("k_scale and v_scale must be float32 tensors of one element")
+        if not t.is_cuda:
+            raise ValueError("all tensors must be CUDA tensors")
 
 
 def _heads(name: str, t: torch.Tensor, shape: tuple) -> tuple:
     """Token and head strides of a [tokens, heads, head_dim] tensor."""
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}")
-    if t.stride(2) != 1 and t.shape[2] > 1:
+    token, head, dim = t.stride()
+    if dim != 1:
         raise ValueError(f"the dims of a head of {name} must be consecutive (stride(2) == 1)")
-    return t.stride(0), t.stride(1)
+    if not t.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors")
+    return token, head
 
 
 def _kv4_tokens(k, v, cache, slots, k_scale, v_scale, kind) -> tuple:
-    _cuda(k, v, cache, slots, k_scale, v_scale)
     nb, h, bs, d = _kv4_cache(cache)
-    if k.dim() != 3:
+    if k.ndim != 3:
         raise ValueError("k and v must be [tokens, num_kv_heads, head_dim]")
-    shape = (k.shape[0], h, d)
+    n = k.shape[0]
+    shape = (n, h, d)
     ks, vs = _heads("k", k, shape), _heads("v", v, shape)
-    if v.dtype != k.dtype:
+    if v.dtype is not k.dtype:
         raise TypeError("k and v must have the same element type")
-    _ints("slots", slots, shape[0], torch.int64)
+    _vectors((("slots", slots, n),), torch.int64)
     _one_scale(k_scale, v_scale)
-    return nb, bs, (_fkind(k), *shape, *ks, *vs), _kv4_kind(kind)
+    return nb, bs, (_fkind(k), n, h, d, *ks, *vs), _kv4_kind(kind)
 
 
 def kv4_cache_write(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor,
@@ -464,10 +482,11 @@ def kv4_cache_write(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, slots
     (e2m1) or absmax / (7 * 448) (int4) of the values met, no group saturates.
     kind: "e2m1" or "int4"."""
     nb, bs, sizes, kd = _kv4_tokens(k, v, cache, slots, k_scale, v_scale, kind)
-    if k.shape[0] == 0:
+    if sizes[1] == 0:
         return
-    check(_lib.load().w8a8_kv4_cache_write(_ptr(k), _ptr(v), *sizes, _ptr(cache), nb, bs, _ptr(slots), _ptr(k_scale),
-                                           _ptr(v_scale), kd, _stream(stream)))
+    check(_lib.load().w8a8_kv4_cache_write(
+        k.data_ptr(), v.data_ptr(), *sizes, cache.data_ptr(), nb, bs, slots.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), kd, _stream_on(cache, stream)))
 
 
 def kv4_cache_read(cache: torch.Tensor, slots: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
@@ -476,10 +495,11 @@ def kv4_cache_read(cache: torch.Tensor, slots: torch.Tensor, k_scale: torch.Tens
     fp16 [tokens, num_kv_heads, head_dim]); zeros for a slot outside the
     cache.  Arguments as for kv4_cache_write."""
     nb, bs, sizes, kd = _kv4_tokens(k, v, cache, slots, k_scale, v_scale, kind)
-    if k.shape[0] == 0:
+    if sizes[1] == 0:
         return
-    check(_lib.load().w8a8_kv4_cache_read(_ptr(cache), nb, bs, _ptr(slots), _ptr(k_scale), _ptr(v_scale), kd,
-                                          _ptr(k), _ptr(v), *sizes, _stream(stream)))
+    check(_lib.load().w8a8_kv4_cache_read(
+        cache.data_ptr(), nb, bs, slots.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), kd, k.data_ptr(),
+        v.data_ptr(), *sizes, _stream_on(cache, stream)))
 
 
 def build_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_blocks: torch.Tensor,
@@ -500,26 +520,21 @@ def build_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_
     the needs up to the last admitted request, negative by the blocks that the
     list was short) and free_count_out (int32 [1], optional: the ids still
     free, the next call's free_count)."""
-    _cuda(context_lens, new_lens, free_blocks, free_count, block_table, query_start, seq_lens, slots, positions,
-          free_left, free_count_out)
-    if block_table.dim() != 2 or block_table.dtype != torch.int32 or not block_table.is_contiguous():
-        raise ValueError("block_table must be a contiguous int32 [batch, max_blocks] tensor")
+    if block_table.dtype is not torch.int32 or block_table.ndim != 2 or not block_table.is_contiguous():
+        raise ValueError("block_table must be a contiguous int32 [batch, max_blocks] CUDA tensor")
     batch, max_blocks = block_table.shape
-    _ints("context_lens", context_lens, batch)
-    _ints("new_lens", new_lens, batch)
-    _ints("free_blocks", free_blocks, None)
-    _ints("free_count", free_count, 1)
-    _ints("query_start", query_start, batch + 1)
-    _ints("seq_lens", seq_lens, batch)
-    _ints("slots", slots, None, torch.int64)
-    _ints("positions", positions, slots.numel())
-    _ints("free_left", free_left, 1)
+    tokens, ids = slots.numel(), free_blocks.numel()
+    _vectors((("context_lens", context_lens, batch), ("new_lens", new_lens, batch), ("free_blocks", free_blocks, ids),
+              ("free_count", free_count, 1), ("query_start", query_start, batch + 1), ("seq_lens", seq_lens, batch),
+              ("positions", positions, tokens), ("free_left", free_left, 1)), torch.int32)
+    _vectors((("slots", slots, tokens),), torch.int64)
     if free_count_out is not None:
-        _ints("free_count_out", free_count_out, 1)
+        _vectors((("free_count_out", free_count_out, 1),), torch.int32)
+    _cuda(block_table)
     check(_lib.load().w8a8_build_block_tables(
-        _ptr(context_lens), _ptr(new_lens), batch, _ptr(free_blocks), _ptr(free_count), free_blocks.numel(),
-        _ptr(block_table), max_blocks, block_size, _ptr(query_start), _ptr(seq_lens), _ptr(slots), _ptr(positions),
-        slots.numel(), _ptr(free_left), _ptr(free_count_out), _stream(stream)))
+        context_lens.data_ptr(), new_lens.data_ptr(), batch, free_blocks.data_ptr(), free_count.data_ptr(), ids,
+        block_table.data_ptr(), max_blocks, block_size, query_start.data_ptr(), seq_lens.data_ptr(), slots.data_ptr(),
+        positions.data_ptr(), tokens, free_left.data_ptr(), _ptr(free_count_out), _stream_on(block_table, stream)))
 
 
 def kv4_attention_workspace_size(batch: int, max_query_len: int, num_q_heads: int, num_kv_heads: int,
@@ -547,24 +562,25 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, 
     one; None: one row a request.  Row i of a request's n sees its tokens
     t <= seq_len - n + i; a row that sees none gives zeros.  sm_scale defaults
     to 1 / sqrt(head_dim)."""
-    _cuda(q, cache, seq_lens, block_table, k_scale, v_scale, out, query_start)
-    lib = _lib.load()
     nb, hkv, bs, d = _kv4_cache(cache)
-    if q.dim() != 3 or q.shape[2] != d:
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != d:
         raise ValueError("q must be [tokens, num_q_heads, head_dim] with the cache's head_dim")
-    tokens, hq = q.shape[0], q.shape[1]
-    qs, os_ = _heads("q", q, tuple(q.shape)), _heads("out", out, tuple(q.shape))
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
-        raise ValueError("block_table must be a contiguous int32 [batch, max_blocks] tensor")
+    tokens, hq, _ = shape
+    qs, os_ = _heads("q", q, shape), _heads("out", out, shape)
+    if block_table.dtype is not torch.int32 or block_table.ndim != 2 or not block_table.is_contiguous():
+        raise ValueError("block_table must be a contiguous int32 [batch, max_blocks] CUDA tensor")
     batch, max_blocks = block_table.shape
-    _ints("seq_lens", seq_lens, batch)
-    if query_start is not None:
-        _ints("query_start", query_start, batch + 1)
+    if query_start is None:
+        _vectors((("seq_lens", seq_lens, batch),), torch.int32)
+    else:
+        _vectors((("seq_lens", seq_lens, batch), ("query_start", query_start, batch + 1)), torch.int32)
     _one_scale(k_scale, v_scale)
+    _cuda(block_table)
     kd = _kv4_kind(kind)
     if tokens == 0:
         return
-    need = _kv4_attention_need(q.device.index, batch, max_query_len, hq, hkv, d)
+    need = _kv4_attention_need(q.get_device(), batch, max_query_len, hq, hkv, d)
     if isinstance(workspace, Workspace):
         wbuf = workspace.ensure(need).buf
     elif workspace is None:
@@ -573,10 +589,10 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, 
         wbuf = workspace
     if sm_scale is None:
         sm_scale = 1.0 / float(d) ** 0.5
-    check(lib.w8a8_kv4_attention(
-        _ptr(q), _fkind(q), tokens, hq, hkv, d, *qs, _ptr(cache), nb, bs, _ptr(block_table), max_blocks,
-        _ptr(seq_lens), _ptr(query_start), batch, max_query_len, _ptr(k_scale), _ptr(v_scale), float(sm_scale), kd,
-        _ptr(out), _fkind(out), *os_, _ptr(wbuf), wbuf.numel() * wbuf.element_size(), _stream(stream)))
+    check(_lib.load().w8a8_kv4_attention(
+        q.data_ptr(), _fkind(q), tokens, hq, hkv, d, *qs, cache.data_ptr(), nb, bs, block_table.data_ptr(), max_blocks,
+        seq_lens.data_ptr(), _ptr(query_start), batch, max_query_len, k_scale.data_ptr(), v_scale.data_ptr(), sm_scale, kd,
+        out.data_ptr(), _fkind(out), *os_, wbuf.data_ptr(), wbuf.numel() * wbuf.element_size(), _stream_on(q, stream)))
 
 
 def verify_drafts(target_probs: torch.Tensor, draft_probs: torch.Tensor | None, draft_tokens: torch.Tensor,
@@ -593,24 +609,25 @@ def verify_drafts(target_probs: torch.Tensor, draft_probs: torch.Tensor | None, 
     random numbers in [0, 1).  Written: out_tokens, int32 [batch,
     max_drafts + 1] (accepted tokens, the drawn one, then -1), and
     num_accepted, int32 [batch]."""
-    _cuda(target_probs, draft_probs, draft_tokens, draft_start, uniform, sample_uniform, out_tokens, num_accepted)
-    if out_tokens.dtype != torch.int32 or out_tokens.dim() != 2 or not out_tokens.is_contiguous():
-        raise ValueError("out_tokens must be a contiguous int32 [batch, max_drafts + 1] tensor")
-    batch, rows = out_tokens.shape[0], draft_tokens.numel()
-    vocab = target_probs.shape[1] if target_probs.dim() == 2 else 0
-    if target_probs.dim() != 2 or target_probs.shape[0] != rows + batch:
+    if out_tokens.dtype is not torch.int32 or out_tokens.ndim != 2 or not out_tokens.is_contiguous():
+        raise ValueError("out_tokens must be a contiguous int32 [batch, max_drafts + 1] CUDA tensor")
+    batch, columns = out_tokens.shape
+    rows = draft_tokens.numel()
+    if target_probs.ndim != 2 or target_probs.shape[0] != rows + batch:
         raise ValueError("target_probs must be [rows + batch, vocab]")
-    if draft_probs is not None and tuple(draft_probs.shape) != (rows, vocab):
-        raise ValueError("draft_probs must be [rows, vocab]")
-    if draft_probs is not None and draft_probs.dtype != target_probs.dtype:
-        raise TypeError("target_probs and draft_probs must have the same element type")
-    _ints("draft_tokens", draft_tokens, rows)
-    _ints("draft_start", draft_start, batch + 1)
-    _ints("uniform", uniform, rows, torch.float32)
-    _ints("sample_uniform", sample_uniform, batch, torch.float32)
-    _ints("num_accepted", num_accepted, batch)
+    vocab = target_probs.shape[1]
+    if draft_probs is not None:
+        if draft_probs.shape != (rows, vocab):
+            raise ValueError("draft_probs must be [rows, vocab]")
+        if draft_probs.dtype is not target_probs.dtype:
+            raise TypeError("target_probs and draft_probs must have the same element type")
+    _vectors((("draft_tokens", draft_tokens, rows), ("draft_start", draft_start, batch + 1),
+              ("num_accepted", num_accepted, batch)), torch.int32)
+    _vectors((("uniform", uniform, rows), ("sample_uniform", sample_uniform, batch)), torch.float32)
+    _cuda(target_probs, draft_probs, out_tokens)
     check(_lib.load().w8a8_verify_drafts(
-        _ptr(target_probs), _ptr(draft_probs), FP32 if target_probs.dtype == torch.float32 else _fkind(target_probs),
-        vocab, _ld(target_probs), vocab if draft_probs is None else _ld(draft_probs), _ptr(draft_tokens),
-        _ptr(draft_start), batch, rows, _ptr(uniform), _ptr(sample_uniform), _ptr(out_tokens),
-        out_tokens.shape[1] - 1, _ptr(num_accepted), _stream(stream)))
+        target_probs.data_ptr(), _ptr(draft_probs),
+        FP32 if target_probs.dtype is torch.float32 else _fkind(target_probs), vocab, _ld(target_probs),
+        vocab if draft_probs is None else _ld(draft_probs), draft_tokens.data_ptr(), draft_start.data_ptr(), batch, rows,
+        uniform.data_ptr(), sample_uniform.data_ptr(), out_tokens.data_ptr(), columns - 1, num_accepted.data_ptr(),
+        _stream_on(target_probs, stream)))
