@@ -1148,8 +1148,8 @@ w8a8_status w8a8_kv4_attention(const void* q, int q_dtype, int64_t tokens, int64
     return fail(W8A8_ERR_INVALID_ARG, "without query_start a request has one token: tokens = batch, max_query_len = 1");
   if (tokens >= (1LL << 31) || max_blocks >= (1LL << 31) / block_size)
     return fail(W8A8_ERR_UNSUPPORTED, "tokens and max_blocks * block_size must be below 2^31");
-  if (batch * num_kv_heads >= (1LL << 34) / (max_blocks * block_size))
-    return fail(W8A8_ERR_UNSUPPORTED, "batch * num_kv_heads * max_blocks * block_size must be below 2^34");
+  if (batch * num_kv_heads >= (1LL << 33) / (max_blocks * block_size))
+    return fail(W8A8_ERR_UNSUPPORTED, "batch * num_kv_heads * max_blocks * block_size must be below 2^33");
   if (q_token_stride < 0 || q_head_stride < 0 || (tokens > 1 && out_token_stride < head_dim) ||
       (num_q_heads > 1 && out_head_stride < head_dim))
     return fail(W8A8_ERR_INVALID_ARG, "strides of q must not be negative, those of out at least head_dim");

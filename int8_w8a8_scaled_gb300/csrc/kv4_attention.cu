@@ -6,8 +6,9 @@
 //
 // ---- Work
 // A unit is one request and KV head: its n new tokens times the G query heads
-// that share the KV head are `rows` rows over the same tokens, taken in steps
-// of kStep tiles (a tile: the 16 tokens of one record).  All units' steps in a
+// that share the KV head are rows over the same tokens (up to 16; 17 to 32 make
+// two units, the second of which finds the cache in L2), taken in steps of
+// kStep tiles (a tile: the 16 tokens of one record).  All units' steps in a
 // row, request by request and head by head, are cut into equal runs, one for
 // each warp of the grid, so that ragged lengths load the SMs evenly.  A warp
 // goes through its run alone: no barrier, no other warp's data.  A unit that
@@ -20,7 +21,7 @@
 // that finds its run itself: the split follows the lengths on the device, and
 // one launch does it all.
 //
-// ---- Few rows (up to 16): mma.sync
+// ---- Few rows: mma.sync
 // Bound by the cache's bytes, 18 head_dim a tile, as long as the decoding
 // keeps up: per tile a warp issues about 250 instructions, of the 390 that
 // the SM has slots for in the time that HBM takes to bring the tile.
@@ -64,11 +65,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kStep = 2;                         // tiles of a step
-constexpr int kRing = 2;                         // steps in a warp's ring
-constexpr int kSmallRows = 16;
+constexpr int kSmallRows = 32;                   // at most two groups of 16
 constexpr float kHeadroom = 2.f;
 constexpr float kNoScore = -1e25f;               // below any product, and finite
 constexpr int kMaxCounters = 1024;               // CTAs that may leave a unit open
@@ -84,8 +81,11 @@ struct Request {
   int first, n;  // its rows in q
   int len;       // tokens
   int steps;     // steps of a unit; 0: nothing to do here
+  int more;      // groups of its rows that a KV head has, less one (0 or 1)
+  int units;
 };
 
+template <int kStep, int kRows>
 __device__ __forceinline__ Request request_of(const Kv4AttnParams& p, int b) {
   Request r;
   r.first = b;
@@ -98,6 +98,8 @@ __device__ __forceinline__ Request request_of(const Kv4AttnParams& p, int b) {
   r.len = static_cast<int>(min(static_cast<long long>(max(__ldg(p.seq_lens + b), 0)), room));
   // an empty request has one step, with no token in it, to write its zeros
   constexpr int kTokens = kStep * kKv4Tokens;
+  r.more = r.n * p.share > kRows;
+  r.units = p.num_kv_heads << r.more;
   r.steps = r.n > 0 ? max(1, (r.len + kTokens - 1) / kTokens) : 0;
   return r;
 }
@@ -111,7 +113,7 @@ struct Start {
 struct Piece {
   int unit;  // the unit's first step; -1: no piece
   int steps; // the unit's
-  int first, n, kvh;
+  int first, kvh, row0, rows;
 };
 
 // ------------------------------------------------------------------ pieces
@@ -186,6 +188,14 @@ struct Joined {
 template <int D, int NT>
 struct Small {
   static constexpr int kRows = 8 * NT;
+  // 8 rows: 8 warps of 128 registers, two CTAs to an SM, steps of two tiles.
+  // 16 rows: the state takes twice the registers, so 12 warps of 168 and one
+  // CTA; the second row block hides latencies as the second tile does (8 warps
+  // with two tiles: 240 registers, and half the rate).
+  static constexpr int kWarps = NT == 1 ? 8 : 12, kThreads = 32 * kWarps;
+  static constexpr int kCtas = NT == 1 ? 2 : 1;
+  static constexpr int kStep = NT == 1 ? 2 : 1;            // tiles of a step
+  static constexpr int kRing = NT == 1 ? 2 : 4;            // steps in a warp's ring
   static constexpr int kTile = kv4_record_bytes(D);
   static constexpr int kSlot = kStep * kTile;
   static constexpr int kRingBytes = kWarps * kRing * kSlot;
@@ -196,8 +206,10 @@ struct Small {
 };
 
 template <int KIND, int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel(const Kv4AttnParams p) {
+__global__ void __launch_bounds__(Small<D, NT>::kThreads, Small<D, NT>::kCtas) kv4_few_rows_kernel(const Kv4AttnParams p) {
   using C = Small<D, NT>;
+  constexpr int kWarps = C::kWarps, kThreads = C::kThreads, kStep = C::kStep, kRing = C::kRing;
+  constexpr uint32_t kAll = (1u << kStep) - 1u;  // a step's records
   constexpr int KW = D / 32;   // words of K codes a lane holds of a token
   constexpr int MT = D / 16;   // m-tiles of the output product, k-blocks of the scores'
   extern __shared__ __align__(128) uint8_t smem[];
@@ -219,14 +231,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- the runs (all units' steps are fewer than 2^31, the launcher sees to it)
-  const int hkv = p.num_kv_heads, workers = static_cast<int>(gridDim.x) * kWarps;
+  const int workers = static_cast<int>(gridDim.x) * kWarps;
   int total = 0, share;
   {
     const int per = (p.batch + kThreads - 1) / kThreads;
     const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
     int mine = 0;
 #pragma unroll 1
-    for (int b = b0; b < b1; ++b) mine += request_of(p, b).steps * hkv;
+    for (int b = b0; b < b1; ++b) {
+      const Request r = request_of<kStep, C::kRows>(p, b);
+      mine += r.steps * r.units;
+    }
     int run = mine;
 #pragma unroll 1
     for (int off = 1; off < 32; off <<= 1) {
@@ -251,7 +266,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
         int before = run;
 #pragma unroll 1
         for (int b = b0; b < b1; ++b) {
-          const int steps = request_of(p, b).steps * hkv;
+          const Request r = request_of<kStep, C::kRows>(p, b);
+          const int steps = r.steps * r.units;
           if (at < before + steps) {
             s_start[w] = {b, before};
             break;
@@ -272,16 +288,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
   bool ok = true;
   if (run_steps > 0) {
   int b = s_start[warp].b;
-  Request rq = request_of(p, b);
-  int kvh = (r0 - s_start[warp].before) / rq.steps;
-  int step = (r0 - s_start[warp].before) - kvh * rq.steps;
+  Request rq = request_of<kStep, C::kRows>(p, b);
+  int ui = (r0 - s_start[warp].before) / rq.steps;  // unit of the request: KV head, then group of rows
+  int step = (r0 - s_start[warp].before) - ui * rq.steps;
 
   // ---- fetching, up to kRing steps ahead of the computation
   const uint64_t pol = policy_evict_first();
   // The places of a batch of 16 steps are looked up at once: lane 2 k + u has
   // record u of the batch's step k, and copies it when its turn comes.
   constexpr int kBatch = 32 / kStep;
-  int fb = b, fkvh = kvh, fpos = 0, fetched = 0;  // fpos: the position in the run that fstep stands for
+  int fb = b, fui = ui, fpos = 0, fetched = 0;  // fpos: the position in the run that fstep stands for
   int fstep = step;
   Request frq = rq;
   const uint8_t* src = nullptr;  // this lane's record
@@ -297,9 +313,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
         fpos = want;
         while (fstep >= frq.steps) {
           fstep -= frq.steps;
-          if (++fkvh == hkv) {
-            fkvh = 0;
-            do frq = request_of(p, ++fb);
+          if (++fui == frq.units) {
+            fui = 0;
+            do frq = request_of<kStep, C::kRows>(p, ++fb);
             while (frq.steps == 0);
           }
         }
@@ -310,20 +326,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
           const int blk = __ldg(p.block_table + static_cast<size_t>(fb) * p.max_blocks + page);
           in = blk >= 0 && blk < p.num_blocks;
           src = static_cast<const uint8_t*>(p.cache) +
-                ((static_cast<long long>(blk) * hkv + fkvh) * p.per_block + (tile - page * p.per_block)) * C::kTile;
+                ((static_cast<long long>(blk) * p.num_kv_heads + (fui >> frq.more)) * p.per_block + (tile - page * p.per_block)) * C::kTile;
         }
       }
       found = __ballot_sync(0xffffffffu, in);
     }
     const int turn = fetched % kBatch, slot = fetched % kRing;
-    const uint32_t live = (found >> (kStep * turn)) & 3u;
-    live_bits = (live_bits & ~(3u << (kStep * slot))) | (live << (kStep * slot));
+    const uint32_t live = (found >> (kStep * turn)) & kAll;
+    live_bits = (live_bits & ~(kAll << (kStep * slot))) | (live << (kStep * slot));
     if (lane / kStep == turn) {
       const uint32_t full = full0 + 8 * slot;
       fence_proxy_async_shared();  // the reads of the slot's last step before the copies that overwrite it
       if (live >> (lane % kStep) & 1u) {
         mbar_arrive_expect_tx(full, C::kTile);
-        bulk_load_hint(smem_addr(ring + slot * C::kSlot + (lane % kStep) * C::kTile), src, C::kTile, full, pol);
+        const uint32_t dst = smem_addr(ring + slot * C::kSlot + (lane % kStep) * C::kTile);
+        if (NT == 1) bulk_load_hint(dst, src, C::kTile, full, pol);
+        else bulk_load(dst, src, C::kTile, full);  // a second group of rows may read it again
       } else {
         mbar_arrive(full);
       }
@@ -339,7 +357,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
   int done = 0;  // steps computed
   while (done < run_steps) {
     const int seg = min(rq.steps - step, run_steps - done);  // this unit's steps in the run
-    const int rows = rq.n * p.share;
+    const int kvh = ui >> rq.more, row0 = (ui & rq.more) * C::kRows;
+    const int rows = min(C::kRows, rq.n * p.share - row0);
 
     // the query: dims D/4 t .. of row g (and 8 + g), scaled by 2^e so that the largest lies in [2^14, 2^15)
     uint32_t qf[NT][MT][2];
@@ -350,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int c = 8 * nt + g;
-        const int i = c / p.share, h = kvh * p.share + c % p.share;
+        const int i = (row0 + c) / p.share, h = kvh * p.share + (row0 + c) % p.share;
         const uint16_t* src = static_cast<const uint16_t*>(p.q) + (rq.first + i) * p.q_token_stride + h * p.q_head_stride +
                               (D / 4) * t;
 #pragma unroll
@@ -414,9 +433,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int col = 8 * nt + 2 * t + c;
-        lim[nt][c] = col < rows ? rq.len - rq.n + col / p.share : rq.len - 1;
+        lim[nt][c] = col < rows ? rq.len - rq.n + (row0 + col) / p.share : rq.len - 1;
       }
-    const int all_seen = rq.len - rq.n;  // tokens up to this one are seen by every row
+    const int all_seen = rq.len - rq.n + row0 / p.share;  // tokens up to this one are seen by every row
 
     // products that may pass the running maximum before it is raised: weights
     // then reach 2^kHeadroom, and come out times 2^(15 - kHeadroom) for f16
@@ -433,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
     for (int x = 0; x < seg; ++x) {
       const int slot = done % kRing;
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(full0 + 8 * slot, (done / kRing) & 1));
-      const uint32_t live = ok ? (live_bits >> (kStep * slot)) & 3u : 0u;
+      const uint32_t live = ok ? (live_bits >> (kStep * slot)) & kAll : 0u;
       const int t0 = (step + x) * kStep * kKv4Tokens;
       const uint8_t* rec0 = ring + slot * C::kSlot;
       if (live) {
@@ -481,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
           }
         }
         // softmax weights
-        const bool edge = t0 + kStep * kKv4Tokens - 1 > all_seen || live != 3u;
+        const bool edge = t0 + kStep * kKv4Tokens - 1 > all_seen || live != kAll;
         if (edge) {
           asm volatile("");  // a branch, not a select for every score of every step
 #pragma unroll
@@ -600,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
         if (col >= rows) continue;
         if (whole) {
           const float inv = l[nt][c] > 0.f ? vscale / l[nt][c] : 0.f;
-          const size_t at = out_at(p, rq.first, kvh, col) + (D / 8) * g;
+          const size_t at = out_at(p, rq.first, kvh, row0 + col) + (D / 8) * g;
 #pragma unroll
           for (int i = 0; i < D / 8; i += 4) store4(p, at + i, y[i] * inv, y[i + 1] * inv, y[i + 2] * inv, y[i + 3] * inv);
         } else {
@@ -612,13 +631,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
                 make_float2(l[nt][c] > 0.f ? m[nt][c] * cs : -INFINITY, l[nt][c]);
         }
       }
-    if (!whole && lane == 0) s_piece[2 * warp + last] = {r0 + done - seg - step, rq.steps, rq.first, rq.n, kvh};
+    if (!whole && lane == 0) s_piece[2 * warp + last] = {r0 + done - seg - step, rq.steps, rq.first, kvh, row0, rows};
 
     // ---- the next unit
     step = 0;
-    if (!last && ++kvh == hkv) {
-      kvh = 0;
-      do rq = request_of(p, ++b);
+    if (!last && ++ui == rq.units) {
+      ui = 0;
+      do rq = request_of<kStep, C::kRows>(p, ++b);
       while (rq.steps == 0);
     }
   }
@@ -649,11 +668,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
       if (unit == u.unit) mine |= 1u << k;
       else if (unit >= 0) next = k;
     }
-    const int rows = u.n * p.share;
     const int c0 = u.unit / cta_share, c1 = (u.unit + u.steps - 1) / cta_share;
     const bool whole = c0 == c1, begun = c0 == static_cast<int>(blockIdx.x);
     float* part = p.partial + (2 * static_cast<size_t>(blockIdx.x) + begun) * C::kPiece;
-    for (int item = tid; item < rows * (D / 4); item += kThreads) {
+    for (int item = tid; item < u.rows * (D / 4); item += kThreads) {
       const int col = item / (D / 4), d = 4 * (item % (D / 4));
       Joined sum;
       float2 ml[2 * kWarps];
@@ -667,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
       for (int k = 0; k < 2 * kWarps; ++k)
         if (mine >> k & 1u) sum.add(ml[k], *reinterpret_cast<const float4*>(piece_at(k) + col * C::kOStride + d));
       if (whole) {
-        sum.store(p, out_at(p, u.first, u.kvh, col) + d, vscale);
+        sum.store(p, out_at(p, u.first, u.kvh, u.row0 + col) + d, vscale);
       } else {
         __stcg(reinterpret_cast<float4*>(part + col * C::kOStride + d), sum.o);
         if (d == 0) __stcg(reinterpret_cast<float2*>(part + col * C::kOStride + D), make_float2(sum.m, sum.l));
@@ -701,9 +719,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
   for (int which = 0; which < 2; ++which) {
     if (!s_last[which]) continue;
     const Piece u = which ? open1 : open0;
-    const int rows = u.n * p.share;
     const int c0 = u.unit / cta_share, parts = (u.unit + u.steps - 1) / cta_share - c0 + 1;
-    for (int item = tid; item < rows * (D / 4); item += kThreads) {
+    for (int item = tid; item < u.rows * (D / 4); item += kThreads) {
       const int col = item / (D / 4), d = 4 * (item % (D / 4));
       // part 0 is the second place of CTA c0, part k the first of CTA c0 + k
       const float* src = p.partial + 2 * static_cast<size_t>(c0) * C::kPiece + col * C::kOStride;
@@ -716,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_rows_kernel
         const float* s = src + (k ? 2 * k : 1) * static_cast<size_t>(C::kPiece);
         sum.add(__ldcg(reinterpret_cast<const float2*>(s + D)), __ldcg(reinterpret_cast<const float4*>(s + d)));
       }
-      sum.store(p, out_at(p, u.first, u.kvh, col) + d, vscale);
+      sum.store(p, out_at(p, u.first, u.kvh, u.row0 + col) + d, vscale);
     }
   }
 }
@@ -744,10 +761,11 @@ cudaError_t launch_few(const Kv4AttnParams& p, int num_sms, cudaStream_t stream)
   // the attribute is per function and device; setting it again is harmless
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Small<D, NT>::kSmem);
   if (e != cudaSuccess) return e;
-  const long long most = static_cast<long long>(p.batch) * p.num_kv_heads *
-                         ((static_cast<long long>(p.max_blocks) * p.per_block + kStep - 1) / kStep);
-  const long long ctas = std::min<long long>((most + kWarps - 1) / kWarps, few_rows_ctas(NT, num_sms));
-  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), Small<D, NT>::kSmem, stream, p);
+  using C = Small<D, NT>;
+  const long long most = 2LL * p.batch * p.num_kv_heads *
+                         ((static_cast<long long>(p.max_blocks) * p.per_block + C::kStep - 1) / C::kStep);
+  const long long ctas = std::min<long long>((most + C::kWarps - 1) / C::kWarps, few_rows_ctas(NT, num_sms));
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(C::kThreads), Small<D, NT>::kSmem, stream, p);
 }
 
 template <int KIND, int D>
