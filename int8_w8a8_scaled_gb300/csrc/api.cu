@@ -746,12 +746,17 @@ w8a8_status w8a8_scaled_mm(const void* a_q, int64_t lda, const void* b_q, int64_
 // activations; the rest run the quantiser into the workspace, then the
 // matmul.  Both give the bits of w8a8_scaled_quant (dynamic, per row)
 // followed by w8a8_scaled_mm.
+// Bytes in front of the two-step route's codes: the matmul's own workspace.
+// The codes never lie on its counters, which stay zero from one call to the
+// next whatever the shapes, with scaled_mm calls on the same buffer too.
+static size_t two_step_mm_bytes(int64_t M, int64_t N, int64_t K, int q_dtype) {
+  return align256(std::max<size_t>(kCounterRegion, w8a8_scaled_mm_workspace_size(M, N, K, q_dtype)));
+}
+
 size_t w8a8_quant_scaled_mm_workspace_size(int64_t M, int64_t N, int64_t K, int q_dtype) {
   if (M < 1 || N < 1 || K < 1) return 0;
-  const size_t mm = w8a8_scaled_mm_workspace_size(M, N, K, q_dtype);
   const size_t ldq = static_cast<size_t>((K + 15) & ~15LL);
-  const size_t two_step = align256(static_cast<size_t>(M) * ldq) + align256(static_cast<size_t>(M) * 4) + mm;
-  return std::max(mm, two_step);
+  return two_step_mm_bytes(M, N, K, q_dtype) + align256(static_cast<size_t>(M) * ldq) + align256(static_cast<size_t>(M) * 4);
 }
 
 w8a8_status w8a8_quant_scaled_mm(const void* x, int x_dtype, int64_t ld_x, const void* b_q, int64_t ldb,
@@ -789,17 +794,18 @@ w8a8_status w8a8_quant_scaled_mm(const void* x, int x_dtype, int64_t ld_x, const
   const long long ldq = (K + 15) & ~15LL;
   const size_t a_bytes = align256(static_cast<size_t>(M) * static_cast<size_t>(ldq));
   const size_t s_bytes = align256(static_cast<size_t>(M) * 4);
-  if (!workspace || workspace_bytes < a_bytes + s_bytes)
+  const size_t mm_bytes = two_step_mm_bytes(M, N, K, q_dtype);
+  if (!workspace || workspace_bytes < mm_bytes + a_bytes + s_bytes)
     return fail(W8A8_ERR_WORKSPACE, "this problem needs %zu bytes of workspace",
                 w8a8_quant_scaled_mm_workspace_size(M, N, K, q_dtype));
   if (!aligned(workspace, 256)) return fail(W8A8_ERR_MISALIGNED, "workspace must be 256-byte aligned");
-  uint8_t* wsb = static_cast<uint8_t*>(workspace);
-  float* sa = scale_a_out ? scale_a_out : reinterpret_cast<float*>(wsb + a_bytes);
-  w8a8_status s1 = w8a8_scaled_quant(x, x_dtype, M, K, ld_x, wsb, q_dtype, ldq, sa, W8A8_PER_ROW, W8A8_DYNAMIC,
+  uint8_t* codes = static_cast<uint8_t*>(workspace) + mm_bytes;
+  float* sa = scale_a_out ? scale_a_out : reinterpret_cast<float*>(codes + a_bytes);
+  w8a8_status s1 = w8a8_scaled_quant(x, x_dtype, M, K, ld_x, codes, q_dtype, ldq, sa, W8A8_PER_ROW, W8A8_DYNAMIC,
                                      nullptr, 0, stream);
   if (s1 != W8A8_OK) return s1;
-  return run_mm(wsb, ldq, b_q, ldb, sa, W8A8_PER_ROW, scale_b, b_gran, out, ldc, M, N, K, q_dtype, out_dtype,
-                wsb + a_bytes + s_bytes, workspace_bytes - a_bytes - s_bytes, nullptr, st);
+  return run_mm(codes, ldq, b_q, ldb, sa, W8A8_PER_ROW, scale_b, b_gran, out, ldc, M, N, K, q_dtype, out_dtype,
+                workspace, mm_bytes, nullptr, st);
 }
 
 w8a8_status w8a8_scaled_mm_with_config(const void* a_q, int64_t lda, const void* b_q, int64_t ldb,
