@@ -188,14 +188,13 @@ struct Joined {
 template <int D, int NT>
 struct Small {
   static constexpr int kRows = 8 * NT;
-  // 8 rows: 8 warps of 128 registers, two CTAs to an SM, steps of two tiles.
-  // 16 rows: the state takes twice the registers, so 12 warps of 168 and one
-  // CTA; the second row block hides latencies as the second tile does (8 warps
-  // with two tiles: 240 registers, and half the rate).
-  static constexpr int kWarps = NT == 1 ? 8 : 12, kThreads = 32 * kWarps;
+  // 8 rows: 128 registers, two CTAs of 8 warps to an SM.  16 rows: the state
+  // takes twice the registers (240), so one CTA (12 warps of 168 registers with
+  // steps of one tile: 61 us for 55 at 32 requests of 12 rows, 2300 tokens)
+  static constexpr int kWarps = 8, kThreads = 32 * kWarps;
   static constexpr int kCtas = NT == 1 ? 2 : 1;
-  static constexpr int kStep = NT == 1 ? 2 : 1;            // tiles of a step
-  static constexpr int kRing = NT == 1 ? 2 : 4;            // steps in a warp's ring
+  static constexpr int kStep = 2;            // tiles of a step
+  static constexpr int kRing = 2;            // steps in a warp's ring
   static constexpr int kTile = kv4_record_bytes(D);
   static constexpr int kSlot = kStep * kTile;
   static constexpr int kRingBytes = kWarps * kRing * kSlot;
