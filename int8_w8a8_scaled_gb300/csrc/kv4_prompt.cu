@@ -267,9 +267,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     fence_barrier_init();
   }
   if (tid < 2) s_open[tid].unit = -1;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // TMEM only now: a kernel in front may still need it
+  // TMEM only now: a kernel in front may still need it.  Dependents start only
+  // when it is taken: one that took it first and then waited for this kernel's
+  // end would never see it.
   if (warp == kMmaWarp) {
     tmem_alloc(smem_addr(&s_tmem), kTmemCols);
     tmem_relinquish();
@@ -318,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = s_tmem;
   const long long r0 = share * blockIdx.x;
   const int run_tiles = static_cast<int>(max(0LL, min(total - r0, min(share, 0x7fffffffLL))));
