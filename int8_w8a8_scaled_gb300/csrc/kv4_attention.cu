@@ -87,7 +87,8 @@ inline int few_rows_ctas(int nt, int num_sms) { return std::min(kMaxCounters, (n
 // ------------------------------------------------------------------ requests
 
 struct Request {
-  int first, n;  // its rows in q
+  int first, n;  // its rows in q that are looked at
+  int all;       // its new tokens (more than n only past max_query_len)
   int len;       // tokens
   int steps;     // steps of a unit; 0: nothing to do here
   int more;      // groups of its rows that a KV head has, less one (0 or 1)
@@ -98,11 +99,12 @@ template <int kStep, int kRows>
 __device__ __forceinline__ Request request_of(const Kv4AttnParams& p, int b) {
   Request r;
   r.first = b;
-  r.n = 1;
+  r.all = 1;
   if (p.query_start) {
     r.first = min(max(__ldg(p.query_start + b), 0), p.tokens);
-    r.n = min(max(__ldg(p.query_start + b + 1) - r.first, 0), min(p.tokens - r.first, p.max_query_len));
+    r.all = max(min(__ldg(p.query_start + b + 1), p.tokens) - r.first, 0);
   }
+  r.n = min(r.all, p.max_query_len);
   const long long room = static_cast<long long>(p.max_blocks) * p.block_size;
   r.len = static_cast<int>(min(static_cast<long long>(max(__ldg(p.seq_lens + b), 0)), room));
   // an empty request has one step, with no token in it, to write its zeros
@@ -441,9 +443,9 @@ __global__ void __launch_bounds__(Small<D, NT>::kThreads, Small<D, NT>::kCtas) k
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int col = 8 * nt + 2 * t + c;
-        lim[nt][c] = col < rows ? rq.len - rq.n + (row0 + col) / p.share : rq.len - 1;
+        lim[nt][c] = col < rows ? rq.len - rq.all + (row0 + col) / p.share : rq.len - 1;
       }
-    const int all_seen = rq.len - rq.n + row0 / p.share;  // tokens up to this one are seen by every row
+    const int all_seen = rq.len - rq.all + row0 / p.share;  // tokens up to this one are seen by every row
 
     // products that may pass the running maximum before it is raised: weights
     // then reach 2^kHeadroom, and come out times 2^(15 - kHeadroom) for f16

@@ -77,17 +77,18 @@ struct Big {
 };
 
 struct Request {
-  int first, n, len, rows;
+  int first, n, all, len, rows;  // all: its new tokens, n: those looked at (fewer past max_query_len)
 };
 
 __device__ __forceinline__ Request request_of(const Kv4AttnParams& p, int b) {
   Request r;
   r.first = b;
-  r.n = 1;
+  r.all = 1;
   if (p.query_start) {
     r.first = min(max(__ldg(p.query_start + b), 0), p.tokens);
-    r.n = min(max(__ldg(p.query_start + b + 1) - r.first, 0), min(p.tokens - r.first, p.max_query_len));
+    r.all = max(min(__ldg(p.query_start + b + 1), p.tokens) - r.first, 0);
   }
+  r.n = min(r.all, p.max_query_len);
   const long long room = static_cast<long long>(p.max_blocks) * p.block_size;
   r.len = static_cast<int>(min(static_cast<long long>(max(__ldg(p.seq_lens + b), 0)), room));
   r.rows = r.n * p.share;
@@ -100,7 +101,7 @@ __device__ __forceinline__ Request request_of(const Kv4AttnParams& p, int b) {
 __device__ __forceinline__ int tiles_of(const Kv4AttnParams& p, const Request& r, int rt) {
   if (rt * kUnitRows >= r.rows) return 0;
   const int last = min(r.rows, (rt + 1) * kUnitRows) - 1;
-  const int seen = min(r.len, max(0, r.len - r.n + last / p.share + 1));
+  const int seen = min(r.len, max(0, r.len - r.all + last / p.share + 1));
   return max(1, (seen + kTileTokens - 1) / kTileTokens);
 }
 
@@ -662,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       if (pair) slot_sync(slot);
       else softmax_sync();
       cs = s_cs[pair ? slot : 0][row];
-      const int lim = real ? rq.len - rq.n + my / p.share : rq.len - 1;  // the last token seen
+      const int lim = real ? rq.len - rq.all + my / p.share : rq.len - 1;  // the last token seen
       const float room = fminf(kHeadroom / cs, 1e38f);
       m = kNoScore;
       l = 0.f;

@@ -304,6 +304,59 @@ def test_attention_leaves_rows_past_max_query_len_and_padding():
     assert (out[9:] == 7.0).all() and not (out[:9] == 7.0).all(2).any()
 
 
+@pytest.mark.parametrize("most", [1, 3, 20])
+def test_attention_of_the_first_rows_only(most):
+    """A max_query_len below a request's new tokens: its first rows, each with
+    the tokens that it sees among all of them; the others stay."""
+    rng = np.random.default_rng(7)
+    lens, start = np.array([90, 200]), np.int32([0, 40, 140])
+    cache, table = build(rng, lens, 2, 64, 16, "e2m1", 0.013, 0.013)
+    q = head_rows(rng, (140, 8, 64), "bf16").cuda()
+    out = torch.full_like(q, 7.0)
+    one = dev(np.float32([0.013]))
+    w8.kv4_attention(q, cache, dev(lens.astype(np.int32)), dev(table), one, one, out, query_start=dev(start), max_query_len=most)
+    rows = np.concatenate([np.arange(most), 40 + np.arange(most)])
+    ref, r, big = kv4.attention(host(q), cache.cpu().numpy(), lens, table, start, np.float32(0.013), np.float32(0.013), 0.125, "e2m1")
+    # besides the module's bounds: a weight is off by up to 2^-38 of the row's
+    # largest (f16's last bit, 2^-25 at half a step, after its scaling by 2^13), on
+    # each of 200 values of at most 6 * 448 * 0.013; it shows where a row's other
+    # weights meet zeros
+    tol = (2.0 ** -8 * np.abs(ref) + r * (2.0 ** -10 + 2.0 ** -18 + 2 * 72 * 2.0 ** -24 * big[..., None]) +
+           2.0 ** -38 * 200 * 6 * 448 * 0.013)
+    assert (np.abs(host(out).astype(np.float64) - ref)[rows] <= tol[rows]).all()
+    rest = np.setdiff1d(np.arange(140), rows)
+    assert (out[torch.from_numpy(rest).cuda()] == 7.0).all()
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_offsets_past_32_bits(new):
+    """Blocks 5 GB into the cache."""
+    rng = np.random.default_rng(8)
+    lens = np.array([100, 60])
+    small, table = build(rng, lens, 1, 64, 16, "int4", 0.013, 0.013)
+    nb = 5_000_000_000 // (18 * 64)
+    cache = torch.empty(w8.kv4_cache_shape(nb, 1, 16, 64), dtype=torch.uint8, device="cuda")
+    far = nb - small.shape[0]
+    cache[far:] = small
+    q = head_rows(rng, (2 * new, 4, 64), "bf16").cuda()
+    start = dev(np.int32([0, new, 2 * new]))
+    one, gl = dev(np.float32([0.013])), dev(lens.astype(np.int32))
+    out, want = torch.empty_like(q), torch.empty_like(q)
+    args = dict(query_start=start, max_query_len=new, kind="int4")
+    w8.kv4_attention(q, small, gl, dev(table), one, one, want, **args)
+    w8.kv4_attention(q, cache, gl, dev(np.where(table >= 0, table + far, -1).astype(np.int32)), one, one, out, **args)
+    assert torch.equal(out, want)
+    k, v = (head_rows(rng, (30, 1, 64), "bf16").cuda() for _ in range(2))
+    slots = torch.arange(30, device="cuda") * 3
+    w8.kv4_cache_write(k, v, small, slots, one, one, kind="int4")
+    w8.kv4_cache_write(k, v, cache, slots + far * 16, one, one, kind="int4")
+    assert torch.equal(cache[far:], small)
+    near, away = ([torch.empty_like(k), torch.empty_like(k)] for _ in range(2))
+    w8.kv4_cache_read(small, slots, one, one, *near, kind="int4")
+    w8.kv4_cache_read(cache, slots + far * 16, one, one, *away, kind="int4")
+    assert torch.equal(near[0], away[0]) and torch.equal(near[1], away[1])
+
+
 @pytest.mark.parametrize("new", [1, 40])
 def test_attention_on_another_stream_in_a_graph_and_repeated(new):
     rng = np.random.default_rng(6)
