@@ -535,7 +535,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       const int my = top + row;
       const bool real = my < rq.rows;
 
-      if (old.tiles > 0 && !old.pair) softmax_sync();  // both slots' last scores are there: the query may go
+      // both slots' last scores are there: the query may go.  With pairs that holds
+      // for the warp's own slot already, but s_cs is another warp's to read: all of
+      // the slot have taken the old unit's scales before one writes the next unit's
+      // (a unit of one tile has no other wait between the two)
+      if (old.tiles > 0) {
+        if (old.pair) slot_sync(slot);
+        else softmax_sync();
+      }
       // ---- the warp's 16 query rows, a 16-byte piece for each lane, scaled by
       // 2^e so that a row's largest element lies in [2^14, 2^15)
       if (more && (pair || slot == 0)) {

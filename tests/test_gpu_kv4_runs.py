@@ -1,0 +1,133 @@
+"""Attention over the 4-bit cache where a CTA or warp goes through many units
+and tiles one after the other, against 64 bits on the GPU.
+
+Tolerance, per output element, with r the weights' mean of |V|:
+  * the output's rounding, half a step: 2^-8 |ref| (bf16), 2^-11 |ref| (fp16),
+    or half the smallest subnormal number below the normal ones;
+  * softmax weights of 11 bits (f16) in the numerator and in the sum: 2^-10 r;
+    below 2^-27 of the largest they are f16 subnormals, off by up to 2^-38 of
+    the largest: 2^-38 sum |V|;
+  * fp32 scores: (2 (d + 8) 2^-24 B + 2^-18) r with B = max_t sum_d |q_d K_td|
+    |sm_scale|: products, sums and the scaling are each off by 2^-24 of at most
+    B, and twice that relative to the maximum; exp2's approximation and the
+    32-bit sums stay below 2^-18;
+  * raising the maximum rescales the sums and outputs, 2^-23 each time: at most
+    one raise a tile, 2^-23 r a tile."""
+import numpy as np
+import pytest
+import torch
+
+import int8_w8a8_scaled_gb300 as w8
+
+pytestmark = pytest.mark.gpu
+
+HALF_STEP = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+def dev(a, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    return t if dtype is None else t.to(dtype)
+
+
+def decoded(records, at, kind):
+    """[tokens, d] in 64 bits of K (at 0) or V (at 9 d) of records [n, 18 d]."""
+    d = records.shape[1] // 18
+    both = records[:, at:at + 8 * d].reshape(-1, d // 2).long()
+    code = torch.stack((both & 15, both >> 4), 2).flatten(1)
+    if kind == "int4":
+        x = torch.where(code >= 8, code - 16, code).double()
+    else:
+        x = torch.where(code >= 8, -1.0, 1.0).double() * torch.tensor(E2M1, dtype=torch.float64, device="cuda")[code % 8]
+    s = records[:, at + 8 * d:at + 9 * d].reshape(-1, d // 16).contiguous().view(torch.float8_e4m3fn).double()
+    return x * s.repeat_interleave(16, 1)
+
+
+def reference(q, cache, lens, news, table, kg, vg, sm, kind):
+    """(out, r, B, sum |V|) in 64 bits, of every row of q."""
+    h, d, bs = cache.shape[1], q.shape[2], 16 * cache.shape[2]
+    share, first = q.shape[1] // h, 0
+    out, r, total = (torch.zeros(q.shape, dtype=torch.float64, device="cuda") for _ in range(3))
+    big = torch.zeros(q.shape[:2], dtype=torch.float64, device="cuda")
+    for b, (length, n) in enumerate(zip(lens, news)):
+        blocks = dev(table[b, :-(-length // bs)].astype(np.int64))
+        limit = length - n + torch.arange(n, device="cuda")
+        seen = (torch.arange(length, device="cuda")[None] <= limit[:, None])[None]
+        for j in range(h if n and length else 0):
+            records = cache[blocks, j].flatten(0, 1)
+            k, v = decoded(records, 0, kind)[:length] * kg, decoded(records, 9 * d, kind)[:length] * vg
+            x = q[first:first + n, j * share:(j + 1) * share].double().transpose(0, 1)      # [share, n, d]
+            s = (x @ k.T * sm).masked_fill(~seen, -np.inf)
+            w = torch.nan_to_num(torch.softmax(s, 2))                                       # rows that see nothing: zeros
+            at = slice(j * share, (j + 1) * share)
+            out[first:first + n, at] = (w @ v).transpose(0, 1)
+            r[first:first + n, at] = (w @ v.abs()).transpose(0, 1)
+            total[first:first + n, at] = (seen.double() @ v.abs()).transpose(0, 1).expand(n, share, d)
+            big[first:first + n, at] = ((x.abs() @ k.abs().T) * abs(sm)).masked_fill(~seen, 0.0).amax(2).T
+        first += n
+    return out, r, big, total
+
+
+def close(got, want, lens):
+    ref, r, big, total = want
+    d, half = got.shape[2], HALF_STEP[got.dtype]
+    tiles = -(-int(max(lens)) // 16)
+    tol = (half * ref.abs() + r * (2.0 ** -10 + 2.0 ** -18 + tiles * 2.0 ** -23 + 2 * (d + 8) * 2.0 ** -24 * big[..., None]) +
+           2.0 ** -38 * total + torch.finfo(got.dtype).smallest_normal * half)
+    assert torch.isfinite(got).all()
+    over = (got.double() - ref).abs() - tol
+    assert (over <= 0).all(), f"{int((over > 0).sum())} of {over.numel()} outside"
+
+
+def serve(lens, news, hq, hkv, d, kind, dtype, bs=32, seed=0, rise=None, loud=None):
+    """One call over requests of these lengths, compared with 64 bits.
+
+    rise: requests (a slice) whose keys point along their queries, further the
+    later the token, so that the maximum goes up to the end.  loud: the queries'
+    scale for each packed token and head."""
+    lens, news = np.asarray(lens), np.asarray(news)
+    rng = np.random.default_rng(seed)
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    blocks = -(-lens // bs)
+    nb = int(blocks.sum()) + 2
+    table = np.full((len(lens), int(blocks.max())), -1, np.int32)
+    table[np.arange(table.shape[1])[None] < blocks[:, None]] = rng.permutation(nb)[:blocks.sum()]
+    k, v = (torch.randn(nb * bs, hkv, d, generator=gen, device="cuda") for _ in range(2))
+    q = torch.randn(int(news.sum()), hq, d, generator=gen, device="cuda")
+    if rise is not None:
+        start = np.concatenate([[0], np.cumsum(news)])
+        for b in range(len(lens))[rise]:
+            q[start[b]:start[b + 1]] += 1.0
+            for i, block in enumerate(table[b, :blocks[b]].tolist()):
+                k[block * bs:(block + 1) * bs] += 0.5 * i / blocks[b]
+    if loud is not None:
+        q *= loud
+    q, k, v = q.to(dtype), k.to(dtype), v.to(dtype)
+    kg, vg = 0.0151, 0.0173
+    cache = torch.zeros(w8.kv4_cache_shape(nb, hkv, bs, d), dtype=torch.uint8, device="cuda")
+    scales = dev(np.float32([kg])), dev(np.float32([vg]))
+    w8.kv4_cache_write(k, v, cache, torch.arange(nb * bs, device="cuda"), *scales, kind=kind)
+    out = torch.full_like(q, float("nan"))
+    start = dev(np.concatenate([[0], np.cumsum(news)]).astype(np.int32))
+    w8.kv4_attention(q, cache, dev(lens.astype(np.int32)), dev(table), *scales, out, query_start=start,
+                     max_query_len=int(news.max()), kind=kind)
+    assert w8.device_status() == 0
+    sm = 1.0 / d ** 0.5
+    close(out, reference(q, cache, lens, news, table, float(np.float32(kg)), float(np.float32(vg)), sm, kind), lens)
+
+
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+@pytest.mark.parametrize("kind", ["e2m1", "int4"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_units_of_one_tile_whose_queries_differ_in_size(d, kind):
+    """Fresh chunks of up to 128 tokens: a CTA goes through several units of one
+    tile each, and the queries' scales differ by powers of two between them."""
+    rng = np.random.default_rng(d)
+    news = rng.integers(65, 129, 120)
+    assert 8 * len(news) >= 5 * sms()
+    loud = 2.0 ** rng.integers(-6, 7, (len(news), 8)).repeat(2, 1).repeat(news, 0)
+    for seed in range(3):
+        serve(news, news, 16, 8, d, kind, torch.bfloat16, seed=seed, loud=dev(loud[..., None]).float())
