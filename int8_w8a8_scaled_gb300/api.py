@@ -16,6 +16,7 @@ semantics" section of "Enable scaled FP8 (e4m3fn) KV cache on ROCm".
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import threading
@@ -93,15 +94,21 @@ class Workspace:
 
     The matmul's split-K counters must start at zero; the library leaves them
     at zero after each successful call, so the buffer only needs zeroing once.
+    It is zeroed on the stream that is current where it is made: a call on
+    another stream has to come after that (``wait_stream``).  A buffer that a
+    call makes larger is zeroed on that call's stream.
     """
 
     def __init__(self, nbytes: int = 0, device=None):
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
         self.buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.device)
 
-    def ensure(self, nbytes: int) -> "Workspace":
+    def ensure(self, nbytes: int, stream=None) -> "Workspace":
+        """At least nbytes, for a call on `stream` (None: the current one)."""
         if nbytes > self.buf.numel():
-            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            with _launching_on(self.device, stream) as launch:
+                self.buf.record_stream(launch)      # earlier calls there may still use it
+                self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
         return self
 
     @property
@@ -109,22 +116,36 @@ class Workspace:
         return self.buf.numel()
 
 
+@contextlib.contextmanager
+def _launching_on(device: torch.device, stream):
+    """The given stream (None: the current one) as the current stream."""
+    if stream is None:
+        yield torch.cuda.current_stream(device)
+    else:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+        with torch.cuda.stream(stream):
+            yield stream
+
+
 _ws_lock = threading.Lock()
 _default_ws: dict = {}
 
 
-def _default_workspace(device: torch.device, nbytes: int, kind: str) -> Workspace:
-    """Per (device, stream, kind) scratch; the matmul's buffer is never shared
-    with the quantiser (whose absmax word would land on a counter)."""
-    key = (kind, device.index, _raw_stream(device.index))
+def _default_workspace(device: torch.device, nbytes: int, kind: str, stream) -> Workspace:
+    """Per (device, stream that the call runs on, kind) scratch, zeroed on that
+    stream; the matmul's buffer is never shared with the quantiser (whose absmax
+    word would land on a counter)."""
+    key = (kind, device.index, _raw_stream(device.index) if stream is None else stream.cuda_stream)
     ws = _default_ws.get(key)
     if ws is not None and ws.buf.numel() >= nbytes:
         return ws
     with _ws_lock:
         ws = _default_ws.get(key)
         if ws is None:
-            ws = _default_ws[key] = Workspace(nbytes, device)
-        return ws.ensure(nbytes)
+            with _launching_on(device, stream):
+                ws = _default_ws[key] = Workspace(nbytes, device)
+        return ws.ensure(nbytes, stream)
 
 
 def quant_workspace_size(rows: int, cols: int, per_token: bool, dynamic: bool) -> int:
@@ -151,7 +172,7 @@ def scaled_quant(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, per_toke
     mode = DYNAMIC if dynamic else STATIC
     need = lib.w8a8_scaled_quant_workspace_size(rows, cols, gran, mode)
     if need and workspace is None:
-        workspace = _default_workspace(x.device, need, "quant").buf
+        workspace = _default_workspace(x.device, need, "quant", stream).buf
     check(lib.w8a8_scaled_quant(
         _ptr(x), _fkind(x), rows, cols, _ld(x), _ptr(q), _qkind(q, q_dtype), _ld(q),
         _ptr(scale), gran, mode, _ptr(workspace) if need else None,
@@ -232,9 +253,9 @@ def scaled_mm(a_q: torch.Tensor, b_q: torch.Tensor, scale_a: torch.Tensor, scale
     need = (lib.w8a8_scaled_mm_config_workspace_size(M, N, K, qk, ctypes.byref(c)) if c is not None
             else lib.w8a8_scaled_mm_workspace_size(M, N, K, qk))
     if isinstance(workspace, Workspace):
-        workspace = workspace.ensure(need).buf
+        workspace = workspace.ensure(need, stream).buf
     elif workspace is None and need:
-        workspace = _default_workspace(a_q.device, need, "mm").buf
+        workspace = _default_workspace(a_q.device, need, "mm", stream).buf
     ws_ptr = _ptr(workspace) if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     args = (_ptr(a_q), _ld(a_q), _ptr(b_q), _ld(b_q), _ptr(scale_a), a_gran, _ptr(scale_b), b_gran,
@@ -279,9 +300,9 @@ def quant_scaled_mm(x: torch.Tensor, b_q: torch.Tensor, scale_b: torch.Tensor, o
     qk = _qkind(b_q)
     need = lib.w8a8_quant_scaled_mm_workspace_size(M, N, K, qk)
     if isinstance(workspace, Workspace):
-        workspace = workspace.ensure(need).buf
+        workspace = workspace.ensure(need, stream).buf
     elif workspace is None and need:
-        workspace = _default_workspace(x.device, need, "mm").buf
+        workspace = _default_workspace(x.device, need, "mm", stream).buf
     ws_ptr = _ptr(workspace) if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     check(lib.w8a8_quant_scaled_mm(_ptr(x), _fkind(x), _ld(x), _ptr(b_q), _ld(b_q), _ptr(scale_b), b_gran,
@@ -379,9 +400,9 @@ def fp8_kv_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
         bt = _ptr(block_table)
     need = lib.w8a8_fp8_kv_attention_workspace_size(batch, hq, max_seq)
     if isinstance(workspace, Workspace):
-        wbuf = workspace.ensure(need).buf
+        wbuf = workspace.ensure(need, stream).buf
     elif workspace is None:
-        wbuf = _default_workspace(q.device, need, "attention").buf
+        wbuf = _default_workspace(q.device, need, "attention", stream).buf
     else:
         wbuf = workspace
     if sm_scale is None:
@@ -582,9 +603,9 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, 
         return
     need = _kv4_attention_need(q.get_device(), batch, max_query_len, hq, hkv, d)
     if isinstance(workspace, Workspace):
-        wbuf = workspace.ensure(need).buf
+        wbuf = workspace.ensure(need, stream).buf
     elif workspace is None:
-        wbuf = _default_workspace(q.device, need, "kv4_attention").buf
+        wbuf = _default_workspace(q.device, need, "kv4_attention", stream).buf
     else:
         wbuf = workspace
     if sm_scale is None:

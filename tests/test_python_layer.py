@@ -1,0 +1,161 @@
+"""The Python layer without a GPU: host tensors that say they are CUDA tensors,
+a library that records its calls, and streams that are only handles."""
+import contextlib
+
+import pytest
+import torch
+
+import int8_w8a8_scaled_gb300 as w8
+from int8_w8a8_scaled_gb300 import api
+
+
+class Pretend(torch.Tensor):
+    """A host tensor on "cuda:index"."""
+    index = 0
+    is_cuda = True
+
+    def get_device(self):
+        return self.index
+
+    @property
+    def device(self):
+        return torch.device("cuda", self.index)
+
+    def record_stream(self, stream):
+        World.kept.append((self.data_ptr(), stream.cuda_stream))
+
+
+def pretend(*shape, dtype=torch.int32, index=0):
+    t = torch.zeros(*shape, dtype=dtype).as_subclass(Pretend)
+    t.index = index
+    return t
+
+
+class Stream:
+    def __init__(self, handle, index=0):
+        self.cuda_stream, self.device_index = handle, index
+
+
+class World:
+    """What the fake CUDA saw."""
+    current = 7           # handle of the current stream
+    device = 0            # the current device
+    zeroed = []           # (address, handle of the stream that the zeroing is ordered on)
+    kept = []
+    calls = []            # (name, arguments)
+
+
+class Library:
+    need = 4096
+
+    def __getattr__(self, name):
+        if name.endswith("workspace_size"):
+            return lambda *a: Library.need
+        def call(*a):
+            World.calls.append((name, a))
+            return 0
+        return call
+
+
+@pytest.fixture
+def world(monkeypatch):
+    World.current, World.device, World.zeroed, World.kept, World.calls, Library.need = 7, 0, [], [], [], 4096
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, World.current = World.current, stream.cuda_stream
+        yield
+        World.current = before
+
+    def zeros(n, dtype, device):
+        t = pretend(n, dtype=dtype, index=torch.device(device).index)
+        World.zeroed.append((t.data_ptr(), World.current))
+        return t
+
+    monkeypatch.setattr(api._lib, "load", lambda: Library())
+    monkeypatch.setattr(api, "_default_ws", {})
+    monkeypatch.setattr(api, "_raw_stream", lambda index: World.current)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: World.current, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: World.device, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: World.device)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(World.current))
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    real = torch.zeros
+    monkeypatch.setattr(torch, "zeros", lambda *a, device=None, **kw: real(*a, **kw) if device is None else zeros(*a, device=device, **kw))
+    return World
+
+
+def attend(stream=None, workspace=None, **edit):
+    t = dict(q=pretend(2, 4, 64, dtype=torch.bfloat16), cache=pretend(3, 2, 1, 18 * 64, dtype=torch.uint8), seq_lens=pretend(2),
+             block_table=pretend(2, 5), k_scale=pretend(1, dtype=torch.float32), v_scale=pretend(1, dtype=torch.float32),
+             out=pretend(2, 4, 64, dtype=torch.bfloat16))
+    t.update(edit)
+    w8.kv4_attention(**t, workspace=workspace, stream=stream)
+    return World.calls[-1][1]
+
+
+def attend_fp8(stream=None, workspace=None):
+    e4m3 = lambda *n: pretend(*n, dtype=torch.uint8)  # noqa: E731
+    w8.fp8_kv_decode_attention(pretend(2, 4, 128, dtype=torch.bfloat16), e4m3(2, 9, 2, 128), e4m3(2, 9, 2, 128), pretend(2),
+                               pretend(1, dtype=torch.float32), pretend(1, dtype=torch.float32),
+                               pretend(2, 4, 128, dtype=torch.bfloat16), workspace=workspace, stream=stream)
+    return World.calls[-1][1]
+
+
+def matmul(stream=None, workspace=None):
+    one = pretend(1, dtype=torch.float32)
+    w8.scaled_mm(pretend(4, 32, dtype=torch.int8), pretend(8, 32, dtype=torch.int8), one, one, pretend(4, 8, dtype=torch.float16),
+                 workspace=workspace, stream=stream)
+    return World.calls[-1][1]
+
+
+def quantising_matmul(stream=None, workspace=None):
+    w8.quant_scaled_mm(pretend(4, 32, dtype=torch.bfloat16), pretend(8, 32, dtype=torch.int8), pretend(1, dtype=torch.float32),
+                       pretend(4, 8, dtype=torch.bfloat16), workspace=workspace, stream=stream)
+    return World.calls[-1][1]
+
+
+def quantise(stream=None, workspace=None):
+    w8.scaled_quant(pretend(4, 32, dtype=torch.bfloat16), pretend(4, 32, dtype=torch.int8), pretend(1, dtype=torch.float32),
+                    per_token=False, workspace=workspace, stream=stream)
+    return World.calls[-1][1]
+
+
+CALLS = [attend, attend_fp8, matmul, quantising_matmul, quantise]
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_default_workspaces_go_by_the_stream_that_the_call_runs_on(world, call):
+    """Two explicit streams under one current stream: a buffer each, zeroed on
+    the stream whose kernel reads it, and again the same one the next time."""
+    buffers = {}
+    for handle in (21, 22):
+        args = call(stream=Stream(handle))
+        address, ordered_on = world.zeroed[-1]
+        assert address in args and args[-1] == handle and ordered_on == handle
+        buffers[handle] = address
+    assert len(set(buffers.values())) == 2 and len(world.zeroed) == 2
+    for handle in (22, 21):
+        assert buffers[handle] in call(stream=Stream(handle))
+    world.current = 21
+    assert buffers[21] in call()                 # the same stream, as the current one
+    world.current = 9
+    call()
+    assert len(world.zeroed) == 3 and world.zeroed[-1][1] == 9
+
+
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("own", [False, True])
+def test_a_workspace_grows_on_the_stream_of_the_call(world, call, own):
+    if own and call is quantise:
+        pytest.skip("takes tensors only")
+    ws = w8.Workspace(device="cuda:0") if own else None
+    call(stream=Stream(31), workspace=ws)
+    old = world.zeroed[-1][0]
+    Library.need = 1 << 20
+    api._kv4_attention_need.cache_clear()
+    args = call(stream=Stream(31), workspace=ws)
+    assert world.zeroed[-1][0] in args and world.zeroed[-1][1] == 31
+    assert (old, 31) in world.kept               # not given away while the call before may run
+    api._kv4_attention_need.cache_clear()
