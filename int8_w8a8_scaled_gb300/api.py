@@ -97,23 +97,41 @@ class Workspace:
     It is zeroed on the stream that is current where it is made: a call on
     another stream has to come after that (``wait_stream``).  A buffer that a
     call makes larger is zeroed on that call's stream.
+
+    A buffer that a captured call uses is kept as long as the Workspace, so that
+    the graph can be replayed after the Workspace has grown.  Make it large
+    enough before the capture: a captured call that needs more gets a buffer of
+    the graph's own, which every replay zeroes.  A replay counts as calls on the
+    stream that it runs on: where it may overlap others, give it a Workspace of
+    its own.
     """
 
     def __init__(self, nbytes: int = 0, device=None):
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
         self.buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+        self._captured = []          # buffers that graphs hold the address of
 
     def ensure(self, nbytes: int, stream=None) -> "Workspace":
         """At least nbytes, for a call on `stream` (None: the current one)."""
-        if nbytes > self.buf.numel():
-            with _launching_on(self.device, stream) as launch:
-                self.buf.record_stream(launch)      # earlier calls there may still use it
-                self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        if nbytes <= self.buf.numel():
+            if _capturing() and not (self._captured and self._captured[-1] is self.buf):
+                self._captured.append(self.buf)
+            return self
+        with _launching_on(self.device, stream) as launch:
+            if _capturing():
+                return Workspace(nbytes, self.device)
+            self.buf.record_stream(launch)          # earlier calls there may still use it
+            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
         return self
 
     @property
     def nbytes(self) -> int:
         return self.buf.numel()
+
+
+def _capturing() -> bool:
+    """Whether the current stream is being captured into a graph."""
+    return torch._C._cuda_isCurrentStreamCapturing()
 
 
 @contextlib.contextmanager
@@ -135,16 +153,22 @@ _default_ws: dict = {}
 def _default_workspace(device: torch.device, nbytes: int, kind: str, stream) -> Workspace:
     """Per (device, stream that the call runs on, kind) scratch, zeroed on that
     stream; the matmul's buffer is never shared with the quantiser (whose absmax
-    word would land on a counter)."""
+    word would land on a counter).  Scratch first made during a capture belongs to
+    the graph, whose replay zeroes it, and is not kept: before that replay it
+    holds anything."""
     key = (kind, device.index, _raw_stream(device.index) if stream is None else stream.cuda_stream)
     ws = _default_ws.get(key)
-    if ws is not None and ws.buf.numel() >= nbytes:
-        return ws
+    if ws is None:
+        with _ws_lock, _launching_on(device, stream):
+            ws = _default_ws.get(key)
+            if ws is None:
+                ws = Workspace(nbytes, device)
+                if not _capturing():
+                    _default_ws[key] = ws
+                return ws
+    if ws.buf.numel() >= nbytes:
+        return ws.ensure(nbytes, stream)
     with _ws_lock:
-        ws = _default_ws.get(key)
-        if ws is None:
-            with _launching_on(device, stream):
-                ws = _default_ws[key] = Workspace(nbytes, device)
         return ws.ensure(nbytes, stream)
 
 

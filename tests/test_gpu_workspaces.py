@@ -75,3 +75,53 @@ def test_two_explicit_streams_with_default_workspaces(problem, no_workspaces):
     for want, out in zip(wants, outs):
         assert all(torch.equal(o, want) for o in out)
     assert w8.device_status() == 0
+
+
+@pytest.mark.parametrize("problem", PROBLEMS)
+def test_graphs_captured_without_a_workspace(problem, no_workspaces):
+    """Two graphs, captured one after the other with no call before them, and the
+    second one replayed first, with calls outside between."""
+    (first, like), (second, _) = (PROBLEMS[problem](seed) for seed in (1, 2))
+    outs = [torch.empty_like(like) for _ in range(4)]
+    graphs = []
+    for call, out in zip((first, second), outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call(out)
+            call(out)
+    with torch.cuda.stream(torch.cuda.graph.default_capture_stream):
+        second(outs[3])
+    torch.cuda.synchronize()
+    second(outs[2])
+    torch.cuda.synchronize()
+    assert torch.equal(outs[2], outs[3])
+    for _ in range(3):
+        outs[1].fill_(0)
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[1], outs[2])
+    first(outs[2])
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[2])
+
+
+def test_a_graph_outlives_the_growth_of_its_default_workspace(no_workspaces):
+    call, like = attention_problem(1, 3)
+    large, like_large = attention_problem(60, 4)
+    out, want = torch.empty_like(like), torch.empty_like(like)
+    call(want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    call(out, stream=s)                                 # the stream's workspace, made before the capture
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        call(out)
+    with torch.cuda.stream(s):
+        large(torch.empty_like(like_large))             # it grows
+        junk = torch.full((1 << 26,), 0xFF, dtype=torch.uint8, device="cuda")
+        for _ in range(3):
+            out.fill_(0)
+            g.replay()
+            assert torch.equal(out, want)
+        assert (junk == 0xFF).all()

@@ -39,6 +39,7 @@ class Stream:
 class World:
     """What the fake CUDA saw."""
     current = 7           # handle of the current stream
+    captured = set()      # handles of the streams under capture
     device = 0            # the current device
     zeroed = []           # (address, handle of the stream that the zeroing is ordered on)
     kept = []
@@ -59,7 +60,7 @@ class Library:
 
 @pytest.fixture
 def world(monkeypatch):
-    World.current, World.device, World.zeroed, World.kept, World.calls, Library.need = 7, 0, [], [], [], 4096
+    World.current, World.device, World.zeroed, World.kept, World.calls, World.captured, Library.need = 7, 0, [], [], [], set(), 4096
 
     @contextlib.contextmanager
     def on(stream):
@@ -76,6 +77,7 @@ def world(monkeypatch):
     monkeypatch.setattr(api, "_default_ws", {})
     monkeypatch.setattr(api, "_raw_stream", lambda index: World.current)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: World.current, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: World.current in World.captured, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: World.device, raising=False)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: World.device)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(World.current))
@@ -158,4 +160,46 @@ def test_a_workspace_grows_on_the_stream_of_the_call(world, call, own):
     args = call(stream=Stream(31), workspace=ws)
     assert world.zeroed[-1][0] in args and world.zeroed[-1][1] == 31
     assert (old, 31) in world.kept               # not given away while the call before may run
+    api._kv4_attention_need.cache_clear()
+
+
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("explicit", [False, True])
+def test_scratch_first_made_in_a_capture_is_the_graphs_own(world, call, explicit):
+    """Its zeros come with that graph's replay alone: another graph, or a call
+    outside, gets a buffer of its own."""
+    world.current = 7 if explicit else 41
+    stream = Stream(41) if explicit else None
+    world.captured = {41}
+    call(stream=stream)
+    call(stream=stream)
+    assert [on for _, on in world.zeroed] == [41, 41]
+    world.captured = set()
+    args = call(stream=stream)
+    assert len(world.zeroed) == 3 and world.zeroed[2][0] in args
+    call(stream=stream)
+    assert len(world.zeroed) == 3
+
+
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("own", [False, True])
+def test_a_captured_buffer_outlives_growth(world, call, own):
+    if own and call is quantise:
+        pytest.skip("takes tensors only")
+    world.current = 51
+    ws = w8.Workspace(4096, device="cuda:0") if own else None
+    call(workspace=ws)
+    keeper = ws if own else next(iter(api._default_ws.values()))
+    first = keeper.buf
+    world.captured = {51}
+    assert first.data_ptr() in call(workspace=ws)            # the graph has its address
+    call(workspace=ws)
+    Library.need = 1 << 20
+    api._kv4_attention_need.cache_clear()
+    args = call(workspace=ws)                                # too small: the graph's own, zeroed by it
+    assert world.zeroed[-1][0] in args and keeper.buf is first
+    world.captured = set()
+    args = call(workspace=ws)
+    assert keeper.buf is not first and keeper.buf.data_ptr() in args
+    assert [b is first for b in keeper._captured] == [True]
     api._kv4_attention_need.cache_clear()
