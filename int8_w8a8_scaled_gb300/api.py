@@ -69,9 +69,14 @@ def _ld(t: torch.Tensor) -> int:
 
 
 def _cuda(*ts):
-    for t in ts:
-        if t is not None and not t.is_cuda:
-            raise ValueError("all tensors must be CUDA tensors")
+    """Refuses tensors that are not on the current device, where the library launches."""
+    devices = {t.get_device() for t in ts if t is not None}
+    if -1 in devices:
+        raise ValueError("all tensors must be CUDA tensors")
+    if len(devices) > 1:
+        raise ValueError("all tensors must be on one device")
+    if devices and torch._C._cuda_getDevice() not in devices:
+        raise ValueError(f"the tensors are on cuda:{devices.pop()}, which is not the current device")
 
 
 def _ptr(t):
@@ -84,9 +89,12 @@ def _raw_stream(device_index: int) -> int:
 
 
 def _stream(stream):
-    if stream is not None:
-        return stream.cuda_stream
-    return _raw_stream(torch.cuda.current_device())
+    """The given stream, or the current one of the current device."""
+    if stream is None:
+        return _raw_stream(torch._C._cuda_getDevice())
+    if getattr(stream, "device_index", None) not in (None, torch._C._cuda_getDevice()):
+        raise ValueError("the stream belongs to another device than the tensors")
+    return stream.cuda_stream
 
 
 class Workspace:
@@ -158,6 +166,8 @@ def _default_workspace(device: torch.device, nbytes: int, kind: str, stream) -> 
     holds anything."""
     key = (kind, device.index, _raw_stream(device.index) if stream is None else stream.cuda_stream)
     ws = _default_ws.get(key)
+    if ws is not None and ws.buf.numel() >= nbytes and not _capturing():
+        return ws
     if ws is None:
         with _ws_lock, _launching_on(device, stream):
             ws = _default_ws.get(key)
@@ -166,8 +176,6 @@ def _default_workspace(device: torch.device, nbytes: int, kind: str, stream) -> 
                 if not _capturing():
                     _default_ws[key] = ws
                 return ws
-    if ws.buf.numel() >= nbytes:
-        return ws.ensure(nbytes, stream)
     with _ws_lock:
         return ws.ensure(nbytes, stream)
 
@@ -280,6 +288,7 @@ def scaled_mm(a_q: torch.Tensor, b_q: torch.Tensor, scale_a: torch.Tensor, scale
         workspace = workspace.ensure(need, stream).buf
     elif workspace is None and need:
         workspace = _default_workspace(a_q.device, need, "mm", stream).buf
+    _cuda(a_q, workspace)
     ws_ptr = _ptr(workspace) if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     args = (_ptr(a_q), _ld(a_q), _ptr(b_q), _ld(b_q), _ptr(scale_a), a_gran, _ptr(scale_b), b_gran,
@@ -318,7 +327,7 @@ def quant_scaled_mm(x: torch.Tensor, b_q: torch.Tensor, scale_b: torch.Tensor, o
     if b_gran == PER_TENSOR and scale_b.numel() != 1:
         raise ValueError("scale_b must have 1 or N elements")
     if scale_a_out is not None:
-        _cuda(scale_a_out)
+        _cuda(x, scale_a_out)
         if scale_a_out.dtype != torch.float32 or scale_a_out.numel() != M or not scale_a_out.is_contiguous():
             raise ValueError("scale_a_out must be a contiguous float32 tensor of M elements")
     qk = _qkind(b_q)
@@ -327,6 +336,7 @@ def quant_scaled_mm(x: torch.Tensor, b_q: torch.Tensor, scale_b: torch.Tensor, o
         workspace = workspace.ensure(need, stream).buf
     elif workspace is None and need:
         workspace = _default_workspace(x.device, need, "mm", stream).buf
+    _cuda(x, workspace)
     ws_ptr = _ptr(workspace) if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     check(lib.w8a8_quant_scaled_mm(_ptr(x), _fkind(x), _ld(x), _ptr(b_q), _ld(b_q), _ptr(scale_b), b_gran,
@@ -417,7 +427,7 @@ def fp8_kv_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
         if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != batch \
                 or not block_table.is_contiguous():
             raise ValueError("block_table must be a contiguous int32 [batch, max_blocks] tensor")
-        _cuda(block_table)
+        _cuda(q, block_table)
         nblk, bsz = k_cache.shape[0], k_cache.shape[1]
         maxb = block_table.shape[1]
         max_seq = maxb * bsz
@@ -429,6 +439,8 @@ def fp8_kv_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
         wbuf = _default_workspace(q.device, need, "attention", stream).buf
     else:
         wbuf = workspace
+    if workspace is not None:
+        _cuda(q, wbuf)
     if sm_scale is None:
         sm_scale = 1.0 / float(d) ** 0.5
     check(lib.w8a8_fp8_kv_decode_attention(
@@ -456,8 +468,6 @@ def _kv4_cache(cache: torch.Tensor) -> tuple:
     nb, h, records, nbytes = cache.shape
     if nbytes % 18:
         raise ValueError("the cache must be a contiguous uint8 CUDA tensor of kv4_cache_shape()")
-    if not cache.is_cuda:
-        raise ValueError("all tensors must be CUDA tensors")
     return nb, h, 16 * records, nbytes // 18
 
 
@@ -468,26 +478,17 @@ def _kv4_kind(kind: str) -> int:
 
 
 def _vectors(checks, dtype) -> None:
-    """Refuses what is not a contiguous CUDA tensor of `dtype` with n elements,
-    for (name, tensor, n) in `checks`."""
+    """Refuses what is not a contiguous tensor of `dtype` with n elements, for
+    (name, tensor, n) in `checks`."""
     for name, t, n in checks:
         if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} vector of {n} entries")
-        if not t.is_cuda:
-            raise ValueError("all tensors must be CUDA tensors")
-
-
-def _stream_on(t: torch.Tensor, stream):
-    """The given stream, or the current one of the tensor's device."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 def _one_scale(*ts: torch.Tensor) -> None:
     for t in ts:
         if t.dtype is not torch.float32 or t.numel() != 1:
             raise ValueError("k_scale and v_scale must be float32 tensors of one element")
-        if not t.is_cuda:
-            raise ValueError("all tensors must be CUDA tensors")
 
 
 def _heads(name: str, t: torch.Tensor, shape: tuple) -> tuple:
@@ -497,8 +498,6 @@ def _heads(name: str, t: torch.Tensor, shape: tuple) -> tuple:
     token, head, dim = t.stride()
     if dim != 1:
         raise ValueError(f"the dims of a head of {name} must be consecutive (stride(2) == 1)")
-    if not t.is_cuda:
-        raise ValueError("all tensors must be CUDA tensors")
     return token, head
 
 
@@ -513,6 +512,7 @@ def _kv4_tokens(k, v, cache, slots, k_scale, v_scale, kind) -> tuple:
         raise TypeError("k and v must have the same element type")
     _vectors((("slots", slots, n),), torch.int64)
     _one_scale(k_scale, v_scale)
+    _cuda(k, v, cache, slots, k_scale, v_scale)
     return nb, bs, (_fkind(k), n, h, d, *ks, *vs), _kv4_kind(kind)
 
 
@@ -531,7 +531,7 @@ def kv4_cache_write(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, slots
         return
     check(_lib.load().w8a8_kv4_cache_write(
         k.data_ptr(), v.data_ptr(), *sizes, cache.data_ptr(), nb, bs, slots.data_ptr(), k_scale.data_ptr(),
-        v_scale.data_ptr(), kd, _stream_on(cache, stream)))
+        v_scale.data_ptr(), kd, _stream(stream)))
 
 
 def kv4_cache_read(cache: torch.Tensor, slots: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
@@ -544,7 +544,7 @@ def kv4_cache_read(cache: torch.Tensor, slots: torch.Tensor, k_scale: torch.Tens
         return
     check(_lib.load().w8a8_kv4_cache_read(
         cache.data_ptr(), nb, bs, slots.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), kd, k.data_ptr(),
-        v.data_ptr(), *sizes, _stream_on(cache, stream)))
+        v.data_ptr(), *sizes, _stream(stream)))
 
 
 def build_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_blocks: torch.Tensor,
@@ -575,11 +575,12 @@ def build_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_
     _vectors((("slots", slots, tokens),), torch.int64)
     if free_count_out is not None:
         _vectors((("free_count_out", free_count_out, 1),), torch.int32)
-    _cuda(block_table)
+    _cuda(context_lens, new_lens, free_blocks, free_count, block_table, query_start, seq_lens, slots, positions, free_left,
+          free_count_out)
     check(_lib.load().w8a8_build_block_tables(
         context_lens.data_ptr(), new_lens.data_ptr(), batch, free_blocks.data_ptr(), free_count.data_ptr(), ids,
         block_table.data_ptr(), max_blocks, block_size, query_start.data_ptr(), seq_lens.data_ptr(), slots.data_ptr(),
-        positions.data_ptr(), tokens, free_left.data_ptr(), _ptr(free_count_out), _stream_on(block_table, stream)))
+        positions.data_ptr(), tokens, free_left.data_ptr(), _ptr(free_count_out), _stream(stream)))
 
 
 def kv4_attention_workspace_size(batch: int, max_query_len: int, num_q_heads: int, num_kv_heads: int,
@@ -621,7 +622,7 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, 
     else:
         _vectors((("seq_lens", seq_lens, batch), ("query_start", query_start, batch + 1)), torch.int32)
     _one_scale(k_scale, v_scale)
-    _cuda(block_table)
+    _cuda(q, cache, seq_lens, block_table, k_scale, v_scale, out, query_start)
     kd = _kv4_kind(kind)
     if tokens == 0:
         return
@@ -632,12 +633,14 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, 
         wbuf = _default_workspace(q.device, need, "kv4_attention", stream).buf
     else:
         wbuf = workspace
+    if workspace is not None:
+        _cuda(q, wbuf)
     if sm_scale is None:
         sm_scale = 1.0 / float(d) ** 0.5
     check(_lib.load().w8a8_kv4_attention(
         q.data_ptr(), _fkind(q), tokens, hq, hkv, d, *qs, cache.data_ptr(), nb, bs, block_table.data_ptr(), max_blocks,
         seq_lens.data_ptr(), _ptr(query_start), batch, max_query_len, k_scale.data_ptr(), v_scale.data_ptr(), sm_scale, kd,
-        out.data_ptr(), _fkind(out), *os_, wbuf.data_ptr(), wbuf.numel() * wbuf.element_size(), _stream_on(q, stream)))
+        out.data_ptr(), _fkind(out), *os_, wbuf.data_ptr(), wbuf.numel() * wbuf.element_size(), _stream(stream)))
 
 
 def verify_drafts(target_probs: torch.Tensor, draft_probs: torch.Tensor | None, draft_tokens: torch.Tensor,
@@ -669,10 +672,10 @@ def verify_drafts(target_probs: torch.Tensor, draft_probs: torch.Tensor | None, 
     _vectors((("draft_tokens", draft_tokens, rows), ("draft_start", draft_start, batch + 1),
               ("num_accepted", num_accepted, batch)), torch.int32)
     _vectors((("uniform", uniform, rows), ("sample_uniform", sample_uniform, batch)), torch.float32)
-    _cuda(target_probs, draft_probs, out_tokens)
+    _cuda(target_probs, draft_probs, draft_tokens, draft_start, uniform, sample_uniform, out_tokens, num_accepted)
     check(_lib.load().w8a8_verify_drafts(
         target_probs.data_ptr(), _ptr(draft_probs),
         FP32 if target_probs.dtype is torch.float32 else _fkind(target_probs), vocab, _ld(target_probs),
         vocab if draft_probs is None else _ld(draft_probs), draft_tokens.data_ptr(), draft_start.data_ptr(), batch, rows,
         uniform.data_ptr(), sample_uniform.data_ptr(), out_tokens.data_ptr(), columns - 1, num_accepted.data_ptr(),
-        _stream_on(target_probs, stream)))
+        _stream(stream)))

@@ -203,3 +203,72 @@ def test_a_captured_buffer_outlives_growth(world, call, own):
     assert keeper.buf is not first and keeper.buf.data_ptr() in args
     assert [b is first for b in keeper._captured] == [True]
     api._kv4_attention_need.cache_clear()
+
+
+def f32(*n, index=0):
+    return pretend(*n, dtype=torch.float32, index=index)
+
+
+def i8(*n, index=0):
+    return pretend(*n, dtype=torch.int8, index=index)
+
+
+def b16(*n, index=0):
+    return pretend(*n, dtype=torch.bfloat16, index=index)
+
+
+def i64(*n, index=0):
+    return pretend(*n, dtype=torch.int64, index=index)
+
+
+def u8(*n, index=0):
+    return pretend(*n, dtype=torch.uint8, index=index)
+
+
+# every entry point with its tensors as (maker, shape); the last positions of some are workspaces
+ENTRIES = {
+    "scaled_quant": (lambda x, q, s, w: w8.scaled_quant(x, q, s, per_token=False, workspace=w),
+                     [(b16, (4, 32)), (i8, (4, 32)), (f32, (1,)), (u8, (4096,))]),
+    "scaled_dequant": (w8.scaled_dequant, [(i8, (4, 32)), (f32, (1,)), (b16, (4, 32))]),
+    "scaled_mm": (w8.scaled_mm, [(i8, (4, 32)), (i8, (8, 32)), (f32, (4,)), (f32, (8,)), (b16, (4, 8)), (u8, (4096,))]),
+    "quant_scaled_mm": (w8.quant_scaled_mm, [(b16, (4, 32)), (i8, (8, 32)), (f32, (8,)), (b16, (4, 8)), (f32, (4,)), (u8, (4096,))]),
+    "expand_shard_scales": (lambda s, b: w8.expand_shard_scales(s, [2, 3], b), [(f32, (2,)), (f32, (5,))]),
+    "requant_shards": (lambda q, s, o, t: w8.requant_shards(q, s, [2, 2], o, t), [(i8, (4, 32)), (f32, (2,)), (i8, (4, 32)), (f32, (1,))]),
+    "fp8_kv_decode_attention": (lambda q, k, v, n, ks, vs, o, t, w: w8.fp8_kv_decode_attention(q, k, v, n, ks, vs, o, block_table=t, workspace=w),
+                                [(b16, (2, 4, 128)), (u8, (9, 16, 2, 128)), (u8, (9, 16, 2, 128)), (pretend, (2,)), (f32, (1,)),
+                                 (f32, (1,)), (b16, (2, 4, 128)), (pretend, (2, 5)), (u8, (4096,))]),
+    "kv4_cache_write": (w8.kv4_cache_write, [(b16, (3, 2, 64)), (b16, (3, 2, 64)), (u8, (3, 2, 1, 1152)), (i64, (3,)), (f32, (1,)), (f32, (1,))]),
+    "kv4_cache_read": (w8.kv4_cache_read, [(u8, (3, 2, 1, 1152)), (i64, (3,)), (f32, (1,)), (f32, (1,)), (b16, (3, 2, 64)), (b16, (3, 2, 64))]),
+    "build_block_tables": (lambda c, n, f, k, t, *rest: w8.build_block_tables(c, n, f, k, t, 16, *rest),
+                           [(pretend, (2,)), (pretend, (2,)), (pretend, (9,)), (pretend, (1,)), (pretend, (2, 5)), (pretend, (3,)),
+                            (pretend, (2,)), (i64, (4,)), (pretend, (4,)), (pretend, (1,)), (pretend, (1,))]),
+    "kv4_attention": (lambda q, c, n, t, ks, vs, o, s, w: w8.kv4_attention(q, c, n, t, ks, vs, o, query_start=s, workspace=w),
+                      [(b16, (2, 4, 64)), (u8, (3, 2, 1, 1152)), (pretend, (2,)), (pretend, (2, 5)), (f32, (1,)), (f32, (1,)),
+                       (b16, (2, 4, 64)), (pretend, (3,)), (u8, (4096,))]),
+    "verify_drafts": (w8.verify_drafts, [(f32, (5, 9)), (f32, (3, 9)), (pretend, (3,)), (pretend, (3,)), (f32, (3,)), (f32, (2,)),
+                                         (pretend, (2, 4)), (pretend, (2,))]),
+}
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+def test_every_tensor_has_to_be_on_the_current_device(world, entry):
+    call, tensors = ENTRIES[entry]
+    make = lambda at, index: [m(*n, index=index if i == at or at is None else 0) for i, (m, n) in enumerate(tensors)]  # noqa: E731
+    call(*make(None, 0))
+    assert len(world.calls) == 1
+    for i in range(len(tensors)):
+        with pytest.raises(ValueError, match="one device"):
+            call(*make(i, 1))
+    with pytest.raises(ValueError, match="current device"):
+        call(*make(None, 1))
+    assert len(world.calls) == 1                              # nothing was launched
+    world.device = 1
+    call(*make(None, 1))
+    assert len(world.calls) == 2
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_a_stream_has_to_be_of_the_current_device(world, call):
+    with pytest.raises(ValueError, match="stream"):
+        call(stream=Stream(61, index=1))
+    assert not world.calls
