@@ -363,7 +363,10 @@ cudaError_t launch_kv4_cache(const Kv4CacheArgs& args, bool write, cudaStream_t 
 
 cudaError_t launch_block_tables(const BlockTableArgs& a, int num_sms, cudaStream_t stream) {
   const int smem = static_cast<int>((2LL * a.batch + 1) * sizeof(int));
-  cudaError_t e = cudaFuncSetAttribute(block_table_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the attribute belongs to the function, for all host threads: always the
+  // largest batch's, so that no thread lowers it in front of another's launch
+  constexpr int kMost = static_cast<int>((2LL * kMaxTableBatch + 1) * sizeof(int));
+  cudaError_t e = cudaFuncSetAttribute(block_table_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
   if (e != cudaSuccess) return e;
   long long grid = (a.tokens + kTableThreads - 1) / kTableThreads;
   if (grid > 2LL * num_sms) grid = 2LL * num_sms;

@@ -1,0 +1,43 @@
+"""Calls from several host threads at once: what a launcher sets on a kernel for
+one thread's sizes may not take another's launch away."""
+import threading
+
+import pytest
+import torch
+
+import int8_w8a8_scaled_gb300 as w8
+
+pytestmark = pytest.mark.gpu
+
+
+def at_once(*calls, times=2000):
+    """Each call repeated by a thread of its own, all starting together."""
+    errors, gate = [], threading.Barrier(len(calls))
+
+    def work(call):
+        try:
+            gate.wait()
+            for _ in range(times):
+                call()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+
+
+def tables(batch):
+    ints = lambda *n, fill=0: torch.full(n, fill, dtype=torch.int32, device="cuda")  # noqa: E731
+    ctx, new, free = ints(batch, fill=3), ints(batch, fill=1), torch.arange(batch + 5, dtype=torch.int32, device="cuda")
+    out = (ints(batch, 4, fill=-1), 16, ints(batch + 1), ints(batch), torch.zeros(batch, dtype=torch.int64, device="cuda"), ints(batch), ints(1))
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    return lambda: w8.build_block_tables(ctx, new, free, free[-1:], *out, stream=stream)
+
+
+def test_block_tables_of_small_and_large_batches():
+    at_once(tables(8), tables(1000), tables(12000))
