@@ -41,3 +41,10 @@ def tables(batch):
 
 def test_block_tables_of_small_and_large_batches():
     at_once(tables(8), tables(1000), tables(12000))
+
+
+def test_a_thread_whose_first_cuda_call_is_a_matmul():
+    a, b = (torch.full((n, 512), 0x38, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for n in (256, 128))
+    one, out = torch.ones(1, device="cuda"), torch.empty(256, 128, dtype=torch.bfloat16, device="cuda")
+    at_once(lambda: w8.scaled_mm(a, b, one, one, out), times=1)
+    assert (out == 512).all()
