@@ -1075,8 +1075,11 @@ cudaError_t launch_one(const CUtensorMap& tp, const CUtensorMap& tq, const MmPar
   const int tmem_occ = 512 / tmem_cols_for(BN, INT8);
   const int fixed = static_cast<int>(fa.sharedSizeBytes) + reserved;
   if (smem_sm / (smem + fixed) > tmem_occ) smem = ((smem_sm / (tmem_occ + 1) + 1 - fixed) + 1023) & ~1023;
-  // the attribute is per function and device; setting it again is harmless
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the attribute is the function's, for all host threads: always all that a
+  // block may have, so that no thread lowers it in front of another's launch
+  int most = 0;
+  if ((e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most - static_cast<int>(fa.sharedSizeBytes));
   if (e != cudaSuccess) return e;
   // all of the unified L1/shared storage as shared memory, so that two
   // CTAs of the narrow (decode) configurations fit on one SM

@@ -527,7 +527,15 @@ cudaError_t launch_pair_t(const CUtensorMap& ta, const CUtensorMap& tb, const Mm
                           cudaStream_t stream) {
   auto kern = w8a8_gemm_pair_kernel<BN, INT8, OutT>;
   const int smem = stages * (kPBytes + (BN / 2) * kRowBytes) + 1024 + kBarBlockBytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the attribute is the function's, for all host threads: always all that a
+  // block may have, so that no thread lowers it in front of another's launch
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  int dev = 0, most = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most - static_cast<int>(fa.sharedSizeBytes));
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   if (e != cudaSuccess) return e;

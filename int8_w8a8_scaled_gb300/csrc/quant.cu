@@ -753,7 +753,8 @@ cudaError_t launch_rows(const QuantArgs& a, cudaStream_t st) {
     const size_t smem = static_cast<size_t>(a.cols) * 2;
     auto kern = quant_row_bulk_kernel<XK, QK>;
     if (smem > 48 * 1024) {
-      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      // for all host threads: the longest row's, never less than another's launch needs
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kBulkRowMaxCols * 2));
       if (e != cudaSuccess) return e;
     }
     return launch_pdl_smem(kern, grid, block, smem, st, x, a.ld_x, a.cols, q, a.ld_q, a.scale, a.per_row, a.dynamic);

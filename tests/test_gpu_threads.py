@@ -48,3 +48,24 @@ def test_a_thread_whose_first_cuda_call_is_a_matmul():
     one, out = torch.ones(1, device="cuda"), torch.empty(256, 128, dtype=torch.bfloat16, device="cuda")
     at_once(lambda: w8.scaled_mm(a, b, one, one, out), times=1)
     assert (out == 512).all()
+
+
+def rows_of(cols):
+    x = torch.randn(3, cols, device="cuda").bfloat16()
+    q, s = torch.empty(3, cols, dtype=torch.int8, device="cuda"), torch.empty(3, device="cuda")
+    return lambda: w8.scaled_quant(x, q, s)
+
+
+def test_quantisers_of_shorter_and_longer_rows():
+    at_once(rows_of(30000), rows_of(65536))
+
+
+def product(stages):
+    a, b = (torch.zeros(n, 512, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for n in (256, 128))
+    one, out = torch.ones(1, device="cuda"), torch.empty(256, 128, dtype=torch.bfloat16, device="cuda")
+    cfg = {"swap_ab": 0, "block_n": 64, "split_k": 1, "stages": stages}
+    return lambda: w8.scaled_mm(a, b, one, one, out, config=cfg)
+
+
+def test_matmuls_with_fewer_and_more_stages():
+    at_once(product(3), product(0))
