@@ -483,7 +483,8 @@ W8A8_API w8a8_status w8a8_build_block_tables(const int32_t* context_lens, const 
  * q; row i of its n sees the tokens t <= seq_lens[b] - n + i:
  *   s_t = sm_scale * sum_d q[i,h,d] K[t,d],  out[i,h,:] = sum_t softmax(s)_t V[t,:]
  * for every query head h, KV head h / (num_q_heads / num_kv_heads).  A row
- * that sees no token gives zeros.
+ * that sees no token gives zeros; a NaN or an infinity in q[i,h,:] stays in
+ * that row's results.
  *   q, out      [tokens, num_q_heads, head_dim] bf16 / fp16, a head's dims
  *               consecutive, token and head strides in elements.
  *   block_table int32 [batch, max_blocks]; tokens of a block whose id is

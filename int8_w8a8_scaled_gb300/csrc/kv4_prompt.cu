@@ -609,17 +609,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         tc_fence_after();
         float a0 = 1.f, a1 = 0.f;  // this slot's factor, the other's
         l = s_l[slot][0][row] + s_l[slot][1][row];
-        float ms = l > 0.f ? m * cs : -INFINITY;
+        // a sum of 0: nothing seen.  A NaN goes on into the row's results
+        float ms = l != 0.f ? m * cs : -INFINITY;
         if (!old.pair && slot == 0) {
-          const float l1 = s_l[1][0][row] + s_l[1][1][row], m1 = l1 > 0.f ? s_m[row] : -INFINITY;
+          const float l1 = s_l[1][0][row] + s_l[1][1][row], m1 = l1 != 0.f ? s_m[row] : -INFINITY;
           const float mn = fmaxf(ms, m1);
-          a0 = l > 0.f ? ex2_fast(ms - mn) : 0.f;
-          a1 = l1 > 0.f ? ex2_fast(m1 - mn) : 0.f;
+          a0 = l != 0.f ? ex2_fast(ms - mn) : 0.f;
+          a1 = l1 != 0.f ? ex2_fast(m1 - mn) : 0.f;
           ms = mn;
           l = a0 * l + a1 * l1;
         }
         if (old.pair || slot == 0) {
-          const float inv = l > 0.f ? vscale / l : 0.f;
+          const float inv = l != 0.f ? vscale / l : 0.f;
           const int prow = row + (old.pair ? slot * kTileRows : 0), r = old.row0 + prow;
           const bool real_row = r < old.rows;
           const size_t to = real_row ? out_at(p, old.first, old.kvh, r) + half * (D / 2) : 0;
@@ -632,13 +633,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             tmem_ld_wait();
             tmem_loaded(o);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = l > 0.f ? __uint_as_float(o[i]) * a0 : 0.f;
+            for (int i = 0; i < 16; ++i) y[i] = l != 0.f ? __uint_as_float(o[i]) * a0 : 0.f;
             if (old.both) {
               tmem_ld16(o_cols + D + 16 * c, o);
               tmem_ld_wait();
               tmem_loaded(o);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) y[i] = l > 0.f ? fmaf(__uint_as_float(o[i]), a1, y[i]) : 0.f;
+              for (int i = 0; i < 16; ++i) y[i] = l != 0.f ? fmaf(__uint_as_float(o[i]), a1, y[i]) : 0.f;
             }
             if (!old.whole) {
 #pragma unroll
@@ -848,9 +849,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     for (int k = 0; k < parts; ++k) {
       const float* s = src + (k ? 2 * k : 1) * static_cast<size_t>(C::kPart) + kUnitRows * D + row;
       const float lk = __ldcg(s + kUnitRows);
-      if (lk > 0.f) l = fmaf(ex2_fast(__ldcg(s) - m), lk, l);
+      if (lk != 0.f) l = fmaf(ex2_fast(__ldcg(s) - m), lk, l);
     }
-    const float inv = l > 0.f ? __ldg(p.v_scale) / l : 0.f;
+    const float inv = l != 0.f ? __ldg(p.v_scale) / l : 0.f;
     const size_t to = out_at(p, u.first, u.kvh, my);
 #pragma unroll 1
     for (int q = tid / kUnitRows; q < D / 8; q += kSoftmaxThreads / kUnitRows) {

@@ -44,7 +44,8 @@ def decoded(records, at, kind):
 
 
 def reference(q, cache, lens, news, table, kg, vg, sm, kind):
-    """(out, r, B, sum |V|) in 64 bits, of every row of q."""
+    """(out, r, B, sum |V|) in 64 bits of every row of q, NaN for a row that sees
+    a score of NaN or +infinity."""
     h, d, bs = cache.shape[1], q.shape[2], 16 * cache.shape[2]
     share, first = q.shape[1] // h, 0
     out, r, total = (torch.zeros(q.shape, dtype=torch.float64, device="cuda") for _ in range(3))
@@ -58,9 +59,10 @@ def reference(q, cache, lens, news, table, kg, vg, sm, kind):
             k, v = decoded(records, 0, kind)[:length] * kg, decoded(records, 9 * d, kind)[:length] * vg
             x = q[first:first + n, j * share:(j + 1) * share].double().transpose(0, 1)      # [share, n, d]
             s = (x @ k.T * sm).masked_fill(~seen, -np.inf)
+            lost = (s.isnan() | (s == np.inf)).any(2, keepdim=True)
             w = torch.nan_to_num(torch.softmax(s, 2))                                       # rows that see nothing: zeros
             at = slice(j * share, (j + 1) * share)
-            out[first:first + n, at] = (w @ v).transpose(0, 1)
+            out[first:first + n, at] = (w @ v).masked_fill(lost, np.nan).transpose(0, 1)
             r[first:first + n, at] = (w @ v.abs()).transpose(0, 1)
             total[first:first + n, at] = (seen.double() @ v.abs()).transpose(0, 1).expand(n, share, d)
             big[first:first + n, at] = ((x.abs() @ k.abs().T) * abs(sm)).masked_fill(~seen, 0.0).amax(2).T
@@ -74,17 +76,18 @@ def close(got, want, lens):
     tiles = -(-int(max(lens)) // 16)
     tol = (half * ref.abs() + r * (2.0 ** -10 + 2.0 ** -18 + tiles * 2.0 ** -23 + 2 * (d + 8) * 2.0 ** -24 * big[..., None]) +
            2.0 ** -38 * total + torch.finfo(got.dtype).smallest_normal * half)
-    assert torch.isfinite(got).all()
-    over = (got.double() - ref).abs() - tol
+    lost = ref.isnan()
+    assert torch.equal(got.isnan(), lost) and torch.isfinite(got[~lost]).all()
+    over = torch.where(lost, 0.0, (got.double() - ref).abs() - tol)
     assert (over <= 0).all(), f"{int((over > 0).sum())} of {over.numel()} outside"
 
 
-def serve(lens, news, hq, hkv, d, kind, dtype, bs=32, seed=0, rise=None, loud=None):
+def serve(lens, news, hq, hkv, d, kind, dtype, bs=32, seed=0, rise=None, loud=None, spoil=None):
     """One call over requests of these lengths, compared with 64 bits.
 
     rise: requests (a slice) whose keys point along their queries, further the
     later the token, so that the maximum goes up to the end.  loud: the queries'
-    scale for each packed token and head."""
+    scale for each packed token and head.  spoil: changes the query in place."""
     lens, news = np.asarray(lens), np.asarray(news)
     rng = np.random.default_rng(seed)
     gen = torch.Generator(device="cuda").manual_seed(seed)
@@ -103,6 +106,8 @@ def serve(lens, news, hq, hkv, d, kind, dtype, bs=32, seed=0, rise=None, loud=No
     if loud is not None:
         q *= loud
     q, k, v = q.to(dtype), k.to(dtype), v.to(dtype)
+    if spoil is not None:
+        spoil(q)
     kg, vg = 0.0151, 0.0173
     cache = torch.zeros(w8.kv4_cache_shape(nb, hkv, bs, d), dtype=torch.uint8, device="cuda")
     scales = dev(np.float32([kg])), dev(np.float32([vg]))
@@ -114,6 +119,7 @@ def serve(lens, news, hq, hkv, d, kind, dtype, bs=32, seed=0, rise=None, loud=No
     assert w8.device_status() == 0
     sm = 1.0 / d ** 0.5
     close(out, reference(q, cache, lens, news, table, float(np.float32(kg)), float(np.float32(vg)), sm, kind), lens)
+    return out
 
 
 def sms():
@@ -131,3 +137,21 @@ def test_units_of_one_tile_whose_queries_differ_in_size(d, kind):
     loud = 2.0 ** rng.integers(-6, 7, (len(news), 8)).repeat(2, 1).repeat(news, 0)
     for seed in range(3):
         serve(news, news, 16, 8, d, kind, torch.bfloat16, seed=seed, loud=dev(loud[..., None]).float())
+
+
+@pytest.mark.parametrize("kind", ["e2m1", "int4"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,hq", [(1, 4), (3, 4), (5, 8), (40, 4), (40, 16), (300, 8)])
+def test_a_query_with_nan_or_infinity_is_seen_in_its_own_row(new, hq, d, kind):
+    """NaN for that token and head, whichever kernel the number of rows picks, and
+    nothing of it in the others; nothing at all where a row sees no token."""
+    lens, news = [700, 2600, max(0, new - 1)], [new] * 3
+
+    def spoil(q):
+        q[0, 1, 5] = float("nan")
+        q[new + new // 2, 0, d - 1] = float("inf")
+        q[2 * new - 1, 2, 17] = -float("inf")
+        q[2 * new, 3] = float("nan")                       # the first row of the last request sees nothing
+    out = serve(lens, news, hq, 2, d, kind, torch.bfloat16, spoil=spoil)
+    assert out[0, 1].isnan().all() and not out[2 * new].any()
+    assert int(out.isnan().any(2).sum()) == 3
