@@ -113,6 +113,13 @@ __host__ __device__ constexpr int kv4_pair_dim(int q, int i) {
   return KIND == W8A8_KV4_E2M1 ? 2 * i + q : 4 * q + i;
 }
 
+// The factor of the outputs: v_scale, or NaN where the scores' scale is one (their
+// own arithmetic takes it for a small number, to keep a masked score's infinity).
+__device__ __forceinline__ float kv4_out_scale(float sm_scale, const float* k_scale, const float* v_scale) {
+  const float s = sm_scale * __ldg(k_scale);
+  return s == s ? __ldg(v_scale) : s;
+}
+
 // Two e4m3 bytes as f16x2.
 __device__ __forceinline__ __half2 e4m3x2_to_half2(uint32_t two) {
   uint32_t h;

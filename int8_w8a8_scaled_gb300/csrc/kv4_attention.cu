@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(Small<D, NT>::kThreads, Small<D, NT>::kCtas) k
   if (static_cast<long long>(cta_share) * blockIdx.x >= total) return;
   const int r0 = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(share) * (blockIdx.x * kWarps + warp)));
   const int run_steps = min(total - r0, share);
-  const float kscale = __ldg(p.k_scale), vscale = __ldg(p.v_scale);
+  const float kscale = __ldg(p.k_scale), vscale = kv4_out_scale(p.sm_scale, p.k_scale, p.v_scale);
   const uint32_t full0 = smem_addr(&s_full[warp][0]);
   uint8_t* const ring = smem + warp * kRing * C::kSlot;
   bool ok = true;

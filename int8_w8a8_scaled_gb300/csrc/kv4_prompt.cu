@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     const int slot = warp / 8, half = warp / 4 % 2, quarter = warp % 4, row = 32 * quarter + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter) << 21);  // this warp's 32 TMEM lanes
     const uint32_t s_cols = lanes + slot * kTileTokens, o_cols = lanes + 2 * kTileTokens + slot * D + half * (D / 2);
-    const float vscale = __ldg(p.v_scale), to_log2 = p.sm_scale * __ldg(p.k_scale) * kLog2e;
+    const float vscale = kv4_out_scale(p.sm_scale, p.k_scale, p.v_scale), to_log2 = p.sm_scale * __ldg(p.k_scale) * kLog2e;
     uint32_t count = 0u;  // tiles of this slot
     int done = 0;
     // the unit before, whose results are written when the next one's query is on its way
@@ -851,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
       const float lk = __ldcg(s + kUnitRows);
       if (lk != 0.f) l = fmaf(ex2_fast(__ldcg(s) - m), lk, l);
     }
-    const float inv = l != 0.f ? __ldg(p.v_scale) / l : 0.f;
+    const float inv = l != 0.f ? kv4_out_scale(p.sm_scale, p.k_scale, p.v_scale) / l : 0.f;
     const size_t to = out_at(p, u.first, u.kvh, my);
 #pragma unroll 1
     for (int q = tid / kUnitRows; q < D / 8; q += kSoftmaxThreads / kUnitRows) {

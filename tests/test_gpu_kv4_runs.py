@@ -155,3 +155,17 @@ def test_a_query_with_nan_or_infinity_is_seen_in_its_own_row(new, hq, d, kind):
     out = serve(lens, news, hq, 2, d, kind, torch.bfloat16, spoil=spoil)
     assert out[0, 1].isnan().all() and not out[2 * new].any()
     assert int(out.isnan().any(2).sum()) == 3
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("which", ["k_scale", "v_scale", "sm_scale"])
+def test_a_scale_of_nan_gives_nan(which, new):
+    """And not the mean of the values; rows that see nothing are zeros."""
+    cache = torch.zeros(w8.kv4_cache_shape(9, 2, 16, 64), dtype=torch.uint8, device="cuda")
+    one, gone = torch.ones(1, device="cuda"), torch.full((1,), float("nan"), device="cuda")
+    q = torch.ones(2 * new, 8, 64, dtype=torch.bfloat16, device="cuda")
+    out, table = torch.empty_like(q), torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
+    w8.kv4_attention(q, cache, dev(np.int32([60, 0])), table, gone if which == "k_scale" else one, gone if which == "v_scale" else one, out,
+                     query_start=dev(np.int32([0, new, 2 * new])), max_query_len=new,
+                     sm_scale=float("nan") if which == "sm_scale" else 0.125)
+    assert out[:new].isnan().all() and not out[new:].any()
