@@ -370,14 +370,16 @@ __global__ void __launch_bounds__(Small<D, NT>::kThreads, Small<D, NT>::kCtas) k
     const int kvh = ui >> rq.more, row0 = (ui & rq.more) * C::kRows;
     const int rows = min(C::kRows, rq.n * p.share - row0);
 
-    // the query: dims D/4 t .. of row g (and 8 + g), scaled by 2^e so that the largest lies in [2^14, 2^15)
+    // the query: dims D/4 t .. of row g (and 8 + g), each row scaled by a 2^e that
+    // brings its largest element into [2^14, 2^15); infinities stay what they are
     uint32_t qf[NT][MT][2];
-    float cs;
+    float cs[NT][2];  // scale of the scores of the columns 2t, 2t + 1
     {
-      float qmax = 0.f;
+      float up[NT];
       uint32_t raw[NT][D / 8];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
+        float qmax = 0.f;
         const int c = 8 * nt + g;
         const int i = (row0 + c) / p.share, h = kvh * p.share + (row0 + c) % p.share;
         const uint16_t* src = static_cast<const uint16_t*>(p.q) + (rq.first + i) * p.q_token_stride + h * p.q_head_stride +
@@ -408,17 +410,19 @@ __global__ void __launch_bounds__(Small<D, NT>::kThreads, Small<D, NT>::kCtas) k
                                     : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[nt][j]));
           qmax = fmaxf(qmax, fmaxf(fabsf(v.x), fabsf(v.y)));
         }
-      }
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, off));
-      // 2^e as a float: qmax in [2^x, 2^(x + 1)) has x + 127 in its exponent bits
-      int e = 0;
-      if (qmax > 0.f && qmax <= 3.0e38f) e = min(100, max(-100, 14 + 127 - static_cast<int>(__float_as_uint(qmax) >> 23)));
-      cs = p.sm_scale * kscale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      // the scale's sign goes to the query: the largest product is the largest score
-      const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), cs);
-      // (no zero, so that a masked score's infinity stays one)
-      cs = fmaxf(fabsf(cs), 1e-37f);
+        for (int off = 1; off < 4; off <<= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, off));
+        // 2^e as a float: qmax in [2^x, 2^(x + 1)) has x + 127 in its exponent bits
+        int e = 0;
+        if (qmax > 0.f) e = min(100, 14 + 127 - static_cast<int>(__float_as_uint(qmax) >> 23));
+        float down = p.sm_scale * kscale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        // the scale's sign goes to the query: the largest product is the largest score
+        up[nt] = copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), down);
+        // (no zero, so that a masked score's infinity stays one)
+        down = fmaxf(fabsf(down), 1e-37f);
+        cs[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
+        cs[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -428,8 +432,8 @@ __global__ void __launch_bounds__(Small<D, NT>::kThreads, Small<D, NT>::kCtas) k
           for (int j = 0; j < 4; ++j) {
             const float2 x = p.q_fp16 ? __half22float2(*reinterpret_cast<const __half2*>(&raw[nt][4 * w + j]))
                                       : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[nt][4 * w + j]));
-            v[2 * j] = x.x * up;
-            v[2 * j + 1] = x.y * up;
+            v[2 * j] = x.x * up[nt];
+            v[2 * j + 1] = x.y * up[nt];
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -447,9 +451,6 @@ __global__ void __launch_bounds__(Small<D, NT>::kThreads, Small<D, NT>::kCtas) k
       }
     const int all_seen = rq.len - rq.all + row0 / p.share;  // tokens up to this one are seen by every row
 
-    // products that may pass the running maximum before it is raised: weights
-    // then reach 2^kHeadroom, and come out times 2^(15 - kHeadroom) for f16
-    const float room = fminf(kHeadroom / cs, 1e38f);
     float m[NT][2], l[NT][4], o[NT][MT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -529,13 +530,14 @@ __global__ void __launch_bounds__(Small<D, NT>::kThreads, Small<D, NT>::kCtas) k
           for (int u = 0; u < kStep; ++u)
 #pragma unroll
             for (int k = 0; k < 4; ++k) mx[k & 1] = fmaxf(mx[k & 1], sp[u][nt][k]);
-          if (__any_sync(0xffffffffu, mx[0] > m[nt][0] + room || mx[1] > m[nt][1] + room)) {
+          // raised when a weight would pass 2^kHeadroom; weights come out times 2^(15 - kHeadroom) for f16
+          if (__any_sync(0xffffffffu, (mx[0] - m[nt][0]) * cs[nt][0] > kHeadroom || (mx[1] - m[nt][1]) * cs[nt][1] > kHeadroom)) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
 #pragma unroll
               for (int off = 4; off < 32; off <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], off));
               const float mn = fmaxf(m[nt][c], mx[c]);
-              const float alpha = ex2_fast((m[nt][c] - mn) * cs);
+              const float alpha = ex2_fast((m[nt][c] - mn) * cs[nt][c]);
               m[nt][c] = mn;
               l[nt][c] *= alpha;
 #pragma unroll
@@ -545,12 +547,12 @@ __global__ void __launch_bounds__(Small<D, NT>::kThreads, Small<D, NT>::kCtas) k
               }
             }
           }
-          const float b0 = fmaf(-m[nt][0], cs, 15.f - kHeadroom), b1 = fmaf(-m[nt][1], cs, 15.f - kHeadroom);
+          const float b0 = fmaf(-m[nt][0], cs[nt][0], 15.f - kHeadroom), b1 = fmaf(-m[nt][1], cs[nt][1], 15.f - kHeadroom);
 #pragma unroll
           for (int u = 0; u < kStep; ++u) {
             float w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = ex2_fast(fmaf(sp[u][nt][k], cs, k & 1 ? b1 : b0));
+            for (int k = 0; k < 4; ++k) w[k] = ex2_fast(fmaf(sp[u][nt][k], cs[nt][k & 1], k & 1 ? b1 : b0));
             pb[u][nt][0] = movmatrix_t(as_u32(__floats2half2_rn(w[0], w[1])));
             pb[u][nt][1] = movmatrix_t(as_u32(__floats2half2_rn(w[2], w[3])));
             // the sum of the rounded weights, as one more row of ones
@@ -638,7 +640,7 @@ __global__ void __launch_bounds__(Small<D, NT>::kThreads, Small<D, NT>::kCtas) k
           for (int i = 0; i < D / 8; i += 4) *reinterpret_cast<float4*>(dst + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
           if (g == 0)  // m in the log2 domain
             *reinterpret_cast<float2*>(piece + col * C::kOStride + D) =
-                make_float2(l[nt][c] > 0.f ? m[nt][c] * cs : -INFINITY, l[nt][c]);
+                make_float2(l[nt][c] > 0.f ? m[nt][c] * cs[nt][c] : -INFINITY, l[nt][c]);
         }
       }
     if (!whole && lane == 0) s_piece[2 * warp + last] = {r0 + done - seg - step, rq.steps, rq.first, kvh, row0, rows};

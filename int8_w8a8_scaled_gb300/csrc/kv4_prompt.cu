@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         else softmax_sync();
       }
       // ---- the warp's 16 query rows, a 16-byte piece for each lane, scaled by
-      // 2^e so that a row's largest element lies in [2^14, 2^15)
+      // 2^e so that a row's largest element lies in [2^14, 2^15); infinities stay
       if (more && (pair || slot == 0)) {
         constexpr int kPerRow = D / 8, kAtOnce = 32 / kPerRow;  // pieces of a row, rows of one load
         constexpr int kBatch = 4;                               // loads in flight
@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
 #pragma unroll
             for (int off = 1; off < kPerRow; off <<= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, off));
             int e = 0;
-            if (qmax > 0.f && qmax <= 3.0e38f) e = min(100, max(-100, 14 + 127 - static_cast<int>(__float_as_uint(qmax) >> 23)));
+            if (qmax > 0.f) e = min(100, 14 + 127 - static_cast<int>(__float_as_uint(qmax) >> 23));
             const float down = to_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
             // the scale's sign goes to the query: the largest product is the largest score
             const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), down);

@@ -82,12 +82,12 @@ def close(got, want, lens):
     assert (over <= 0).all(), f"{int((over > 0).sum())} of {over.numel()} outside"
 
 
-def serve(lens, news, hq, hkv, d, kind, dtype, bs=32, seed=0, rise=None, loud=None, spoil=None):
+def serve(lens, news, hq, hkv, d, kind, dtype, bs=32, seed=0, rise=None, loud=None, spoil=None, only=slice(None), sm=None):
     """One call over requests of these lengths, compared with 64 bits.
 
     rise: requests (a slice) whose keys point along their queries, further the
     later the token, so that the maximum goes up to the end.  loud: the queries'
-    scale for each packed token and head.  spoil: changes the query in place."""
+    scale for each packed token and head.  spoil: changes the query in place.  only: the heads compared."""
     lens, news = np.asarray(lens), np.asarray(news)
     rng = np.random.default_rng(seed)
     gen = torch.Generator(device="cuda").manual_seed(seed)
@@ -114,11 +114,12 @@ def serve(lens, news, hq, hkv, d, kind, dtype, bs=32, seed=0, rise=None, loud=No
     w8.kv4_cache_write(k, v, cache, torch.arange(nb * bs, device="cuda"), *scales, kind=kind)
     out = torch.full_like(q, float("nan"))
     start = dev(np.concatenate([[0], np.cumsum(news)]).astype(np.int32))
+    sm = 1.0 / d ** 0.5 if sm is None else sm
     w8.kv4_attention(q, cache, dev(lens.astype(np.int32)), dev(table), *scales, out, query_start=start,
-                     max_query_len=int(news.max()), kind=kind)
+                     max_query_len=int(news.max()), kind=kind, sm_scale=sm)
     assert w8.device_status() == 0
-    sm = 1.0 / d ** 0.5
-    close(out, reference(q, cache, lens, news, table, float(np.float32(kg)), float(np.float32(vg)), sm, kind), lens)
+    want = reference(q, cache, lens, news, table, float(np.float32(kg)), float(np.float32(vg)), sm, kind)
+    close(out[:, only], [x[:, only] for x in want], lens)
     return out
 
 
@@ -169,3 +170,22 @@ def test_a_scale_of_nan_gives_nan(which, new):
                      query_start=dev(np.int32([0, new, 2 * new])), max_query_len=new,
                      sm_scale=float("nan") if which == "sm_scale" else 0.125)
     assert out[:new].isnan().all() and not out[new:].any()
+
+
+@pytest.mark.parametrize("size", [2.0 ** 70, 2.0 ** -70, float("inf")])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,hq", [(1, 8), (3, 8), (5, 8), (40, 8)])
+def test_a_head_of_another_size_leaves_the_others_alone(new, hq, d, size):
+    """Each row has a scale of its own: one head far above or below the others of
+    its KV head takes no bits of theirs."""
+    def spoil(q):
+        q[:, ::4] *= size
+    serve([900, 2600], [new] * 2, hq, 2, d, "e2m1", torch.bfloat16, spoil=spoil, only=[1, 2, 3, 5, 6, 7])
+
+
+@pytest.mark.parametrize("new", [1, 5, 40])
+def test_a_query_far_below_the_normal_numbers(new):
+    """Among heads of ordinary size, one whose scores come out ordinary by the scale alone."""
+    def spoil(q):
+        q[:, 1] *= 2.0 ** -70
+    serve([900, 2600], [new] * 2, 4, 1, 64, "e2m1", torch.bfloat16, spoil=spoil, only=[1], sm=2.0 ** 67)
