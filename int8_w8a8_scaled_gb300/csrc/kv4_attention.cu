@@ -547,12 +547,13 @@ __global__ void __launch_bounds__(Small<D, NT>::kThreads, Small<D, NT>::kCtas) k
               }
             }
           }
-          const float b0 = fmaf(-m[nt][0], cs[nt][0], 15.f - kHeadroom), b1 = fmaf(-m[nt][1], cs[nt][1], 15.f - kHeadroom);
 #pragma unroll
           for (int u = 0; u < kStep; ++u) {
+            // (s - m) cs and not s cs - m cs: with scores of 2^26 and more the rounding of
+            // m cs alone would push weights out of f16
             float w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = ex2_fast(fmaf(sp[u][nt][k], cs[nt][k & 1], k & 1 ? b1 : b0));
+            for (int k = 0; k < 4; ++k) w[k] = ex2_fast(fmaf(sp[u][nt][k] - m[nt][k & 1], cs[nt][k & 1], 15.f - kHeadroom));
             pb[u][nt][0] = movmatrix_t(as_u32(__floats2half2_rn(w[0], w[1])));
             pb[u][nt][1] = movmatrix_t(as_u32(__floats2half2_rn(w[2], w[3])));
             // the sum of the rounded weights, as one more row of ones

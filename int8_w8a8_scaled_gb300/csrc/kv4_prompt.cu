@@ -60,6 +60,10 @@ constexpr int kRecords = kTileTokens / kKv4Tokens;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kHeadroom = 2.f;
 constexpr float kNoScore = -1e25f;
+// Scores (in the log2 domain) up to which a weight's exponent is one FMA,
+// s cs + (13 - m cs): the rounding of m cs moves all weights of a row by the same
+// 2^-9 at most.  From 2^26 on it would push them out of f16.
+constexpr float kFar = 65536.f;
 constexpr int kMaxCounters = 1024;
 constexpr size_t kCounterBytes = kMaxCounters * sizeof(unsigned);
 constexpr uint32_t kTmemCols = 512;
@@ -750,7 +754,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
           }
         }
         // the tokens' weights, over this half's scores as they are read
-        const float bias = fmaf(-m, cs, 15.f - kHeadroom);
+        float bias = fmaf(-m, cs, 15.f - kHeadroom);
+        if (__builtin_expect(__any_sync(0xffffffffu, fabsf(bias) > kFar), 0)) {
+          // s - m in place of far scores s: rare, and apart as above (subtracting in
+          // the loop below: 816 us, with this branch 808, without either 798)
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t s[16];
+            tmem_ld16(cols + 16 * c, s);
+            tmem_ld_wait();
+            tmem_loaded(s);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) - m);
+            tmem_st16(cols + 16 * c, s);
+          }
+          tmem_st_wait();
+          bias = 15.f - kHeadroom;
+        }
         const uint64_t cs2 = pack2(cs, cs), bias2 = pack2(bias, bias);
         uint64_t sum = 0;
         auto weights = [&](const uint32_t (&s)[16], uint32_t* w) {

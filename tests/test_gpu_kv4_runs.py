@@ -189,3 +189,27 @@ def test_a_query_far_below_the_normal_numbers(new):
     def spoil(q):
         q[:, 1] *= 2.0 ** -70
     serve([900, 2600], [new] * 2, 4, 1, 64, "e2m1", torch.bfloat16, spoil=spoil, only=[1], sm=2.0 ** 67)
+
+
+@pytest.mark.parametrize("power", [10, 17, 26, 28, 40, 70])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,hq", [(1, 4), (5, 4), (40, 8)])
+def test_scores_of_any_size(new, hq, d, power):
+    """A query along one token's key, larger by powers of two: that token's value
+    alone, however far its score (2^26 and more) is above the others."""
+    gen = torch.Generator(device="cuda").manual_seed(power)
+    length, hkv = 1500, 2
+    nb = -(-length // 16)
+    k, v = (torch.randn(nb * 16, hkv, d, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    cache = torch.zeros(w8.kv4_cache_shape(nb, hkv, 16, d), dtype=torch.uint8, device="cuda")
+    one = torch.full((1,), 0.0137, device="cuda")
+    w8.kv4_cache_write(k, v, cache, torch.arange(nb * 16, device="cuda"), one, one)
+    token = torch.randint(0, length - new, (new, hq), generator=gen, device="cuda")
+    head = torch.arange(hq, device="cuda") // (hq // hkv)
+    q = (k[token, head].float() * 2.0 ** power).bfloat16()
+    out = torch.empty_like(q)
+    table = torch.arange(nb, dtype=torch.int32, device="cuda")[None]
+    w8.kv4_attention(q, cache, dev(np.int32([length])), table, one, one, out, query_start=dev(np.int32([0, new])), max_query_len=new)
+    want = torch.stack([decoded(cache[:, j].flatten(0, 1), 9 * d, "e2m1") for j in range(hkv)], 1)[token, head] * 0.0137
+    # the output's half step, and one weight of 11 bits
+    assert ((out.double() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -11)).all()
