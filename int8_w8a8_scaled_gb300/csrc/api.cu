@@ -1195,7 +1195,8 @@ w8a8_status w8a8_kv4_attention(const void* q, int q_dtype, int64_t tokens, int64
   p.seq_lens = seq_lens;
   p.query_start = query_start;
   p.tokens = static_cast<int>(tokens);
-  p.max_query_len = static_cast<int>(max_query_len);
+  // no request has more rows than there are tokens, however generous the limit
+  p.max_query_len = static_cast<int>(std::min(max_query_len, tokens));
   p.batch = static_cast<int>(batch);
   p.num_q_heads = static_cast<int>(num_q_heads);
   p.num_kv_heads = static_cast<int>(num_kv_heads);

@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
   }
 
   // ---- this CTA's run; an item is one request and row block, all KV heads
-  const int blocks_max = (p.share * p.max_query_len + kUnitRows - 1) / kUnitRows;
+  const int blocks_max = static_cast<int>((static_cast<long long>(p.share) * p.max_query_len + kUnitRows - 1) / kUnitRows);
   const int items = p.batch * blocks_max;  // below 2^31, the launcher sees to it
   long long total = 0, share;
   {

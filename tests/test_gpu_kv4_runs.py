@@ -213,3 +213,21 @@ def test_scores_of_any_size(new, hq, d, power):
     want = torch.stack([decoded(cache[:, j].flatten(0, 1), 9 * d, "e2m1") for j in range(hkv)], 1)[token, head] * 0.0137
     # the output's half step, and one weight of 11 bits
     assert ((out.double() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -11)).all()
+
+
+@pytest.mark.parametrize("new", [1, 7, 300])
+def test_a_max_query_len_that_means_no_limit(new):
+    """The largest number that the sizes allow, for one head and one request."""
+    rng = np.random.default_rng(new)
+    nb = 40
+    cache = torch.zeros(w8.kv4_cache_shape(nb, 1, 16, 64), dtype=torch.uint8, device="cuda")
+    k, v = (torch.from_numpy(rng.standard_normal((nb * 16, 1, 64)).astype(np.float32)).cuda().bfloat16() for _ in range(2))
+    one = torch.full((1,), 0.0137, device="cuda")
+    w8.kv4_cache_write(k, v, cache, torch.arange(nb * 16, device="cuda"), one, one)
+    q = torch.from_numpy(rng.standard_normal((new, 1, 64)).astype(np.float32)).cuda().bfloat16()
+    table = torch.arange(nb, dtype=torch.int32, device="cuda")[None]
+    for most in (2 ** 31 - 1, 1 << 20, new):
+        out = torch.full_like(q, float("nan"))
+        w8.kv4_attention(q, cache, dev(np.int32([600])), table, one, one, out, query_start=dev(np.int32([0, new])), max_query_len=most)
+        close(out, reference(q, cache, [600], [new], np.arange(nb, dtype=np.int32)[None], 0.013700000010430813, 0.013700000010430813,
+                             0.125, "e2m1"), [600])
