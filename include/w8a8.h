@@ -459,8 +459,9 @@ W8A8_API w8a8_status w8a8_kv4_cache_read(const void* cache, int64_t num_blocks, 
  *                 or -1 for tokens of refused requests, of context blocks
  *                 whose entry is negative, and past the last new token
  *                 (padding of a captured step); context + i, or 0 for
- *                 padding.  tokens must hold every new token: blocks are
- *                 entered by their first token.
+ *                 padding.  A request with a new token past `tokens` is
+ *                 refused, as for want of blocks, and so is then every later
+ *                 one with new tokens.
  *   free_left     int32 [1], the balance: free_count less the needs of
  *                 every request up to the last admitted one.  Refused requests
  *                 among them count as waiting for their blocks, so that a

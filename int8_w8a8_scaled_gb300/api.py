@@ -559,7 +559,7 @@ def build_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_
     [1]) are free; blocks are taken from the end, in request order.
     Written: the new entries of block_table (int32 [batch, max_blocks]),
     query_start (int32 [batch + 1]), seq_lens (int32 [batch]; 0 for a request
-    that its table or the free list has no room for), slots (int64) and
+    that its table, the free list or the packed tokens have no room for), slots (int64) and
     positions (int32) of the packed tokens (-1 and 0 past the last one, -1 for
     a refused request's), free_left (int32 [1], the balance: free_count less
     the needs up to the last admitted request, negative by the blocks that the

@@ -218,8 +218,8 @@ __global__ void __launch_bounds__(kCacheThreads) kv4_read_kernel(const Kv4CacheA
 // need_b = ceil((ctx + new) / S) - ceil(ctx / S) blocks for request b (none
 // if it would not fit its table), taken in request order from the end of the
 // free list: block i of request b is free[count - 1 - before_b - i], before_b
-// the sum of the needs in front of it.  A request is admitted if it fits and
-// needs nothing or before_b + need_b <= count.
+// the sum of the needs in front of it.  A request is admitted if it fits its
+// table and the packed tokens, and needs nothing or before_b + need_b <= count.
 //
 // Every thread block makes the two prefix sums (new tokens, needs; one scan
 // of 64-bit pairs) over all requests for itself, in shared memory, and then
@@ -270,8 +270,10 @@ __global__ void __launch_bounds__(kTableThreads) block_table_kernel(const BlockT
     const bool fits = ctx + add <= room;
     const unsigned need = fits ? blocks_for(ctx + add, p.block_size) - blocks_for(ctx, p.block_size) : 0;
     const unsigned before = static_cast<unsigned>(run >> 32);
-    const bool ok = fits && (need == 0 || static_cast<unsigned long long>(before) + need <= static_cast<unsigned>(count));
     const int start = static_cast<int>(run & 0xffffffffu);
+    // its tokens past the packed arrays would leave blocks without an entry
+    const bool packed = add == 0 || start + add <= p.tokens;
+    const bool ok = fits && packed && (need == 0 || static_cast<unsigned long long>(before) + need <= static_cast<unsigned>(count));
     s_start[b] = start;
     s_before[b] = ok ? static_cast<int>(min(before, 0x7fffffffu)) : -1;
     if (ok) upto = max(upto, before + need);

@@ -139,7 +139,7 @@ def block_tables(context_lens, new_lens, free_blocks, free_count: int, table, bl
         first, last = -(-ctx // block_size), -(-(ctx + new) // block_size)
         fits = ctx + new <= table.shape[1] * block_size
         need = last - first if fits else 0
-        ok = fits and (need == 0 or before + need <= count)
+        ok = fits and (new == 0 or start + new <= tokens) and (need == 0 or before + need <= count)
         for i in range(need if ok else 0):
             table[b, first + i] = free_blocks[count - 1 - before - i]
         if ok:
