@@ -468,8 +468,10 @@ W8A8_API w8a8_status w8a8_kv4_cache_read(const void* cache, int64_t num_blocks, 
  *                 negative number says how many blocks the list was short.
  *   free_count_out  int32 [1] or NULL: the number of ids that are still free,
  *                 free_blocks[0 .. free_count_out - 1] (the next call's
- *                 free_count).  Neither may alias free_count.
- * The inputs are not changed, so a call can be repeated.  Limits:
+ *                 free_count).
+ * No output may lie over an input or another output (context_lens, say, as
+ * seq_lens): INVALID_ARG.  The inputs are not changed, so a call can be
+ * repeated.  Limits:
  * 1 <= batch <= 16384, the sum of new_lens below 2^31. */
 W8A8_API w8a8_status w8a8_build_block_tables(const int32_t* context_lens, const int32_t* new_lens,
                                              int64_t batch, const int32_t* free_blocks,

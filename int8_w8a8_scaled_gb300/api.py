@@ -564,7 +564,8 @@ def build_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_
     a refused request's), free_left (int32 [1], the balance: free_count less
     the needs up to the last admitted request, negative by the blocks that the
     list was short) and free_count_out (int32 [1], optional: the ids still
-    free, the next call's free_count)."""
+    free, the next call's free_count).  None of them may share memory with an
+    input or with each other."""
     if block_table.dtype is not torch.int32 or block_table.ndim != 2 or not block_table.is_contiguous():
         raise ValueError("block_table must be a contiguous int32 [batch, max_blocks] CUDA tensor")
     batch, max_blocks = block_table.shape

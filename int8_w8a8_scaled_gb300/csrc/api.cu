@@ -1094,6 +1094,25 @@ w8a8_status w8a8_build_block_tables(const int32_t* context_lens, const int32_t* 
                           static_cast<const void*>(free_left), static_cast<const void*>(free_count_out)})
     if (!aligned(ptr, 4)) return fail(W8A8_ERR_MISALIGNED, "int32 arrays must be 4-byte aligned");
   if (!aligned(slots, 8)) return fail(W8A8_ERR_MISALIGNED, "slots must be 8-byte aligned");
+  // every thread block reads the inputs for itself while the first one writes
+  // outputs: nothing written may lie over something read, or over another output
+  struct Range {
+    const void* at;
+    int64_t bytes;
+  };
+  const Range written[] = {{block_table, 4 * batch * max_blocks}, {query_start, 4 * (batch + 1)}, {seq_lens, 4 * batch},
+                           {slots, 8 * tokens}, {positions, 4 * tokens}, {free_left, 4}, {free_count_out, 4}};
+  const Range read[] = {{context_lens, 4 * batch}, {new_lens, 4 * batch}, {free_blocks, 4 * free_capacity}, {free_count, 4}};
+  auto overlap = [](const Range& x, const Range& y) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.at), b = reinterpret_cast<uintptr_t>(y.at);
+    return a && b && a < b + static_cast<uintptr_t>(y.bytes) && b < a + static_cast<uintptr_t>(x.bytes);
+  };
+  for (const Range& w : written) {
+    for (const Range& r : read)
+      if (overlap(w, r)) return fail(W8A8_ERR_INVALID_ARG, "an output lies over an input");
+    for (const Range& o : written)
+      if (&o != &w && overlap(w, o)) return fail(W8A8_ERR_INVALID_ARG, "two outputs lie over each other");
+  }
   w8a8_status st;
   DeviceInfo dev;
   if ((st = device_info(&dev)) != W8A8_OK) return st;
