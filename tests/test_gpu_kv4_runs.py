@@ -231,3 +231,74 @@ def test_a_max_query_len_that_means_no_limit(new):
         w8.kv4_attention(q, cache, dev(np.int32([600])), table, one, one, out, query_start=dev(np.int32([0, new])), max_query_len=most)
         close(out, reference(q, cache, [600], [new], np.arange(nb, dtype=np.int32)[None], 0.013700000010430813, 0.013700000010430813,
                              0.125, "e2m1"), [600])
+
+
+def few_rows_run(lens, news, hq, hkv):
+    """Steps of 32 tokens that each warp of the few-rows kernel goes through."""
+    rows = int(news.max()) * hq // hkv
+    groups = 1 + (news * (hq // hkv) > 16) if rows > 8 else np.ones_like(news)
+    steps = (np.maximum(1, -(-lens // 32)) * (news > 0) * groups).sum() * hkv
+    return steps / (sms() * 8 * (2 if rows <= 8 else 1))
+
+
+def many_rows_run(lens, news, hq, hkv):
+    """Tiles of 128 tokens that each CTA of the many-rows kernel goes through."""
+    share, tiles = hq // hkv, 0
+    for length, n in zip(lens, news):
+        for row in range(0, n * share, 256):
+            last = min(n * share, row + 256) - 1
+            tiles += max(1, -(-min(length, max(0, length - n + last // share + 1)) // 128))
+    return tiles * hkv / sms()
+
+
+EVERY_OTHER = slice(0, None, 2)
+
+
+@pytest.mark.parametrize("kind", ["e2m1", "int4"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,hq", [(1, 32), (1, 64), (2, 32), (3, 32), (5, 32)])
+def test_few_rows_long_runs(new, hq, d, kind):
+    """Ragged requests up to 8000 tokens: a warp's run is longer than the batch of
+    16 steps whose places it looks up at once, through several units, with
+    maxima that go up to the end in every other request.  4, 8 and 16 rows, and
+    20 in two groups."""
+    rng = np.random.default_rng(new + d)
+    lens = rng.integers(500, 8001, 64)
+    news = np.full(64, new) if new == 1 else rng.integers(1, new + 1, 64)
+    news[0] = new
+    assert few_rows_run(lens, news, hq, 8) > 20
+    serve(lens, news, hq, 8, d, kind, torch.bfloat16 if kind == "e2m1" else torch.float16, rise=EVERY_OTHER)
+
+
+@pytest.mark.parametrize("new,hq", [(1, 32), (3, 32), (5, 32)])
+def test_few_rows_many_units_to_a_run(new, hq):
+    """Short requests, empty ones and ones without new tokens among them."""
+    rng = np.random.default_rng(new)
+    lens, news = rng.integers(0, 300, 900), rng.integers(0 if new > 1 else 1, new + 1, 900)
+    lens[::7] = 0
+    assert few_rows_run(lens, news, hq, 8) > 12
+    serve(lens, news, hq, 8, 64, "e2m1", torch.bfloat16, rise=EVERY_OTHER)
+
+
+@pytest.mark.parametrize("kind", ["e2m1", "int4"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_rows_long_runs(d, kind):
+    """Chunks of prompts: dozens of tiles to a CTA, pairs of row slots."""
+    lens, news = np.array([2500, 2300]), np.array([1500, 1333])
+    assert many_rows_run(lens, news, 32, 8) > 30
+    serve(lens, news, 32, 8, d, kind, torch.bfloat16 if kind == "e2m1" else torch.float16, rise=slice(0, 1))
+
+
+@pytest.mark.parametrize("kind", ["e2m1", "int4"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("seed", [1, 2])
+def test_many_rows_units_of_all_forms_in_a_run(d, kind, seed):
+    """Units of up to 128 rows (both slots take the same ones, the tiles in turn)
+    and of more (a slot each), of one tile, of two and of many, whole and cut."""
+    rng = np.random.default_rng(seed)
+    news = rng.choice([0, 1, 9, 20, 32, 33, 40, 64, 65, 100, 200], 90)
+    news[:2] = 200, 1
+    lens = news + rng.choice([-1, 0, 0, 30, 128, 250, 1000, 6000], 90) * (news > 0)
+    lens = np.maximum(lens, 0)
+    assert many_rows_run(lens, news, 32, 8) > 30
+    serve(lens, news, 32, 8, d, kind, torch.bfloat16, seed=seed, rise=EVERY_OTHER)
