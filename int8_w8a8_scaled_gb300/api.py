@@ -68,31 +68,38 @@ def _ld(t: torch.Tensor) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
-def _cuda(*ts):
-    """Refuses tensors that are not on the current device, where the library launches."""
+@functools.lru_cache(maxsize=None)
+def _gpus() -> int:
+    return torch.cuda.device_count()
+
+
+def _cuda(*ts) -> int:
+    """The current device, where the library launches; refuses tensors that are
+    not on it.  With one GPU visible every CUDA tensor is (which saves a call
+    about 1 us: 11 for one short attention request, 12 with the devices looked at)."""
+    for t in ts:
+        if t is not None and not t.is_cuda:
+            raise ValueError("all tensors must be CUDA tensors")
+    if _gpus() == 1:
+        return 0
     devices = {t.get_device() for t in ts if t is not None}
-    if -1 in devices:
-        raise ValueError("all tensors must be CUDA tensors")
     if len(devices) > 1:
         raise ValueError("all tensors must be on one device")
-    if devices and torch._C._cuda_getDevice() not in devices:
+    device = torch._C._cuda_getDevice()
+    if devices != {device}:
         raise ValueError(f"the tensors are on cuda:{devices.pop()}, which is not the current device")
+    return device
 
 
 def _ptr(t):
     return t.data_ptr() if t is not None else None
 
 
-def _raw_stream(device_index: int) -> int:
-    """The device's current stream, without making a Stream object of it."""
-    return torch._C._cuda_getCurrentRawStream(device_index)
-
-
-def _stream(stream):
-    """The given stream, or the current one of the current device."""
+def _stream(stream, device: int) -> int:
+    """The given stream of `device`, the current one, or its current stream."""
     if stream is None:
-        return _raw_stream(torch._C._cuda_getDevice())
-    if getattr(stream, "device_index", None) not in (None, torch._C._cuda_getDevice()):
+        return torch._C._cuda_getCurrentRawStream(device)
+    if getattr(stream, "device_index", None) not in (None, device):
         raise ValueError("the stream belongs to another device than the tensors")
     return stream.cuda_stream
 
@@ -158,21 +165,23 @@ _ws_lock = threading.Lock()
 _default_ws: dict = {}
 
 
-def _default_workspace(device: torch.device, nbytes: int, kind: str, stream) -> Workspace:
+def _default_workspace(device: int, nbytes: int, kind: str, stream, handle: int) -> Workspace:
     """Per (device, stream that the call runs on, kind) scratch, zeroed on that
     stream; the matmul's buffer is never shared with the quantiser (whose absmax
     word would land on a counter).  Scratch first made during a capture belongs to
     the graph, whose replay zeroes it, and is not kept: before that replay it
-    holds anything."""
-    key = (kind, device.index, _raw_stream(device.index) if stream is None else stream.cuda_stream)
+    holds anything.  stream: as given to the call, handle: what it stands for."""
+    key = (kind, device, handle)
     ws = _default_ws.get(key)
-    if ws is not None and ws.buf.numel() >= nbytes and not _capturing():
+    # (the legacy default stream, handle 0, cannot be captured)
+    if ws is not None and ws.buf.numel() >= nbytes and (handle == 0 or not _capturing()):
         return ws
     if ws is None:
-        with _ws_lock, _launching_on(device, stream):
+        on = torch.device("cuda", device)
+        with _ws_lock, _launching_on(on, stream):
             ws = _default_ws.get(key)
             if ws is None:
-                ws = Workspace(nbytes, device)
+                ws = Workspace(nbytes, on)
                 if not _capturing():
                     _default_ws[key] = ws
                 return ws
@@ -190,7 +199,8 @@ def scaled_quant(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, per_toke
                  stream=None) -> None:
     """q = sat_round(x / scale); dynamic mode writes scale = absmax / 448
     (e4m3) or absmax / 127 (int8), per token (row) or per tensor."""
-    _cuda(x, q, scale, workspace)
+    device = _cuda(x, q, scale, workspace)
+    handle = _stream(stream, device)
     lib = _lib.load()
     rows, cols = x.shape
     if tuple(q.shape) != (rows, cols):
@@ -204,17 +214,17 @@ def scaled_quant(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, per_toke
     mode = DYNAMIC if dynamic else STATIC
     need = lib.w8a8_scaled_quant_workspace_size(rows, cols, gran, mode)
     if need and workspace is None:
-        workspace = _default_workspace(x.device, need, "quant", stream).buf
+        workspace = _default_workspace(device, need, "quant", stream, handle).buf
     check(lib.w8a8_scaled_quant(
         _ptr(x), _fkind(x), rows, cols, _ld(x), _ptr(q), _qkind(q, q_dtype), _ld(q),
         _ptr(scale), gran, mode, _ptr(workspace) if need else None,
-        workspace.numel() if (need and workspace is not None) else 0, _stream(stream)))
+        workspace.numel() if (need and workspace is not None) else 0, handle))
 
 
 def scaled_dequant(q: torch.Tensor, scale: torch.Tensor, y: torch.Tensor, per_token: bool = False,
                    q_dtype=None, stream=None) -> None:
     """y = round16(decode(q) * scale)."""
-    _cuda(q, scale, y)
+    device = _cuda(q, scale, y)
     lib = _lib.load()
     rows, cols = q.shape
     if tuple(y.shape) != (rows, cols):
@@ -223,7 +233,7 @@ def scaled_dequant(q: torch.Tensor, scale: torch.Tensor, y: torch.Tensor, per_to
         raise ValueError("scale must be a contiguous float32 tensor")
     check(lib.w8a8_scaled_dequant(
         _ptr(q), _qkind(q, q_dtype), rows, cols, _ld(q), _ptr(scale),
-        PER_ROW if per_token else PER_TENSOR, _ptr(y), _fkind(y), _ld(y), _stream(stream)))
+        PER_ROW if per_token else PER_TENSOR, _ptr(y), _fkind(y), _ld(y), _stream(stream, device)))
 
 
 def _cfg(config) -> MmConfig | None:
@@ -261,7 +271,8 @@ def scaled_mm(a_q: torch.Tensor, b_q: torch.Tensor, scale_a: torch.Tensor, scale
     scale_b: [N] or [1] fp32.  out: [M, N] bf16 / fp16 (or float32 for the
     unrounded e4m3 result, int32 for the raw int8 accumulators).
     """
-    _cuda(a_q, b_q, scale_a, scale_b, out)
+    device = _cuda(a_q, b_q, scale_a, scale_b, out)
+    handle = _stream(stream, device)
     lib = _lib.load()
     M, K = a_q.shape
     N, K2 = b_q.shape
@@ -287,16 +298,16 @@ def scaled_mm(a_q: torch.Tensor, b_q: torch.Tensor, scale_a: torch.Tensor, scale
     if isinstance(workspace, Workspace):
         workspace = workspace.ensure(need, stream).buf
     elif workspace is None and need:
-        workspace = _default_workspace(a_q.device, need, "mm", stream).buf
+        workspace = _default_workspace(device, need, "mm", stream, handle).buf
     _cuda(a_q, workspace)
     ws_ptr = _ptr(workspace) if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     args = (_ptr(a_q), _ld(a_q), _ptr(b_q), _ld(b_q), _ptr(scale_a), a_gran, _ptr(scale_b), b_gran,
             _ptr(out), _ld(out), M, N, K, qk, _fkind(out, wide=True), ws_ptr, ws_bytes)
     if c is None:
-        check(lib.w8a8_scaled_mm(*args, _stream(stream)))
+        check(lib.w8a8_scaled_mm(*args, handle))
     else:
-        check(lib.w8a8_scaled_mm_with_config(*args, ctypes.byref(c), _stream(stream)))
+        check(lib.w8a8_scaled_mm_with_config(*args, ctypes.byref(c), handle))
     return out
 
 
@@ -313,7 +324,8 @@ def quant_scaled_mm(x: torch.Tensor, b_q: torch.Tensor, scale_b: torch.Tensor, o
     the per-token scales.  route: "auto", "one_kernel" (the matmul
     quantises its own activations; decode shapes only) or "two_step".
     """
-    _cuda(x, b_q, scale_b, out)
+    device = _cuda(x, b_q, scale_b, out)
+    handle = _stream(stream, device)
     lib = _lib.load()
     M, K = x.shape
     N, K2 = b_q.shape
@@ -335,14 +347,14 @@ def quant_scaled_mm(x: torch.Tensor, b_q: torch.Tensor, scale_b: torch.Tensor, o
     if isinstance(workspace, Workspace):
         workspace = workspace.ensure(need, stream).buf
     elif workspace is None and need:
-        workspace = _default_workspace(x.device, need, "mm", stream).buf
+        workspace = _default_workspace(device, need, "mm", stream, handle).buf
     _cuda(x, workspace)
     ws_ptr = _ptr(workspace) if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     check(lib.w8a8_quant_scaled_mm(_ptr(x), _fkind(x), _ld(x), _ptr(b_q), _ld(b_q), _ptr(scale_b), b_gran,
                                    _ptr(out), _ld(out), M, N, K, qk, _fkind(out, wide=True),
                                    _ptr(scale_a_out) if scale_a_out is not None else None,
-                                   _lib.ROUTES[route], ws_ptr, ws_bytes, _stream(stream)))
+                                   _lib.ROUTES[route], ws_ptr, ws_bytes, handle))
     return out
 
 
@@ -354,9 +366,9 @@ def _shard_rows(shard_rows):
 def expand_shard_scales(shard_scales: torch.Tensor, shard_rows, scale_b: torch.Tensor, stream=None) -> torch.Tensor:
     """scale_b[n] = shard_scales[shard of row n]: per-shard weight scales of a
     merged layer as a per-channel vector for the fused epilogue."""
-    _cuda(shard_scales, scale_b)
+    device = _cuda(shard_scales, scale_b)
     arr, n = _shard_rows(shard_rows)
-    check(_lib.load().w8a8_expand_shard_scales(_ptr(shard_scales), arr, n, _ptr(scale_b), _stream(stream)))
+    check(_lib.load().w8a8_expand_shard_scales(_ptr(shard_scales), arr, n, _ptr(scale_b), _stream(stream, device)))
     return scale_b
 
 
@@ -364,13 +376,13 @@ def requant_shards(q: torch.Tensor, shard_scales: torch.Tensor, shard_rows, q_ou
                    scale_out: torch.Tensor, q_dtype=None, stream=None) -> None:
     """Rewrite a row-sharded merged weight to one shared scale (the largest
     shard scale, written to scale_out): q' = encode(decode(q) * s_i / s_max)."""
-    _cuda(q, shard_scales, q_out, scale_out)
+    device = _cuda(q, shard_scales, q_out, scale_out)
     arr, n = _shard_rows(shard_rows)
     rows, cols = q.shape
     if tuple(q_out.shape) != (rows, cols):
         raise ValueError("q_out must have the shape of q")
     check(_lib.load().w8a8_requant_shards(_ptr(q), _qkind(q, q_dtype), cols, _ld(q), _ptr(shard_scales), arr, n,
-                                          _ptr(q_out), _ld(q_out), _ptr(scale_out), _stream(stream)))
+                                          _ptr(q_out), _ld(q_out), _ptr(scale_out), _stream(stream, device)))
 
 
 def device_status() -> int:
@@ -398,7 +410,8 @@ def fp8_kv_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     num_kv_heads, 128] (the paged cache).  Codes are float8_e4m3fn (or uint8
     views).  seq_lens: int32 [batch]; k_scale, v_scale: float32 [1].
     sm_scale defaults to 1/sqrt(128)."""
-    _cuda(q, k_cache, v_cache, seq_lens, k_scale, v_scale, out)
+    device = _cuda(q, k_cache, v_cache, seq_lens, k_scale, v_scale, out)
+    handle = _stream(stream, device)
     lib = _lib.load()
     if q.dim() != 3 or not q.is_contiguous() or tuple(out.shape) != tuple(q.shape) or not out.is_contiguous():
         raise ValueError("q and out must be contiguous [batch, num_q_heads, head_dim] tensors")
@@ -436,7 +449,7 @@ def fp8_kv_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     if isinstance(workspace, Workspace):
         wbuf = workspace.ensure(need, stream).buf
     elif workspace is None:
-        wbuf = _default_workspace(q.device, need, "attention", stream).buf
+        wbuf = _default_workspace(device, need, "attention", stream, handle).buf
     else:
         wbuf = workspace
     if workspace is not None:
@@ -446,7 +459,7 @@ def fp8_kv_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     check(lib.w8a8_fp8_kv_decode_attention(
         _ptr(q), _fkind(q), batch, hq, hkv, d, _ptr(k_cache), _ptr(v_cache), max_seq, bt, bsz, maxb, nblk,
         _ptr(seq_lens), _ptr(k_scale), _ptr(v_scale), float(sm_scale), _ptr(out), _fkind(out),
-        _ptr(wbuf), wbuf.numel(), _stream(stream)))
+        _ptr(wbuf), wbuf.numel(), handle))
 
 
 # ---------------------------------------------------------------- a serving step over a 4-bit paged KV cache
@@ -512,8 +525,8 @@ def _kv4_tokens(k, v, cache, slots, k_scale, v_scale, kind) -> tuple:
         raise TypeError("k and v must have the same element type")
     _vectors((("slots", slots, n),), torch.int64)
     _one_scale(k_scale, v_scale)
-    _cuda(k, v, cache, slots, k_scale, v_scale)
-    return nb, bs, (_fkind(k), n, h, d, *ks, *vs), _kv4_kind(kind)
+    device = _cuda(k, v, cache, slots, k_scale, v_scale)
+    return nb, bs, (_fkind(k), n, h, d, *ks, *vs), _kv4_kind(kind), device
 
 
 def kv4_cache_write(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor,
@@ -526,12 +539,12 @@ def kv4_cache_write(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, slots
     k_scale, v_scale: float32 [1], the tensors' scales: with absmax / (6 * 448)
     (e2m1) or absmax / (7 * 448) (int4) of the values met, no group saturates.
     kind: "e2m1" or "int4"."""
-    nb, bs, sizes, kd = _kv4_tokens(k, v, cache, slots, k_scale, v_scale, kind)
+    nb, bs, sizes, kd, device = _kv4_tokens(k, v, cache, slots, k_scale, v_scale, kind)
     if sizes[1] == 0:
         return
     check(_lib.load().w8a8_kv4_cache_write(
         k.data_ptr(), v.data_ptr(), *sizes, cache.data_ptr(), nb, bs, slots.data_ptr(), k_scale.data_ptr(),
-        v_scale.data_ptr(), kd, _stream(stream)))
+        v_scale.data_ptr(), kd, _stream(stream, device)))
 
 
 def kv4_cache_read(cache: torch.Tensor, slots: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
@@ -539,12 +552,12 @@ def kv4_cache_read(cache: torch.Tensor, slots: torch.Tensor, k_scale: torch.Tens
     """The values that the tokens at `slots` stand for, into k and v (bf16 /
     fp16 [tokens, num_kv_heads, head_dim]); zeros for a slot outside the
     cache.  Arguments as for kv4_cache_write."""
-    nb, bs, sizes, kd = _kv4_tokens(k, v, cache, slots, k_scale, v_scale, kind)
+    nb, bs, sizes, kd, device = _kv4_tokens(k, v, cache, slots, k_scale, v_scale, kind)
     if sizes[1] == 0:
         return
     check(_lib.load().w8a8_kv4_cache_read(
         cache.data_ptr(), nb, bs, slots.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), kd, k.data_ptr(),
-        v.data_ptr(), *sizes, _stream(stream)))
+        v.data_ptr(), *sizes, _stream(stream, device)))
 
 
 def build_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_blocks: torch.Tensor,
@@ -576,12 +589,12 @@ def build_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_
     _vectors((("slots", slots, tokens),), torch.int64)
     if free_count_out is not None:
         _vectors((("free_count_out", free_count_out, 1),), torch.int32)
-    _cuda(context_lens, new_lens, free_blocks, free_count, block_table, query_start, seq_lens, slots, positions, free_left,
-          free_count_out)
+    device = _cuda(context_lens, new_lens, free_blocks, free_count, block_table, query_start, seq_lens, slots, positions,
+                   free_left, free_count_out)
     check(_lib.load().w8a8_build_block_tables(
         context_lens.data_ptr(), new_lens.data_ptr(), batch, free_blocks.data_ptr(), free_count.data_ptr(), ids,
         block_table.data_ptr(), max_blocks, block_size, query_start.data_ptr(), seq_lens.data_ptr(), slots.data_ptr(),
-        positions.data_ptr(), tokens, free_left.data_ptr(), _ptr(free_count_out), _stream(stream)))
+        positions.data_ptr(), tokens, free_left.data_ptr(), _ptr(free_count_out), _stream(stream, device)))
 
 
 def kv4_attention_workspace_size(batch: int, max_query_len: int, num_q_heads: int, num_kv_heads: int,
@@ -623,15 +636,16 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, 
     else:
         _vectors((("seq_lens", seq_lens, batch), ("query_start", query_start, batch + 1)), torch.int32)
     _one_scale(k_scale, v_scale)
-    _cuda(q, cache, seq_lens, block_table, k_scale, v_scale, out, query_start)
+    device = _cuda(q, cache, seq_lens, block_table, k_scale, v_scale, out, query_start)
+    handle = _stream(stream, device)
     kd = _kv4_kind(kind)
     if tokens == 0:
         return
-    need = _kv4_attention_need(q.get_device(), batch, max_query_len, hq, hkv, d)
+    need = _kv4_attention_need(device, batch, max_query_len, hq, hkv, d)
     if isinstance(workspace, Workspace):
         wbuf = workspace.ensure(need, stream).buf
     elif workspace is None:
-        wbuf = _default_workspace(q.device, need, "kv4_attention", stream).buf
+        wbuf = _default_workspace(device, need, "kv4_attention", stream, handle).buf
     else:
         wbuf = workspace
     if workspace is not None:
@@ -641,7 +655,7 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, 
     check(_lib.load().w8a8_kv4_attention(
         q.data_ptr(), _fkind(q), tokens, hq, hkv, d, *qs, cache.data_ptr(), nb, bs, block_table.data_ptr(), max_blocks,
         seq_lens.data_ptr(), _ptr(query_start), batch, max_query_len, k_scale.data_ptr(), v_scale.data_ptr(), sm_scale, kd,
-        out.data_ptr(), _fkind(out), *os_, wbuf.data_ptr(), wbuf.numel() * wbuf.element_size(), _stream(stream)))
+        out.data_ptr(), _fkind(out), *os_, wbuf.data_ptr(), wbuf.numel() * wbuf.element_size(), handle))
 
 
 def verify_drafts(target_probs: torch.Tensor, draft_probs: torch.Tensor | None, draft_tokens: torch.Tensor,
@@ -673,10 +687,10 @@ def verify_drafts(target_probs: torch.Tensor, draft_probs: torch.Tensor | None, 
     _vectors((("draft_tokens", draft_tokens, rows), ("draft_start", draft_start, batch + 1),
               ("num_accepted", num_accepted, batch)), torch.int32)
     _vectors((("uniform", uniform, rows), ("sample_uniform", sample_uniform, batch)), torch.float32)
-    _cuda(target_probs, draft_probs, draft_tokens, draft_start, uniform, sample_uniform, out_tokens, num_accepted)
+    device = _cuda(target_probs, draft_probs, draft_tokens, draft_start, uniform, sample_uniform, out_tokens, num_accepted)
     check(_lib.load().w8a8_verify_drafts(
         target_probs.data_ptr(), _ptr(draft_probs),
         FP32 if target_probs.dtype is torch.float32 else _fkind(target_probs), vocab, _ld(target_probs),
         vocab if draft_probs is None else _ld(draft_probs), draft_tokens.data_ptr(), draft_start.data_ptr(), batch, rows,
         uniform.data_ptr(), sample_uniform.data_ptr(), out_tokens.data_ptr(), columns - 1, num_accepted.data_ptr(),
-        _stream(stream)))
+        _stream(stream, device)))

@@ -75,7 +75,7 @@ def world(monkeypatch):
 
     monkeypatch.setattr(api._lib, "load", lambda: Library())
     monkeypatch.setattr(api, "_default_ws", {})
-    monkeypatch.setattr(api, "_raw_stream", lambda index: World.current)
+    monkeypatch.setattr(api, "_gpus", lambda: 2)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: World.current, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: World.current in World.captured, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: World.device, raising=False)
@@ -272,3 +272,16 @@ def test_a_stream_has_to_be_of_the_current_device(world, call):
     with pytest.raises(ValueError, match="stream"):
         call(stream=Stream(61, index=1))
     assert not world.calls
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+@pytest.mark.parametrize("gpus", [1, 2])
+def test_no_tensor_of_the_host(world, monkeypatch, entry, gpus):
+    monkeypatch.setattr(api, "_gpus", lambda: gpus)
+    call, tensors = ENTRIES[entry]
+    make = lambda at: [m(*n).as_subclass(torch.Tensor) if i == at else m(*n) for i, (m, n) in enumerate(tensors)]  # noqa: E731
+    call(*make(None))
+    for i in range(len(tensors)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call(*make(i))
+    assert len(world.calls) == 1
