@@ -462,10 +462,11 @@ W8A8_API w8a8_status w8a8_kv4_cache_read(const void* cache, int64_t num_blocks, 
  *                 padding.  A request with a new token past `tokens` is
  *                 refused, as for want of blocks, and so is then every later
  *                 one with new tokens.
- *   free_left     int32 [1], the balance: free_count less the needs of
- *                 every request up to the last admitted one.  Refused requests
- *                 among them count as waiting for their blocks, so that a
- *                 negative number says how many blocks the list was short.
+ *   free_left     int32 [1], a balance, not a number of free ids: free_count
+ *                 less the needs of all requests up to the last admitted one,
+ *                 refused ones among them included.  It is negative where a
+ *                 request that needs no block stands behind refused ones, and
+ *                 says nothing of requests refused behind the last admitted.
  *   free_count_out  int32 [1] or NULL: the number of ids that are still free,
  *                 free_blocks[0 .. free_count_out - 1] (the next call's
  *                 free_count).
@@ -495,18 +496,23 @@ W8A8_API w8a8_status w8a8_build_block_tables(const int32_t* context_lens, const 
  *   seq_lens    int32 [batch], clamped to [0, max_blocks * block_size].
  *   query_start int32 [batch + 1], clamped to [0, tokens]; NULL: one token
  *               a request (tokens = batch).
- *   max_query_len  the largest n (rows of a request past it are not
- *               written).
+ *   max_query_len  the largest n or more (rows of a request past it are not
+ *               written).  Up to 32 rows a KV head (max_query_len, or tokens
+ *               if that is less, times the quotient of the head counts) run in
+ *               the kernel for few rows.
  *   workspace   w8a8_kv4_attention_workspace_size() bytes, 16-byte aligned,
  *               zero-filled before its first use; every call leaves its
  *               counters zero again.  Calls that may overlap on the GPU
  *               need workspaces of their own.
- * Scores, softmax statistics and sums are fp32; the softmax weights enter the
- * second product as f16 (11 bits; fewer below 2^-27 of a row's largest).  Limits: num_q_heads a multiple of
+ * Scores, softmax statistics and sums are fp32; the query enters the scores
+ * as f16 after a scaling of each row by a power of two (exact for bf16 and fp16
+ * down to 2^-28 of the row's largest element), the softmax weights the second
+ * product as f16 (11 bits; fewer below 2^-27 of a row's largest).  A NaN in
+ * k_scale, v_scale or sm_scale gives NaN.  Limits: num_q_heads a multiple of
  * num_kv_heads with a quotient of at most 64; max_blocks * block_size < 2^31
  * and its product with batch * num_kv_heads < 2^33; batch * max_query_len *
- * num_q_heads < 2^31; batch and head counts <= 65535.  The workspace size is 0 for sizes outside
- * the limits. */
+ * num_q_heads < 2^31; batch and head counts <= 65535.  The workspace size is 0
+ * for sizes outside the limits. */
 W8A8_API size_t w8a8_kv4_attention_workspace_size(int64_t batch, int64_t max_query_len, int64_t num_q_heads,
                                                   int64_t num_kv_heads, int64_t head_dim);
 
@@ -536,7 +542,8 @@ W8A8_API w8a8_status w8a8_kv4_attention(
  *   out_tokens   int32 [batch, max_drafts + 1]: kept tokens, the drawn one
  *                (-1 if no token has any probability), then -1.
  *   num_accepted int32 [batch], the number kept.
- * Comparisons and sums are made in 64 bits. */
+ * uniform_i * q_i(x_i) and the comparisons are made in 64 bits, the sums over
+ * a row in pairs of fp32 numbers (about 48 bits), joined in 64. */
 W8A8_API w8a8_status w8a8_verify_drafts(const void* target_probs, const void* draft_probs, int dtype,
                                         int64_t vocab, int64_t target_ld, int64_t draft_ld,
                                         const int32_t* draft_tokens, const int32_t* draft_start, int64_t batch,

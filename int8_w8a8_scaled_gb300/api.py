@@ -574,9 +574,9 @@ def build_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_
     query_start (int32 [batch + 1]), seq_lens (int32 [batch]; 0 for a request
     that its table, the free list or the packed tokens have no room for), slots (int64) and
     positions (int32) of the packed tokens (-1 and 0 past the last one, -1 for
-    a refused request's), free_left (int32 [1], the balance: free_count less
-    the needs up to the last admitted request, negative by the blocks that the
-    list was short) and free_count_out (int32 [1], optional: the ids still
+    a refused request's), free_left (int32 [1], a balance: free_count less the
+    needs of all requests up to the last admitted one, refused ones among them
+    included, so that it may be negative) and free_count_out (int32 [1], optional: the ids still
     free, the next call's free_count).  None of them may share memory with an
     input or with each other."""
     if block_table.dtype is not torch.int32 or block_table.ndim != 2 or not block_table.is_contiguous():
@@ -619,9 +619,11 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, 
     strides.  seq_lens: int32 [batch], lengths with the new tokens.
     block_table: int32 [batch, max_blocks].  query_start: int32 [batch + 1],
     the first row of each request in q, with max_query_len the most rows of
-    one; None: one row a request.  Row i of a request's n sees its tokens
+    one (or more; rows past it are not written); None: one row a request.  Row i of a request's n sees its tokens
     t <= seq_len - n + i; a row that sees none gives zeros.  sm_scale defaults
-    to 1 / sqrt(head_dim)."""
+    to 1 / sqrt(head_dim).  workspace: a Workspace, or a zero-filled uint8
+    tensor of kv4_attention_workspace_size(); None: the default one of the
+    stream that the call runs on."""
     nb, hkv, bs, d = _kv4_cache(cache)
     shape = q.shape
     if len(shape) != 3 or shape[2] != d:

@@ -58,10 +58,11 @@
 //      same + 8: the K reads are then free of bank conflicts (V's two-way).
 //
 // Measured (device time, cold L2): 64 requests up to 8192 tokens, 8 KV heads of
-// 128, 4 query heads each: 88 us, 3.9 TB/s of the cache (58 % of the 6.78 TB/s
-// that a copy reaches; the steps run at 88 % of it, the rest is the launch, the
-// first copies and the joins); 128 requests up to 16384: 262 us, 5.3 TB/s (78 %);
-// one request of 1023: 18 us, of which the launch and the measurement are 6.
+// 128, 4 query heads each: 88 us, 3.9 TB/s of the cache (58 % of the 6.7 TB/s that
+// a copy reaches; the steps run at 88 % of it, the rest is the launch, the first
+// copies and the joins); heads of 64: 62 us, 2.8 TB/s; 128 requests up to 16384:
+// 269 us, 5.1 TB/s (77 %); one request of 1023: 17 us, of which the launch and the
+// measurement are 6.
 #include <algorithm>
 
 #include "internal.h"
@@ -74,7 +75,10 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-constexpr int kSmallRows = 32;                   // at most two groups of 16
+// At most two groups of 16.  20 rows (32 requests of up to 4096 tokens, cold): 79 us
+// here, 121 in the many-rows kernel, which takes 128 rows at a time; one group 57.
+// A third group was not tried.
+constexpr int kSmallRows = 32;
 constexpr float kHeadroom = 2.f;
 constexpr float kNoScore = -1e25f;               // below any product, and finite
 constexpr int kMaxCounters = 1024;               // CTAs that may leave a unit open

@@ -11,7 +11,10 @@
 //                                                    dims contiguous)
 // The decoded cache is exact in f16; a row of Q is scaled by a power of two
 // before its conversion; the weights are f16(2^(s - m + 13)), with the maximum
-// m raised (and O rescaled) only when a score passes it by 2^2.
+// m raised (and O rescaled) only when a score passes it by 2^2.  The sum that
+// divides is of the weights in fp32, each off by at most 2^-11 of itself from the
+// one in the product: widening the rounded ones again would lengthen the softmax,
+// which is what bounds this kernel (few rows get their sum from one more MMA).
 //
 // One CTA to an SM, 22 warps: two slots of 8 softmax warps, one warp that
 // copies the codes, four that decode K and V into swizzled tiles two deep, one
@@ -30,8 +33,10 @@
 // cycle) and the shared memory about 2300 for their operands and the decoded
 // tiles; a turn takes about 4200: what bounds it now is the chain of one slot,
 // softmax (1800) - product with V - next scores - softmax, as S and P share their
-// TMEM columns.  2 x 4000 new tokens after 4200, 32 query and 8 KV heads of 128:
-// 781 us, 1.04 PFLOP/s, 54 % of the 1.91 that a bf16 matrix product reaches.
+// TMEM columns (P fills half of them; scores into the other half meanwhile were not
+// tried).  2 x 4000 new tokens after 4200, 32 query and 8 KV heads of 128: 801 us,
+// 1.01 PFLOP/s, 52 % of the 1.97 that a bf16 matrix product reaches; heads of 64:
+// 641 us, 0.63 PFLOP/s.
 //
 // A unit is one request, KV head and 256 rows; its work is the token tiles up
 // to the last one that its last row sees.  All units' tiles in a row are cut
