@@ -108,14 +108,15 @@ class Workspace:
     """A zero-filled device scratch buffer reused across calls on one stream.
 
     The matmul's split-K counters must start at zero; the library leaves them
-    at zero after each successful call, so the buffer only needs zeroing once.
-    It is zeroed on the stream that is current where it is made: a call on
-    another stream has to come after that (``wait_stream``).  A buffer that a
-    call makes larger is zeroed on that call's stream.
+    at zero after each successful call, so the buffer only needs zeroing once,
+    on the stream that is current where it is made (a larger one that a call
+    needs: on that call's stream).  The first call on another stream waits for
+    the zeroing; what calls on several streams do with the buffer is for their
+    caller to order.
 
     A buffer that a captured call uses is kept as long as the Workspace, so that
-    the graph can be replayed after the Workspace has grown.  Make it large
-    enough before the capture: a captured call that needs more gets a buffer of
+    the graph can be replayed after the Workspace has grown.  Make it before the
+    capture and large enough: a captured call that needs more gets a buffer of
     the graph's own, which every replay zeroes.  A replay counts as calls on the
     stream that it runs on: where it may overlap others, give it a Workspace of
     its own.
@@ -123,20 +124,34 @@ class Workspace:
 
     def __init__(self, nbytes: int = 0, device=None):
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-        self.buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.device)
         self._captured = []          # buffers that graphs hold the address of
+        self._zero(max(nbytes, 256), torch.cuda.current_stream(self.device))
+
+    def _zero(self, nbytes: int, stream) -> None:
+        """A new buffer, zeroed on `stream`, the current one."""
+        self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        self._ordered = {stream.cuda_stream}        # streams that come after the zeroing
+        self._zeroed = None if _capturing() else stream.record_event()
 
     def ensure(self, nbytes: int, stream=None) -> "Workspace":
         """At least nbytes, for a call on `stream` (None: the current one)."""
+        handle = torch._C._cuda_getCurrentRawStream(self.buf.get_device()) if stream is None else stream.cuda_stream
+        capturing = handle != 0 and _capturing()    # (the legacy default stream, handle 0, cannot be captured)
         if nbytes <= self.buf.numel():
-            if _capturing() and not (self._captured and self._captured[-1] is self.buf):
-                self._captured.append(self.buf)
+            if capturing:
+                if not (self._captured and self._captured[-1] is self.buf):
+                    self._captured.append(self.buf)
+            elif handle not in self._ordered and self._zeroed is not None:
+                with _launching_on(self.device, stream) as launch:
+                    launch.wait_event(self._zeroed)
+                    self.buf.record_stream(launch)
+                self._ordered.add(handle)
             return self
         with _launching_on(self.device, stream) as launch:
             if _capturing():
                 return Workspace(nbytes, self.device)
             self.buf.record_stream(launch)          # earlier calls there may still use it
-            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            self._zero(nbytes, launch)
         return self
 
     @property

@@ -125,3 +125,21 @@ def test_a_graph_outlives_the_growth_of_its_default_workspace(no_workspaces):
             g.replay()
             assert torch.equal(out, want)
         assert (junk == 0xFF).all()
+
+
+@pytest.mark.parametrize("problem", PROBLEMS)
+def test_a_workspace_of_another_stream_given_up_at_once(problem, no_workspaces):
+    """Made on the current stream behind much other work, used on another one, and
+    dropped while that call runs."""
+    call, like = PROBLEMS[problem](5)
+    want = torch.empty_like(like)
+    call(want)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = [torch.empty_like(like) for _ in range(20)]
+    for out in outs:
+        torch.cuda._sleep(200000)
+        call(out, stream=s, workspace=w8.Workspace(64 << 20))
+        torch.full((64 << 20,), 0xFF, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, want) for out in outs)

@@ -35,6 +35,13 @@ class Stream:
     def __init__(self, handle, index=0):
         self.cuda_stream, self.device_index = handle, index
 
+    def record_event(self):
+        World.events.append(self.cuda_stream)
+        return len(World.events) - 1
+
+    def wait_event(self, event):
+        World.waits.append((self.cuda_stream, event))
+
 
 class World:
     """What the fake CUDA saw."""
@@ -43,6 +50,7 @@ class World:
     device = 0            # the current device
     zeroed = []           # (address, handle of the stream that the zeroing is ordered on)
     kept = []
+    events, waits = [], []    # the streams that events were recorded on; (stream, event waited for)
     calls = []            # (name, arguments)
 
 
@@ -61,6 +69,7 @@ class Library:
 @pytest.fixture
 def world(monkeypatch):
     World.current, World.device, World.zeroed, World.kept, World.calls, World.captured, Library.need = 7, 0, [], [], [], set(), 4096
+    World.events, World.waits = [], []
 
     @contextlib.contextmanager
     def on(stream):
@@ -285,3 +294,21 @@ def test_no_tensor_of_the_host(world, monkeypatch, entry, gpus):
         with pytest.raises(ValueError, match="CUDA"):
             call(*make(i))
     assert len(world.calls) == 1
+
+
+@pytest.mark.parametrize("call", [c for c in CALLS if c is not quantise])
+def test_a_workspace_made_on_another_stream_is_waited_for_once(world, call):
+    ws = w8.Workspace(4096, device="cuda:0")                 # zeroed on stream 7
+    assert world.events == [7]
+    for _ in range(2):
+        call(stream=Stream(71), workspace=ws)
+    world.current = 72
+    call(workspace=ws)
+    assert world.waits == [(71, 0), (72, 0)]
+    assert {handle for _, handle in world.kept} == {71, 72}   # freed only behind what runs there
+    world.current = 7
+    call(workspace=ws)
+    assert len(world.waits) == 2
+    world.captured, world.current = {73}, 73
+    call(workspace=ws)                                        # no wait for what lies outside the capture
+    assert len(world.waits) == 2
