@@ -552,6 +552,151 @@ W8A8_API w8a8_status w8a8_verify_drafts(const void* target_probs, const void* dr
                                         w8a8_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Long contexts over the paged fp8 KV cache
+ *
+ * The cache that w8a8_fp8_kv_decode_attention reads, filled by slots and read
+ * by any number of new tokens: k_cache and v_cache are [num_blocks,
+ * block_size, num_kv_heads, head_dim] e4m3 codes with one fp32 scale each.
+ * head_dim is 64 or 128, block_size a multiple of 16 up to 8192, num_blocks *
+ * block_size below 2^31, the bases 16-byte aligned.  Token t of a request is
+ * token t % block_size of block block_table[b * max_blocks + t / block_size];
+ * tokens of a block whose id is outside [0, num_blocks) are skipped.
+ * Request b's new tokens are rows query_start[b] .. query_start[b + 1] - 1 of
+ * q (int32 [batch + 1], clamped to [0, tokens]; NULL: one token a request,
+ * tokens = batch), of which the first max_query_len are looked at; seq_lens
+ * (int32 [batch], clamped to [0, max_blocks * block_size]) counts them in.
+ * Row i of a request's n new tokens stands at position p = seq_lens[b] - n + i
+ * and sees the tokens t <= p.  Rows that belong to no request, or lie past
+ * max_query_len, are left as they are.  All calls are asynchronous, allocate
+ * nothing and can be captured in a CUDA graph.
+ * ---------------------------------------------------------------------- */
+
+/* Rotates queries and keys by their positions and writes keys and values into
+ * the cache.  Pair i of the first rot_dim dims of a head (dims i and i +
+ * rot_dim / 2, or with `interleaved` 2 i and 2 i + 1) becomes
+ *   (x cos - y sin, y cos + x sin),
+ * each product and sum rounded to fp32, with the angle of row positions[a *
+ * tokens + token] of cos_sin, a the axis of the pair; other dims stay.  q is
+ * rounded once into q_out; k / k_scale and v / v_scale (correctly rounded fp32
+ * quotients) become e4m3 codes as in w8a8_scaled_quant with W8A8_STATIC.
+ *   q, k, v   [tokens, heads, head_dim] bf16 or fp16 (dtype), a head's dims
+ *             consecutive, token and head strides in elements.  num_q_heads
+ *             may be 0: then q and q_out are not looked at.
+ *   q_out     as q; q itself (same pointer and strides) or memory of its own.
+ *   cos_sin   fp32 [max_position, rot_dim]: cosines of the rot_dim / 2 pairs,
+ *             then sines.  A position outside it gives NaN for its pairs.
+ *   positions int32 [axes, tokens]; axes is 1 to 4.
+ *   sections  HOST array of `axes` counts that add up to rot_dim / 2: pairs of
+ *             the first axis, then of the second, ...; NULL for one axis.
+ *   slots     int64 [tokens], block * block_size + offset; a slot outside the
+ *             cache is skipped (the query is rotated all the same).  No slot
+ *             twice in a call.
+ * rot_dim is even, 2 .. head_dim.  Alignment: 2 bytes; 16-byte aligned bases
+ * and strides with rot_dim a multiple of 16 take the vectorised path. */
+W8A8_API w8a8_status w8a8_fp8_kv_rotate_write(
+    const void* q, const void* k, const void* v, int dtype, int64_t tokens, int64_t num_q_heads,
+    int64_t num_kv_heads, int64_t head_dim, int64_t q_token_stride, int64_t q_head_stride,
+    int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+    const float* cos_sin, int64_t max_position, int64_t rot_dim, const int32_t* positions, int axes,
+    const int32_t* sections, int interleaved, void* k_cache, void* v_cache, int64_t num_blocks,
+    int64_t block_size, const int64_t* slots, const float* k_scale, const float* v_scale, void* q_out,
+    int64_t q_out_token_stride, int64_t q_out_head_stride, w8a8_stream_t stream);
+
+/* Attention of the new tokens over the cache (their own K and V already in it):
+ *   s_t = sm_scale * sum_d q[i,h,d] K[t,d],  out[i,h,:] = sum_t softmax(s)_t V[t,:]
+ * for every query head h, KV head h / (num_q_heads / num_kv_heads), with K and
+ * V the codes times k_scale and v_scale.  A row that sees no token gives zeros.
+ * What a row does not see has no part in it, NaN codes included; a NaN or an
+ * infinity in q[i,h,:] gives NaN in that row.
+ *   q, out      [tokens, num_q_heads, head_dim] bf16 / fp16, a head's dims
+ *               consecutive, token and head strides in elements; out may not
+ *               share memory with q.
+ *   max_query_len  the largest number of new tokens of a request, or more.
+ *   workspace   w8a8_fp8_kv_paged_attention_workspace_size() bytes, 16-byte
+ *               aligned, zero-filled before its first use; every call leaves
+ *               its counters zero again.  Calls that may overlap on the GPU
+ *               need workspaces of their own.
+ * Limits: num_q_heads a multiple of num_kv_heads with a quotient of at most 64;
+ * max_blocks * block_size < 2^31 and its product with batch * num_kv_heads <
+ * 2^33; batch * max_query_len * num_q_heads < 2^31; batch and head counts <=
+ * 65535.  The workspace size is 0 for sizes outside the limits. */
+W8A8_API size_t w8a8_fp8_kv_paged_attention_workspace_size(int64_t batch, int64_t max_query_len,
+                                                           int64_t num_q_heads, int64_t num_kv_heads,
+                                                           int64_t head_dim);
+
+W8A8_API w8a8_status w8a8_fp8_kv_paged_attention(
+    const void* q, int q_dtype, int64_t tokens, int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
+    int64_t q_token_stride, int64_t q_head_stride, const void* k_cache, const void* v_cache,
+    int64_t num_blocks, int64_t block_size, const int32_t* block_table, int64_t max_blocks,
+    const int32_t* seq_lens, const int32_t* query_start, int64_t batch, int64_t max_query_len,
+    const float* k_scale, const float* v_scale, float sm_scale, void* out, int out_dtype,
+    int64_t out_token_stride, int64_t out_head_stride, void* workspace, size_t workspace_bytes,
+    w8a8_stream_t stream);
+
+/* 8-bit means of the keys of the blocks that got new tokens, columns (L - n) /
+ * block_size .. (L - 1) / block_size of each request of L tokens, n of them
+ * new.  For each KV head, over the tokens of the block that lie below L:
+ *   mean = fl(sum of the codes' values) / count,  scale = absmax / 127 (1 if
+ *   that is 0),  code = round(mean / scale), half to even,
+ * the sum exact (NaN codes count as 0), the quotients correctly rounded fp32.
+ * The means are in units of k_scale, which has no part in their order.
+ *   means        int8 [num_blocks, num_kv_heads, head_dim], 16-byte aligned
+ *   mean_scales  fp32 [num_blocks, num_kv_heads]
+ * Rows of other blocks are left as they are.  No block of two requests in a
+ * call may be among the written ones. */
+W8A8_API w8a8_status w8a8_fp8_kv_block_means(const void* k_cache, int64_t num_blocks, int64_t block_size,
+                                             int64_t num_kv_heads, int64_t head_dim,
+                                             const int32_t* block_table, int64_t max_blocks,
+                                             const int32_t* seq_lens, const int32_t* query_start,
+                                             int64_t tokens, int64_t batch, int64_t max_query_len,
+                                             int8_t* means, float* mean_scales, w8a8_stream_t stream);
+
+/* For each new token and KV head the blocks that matter most to it, by the
+ * 8-bit means.  Each query head's row is quantised to int8 like a row in
+ * w8a8_scaled_quant (dynamic); the score of a block is
+ *   fl(max over the KV head's query heads of fl(dot * q_scale) * mean_scale),
+ * dot the exact product of the codes.  Of the blocks up to the token's own
+ * (column p / block_size) the first first_blocks and the last last_blocks are
+ * taken, then those of the highest scores, the lower column of equal ones
+ * (NaN, and blocks outside the cache, count as the lowest).
+ *   selected   int32 [tokens, num_kv_heads, budget]: columns of the block
+ *              table in rising order, then -1.
+ *   workspace  w8a8_fp8_kv_select_blocks_workspace_size() bytes, 16-byte
+ *              aligned; holds nothing from one call to the next.
+ * first_blocks >= 0, last_blocks >= 1, their sum at most budget;
+ * max_blocks <= 49152; num_q_heads / num_kv_heads at most 64. */
+W8A8_API size_t w8a8_fp8_kv_select_blocks_workspace_size(int64_t tokens, int64_t num_kv_heads, int64_t max_blocks);
+
+W8A8_API w8a8_status w8a8_fp8_kv_select_blocks(
+    const void* q, int q_dtype, int64_t tokens, int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
+    int64_t q_token_stride, int64_t q_head_stride, const int8_t* means, const float* mean_scales,
+    int64_t num_blocks, int64_t block_size, const int32_t* block_table, int64_t max_blocks,
+    const int32_t* seq_lens, const int32_t* query_start, int64_t batch, int64_t max_query_len,
+    int64_t first_blocks, int64_t last_blocks, int64_t budget, int32_t* selected, void* workspace,
+    size_t workspace_bytes, w8a8_stream_t stream);
+
+/* Attention of each new token over the blocks selected for it and its KV head:
+ * as w8a8_fp8_kv_paged_attention, the sums over the tokens t <= p of the
+ * columns in selected[token, kv head, :] alone.  Entries outside [0,
+ * max_blocks) are skipped, those past the token's own block see nothing; a
+ * column named twice counts twice.
+ *   workspace  w8a8_fp8_kv_sparse_attention_workspace_size() bytes, 16-byte
+ *              aligned, zero-filled before its first use and left so.
+ * budget * block_size < 2^24; the other limits as above. */
+W8A8_API size_t w8a8_fp8_kv_sparse_attention_workspace_size(int64_t tokens, int64_t num_q_heads,
+                                                            int64_t num_kv_heads, int64_t head_dim,
+                                                            int64_t budget, int64_t block_size);
+
+W8A8_API w8a8_status w8a8_fp8_kv_sparse_attention(
+    const void* q, int q_dtype, int64_t tokens, int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
+    int64_t q_token_stride, int64_t q_head_stride, const void* k_cache, const void* v_cache,
+    int64_t num_blocks, int64_t block_size, const int32_t* block_table, int64_t max_blocks,
+    const int32_t* seq_lens, const int32_t* query_start, int64_t batch, int64_t max_query_len,
+    const int32_t* selected, int64_t budget, const float* k_scale, const float* v_scale, float sm_scale,
+    void* out, int out_dtype, int64_t out_token_stride, int64_t out_head_stride, void* workspace,
+    size_t workspace_bytes, w8a8_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Scaled matmul without a caller-provided workspace
  *
  * No counterpart on the source pages: this entry point exists for callers

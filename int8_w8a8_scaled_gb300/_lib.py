@@ -58,6 +58,14 @@ EXPORTS = (
     "w8a8_kv4_attention_workspace_size",
     "w8a8_kv4_attention",
     "w8a8_verify_drafts",
+    "w8a8_fp8_kv_rotate_write",
+    "w8a8_fp8_kv_paged_attention_workspace_size",
+    "w8a8_fp8_kv_paged_attention",
+    "w8a8_fp8_kv_block_means",
+    "w8a8_fp8_kv_select_blocks_workspace_size",
+    "w8a8_fp8_kv_select_blocks",
+    "w8a8_fp8_kv_sparse_attention_workspace_size",
+    "w8a8_fp8_kv_sparse_attention",
 )
 
 
@@ -152,6 +160,27 @@ def load(build_if_needed: bool = True):
                                            P, P, ctypes.c_float, I, P, I, I64, I64, P, SZ, P]
         lib.w8a8_verify_drafts.restype = I
         lib.w8a8_verify_drafts.argtypes = [P, P, I, I64, I64, I64, P, P, I64, I64, P, P, P, I64, P, P]
+        F = ctypes.c_float
+        lib.w8a8_fp8_kv_rotate_write.restype = I
+        lib.w8a8_fp8_kv_rotate_write.argtypes = [P, P, P, I, I64, I64, I64, I64, I64, I64, I64, I64, I64, I64, P, I64, I64, P, I, P,
+                                                 I, P, P, I64, I64, P, P, P, P, I64, I64, P]
+        lib.w8a8_fp8_kv_paged_attention_workspace_size.restype = SZ
+        lib.w8a8_fp8_kv_paged_attention_workspace_size.argtypes = [I64, I64, I64, I64, I64]
+        lib.w8a8_fp8_kv_paged_attention.restype = I
+        lib.w8a8_fp8_kv_paged_attention.argtypes = [P, I, I64, I64, I64, I64, I64, I64, P, P, I64, I64, P, I64, P, P, I64, I64, P, P,
+                                                    F, P, I, I64, I64, P, SZ, P]
+        lib.w8a8_fp8_kv_block_means.restype = I
+        lib.w8a8_fp8_kv_block_means.argtypes = [P, I64, I64, I64, I64, P, I64, P, P, I64, I64, I64, P, P, P]
+        lib.w8a8_fp8_kv_select_blocks_workspace_size.restype = SZ
+        lib.w8a8_fp8_kv_select_blocks_workspace_size.argtypes = [I64, I64, I64]
+        lib.w8a8_fp8_kv_select_blocks.restype = I
+        lib.w8a8_fp8_kv_select_blocks.argtypes = [P, I, I64, I64, I64, I64, I64, I64, P, P, I64, I64, P, I64, P, P, I64, I64, I64,
+                                                  I64, I64, P, P, SZ, P]
+        lib.w8a8_fp8_kv_sparse_attention_workspace_size.restype = SZ
+        lib.w8a8_fp8_kv_sparse_attention_workspace_size.argtypes = [I64, I64, I64, I64, I64, I64]
+        lib.w8a8_fp8_kv_sparse_attention.restype = I
+        lib.w8a8_fp8_kv_sparse_attention.argtypes = [P, I, I64, I64, I64, I64, I64, I64, P, P, I64, I64, P, I64, P, P, I64, I64, P,
+                                                     I64, P, P, F, P, I, I64, I64, P, SZ, P]
         lib.w8a8_device_status.restype = I
         lib.w8a8_device_status.argtypes = [ctypes.POINTER(ctypes.c_int)]
         _lib = lib

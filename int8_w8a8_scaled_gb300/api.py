@@ -32,7 +32,9 @@ __all__ = [
     "quant_workspace_size", "pick_config", "device_status", "Workspace", "quant_scaled_mm",
     "expand_shard_scales", "requant_shards", "fp8_kv_decode_attention", "attention_workspace_size",
     "kv4_cache_shape", "kv4_cache_write", "kv4_cache_read", "build_block_tables", "kv4_attention",
-    "kv4_attention_workspace_size", "verify_drafts",
+    "kv4_attention_workspace_size", "verify_drafts", "fp8_kv_rotate_write", "fp8_kv_attention",
+    "fp8_kv_attention_workspace_size", "fp8_kv_block_means", "fp8_kv_select_blocks",
+    "fp8_kv_select_blocks_workspace_size", "fp8_kv_sparse_attention", "fp8_kv_sparse_attention_workspace_size",
     "W8A8Error", "MmConfig",
 ]
 
@@ -711,3 +713,280 @@ def verify_drafts(target_probs: torch.Tensor, draft_probs: torch.Tensor | None, 
         vocab if draft_probs is None else _ld(draft_probs), draft_tokens.data_ptr(), draft_start.data_ptr(), batch, rows,
         uniform.data_ptr(), sample_uniform.data_ptr(), out_tokens.data_ptr(), columns - 1, num_accepted.data_ptr(),
         _stream(stream, device)))
+
+
+# ---------------------------------------------------------------- long contexts over the paged fp8 KV cache
+
+
+def _fp8_cache(cache: torch.Tensor, name: str) -> tuple:
+    """(num_blocks, block_size, num_kv_heads, head_dim) of an fp8 cache."""
+    if cache.ndim != 4 or not cache.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [num_blocks, block_size, num_kv_heads, head_dim] tensor")
+    if cache.dtype is not torch.float8_e4m3fn and cache.dtype is not torch.uint8:
+        raise TypeError(f"{name} must hold float8_e4m3fn codes (or a uint8 view)")
+    return tuple(cache.shape)
+
+
+def _fp8_caches(k_cache: torch.Tensor, v_cache: torch.Tensor) -> tuple:
+    shape = _fp8_cache(k_cache, "k_cache")
+    if _fp8_cache(v_cache, "v_cache") != shape:
+        raise ValueError("k_cache and v_cache must have one shape")
+    return shape
+
+
+def _paged_rows(seq_lens: torch.Tensor, block_table: torch.Tensor, query_start: torch.Tensor | None) -> tuple:
+    """(batch, max_blocks) of a step's requests."""
+    if block_table.dtype is not torch.int32 or block_table.ndim != 2 or not block_table.is_contiguous():
+        raise ValueError("block_table must be a contiguous int32 [batch, max_blocks] CUDA tensor")
+    batch, max_blocks = block_table.shape
+    if query_start is None:
+        _vectors((("seq_lens", seq_lens, batch),), torch.int32)
+    else:
+        _vectors((("seq_lens", seq_lens, batch), ("query_start", query_start, batch + 1)), torch.int32)
+    return batch, max_blocks
+
+
+def _scratch(workspace, need: int, kind: str, device: int, stream, handle: int, like: torch.Tensor) -> torch.Tensor:
+    """A call's scratch: its caller's, or the default one of its stream."""
+    if workspace is None:
+        return _default_workspace(device, need, kind, stream, handle).buf
+    buf = workspace.ensure(need, stream).buf if isinstance(workspace, Workspace) else workspace
+    _cuda(like, buf)
+    return buf
+
+
+def fp8_kv_rotate_write(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor,
+                        positions: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, slots: torch.Tensor,
+                        k_scale: torch.Tensor, v_scale: torch.Tensor, q_out: torch.Tensor | None, sections=None,
+                        interleaved: bool = False, stream=None) -> None:
+    """Rotate queries and keys by their positions, and write keys and values
+    into the paged fp8 cache at their slots.
+
+    q: [tokens, num_q_heads, head_dim], k, v: [tokens, num_kv_heads,
+    head_dim], bf16 / fp16, any token and head strides.  cos_sin: float32
+    [max_position, rot_dim], cosines of the rot_dim / 2 pairs, then sines;
+    pairs are dims i and i + rot_dim / 2 of a head, with interleaved 2 i and
+    2 i + 1; dims from rot_dim on stay.  positions: int32 [tokens], or
+    [axes, tokens] with sections, the number of pairs that turn by each axis
+    (they add up to rot_dim / 2); one outside cos_sin gives NaN.  k_cache,
+    v_cache: [num_blocks, block_size, num_kv_heads, head_dim] float8_e4m3fn (or
+    uint8 views).  slots: int64 [tokens] (block * block_size + offset; one
+    outside the cache is skipped).  k_scale, v_scale: float32 [1].  q_out:
+    rotated queries, as q; q itself is fine.  q and q_out may be None."""
+    nb, bs, h, d = _fp8_caches(k_cache, v_cache)
+    if k.ndim != 3:
+        raise ValueError("k and v must be [tokens, num_kv_heads, head_dim]")
+    n = k.shape[0]
+    ks, vs = _heads("k", k, (n, h, d)), _heads("v", v, (n, h, d))
+    if v.dtype is not k.dtype:
+        raise TypeError("q, k, v and q_out must have the same element type")
+    hq, qs, os_ = 0, (0, 0), (0, 0)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        if q.ndim != 3:
+            raise ValueError("q must be [tokens, num_q_heads, head_dim]")
+        hq = q.shape[1]
+        qs, os_ = _heads("q", q, (n, hq, d)), _heads("q_out", q_out, (n, hq, d))
+        if q.dtype is not k.dtype or q_out.dtype is not k.dtype:
+            raise TypeError("q, k, v and q_out must have the same element type")
+    if cos_sin.dtype is not torch.float32 or cos_sin.ndim != 2 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be a contiguous float32 [max_position, rot_dim] tensor")
+    axes, counts = 1, None
+    if sections is not None:
+        axes = len(sections)
+        if not 1 <= axes <= 4:
+            raise ValueError("there are 1 to 4 sections")
+        counts = (ctypes.c_int32 * axes)(*sections)
+    if positions.dtype is not torch.int32 or not positions.is_contiguous() or \
+            tuple(positions.shape) not in (((axes, n), (n,)) if axes == 1 else ((axes, n),)):
+        raise ValueError(f"positions must be a contiguous int32 {'[tokens]' if axes == 1 else f'[{axes}, tokens]'} tensor")
+    _vectors((("slots", slots, n),), torch.int64)
+    _one_scale(k_scale, v_scale)
+    device = _cuda(q, k, v, cos_sin, positions, k_cache, v_cache, slots, k_scale, v_scale, q_out)
+    dtype = _fkind(k)
+    if n == 0:
+        return
+    check(_lib.load().w8a8_fp8_kv_rotate_write(
+        _ptr(q), k.data_ptr(), v.data_ptr(), dtype, n, hq, h, d, *qs, *ks, *vs, cos_sin.data_ptr(), *cos_sin.shape,
+        positions.data_ptr(), axes, counts, int(interleaved), k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, slots.data_ptr(),
+        k_scale.data_ptr(), v_scale.data_ptr(), _ptr(q_out), *os_, _stream(stream, device)))
+
+
+def fp8_kv_attention_workspace_size(batch: int, max_query_len: int, num_q_heads: int, num_kv_heads: int,
+                                    head_dim: int) -> int:
+    return int(_lib.load().w8a8_fp8_kv_paged_attention_workspace_size(batch, max_query_len, num_q_heads, num_kv_heads, head_dim))
+
+
+@functools.lru_cache(maxsize=4096)
+def _fp8_attention_need(device_index: int, *sizes: int) -> int:
+    """The same, looked up once for a device and sizes (it depends on nothing else)."""
+    return fp8_kv_attention_workspace_size(*sizes)
+
+
+def fp8_kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, seq_lens: torch.Tensor,
+                     block_table: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor, out: torch.Tensor,
+                     query_start: torch.Tensor | None = None, max_query_len: int = 1, sm_scale: float | None = None,
+                     workspace=None, stream=None) -> None:
+    """Attention of new tokens (single ones, drafts, prompt chunks) over the
+    paged fp8 cache that holds their keys and values already.
+
+    q, out: [tokens, num_q_heads, head_dim] bf16 / fp16, any token and head
+    strides; out may not share memory with q.  k_cache, v_cache:
+    [num_blocks, block_size, num_kv_heads, head_dim] float8_e4m3fn (or uint8
+    views), block_size a multiple of 16, head_dim 64 or 128.  seq_lens: int32
+    [batch], lengths with the new tokens.  block_table: int32 [batch,
+    max_blocks].  query_start: int32 [batch + 1], the first row of each request
+    in q, with max_query_len the most rows of one (or more; rows past it are
+    not written); None: one row a request.  Row i of a request's n sees its
+    tokens t <= seq_len - n + i; a row that sees none gives zeros.  sm_scale
+    defaults to 1 / sqrt(head_dim).  workspace: a Workspace, or a zero-filled
+    uint8 tensor of fp8_kv_attention_workspace_size(); None: the default one of
+    the stream that the call runs on."""
+    nb, bs, hkv, d = _fp8_caches(k_cache, v_cache)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != d:
+        raise ValueError("q must be [tokens, num_q_heads, head_dim] with the cache's head_dim")
+    tokens, hq, _ = shape
+    qs, os_ = _heads("q", q, shape), _heads("out", out, shape)
+    batch, max_blocks = _paged_rows(seq_lens, block_table, query_start)
+    _one_scale(k_scale, v_scale)
+    device = _cuda(q, k_cache, v_cache, seq_lens, block_table, k_scale, v_scale, out, query_start)
+    handle = _stream(stream, device)
+    if tokens == 0:
+        return
+    buf = _scratch(workspace, _fp8_attention_need(device, batch, max_query_len, hq, hkv, d), "fp8_attention", device, stream,
+                   handle, q)
+    if sm_scale is None:
+        sm_scale = 1.0 / float(d) ** 0.5
+    check(_lib.load().w8a8_fp8_kv_paged_attention(
+        q.data_ptr(), _fkind(q), tokens, hq, hkv, d, *qs, k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, block_table.data_ptr(),
+        max_blocks, seq_lens.data_ptr(), _ptr(query_start), batch, max_query_len, k_scale.data_ptr(), v_scale.data_ptr(), sm_scale,
+        out.data_ptr(), _fkind(out), *os_, buf.data_ptr(), buf.numel() * buf.element_size(), handle))
+
+
+def _block_means(means: torch.Tensor, mean_scales: torch.Tensor) -> tuple:
+    """(num_blocks, num_kv_heads, head_dim) of the blocks' means."""
+    if means.dtype is not torch.int8 or means.ndim != 3 or not means.is_contiguous():
+        raise ValueError("means must be a contiguous int8 [num_blocks, num_kv_heads, head_dim] tensor")
+    if mean_scales.dtype is not torch.float32 or mean_scales.shape != means.shape[:2] or not mean_scales.is_contiguous():
+        raise ValueError("mean_scales must be a contiguous float32 [num_blocks, num_kv_heads] tensor")
+    return tuple(means.shape)
+
+
+def fp8_kv_block_means(k_cache: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor, means: torch.Tensor,
+                       mean_scales: torch.Tensor, query_start: torch.Tensor | None = None, max_query_len: int = 1,
+                       stream=None) -> None:
+    """8-bit means of the keys of the blocks that a step wrote to, for
+    fp8_kv_select_blocks.
+
+    Written: the rows of means (int8 [num_blocks, num_kv_heads, head_dim]) and
+    mean_scales (float32 [num_blocks, num_kv_heads]) of the blocks that hold
+    the last n of each request's seq_len tokens, over the tokens that it
+    holds; other rows stay.  No block may belong to two requests of the call
+    there.  query_start: int32 [batch + 1], whose differences are the n, at
+    most max_query_len (both as for fp8_kv_attention); None: one each."""
+    nb, bs, h, d = _fp8_cache(k_cache, "k_cache")
+    if _block_means(means, mean_scales) != (nb, h, d):
+        raise ValueError("means must be [num_blocks, num_kv_heads, head_dim] of the cache")
+    batch, max_blocks = _paged_rows(seq_lens, block_table, query_start)
+    device = _cuda(k_cache, seq_lens, block_table, means, mean_scales, query_start)
+    if batch == 0:
+        return
+    # no row of q is looked at: any number of them that the starts may name
+    tokens = batch if query_start is None else (1 << 31) - 1
+    check(_lib.load().w8a8_fp8_kv_block_means(
+        k_cache.data_ptr(), nb, bs, h, d, block_table.data_ptr(), max_blocks, seq_lens.data_ptr(), _ptr(query_start), tokens, batch,
+        max_query_len, means.data_ptr(), mean_scales.data_ptr(), _stream(stream, device)))
+
+
+def fp8_kv_select_blocks_workspace_size(tokens: int, num_kv_heads: int, max_blocks: int) -> int:
+    return int(_lib.load().w8a8_fp8_kv_select_blocks_workspace_size(tokens, num_kv_heads, max_blocks))
+
+
+def fp8_kv_select_blocks(q: torch.Tensor, means: torch.Tensor, mean_scales: torch.Tensor, seq_lens: torch.Tensor,
+                         block_table: torch.Tensor, block_size: int, selected: torch.Tensor,
+                         query_start: torch.Tensor | None = None, max_query_len: int = 1, first_blocks: int = 1,
+                         last_blocks: int = 2, workspace=None, stream=None) -> None:
+    """The blocks that matter most to each new token and KV head, for
+    fp8_kv_sparse_attention.
+
+    Of the blocks up to the token's own, the first first_blocks and the last
+    last_blocks are taken, then those of the highest scores, the lower block of
+    equal ones: the largest product of the 8-bit mean of the block's keys
+    (means and mean_scales of fp8_kv_block_means) with the query heads that
+    share the KV head, each quantised to 8 bits.  selected: int32 [tokens,
+    num_kv_heads, budget], columns of the block table in rising order, then
+    -1.  q, seq_lens, block_table, query_start and max_query_len: as for
+    fp8_kv_attention; rows of no request are not written.  workspace: a
+    Workspace, or a uint8 tensor of fp8_kv_select_blocks_workspace_size()."""
+    nb, hkv, d = _block_means(means, mean_scales)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != d:
+        raise ValueError("q must be [tokens, num_q_heads, head_dim] with the means' head_dim")
+    tokens, hq, _ = shape
+    qs = _heads("q", q, shape)
+    if selected.dtype is not torch.int32 or selected.ndim != 3 or not selected.is_contiguous() or \
+            selected.shape[:2] != (tokens, hkv):
+        raise ValueError("selected must be a contiguous int32 [tokens, num_kv_heads, budget] tensor")
+    batch, max_blocks = _paged_rows(seq_lens, block_table, query_start)
+    device = _cuda(q, means, mean_scales, seq_lens, block_table, selected, query_start)
+    handle = _stream(stream, device)
+    if tokens == 0:
+        return
+    lib = _lib.load()
+    buf = _scratch(workspace, lib.w8a8_fp8_kv_select_blocks_workspace_size(tokens, hkv, max_blocks), "fp8_select", device, stream,
+                   handle, q)
+    check(lib.w8a8_fp8_kv_select_blocks(
+        q.data_ptr(), _fkind(q), tokens, hq, hkv, d, *qs, means.data_ptr(), mean_scales.data_ptr(), nb, block_size,
+        block_table.data_ptr(), max_blocks, seq_lens.data_ptr(), _ptr(query_start), batch, max_query_len, first_blocks, last_blocks,
+        selected.shape[2], selected.data_ptr(), buf.data_ptr(), buf.numel() * buf.element_size(), handle))
+
+
+def fp8_kv_sparse_attention_workspace_size(tokens: int, num_q_heads: int, num_kv_heads: int, head_dim: int, budget: int,
+                                           block_size: int) -> int:
+    return int(_lib.load().w8a8_fp8_kv_sparse_attention_workspace_size(tokens, num_q_heads, num_kv_heads, head_dim, budget,
+                                                                       block_size))
+
+
+@functools.lru_cache(maxsize=4096)
+def _fp8_sparse_need(device_index: int, *sizes: int) -> int:
+    """The same, looked up once for a device and sizes (it depends on nothing else)."""
+    return fp8_kv_sparse_attention_workspace_size(*sizes)
+
+
+def fp8_kv_sparse_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, seq_lens: torch.Tensor,
+                            block_table: torch.Tensor, selected: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                            out: torch.Tensor, query_start: torch.Tensor | None = None, max_query_len: int = 1,
+                            sm_scale: float | None = None, workspace=None, stream=None) -> None:
+    """Attention of each new token over the blocks selected for it.
+
+    selected: int32 [tokens, num_kv_heads, budget], columns of the block table
+    (fp8_kv_select_blocks gives them); ones outside it are skipped, the tokens
+    of a column named twice count twice.  A row sees the tokens of its columns
+    up to its own position; one that sees none gives zeros.  The other
+    arguments: as for fp8_kv_attention (workspace: of
+    fp8_kv_sparse_attention_workspace_size())."""
+    nb, bs, hkv, d = _fp8_caches(k_cache, v_cache)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != d:
+        raise ValueError("q must be [tokens, num_q_heads, head_dim] with the cache's head_dim")
+    tokens, hq, _ = shape
+    qs, os_ = _heads("q", q, shape), _heads("out", out, shape)
+    if selected.dtype is not torch.int32 or selected.ndim != 3 or not selected.is_contiguous() or \
+            selected.shape[:2] != (tokens, hkv):
+        raise ValueError("selected must be a contiguous int32 [tokens, num_kv_heads, budget] tensor")
+    batch, max_blocks = _paged_rows(seq_lens, block_table, query_start)
+    _one_scale(k_scale, v_scale)
+    device = _cuda(q, k_cache, v_cache, seq_lens, block_table, selected, k_scale, v_scale, out, query_start)
+    handle = _stream(stream, device)
+    if tokens == 0:
+        return
+    budget = selected.shape[2]
+    buf = _scratch(workspace, _fp8_sparse_need(device, tokens, hq, hkv, d, budget, bs), "fp8_sparse", device, stream, handle, q)
+    if sm_scale is None:
+        sm_scale = 1.0 / float(d) ** 0.5
+    check(_lib.load().w8a8_fp8_kv_sparse_attention(
+        q.data_ptr(), _fkind(q), tokens, hq, hkv, d, *qs, k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, block_table.data_ptr(),
+        max_blocks, seq_lens.data_ptr(), _ptr(query_start), batch, max_query_len, selected.data_ptr(), budget, k_scale.data_ptr(),
+        v_scale.data_ptr(), sm_scale, out.data_ptr(), _fkind(out), *os_, buf.data_ptr(), buf.numel() * buf.element_size(), handle))

@@ -1234,6 +1234,364 @@ w8a8_status w8a8_kv4_attention(const void* q, int q_dtype, int64_t tokens, int64
   return ok();
 }
 
+namespace {
+
+// The cache's and the step's sizes, for every call over the paged fp8 cache.
+w8a8_status fp8_paged(const int32_t* block_table, int64_t max_blocks, const int32_t* seq_lens, const int32_t* query_start,
+                      int64_t tokens, int64_t batch, int64_t max_query_len, int64_t num_blocks, int64_t block_size,
+                      int64_t num_kv_heads, int64_t head_dim, w8a8::Fp8Paged* c) {
+  if (!block_table || !seq_lens) return fail(W8A8_ERR_INVALID_ARG, "null pointer argument");
+  if (num_blocks < 1 || num_kv_heads < 1 || block_size < 1 || max_blocks < 1 || tokens < 1 || batch < 1 || max_query_len < 1)
+    return fail(W8A8_ERR_INVALID_ARG, "num_blocks, num_kv_heads, block_size, max_blocks, tokens, batch and max_query_len must be >= 1");
+  if (!query_start && (tokens != batch || max_query_len != 1))
+    return fail(W8A8_ERR_INVALID_ARG, "without query_start a request has one token: tokens = batch, max_query_len = 1");
+  if (head_dim != 64 && head_dim != 128) return fail(W8A8_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (block_size % 16 != 0 || block_size > 8192)
+    return fail(W8A8_ERR_UNSUPPORTED, "block_size must be a multiple of 16, at most 8192");
+  if (num_kv_heads > 65535 || batch > 65535 || tokens >= (1LL << 31) || max_query_len >= (1LL << 31))
+    return fail(W8A8_ERR_UNSUPPORTED, "num_kv_heads, batch, tokens or max_query_len out of range");
+  if (num_blocks >= (1LL << 31) / block_size) return fail(W8A8_ERR_UNSUPPORTED, "num_blocks * block_size must be below 2^31");
+  if (max_blocks >= (1LL << 31) / block_size) return fail(W8A8_ERR_UNSUPPORTED, "max_blocks * block_size must be below 2^31");
+  if (batch * num_kv_heads >= (1LL << 33) / (max_blocks * block_size))
+    return fail(W8A8_ERR_UNSUPPORTED, "batch * num_kv_heads * max_blocks * block_size must be below 2^33");
+  if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(query_start, 4))
+    return fail(W8A8_ERR_MISALIGNED, "lengths, starts and block table must be 4-byte aligned");
+  c->num_blocks = static_cast<int>(num_blocks);
+  c->block_size = static_cast<int>(block_size);
+  c->num_kv_heads = static_cast<int>(num_kv_heads);
+  c->head_dim = static_cast<int>(head_dim);
+  c->block_table = block_table;
+  c->max_blocks = static_cast<int>(max_blocks);
+  c->seq_lens = seq_lens;
+  c->query_start = query_start;
+  c->tokens = static_cast<int>(tokens);
+  // no request has more rows than there are tokens, however generous the limit
+  c->max_query_len = static_cast<int>(std::min(max_query_len, tokens));
+  c->batch = static_cast<int>(batch);
+  return W8A8_OK;
+}
+
+// Query heads over KV heads.
+w8a8_status fp8_heads(int64_t batch, int64_t max_query_len, int64_t num_q_heads, int64_t num_kv_heads) {
+  if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0)
+    return fail(W8A8_ERR_INVALID_ARG, "num_q_heads must be a multiple of num_kv_heads, both >= 1");
+  if (num_q_heads > 65535 || max_query_len >= (1LL << 31) / num_q_heads || max_query_len * num_q_heads >= (1LL << 31) / batch)
+    return fail(W8A8_ERR_UNSUPPORTED, "batch * max_query_len * num_q_heads must be below 2^31, num_q_heads <= 65535");
+  if (num_q_heads / num_kv_heads > 64) return fail(W8A8_ERR_UNSUPPORTED, "num_q_heads / num_kv_heads must be at most 64");
+  return W8A8_OK;
+}
+
+// A [tokens, heads, head_dim] operand's bytes, from its first to its last element.
+struct Span {
+  uintptr_t begin, end;
+  Span(const void* p, int64_t tokens, int64_t heads, int64_t head_dim, int64_t token_stride, int64_t head_stride)
+      : begin(reinterpret_cast<uintptr_t>(p)),
+        end(begin + 2 * static_cast<uintptr_t>((tokens - 1) * token_stride + (heads - 1) * head_stride + head_dim)) {}
+  bool meets(const Span& o) const { return begin < o.end && o.begin < end; }
+};
+
+// Strides of an operand: not negative, and small enough that offsets fit 62 bits.
+bool strides_ok(int64_t tokens, int64_t heads, int64_t token_stride, int64_t head_stride) {
+  return token_stride >= 0 && head_stride >= 0 && token_stride < (1LL << 61) / tokens && head_stride < (1LL << 60) / heads;
+}
+
+w8a8_status fp8_attention_call(const void* q, int q_dtype, int64_t num_q_heads, int64_t q_token_stride, int64_t q_head_stride,
+                               const void* k_cache, const void* v_cache, const w8a8::Fp8Paged& c, const int32_t* selected,
+                               int64_t budget, const float* k_scale, const float* v_scale, float sm_scale, void* out,
+                               int out_dtype, int64_t out_token_stride, int64_t out_head_stride, void* workspace,
+                               size_t workspace_bytes, size_t need, w8a8_stream_t stream) {
+  if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !out) return fail(W8A8_ERR_INVALID_ARG, "null pointer argument");
+  if ((q_dtype != W8A8_BF16 && q_dtype != W8A8_FP16) || (out_dtype != W8A8_BF16 && out_dtype != W8A8_FP16))
+    return fail(W8A8_ERR_INVALID_ARG, "q and out must be BF16 or FP16");
+  const int64_t tokens = c.tokens, d = c.head_dim;
+  if (!strides_ok(tokens, num_q_heads, q_token_stride, q_head_stride) ||
+      !strides_ok(tokens, num_q_heads, out_token_stride, out_head_stride) || (tokens > 1 && out_token_stride < d) ||
+      (num_q_heads > 1 && out_head_stride < d))
+    return fail(W8A8_ERR_INVALID_ARG, "strides of q must not be negative, those of out at least head_dim");
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return fail(W8A8_ERR_MISALIGNED, "the caches must be 16-byte aligned");
+  if (!aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(selected, 4) || !aligned(q, 2) || !aligned(out, 2))
+    return fail(W8A8_ERR_MISALIGNED, "misaligned q, out, scale or selection pointer");
+  if (Span(q, tokens, num_q_heads, d, q_token_stride, q_head_stride).meets(Span(out, tokens, num_q_heads, d, out_token_stride, out_head_stride)))
+    return fail(W8A8_ERR_INVALID_ARG, "out must not share memory with q");
+  if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+    return fail(W8A8_ERR_WORKSPACE, "workspace must be 16-byte aligned and hold %zu bytes", need);
+  w8a8_status st;
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != W8A8_OK) return st;
+  w8a8::Fp8AttnParams p{};
+  p.c = c;
+  p.q = q;
+  p.q_token_stride = q_token_stride;
+  p.q_head_stride = q_head_stride;
+  p.q_fp16 = q_dtype == W8A8_FP16;
+  p.q_vec = aligned(q, 16) && (q_token_stride | q_head_stride) % 8 == 0;
+  p.num_q_heads = static_cast<int>(num_q_heads);
+  p.share = static_cast<int>(num_q_heads / c.num_kv_heads);
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.selected = selected;
+  p.budget = static_cast<int>(budget);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.sm_scale = sm_scale;
+  p.out = out;
+  p.out_token_stride = out_token_stride;
+  p.out_head_stride = out_head_stride;
+  p.out_fp16 = out_dtype == W8A8_FP16;
+  p.out_vec = aligned(out, 16) && (out_token_stride | out_head_stride) % 8 == 0;
+  cudaError_t e = w8a8::launch_fp8_attention(p, dev.sms, workspace, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, selected ? "sparse fp8 KV attention launch" : "paged fp8 KV attention launch");
+  return ok();
+}
+
+}  // namespace
+
+w8a8_status w8a8_fp8_kv_rotate_write(const void* q, const void* k, const void* v, int dtype, int64_t tokens,
+                                     int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim, int64_t q_token_stride,
+                                     int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                                     int64_t v_token_stride, int64_t v_head_stride, const float* cos_sin,
+                                     int64_t max_position, int64_t rot_dim, const int32_t* positions, int axes,
+                                     const int32_t* sections, int interleaved, void* k_cache, void* v_cache,
+                                     int64_t num_blocks, int64_t block_size, const int64_t* slots, const float* k_scale,
+                                     const float* v_scale, void* q_out, int64_t q_out_token_stride,
+                                     int64_t q_out_head_stride, w8a8_stream_t stream) {
+  if (!k || !v || !cos_sin || !positions || !k_cache || !v_cache || !slots || !k_scale || !v_scale ||
+      (num_q_heads > 0 && (!q || !q_out)))
+    return fail(W8A8_ERR_INVALID_ARG, "null pointer argument");
+  if (dtype != W8A8_BF16 && dtype != W8A8_FP16) return fail(W8A8_ERR_INVALID_ARG, "q, k and v must be BF16 or FP16");
+  if (tokens < 1 || num_q_heads < 0 || num_kv_heads < 1 || num_blocks < 1 || block_size < 1 || max_position < 1)
+    return fail(W8A8_ERR_INVALID_ARG, "tokens, num_kv_heads, num_blocks, block_size and max_position must be >= 1, num_q_heads >= 0");
+  if (head_dim != 64 && head_dim != 128) return fail(W8A8_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (block_size % 16 != 0 || block_size > 8192)
+    return fail(W8A8_ERR_UNSUPPORTED, "block_size must be a multiple of 16, at most 8192");
+  if (num_blocks >= (1LL << 31) / block_size) return fail(W8A8_ERR_UNSUPPORTED, "num_blocks * block_size must be below 2^31");
+  if (tokens >= (1LL << 31) || num_q_heads > 65535 || num_kv_heads > 65535 || max_position >= (1LL << 31))
+    return fail(W8A8_ERR_UNSUPPORTED, "tokens, max_position or head counts out of range");
+  if (rot_dim < 2 || rot_dim > head_dim || rot_dim % 2 != 0)
+    return fail(W8A8_ERR_INVALID_ARG, "rot_dim must be even, from 2 to head_dim");
+  if (axes < 1 || axes > 4 || (axes > 1 && !sections))
+    return fail(W8A8_ERR_INVALID_ARG, "positions have 1 to 4 axes, several need sections");
+  w8a8::Fp8WriteArgs a{};
+  int64_t pairs = 0;
+  for (int i = 0; i < axes; ++i) {
+    const int64_t n = sections ? sections[i] : rot_dim / 2;
+    if (n < 0) return fail(W8A8_ERR_INVALID_ARG, "sections must not be negative");
+    pairs += n;
+    a.section_end[i] = static_cast<int>(std::min<int64_t>(pairs, rot_dim));
+  }
+  if (pairs != rot_dim / 2) return fail(W8A8_ERR_INVALID_ARG, "sections must add up to rot_dim / 2");
+  const int64_t q_heads = std::max<int64_t>(num_q_heads, 1);
+  if (!strides_ok(tokens, num_kv_heads, k_token_stride, k_head_stride) || !strides_ok(tokens, num_kv_heads, v_token_stride, v_head_stride) ||
+      (num_q_heads > 0 && (!strides_ok(tokens, q_heads, q_token_stride, q_head_stride) ||
+                           !strides_ok(tokens, q_heads, q_out_token_stride, q_out_head_stride) ||
+                           (tokens > 1 && q_out_token_stride < head_dim) || (num_q_heads > 1 && q_out_head_stride < head_dim))))
+    return fail(W8A8_ERR_INVALID_ARG, "strides must not be negative, those of q_out at least head_dim");
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return fail(W8A8_ERR_MISALIGNED, "the caches must be 16-byte aligned");
+  if (!aligned(k, 2) || !aligned(v, 2) || !aligned(q, 2) || !aligned(q_out, 2) || !aligned(cos_sin, 4) || !aligned(positions, 4) ||
+      !aligned(slots, 8) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+    return fail(W8A8_ERR_MISALIGNED, "misaligned q, k, v, cos_sin, positions, slots or scale pointer");
+  if (num_q_heads > 0 && !(q == q_out && q_token_stride == q_out_token_stride && q_head_stride == q_out_head_stride)) {
+    const Span o(q_out, tokens, num_q_heads, head_dim, q_out_token_stride, q_out_head_stride);
+    if (o.meets(Span(q, tokens, num_q_heads, head_dim, q_token_stride, q_head_stride)) ||
+        o.meets(Span(k, tokens, num_kv_heads, head_dim, k_token_stride, k_head_stride)) ||
+        o.meets(Span(v, tokens, num_kv_heads, head_dim, v_token_stride, v_head_stride)))
+      return fail(W8A8_ERR_INVALID_ARG, "q_out must be q itself or share no memory with q, k and v");
+  }
+  w8a8_status st;
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != W8A8_OK) return st;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_out = q_out;
+  a.q_token_stride = q_token_stride;
+  a.q_head_stride = q_head_stride;
+  a.k_token_stride = k_token_stride;
+  a.k_head_stride = k_head_stride;
+  a.v_token_stride = v_token_stride;
+  a.v_head_stride = v_head_stride;
+  a.q_out_token_stride = q_out_token_stride;
+  a.q_out_head_stride = q_out_head_stride;
+  a.fp16 = dtype == W8A8_FP16;
+  a.tokens = tokens;
+  a.num_q_heads = static_cast<int>(num_q_heads);
+  a.num_kv_heads = static_cast<int>(num_kv_heads);
+  a.head_dim = static_cast<int>(head_dim);
+  a.rot_dim = static_cast<int>(rot_dim);
+  a.cos_sin = cos_sin;
+  a.max_position = max_position;
+  a.positions = positions;
+  a.axes = axes;
+  a.interleaved = interleaved != 0;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.cache_rows = num_blocks * block_size;
+  a.slots = slots;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  int64_t strides = k_token_stride | k_head_stride | v_token_stride | v_head_stride;
+  bool vec = aligned(k, 16) && aligned(v, 16) && aligned(cos_sin, 16);
+  if (num_q_heads > 0) {
+    strides |= q_token_stride | q_head_stride | q_out_token_stride | q_out_head_stride;
+    vec = vec && aligned(q, 16) && aligned(q_out, 16);
+  }
+  a.vec = vec && strides % 8 == 0 && rot_dim % 16 == 0;
+  cudaError_t e = w8a8::launch_fp8_rotate_write(a, dev.sms, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rotation and cache write launch");
+  return ok();
+}
+
+size_t w8a8_fp8_kv_paged_attention_workspace_size(int64_t batch, int64_t max_query_len, int64_t num_q_heads,
+                                                  int64_t num_kv_heads, int64_t head_dim) {
+  if (batch < 1 || batch > 65535 || max_query_len < 1) {
+    fail(W8A8_ERR_INVALID_ARG, "batch must be 1 to 65535, max_query_len >= 1");
+    return 0;
+  }
+  if (fp8_heads(batch, max_query_len, num_q_heads, num_kv_heads) != W8A8_OK) return 0;
+  if (head_dim != 64 && head_dim != 128) {
+    fail(W8A8_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+    return 0;
+  }
+  t_last_error.clear();
+  return w8a8::fp8_paged_attention_workspace(static_cast<int>(num_q_heads / num_kv_heads), max_query_len,
+                                             static_cast<int>(head_dim), sms_or_default());
+}
+
+w8a8_status w8a8_fp8_kv_paged_attention(const void* q, int q_dtype, int64_t tokens, int64_t num_q_heads, int64_t num_kv_heads,
+                                        int64_t head_dim, int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,
+                                        const void* v_cache, int64_t num_blocks, int64_t block_size,
+                                        const int32_t* block_table, int64_t max_blocks, const int32_t* seq_lens,
+                                        const int32_t* query_start, int64_t batch, int64_t max_query_len,
+                                        const float* k_scale, const float* v_scale, float sm_scale, void* out, int out_dtype,
+                                        int64_t out_token_stride, int64_t out_head_stride, void* workspace,
+                                        size_t workspace_bytes, w8a8_stream_t stream) {
+  w8a8::Fp8Paged c{};
+  w8a8_status st = fp8_paged(block_table, max_blocks, seq_lens, query_start, tokens, batch, max_query_len, num_blocks, block_size,
+                             num_kv_heads, head_dim, &c);
+  if (st != W8A8_OK) return st;
+  if ((st = fp8_heads(batch, max_query_len, num_q_heads, num_kv_heads)) != W8A8_OK) return st;
+  const size_t need = w8a8::fp8_paged_attention_workspace(static_cast<int>(num_q_heads / num_kv_heads), max_query_len,
+                                                          static_cast<int>(head_dim), sms_or_default());
+  return fp8_attention_call(q, q_dtype, num_q_heads, q_token_stride, q_head_stride, k_cache, v_cache, c, nullptr, 0, k_scale,
+                            v_scale, sm_scale, out, out_dtype, out_token_stride, out_head_stride, workspace, workspace_bytes,
+                            need, stream);
+}
+
+w8a8_status w8a8_fp8_kv_block_means(const void* k_cache, int64_t num_blocks, int64_t block_size, int64_t num_kv_heads,
+                                    int64_t head_dim, const int32_t* block_table, int64_t max_blocks, const int32_t* seq_lens,
+                                    const int32_t* query_start, int64_t tokens, int64_t batch, int64_t max_query_len,
+                                    int8_t* means, float* mean_scales, w8a8_stream_t stream) {
+  if (!k_cache || !means || !mean_scales) return fail(W8A8_ERR_INVALID_ARG, "null pointer argument");
+  w8a8::Fp8MeansArgs a{};
+  w8a8_status st = fp8_paged(block_table, max_blocks, seq_lens, query_start, tokens, batch, max_query_len, num_blocks, block_size,
+                             num_kv_heads, head_dim, &a.c);
+  if (st != W8A8_OK) return st;
+  if (!aligned(k_cache, 16) || !aligned(means, 16) || !aligned(mean_scales, 4))
+    return fail(W8A8_ERR_MISALIGNED, "the cache and the means must be 16-byte aligned, their scales 4-byte");
+  if ((std::min(max_query_len, tokens) / block_size + 2) * num_kv_heads >= (1LL << 31))
+    return fail(W8A8_ERR_UNSUPPORTED, "max_query_len / block_size * num_kv_heads out of range");
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != W8A8_OK) return st;
+  a.k_cache = k_cache;
+  a.means = means;
+  a.mean_scales = mean_scales;
+  cudaError_t e = w8a8::launch_fp8_block_means(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "block means launch");
+  return ok();
+}
+
+size_t w8a8_fp8_kv_select_blocks_workspace_size(int64_t tokens, int64_t num_kv_heads, int64_t max_blocks) {
+  if (tokens < 1 || tokens >= (1LL << 31) || num_kv_heads < 1 || num_kv_heads > 65535 || max_blocks < 1 ||
+      max_blocks > w8a8::kMaxSelectBlocks)
+    return 0;
+  return w8a8::fp8_select_workspace(tokens, num_kv_heads, max_blocks);
+}
+
+w8a8_status w8a8_fp8_kv_select_blocks(const void* q, int q_dtype, int64_t tokens, int64_t num_q_heads, int64_t num_kv_heads,
+                                      int64_t head_dim, int64_t q_token_stride, int64_t q_head_stride, const int8_t* means,
+                                      const float* mean_scales, int64_t num_blocks, int64_t block_size,
+                                      const int32_t* block_table, int64_t max_blocks, const int32_t* seq_lens,
+                                      const int32_t* query_start, int64_t batch, int64_t max_query_len, int64_t first_blocks,
+                                      int64_t last_blocks, int64_t budget, int32_t* selected, void* workspace,
+                                      size_t workspace_bytes, w8a8_stream_t stream) {
+  if (!q || !means || !mean_scales || !selected) return fail(W8A8_ERR_INVALID_ARG, "null pointer argument");
+  if (q_dtype != W8A8_BF16 && q_dtype != W8A8_FP16) return fail(W8A8_ERR_INVALID_ARG, "q must be BF16 or FP16");
+  w8a8::Fp8SelectArgs a{};
+  w8a8_status st = fp8_paged(block_table, max_blocks, seq_lens, query_start, tokens, batch, max_query_len, num_blocks, block_size,
+                             num_kv_heads, head_dim, &a.c);
+  if (st != W8A8_OK) return st;
+  if ((st = fp8_heads(batch, max_query_len, num_q_heads, num_kv_heads)) != W8A8_OK) return st;
+  if (first_blocks < 0 || last_blocks < 1 || budget < 1 || first_blocks > budget || last_blocks > budget - first_blocks)
+    return fail(W8A8_ERR_INVALID_ARG, "first_blocks >= 0, last_blocks >= 1, and their sum at most budget");
+  if (max_blocks > w8a8::kMaxSelectBlocks)
+    return fail(W8A8_ERR_UNSUPPORTED, "max_blocks must be at most %d", w8a8::kMaxSelectBlocks);
+  if (budget >= (1LL << 31)) return fail(W8A8_ERR_UNSUPPORTED, "budget out of range");
+  if (!strides_ok(tokens, num_q_heads, q_token_stride, q_head_stride))
+    return fail(W8A8_ERR_INVALID_ARG, "strides must not be negative");
+  if (!aligned(means, 16) || !aligned(mean_scales, 4) || !aligned(selected, 4) || !aligned(q, 2))
+    return fail(W8A8_ERR_MISALIGNED, "the means must be 16-byte aligned, q, scales and selection to their elements");
+  const size_t need = w8a8::fp8_select_workspace(tokens, num_kv_heads, max_blocks);
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
+    return fail(W8A8_ERR_WORKSPACE, "workspace must be 16-byte aligned and hold %zu bytes", need);
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != W8A8_OK) return st;
+  a.q = q;
+  a.q_token_stride = q_token_stride;
+  a.q_head_stride = q_head_stride;
+  a.q_fp16 = q_dtype == W8A8_FP16;
+  a.q_vec = aligned(q, 16) && (q_token_stride | q_head_stride) % 8 == 0;
+  a.share = static_cast<int>(num_q_heads / num_kv_heads);
+  a.means = means;
+  a.mean_scales = mean_scales;
+  a.first_blocks = static_cast<int>(first_blocks);
+  a.last_blocks = static_cast<int>(last_blocks);
+  a.budget = static_cast<int>(budget);
+  a.selected = selected;
+  a.scores = static_cast<float*>(workspace);
+  cudaError_t e = w8a8::launch_fp8_select(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "block selection launch");
+  return ok();
+}
+
+size_t w8a8_fp8_kv_sparse_attention_workspace_size(int64_t tokens, int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
+                                                   int64_t budget, int64_t block_size) {
+  if (tokens < 1 || tokens >= (1LL << 31) || budget < 1 || block_size < 1 || budget >= (1LL << 24) || block_size > 8192 ||
+      budget * block_size >= (1LL << 24) || (head_dim != 64 && head_dim != 128)) {
+    fail(W8A8_ERR_INVALID_ARG, "tokens, head_dim or budget * block_size out of range");
+    return 0;
+  }
+  if (fp8_heads(1, tokens, num_q_heads, num_kv_heads) != W8A8_OK) return 0;
+  t_last_error.clear();
+  return w8a8::fp8_sparse_attention_workspace(tokens, static_cast<int>(num_kv_heads), static_cast<int>(num_q_heads / num_kv_heads),
+                                              static_cast<int>(head_dim), budget * block_size, sms_or_default());
+}
+
+w8a8_status w8a8_fp8_kv_sparse_attention(const void* q, int q_dtype, int64_t tokens, int64_t num_q_heads, int64_t num_kv_heads,
+                                         int64_t head_dim, int64_t q_token_stride, int64_t q_head_stride,
+                                         const void* k_cache, const void* v_cache, int64_t num_blocks, int64_t block_size,
+                                         const int32_t* block_table, int64_t max_blocks, const int32_t* seq_lens,
+                                         const int32_t* query_start, int64_t batch, int64_t max_query_len,
+                                         const int32_t* selected, int64_t budget, const float* k_scale, const float* v_scale,
+                                         float sm_scale, void* out, int out_dtype, int64_t out_token_stride,
+                                         int64_t out_head_stride, void* workspace, size_t workspace_bytes,
+                                         w8a8_stream_t stream) {
+  if (!selected) return fail(W8A8_ERR_INVALID_ARG, "null pointer argument");
+  w8a8::Fp8Paged c{};
+  w8a8_status st = fp8_paged(block_table, max_blocks, seq_lens, query_start, tokens, batch, max_query_len, num_blocks, block_size,
+                             num_kv_heads, head_dim, &c);
+  if (st != W8A8_OK) return st;
+  if ((st = fp8_heads(1, tokens, num_q_heads, num_kv_heads)) != W8A8_OK) return st;
+  if (budget < 1) return fail(W8A8_ERR_INVALID_ARG, "budget must be >= 1");
+  if (budget >= (1LL << 24) || budget * block_size >= (1LL << 24))
+    return fail(W8A8_ERR_UNSUPPORTED, "budget * block_size must be below 2^24");
+  const size_t need = w8a8::fp8_sparse_attention_workspace(tokens, static_cast<int>(num_kv_heads),
+                                                           static_cast<int>(num_q_heads / num_kv_heads),
+                                                           static_cast<int>(head_dim), budget * block_size, sms_or_default());
+  return fp8_attention_call(q, q_dtype, num_q_heads, q_token_stride, q_head_stride, k_cache, v_cache, c, selected, budget, k_scale,
+                            v_scale, sm_scale, out, out_dtype, out_token_stride, out_head_stride, workspace, workspace_bytes,
+                            need, stream);
+}
+
 w8a8_status w8a8_verify_drafts(const void* target_probs, const void* draft_probs, int dtype, int64_t vocab,
                                int64_t target_ld, int64_t draft_ld, const int32_t* draft_tokens,
                                const int32_t* draft_start, int64_t batch, int64_t rows, const float* uniform,

@@ -226,6 +226,94 @@ cudaError_t read_clear_kv4_prompt_status(int* flags);
 // Reads and clears the kernels' status word (call after a sync).
 cudaError_t read_clear_kv4_status(int* flags);
 
+// The paged fp8 KV cache, its geometry and a step's rows: what the operators
+// of a step over it share.
+struct Fp8Paged {
+  int num_blocks, block_size;  // rows of the cache: their product, below 2^31
+  int num_kv_heads, head_dim;
+  const int* block_table;      // [batch, max_blocks]; entries outside the cache are skipped
+  int max_blocks;
+  const int* seq_lens;         // [batch], clamped to [0, max_blocks * block_size]
+  const int* query_start;      // [batch + 1], or null: one token a request
+  int tokens, max_query_len, batch;
+};
+
+// Rotation and cache write (fp8_write.cu).
+struct Fp8WriteArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  long long q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride,
+      q_out_token_stride, q_out_head_stride;  // elements
+  int fp16;
+  int vec;                // 16-byte vectors everywhere, rot_dim a multiple of 16
+  long long tokens;
+  int num_q_heads, num_kv_heads, head_dim, rot_dim;
+  const float* cos_sin;   // [max_position, rot_dim]
+  long long max_position;
+  const int* positions;   // [axes, tokens]
+  int axes;
+  int section_end[4];     // pairs below section_end[a] (and of no earlier axis) turn by axis a
+  int interleaved;
+  void* k_cache;
+  void* v_cache;
+  long long cache_rows;   // num_blocks * block_size
+  const int64_t* slots;
+  const float* k_scale;
+  const float* v_scale;
+};
+cudaError_t launch_fp8_rotate_write(const Fp8WriteArgs& a, int num_sms, cudaStream_t stream);
+
+// Means of the written blocks' keys, and the selection by them (fp8_select.cu).
+struct Fp8MeansArgs {
+  Fp8Paged c;
+  const void* k_cache;
+  int8_t* means;          // [num_blocks, num_kv_heads, head_dim]
+  float* mean_scales;     // [num_blocks, num_kv_heads]
+};
+cudaError_t launch_fp8_block_means(const Fp8MeansArgs& a, cudaStream_t stream);
+
+struct Fp8SelectArgs {
+  Fp8Paged c;
+  const void* q;
+  long long q_token_stride, q_head_stride;
+  int q_fp16, q_vec;
+  int share;              // num_q_heads / num_kv_heads
+  const int8_t* means;
+  const float* mean_scales;
+  int first_blocks, last_blocks, budget;
+  int* selected;          // [tokens, num_kv_heads, budget]
+  float* scores;          // [tokens of a slab, num_kv_heads, max_blocks]
+  int slab;               // tokens whose scores the workspace holds
+};
+constexpr int kMaxSelectBlocks = 49152;  // a token's scores lie in shared memory
+size_t fp8_select_workspace(long long tokens, long long num_kv_heads, long long max_blocks);
+cudaError_t launch_fp8_select(const Fp8SelectArgs& a, cudaStream_t stream);
+
+// Attention over the paged fp8 cache (fp8_attention.cu).
+struct Fp8AttnParams {
+  Fp8Paged c;
+  const void* q;          // [tokens, num_q_heads, head_dim] of 16-bit values
+  long long q_token_stride, q_head_stride;  // elements
+  int q_fp16, q_vec;      // q_vec: rows are 16-byte aligned
+  int num_q_heads, share; // share: num_q_heads / num_kv_heads
+  const void* k_cache;
+  const void* v_cache;
+  const int* selected;    // [tokens, num_kv_heads, budget] columns, or null: all
+  int budget;
+  const float* k_scale;
+  const float* v_scale;
+  float sm_scale;
+  void* out;              // as q
+  long long out_token_stride, out_head_stride;
+  int out_fp16, out_vec;
+};
+size_t fp8_paged_attention_workspace(int share, long long max_query_len, int head_dim, int num_sms);
+size_t fp8_sparse_attention_workspace(long long tokens, int num_kv_heads, int share, int head_dim, long long budget_tokens,
+                                      int num_sms);
+cudaError_t launch_fp8_attention(const Fp8AttnParams& p, int num_sms, void* workspace, cudaStream_t stream);
+
 // Verification of drafted tokens (verify.cu).
 struct VerifyArgs {
   const void* target;       // [rows + batch, vocab]
