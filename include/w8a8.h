@@ -636,9 +636,10 @@ W8A8_API w8a8_status w8a8_fp8_kv_paged_attention(
 /* 8-bit means of the keys of the blocks that got new tokens, columns (L - n) /
  * block_size .. (L - 1) / block_size of each request of L tokens, n of them
  * new.  For each KV head, over the tokens of the block that lie below L:
- *   mean = fl(sum of the codes' values) / count,  scale = absmax / 127 (1 if
- *   that is 0),  code = round(mean / scale), half to even,
- * the sum exact (NaN codes count as 0), the quotients correctly rounded fp32.
+ *   mean = fl(sum of the codes' values) / count,  scale = absmax * fl(1 / 127)
+ *   (1 if that is 0),  code = round(mean / scale), half to even,
+ * the sum exact (NaN codes count as 0), the quotients and the product correctly
+ * rounded fp32.
  * The means are in units of k_scale, which has no part in their order.
  *   means        int8 [num_blocks, num_kv_heads, head_dim], 16-byte aligned
  *   mean_scales  fp32 [num_blocks, num_kv_heads]
@@ -652,8 +653,8 @@ W8A8_API w8a8_status w8a8_fp8_kv_block_means(const void* k_cache, int64_t num_bl
                                              int8_t* means, float* mean_scales, w8a8_stream_t stream);
 
 /* For each new token and KV head the blocks that matter most to it, by the
- * 8-bit means.  Each query head's row is quantised to int8 like a row in
- * w8a8_scaled_quant (dynamic); the score of a block is
+ * 8-bit means.  Each query head's row is quantised to int8 as the means are (NaN
+ * becomes 0 and has no part in the absmax); the score of a block is
  *   fl(max over the KV head's query heads of fl(dot * q_scale) * mean_scale),
  * dot the exact product of the codes.  Of the blocks up to the token's own
  * (column p / block_size) the first first_blocks and the last last_blocks are

@@ -33,6 +33,10 @@ namespace w8a8 {
 
 namespace {
 
+// The scale of 8-bit codes: absmax times 1/127, both in fp32, 1 for zeros (a
+// product and not a quotient: the codes are of this scale, whatever its last bit).
+__device__ __forceinline__ float int8_scale(float top) { return top > 0.f ? __fmul_rn(top, 1.f / 127.f) : 1.f; }
+
 // ------------------------------------------------------------------ means
 
 constexpr int kMeanThreads = 128;
@@ -112,7 +116,7 @@ __global__ void __launch_bounds__(kMeanThreads) fp8_block_means_kernel(const Fp8
   float top = s_top[0];
 #pragma unroll
   for (int i = 1; i < D / 32; ++i) top = fmaxf(top, s_top[i]);
-  scale = scale_from_amax<1>(top);
+  scale = int8_scale(top);
   const size_t at = static_cast<size_t>(block) * a.c.num_kv_heads + kvh;
   a.means[at * D + tid] = static_cast<int8_t>(enc1<1>(__fdiv_rn(mean, scale)));
   if (tid == 0) a.mean_scales[at] = scale;
@@ -202,7 +206,7 @@ __global__ void __launch_bounds__(kScoreThreads) fp8_block_scores_kernel(const F
       for (int k = 0; k < kPer / 8; ++k) top = fmaxf(top, fabsf(f[k]));
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-      const float scale = scale_from_amax<1>(top);
+      const float scale = int8_scale(top);
 #pragma unroll
       for (int k = 0; k < kPer / 8; ++k)
         s_q[row * kStride + (kPer / 8) * lane + k] = static_cast<int8_t>(enc1<1>(__fdiv_rn(f[k], scale)));

@@ -114,7 +114,7 @@ def quantise8(x):
     x = np.asarray(x, np.float32)
     top = np.max(np.where(np.isnan(x), np.float32(0), np.abs(x)), axis=-1, keepdims=True)
     with np.errstate(all="ignore"):
-        scale = np.where(top > 0, top / np.float32(127), np.float32(1)).astype(np.float32)
+        scale = np.where(top > 0, top * (np.float32(1) / np.float32(127)), np.float32(1)).astype(np.float32)
         y = x / scale
     y = np.where(np.isnan(y), np.float32(0), y).astype(np.float64)
     return np.clip(np.rint(y), -128, 127).astype(np.int8), scale[..., 0]
