@@ -135,6 +135,33 @@ w8a8_status make_operand_map(CUtensorMap* map, const void* base, bool f16, long 
   return W8A8_OK;
 }
 
+// An fp8 cache as [rows, row_bytes] bytes, boxes of box_rows rows and `bytes` (64
+// or 128) bytes, swizzled over a row of the box.
+w8a8_status make_cache_map(CUtensorMap* map, const void* base, long long rows, long long row_bytes, int bytes, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(W8A8_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(bytes), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  auto encode = [&] {
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  if (r == CUDA_ERROR_INVALID_CONTEXT) {
+    // (as above: a host thread whose first CUDA call this is)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaSetDevice(dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+    r = encode();
+  }
+  if (r != CUDA_SUCCESS) return fail(W8A8_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return W8A8_OK;
+}
+
 // ------------------------------------------------------------------ GEMM configuration
 
 // SM count of the current device; without a usable device (host-only size
@@ -1339,7 +1366,13 @@ w8a8_status fp8_attention_call(const void* q, int q_dtype, int64_t num_q_heads, 
   p.out_head_stride = out_head_stride;
   p.out_fp16 = out_dtype == W8A8_FP16;
   p.out_vec = aligned(out, 16) && (out_token_stride | out_head_stride) % 8 == 0;
-  cudaError_t e = w8a8::launch_fp8_attention(p, dev.sms, workspace, reinterpret_cast<cudaStream_t>(stream));
+  p.box = 16;
+  while (p.box < 128 && c.block_size % (2 * p.box) == 0) p.box *= 2;
+  CUtensorMap map_k, map_v;
+  const long long rows = static_cast<long long>(c.num_blocks) * c.block_size, row_bytes = static_cast<long long>(c.num_kv_heads) * d;
+  if ((st = make_cache_map(&map_k, k_cache, rows, row_bytes, c.head_dim, p.box)) != W8A8_OK) return st;
+  if ((st = make_cache_map(&map_v, v_cache, rows, row_bytes, c.head_dim, p.box)) != W8A8_OK) return st;
+  cudaError_t e = w8a8::launch_fp8_attention(p, map_k, map_v, dev.sms, workspace, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, selected ? "sparse fp8 KV attention launch" : "paged fp8 KV attention launch");
   return ok();
 }
@@ -1562,8 +1595,8 @@ size_t w8a8_fp8_kv_sparse_attention_workspace_size(int64_t tokens, int64_t num_q
   }
   if (fp8_heads(1, tokens, num_q_heads, num_kv_heads) != W8A8_OK) return 0;
   t_last_error.clear();
-  return w8a8::fp8_sparse_attention_workspace(tokens, static_cast<int>(num_kv_heads), static_cast<int>(num_q_heads / num_kv_heads),
-                                              static_cast<int>(head_dim), budget * block_size, sms_or_default());
+  return w8a8::fp8_sparse_attention_workspace(static_cast<int>(num_q_heads / num_kv_heads), static_cast<int>(head_dim),
+                                              sms_or_default());
 }
 
 w8a8_status w8a8_fp8_kv_sparse_attention(const void* q, int q_dtype, int64_t tokens, int64_t num_q_heads, int64_t num_kv_heads,
@@ -1584,9 +1617,8 @@ w8a8_status w8a8_fp8_kv_sparse_attention(const void* q, int q_dtype, int64_t tok
   if (budget < 1) return fail(W8A8_ERR_INVALID_ARG, "budget must be >= 1");
   if (budget >= (1LL << 24) || budget * block_size >= (1LL << 24))
     return fail(W8A8_ERR_UNSUPPORTED, "budget * block_size must be below 2^24");
-  const size_t need = w8a8::fp8_sparse_attention_workspace(tokens, static_cast<int>(num_kv_heads),
-                                                           static_cast<int>(num_q_heads / num_kv_heads),
-                                                           static_cast<int>(head_dim), budget * block_size, sms_or_default());
+  const size_t need = w8a8::fp8_sparse_attention_workspace(static_cast<int>(num_q_heads / num_kv_heads),
+                                                           static_cast<int>(head_dim), sms_or_default());
   return fp8_attention_call(q, q_dtype, num_q_heads, q_token_stride, q_head_stride, k_cache, v_cache, c, selected, budget, k_scale,
                             v_scale, sm_scale, out, out_dtype, out_token_stride, out_head_stride, workspace, workspace_bytes,
                             need, stream);
@@ -1657,6 +1689,9 @@ w8a8_status w8a8_device_status(int* flags) {
   if (e != cudaSuccess) return cuda_fail(e, "device status read");
   *flags |= qf;
   e = read_clear_kv4_status(&qf);
+  if (e != cudaSuccess) return cuda_fail(e, "device status read");
+  *flags |= qf;
+  e = w8a8::read_clear_fp8_status(&qf);
   if (e != cudaSuccess) return cuda_fail(e, "device status read");
   *flags |= qf;
   return ok();

@@ -87,11 +87,30 @@ __global__ void __launch_bounds__(kThreads) fp8_attention_simple_kernel(const Fp
 
 }  // namespace
 
-size_t fp8_paged_attention_workspace(int, long long, int, int) { return 16; }
+namespace {
+// Rows up to which the few-rows kernel takes a call.
+constexpr int kFewRows = 32;
+}  // namespace
 
-size_t fp8_sparse_attention_workspace(long long, int, int, int, long long, int) { return 16; }
+size_t fp8_paged_attention_workspace(int share, long long max_query_len, int head_dim, int num_sms) {
+  const long long rows = share * max_query_len;
+  return fp8_rows_workspace(static_cast<int>(std::min<long long>(rows, kFewRows)), head_dim, num_sms);
+}
 
-cudaError_t launch_fp8_attention(const Fp8AttnParams& p, int, void*, cudaStream_t stream) {
+size_t fp8_sparse_attention_workspace(int share, int head_dim, int num_sms) {
+  return fp8_rows_workspace(std::min(share, kFewRows), head_dim, num_sms);
+}
+
+cudaError_t read_clear_fp8_status(int* flags) { return read_clear_fp8_rows_status(flags); }
+
+cudaError_t launch_fp8_attention(const Fp8AttnParams& args, const CUtensorMap& map_k, const CUtensorMap& map_v, int num_sms,
+                                 void* workspace, cudaStream_t stream) {
+  Fp8AttnParams p = args;
+  p.counters = static_cast<unsigned*>(workspace);
+  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kFp8CounterBytes);
+  p.few_rows = kFewRows;
+  const long long rows = p.selected ? std::min(p.share, kFewRows) : static_cast<long long>(p.share) * p.c.max_query_len;
+  if (rows <= kFewRows) return launch_fp8_rows(p, static_cast<int>(rows), map_k, map_v, num_sms, stream);
   const dim3 grid(p.c.tokens, p.num_q_heads);
   if (p.c.head_dim == 64) return fp8_launch(fp8_attention_simple_kernel<64>, grid, dim3(kThreads), 0, stream, p);
   return fp8_launch(fp8_attention_simple_kernel<128>, grid, dim3(kThreads), 0, stream, p);

@@ -1,0 +1,1014 @@
+// fp8_rows.cu -- attention over the paged fp8 cache for few rows: single tokens,
+// drafts, and every token of a sparse selection (sm_103a).
+//
+// The rows of a unit (a request or a token, a KV head, up to R of its tokens
+// times query heads) are the N of both products, the cache their M, straight
+// from its e4m3 codes:
+//   S^T[128 tokens x N] = K[128 x D] . Q^T       O^T[D x N] += V^T[D x 128] . P^T
+// by tcgen05 kind::f8f6f4 with fp32 sums in TMEM.  No code is decoded: tiles of
+// 128 tokens go from HBM to the tensor cores by TMA, V as it lies (dims
+// contiguous, so V^T is an operand with M contiguous).  What is not e4m3 is
+// made of several e4m3 numbers, which cost columns of N only:
+//   a query element is q 2^e = a + b 2^-4 + c 2^-8, with e such that the row's
+//     largest element lies in [2^7, 2^8): exact for bf16 and fp16 (4 bits a
+//     part) down to 2^-13 of that element, rounded at 2^-24 of it below;
+//   a weight is f16(2^(s - m + 6)) = a + b 2^-4 + c 2^-8 + d 2^-12, exact (11
+//     bits) for weights above 2^-18 of the largest, rounded at 2^-28 below; the
+//     sum that divides is of the weights before that rounding.
+// The maximum m is raised, and O rescaled, only when a score passes it by 2^2.
+//
+// Bound by the cache's bytes, 2 D a token: the MMAs of a tile take about half of
+// the time that HBM needs for it, and its softmax (128 tokens x R rows) less.
+//
+// One CTA to an SM, 12 warps: one copies tiles ahead into a ring, one issues the
+// MMAs, two prepare the next unit's query, and two groups of four warps take the
+// tiles in turn, each with scores, weights and sums O of its own, joined at the
+// unit's end.  A thread is a token: the weights of a token need nothing of
+// another but the maximum, which all agree on by one vote.
+//
+// All units' tiles in a row are cut into equal runs, one for each CTA, so that
+// ragged lengths load the SMs evenly; a cut unit leaves a part in the workspace
+// from each of its CTAs, joined by the last to arrive, in their order: results
+// do not depend on timing.
+//
+// Weights of 0 do not cancel a NaN code, so the rows of V that no row of the unit
+// sees are cleared in shared memory before the product, and NaN codes of tokens
+// that only some rows see are taken out and put into those rows' results.
+#include <algorithm>
+
+#include "fp8_paged.cuh"
+#include "sm103_ptx.cuh"
+
+namespace w8a8 {
+
+namespace {
+
+constexpr int kTile = 128;                    // tokens
+constexpr int kGroupThreads = 128;            // a softmax group
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kQueryWarp = 10, kQueryWarps = 2;
+constexpr int kThreads = 32 * (kQueryWarp + kQueryWarps);
+constexpr float kHeadroom = 2.f;
+constexpr float kNoScore = -1e25f;
+constexpr int kDead = 0x7f000000;             // the position of a token that is not there
+constexpr size_t kSmemMost = 227 * 1024;
+
+template <int D, int R>
+struct Few {
+  static constexpr int kQParts = 3, kPParts = 4;
+  static constexpr int kNS = (kQParts * R + 15) / 16 * 16;  // columns of the scores (M = 128: a multiple of 16)
+  static constexpr int kNP = kPParts * R;                   // columns of the output
+  static constexpr int kHalf = kTile * D;                   // K or V of a tile
+  static constexpr int kQ = kNS * D, kP = kNP * kTile, kDump = R * D * 4;
+  static constexpr int kFixed = 2 * kQ + 2 * kP + kDump + 1024;  // + alignment
+  static constexpr int kStatic = 8 * 1024;                  // room for the kernel's static shared memory
+  static constexpr int kFit = static_cast<int>((kSmemMost - kStatic - kFixed) / (2 * kHalf));
+  static constexpr int kStages = kFit > 8 ? 8 : kFit;
+  static_assert(kStages >= 3, "the ring holds the tiles of both groups and one more");
+  static constexpr int kSmem = kStages * 2 * kHalf + kFixed;
+  static constexpr uint32_t kCols = 2 * (kNS + kNP);
+  static constexpr uint32_t kTmem = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+  static_assert(kCols <= 512, "scores and outputs of both groups fit TMEM");
+  static constexpr int kPart = R * (D + 2);                 // floats: o [R][D], m [R], l [R]
+};
+
+__device__ __forceinline__ float ex2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
+
+// Two f16 numbers to e4m3 codes (the low one in the low byte), and back.
+__device__ __forceinline__ uint32_t to_e4m3x2(uint32_t h2) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+  return r;
+}
+__device__ __forceinline__ uint32_t from_e4m3x2(uint32_t codes) {
+  uint32_t r;
+  const uint16_t c = static_cast<uint16_t>(codes);
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  return r;
+}
+
+// Parts of two f16 numbers of at most 448: x = p0 + p1 2^-4 + p2 2^-8 ...; what
+// a part leaves over is at most 2^-4 of a power of two above it, and exact.
+template <int N>
+__device__ __forceinline__ void parts_of(uint32_t x, uint32_t (&part)[N]) {
+  const __half2 up = __float2half2_rn(16.f), down = __float2half2_rn(-16.f);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    part[i] = to_e4m3x2(x);
+    if (i + 1 < N) x = as_u32(__hfma2(as_half2(from_e4m3x2(part[i])), down, __hmul2(as_half2(x), up)));
+  }
+}
+
+__device__ __forceinline__ void mma_f8_by(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
+}
+
+// Descriptor of an operand tile of 64-byte rows with the 64-byte swizzle, atoms of
+// 8 rows (512 bytes); with M contiguous the next 64 elements are `next` bytes on.
+__device__ __forceinline__ uint64_t desc_sw64(uint32_t saddr, uint32_t next) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((next >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>(512u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(4u) << 61;
+  return d;
+}
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)); }
+
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Named barriers: 1 + g a group's own; 3 group 1's state is there, 4 it has been read.
+__device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroupThreads) : "memory"); }
+__device__ __forceinline__ bool group_any(int group, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x)), "r"(1 + group), "n"(kGroupThreads)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void both_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(2 * kGroupThreads) : "memory"); }
+__device__ __forceinline__ void both_arrive(int id) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(2 * kGroupThreads) : "memory"); }
+
+// ------------------------------------------------------------------ units
+
+// A unit: rows over the same tokens.  Dense: one request, KV head and R of its
+// rows (row r: token r / share, head r % share).  Sparse: one token, KV head and R
+// of its heads; its tokens are those of the selected columns, in their order.
+struct Unit {
+  int b;               // request, -1: a row of q that belongs to none
+  int first;           // first row of q of the request (sparse: the token's row)
+  int kvh, row0, rows; // rows of the unit: row0 .. row0 + rows - 1
+  int base;            // position of the request's new token 0 (sparse: the token's position)
+  int len;             // tokens of the request
+  int tiles;
+};
+
+// A place in the row of all units' tiles.
+template <int R, bool SPARSE>
+struct Cursor {
+  Unit u;
+  int group, groups, tile;  // row group of the unit, groups of the request; next tile
+  int token;                // sparse: the row of q
+
+  // Sparse: the request of `token`, looked for from request u.b on (starts rise).
+  __device__ __forceinline__ void find(const Fp8AttnParams& p, int from) {
+    const Fp8Paged& c = p.c;
+    u.b = u.base = -1;
+    u.len = 0;
+    for (int b = from; b < c.batch; ++b) {
+      const Fp8Request r = fp8_request(c, b);
+      if (token < r.first) break;
+      if (token < r.first + r.all) {
+        if (token - r.first < r.n) {
+          u.b = b;
+          u.len = r.len;
+          u.base = r.len - r.all + token - r.first;
+        }
+        seen = b;
+        return;
+      }
+      seen = b;
+    }
+  }
+  int seen;                 // sparse: requests in front of this one end before `token`
+
+  __device__ __forceinline__ void dense(const Fp8AttnParams& p, int b) {
+    const Fp8Request r = fp8_request(p.c, b);
+    u.b = b;
+    u.first = r.first;
+    u.len = r.len;
+    u.base = r.len - r.all;
+    rows_all = r.n * p.share;
+    groups = tiles_of(p, r) == 0 ? 0 : (rows_all + R - 1) / R;
+    u.tiles = tiles_of(p, r);
+  }
+  int rows_all;
+
+  // Tiles of each of a request's units, 0 if it is not this kernel's.
+  static __device__ __forceinline__ int tiles_of(const Fp8AttnParams& p, const Fp8Request& r) {
+    const int rows = r.n * p.share;
+    if (rows == 0 || rows > p.few_rows) return 0;
+    return max(1, (r.len + kTile - 1) / kTile);
+  }
+
+  __device__ __forceinline__ void set_rows(const Fp8AttnParams& p) {
+    u.row0 = group * R;
+    u.rows = min(R, (SPARSE ? p.share : rows_all) - u.row0);
+  }
+
+  __device__ __forceinline__ void next_unit(const Fp8AttnParams& p) {
+    tile = 0;
+    if (++group < groups) {
+      set_rows(p);
+      return;
+    }
+    group = 0;
+    if (++u.kvh == p.c.num_kv_heads) {
+      u.kvh = 0;
+      if (SPARSE) {
+        u.first = ++token;
+        find(p, seen);
+      } else {
+        int b = u.b;
+        do dense(p, ++b);
+        while (groups == 0);
+      }
+    }
+    set_rows(p);
+  }
+};
+
+// A unit that goes on in other CTAs.
+struct Open {
+  int b, first, rows, row0, kvh;
+  long long unit;  // its first tile; -1: none
+  int tiles;
+};
+
+__device__ __forceinline__ size_t out_at(const Fp8AttnParams& p, bool sparse, int first, int kvh, int row) {
+  const int token = sparse ? first : first + row / p.share, head = kvh * p.share + (sparse ? row : row % p.share);
+  return token * p.out_token_stride + head * p.out_head_stride;
+}
+
+__device__ __forceinline__ void store1(const Fp8AttnParams& p, size_t at, float y) {
+  if (p.out_fp16) static_cast<__half*>(p.out)[at] = __float2half_rn(y);
+  else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
+}
+
+template <int D, int R, bool SPARSE>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_rows_kernel(const Fp8AttnParams p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+  using C = Few<D, R>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* const s_ring = smem;                               // [stage] K, V
+  uint8_t* const s_p = smem + C::kStages * 2 * C::kHalf;      // [group] weights
+  uint8_t* const s_q = s_p + 2 * C::kP;                       // [2] queries
+  float* const s_dump = reinterpret_cast<float*>(s_q + 2 * C::kQ);  // group 1's outputs [R][D]
+  __shared__ uint64_t s_kfull[C::kStages], s_vfull[C::kStages], s_kempty[C::kStages], s_vempty[C::kStages];
+  __shared__ uint64_t s_qfull[2], s_qempty[2], s_sfull[2], s_sfree[2], s_pfull[2], s_pvdone[2];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_pos[C::kStages][8];       // positions of the first tokens of a tile's boxes
+  __shared__ long long s_scan[kThreads / 32], s_before;
+  __shared__ int s_item, s_found, s_last[2];
+  __shared__ Open s_open[2];
+  __shared__ __align__(16) float s_cs[2][R];   // [query buffer] factor of each row's scores
+  __shared__ __align__(16) int s_lim[2][R];    // last position that each row sees
+  __shared__ int s_limits[2][2];               // smallest and largest of them
+  __shared__ __align__(16) float s_m[2][R];    // [group] maxima
+  __shared__ float s_red[2][4][R];             // [group][warp]
+  __shared__ float s_state[2][2][R];           // [group] m in the log2 domain, l
+  __shared__ int s_nan[2][D];                  // [group] first token with a NaN in a dim
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int boxes = kTile / p.box;             // copies of a tile's K (or V)
+
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(smem_addr(&s_kfull[i]), boxes);
+      mbar_init(smem_addr(&s_vfull[i]), boxes);
+      mbar_init(smem_addr(&s_kempty[i]), 1);
+      mbar_init(smem_addr(&s_vempty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&s_qfull[i]), kQueryWarps);
+      mbar_init(smem_addr(&s_qempty[i]), 8);
+      mbar_init(smem_addr(&s_sfull[i]), 1);
+      mbar_init(smem_addr(&s_sfree[i]), 4);
+      mbar_init(smem_addr(&s_pfull[i]), 4);
+      mbar_init(smem_addr(&s_pvdone[i]), 1);
+    }
+    fence_barrier_init();
+  }
+  if (tid < 2) s_open[tid].unit = -1;
+  for (int i = tid; i < 2 * D; i += kThreads) (&s_nan[0][0])[i] = kDead;
+  // TMEM only after the wait: a kernel in front may still need it.  Dependents start
+  // only when it is taken: one that took it first and then waited for this kernel's
+  // end would never see it.
+  fp8_wait_for_predecessor();
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_addr(&s_tmem), C::kTmem);
+    tmem_relinquish();
+  }
+
+  // ---- this CTA's run
+  long long total = 0, share;
+  if constexpr (!SPARSE) {
+    const int per = (p.c.batch + kThreads - 1) / kThreads;
+    const int b0 = min(p.c.batch, tid * per), b1 = min(p.c.batch, b0 + per);
+    auto tiles_of = [&](int b) {
+      const Fp8Request r = fp8_request(p.c, b);
+      return static_cast<long long>(Cursor<R, SPARSE>::tiles_of(p, r)) * p.c.num_kv_heads * ((r.n * p.share + R - 1) / R);
+    };
+    long long mine = 0;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) mine += tiles_of(b);
+    long long run = mine;
+#pragma unroll 1
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, run, off);
+      if (lane >= off) run += o;
+    }
+    if (lane == 31) s_scan[warp] = run;
+    __syncthreads();
+    run -= mine;
+#pragma unroll 1
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) run += s_scan[w];
+      total += s_scan[w];
+    }
+    share = max(1LL, (total + gridDim.x - 1) / gridDim.x);
+    const long long at = share * blockIdx.x;
+    if (at >= run && at < run + mine) {
+#pragma unroll 1
+      for (int b = b0; b < b1; ++b) {
+        const long long w = tiles_of(b);
+        if (at < run + w) {
+          s_item = b;
+          s_before = run;
+          break;
+        }
+        run += w;
+      }
+    }
+  }
+  const int sparse_tiles = SPARSE ? static_cast<int>((static_cast<long long>(p.budget) * p.c.block_size + kTile - 1) / kTile) : 0;
+  const int sparse_groups = SPARSE ? (p.share + R - 1) / R : 0;
+  int sparse_seen = 0;
+  if constexpr (SPARSE) {
+    const long long per_token = static_cast<long long>(sparse_tiles) * sparse_groups * p.c.num_kv_heads;
+    total = per_token * p.c.tokens;
+    share = max(1LL, (total + gridDim.x - 1) / gridDim.x);
+    // the request of the run's first token: all threads look at once
+    const long long token = share * blockIdx.x / per_token;
+    if (tid == 0) s_found = 0;
+    __syncthreads();
+    if (p.c.query_start && token < p.c.tokens)
+      for (int b = tid; b < p.c.batch; b += kThreads)
+        if (__ldg(p.c.query_start + b) <= token) atomicMax(&s_found, b);
+    __syncthreads();
+    sparse_seen = p.c.query_start ? s_found : static_cast<int>(min(token, static_cast<long long>(p.c.batch)));
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  fp8_let_dependents_start();
+  const uint32_t tmem = s_tmem;
+  const long long r0 = share * blockIdx.x;
+  const int run_tiles = static_cast<int>(max(0LL, min(total - r0, min(share, 0x7fffffffLL))));
+  Cursor<R, SPARSE> at;
+  at.u.b = -1;
+  if (run_tiles > 0) {
+    if constexpr (SPARSE) {
+      const long long unit = r0 / sparse_tiles;
+      at.groups = sparse_groups;
+      at.group = static_cast<int>(unit % sparse_groups);
+      at.u.kvh = static_cast<int>(unit / sparse_groups % p.c.num_kv_heads);
+      at.token = at.u.first = static_cast<int>(unit / sparse_groups / p.c.num_kv_heads);
+      at.u.tiles = sparse_tiles;
+      at.tile = static_cast<int>(r0 % sparse_tiles);
+      at.find(p, at.seen = sparse_seen);
+    } else {
+      at.dense(p, s_item);
+      const long long in = r0 - s_before;
+      const int unit = static_cast<int>(in / at.u.tiles);
+      at.tile = static_cast<int>(in % at.u.tiles);
+      at.u.kvh = unit / at.groups;
+      at.group = unit % at.groups;
+    }
+    at.set_rows(p);
+  }
+  bool ok = true;
+
+  if (run_tiles == 0) {
+    // nothing to do
+  } else if (warp == kCopyWarp) {
+    // ================= copies: lane x has box x of the tile (K, then V)
+    const uint32_t ring = smem_addr(s_ring);
+    const uint32_t bytes = static_cast<uint32_t>(p.box * D);
+    const uint64_t pol = policy_evict_first();
+    // the place of this lane's box of a tile, a batch of tiles at once
+    const int ahead = 32 / boxes;          // tiles of a batch
+    Cursor<R, SPARSE> mine = at;           // the tile this lane looks up
+    int mine_at = 0;
+    int row = -1, pos = kDead;
+    auto look_up = [&](int tile_of_run) {
+      row = -1;
+      pos = kDead;
+      if (tile_of_run >= run_tiles) return;
+      int left = tile_of_run - mine_at;
+      mine_at = tile_of_run;
+      while (left > 0) {
+        const int step = min(left, mine.u.tiles - mine.tile);
+        left -= step;
+        mine.tile += step;
+        if (mine.tile == mine.u.tiles && left >= 0) mine.next_unit(p);
+      }
+      if (SPARSE && mine.u.b < 0) return;
+      const long long t = static_cast<long long>(mine.tile) * kTile + (lane % boxes) * p.box;
+      int col, off;
+      if (SPARSE) {
+        const int entry = static_cast<int>(t / p.c.block_size);
+        off = static_cast<int>(t - static_cast<long long>(entry) * p.c.block_size);
+        if (entry >= p.budget) return;
+        col = __ldg(p.selected + (static_cast<size_t>(mine.token) * p.c.num_kv_heads + mine.u.kvh) * p.budget + entry);
+        if (col < 0 || col >= p.c.max_blocks) return;
+        const long long first = static_cast<long long>(col) * p.c.block_size + off;
+        if (first > mine.u.base) return;
+        pos = static_cast<int>(first);
+      } else {
+        if (t >= mine.u.len) return;
+        col = static_cast<int>(t) / p.c.block_size;
+        off = static_cast<int>(t) - col * p.c.block_size;
+        pos = static_cast<int>(t);
+      }
+      const int block = __ldg(p.c.block_table + static_cast<size_t>(mine.u.b) * p.c.max_blocks + col);
+      if (block < 0 || block >= p.c.num_blocks) {
+        pos = kDead;
+        return;
+      }
+      row = block * p.c.block_size + off;
+    };
+    Cursor<R, SPARSE> head = at;  // the tile that is copied: its KV head
+    int j = 0;
+#pragma unroll 1
+    for (; j < run_tiles; ++j) {
+      if (j % ahead == 0) look_up(j + lane / boxes);
+      const int stage = j % C::kStages, src = (j % ahead) * boxes;
+      if (j >= C::kStages && !(ok = warp_wait(smem_addr(&s_kempty[stage]), ((j / C::kStages) & 1) ^ 1u))) break;
+      // (the positions of the stage's last tile were read before its V was given back)
+      if (j >= C::kStages && !(ok = warp_wait(smem_addr(&s_vempty[stage]), ((j / C::kStages) & 1) ^ 1u))) break;
+      const bool turn = lane >= src && lane < src + boxes;
+      if (turn) s_pos[stage][lane - src] = pos;
+      __syncwarp();
+      if (turn) {
+        const uint32_t kbar = smem_addr(&s_kfull[stage]), vbar = smem_addr(&s_vfull[stage]);
+        const uint32_t dst = ring + stage * 2 * C::kHalf + (lane - src) * bytes;
+        fence_proxy_async_shared();  // what was written there by hand before the copy over it
+        if (row >= 0) {
+          mbar_arrive_expect_tx(kbar, bytes);
+          tma_load_2d_hint(dst, &map_k, kbar, head.u.kvh * D, row, pol);
+          mbar_arrive_expect_tx(vbar, bytes);
+          tma_load_2d_hint(dst + C::kHalf, &map_v, vbar, head.u.kvh * D, row, pol);
+        } else {
+          mbar_arrive(kbar);
+          mbar_arrive(vbar);
+        }
+      }
+      if (j + 1 < run_tiles && ++head.tile == head.u.tiles) head.next_unit(p);
+    }
+    // a wait gave up: the copies in flight land before shared memory is released
+    if (!ok)
+      for (int i = max(0, j - C::kStages); i < j; ++i) {
+        mbar_wait(smem_addr(&s_kfull[i % C::kStages]), (i / C::kStages) & 1);
+        mbar_wait(smem_addr(&s_vfull[i % C::kStages]), (i / C::kStages) & 1);
+      }
+  } else if (warp == kMmaWarp) {
+    // ================= MMAs: tile j belongs to group j % 2 of its unit's tiles
+    const uint32_t leader = elect_one();
+    constexpr uint32_t kIdescS = make_idesc(kTile, C::kNS, 0);
+    constexpr uint32_t kIdescO = make_idesc(128, C::kNP, 0) | (1u << 15);  // V^T: M contiguous
+    const uint32_t tm = uniform(tmem);
+    const uint32_t ring = smem_addr(s_ring), pbuf = smem_addr(s_p), qbuf = smem_addr(s_q);
+    auto desc_k = [](uint32_t a) { return D == 128 ? smem_desc_sw128(a) : desc_sw64(a, 16); };
+    // heads of 64 fill half of M = 128; the other half reads what lies behind (the next
+    // 8 KB, always within the ring or the weights) and is not looked at
+    auto desc_v = [](uint32_t a) { return D == 128 ? smem_desc_mn_sw128(a, 16384) : desc_sw64(a, 8192); };
+    const int all = uniform(run_tiles);
+    uint32_t scount[2] = {0u, 0u}, pcount[2] = {0u, 0u};
+    int done = 0, units = 0;
+    auto scores = [&](int tile, int group, int q) {
+      const int stage = tile % C::kStages;
+      if (scount[group] > 0) ok = ok && warp_wait(smem_addr(&s_sfree[group]), (scount[group] - 1) & 1);
+      ++scount[group];
+      ok = ok && warp_wait(smem_addr(&s_kfull[stage]), (tile / C::kStages) & 1);
+      if (!ok) return;
+      tc_fence_after();
+      const uint64_t dk = desc_k(ring + stage * 2 * C::kHalf), dq = desc_k(qbuf + q * C::kQ);
+#pragma unroll
+      for (int kk = 0; kk < D / 32; ++kk) mma_f8_by(leader, tm + group * C::kNS, dk + 2 * kk, dq + 2 * kk, kIdescS, kk > 0);
+      mma_commit_by(leader, smem_addr(&s_kempty[stage]));
+      mma_commit_by(leader, smem_addr(&s_sfull[group]));
+    };
+#pragma unroll 1
+    while (done < all && ok) {
+      const int nt = uniform(min(at.u.tiles - at.tile, all - done));
+      const int q = units & 1;
+      ok = warp_wait(smem_addr(&s_qfull[q]), (units / 2) & 1);
+      tc_fence_after();
+#pragma unroll 1
+      for (int j = 0; j < 2 && j < nt && ok; ++j) scores(done + j, j, q);
+#pragma unroll 1
+      for (int j = 0; j < nt && ok; ++j) {
+        const int group = j & 1, stage = (done + j) % C::kStages;
+        ok = warp_wait(smem_addr(&s_pfull[group]), pcount[group] & 1);
+        ++pcount[group];
+        ok = ok && warp_wait(smem_addr(&s_vfull[stage]), ((done + j) / C::kStages) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t dv = desc_v(ring + stage * 2 * C::kHalf + C::kHalf);
+        const uint64_t dp = smem_desc_sw128(pbuf + group * C::kP);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 32; ++kk)
+          mma_f8_by(leader, tm + 2 * C::kNS + group * C::kNP, dv + kk * ((32 * D) >> 4), dp + 2 * kk, kIdescO, kk > 0 || j >= 2);
+        mma_commit_by(leader, smem_addr(&s_vempty[stage]));
+        mma_commit_by(leader, smem_addr(&s_pvdone[group]));
+        if (j + 2 < nt) scores(done + j + 2, group, q);
+      }
+      done += nt;
+      ++units;
+      at.tile += nt;
+      if (done < all) at.next_unit(p);
+    }
+  } else if (warp >= kQueryWarp) {
+    // ================= queries: rows w, w + 2, ... of the next unit
+    const int w = warp - kQueryWarp;
+    constexpr int kPer = D / 32;  // elements of a lane
+    const float ks = __ldg(p.k_scale), to_log2 = p.sm_scale * ks * kFp8Log2e;
+    int done = 0, units = 0;
+#pragma unroll 1
+    while (done < run_tiles) {
+      const int nt = min(at.u.tiles - at.tile, run_tiles - done);
+      const int buf = units & 1;
+      if (units >= 2 && !(ok = warp_wait(smem_addr(&s_qempty[buf]), ((units / 2) & 1) ^ 1u))) break;
+      uint8_t* const dst = s_q + buf * C::kQ;
+      constexpr int kBatch = 4;  // rows whose loads are in flight
+#pragma unroll 1
+      for (int i0 = w; i0 < R; i0 += kBatch * kQueryWarps) {
+        uint32_t raw[kBatch][kPer / 2];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = i0 + i * kQueryWarps;
+          const bool real = r < at.u.rows && at.u.b >= 0;
+          const int row = at.u.row0 + r, token = SPARSE ? at.u.first : at.u.first + row / p.share;
+          const int headq = at.u.kvh * p.share + (SPARSE ? row : row % p.share);
+          const uint16_t* src = static_cast<const uint16_t*>(p.q) + token * p.q_token_stride + headq * p.q_head_stride + kPer * lane;
+#pragma unroll
+          for (int k = 0; k < kPer / 2; ++k) {
+            raw[i][k] = 0u;
+            if (real)
+              raw[i][k] = p.q_vec ? __ldg(reinterpret_cast<const uint32_t*>(src) + k)
+                                  : static_cast<uint32_t>(__ldg(src + 2 * k)) | (static_cast<uint32_t>(__ldg(src + 2 * k + 1)) << 16);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = i0 + i * kQueryWarps;
+          if (r >= R) break;
+          float x[kPer], top = 0.f;
+          bool odd = false;
+#pragma unroll
+          for (int k = 0; k < kPer / 2; ++k) {
+            const float2 f = fp8_to_float2(raw[i][k], p.q_fp16);
+            x[2 * k] = f.x;
+            x[2 * k + 1] = f.y;
+            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+            odd = odd || !(fabsf(f.x) < INFINITY) || !(fabsf(f.y) < INFINITY);
+          }
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+          odd = __any_sync(0xffffffffu, odd);
+          // 2^e brings the largest element into [2^7, 2^8)
+          int e = 0;
+          if (top > 0.f && !odd) e = min(100, 7 + 127 - static_cast<int>(__float_as_uint(top) >> 23));
+          const float down = to_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          // the scale's sign goes to the query: the largest product is the largest score
+          const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), down);
+          if (lane == 0) {
+            // a row with a NaN or an infinity, or any row under a NaN scale, has NaN scores
+            s_cs[buf][r] = odd || !(fabsf(down) <= INFINITY) ? __int_as_float(0x7fffffff) : fmaxf(fabsf(down), 1e-37f);
+            s_lim[buf][r] = r < at.u.rows ? at.u.base + (SPARSE ? 0 : (at.u.row0 + r) / p.share) : -1;
+          }
+          uint32_t code[C::kQParts][kPer / 2];
+#pragma unroll
+          for (int k = 0; k < kPer / 2; ++k) {
+            uint32_t part[C::kQParts];
+            parts_of(as_u32(__floats2half2_rn(odd ? 0.f : x[2 * k] * up, odd ? 0.f : x[2 * k + 1] * up)), part);
+#pragma unroll
+            for (int j = 0; j < C::kQParts; ++j) code[j][k] = part[j];
+          }
+#pragma unroll
+          for (int j = 0; j < C::kQParts; ++j) {
+            const int n = j * R + r, byte = kPer * lane;
+            const int swz = D == 128 ? (((byte >> 4) ^ (n & 7)) << 4) : (((byte >> 4) ^ ((n >> 1) & 3)) << 4);
+            uint8_t* to = dst + n * D + swz + (byte & 15);
+            if (D == 128) *reinterpret_cast<uint32_t*>(to) = code[j][0] | (code[j][kPer / 2 - 1] << 16);
+            else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(code[j][0]);
+          }
+        }
+      }
+      // (columns past the last part are not looked at, but are finite)
+      for (int i = 32 * w + lane; i < (C::kNS - C::kQParts * R) * D / 4; i += 32 * kQueryWarps)
+        reinterpret_cast<uint32_t*>(dst + C::kQParts * R * D)[i] = 0u;
+      if (w == 0 && lane == 0) {
+        const int low = at.u.base + (SPARSE ? 0 : at.u.row0 / p.share);
+        s_limits[buf][0] = low;
+        s_limits[buf][1] = SPARSE ? low : at.u.base + (at.u.row0 + at.u.rows - 1) / p.share;
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&s_qfull[buf]));
+      done += nt;
+      ++units;
+      at.tile += nt;
+      if (done < run_tiles) at.next_unit(p);
+    }
+  } else {
+    // ================= softmax: thread = token of the tile (in the outputs: dim)
+    const int group = warp / 4, quarter = warp % 4, token = 32 * quarter + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter) << 21);
+    const uint32_t s_cols = lanes + group * C::kNS, o_cols = lanes + 2 * C::kNS + group * C::kNP;
+    const uint32_t weights = smem_addr(s_p) + group * C::kP;
+    uint32_t swz[8];  // a token's byte in rows n of the weights, by n % 8
+#pragma unroll
+    for (int i = 0; i < 8; ++i) swz[i] = weights + i * 128 + (((token >> 4) ^ i) << 4) + (token & 15);
+    float* const m = s_m[group];
+    const float vscale = __ldg(p.v_scale);
+    uint32_t count = 0u;  // tiles of this group
+    int done = 0, units = 0;
+#pragma unroll 1
+    while (done < run_tiles) {
+      const int nt = min(at.u.tiles - at.tile, run_tiles - done);
+      const int buf = units & 1;
+      float l[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) l[r] = 0.f;
+      if (ok) ok = warp_wait(smem_addr(&s_qfull[buf]), (units / 2) & 1);
+      const int low = s_limits[buf][0], high = s_limits[buf][1];
+      group_sync(group);  // the last unit's maxima have been read
+      if (token < R) m[token] = kNoScore;
+      group_sync(group);
+      int mine = 0;
+#pragma unroll 1
+      for (int j = group; j < nt; j += 2) {
+        const int stage = (done + j) % C::kStages;
+        if (ok) ok = warp_wait(smem_addr(&s_sfull[group]), count & 1);
+        if (ok) ok = warp_wait(smem_addr(&s_kfull[stage]), ((done + j) / C::kStages) & 1);  // (long over: for s_pos)
+        tc_fence_after();
+        const int first = s_pos[stage][token / p.box], pos = first + token % p.box;
+        float s[R];
+#pragma unroll
+        for (int r0 = 0; r0 < R; r0 += 8) {
+          uint32_t x[C::kQParts][8];
+#pragma unroll
+          for (int i = 0; i < C::kQParts; ++i) tmem_ld8(s_cols + i * R + r0, x[i]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < C::kQParts; ++i) tmem_loaded(x[i]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            s[r0 + i] = fmaf(fmaf(__uint_as_float(x[2][i]), 0.0625f, __uint_as_float(x[1][i])), 0.0625f, __uint_as_float(x[0][i]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&s_sfree[group]));
+        // tokens that some row does not see: the last ones, and places without a token
+        const bool hidden = pos > low;
+        uint32_t blind = 0u;
+        const bool edge = __any_sync(0xffffffffu, hidden);
+        if (edge) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            if (pos > s_lim[buf][r]) {
+              blind |= 1u << r;
+              s[r] = -INFINITY;
+            }
+          }
+          // V's row must not reach the rows that do not see it as 0 times NaN
+          if (ok) ok = warp_wait(smem_addr(&s_vfull[stage]), ((done + j) / C::kStages) & 1);
+          if (hidden && ok) {
+            uint4* v = reinterpret_cast<uint4*>(s_ring + stage * 2 * C::kHalf + C::kHalf + token * D);
+            if (pos > high) {
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+            } else {
+#pragma unroll 1
+              for (int i = 0; i < D / 16; ++i) {
+                const uint4 x = v[i];
+                const uint4 y = make_uint4(fp8_nan_to_zero(x.x), fp8_nan_to_zero(x.y), fp8_nan_to_zero(x.z), fp8_nan_to_zero(x.w));
+                if (x.x == y.x && x.y == y.y && x.z == y.z && x.w == y.w) continue;
+                v[i] = y;
+                // chunk i of the row holds dims 16 (i ^ swizzle) ..
+                const int chunk = D == 128 ? i ^ (token & 7) : i ^ ((token >> 1) & 3);
+                const uint32_t from[4] = {x.x, x.y, x.z, x.w};
+                for (int c = 0; c < 16; ++c)
+                  if ((from[c / 4] >> (8 * (c % 4)) & 0x7Fu) == 0x7Fu) atomicMin(&s_nan[group][16 * chunk + c], pos);
+              }
+            }
+          }
+        }
+        // ---- the maximum, raised when a weight would pass 2^kHeadroom
+        bool past = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r) past = past || (s[r] - m[r]) * s_cs[buf][r] > kHeadroom;
+        if (group_any(group, past)) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            float x = s[r];
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+            if (lane == 0) s_red[group][quarter][r] = x;
+          }
+          group_sync(group);
+          if (mine > 0) {
+            // the product before this one has to be in
+            if (ok) ok = warp_wait(smem_addr(&s_pvdone[group]), (count - 1) & 1);
+            tc_fence_after();
+          }
+#pragma unroll 1
+          for (int r0 = 0; r0 < R; r0 += 8) {
+            float alpha[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = r0 + i;
+              const float top = fmaxf(fmaxf(s_red[group][0][r], s_red[group][1][r]), fmaxf(s_red[group][2][r], s_red[group][3][r]));
+              const float old = m[r], now = fmaxf(old, top);
+              alpha[i] = now > old ? ex2_fast((old - now) * s_cs[buf][r]) : 1.f;
+            }
+            if (mine > 0) {
+#pragma unroll 1
+              for (int part = 0; part < C::kPParts; ++part) {
+                uint32_t o[8];
+                tmem_ld8(o_cols + part * R + r0, o);
+                tmem_ld_wait();
+                tmem_loaded(o);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[i]);
+                tmem_st8(o_cols + part * R + r0, o);
+              }
+              tmem_st_wait();
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float top = fmaxf(fmaxf(s_red[group][0][r], s_red[group][1][r]), fmaxf(s_red[group][2][r], s_red[group][3][r]));
+            const float old = m[r], now = fmaxf(old, top);
+            if (now > old) l[r] *= ex2_fast((old - now) * s_cs[buf][r]);
+          }
+          group_sync(group);  // all have read the old maxima
+          if (token < R)
+            m[token] = fmaxf(m[token], fmaxf(fmaxf(s_red[group][0][token], s_red[group][1][token]),
+                                             fmaxf(s_red[group][2][token], s_red[group][3][token])));
+          group_sync(group);
+        }
+        // ---- weights times 2^6, and their parts; the last product has read its own
+        if (count > 0 && ok) ok = warp_wait(smem_addr(&s_pvdone[group]), (count - 1) & 1);
+#pragma unroll
+        for (int r = 0; r < R; r += 2) {
+          float a = ex2_fast(fmaf(s[r] - m[r], s_cs[buf][r], 8.f - kHeadroom));
+          float b = ex2_fast(fmaf(s[r + 1] - m[r + 1], s_cs[buf][r + 1], 8.f - kHeadroom));
+          if (edge) {
+            if (blind >> r & 1u) a = 0.f;
+            if (blind >> r & 2u) b = 0.f;
+          }
+          l[r] += a;
+          l[r + 1] += b;
+          uint32_t part[C::kPParts];
+          parts_of(as_u32(__floats2half2_rn(a, b)), part);
+#pragma unroll
+          for (int i = 0; i < C::kPParts; ++i) {
+            const int n = i * R + r;
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(swz[n & 7] + (n & ~7) * 128), "r"(part[i]) : "memory");
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(swz[(n + 1) & 7] + ((n + 1) & ~7) * 128), "r"(part[i] >> 8) : "memory");
+          }
+        }
+        fence_proxy_async_shared();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&s_pfull[group]));
+        ++count;
+        ++mine;
+      }
+
+      // ---- the unit's end, or the run's
+      const bool whole = at.tile == 0 && nt == at.u.tiles;
+      if (mine > 0 && ok) ok = warp_wait(smem_addr(&s_pvdone[group]), (count - 1) & 1);
+      tc_fence_after();
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float x = l[r];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+        if (lane == 0) s_red[group][quarter][r] = x;
+      }
+      group_sync(group);
+      if (group == 1 && units > 0) both_sync(4);  // the last unit's state and outputs have been read
+      if (token < R) {
+        const float sum = (s_red[group][0][token] + s_red[group][1][token]) + (s_red[group][2][token] + s_red[group][3][token]);
+        s_state[group][0][token] = sum != 0.f ? m[token] * s_cs[buf][token] : -INFINITY;  // a sum of 0: nothing seen
+        s_state[group][1][token] = sum;
+      }
+      group_sync(group);
+      const int nan_from = token < D ? s_nan[group][token] : kDead;
+      // this group's output of dim `token` and row r
+      auto output = [&](int r0, float (&y)[8]) {
+        uint32_t o[C::kPParts][8];
+#pragma unroll
+        for (int i = 0; i < C::kPParts; ++i) tmem_ld8(o_cols + i * R + r0, o[i]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < C::kPParts; ++i) tmem_loaded(o[i]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float x = __uint_as_float(o[C::kPParts - 1][i]);
+#pragma unroll
+          for (int k = C::kPParts - 2; k >= 0; --k) x = fmaf(x, 0.0625f, __uint_as_float(o[k][i]));
+          y[i] = mine > 0 ? x : 0.f;
+        }
+        if (nan_from != kDead) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (nan_from <= s_lim[buf][r0 + i]) y[i] = __int_as_float(0x7fffffff);
+        }
+      };
+      if (group == 1) {
+#pragma unroll 1
+        for (int r0 = 0; r0 < R; r0 += 8) {
+          float y[8];
+          output(r0, y);
+          if (token < D) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s_dump[(r0 + i) * D + token] = y[i];
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        both_arrive(3);
+      } else {
+        both_sync(3);
+        float* part = nullptr;
+        const long long unit = r0 + done - at.tile;
+        const bool begun = unit / share == blockIdx.x;
+        if (!whole) part = p.partial + (2 * static_cast<size_t>(blockIdx.x) + begun) * C::kPart;
+#pragma unroll 1
+        for (int r0 = 0; r0 < R; r0 += 8) {
+          float y[8];
+          output(r0, y);
+          tc_fence_before();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = r0 + i;
+            if (r >= at.u.rows || token >= D) continue;
+            const float m0 = s_state[0][0][r], m1 = s_state[1][0][r], l0 = s_state[0][1][r], l1 = s_state[1][1][r];
+            const float mx = fmaxf(m0, m1);
+            const float a0 = l0 != 0.f ? ex2_fast(m0 - mx) : 0.f, a1 = l1 != 0.f ? ex2_fast(m1 - mx) : 0.f;
+            // (a factor of 0 takes what was never written out of the sum)
+            float o = (l0 != 0.f ? a0 * y[i] : 0.f) + (l1 != 0.f ? a1 * s_dump[r * D + token] : 0.f);
+            const float sum = (l0 != 0.f ? a0 * l0 : 0.f) + (l1 != 0.f ? a1 * l1 : 0.f);
+            if (whole) {
+              if (!SPARSE || at.u.b >= 0)
+                store1(p, out_at(p, SPARSE, at.u.first, at.u.kvh, at.u.row0 + r) + token, sum != 0.f ? o * (vscale / sum) : 0.f);
+            } else {
+              __stcg(part + r * D + token, o);
+              if (token == 0) {
+                __stcg(part + R * D + r, mx);
+                __stcg(part + R * (D + 1) + r, sum);
+              }
+            }
+          }
+        }
+        if (!whole && tid == 0) s_open[begun] = {at.u.b, at.u.first, at.u.rows, at.u.row0, at.u.kvh, unit, at.u.tiles};
+        __syncwarp();
+        both_arrive(4);
+      }
+      if (nan_from != kDead) s_nan[group][token] = kDead;  // (read by this thread alone)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&s_qempty[buf]));
+      done += nt;
+      ++units;
+      at.tile += nt;
+      if (done < run_tiles) at.next_unit(p);
+    }
+    if (group == 1) both_sync(4);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmem);
+  }
+  if (s_open[0].unit < 0 && s_open[1].unit < 0) return;
+
+  // ---- join the CTAs' parts of a unit, in the last CTA to arrive
+  if (tid < 2) {
+    const Open u = s_open[tid];
+    s_last[tid] = 0;
+    if (u.unit >= 0) {
+      const long long c0 = u.unit / share, c1 = (u.unit + u.tiles - 1) / share;
+      __threadfence();  // the CTA's stores, seen through the barrier, before the arrival
+      s_last[tid] = atomicAdd(p.counters + c0, 1u) == static_cast<unsigned>(c1 - c0);
+      if (s_last[tid]) {
+        p.counters[c0] = 0u;
+        __threadfence();
+      }
+    }
+  }
+  __syncthreads();
+  const float vscale = __ldg(p.v_scale);
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    if (!s_last[which]) continue;
+    const Open u = s_open[which];
+    if (SPARSE && u.b < 0) continue;
+    const long long c0 = u.unit / share;
+    const int parts = static_cast<int>((u.unit + u.tiles - 1) / share - c0) + 1;
+    // part 0 is the second place of CTA c0, part k the first of CTA c0 + k
+    const float* src = p.partial + 2 * static_cast<size_t>(c0) * C::kPart;
+#pragma unroll 1
+    for (int item = tid; item < u.rows * (D / 4); item += kThreads) {
+      const int r = item / (D / 4), d = 4 * (item % (D / 4));
+      float mx = -INFINITY, sum = 0.f;
+#pragma unroll 8
+      for (int k = 0; k < parts; ++k) mx = fmaxf(mx, __ldcg(src + (k ? 2 * k : 1) * static_cast<size_t>(C::kPart) + R * D + r));
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int k = 0; k < parts; ++k) {
+        const float* s = src + (k ? 2 * k : 1) * static_cast<size_t>(C::kPart);
+        const float l = __ldcg(s + R * (D + 1) + r), mk = __ldcg(s + R * D + r);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(s + r * D + d));
+        if (l == 0.f) continue;
+        const float a = ex2_fast(mk - mx);
+        sum = fmaf(a, l, sum);
+        o = make_float4(fmaf(a, v.x, o.x), fmaf(a, v.y, o.y), fmaf(a, v.z, o.z), fmaf(a, v.w, o.w));
+      }
+      const float inv = sum != 0.f ? vscale / sum : 0.f;
+      const size_t to = out_at(p, SPARSE, u.first, u.kvh, u.row0 + r) + d;
+      store1(p, to, sum != 0.f ? o.x * inv : 0.f);
+      store1(p, to + 1, sum != 0.f ? o.y * inv : 0.f);
+      store1(p, to + 2, sum != 0.f ? o.z * inv : 0.f);
+      store1(p, to + 3, sum != 0.f ? o.w * inv : 0.f);
+    }
+  }
+}
+
+template <int D, int R, bool SPARSE>
+cudaError_t launch_t(const Fp8AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, int num_sms, cudaStream_t stream) {
+  auto kern = fp8_rows_kernel<D, R, SPARSE>;
+  // the attribute is per function and device; setting it again is harmless
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<D, R>::kSmem);
+  if (e != cudaSuccess) return e;
+  return fp8_launch(kern, dim3(static_cast<unsigned>(std::min(num_sms, kFp8MaxCtas))), dim3(kThreads), Few<D, R>::kSmem, stream, p, k, v);
+}
+
+template <int D, bool SPARSE>
+cudaError_t launch_r(const Fp8AttnParams& p, int rows, const CUtensorMap& k, const CUtensorMap& v, int num_sms, cudaStream_t stream) {
+  if (rows <= 8) return launch_t<D, 8, SPARSE>(p, k, v, num_sms, stream);
+  if (rows <= 16) return launch_t<D, 16, SPARSE>(p, k, v, num_sms, stream);
+  return launch_t<D, 32, SPARSE>(p, k, v, num_sms, stream);
+}
+
+}  // namespace
+
+size_t fp8_rows_workspace(int rows, int head_dim, int num_sms) {
+  const int r = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  return kFp8CounterBytes + static_cast<size_t>(std::min(num_sms, kFp8MaxCtas)) * 2 * r * (head_dim + 2) * sizeof(float);
+}
+
+cudaError_t read_clear_fp8_rows_status(int* flags) {
+  int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_device_status, sizeof(int));
+  if (e != cudaSuccess) return e;
+  const int zero = 0;
+  e = cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int));
+  *flags = v;
+  return e;
+}
+
+cudaError_t launch_fp8_rows(const Fp8AttnParams& p, int rows, const CUtensorMap& map_k, const CUtensorMap& map_v, int num_sms,
+                            cudaStream_t stream) {
+  if (p.selected)
+    return p.c.head_dim == 64 ? launch_r<64, true>(p, rows, map_k, map_v, num_sms, stream)
+                              : launch_r<128, true>(p, rows, map_k, map_v, num_sms, stream);
+  return p.c.head_dim == 64 ? launch_r<64, false>(p, rows, map_k, map_v, num_sms, stream)
+                            : launch_r<128, false>(p, rows, map_k, map_v, num_sms, stream);
+}
+
+}  // namespace w8a8

@@ -308,11 +308,27 @@ struct Fp8AttnParams {
   void* out;              // as q
   long long out_token_stride, out_head_stride;
   int out_fp16, out_vec;
+  int box;                // tokens of one copy: the largest power of two in block_size, at most 128
+  // set by the launchers
+  int few_rows;           // requests of more rows than this are not the few-rows kernel's
+  unsigned* counters;     // parts of a cut unit that have arrived, left zero
+  float* partial;         // [CTAs][2] partial results
 };
+constexpr int kFp8MaxCtas = 1024;
+constexpr size_t kFp8CounterBytes = kFp8MaxCtas * sizeof(unsigned);
+// Units of at most 32 rows (fp8_rows.cu; `rows`: the most of a request, or a
+// token's heads).  The maps: caches as [rows, num_kv_heads * head_dim] bytes, a
+// box of `box` rows and head_dim bytes, swizzled over a row of the box.
+size_t fp8_rows_workspace(int rows, int head_dim, int num_sms);
+cudaError_t launch_fp8_rows(const Fp8AttnParams& p, int rows, const CUtensorMap& map_k, const CUtensorMap& map_v, int num_sms,
+                            cudaStream_t stream);
+cudaError_t read_clear_fp8_rows_status(int* flags);
 size_t fp8_paged_attention_workspace(int share, long long max_query_len, int head_dim, int num_sms);
-size_t fp8_sparse_attention_workspace(long long tokens, int num_kv_heads, int share, int head_dim, long long budget_tokens,
-                                      int num_sms);
-cudaError_t launch_fp8_attention(const Fp8AttnParams& p, int num_sms, void* workspace, cudaStream_t stream);
+size_t fp8_sparse_attention_workspace(int share, int head_dim, int num_sms);
+cudaError_t launch_fp8_attention(const Fp8AttnParams& p, const CUtensorMap& map_k, const CUtensorMap& map_v, int num_sms,
+                                 void* workspace, cudaStream_t stream);
+// Reads and clears the kernels' status words (call after a sync).
+cudaError_t read_clear_fp8_status(int* flags);
 
 // Verification of drafted tokens (verify.cu).
 struct VerifyArgs {
