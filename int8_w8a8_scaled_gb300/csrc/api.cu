@@ -136,8 +136,10 @@ w8a8_status make_operand_map(CUtensorMap* map, const void* base, bool f16, long 
 }
 
 // An fp8 cache as [rows, row_bytes] bytes, boxes of box_rows rows and `bytes` (64
-// or 128) bytes, swizzled over a row of the box.
-w8a8_status make_cache_map(CUtensorMap* map, const void* base, long long rows, long long row_bytes, int bytes, int box_rows) {
+// or 128) bytes, swizzled over a row of the box.  `alone`: the neighbouring heads' rows
+// are not read at about the same time, so L2 is to fetch no more than the box's own.
+w8a8_status make_cache_map(CUtensorMap* map, const void* base, long long rows, long long row_bytes, int bytes, int box_rows,
+                           bool alone) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(W8A8_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
@@ -147,7 +149,9 @@ w8a8_status make_cache_map(CUtensorMap* map, const void* base, long long rows, l
   auto encode = [&] {
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+              !alone ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                     : bytes == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   };
   CUresult r = encode();
   if (r == CUDA_ERROR_INVALID_CONTEXT) {
@@ -1370,8 +1374,8 @@ w8a8_status fp8_attention_call(const void* q, int q_dtype, int64_t num_q_heads, 
   while (p.box < 128 && c.block_size % (2 * p.box) == 0) p.box *= 2;
   CUtensorMap map_k, map_v;
   const long long rows = static_cast<long long>(c.num_blocks) * c.block_size, row_bytes = static_cast<long long>(c.num_kv_heads) * d;
-  if ((st = make_cache_map(&map_k, k_cache, rows, row_bytes, c.head_dim, p.box)) != W8A8_OK) return st;
-  if ((st = make_cache_map(&map_v, v_cache, rows, row_bytes, c.head_dim, p.box)) != W8A8_OK) return st;
+  if ((st = make_cache_map(&map_k, k_cache, rows, row_bytes, c.head_dim, p.box, selected != nullptr)) != W8A8_OK) return st;
+  if ((st = make_cache_map(&map_v, v_cache, rows, row_bytes, c.head_dim, p.box, selected != nullptr)) != W8A8_OK) return st;
   cudaError_t e = w8a8::launch_fp8_attention(p, map_k, map_v, dev.sms, workspace, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, selected ? "sparse fp8 KV attention launch" : "paged fp8 KV attention launch");
   return ok();

@@ -20,14 +20,16 @@
 // Bound by the cache's bytes, 2 D a token: the MMAs of a tile take about half of
 // the time that HBM needs for it, and its softmax (128 tokens x R rows) less.
 //
-// One CTA to an SM, 12 warps: one copies tiles ahead into a ring, one issues the
-// MMAs, two prepare the next unit's query, and two groups of four warps take the
-// tiles in turn, each with scores, weights and sums O of its own, joined at the
-// unit's end.  A thread is a token: the weights of a token need nothing of
+// One CTA to an SM, 12 warps: one copies tiles ahead into a ring, one prepares the
+// next unit's query, and two groups of four warps take the tiles in turn, each with
+// scores, weights and sums O of its own, joined at the unit's end, and each with a
+// warp that issues its MMAs (one for both spent 1300 cycles a tile on waits that
+// were over and on issuing, more than HBM's time for it).  A thread is a token: the weights of a token need nothing of
 // another but the maximum, which all agree on by one vote.
 //
 // All units' tiles in a row are cut into equal runs, one for each CTA, so that
-// ragged lengths load the SMs evenly; a cut unit leaves a part in the workspace
+// ragged lengths load the SMs evenly (CTAs side by side take neighbouring KV heads of
+// the same tokens: a head's rows are 128-byte pieces of the cache's); a cut unit leaves a part in the workspace
 // from each of its CTAs, joined by the last to arrive, in their order: results
 // do not depend on timing.
 //
@@ -45,10 +47,13 @@ namespace {
 
 constexpr int kTile = 128;                    // tokens
 constexpr int kGroupThreads = 128;            // a softmax group
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kQueryWarp = 10, kQueryWarps = 2;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kQueryWarp = 11, kQueryWarps = 1;
 constexpr int kThreads = 32 * (kQueryWarp + kQueryWarps);
 constexpr float kHeadroom = 2.f;
 constexpr float kNoScore = -1e25f;
+// Tiles whose places are kept: keys are fetched at most half as many tiles ahead of
+// the values, and a group has read a tile's places before its next scores are made.
+constexpr int kPlaces = 32;
 constexpr int kDead = 0x7f000000;             // the position of a token that is not there
 constexpr size_t kSmemMost = 227 * 1024;
 
@@ -62,8 +67,10 @@ struct Few {
   static constexpr int kFixed = 2 * kQ + 2 * kP + kDump + 1024;  // + alignment
   static constexpr int kStatic = 8 * 1024;                  // room for the kernel's static shared memory
   static constexpr int kFit = static_cast<int>((kSmemMost - kStatic - kFixed) / (2 * kHalf));
-  static constexpr int kStages = kFit > 8 ? 8 : kFit;
-  static_assert(kStages >= 3, "the ring holds the tiles of both groups and one more");
+  // even, and the groups take every second tile of the run, so that the tile before in a
+  // stage was the same group's: no wait for a stage can mistake another phase for its own
+  static constexpr int kStages = kFit > 8 ? 8 : kFit / 2 * 2;
+  static_assert(kStages >= 4, "the ring holds two tiles of each group");
   static constexpr int kSmem = kStages * 2 * kHalf + kFixed;
   static constexpr uint32_t kCols = 2 * (kNS + kNP);
   static constexpr uint32_t kTmem = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
@@ -126,16 +133,44 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
 }
 
-// Descriptor of an operand tile of 64-byte rows with the 64-byte swizzle, atoms of
-// 8 rows (512 bytes); with M contiguous the next 64 elements are `next` bytes on.
-__device__ __forceinline__ uint64_t desc_sw64(uint32_t saddr, uint32_t next) {
+// The largest of a warp's numbers (NaN has no part in it).
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Descriptor of an operand tile of ROW-byte rows (32, 64 or 128) with the swizzle of
+// that width, in atoms of 8 rows.  With M or N contiguous a row is one K index, and
+// the next ROW elements of M or N are `next` bytes on.
+template <int ROW>
+__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr, uint32_t next) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
   d |= static_cast<uint64_t>((next >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>(512u >> 4) << 32;
+  d |= static_cast<uint64_t>((8u * ROW) >> 4) << 32;
   d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(4u) << 61;
+  d |= static_cast<uint64_t>(ROW == 128 ? 2u : ROW == 64 ? 4u : 6u) << 61;
   return d;
+}
+
+// Where the 16-byte chunk `chunk` of row `row` lies in such a tile.
+template <int ROW>
+__device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
+  const int turn = ROW == 128 ? row & 7 : ROW == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
+  return static_cast<uint32_t>(row * ROW + ((chunk ^ turn) << 4));
+}
+
+__device__ __forceinline__ bool mbar_is_over(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)); }
@@ -175,6 +210,7 @@ struct Unit {
 template <int R, bool SPARSE>
 struct Cursor {
   Unit u;
+  int lane;                 // the CTA's place among those that go side by side over the KV heads
   int group, groups, tile;  // row group of the unit, groups of the request; next tile
   int token;                // sparse: the row of q
 
@@ -231,8 +267,9 @@ struct Cursor {
       return;
     }
     group = 0;
-    if (++u.kvh == p.c.num_kv_heads) {
-      u.kvh = 0;
+    u.kvh += p.side;
+    if (u.kvh >= p.c.num_kv_heads) {
+      u.kvh = lane;
       if (SPARSE) {
         u.first = ++token;
         find(p, seen);
@@ -276,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t s_kfull[C::kStages], s_vfull[C::kStages], s_kempty[C::kStages], s_vempty[C::kStages];
   __shared__ uint64_t s_qfull[2], s_qempty[2], s_sfull[2], s_sfree[2], s_pfull[2], s_pvdone[2];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_pos[C::kStages][8];       // positions of the first tokens of a tile's boxes
+  __shared__ int s_pos[kPlaces][8], s_row[kPlaces][8];  // of a tile's boxes: positions of the first tokens, rows of the cache
   __shared__ long long s_scan[kThreads / 32], s_before;
   __shared__ int s_item, s_found, s_last[2];
   __shared__ Open s_open[2];
@@ -285,6 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int s_limits[2][2];               // smallest and largest of them
   __shared__ __align__(16) float s_m[2][R];    // [group] maxima
   __shared__ float s_red[2][4][R];             // [group][warp]
+  __shared__ __align__(16) float s_alpha[2][R]; // [group] what a raised maximum makes of the sums so far
   __shared__ float s_state[2][2][R];           // [group] m in the log2 domain, l
   __shared__ int s_nan[2][D];                  // [group] first token with a NaN in a dim
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -299,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&s_qfull[i]), kQueryWarps);
-      mbar_init(smem_addr(&s_qempty[i]), 8);
+      mbar_init(smem_addr(&s_qempty[i]), 10);  // the softmax warps, and the MMA warps, so that none falls a phase behind
       mbar_init(smem_addr(&s_sfull[i]), 1);
       mbar_init(smem_addr(&s_sfree[i]), 4);
       mbar_init(smem_addr(&s_pfull[i]), 4);
@@ -318,14 +356,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
 
-  // ---- this CTA's run
+  // ---- this CTA's run: number `nth` of those of its place `place`, over every side-th
+  // KV head from that one on
+  const int place = static_cast<int>(blockIdx.x) % p.side, nth = static_cast<int>(blockIdx.x) / p.side;
+  const int runs = static_cast<int>(gridDim.x) / p.side;
   long long total = 0, share;
   if constexpr (!SPARSE) {
     const int per = (p.c.batch + kThreads - 1) / kThreads;
     const int b0 = min(p.c.batch, tid * per), b1 = min(p.c.batch, b0 + per);
     auto tiles_of = [&](int b) {
       const Fp8Request r = fp8_request(p.c, b);
-      return static_cast<long long>(Cursor<R, SPARSE>::tiles_of(p, r)) * p.c.num_kv_heads * ((r.n * p.share + R - 1) / R);
+      return static_cast<long long>(Cursor<R, SPARSE>::tiles_of(p, r)) * (p.c.num_kv_heads / p.side) * ((r.n * p.share + R - 1) / R);
     };
     long long mine = 0;
 #pragma unroll 1
@@ -344,8 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w < warp) run += s_scan[w];
       total += s_scan[w];
     }
-    share = max(1LL, (total + gridDim.x - 1) / gridDim.x);
-    const long long at = share * blockIdx.x;
+    share = max(1LL, (total + runs - 1) / runs);
+    const long long at = share * nth;
     if (at >= run && at < run + mine) {
 #pragma unroll 1
       for (int b = b0; b < b1; ++b) {
@@ -363,11 +404,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int sparse_groups = SPARSE ? (p.share + R - 1) / R : 0;
   int sparse_seen = 0;
   if constexpr (SPARSE) {
-    const long long per_token = static_cast<long long>(sparse_tiles) * sparse_groups * p.c.num_kv_heads;
+    const long long per_token = static_cast<long long>(sparse_tiles) * sparse_groups * (p.c.num_kv_heads / p.side);
     total = per_token * p.c.tokens;
-    share = max(1LL, (total + gridDim.x - 1) / gridDim.x);
+    share = max(1LL, (total + runs - 1) / runs);
     // the request of the run's first token: all threads look at once
-    const long long token = share * blockIdx.x / per_token;
+    const long long token = share * nth / per_token;
     if (tid == 0) s_found = 0;
     __syncthreads();
     if (p.c.query_start && token < p.c.tokens)
@@ -381,17 +422,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   fp8_let_dependents_start();
   const uint32_t tmem = s_tmem;
-  const long long r0 = share * blockIdx.x;
+  const long long r0 = share * nth;
   const int run_tiles = static_cast<int>(max(0LL, min(total - r0, min(share, 0x7fffffffLL))));
   Cursor<R, SPARSE> at;
   at.u.b = -1;
+  at.lane = place;
   if (run_tiles > 0) {
     if constexpr (SPARSE) {
       const long long unit = r0 / sparse_tiles;
       at.groups = sparse_groups;
       at.group = static_cast<int>(unit % sparse_groups);
-      at.u.kvh = static_cast<int>(unit / sparse_groups % p.c.num_kv_heads);
-      at.token = at.u.first = static_cast<int>(unit / sparse_groups / p.c.num_kv_heads);
+      const int heads = p.c.num_kv_heads / p.side;
+      at.u.kvh = place + p.side * static_cast<int>(unit / sparse_groups % heads);
+      at.token = at.u.first = static_cast<int>(unit / sparse_groups / heads);
       at.u.tiles = sparse_tiles;
       at.tile = static_cast<int>(r0 % sparse_tiles);
       at.find(p, at.seen = sparse_seen);
@@ -400,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long in = r0 - s_before;
       const int unit = static_cast<int>(in / at.u.tiles);
       at.tile = static_cast<int>(in % at.u.tiles);
-      at.u.kvh = unit / at.groups;
+      at.u.kvh = place + p.side * (unit / at.groups);
       at.group = unit % at.groups;
     }
     at.set_rows(p);
@@ -456,66 +499,97 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       row = block * p.c.block_size + off;
     };
-    Cursor<R, SPARSE> head = at;  // the tile that is copied: its KV head
-    int j = 0;
+    // K and V each go out when their place in the ring is free: K's is long before V's
+    Cursor<R, SPARSE> khead = at, vhead = at;  // their tiles: the KV heads
+    int jk = 0, jv = 0;
+    uint64_t since = 0;
 #pragma unroll 1
-    for (; j < run_tiles; ++j) {
-      if (j % ahead == 0) look_up(j + lane / boxes);
-      const int stage = j % C::kStages, src = (j % ahead) * boxes;
-      if (j >= C::kStages && !(ok = warp_wait(smem_addr(&s_kempty[stage]), ((j / C::kStages) & 1) ^ 1u))) break;
-      // (the positions of the stage's last tile were read before its V was given back)
-      if (j >= C::kStages && !(ok = warp_wait(smem_addr(&s_vempty[stage]), ((j / C::kStages) & 1) ^ 1u))) break;
-      const bool turn = lane >= src && lane < src + boxes;
-      if (turn) s_pos[stage][lane - src] = pos;
-      __syncwarp();
-      if (turn) {
-        const uint32_t kbar = smem_addr(&s_kfull[stage]), vbar = smem_addr(&s_vfull[stage]);
-        const uint32_t dst = ring + stage * 2 * C::kHalf + (lane - src) * bytes;
-        fence_proxy_async_shared();  // what was written there by hand before the copy over it
-        if (row >= 0) {
-          mbar_arrive_expect_tx(kbar, bytes);
-          tma_load_2d_hint(dst, &map_k, kbar, head.u.kvh * D, row, pol);
-          mbar_arrive_expect_tx(vbar, bytes);
-          tma_load_2d_hint(dst + C::kHalf, &map_v, vbar, head.u.kvh * D, row, pol);
-        } else {
-          mbar_arrive(kbar);
-          mbar_arrive(vbar);
+    while (jv < run_tiles) {
+      bool moved = false;
+      if (jk < run_tiles && jk < jv + kPlaces / 2 &&
+          (jk < C::kStages || uniform(mbar_is_over(smem_addr(&s_kempty[jk % C::kStages]), ((jk / C::kStages) & 1) ^ 1u)))) {
+        if (jk % ahead == 0) look_up(jk + lane / boxes);
+        const int stage = jk % C::kStages, src = (jk % ahead) * boxes;
+        const bool turn = lane >= src && lane < src + boxes;
+        if (turn) {
+          s_pos[jk % kPlaces][lane - src] = pos;
+          s_row[jk % kPlaces][lane - src] = row;
+          const uint32_t bar = smem_addr(&s_kfull[stage]);
+          if (row >= 0) {
+            mbar_arrive_expect_tx(bar, bytes);
+            tma_load_2d_hint(ring + stage * 2 * C::kHalf + (lane - src) * bytes, &map_k, bar, khead.u.kvh * D, row, pol);
+          } else {
+            mbar_arrive(bar);
+          }
         }
+        if (++jk < run_tiles && ++khead.tile == khead.u.tiles) khead.next_unit(p);
+        __syncwarp();
+        moved = true;
       }
-      if (j + 1 < run_tiles && ++head.tile == head.u.tiles) head.next_unit(p);
+      if (jv < jk && (jv < C::kStages || uniform(mbar_is_over(smem_addr(&s_vempty[jv % C::kStages]), ((jv / C::kStages) & 1) ^ 1u)))) {
+        const int stage = jv % C::kStages;
+        if (lane < boxes) {
+          const int at_row = s_row[jv % kPlaces][lane];
+          const uint32_t bar = smem_addr(&s_vfull[stage]);
+          fence_proxy_async_shared();  // what was written there by hand before the copy over it
+          if (at_row >= 0) {
+            mbar_arrive_expect_tx(bar, bytes);
+            tma_load_2d_hint(ring + stage * 2 * C::kHalf + C::kHalf + lane * bytes, &map_v, bar, vhead.u.kvh * D, at_row, pol);
+          } else {
+            mbar_arrive(bar);
+          }
+        }
+        if (++jv < run_tiles && ++vhead.tile == vhead.u.tiles) vhead.next_unit(p);
+        moved = true;
+      }
+      // bounded like every wait: a product that never ends frees no place
+      if (moved) {
+        since = 0;
+      } else if (since == 0) {
+        since = global_timer_ns();
+      } else if (uniform(global_timer_ns() - since > W8A8_WAIT_NS)) {
+        if (lane == 0) atomicOr(&g_device_status, 1);
+        ok = false;
+        break;
+      }
     }
     // a wait gave up: the copies in flight land before shared memory is released
     if (!ok)
-      for (int i = max(0, j - C::kStages); i < j; ++i) {
-        mbar_wait(smem_addr(&s_kfull[i % C::kStages]), (i / C::kStages) & 1);
-        mbar_wait(smem_addr(&s_vfull[i % C::kStages]), (i / C::kStages) & 1);
+      for (int i = 0; i < C::kStages; ++i) {
+        if (jk > i) mbar_wait(smem_addr(&s_kfull[(jk - 1 - i) % C::kStages]), ((jk - 1 - i) / C::kStages) & 1);
+        if (jv > i) mbar_wait(smem_addr(&s_vfull[(jv - 1 - i) % C::kStages]), ((jv - 1 - i) / C::kStages) & 1);
       }
-  } else if (warp == kMmaWarp) {
-    // ================= MMAs: tile j belongs to group j % 2 of its unit's tiles
+  } else if (warp >= kMmaWarp && warp < kQueryWarp) {
+    // ================= MMAs, a warp for each group: every second tile of the run
+    const int group = warp - kMmaWarp;
     const uint32_t leader = elect_one();
     constexpr uint32_t kIdescS = make_idesc(kTile, C::kNS, 0);
-    constexpr uint32_t kIdescO = make_idesc(128, C::kNP, 0) | (1u << 15);  // V^T: M contiguous
+    // V^T and P^T: their tokens are the rows as they lie, M and N contiguous
+    constexpr uint32_t kIdescO = make_idesc(128, C::kNP, 0) | (1u << 15) | (1u << 16);
     const uint32_t tm = uniform(tmem);
-    const uint32_t ring = smem_addr(s_ring), pbuf = smem_addr(s_p), qbuf = smem_addr(s_q);
-    auto desc_k = [](uint32_t a) { return D == 128 ? smem_desc_sw128(a) : desc_sw64(a, 16); };
-    // heads of 64 fill half of M = 128; the other half reads what lies behind (the next
-    // 8 KB, always within the ring or the weights) and is not looked at
-    auto desc_v = [](uint32_t a) { return D == 128 ? smem_desc_mn_sw128(a, 16384) : desc_sw64(a, 8192); };
+    const uint32_t ring = smem_addr(s_ring), qbuf = smem_addr(s_q);
+    const uint32_t to_s = tm + group * C::kNS, to_o = tm + 2 * C::kNS + group * C::kNP;
+    const uint64_t dp = desc_rows<C::kNP>(smem_addr(s_p) + group * C::kP, 16);
+    // (heads of 64 fill half of M = 128; the other half reads what lies behind, the next
+    // 8 KB, always within the ring or the weights, and is not looked at)
+    constexpr uint32_t kNext = C::kHalf;
+    const uint32_t sfree = smem_addr(&s_sfree[group]), sfull = smem_addr(&s_sfull[group]);
+    const uint32_t pfull = smem_addr(&s_pfull[group]), pvdone = smem_addr(&s_pvdone[group]);
     const int all = uniform(run_tiles);
-    uint32_t scount[2] = {0u, 0u}, pcount[2] = {0u, 0u};
+    uint32_t scount = 0u, pcount = 0u;
     int done = 0, units = 0;
-    auto scores = [&](int tile, int group, int q) {
+    auto scores = [&](int tile, int q) {
       const int stage = tile % C::kStages;
-      if (scount[group] > 0) ok = ok && warp_wait(smem_addr(&s_sfree[group]), (scount[group] - 1) & 1);
-      ++scount[group];
+      if (scount > 0) ok = ok && warp_wait(sfree, (scount - 1) & 1);
+      ++scount;
       ok = ok && warp_wait(smem_addr(&s_kfull[stage]), (tile / C::kStages) & 1);
       if (!ok) return;
       tc_fence_after();
-      const uint64_t dk = desc_k(ring + stage * 2 * C::kHalf), dq = desc_k(qbuf + q * C::kQ);
+      const uint64_t dk = desc_rows<D>(ring + stage * 2 * C::kHalf, 16), dq = desc_rows<D>(qbuf + q * C::kQ, 16);
 #pragma unroll
-      for (int kk = 0; kk < D / 32; ++kk) mma_f8_by(leader, tm + group * C::kNS, dk + 2 * kk, dq + 2 * kk, kIdescS, kk > 0);
+      for (int kk = 0; kk < D / 32; ++kk) mma_f8_by(leader, to_s, dk + 2 * kk, dq + 2 * kk, kIdescS, kk > 0);
+      mma_commit_by(leader, sfull);
       mma_commit_by(leader, smem_addr(&s_kempty[stage]));
-      mma_commit_by(leader, smem_addr(&s_sfull[group]));
     };
 #pragma unroll 1
     while (done < all && ok) {
@@ -523,25 +597,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int q = units & 1;
       ok = warp_wait(smem_addr(&s_qfull[q]), (units / 2) & 1);
       tc_fence_after();
+      const int j0 = (done ^ group) & 1;
+      if (j0 < nt && ok) scores(done + j0, q);
 #pragma unroll 1
-      for (int j = 0; j < 2 && j < nt && ok; ++j) scores(done + j, j, q);
-#pragma unroll 1
-      for (int j = 0; j < nt && ok; ++j) {
-        const int group = j & 1, stage = (done + j) % C::kStages;
-        ok = warp_wait(smem_addr(&s_pfull[group]), pcount[group] & 1);
-        ++pcount[group];
+      for (int j = j0; j < nt && ok; j += 2) {
+        const int stage = (done + j) % C::kStages;
+        // the next scores as soon as the group has read these, if their keys are there;
+        // else after the product, which gives V's place in the ring back
+        bool more = j + 2 < nt;
+        if (more && uniform(mbar_is_over(smem_addr(&s_kfull[(done + j + 2) % C::kStages]), ((done + j + 2) / C::kStages) & 1))) {
+          scores(done + j + 2, q);
+          more = false;
+        }
         ok = ok && warp_wait(smem_addr(&s_vfull[stage]), ((done + j) / C::kStages) & 1);
+        ok = ok && warp_wait(pfull, pcount & 1);
+        ++pcount;
         if (!ok) break;
         tc_fence_after();
-        const uint64_t dv = desc_v(ring + stage * 2 * C::kHalf + C::kHalf);
-        const uint64_t dp = smem_desc_sw128(pbuf + group * C::kP);
+        const uint64_t dv = desc_rows<D>(ring + stage * 2 * C::kHalf + C::kHalf, kNext);
 #pragma unroll
         for (int kk = 0; kk < kTile / 32; ++kk)
-          mma_f8_by(leader, tm + 2 * C::kNS + group * C::kNP, dv + kk * ((32 * D) >> 4), dp + 2 * kk, kIdescO, kk > 0 || j >= 2);
+          mma_f8_by(leader, to_o, dv + kk * ((32 * D) >> 4), dp + kk * ((32 * C::kNP) >> 4), kIdescO, kk > 0 || j >= 2);
         mma_commit_by(leader, smem_addr(&s_vempty[stage]));
-        mma_commit_by(leader, smem_addr(&s_pvdone[group]));
-        if (j + 2 < nt) scores(done + j + 2, group, q);
+        mma_commit_by(leader, pvdone);
+        if (more) scores(done + j + 2, q);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&s_qempty[q]));
       done += nt;
       ++units;
       at.tile += nt;
@@ -559,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int buf = units & 1;
       if (units >= 2 && !(ok = warp_wait(smem_addr(&s_qempty[buf]), ((units / 2) & 1) ^ 1u))) break;
       uint8_t* const dst = s_q + buf * C::kQ;
-      constexpr int kBatch = 4;  // rows whose loads are in flight
+      constexpr int kBatch = 8;  // rows whose loads are in flight
 #pragma unroll 1
       for (int i0 = w; i0 < R; i0 += kBatch * kQueryWarps) {
         uint32_t raw[kBatch][kPer / 2];
@@ -616,9 +698,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int j = 0; j < C::kQParts; ++j) {
-            const int n = j * R + r, byte = kPer * lane;
-            const int swz = D == 128 ? (((byte >> 4) ^ (n & 7)) << 4) : (((byte >> 4) ^ ((n >> 1) & 3)) << 4);
-            uint8_t* to = dst + n * D + swz + (byte & 15);
+            const int byte = kPer * lane;
+            uint8_t* to = dst + chunk_at<D>(j * R + r, byte >> 4) + (byte & 15);
             if (D == 128) *reinterpret_cast<uint32_t*>(to) = code[j][0] | (code[j][kPer / 2 - 1] << 16);
             else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(code[j][0]);
           }
@@ -645,10 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int group = warp / 4, quarter = warp % 4, token = 32 * quarter + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter) << 21);
     const uint32_t s_cols = lanes + group * C::kNS, o_cols = lanes + 2 * C::kNS + group * C::kNP;
-    const uint32_t weights = smem_addr(s_p) + group * C::kP;
-    uint32_t swz[8];  // a token's byte in rows n of the weights, by n % 8
-#pragma unroll
-    for (int i = 0; i < 8; ++i) swz[i] = weights + i * 128 + (((token >> 4) ^ i) << 4) + (token & 15);
+    uint8_t* const weights = s_p + group * C::kP;  // a row of kNP bytes for each token
     float* const m = s_m[group];
     const float vscale = __ldg(p.v_scale);
     uint32_t count = 0u;  // tiles of this group
@@ -667,24 +745,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       group_sync(group);
       int mine = 0;
 #pragma unroll 1
-      for (int j = group; j < nt; j += 2) {
+      for (int j = (done ^ group) & 1; j < nt; j += 2) {
         const int stage = (done + j) % C::kStages;
         if (ok) ok = warp_wait(smem_addr(&s_sfull[group]), count & 1);
-        if (ok) ok = warp_wait(smem_addr(&s_kfull[stage]), ((done + j) / C::kStages) & 1);  // (long over: for s_pos)
+        // (for s_pos and the rows of V that are cleared; the keys' barrier may be phases
+        // ahead by now, V's waits for this tile's product)
+        if (ok) ok = warp_wait(smem_addr(&s_vfull[stage]), ((done + j) / C::kStages) & 1);
         tc_fence_after();
-        const int first = s_pos[stage][token / p.box], pos = first + token % p.box;
+        const int first = s_pos[(done + j) % kPlaces][token / p.box], pos = first + token % p.box;
         float s[R];
+        constexpr int kAtOnce = R < 16 ? R : 16;
 #pragma unroll
-        for (int r0 = 0; r0 < R; r0 += 8) {
-          uint32_t x[C::kQParts][8];
+        for (int r0 = 0; r0 < R; r0 += kAtOnce) {
+          uint32_t x[C::kQParts][kAtOnce / 8][8];
 #pragma unroll
-          for (int i = 0; i < C::kQParts; ++i) tmem_ld8(s_cols + i * R + r0, x[i]);
+          for (int i = 0; i < C::kQParts; ++i)
+#pragma unroll
+            for (int k = 0; k < kAtOnce / 8; ++k) tmem_ld8(s_cols + i * R + r0 + 8 * k, x[i][k]);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < C::kQParts; ++i) tmem_loaded(x[i]);
+          for (int i = 0; i < C::kQParts; ++i)
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            s[r0 + i] = fmaf(fmaf(__uint_as_float(x[2][i]), 0.0625f, __uint_as_float(x[1][i])), 0.0625f, __uint_as_float(x[0][i]));
+            for (int k = 0; k < kAtOnce / 8; ++k) tmem_loaded(x[i][k]);
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i)
+            s[r0 + i] = fmaf(fmaf(__uint_as_float(x[2][i / 8][i % 8]), 0.0625f, __uint_as_float(x[1][i / 8][i % 8])), 0.0625f,
+                             __uint_as_float(x[0][i / 8][i % 8]));
         }
         tc_fence_before();
         __syncwarp();
@@ -702,7 +788,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           // V's row must not reach the rows that do not see it as 0 times NaN
-          if (ok) ok = warp_wait(smem_addr(&s_vfull[stage]), ((done + j) / C::kStages) & 1);
           if (hidden && ok) {
             uint4* v = reinterpret_cast<uint4*>(s_ring + stage * 2 * C::kHalf + C::kHalf + token * D);
             if (pos > high) {
@@ -715,8 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint4 y = make_uint4(fp8_nan_to_zero(x.x), fp8_nan_to_zero(x.y), fp8_nan_to_zero(x.z), fp8_nan_to_zero(x.w));
                 if (x.x == y.x && x.y == y.y && x.z == y.z && x.w == y.w) continue;
                 v[i] = y;
-                // chunk i of the row holds dims 16 (i ^ swizzle) ..
-                const int chunk = D == 128 ? i ^ (token & 7) : i ^ ((token >> 1) & 3);
+                const int chunk = i ^ (D == 128 ? token & 7 : (token >> 1) & 3);  // of the row's dims
                 const uint32_t from[4] = {x.x, x.y, x.z, x.w};
                 for (int c = 0; c < 16; ++c)
                   if ((from[c / 4] >> (8 * (c % 4)) & 0x7Fu) == 0x7Fu) atomicMin(&s_nan[group][16 * chunk + c], pos);
@@ -725,78 +809,95 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // ---- the maximum, raised when a weight would pass 2^kHeadroom
-        bool past = false;
+        float past = -INFINITY;
 #pragma unroll
-        for (int r = 0; r < R; ++r) past = past || (s[r] - m[r]) * s_cs[buf][r] > kHeadroom;
-        if (group_any(group, past)) {
+        for (int r = 0; r < R; r += 4) {
+          const float4 m4 = *reinterpret_cast<const float4*>(m + r), c4 = *reinterpret_cast<const float4*>(&s_cs[buf][r]);
+          past = fmaxf(fmaxf(past, (s[r] - m4.x) * c4.x), (s[r + 1] - m4.y) * c4.y);
+          past = fmaxf(fmaxf(past, (s[r + 2] - m4.z) * c4.z), (s[r + 3] - m4.w) * c4.w);
+        }
+        if (group_any(group, past > kHeadroom)) {
+          float top = 0.f;
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            float x = s[r];
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-            if (lane == 0) s_red[group][quarter][r] = x;
+            const float x = warp_max(s[r]);
+            if (lane == r) top = x;
+          }
+          if (lane < R) s_red[group][quarter][lane] = top;
+          group_sync(group);
+          if (token < R) {
+            const float old = m[token];
+            const float now = fmaxf(old, fmaxf(fmaxf(s_red[group][0][token], s_red[group][1][token]),
+                                               fmaxf(s_red[group][2][token], s_red[group][3][token])));
+            s_alpha[group][token] = now > old ? ex2_fast((old - now) * s_cs[buf][token]) : 1.f;
+            m[token] = now;
           }
           group_sync(group);
           if (mine > 0) {
-            // the product before this one has to be in
+            // the product before this one has to be in; rows are rescaled by 8 where one is raised
             if (ok) ok = warp_wait(smem_addr(&s_pvdone[group]), (count - 1) & 1);
             tc_fence_after();
-          }
 #pragma unroll 1
-          for (int r0 = 0; r0 < R; r0 += 8) {
-            float alpha[8];
+            for (int r0 = 0; r0 < R; r0 += 8) {
+              float alpha[8], other = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = r0 + i;
-              const float top = fmaxf(fmaxf(s_red[group][0][r], s_red[group][1][r]), fmaxf(s_red[group][2][r], s_red[group][3][r]));
-              const float old = m[r], now = fmaxf(old, top);
-              alpha[i] = now > old ? ex2_fast((old - now) * s_cs[buf][r]) : 1.f;
-            }
-            if (mine > 0) {
-#pragma unroll 1
-              for (int part = 0; part < C::kPParts; ++part) {
-                uint32_t o[8];
-                tmem_ld8(o_cols + part * R + r0, o);
-                tmem_ld_wait();
-                tmem_loaded(o);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[i]);
-                tmem_st8(o_cols + part * R + r0, o);
+              for (int i = 0; i < 8; ++i) {
+                alpha[i] = s_alpha[group][r0 + i];
+                other += alpha[i];
               }
-              tmem_st_wait();
+              if (other == 8.f) continue;
+              uint32_t o[C::kPParts][8];
+#pragma unroll
+              for (int k = 0; k < C::kPParts; ++k) tmem_ld8(o_cols + k * R + r0, o[k]);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < C::kPParts; ++k) {
+                tmem_loaded(o[k]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[k][i] = __float_as_uint(__uint_as_float(o[k][i]) * alpha[i]);
+                tmem_st8(o_cols + k * R + r0, o[k]);
+              }
             }
+            tmem_st_wait();
           }
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const float top = fmaxf(fmaxf(s_red[group][0][r], s_red[group][1][r]), fmaxf(s_red[group][2][r], s_red[group][3][r]));
-            const float old = m[r], now = fmaxf(old, top);
-            if (now > old) l[r] *= ex2_fast((old - now) * s_cs[buf][r]);
-          }
-          group_sync(group);  // all have read the old maxima
-          if (token < R)
-            m[token] = fmaxf(m[token], fmaxf(fmaxf(s_red[group][0][token], s_red[group][1][token]),
-                                             fmaxf(s_red[group][2][token], s_red[group][3][token])));
-          group_sync(group);
+          for (int r = 0; r < R; ++r) l[r] *= s_alpha[group][r];
         }
         // ---- weights times 2^6, and their parts; the last product has read its own
         if (count > 0 && ok) ok = warp_wait(smem_addr(&s_pvdone[group]), (count - 1) & 1);
+        // (16 rows of a part, or 8 of two parts, are a 16-byte chunk)
+        constexpr int kRows = R < 16 ? R : 16, kWords = kRows / 4;
 #pragma unroll
-        for (int r = 0; r < R; r += 2) {
-          float a = ex2_fast(fmaf(s[r] - m[r], s_cs[buf][r], 8.f - kHeadroom));
-          float b = ex2_fast(fmaf(s[r + 1] - m[r + 1], s_cs[buf][r + 1], 8.f - kHeadroom));
-          if (edge) {
-            if (blind >> r & 1u) a = 0.f;
-            if (blind >> r & 2u) b = 0.f;
+        for (int r0 = 0; r0 < R; r0 += kRows) {
+          uint32_t code[C::kPParts][kWords];
+#pragma unroll
+          for (int r = 0; r < kRows; r += 2) {
+            const float2 m2 = *reinterpret_cast<const float2*>(m + r0 + r), c2 = *reinterpret_cast<const float2*>(&s_cs[buf][r0 + r]);
+            float w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              w[i] = ex2_fast(fmaf(s[r0 + r + i] - (i ? m2.y : m2.x), i ? c2.y : c2.x, 8.f - kHeadroom));
+              if (edge && (blind >> (r0 + r + i) & 1u)) w[i] = 0.f;
+              l[r0 + r + i] += w[i];
+            }
+            uint32_t part[C::kPParts];
+            parts_of(as_u32(__floats2half2_rn(w[0], w[1])), part);
+#pragma unroll
+            for (int i = 0; i < C::kPParts; ++i) {
+              if (r % 4 == 0) code[i][r / 4] = part[i];
+              else code[i][r / 4] = __byte_perm(code[i][r / 4], part[i], 0x5410);
+            }
           }
-          l[r] += a;
-          l[r + 1] += b;
-          uint32_t part[C::kPParts];
-          parts_of(as_u32(__floats2half2_rn(a, b)), part);
+          if constexpr (R == 8) {
 #pragma unroll
-          for (int i = 0; i < C::kPParts; ++i) {
-            const int n = i * R + r;
-            asm volatile("st.shared.u8 [%0], %1;" ::"r"(swz[n & 7] + (n & ~7) * 128), "r"(part[i]) : "memory");
-            asm volatile("st.shared.u8 [%0], %1;" ::"r"(swz[(n + 1) & 7] + ((n + 1) & ~7) * 128), "r"(part[i] >> 8) : "memory");
+            for (int i = 0; i < 2; ++i)
+              *reinterpret_cast<uint4*>(weights + chunk_at<C::kNP>(token, i)) =
+                  make_uint4(code[2 * i][0], code[2 * i][1], code[2 * i + 1][0], code[2 * i + 1][1]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < C::kPParts; ++i)
+              *reinterpret_cast<uint4*>(weights + chunk_at<C::kNP>(token, (i * R + r0) / 16)) =
+                  make_uint4(code[i][0], code[i][1], code[i][kWords - 2], code[i][kWords - 1]);
           }
         }
         fence_proxy_async_shared();
@@ -865,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         both_sync(3);
         float* part = nullptr;
         const long long unit = r0 + done - at.tile;
-        const bool begun = unit / share == blockIdx.x;
+        const bool begun = unit / share == nth;
         if (!whole) part = p.partial + (2 * static_cast<size_t>(blockIdx.x) + begun) * C::kPart;
 #pragma unroll 1
         for (int r0 = 0; r0 < R; r0 += 8) {
@@ -924,9 +1025,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (u.unit >= 0) {
       const long long c0 = u.unit / share, c1 = (u.unit + u.tiles - 1) / share;
       __threadfence();  // the CTA's stores, seen through the barrier, before the arrival
-      s_last[tid] = atomicAdd(p.counters + c0, 1u) == static_cast<unsigned>(c1 - c0);
+      s_last[tid] = atomicAdd(p.counters + c0 * p.side + place, 1u) == static_cast<unsigned>(c1 - c0);
       if (s_last[tid]) {
-        p.counters[c0] = 0u;
+        p.counters[c0 * p.side + place] = 0u;
         __threadfence();
       }
     }
@@ -940,18 +1041,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (SPARSE && u.b < 0) continue;
     const long long c0 = u.unit / share;
     const int parts = static_cast<int>((u.unit + u.tiles - 1) / share - c0) + 1;
-    // part 0 is the second place of CTA c0, part k the first of CTA c0 + k
-    const float* src = p.partial + 2 * static_cast<size_t>(c0) * C::kPart;
+    // part 0 is the second place of run c0's CTA, part k the first of run c0 + k's
+    const float* src = p.partial + 2 * (static_cast<size_t>(c0) * p.side + place) * C::kPart;
+    const size_t next = 2 * static_cast<size_t>(p.side) * C::kPart;
+    auto part_at = [&](int k) { return src + (k ? k * next : C::kPart); };
 #pragma unroll 1
     for (int item = tid; item < u.rows * (D / 4); item += kThreads) {
       const int r = item / (D / 4), d = 4 * (item % (D / 4));
       float mx = -INFINITY, sum = 0.f;
 #pragma unroll 8
-      for (int k = 0; k < parts; ++k) mx = fmaxf(mx, __ldcg(src + (k ? 2 * k : 1) * static_cast<size_t>(C::kPart) + R * D + r));
+      for (int k = 0; k < parts; ++k) mx = fmaxf(mx, __ldcg(part_at(k) + R * D + r));
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
       for (int k = 0; k < parts; ++k) {
-        const float* s = src + (k ? 2 * k : 1) * static_cast<size_t>(C::kPart);
+        const float* s = part_at(k);
         const float l = __ldcg(s + R * (D + 1) + r), mk = __ldcg(s + R * D + r);
         const float4 v = __ldcg(reinterpret_cast<const float4*>(s + r * D + d));
         if (l == 0.f) continue;
@@ -975,7 +1078,8 @@ cudaError_t launch_t(const Fp8AttnParams& p, const CUtensorMap& k, const CUtenso
   // the attribute is per function and device; setting it again is harmless
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<D, R>::kSmem);
   if (e != cudaSuccess) return e;
-  return fp8_launch(kern, dim3(static_cast<unsigned>(std::min(num_sms, kFp8MaxCtas))), dim3(kThreads), Few<D, R>::kSmem, stream, p, k, v);
+  const int ctas = std::min(num_sms, kFp8MaxCtas) / p.side * p.side;
+  return fp8_launch(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), Few<D, R>::kSmem, stream, p, k, v);
 }
 
 template <int D, bool SPARSE>
@@ -1002,8 +1106,14 @@ cudaError_t read_clear_fp8_rows_status(int* flags) {
   return e;
 }
 
-cudaError_t launch_fp8_rows(const Fp8AttnParams& p, int rows, const CUtensorMap& map_k, const CUtensorMap& map_v, int num_sms,
+cudaError_t launch_fp8_rows(const Fp8AttnParams& args, int rows, const CUtensorMap& map_k, const CUtensorMap& map_v, int num_sms,
                             cudaStream_t stream) {
+  Fp8AttnParams p = args;
+  // A token's KV heads lie side by side in the cache, head_dim bytes each: as many as fill
+  // 1 KB are read at the same time, by CTAs next to each other
+  p.side = 1;
+  for (int i = 2; i <= std::min(1024 / p.c.head_dim, num_sms); ++i)
+    if (!p.selected && p.c.num_kv_heads % i == 0) p.side = i;
   if (p.selected)
     return p.c.head_dim == 64 ? launch_r<64, true>(p, rows, map_k, map_v, num_sms, stream)
                               : launch_r<128, true>(p, rows, map_k, map_v, num_sms, stream);

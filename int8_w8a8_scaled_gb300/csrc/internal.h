@@ -310,6 +310,7 @@ struct Fp8AttnParams {
   int out_fp16, out_vec;
   int box;                // tokens of one copy: the largest power of two in block_size, at most 128
   // set by the launchers
+  int side;               // few rows: KV heads that CTAs next to each other take
   int few_rows;           // requests of more rows than this are not the few-rows kernel's
   unsigned* counters;     // parts of a cut unit that have arrived, left zero
   float* partial;         // [CTAs][2] partial results
