@@ -21,7 +21,7 @@
 // the time that HBM needs for it, and its softmax (128 tokens x R rows) less.
 //
 // One CTA to an SM, 12 warps: one copies tiles ahead into a ring, one prepares the
-// next unit's query, and two groups of four warps take the tiles in turn, each with
+// next unit's query (the first one's all softmax warps: by one warp it was 5 us), and two groups of four warps take the tiles in turn, each with
 // scores, weights and sums O of its own, joined at the unit's end, and each with a
 // warp that issues its MMAs (one for both spent 1300 cycles a tile on waits that
 // were over and on issuing, more than HBM's time for it).  A thread is a token: the weights of a token need nothing of
@@ -47,8 +47,9 @@ namespace {
 
 constexpr int kTile = 128;                    // tokens
 constexpr int kGroupThreads = 128;            // a softmax group
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kQueryWarp = 11, kQueryWarps = 1;
-constexpr int kThreads = 32 * (kQueryWarp + kQueryWarps);
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kQueryWarp = 11;
+constexpr int kThreads = 32 * (kQueryWarp + 1);
+constexpr int kQueryArrivals = 8;             // the first query is made by the softmax warps
 constexpr float kHeadroom = 2.f;
 constexpr float kNoScore = -1e25f;
 // Tiles whose places are kept: keys are fetched at most half as many tiles ahead of
@@ -177,6 +178,10 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) { retur
 
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
+__device__ __forceinline__ void mbar_arrive_many(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
 // Named barriers: 1 + g a group's own; 3 group 1's state is there, 4 it has been read.
 __device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroupThreads) : "memory"); }
 __device__ __forceinline__ bool group_any(int group, bool x) {
@@ -300,6 +305,95 @@ __device__ __forceinline__ void store1(const Fp8AttnParams& p, size_t at, float 
   else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
 }
 
+// The query of a unit as the scores' N operand, its rows' factors and limits: rows w,
+// w + warps, ... by this warp, a row at a time (a rolled loop: code that runs once is
+// paid for in instruction fetches).
+template <int D, int R, bool SPARSE>
+__device__ __forceinline__ void write_query(const Fp8AttnParams& p, const Unit& u, uint8_t* dst, float* cs, int* lim, int* limits,
+                                            int w, int warps) {
+  using C = Few<D, R>;
+  constexpr int kPer = D / 32;  // elements of a lane
+  const int lane = threadIdx.x % 32;
+  const float to_log2 = p.sm_scale * __ldg(p.k_scale) * kFp8Log2e;
+  auto load = [&](int r, uint32_t (&raw)[kPer / 2]) {
+#pragma unroll
+    for (int k = 0; k < kPer / 2; ++k) raw[k] = 0u;
+    if (r >= u.rows || u.b < 0) return;
+    const int row = u.row0 + r, token = SPARSE ? u.first : u.first + row / p.share;
+    const int head = u.kvh * p.share + (SPARSE ? row : row % p.share);
+    const uint16_t* src = static_cast<const uint16_t*>(p.q) + token * p.q_token_stride + head * p.q_head_stride + kPer * lane;
+    if (p.q_vec) {
+      if constexpr (D == 128) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+        raw[0] = x.x;
+        raw[kPer / 2 - 1] = x.y;
+      } else {
+        raw[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kPer / 2; ++k)
+        raw[k] = static_cast<uint32_t>(__ldg(src + 2 * k)) | (static_cast<uint32_t>(__ldg(src + 2 * k + 1)) << 16);
+    }
+  };
+  uint32_t next[kPer / 2];
+  load(w, next);
+#pragma unroll 1
+  for (int r = w; r < R; r += warps) {
+    uint32_t raw[kPer / 2];
+#pragma unroll
+    for (int k = 0; k < kPer / 2; ++k) raw[k] = next[k];
+    if (r + warps < R) load(r + warps, next);
+    float x[kPer], top = 0.f;
+    bool odd = false;
+#pragma unroll
+    for (int k = 0; k < kPer / 2; ++k) {
+      const float2 f = fp8_to_float2(raw[k], p.q_fp16);
+      x[2 * k] = f.x;
+      x[2 * k + 1] = f.y;
+      top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+      odd = odd || !(fabsf(f.x) < INFINITY) || !(fabsf(f.y) < INFINITY);
+    }
+    top = warp_max(top);
+    odd = __any_sync(0xffffffffu, odd);
+    // 2^e brings the largest element into [2^7, 2^8)
+    int e = 0;
+    if (top > 0.f && !odd) e = min(100, 7 + 127 - static_cast<int>(__float_as_uint(top) >> 23));
+    const float down = to_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    // the scale's sign goes to the query: the largest product is the largest score
+    const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), down);
+    if (lane == 0) {
+      // a row with a NaN or an infinity, or any row under a NaN scale, has NaN scores
+      cs[r] = odd || !(fabsf(down) <= INFINITY) ? __int_as_float(0x7fffffff) : fmaxf(fabsf(down), 1e-37f);
+      lim[r] = r < u.rows ? u.base + (SPARSE ? 0 : (u.row0 + r) / p.share) : -1;
+    }
+    uint32_t code[C::kQParts][kPer / 2];
+#pragma unroll
+    for (int k = 0; k < kPer / 2; ++k) {
+      uint32_t part[C::kQParts];
+      parts_of(as_u32(__floats2half2_rn(odd ? 0.f : x[2 * k] * up, odd ? 0.f : x[2 * k + 1] * up)), part);
+#pragma unroll
+      for (int j = 0; j < C::kQParts; ++j) code[j][k] = part[j];
+    }
+#pragma unroll
+    for (int j = 0; j < C::kQParts; ++j) {
+      const int byte = kPer * lane;
+      uint8_t* to = dst + chunk_at<D>(j * R + r, byte >> 4) + (byte & 15);
+      if (D == 128) *reinterpret_cast<uint32_t*>(to) = code[j][0] | (code[j][kPer / 2 - 1] << 16);
+      else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(code[j][0]);
+    }
+  }
+  // (columns past the last part are not looked at, but are finite)
+  for (int i = 32 * w + lane; i < (C::kNS - C::kQParts * R) * D / 4; i += 32 * warps)
+    reinterpret_cast<uint32_t*>(dst + C::kQParts * R * D)[i] = 0u;
+  if (w == 0 && lane == 0) {
+    limits[0] = u.base + (SPARSE ? 0 : u.row0 / p.share);
+    limits[1] = SPARSE ? limits[0] : u.base + (u.row0 + u.rows - 1) / p.share;
+  }
+  fence_proxy_async_shared();
+  __syncwarp();
+}
+
 template <int D, int R, bool SPARSE>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_rows_kernel(const Fp8AttnParams p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
@@ -336,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_addr(&s_vempty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_addr(&s_qfull[i]), kQueryWarps);
+      mbar_init(smem_addr(&s_qfull[i]), kQueryArrivals);
       mbar_init(smem_addr(&s_qempty[i]), 10);  // the softmax warps, and the MMA warps, so that none falls a phase behind
       mbar_init(smem_addr(&s_sfull[i]), 1);
       mbar_init(smem_addr(&s_sfree[i]), 4);
@@ -630,92 +724,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (done < all) at.next_unit(p);
     }
   } else if (warp >= kQueryWarp) {
-    // ================= queries: rows w, w + 2, ... of the next unit
-    const int w = warp - kQueryWarp;
-    constexpr int kPer = D / 32;  // elements of a lane
-    const float ks = __ldg(p.k_scale), to_log2 = p.sm_scale * ks * kFp8Log2e;
-    int done = 0, units = 0;
+    // ================= queries of the units after the first
+    int done = min(at.u.tiles - at.tile, run_tiles), units = 1;
+    at.tile += done;
+    if (done < run_tiles) at.next_unit(p);
 #pragma unroll 1
     while (done < run_tiles) {
-      const int nt = min(at.u.tiles - at.tile, run_tiles - done);
       const int buf = units & 1;
       if (units >= 2 && !(ok = warp_wait(smem_addr(&s_qempty[buf]), ((units / 2) & 1) ^ 1u))) break;
-      uint8_t* const dst = s_q + buf * C::kQ;
-      constexpr int kBatch = 8;  // rows whose loads are in flight
-#pragma unroll 1
-      for (int i0 = w; i0 < R; i0 += kBatch * kQueryWarps) {
-        uint32_t raw[kBatch][kPer / 2];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int r = i0 + i * kQueryWarps;
-          const bool real = r < at.u.rows && at.u.b >= 0;
-          const int row = at.u.row0 + r, token = SPARSE ? at.u.first : at.u.first + row / p.share;
-          const int headq = at.u.kvh * p.share + (SPARSE ? row : row % p.share);
-          const uint16_t* src = static_cast<const uint16_t*>(p.q) + token * p.q_token_stride + headq * p.q_head_stride + kPer * lane;
-#pragma unroll
-          for (int k = 0; k < kPer / 2; ++k) {
-            raw[i][k] = 0u;
-            if (real)
-              raw[i][k] = p.q_vec ? __ldg(reinterpret_cast<const uint32_t*>(src) + k)
-                                  : static_cast<uint32_t>(__ldg(src + 2 * k)) | (static_cast<uint32_t>(__ldg(src + 2 * k + 1)) << 16);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int r = i0 + i * kQueryWarps;
-          if (r >= R) break;
-          float x[kPer], top = 0.f;
-          bool odd = false;
-#pragma unroll
-          for (int k = 0; k < kPer / 2; ++k) {
-            const float2 f = fp8_to_float2(raw[i][k], p.q_fp16);
-            x[2 * k] = f.x;
-            x[2 * k + 1] = f.y;
-            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-            odd = odd || !(fabsf(f.x) < INFINITY) || !(fabsf(f.y) < INFINITY);
-          }
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-          odd = __any_sync(0xffffffffu, odd);
-          // 2^e brings the largest element into [2^7, 2^8)
-          int e = 0;
-          if (top > 0.f && !odd) e = min(100, 7 + 127 - static_cast<int>(__float_as_uint(top) >> 23));
-          const float down = to_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-          // the scale's sign goes to the query: the largest product is the largest score
-          const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), down);
-          if (lane == 0) {
-            // a row with a NaN or an infinity, or any row under a NaN scale, has NaN scores
-            s_cs[buf][r] = odd || !(fabsf(down) <= INFINITY) ? __int_as_float(0x7fffffff) : fmaxf(fabsf(down), 1e-37f);
-            s_lim[buf][r] = r < at.u.rows ? at.u.base + (SPARSE ? 0 : (at.u.row0 + r) / p.share) : -1;
-          }
-          uint32_t code[C::kQParts][kPer / 2];
-#pragma unroll
-          for (int k = 0; k < kPer / 2; ++k) {
-            uint32_t part[C::kQParts];
-            parts_of(as_u32(__floats2half2_rn(odd ? 0.f : x[2 * k] * up, odd ? 0.f : x[2 * k + 1] * up)), part);
-#pragma unroll
-            for (int j = 0; j < C::kQParts; ++j) code[j][k] = part[j];
-          }
-#pragma unroll
-          for (int j = 0; j < C::kQParts; ++j) {
-            const int byte = kPer * lane;
-            uint8_t* to = dst + chunk_at<D>(j * R + r, byte >> 4) + (byte & 15);
-            if (D == 128) *reinterpret_cast<uint32_t*>(to) = code[j][0] | (code[j][kPer / 2 - 1] << 16);
-            else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(code[j][0]);
-          }
-        }
-      }
-      // (columns past the last part are not looked at, but are finite)
-      for (int i = 32 * w + lane; i < (C::kNS - C::kQParts * R) * D / 4; i += 32 * kQueryWarps)
-        reinterpret_cast<uint32_t*>(dst + C::kQParts * R * D)[i] = 0u;
-      if (w == 0 && lane == 0) {
-        const int low = at.u.base + (SPARSE ? 0 : at.u.row0 / p.share);
-        s_limits[buf][0] = low;
-        s_limits[buf][1] = SPARSE ? low : at.u.base + (at.u.row0 + at.u.rows - 1) / p.share;
-      }
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&s_qfull[buf]));
+      write_query<D, R, SPARSE>(p, at.u, s_q + buf * C::kQ, s_cs[buf], s_lim[buf], s_limits[buf], 0, 1);
+      if (lane == 0) mbar_arrive_many(smem_addr(&s_qfull[buf]), kQueryArrivals);
+      const int nt = min(at.u.tiles - at.tile, run_tiles - done);
       done += nt;
       ++units;
       at.tile += nt;
@@ -731,6 +750,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float vscale = __ldg(p.v_scale);
     uint32_t count = 0u;  // tiles of this group
     int done = 0, units = 0;
+    // nothing to do yet: the first unit's query
+    write_query<D, R, SPARSE>(p, at.u, s_q, s_cs[0], s_lim[0], s_limits[0], warp, 8);
+    if (lane == 0) mbar_arrive(smem_addr(&s_qfull[0]));
 #pragma unroll 1
     while (done < run_tiles) {
       const int nt = min(at.u.tiles - at.tile, run_tiles - done);
