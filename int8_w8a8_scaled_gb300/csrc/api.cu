@@ -1371,7 +1371,7 @@ w8a8_status fp8_attention_call(const void* q, int q_dtype, int64_t num_q_heads, 
   p.out_fp16 = out_dtype == W8A8_FP16;
   p.out_vec = aligned(out, 16) && (out_token_stride | out_head_stride) % 8 == 0;
   p.box = 16;
-  while (p.box < 128 && c.block_size % (2 * p.box) == 0) p.box *= 2;
+  while (p.box < 64 && c.block_size % (2 * p.box) == 0) p.box *= 2;
   CUtensorMap map_k, map_v;
   const long long rows = static_cast<long long>(c.num_blocks) * c.block_size, row_bytes = static_cast<long long>(c.num_kv_heads) * d;
   if ((st = make_cache_map(&map_k, k_cache, rows, row_bytes, c.head_dim, p.box, selected != nullptr)) != W8A8_OK) return st;

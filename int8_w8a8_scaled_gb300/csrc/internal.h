@@ -308,7 +308,7 @@ struct Fp8AttnParams {
   void* out;              // as q
   long long out_token_stride, out_head_stride;
   int out_fp16, out_vec;
-  int box;                // tokens of one copy: the largest power of two in block_size, at most 128
+  int box;                // tokens of one copy: the largest power of two in block_size, at most 64
   // set by the launchers
   int side;               // few rows: KV heads that CTAs next to each other take
   int few_rows;           // requests of more rows than this are not the few-rows kernel's
@@ -324,6 +324,11 @@ size_t fp8_rows_workspace(int rows, int head_dim, int num_sms);
 cudaError_t launch_fp8_rows(const Fp8AttnParams& p, int rows, const CUtensorMap& map_k, const CUtensorMap& map_v, int num_sms,
                             cudaStream_t stream);
 cudaError_t read_clear_fp8_rows_status(int* flags);
+// Units of 256 rows of the requests that have more than p.few_rows (fp8_chunk.cu).
+size_t fp8_chunk_workspace(int head_dim, int num_sms);
+cudaError_t launch_fp8_chunk(const Fp8AttnParams& p, const CUtensorMap& map_k, const CUtensorMap& map_v, int num_sms,
+                             cudaStream_t stream);
+cudaError_t read_clear_fp8_chunk_status(int* flags);
 size_t fp8_paged_attention_workspace(int share, long long max_query_len, int head_dim, int num_sms);
 size_t fp8_sparse_attention_workspace(int share, int head_dim, int num_sms);
 cudaError_t launch_fp8_attention(const Fp8AttnParams& p, const CUtensorMap& map_k, const CUtensorMap& map_v, int num_sms,
