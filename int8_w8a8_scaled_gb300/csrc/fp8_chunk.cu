@@ -17,9 +17,8 @@
 // twice the rate, and as much more of it, with a longer softmax.)
 //
 // One CTA to an SM, 22 warps: two slots of 8 softmax warps, one that copies the codes
-// by TMA, 64 tokens of K or V at a time (shared memory holds no more beside the f16
-// tiles), four that write them as swizzled f16 tiles two deep, one that issues the
-// MMAs.  While one slot is at its softmax the tensor cores work for the other; the
+// by TMA, 64 tokens of K or V at a time, four that write them as swizzled f16 tiles,
+// one that issues the MMAs.  While one slot is at its softmax the tensor cores work for the other; the
 // MMA warp serves them strictly in turn, which keeps them out of step.  With more
 // than 128 rows the slots take 128 rows each of the same tokens; with fewer both
 // take the same rows, and the token tiles in turn, and their states are joined at
@@ -52,9 +51,11 @@ constexpr int kSlotThreads = kSoftmaxThreads / 2;
 constexpr int kDecodeThreads = 128;
 constexpr int kDecodeWarp = kSoftmaxThreads / 32, kMmaWarp = kDecodeWarp + kDecodeThreads / 32, kCopyWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kCopyWarp + 1);
-constexpr int kRaw = 3;                                // quarters (64 tokens of K or V) of codes in flight
+constexpr int kRaw = 7;                                // quarters (64 tokens of K or V) of codes in flight
 constexpr int kQuarter = kTileTokens / 2;
-constexpr int kStages = 2;
+// f16 tiles: one of K, free again when the scores are made, long before the next ones are
+// due; two of V.  The rest is for codes on their way.
+constexpr int kKStages = 1, kVStages = 2;
 constexpr int kPageTokens = 16, kRecords = kTileTokens / kPageTokens;  // tokens that surely share a block
 constexpr int kDead = 0x7fffffff;
 constexpr float kHeadroom = 2.f;
@@ -70,8 +71,8 @@ struct Big {
   static constexpr int kHalves = D / 64;                        // 128-byte column blocks of a row
   static constexpr int kBlockBytes = 128 * 128;                 // 128 rows x 128 bytes
   static constexpr int kTileBytes = kHalves * kBlockBytes;      // a Q, K or V tile
-  static constexpr int kQ = 0, kK = 2 * kTileBytes, kV = kK + kStages * kTileBytes;
-  static constexpr int kCodes = kV + kStages * kTileBytes, kCodeBytes = kQuarter * D;
+  static constexpr int kQ = 0, kK = 2 * kTileBytes, kV = kK + kKStages * kTileBytes;
+  static constexpr int kCodes = kV + kVStages * kTileBytes, kCodeBytes = kQuarter * D;
   static constexpr int kSmem = kCodes + kRaw * kCodeBytes + 1024;  // + alignment
   static constexpr int kPart = kUnitRows * (D + 2);             // floats: o [D / 4][256][4], m [256], l [256]
   static constexpr int kPieces = kQuarter * D / 16 / kDecodeThreads;  // 16-byte pieces of a quarter that a thread takes
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Big<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t s_kfull[kStages], s_kempty[kStages], s_vfull[kStages], s_vempty[kStages];
+  __shared__ uint64_t s_kfull[kKStages], s_kempty[kKStages], s_vfull[kVStages], s_vempty[kVStages];
   __shared__ uint64_t s_rfull[kRaw], s_rempty[kRaw];
   __shared__ uint8_t s_live[kRaw];  // which of a quarter's boxes lie in the cache
   __shared__ uint64_t s_qfull, s_sfull[2], s_pfull[2], s_pvdone[2];
@@ -209,10 +210,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kKStages; ++i) {
       mbar_init(smem_addr(&s_kfull[i]), kDecodeThreads / 32);
-      mbar_init(smem_addr(&s_vfull[i]), kDecodeThreads / 32);
       mbar_init(smem_addr(&s_kempty[i]), 1);
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(smem_addr(&s_vfull[i]), kDecodeThreads / 32);
       mbar_init(smem_addr(&s_vempty[i]), 1);
     }
     for (int i = 0; i < kRaw; ++i) {
@@ -305,67 +308,84 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kStride = kDecodeThreads / kPerRow;     // tokens between a thread's pieces
     const int piece = dt % kPerRow, token0 = dt / kPerRow;
     const uint32_t base = smem_addr(smem);
-    // the second block's lanes store their chunks in another order: the eight lanes of
-    // a store then meet eight different bank groups
+    // the second block's lanes take their 8-dim halves in another order: the eight lanes
+    // of a store then meet eight different bank groups
     const int turn = D == 128 && piece >= 4;
     const int box_shift = 31 - __clz(p.box);
-    int unit = 0;
+    const uint32_t all_live = (1u << (kQuarter / p.box)) - 1u;
+    // a thread's tokens are a multiple of 8 apart: one swizzle for all of them
+    static_assert(kStride % 8 == 0, "tokens of a thread share their swizzle");
+    const uint32_t from = C::kCodes + token0 * D + ((piece ^ (D == 128 ? token0 & 7 : (token0 >> 1) & 3)) << 4) + 8 * turn;
+    const uint32_t block = base + (D == 128 ? piece / 4 : 0) * C::kBlockBytes + token0 * 128;
+    const uint32_t to0 = block + ((((piece % 4) * 2 + turn) ^ (token0 & 7)) << 4), to1 = to0 ^ 16u;
+    int unit = 0, slot = -1, turns = 0;
+    // the last position that the unit's first row sees
+    auto first_sees = [&] { return at.rq.len - at.rq.all + at.rt * kUnitRows / p.share; };
+    int seen = first_sees();
     // quarter h of the run: tokens 64 (h % 2) .. of the keys, then the values, of tile h / 4
 #pragma unroll 1
     for (int h = 0; h < 4 * run_tiles; ++h) {
-      const int j = h / 4, w = h >> 1 & 1, part = h & 1, stage = j % kStages, slot = h % kRaw;
-      if (!(ok = warp_wait(smem_addr(&s_rfull[slot]), (h / kRaw) & 1))) break;
-      const uint8_t* codes = smem + C::kCodes + slot * C::kCodeBytes;
-      const uint32_t live = s_live[slot];
-      const int end = at.rq.len - at.tile * kTileTokens - part * kQuarter;
-      uint4 raw[C::kPieces];
+      const int j = h / 4, w = h >> 1 & 1, part = h & 1;
+      const int stages = w ? kVStages : kKStages, stage = j % stages;
+      if (++slot == kRaw) {
+        slot = 0;
+        ++turns;
+      }
+      if (!(ok = warp_wait(smem_addr(&s_rfull[slot]), turns & 1))) break;
+      const uint8_t* codes = smem + slot * C::kCodeBytes + from;
+      uint2 raw[C::kPieces][2];  // dims 16 piece + 8 turn .., and the other 8
 #pragma unroll
       for (int x = 0; x < C::kPieces; ++x) {
-        const int token = token0 + x * kStride;
-        raw[x] = *reinterpret_cast<const uint4*>(codes + token * D + ((piece ^ (D == 128 ? token & 7 : (token >> 1) & 3)) << 4));
-        // what is not a token of the request becomes zeros, whatever the cache holds there
-        if (token >= end || !(live >> (token >> box_shift) & 1u)) raw[x] = make_uint4(0u, 0u, 0u, 0u);
+        raw[x][0] = *reinterpret_cast<const uint2*>(codes + x * kStride * D);
+        raw[x][1] = *reinterpret_cast<const uint2*>(codes + x * kStride * D + (turn ? -8 : 8));
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&s_rempty[slot]));
-      if (j >= kStages && part == 0) ok = warp_wait(smem_addr(w ? &s_vempty[stage] : &s_kempty[stage]), ((j / kStages) & 1) ^ 1u);
-      if (!ok) break;
-      // tokens that the unit's first row does not see: NaN codes of V there go apart
-      const int low = at.rq.len - at.rq.all + at.rt * kUnitRows / p.share - at.tile * kTileTokens - part * kQuarter;
-      if (w && low < kQuarter - 1) {
+      const uint32_t live = s_live[slot];
+      const int end = at.rq.len - at.tile * kTileTokens - part * kQuarter;
+      if (end < kQuarter || live != all_live) {
         asm volatile("");  // a branch, for few tiles
+        // what is not a token of the request becomes zeros, whatever the cache holds there
 #pragma unroll
         for (int x = 0; x < C::kPieces; ++x) {
           const int token = token0 + x * kStride;
-          const uint4 was = raw[x];
-          if (token <= low) continue;
-          raw[x] = make_uint4(fp8_nan_to_zero(was.x), fp8_nan_to_zero(was.y), fp8_nan_to_zero(was.z), fp8_nan_to_zero(was.w));
-          if (raw[x].x == was.x && raw[x].y == was.y && raw[x].z == was.z && raw[x].w == was.w) continue;
-#pragma unroll 1
-          for (int c = 0; c < 16; ++c) {
-            const uint32_t word = c < 4 ? was.x : c < 8 ? was.y : c < 12 ? was.z : was.w;
-            if ((word >> (8 * (c % 4)) & 0x7Fu) != 0x7Fu) continue;
-            const int position = at.tile * kTileTokens + part * kQuarter + token;
-            atomicMin(&s_nan[unit & 3][0][16 * piece + c], position);
-            atomicMin(&s_nan[unit & 3][1][16 * piece + c], position);
-          }
+          if (token >= end || !(live >> (token >> box_shift) & 1u)) raw[x][0] = raw[x][1] = make_uint2(0u, 0u);
         }
       }
-      const uint32_t tile = base + (w ? C::kV : C::kK) + stage * C::kTileBytes + (D == 128 ? piece / 4 : 0) * C::kBlockBytes;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&s_rempty[slot]));
+      // tokens that the unit's first row does not see: NaN codes of V there go apart
+      const int low = seen - at.tile * kTileTokens - part * kQuarter;
+      if (w && low < kQuarter - 1) {
+        asm volatile("");
+#pragma unroll
+        for (int x = 0; x < C::kPieces; ++x)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int token = token0 + x * kStride;
+            const uint2 was = raw[x][i];
+            if (token <= low) continue;
+            raw[x][i] = make_uint2(fp8_nan_to_zero(was.x), fp8_nan_to_zero(was.y));
+            if (raw[x][i].x == was.x && raw[x][i].y == was.y) continue;
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              if (((c < 4 ? was.x : was.y) >> (8 * (c % 4)) & 0x7Fu) != 0x7Fu) continue;
+              const int dim = 16 * piece + 8 * (i ^ turn) + c, position = at.tile * kTileTokens + part * kQuarter + token;
+              atomicMin(&s_nan[unit & 3][0][dim], position);
+              atomicMin(&s_nan[unit & 3][1][dim], position);
+            }
+          }
+      }
+      if (j >= stages && part == 0) ok = warp_wait(smem_addr(w ? &s_vempty[stage] : &s_kempty[stage]), ((j / stages) & 1) ^ 1u);
+      if (!ok) break;
+      const uint32_t tile = (w ? C::kV : C::kK) + stage * C::kTileBytes + part * kQuarter * 128;
 #pragma unroll
       for (int x = 0; x < C::kPieces; ++x) {
-        const int token = part * kQuarter + token0 + x * kStride;
-        uint32_t v[8];
-        e4m3x4_to_f16x2x2(raw[x].x, v[0], v[1]);
-        e4m3x4_to_f16x2x2(raw[x].y, v[2], v[3]);
-        e4m3x4_to_f16x2x2(raw[x].z, v[4], v[5]);
-        e4m3x4_to_f16x2x2(raw[x].w, v[6], v[7]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int chunk = (piece % 4) * 2 + (i ^ turn);
-          st_shared_v4(tile + token * 128 + ((chunk ^ (token & 7)) << 4), turn == i ? v[0] : v[4], turn == i ? v[1] : v[5],
-                       turn == i ? v[2] : v[6], turn == i ? v[3] : v[7]);
-        }
+        uint32_t v[4];
+        e4m3x4_to_f16x2x2(raw[x][0].x, v[0], v[1]);
+        e4m3x4_to_f16x2x2(raw[x][0].y, v[2], v[3]);
+        st_shared_v4(to0 + tile + x * kStride * 128, v[0], v[1], v[2], v[3]);
+        e4m3x4_to_f16x2x2(raw[x][1].x, v[0], v[1]);
+        e4m3x4_to_f16x2x2(raw[x][1].y, v[2], v[3]);
+        st_shared_v4(to1 + tile + x * kStride * 128, v[0], v[1], v[2], v[3]);
       }
       if (part == 0) continue;
       fence_proxy_async_shared();  // the stores before the tensor cores' reads
@@ -373,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(smem_addr(w ? &s_vfull[stage] : &s_kfull[stage]));
       if (w && h + 1 < 4 * run_tiles && ++at.tile == at.tiles) {
         at.next_unit(p);
+        seen = first_sees();
         ++unit;
       }
     }
@@ -433,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t pcount[2] = {0u, 0u};  // weight tiles taken, each slot
     int done = 0, units = 0;
     auto scores = [&](int tile, int slot, int q) {
-      const int stage = tile % kStages;
+      const int stage = tile % kKStages;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (kk / 4) * (C::kBlockBytes >> 4) + 2 * (kk % 4);
@@ -443,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit_by(leader, smem_addr(&s_sfull[slot]));
     };
     auto wait_k = [&](int tile) {
-      if (ok) ok = warp_wait(smem_addr(&s_kfull[tile % kStages]), (tile / kStages) & 1);
+      if (ok) ok = warp_wait(smem_addr(&s_kfull[tile % kKStages]), (tile / kKStages) & 1);
       tc_fence_after();
     };
 #pragma unroll 1
@@ -464,13 +485,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
 #pragma unroll 1
         for (int slot = pair ? 0 : j; slot < (pair ? 2 : j + 1); ++slot) scores(done + j, slot, pair ? slot : 0);
-        mma_commit_by(leader, smem_addr(&s_kempty[(done + j) % kStages]));
+        mma_commit_by(leader, smem_addr(&s_kempty[(done + j) % kKStages]));
       }
 #pragma unroll 1
       for (int j = 0; j < nt && ok; ++j) {
-        const int stage = (done + j) % kStages;
+        const int stage = (done + j) % kVStages;
         const bool more = j + ahead < nt;
-        ok = warp_wait(smem_addr(&s_vfull[stage]), ((done + j) / kStages) & 1);
+        ok = warp_wait(smem_addr(&s_vfull[stage]), ((done + j) / kVStages) & 1);
 #pragma unroll 1
         for (int slot = pair ? 0 : j & 1, end = pair ? 2 : slot + 1; slot < end && ok; ++slot) {
           const uint32_t parity = (slot ? pcount[1] : pcount[0]) & 1u;
@@ -491,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         mma_commit_by(leader, smem_addr(&s_vempty[stage]));
-        if (more) mma_commit_by(leader, smem_addr(&s_kempty[(done + j + ahead) % kStages]));
+        if (more) mma_commit_by(leader, smem_addr(&s_kempty[(done + j + ahead) % kKStages]));
       }
       done += nt;
       ++units;
