@@ -136,7 +136,7 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
 
 // Tokens [token0, token0 + slab) of q; p.scores is theirs.
 template <int D>
-__global__ void __launch_bounds__(kScoreThreads) fp8_block_scores_kernel(const Fp8SelectArgs a, int token0) {
+__global__ void __launch_bounds__(kScoreThreads, 4) fp8_block_scores_kernel(const Fp8SelectArgs a, int token0) {
   constexpr int kStride = D + 16;   // bytes of a query row: 16-byte reads of 8 rows meet 8 bank groups
   constexpr int kSteps = D / 32;    // k-steps of an MMA
   constexpr int kPer = D / 4;       // dims of a lane
@@ -183,38 +183,51 @@ __global__ void __launch_bounds__(kScoreThreads) fp8_block_scores_kernel(const F
   for (int i = i0; i < i1; i += per_pass) {
     const int n = min(per_pass, i1 - i);
     __syncthreads();
-    // a warp quantises a row at a time, D / 32 values a lane, zeros for padding
+    // a warp quantises its rows, D / 32 values a lane, four rows' loads in flight; zeros for
+    // padding, up to a whole tile of 8
+    const int rows = (n * rows_of + 7) / 8 * 8;
+    constexpr int kAtOnce = 4;
 #pragma unroll 1
-    for (int row = warp; row < kRowTile; row += kScoreWarps) {
-      const int tok = row / rows_of, head = row % rows_of;
-      float f[kPer / 8];
+    for (int first = warp; first < rows; first += kAtOnce * kScoreWarps) {
+      uint32_t raw[kAtOnce][kPer / 16];
+      bool real[kAtOnce];
 #pragma unroll
-      for (int k = 0; k < kPer / 8; ++k) f[k] = 0.f;
-      if (tok < n && head < a.share) {
+      for (int x = 0; x < kAtOnce; ++x) {
+        const int row = first + x * kScoreWarps, tok = row / rows_of, head = row % rows_of;
+        real[x] = tok < n && head < a.share;
+#pragma unroll
+        for (int k = 0; k < kPer / 16; ++k) raw[x][k] = 0u;
+        if (!real[x]) continue;
         const uint16_t* src = static_cast<const uint16_t*>(a.q) + (r.first + i + tok) * a.q_token_stride +
                               (kvh * a.share + head) * a.q_head_stride + (kPer / 8) * lane;
 #pragma unroll
-        for (int k = 0; k < kPer / 8; k += 2) {
-          const uint32_t two = a.q_vec ? __ldg(reinterpret_cast<const uint32_t*>(src + k))
-                                       : static_cast<uint32_t>(__ldg(src + k)) | (static_cast<uint32_t>(__ldg(src + k + 1)) << 16);
-          const float2 v = fp8_to_float2(two, a.q_fp16);
-          f[k] = v.x, f[k + 1] = v.y;
-        }
+        for (int k = 0; k < kPer / 16; ++k)
+          raw[x][k] = a.q_vec ? __ldg(reinterpret_cast<const uint32_t*>(src) + k)
+                              : static_cast<uint32_t>(__ldg(src + 2 * k)) | (static_cast<uint32_t>(__ldg(src + 2 * k + 1)) << 16);
       }
-      float top = 0.f;
 #pragma unroll
-      for (int k = 0; k < kPer / 8; ++k) top = fmaxf(top, fabsf(f[k]));
+      for (int x = 0; x < kAtOnce; ++x) {
+        const int row = first + x * kScoreWarps;
+        if (row >= rows) break;
+        float f[kPer / 8], top = 0.f;
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-      const float scale = int8_scale(top);
+        for (int k = 0; k < kPer / 16; ++k) {
+          const float2 v = fp8_to_float2(raw[x][k], a.q_fp16);
+          f[2 * k] = v.x, f[2 * k + 1] = v.y;
+          top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+        }
 #pragma unroll
-      for (int k = 0; k < kPer / 8; ++k)
-        s_q[row * kStride + (kPer / 8) * lane + k] = static_cast<int8_t>(enc1<1>(__fdiv_rn(f[k], scale)));
-      // (a padded head's NaN never is a maximum)
-      if (lane == 0) s_scale[row] = tok < n && head < a.share ? scale : __int_as_float(0x7fffffff);
+        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const float scale = int8_scale(top);
+#pragma unroll
+        for (int k = 0; k < kPer / 8; ++k)
+          s_q[row * kStride + (kPer / 8) * lane + k] = static_cast<int8_t>(enc1<1>(__fdiv_rn(f[k], scale)));
+        // (a padded head's NaN never is a maximum)
+        if (lane == 0) s_scale[row] = real[x] ? scale : __int_as_float(0x7fffffff);
+      }
     }
     __syncthreads();
-    const int used = (n * rows_of + 7) / 8;
+    const int used = rows / 8;
     float best[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
 #pragma unroll 1
     for (int nt = 0; nt < used; ++nt) {
@@ -267,7 +280,6 @@ __global__ void __launch_bounds__(kScoreThreads) fp8_block_scores_kernel(const F
 
 // ------------------------------------------------------------------ selection
 
-constexpr int kPickThreads = 256, kPickWarps = kPickThreads / 32;
 constexpr int kBins = 2048;
 
 // Order-preserving: a larger score, a larger key; the lowest score has key 0x007fffff.
@@ -276,8 +288,10 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+template <int kPickThreads>
 __global__ void __launch_bounds__(kPickThreads) fp8_pick_blocks_kernel(const Fp8SelectArgs a, int token0) {
-  extern __shared__ uint32_t s_key[];  // [max_blocks]
+  constexpr int kPickWarps = kPickThreads / 32;
+  extern __shared__ __align__(16) uint32_t s_key[];  // [max_blocks]
   __shared__ int s_hist[kBins];
   __shared__ int s_found, s_warp[kPickWarps], s_warp2[kPickWarps], s_bin, s_above;
   fp8_let_dependents_start();
@@ -301,6 +315,7 @@ __global__ void __launch_bounds__(kPickThreads) fp8_pick_blocks_kernel(const Fp8
   // ---- the threshold: `want` keys are taken, those above `prefix` and the first
   // at it; bits below `shift` are not fixed yet
   int want = a.budget - a.first_blocks - a.last_blocks;
+  const bool none = want == 0;
   uint32_t prefix = 0u, mask = 0u;
 #pragma unroll 1
   for (int pass = 0; pass < 3 && want > 0; ++pass) {
@@ -346,8 +361,6 @@ __global__ void __launch_bounds__(kPickThreads) fp8_pick_blocks_kernel(const Fp8
     mask |= ((1u << bits) - 1u) << shift;
     __syncthreads();
   }
-  // (with nothing wanted no key lies above the mask-less threshold)
-  const bool none = a.budget - a.first_blocks - a.last_blocks == 0;
 
   // ---- columns in rising order: each warp has a stretch of them
   const int per = ((n + kPickWarps - 1) / kPickWarps + 31) / 32 * 32;
@@ -419,16 +432,21 @@ size_t fp8_select_workspace(long long tokens, long long num_kv_heads, long long 
 cudaError_t launch_fp8_select(const Fp8SelectArgs& args, cudaStream_t stream) {
   Fp8SelectArgs a = args;
   a.slab = slab_of(a.c.tokens, a.c.num_kv_heads, a.c.max_blocks);
-  const int smem = a.c.max_blocks * static_cast<int>(sizeof(uint32_t));
+  const int smem = (a.c.max_blocks + 3) / 4 * 4 * static_cast<int>(sizeof(uint32_t));
+  // more threads where there are many columns: 4096 of them (16 tokens, 8 heads) 12.8 us by 1024
+  // threads, 16.5 by 256; 300 (32 tokens, 8 heads) 9.0 by 256.  (Ranks in place of the
+  // threshold, every key against every other, were 15.8 there.)
+  const bool wide = a.c.max_blocks > 2048;
+  auto pick = wide ? fp8_pick_blocks_kernel<1024> : fp8_pick_blocks_kernel<256>;
   // one limit for every call, so that host threads with other sizes do not lower it
-  cudaError_t e = cudaFuncSetAttribute(fp8_pick_blocks_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(pick, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kMaxSelectBlocks * static_cast<int>(sizeof(uint32_t)));
   if (e != cudaSuccess) return e;
   for (long long t0 = 0; t0 < a.c.tokens; t0 += a.slab) {
     const int n = static_cast<int>(std::min<long long>(a.slab, a.c.tokens - t0));
     e = a.c.head_dim == 64 ? launch_scores<64>(a, static_cast<int>(t0), stream) : launch_scores<128>(a, static_cast<int>(t0), stream);
     if (e != cudaSuccess) return e;
-    e = fp8_launch(fp8_pick_blocks_kernel, dim3(n, a.c.num_kv_heads), dim3(kPickThreads), smem, stream, a, static_cast<int>(t0));
+    e = fp8_launch(pick, dim3(n, a.c.num_kv_heads), dim3(wide ? 1024 : 256), smem, stream, a, static_cast<int>(t0));
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -11,7 +11,7 @@
 // of 16 bytes; a CTA takes heads of one token, so that a thread meets the same
 // pairs in each of its heads and loads their angles once.  With few tokens the
 // heads of one go to several CTAs, a unit to a thread; with many a thread has
-// kBatch units' loads in flight.
+// kBatch units' loads in flight and the next token's position and slot.
 #include <algorithm>
 
 #include "fp8_paged.cuh"
@@ -88,44 +88,19 @@ __device__ __forceinline__ Head head_of(const Fp8WriteArgs& a, long long token, 
 
 // kBatch: units a thread loads before it works on them.
 template <int D, bool kInterleaved, int kBatch>
-__global__ void __launch_bounds__(kThreads) fp8_rotate_write_kernel(const Fp8WriteArgs a, int heads_per_cta) {
+__global__ void __launch_bounds__(kThreads, kBatch > 1 ? 5 : 1) fp8_rotate_write_kernel(const Fp8WriteArgs a, int heads_per_cta) {
   constexpr int kUnits = D / 16;              // of a head
   constexpr int kAtOnce = kThreads / kUnits;  // heads
   fp8_let_dependents_start();
   fp8_wait_for_predecessor();
-  const long long token = blockIdx.x;
   const int unit = threadIdx.x % kUnits, mine = threadIdx.x / kUnits;
   const int all = a.num_q_heads + 2 * a.num_kv_heads;
   const int first = blockIdx.y * heads_per_cta, end = min(all, first + heads_per_cta);
-  const long long slot = __ldg(a.slots + token);
 
   // the unit's elements: 8 at `lo` and 8 at `hi`
   const bool rotated = unit < a.rot_dim / 16;
   const int lo = kInterleaved || !rotated ? 16 * unit : 8 * unit;
   const int hi = kInterleaved || !rotated ? lo + 8 : a.rot_dim / 2 + lo;
-  // angles of its pairs, which are 8 * unit + 0..7 either way
-  float c[8], s[8];
-  if (rotated && first < a.num_q_heads + a.num_kv_heads) {
-    if (a.axes == 1) {
-      const int pos = __ldg(a.positions + token);
-      if (pos >= 0 && pos < a.max_position) {
-        const float* row = a.cos_sin + static_cast<long long>(pos) * a.rot_dim + 8 * unit;
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          const float4 x = __ldg(reinterpret_cast<const float4*>(row + i));
-          const float4 y = __ldg(reinterpret_cast<const float4*>(row + a.rot_dim / 2 + i));
-          c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
-          s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = s[i] = __int_as_float(0x7fffffff);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) angle_of(a, token, 8 * unit + i, c[i], s[i]);
-    }
-  }
   float scale[2], inv[2];
   bool fine[2];
 #pragma unroll
@@ -134,46 +109,82 @@ __global__ void __launch_bounds__(kThreads) fp8_rotate_write_kernel(const Fp8Wri
     fine[i] = recip_ok(scale[i], &inv[i]);
   }
 
+  // the token after this one has its position and slot looked up meanwhile: they stand in
+  // front of its angles and of where it goes
+  long long next_slot = __ldg(a.slots + blockIdx.x);
+  int next_pos = a.axes == 1 ? __ldg(a.positions + blockIdx.x) : 0;
 #pragma unroll 1
-  for (int h0 = first + mine; h0 < end; h0 += kBatch * kAtOnce) {
-    Head head[kBatch];
-    uint4 w[kBatch][2];
+  for (long long token = blockIdx.x; token < a.tokens; token += gridDim.x) {
+    const long long slot = next_slot;
+    const int this_pos = next_pos;
+    if (token + gridDim.x < a.tokens) {
+      next_slot = __ldg(a.slots + token + gridDim.x);
+      if (a.axes == 1) next_pos = __ldg(a.positions + token + gridDim.x);
+    }
+    // angles of its pairs, which are 8 * unit + 0..7 either way
+    float c[8], s[8];
+    if (rotated && first < a.num_q_heads + a.num_kv_heads) {
+      if (a.axes == 1) {
+        const int pos = this_pos;
+        if (pos >= 0 && pos < a.max_position) {
+          const float* row = a.cos_sin + static_cast<long long>(pos) * a.rot_dim + 8 * unit;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int h = h0 + i * kAtOnce;
-      head[i] = head_of(a, token, slot, h < end ? h : all);
-      if (head[i].kind != 3) {
-        w[i][0] = *reinterpret_cast<const uint4*>(head[i].src + lo);  // (q may be written in place)
-        w[i][1] = *reinterpret_cast<const uint4*>(head[i].src + hi);
+          for (int i = 0; i < 8; i += 4) {
+            const float4 x = __ldg(reinterpret_cast<const float4*>(row + i));
+            const float4 y = __ldg(reinterpret_cast<const float4*>(row + a.rot_dim / 2 + i));
+            c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
+            s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) c[i] = s[i] = __int_as_float(0x7fffffff);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) angle_of(a, token, 8 * unit + i, c[i], s[i]);
       }
     }
+#pragma unroll 1
+    for (int h0 = first + mine; h0 < end; h0 += kBatch * kAtOnce) {
+      Head head[kBatch];
+      uint4 w[kBatch][2];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (head[i].kind == 3) continue;
-      float x[16];
-      unpack16(w[i][0], w[i][1], a.fp16, x);
-      if (rotated && head[i].kind != 2) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (kInterleaved) turn(x[2 * j], x[2 * j + 1], c[j], s[j]);
-          else turn(x[j], x[8 + j], c[j], s[j]);
+      for (int i = 0; i < kBatch; ++i) {
+        const int h = h0 + i * kAtOnce;
+        head[i] = head_of(a, token, slot, h < end ? h : all);
+        if (head[i].kind != 3) {
+          w[i][0] = *reinterpret_cast<const uint4*>(head[i].src + lo);  // (q may be written in place)
+          w[i][1] = *reinterpret_cast<const uint4*>(head[i].src + hi);
         }
       }
-      if (head[i].kind == 0) {
-        uint32_t o[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = fp8_pack2(x[2 * j], x[2 * j + 1], a.fp16);
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(head[i].dst) + lo) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(head[i].dst) + hi) = make_uint4(o[4], o[5], o[6], o[7]);
-      } else {
-        const int v = head[i].kind - 1;
-        const uint4 q = v ? quant16<0>(x, scale[1], inv[1], fine[1], false) : quant16<0>(x, scale[0], inv[0], fine[0], false);
-        uint8_t* dst = static_cast<uint8_t*>(head[i].dst);
-        if (hi == lo + 8) {
-          *reinterpret_cast<uint4*>(dst + lo) = q;
+      for (int i = 0; i < kBatch; ++i) {
+        if (head[i].kind == 3) continue;
+        float x[16];
+        unpack16(w[i][0], w[i][1], a.fp16, x);
+        if (rotated && head[i].kind != 2) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (kInterleaved) turn(x[2 * j], x[2 * j + 1], c[j], s[j]);
+            else turn(x[j], x[8 + j], c[j], s[j]);
+          }
+        }
+        if (head[i].kind == 0) {
+          uint32_t o[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] = fp8_pack2(x[2 * j], x[2 * j + 1], a.fp16);
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(head[i].dst) + lo) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(head[i].dst) + hi) = make_uint4(o[4], o[5], o[6], o[7]);
         } else {
-          *reinterpret_cast<uint2*>(dst + lo) = make_uint2(q.x, q.y);
-          *reinterpret_cast<uint2*>(dst + hi) = make_uint2(q.z, q.w);
+          const int v = head[i].kind - 1;
+          const uint4 q = v ? quant16<0>(x, scale[1], inv[1], fine[1], false) : quant16<0>(x, scale[0], inv[0], fine[0], false);
+          uint8_t* dst = static_cast<uint8_t*>(head[i].dst);
+          if (hi == lo + 8) {
+            *reinterpret_cast<uint4*>(dst + lo) = q;
+          } else {
+            *reinterpret_cast<uint2*>(dst + lo) = make_uint2(q.x, q.y);
+            *reinterpret_cast<uint2*>(dst + hi) = make_uint2(q.z, q.w);
+          }
         }
       }
     }
@@ -224,7 +235,8 @@ cudaError_t launch_t(const Fp8WriteArgs& a, int num_sms, cudaStream_t stream) {
   // one unit to a thread while that leaves the CTAs below 16 an SM, all resident
   if (a.tokens * turns <= 16LL * num_sms)
     return fp8_launch(fp8_rotate_write_kernel<D, kInterleaved, 1>, dim3(tokens, turns), block, 0, stream, a, kAtOnce);
-  return fp8_launch(fp8_rotate_write_kernel<D, kInterleaved, 3>, dim3(tokens), block, 0, stream, a, all);
+  // a resident grid (5 CTAs of 96 registers an SM) goes over the tokens
+  return fp8_launch(fp8_rotate_write_kernel<D, kInterleaved, 3>, dim3(std::min(tokens, 5u * num_sms)), block, 0, stream, a, all);
 }
 
 }  // namespace
