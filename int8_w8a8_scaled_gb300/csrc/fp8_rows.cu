@@ -64,8 +64,8 @@ struct Few {
   static constexpr int kNS = (kQParts * R + 15) / 16 * 16;  // columns of the scores (M = 128: a multiple of 16)
   static constexpr int kNP = kPParts * R;                   // columns of the output
   static constexpr int kHalf = kTile * D;                   // K or V of a tile
-  static constexpr int kQ = kNS * D, kP = kNP * kTile, kDump = R * D * 4;
-  static constexpr int kFixed = 2 * kQ + 2 * kP + kDump + 1024;  // + alignment
+  static constexpr int kQ = kNS * D, kP = kNP * kTile, kDump = R * D * 4, kRawQ = R * D * 2;
+  static constexpr int kFixed = 2 * kQ + 2 * kP + kDump + kRawQ + 1024;  // + alignment
   static constexpr int kStatic = 8 * 1024;                  // room for the kernel's static shared memory
   static constexpr int kFit = static_cast<int>((kSmemMost - kStatic - kFixed) / (2 * kHalf));
   // even, and the groups take every second tile of the run, so that the tile before in a
@@ -306,44 +306,44 @@ __device__ __forceinline__ void store1(const Fp8AttnParams& p, size_t at, float 
 }
 
 // The query of a unit as the scores' N operand, its rows' factors and limits: rows w,
-// w + warps, ... by this warp, a row at a time (a rolled loop: code that runs once is
-// paid for in instruction fetches).
+// w + warps, ... by this warp, converted a row at a time (a rolled loop: code that
+// runs once is paid for in instruction fetches).
 template <int D, int R, bool SPARSE>
-__device__ __forceinline__ void write_query(const Fp8AttnParams& p, const Unit& u, uint8_t* dst, float* cs, int* lim, int* limits,
-                                            int w, int warps) {
+__device__ __forceinline__ void write_query(const Fp8AttnParams& p, const Unit& u, uint8_t* rows, uint8_t* dst, float* cs,
+                                            int* lim, int* limits, int w, int warps) {
   using C = Few<D, R>;
   constexpr int kPer = D / 32;  // elements of a lane
   const int lane = threadIdx.x % 32;
   const float to_log2 = p.sm_scale * __ldg(p.k_scale) * kFp8Log2e;
-  auto load = [&](int r, uint32_t (&raw)[kPer / 2]) {
+  // the rows as they are first, many loads in flight: with the cache streaming a load
+  // takes 2 us, and row after row a unit's query took longer than the unit
+  constexpr int kPerRow = D / 8, kBatch = 8;
+  const int pieces = (R - w + warps - 1) / warps * kPerRow;
+#pragma unroll 1
+  for (int i0 = lane; i0 < pieces; i0 += 32 * kBatch) {
+    uint4 x[kBatch];
 #pragma unroll
-    for (int k = 0; k < kPer / 2; ++k) raw[k] = 0u;
-    if (r >= u.rows || u.b < 0) return;
-    const int row = u.row0 + r, token = SPARSE ? u.first : u.first + row / p.share;
-    const int head = u.kvh * p.share + (SPARSE ? row : row % p.share);
-    const uint16_t* src = static_cast<const uint16_t*>(p.q) + token * p.q_token_stride + head * p.q_head_stride + kPer * lane;
-    if (p.q_vec) {
-      if constexpr (D == 128) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
-        raw[0] = x.x;
-        raw[kPer / 2 - 1] = x.y;
-      } else {
-        raw[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < kPer / 2; ++k)
-        raw[k] = static_cast<uint32_t>(__ldg(src + 2 * k)) | (static_cast<uint32_t>(__ldg(src + 2 * k + 1)) << 16);
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + 32 * k, r = w + i / kPerRow * warps;
+      x[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (i >= pieces || r >= u.rows || u.b < 0) continue;
+      const int row = u.row0 + r, token = SPARSE ? u.first : u.first + row / p.share;
+      const int head = u.kvh * p.share + (SPARSE ? row : row % p.share);
+      x[k] = fp8_load8(static_cast<const uint16_t*>(p.q) + token * p.q_token_stride + head * p.q_head_stride + 8 * (i % kPerRow),
+                       p.q_vec);
     }
-  };
-  uint32_t next[kPer / 2];
-  load(w, next);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + 32 * k, r = w + i / kPerRow * warps;
+      if (i < pieces) reinterpret_cast<uint4*>(rows)[r * kPerRow + i % kPerRow] = x[k];
+    }
+  }
+  __syncwarp();
 #pragma unroll 1
   for (int r = w; r < R; r += warps) {
     uint32_t raw[kPer / 2];
 #pragma unroll
-    for (int k = 0; k < kPer / 2; ++k) raw[k] = next[k];
-    if (r + warps < R) load(r + warps, next);
+    for (int k = 0; k < kPer / 2; ++k) raw[k] = reinterpret_cast<const uint32_t*>(rows)[(r * D + kPer * lane) / 2 + k];
     float x[kPer], top = 0.f;
     bool odd = false;
 #pragma unroll
@@ -404,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* const s_p = smem + C::kStages * 2 * C::kHalf;      // [group] weights
   uint8_t* const s_q = s_p + 2 * C::kP;                       // [2] queries
   float* const s_dump = reinterpret_cast<float*>(s_q + 2 * C::kQ);  // group 1's outputs [R][D]
+  uint8_t* const s_rows = reinterpret_cast<uint8_t*>(s_dump) + C::kDump;  // a query as it is given
   __shared__ uint64_t s_kfull[C::kStages], s_vfull[C::kStages], s_kempty[C::kStages], s_vempty[C::kStages];
   __shared__ uint64_t s_qfull[2], s_qempty[2], s_sfull[2], s_sfree[2], s_pfull[2], s_pvdone[2];
   __shared__ uint32_t s_tmem;
@@ -418,6 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ float s_red[2][4][R];             // [group][warp]
   __shared__ __align__(16) float s_alpha[2][R]; // [group] what a raised maximum makes of the sums so far
   __shared__ float s_state[2][2][R];           // [group] m in the log2 domain, l
+  __shared__ __align__(16) float s_factor[3][R];  // of a unit's outputs: each group's, the whole's
+  __shared__ __align__(16) long long s_to[R];  // where a unit's rows go, -1: nowhere
   __shared__ int s_nan[2][D];                  // [group] first token with a NaN in a dim
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int boxes = kTile / p.box;             // copies of a tile's K (or V)
@@ -732,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (done < run_tiles) {
       const int buf = units & 1;
       if (units >= 2 && !(ok = warp_wait(smem_addr(&s_qempty[buf]), ((units / 2) & 1) ^ 1u))) break;
-      write_query<D, R, SPARSE>(p, at.u, s_q + buf * C::kQ, s_cs[buf], s_lim[buf], s_limits[buf], 0, 1);
+      write_query<D, R, SPARSE>(p, at.u, s_rows, s_q + buf * C::kQ, s_cs[buf], s_lim[buf], s_limits[buf], 0, 1);
       if (lane == 0) mbar_arrive_many(smem_addr(&s_qfull[buf]), kQueryArrivals);
       const int nt = min(at.u.tiles - at.tile, run_tiles - done);
       done += nt;
@@ -751,7 +754,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t count = 0u;  // tiles of this group
     int done = 0, units = 0;
     // nothing to do yet: the first unit's query
-    write_query<D, R, SPARSE>(p, at.u, s_q, s_cs[0], s_lim[0], s_limits[0], warp, 8);
+    // (by way of the outputs' place: the query warp may be at the second unit's already)
+    write_query<D, R, SPARSE>(p, at.u, reinterpret_cast<uint8_t*>(s_dump), s_q, s_cs[0], s_lim[0], s_limits[0], warp, 8);
     if (lane == 0) mbar_arrive(smem_addr(&s_qfull[0]));
 #pragma unroll 1
     while (done < run_tiles) {
@@ -973,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (group == 1) {
 #pragma unroll 1
-        for (int r0 = 0; r0 < R; r0 += 8) {
+        for (int r0 = 0; r0 < R && r0 < at.u.rows; r0 += 8) {
           float y[8];
           output(r0, y);
           if (token < D) {
@@ -990,33 +994,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long unit = r0 + done - at.tile;
         const bool begun = unit / share == nth;
         if (!whole) part = p.partial + (2 * static_cast<size_t>(blockIdx.x) + begun) * C::kPart;
+        // a thread for each row: the groups' factors (negative: nothing seen, and what was never
+        // written stays out of the sum), and where the row goes
+        if (token < R) {
+          const float m0 = s_state[0][0][token], m1 = s_state[1][0][token], l0 = s_state[0][1][token], l1 = s_state[1][1][token];
+          const float mx = fmaxf(m0, m1);
+          const float a0 = l0 != 0.f ? ex2_fast(m0 - mx) : -1.f, a1 = l1 != 0.f ? ex2_fast(m1 - mx) : -1.f;
+          const float sum = (l0 != 0.f ? a0 * l0 : 0.f) + (l1 != 0.f ? a1 * l1 : 0.f);
+          s_factor[0][token] = a0;
+          s_factor[1][token] = a1;
+          if (whole) {
+            s_factor[2][token] = sum != 0.f ? vscale / sum : 0.f;
+            s_to[token] = token < at.u.rows && (!SPARSE || at.u.b >= 0)
+                              ? static_cast<long long>(out_at(p, SPARSE, at.u.first, at.u.kvh, at.u.row0 + token)) : -1;
+          } else {
+            __stcg(part + R * D + token, mx);
+            __stcg(part + R * (D + 1) + token, sum);
+          }
+        }
+        group_sync(0);
 #pragma unroll 1
-        for (int r0 = 0; r0 < R; r0 += 8) {
+        for (int r0 = 0; r0 < R && r0 < at.u.rows; r0 += 8) {
           float y[8];
           output(r0, y);
-          tc_fence_before();
+          if (token < D) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = r0 + i;
-            if (r >= at.u.rows || token >= D) continue;
-            const float m0 = s_state[0][0][r], m1 = s_state[1][0][r], l0 = s_state[0][1][r], l1 = s_state[1][1][r];
-            const float mx = fmaxf(m0, m1);
-            const float a0 = l0 != 0.f ? ex2_fast(m0 - mx) : 0.f, a1 = l1 != 0.f ? ex2_fast(m1 - mx) : 0.f;
-            // (a factor of 0 takes what was never written out of the sum)
-            float o = (l0 != 0.f ? a0 * y[i] : 0.f) + (l1 != 0.f ? a1 * s_dump[r * D + token] : 0.f);
-            const float sum = (l0 != 0.f ? a0 * l0 : 0.f) + (l1 != 0.f ? a1 * l1 : 0.f);
+            for (int i = 0; i < 8; ++i) {
+              const float a0 = s_factor[0][r0 + i], a1 = s_factor[1][r0 + i], other = s_dump[(r0 + i) * D + token];
+              y[i] = (a0 < 0.f ? 0.f : a0 * y[i]) + (a1 < 0.f ? 0.f : a1 * other);
+            }
             if (whole) {
-              if (!SPARSE || at.u.b >= 0)
-                store1(p, out_at(p, SPARSE, at.u.first, at.u.kvh, at.u.row0 + r) + token, sum != 0.f ? o * (vscale / sum) : 0.f);
-            } else {
-              __stcg(part + r * D + token, o);
-              if (token == 0) {
-                __stcg(part + R * D + r, mx);
-                __stcg(part + R * (D + 1) + r, sum);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const long long to = s_to[r0 + i];
+                if (to >= 0) store1(p, to + token, y[i] * s_factor[2][r0 + i]);
               }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) __stcg(part + (r0 + i) * D + token, y[i]);
             }
           }
         }
+        tc_fence_before();
         if (!whole && tid == 0) s_open[begun] = {at.u.b, at.u.first, at.u.rows, at.u.row0, at.u.kvh, unit, at.u.tiles};
         __syncwarp();
         both_arrive(4);
