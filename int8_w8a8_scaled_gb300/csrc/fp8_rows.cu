@@ -20,8 +20,9 @@
 // Bound by the cache's bytes, 2 D a token: the MMAs of a tile take about half of
 // the time that HBM needs for it, and its softmax (128 tokens x R rows) less.
 //
-// One CTA to an SM, 12 warps: one copies tiles ahead into a ring, one prepares the
-// next unit's query (the first one's all softmax warps: by one warp it was 5 us), and two groups of four warps take the tiles in turn, each with
+// One CTA to an SM, 12 warps: one copies tiles ahead into a ring, one prepares the next
+// unit's query (the first one's all softmax warps: by one warp it was 5 us) and with 8
+// rows takes over the copies of V, and two groups of four warps take the tiles in turn, each with
 // scores, weights and sums O of its own, joined at the unit's end, and each with a
 // warp that issues its MMAs (one for both spent 1300 cycles a tile on waits that
 // were over and on issuing, more than HBM's time for it).  A thread is a token: the weights of a token need nothing of
@@ -77,6 +78,10 @@ struct Few {
   static constexpr uint32_t kTmem = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static_assert(kCols <= 512, "scores and outputs of both groups fit TMEM");
   static constexpr int kPart = R * (D + 2);                 // floats: o [R][D], m [R], l [R]
+  // V by a warp of its own, the query's: one warp's copies do not keep up with HBM (64
+  // single tokens, 8 rows: 116 us for 126).  With more rows a tile's softmax takes longer
+  // than that, the query too, and V would wait for it (32 x 5 drafts: 97 us for 80)
+  static constexpr bool kSplit = R == 8;
 };
 
 __device__ __forceinline__ float ex2_fast(float x) {
@@ -174,7 +179,35 @@ __device__ __forceinline__ bool mbar_is_over(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Whether a phase is over, for every lane.
+__device__ __forceinline__ bool warp_over(uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_is_over(bar, parity)); }
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)); }
+
+// Whether a warp that polls several barriers may go on: bounded like every wait, from
+// the first look that found nothing.  The timer is read now and then.
+struct Patience {
+  uint64_t since = 0;
+  uint32_t looks = 0;
+  __device__ __forceinline__ void again() { looks = 0; }
+  __device__ __forceinline__ bool left() {
+    if (++looks & 255u) return true;
+    const uint64_t now = global_timer_ns();
+    if (looks == 256u) since = now;
+    if (!__any_sync(0xffffffffu, now - since > W8A8_WAIT_NS)) return true;
+    if (threadIdx.x % 32 == 0) atomicOr(&g_device_status, 1);
+    return false;
+  }
+};
+
+// A count that one warp raises and another follows.
+__device__ __forceinline__ void publish(int* to, int x) {
+  asm volatile("st.release.cta.shared.u32 [%0], %1;" ::"r"(smem_addr(to)), "r"(x) : "memory");
+}
+__device__ __forceinline__ int follow(const int* from) {
+  int x;
+  asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(x) : "r"(smem_addr(from)) : "memory");
+  return __shfl_sync(0xffffffffu, x, 0);
+}
 
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
@@ -411,6 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int s_pos[kPlaces][8], s_row[kPlaces][8];  // of a tile's boxes: positions of the first tokens, rows of the cache
   __shared__ long long s_scan[kThreads / 32], s_before;
   __shared__ int s_item, s_found, s_last[2];
+  __shared__ int s_jk, s_jv;                   // tiles whose K has been sent for, whose V has
   __shared__ Open s_open[2];
   __shared__ __align__(16) float s_cs[2][R];   // [query buffer] factor of each row's scores
   __shared__ __align__(16) int s_lim[2][R];    // last position that each row sees
@@ -443,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
   }
   if (tid < 2) s_open[tid].unit = -1;
+  if (tid == 0) s_jk = s_jv = 0;
   for (int i = tid; i < 2 * D; i += kThreads) (&s_nan[0][0])[i] = kDead;
   // TMEM only after the wait: a kernel in front may still need it.  Dependents start
   // only when it is taken: one that took it first and then waited for this kernel's
@@ -547,13 +582,40 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   bool ok = true;
 
+  const uint32_t bytes = static_cast<uint32_t>(p.box * D);  // of a copy
+  const uint64_t pol = policy_evict_first();
+  int jv = 0;  // the next tile whose V is to go out
+  // sends for V of tile jv of the run (`head`) if K's copies have gone out as far, and its
+  // place in the ring is free
+  auto copy_v = [&](Cursor<R, SPARSE>& head, int sent) -> bool {
+    const int stage = jv % C::kStages;
+    if (jv >= min(sent, run_tiles)) return false;
+    if (jv >= C::kStages && !warp_over(smem_addr(&s_vempty[stage]), ((jv / C::kStages) & 1) ^ 1u)) return false;
+    if (lane < boxes) {
+      const int row = s_row[jv % kPlaces][lane];
+      const uint32_t bar = smem_addr(&s_vfull[stage]);
+      fence_proxy_async_shared();  // what was written there by hand before the copy over it
+      if (row >= 0) {
+        mbar_arrive_expect_tx(bar, bytes);
+        tma_load_2d_hint(smem_addr(s_ring) + stage * 2 * C::kHalf + C::kHalf + lane * bytes, &map_v, bar, head.u.kvh * D, row, pol);
+      } else {
+        mbar_arrive(bar);
+      }
+    }
+    __syncwarp();
+    if (++jv < run_tiles && ++head.tile == head.u.tiles) head.next_unit(p);
+    return true;
+  };
+  // a wait gave up: the copies in flight land before shared memory is released
+  auto land = [&](uint64_t* full, int sent) {
+    for (int i = max(0, sent - C::kStages); i < sent; ++i) mbar_wait(smem_addr(&full[i % C::kStages]), (i / C::kStages) & 1);
+  };
+
   if (run_tiles == 0) {
     // nothing to do
   } else if (warp == kCopyWarp) {
-    // ================= copies: lane x has box x of the tile (K, then V)
+    // ================= copies: lane x has box x of the tile
     const uint32_t ring = smem_addr(s_ring);
-    const uint32_t bytes = static_cast<uint32_t>(p.box * D);
-    const uint64_t pol = policy_evict_first();
     // the place of this lane's box of a tile, a batch of tiles at once
     const int ahead = 32 / boxes;          // tiles of a batch
     Cursor<R, SPARSE> mine = at;           // the tile this lane looks up
@@ -598,19 +660,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // K and V each go out when their place in the ring is free: K's is long before V's
     Cursor<R, SPARSE> khead = at, vhead = at;  // their tiles: the KV heads
-    int jk = 0, jv = 0;
-    uint64_t since = 0;
+    int jk = 0;
+    Patience patience;
 #pragma unroll 1
-    while (jv < run_tiles) {
+    while (jk < run_tiles || (!C::kSplit && jv < run_tiles)) {
       bool moved = false;
-      if (jk < run_tiles && jk < jv + kPlaces / 2 &&
-          (jk < C::kStages || uniform(mbar_is_over(smem_addr(&s_kempty[jk % C::kStages]), ((jk / C::kStages) & 1) ^ 1u)))) {
+      if (jk < run_tiles && jk < (C::kSplit ? follow(&s_jv) : jv) + kPlaces / 2 &&
+          (jk < C::kStages || warp_over(smem_addr(&s_kempty[jk % C::kStages]), ((jk / C::kStages) & 1) ^ 1u))) {
         if (jk % ahead == 0) look_up(jk + lane / boxes);
         const int stage = jk % C::kStages, src = (jk % ahead) * boxes;
         const bool turn = lane >= src && lane < src + boxes;
         if (turn) {
           s_pos[jk % kPlaces][lane - src] = pos;
           s_row[jk % kPlaces][lane - src] = row;
+        }
+        __syncwarp();
+        if (C::kSplit && lane == 0) publish(&s_jk, jk + 1);
+        if (turn) {
           const uint32_t bar = smem_addr(&s_kfull[stage]);
           if (row >= 0) {
             mbar_arrive_expect_tx(bar, bytes);
@@ -620,42 +686,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (++jk < run_tiles && ++khead.tile == khead.u.tiles) khead.next_unit(p);
-        __syncwarp();
         moved = true;
       }
-      if (jv < jk && (jv < C::kStages || uniform(mbar_is_over(smem_addr(&s_vempty[jv % C::kStages]), ((jv / C::kStages) & 1) ^ 1u)))) {
-        const int stage = jv % C::kStages;
-        if (lane < boxes) {
-          const int at_row = s_row[jv % kPlaces][lane];
-          const uint32_t bar = smem_addr(&s_vfull[stage]);
-          fence_proxy_async_shared();  // what was written there by hand before the copy over it
-          if (at_row >= 0) {
-            mbar_arrive_expect_tx(bar, bytes);
-            tma_load_2d_hint(ring + stage * 2 * C::kHalf + C::kHalf + lane * bytes, &map_v, bar, vhead.u.kvh * D, at_row, pol);
-          } else {
-            mbar_arrive(bar);
-          }
-        }
-        if (++jv < run_tiles && ++vhead.tile == vhead.u.tiles) vhead.next_unit(p);
-        moved = true;
-      }
-      // bounded like every wait: a product that never ends frees no place
-      if (moved) {
-        since = 0;
-      } else if (since == 0) {
-        since = global_timer_ns();
-      } else if (uniform(global_timer_ns() - since > W8A8_WAIT_NS)) {
-        if (lane == 0) atomicOr(&g_device_status, 1);
-        ok = false;
-        break;
-      }
+      if (!C::kSplit) moved |= copy_v(vhead, jk);
+      if (moved) patience.again();
+      else if (!(ok = patience.left())) break;
     }
-    // a wait gave up: the copies in flight land before shared memory is released
-    if (!ok)
-      for (int i = 0; i < C::kStages; ++i) {
-        if (jk > i) mbar_wait(smem_addr(&s_kfull[(jk - 1 - i) % C::kStages]), ((jk - 1 - i) / C::kStages) & 1);
-        if (jv > i) mbar_wait(smem_addr(&s_vfull[(jv - 1 - i) % C::kStages]), ((jv - 1 - i) / C::kStages) & 1);
-      }
+    if (!ok) {
+      land(s_kfull, jk);
+      if (!C::kSplit) land(s_vfull, jv);
+    }
   } else if (warp >= kMmaWarp && warp < kQueryWarp) {
     // ================= MMAs, a warp for each group: every second tile of the run
     const int group = warp - kMmaWarp;
@@ -677,16 +717,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     int done = 0, units = 0;
     auto scores = [&](int tile, int q) {
       const int stage = tile % C::kStages;
-      if (scount > 0) ok = ok && warp_wait(sfree, (scount - 1) & 1);
-      ++scount;
-      ok = ok && warp_wait(smem_addr(&s_kfull[stage]), (tile / C::kStages) & 1);
-      if (!ok) return;
       tc_fence_after();
       const uint64_t dk = desc_rows<D>(ring + stage * 2 * C::kHalf, 16), dq = desc_rows<D>(qbuf + q * C::kQ, 16);
 #pragma unroll
       for (int kk = 0; kk < D / 32; ++kk) mma_f8_by(leader, to_s, dk + 2 * kk, dq + 2 * kk, kIdescS, kk > 0);
       mma_commit_by(leader, sfull);
       mma_commit_by(leader, smem_addr(&s_kempty[stage]));
+      ++scount;
     };
 #pragma unroll 1
     while (done < all && ok) {
@@ -695,29 +732,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = warp_wait(smem_addr(&s_qfull[q]), (units / 2) & 1);
       tc_fence_after();
       const int j0 = (done ^ group) & 1;
-      if (j0 < nt && ok) scores(done + j0, q);
+      if (j0 < nt && ok) {
+        if (scount > 0) ok = warp_wait(sfree, (scount - 1) & 1);
+        ok = ok && warp_wait(smem_addr(&s_kfull[(done + j0) % C::kStages]), ((done + j0) / C::kStages) & 1);
+        if (ok) scores(done + j0, q);
+      }
 #pragma unroll 1
       for (int j = j0; j < nt && ok; j += 2) {
-        const int stage = (done + j) % C::kStages;
-        // the next scores as soon as the group has read these, if their keys are there;
-        // else after the product, which gives V's place in the ring back
-        bool more = j + 2 < nt;
-        if (more && uniform(mbar_is_over(smem_addr(&s_kfull[(done + j + 2) % C::kStages]), ((done + j + 2) / C::kStages) & 1))) {
-          scores(done + j + 2, q);
-          more = false;
-        }
-        ok = ok && warp_wait(smem_addr(&s_vfull[stage]), ((done + j) / C::kStages) & 1);
-        ok = ok && warp_wait(pfull, pcount & 1);
-        ++pcount;
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t dv = desc_rows<D>(ring + stage * 2 * C::kHalf + C::kHalf, kNext);
+        // the product with these weights, and the next scores as soon as the group has read
+        // its own and their keys are there: whichever can go first
+        const int stage = (done + j) % C::kStages, next = done + j + 2;
+        bool product = true, more = j + 2 < nt;
+        if (more) ok = warp_wait(sfree, (scount - 1) & 1);
+        Patience patience;
+        while ((product || more) && ok) {
+          bool moved = false;
+          if (more && warp_over(smem_addr(&s_kfull[next % C::kStages]), (next / C::kStages) & 1)) {
+            scores(next, q);
+            more = false;
+            moved = true;
+          }
+          if (product && warp_over(pfull, pcount & 1) && warp_over(smem_addr(&s_vfull[stage]), ((done + j) / C::kStages) & 1)) {
+            tc_fence_after();
+            const uint64_t dv = desc_rows<D>(ring + stage * 2 * C::kHalf + C::kHalf, kNext);
 #pragma unroll
-        for (int kk = 0; kk < kTile / 32; ++kk)
-          mma_f8_by(leader, to_o, dv + kk * ((32 * D) >> 4), dp + kk * ((32 * C::kNP) >> 4), kIdescO, kk > 0 || j >= 2);
-        mma_commit_by(leader, smem_addr(&s_vempty[stage]));
-        mma_commit_by(leader, pvdone);
-        if (more) scores(done + j + 2, q);
+            for (int kk = 0; kk < kTile / 32; ++kk)
+              mma_f8_by(leader, to_o, dv + kk * ((32 * D) >> 4), dp + kk * ((32 * C::kNP) >> 4), kIdescO, kk > 0 || j >= 2);
+            mma_commit_by(leader, smem_addr(&s_vempty[stage]));
+            mma_commit_by(leader, pvdone);
+            ++pcount;
+            product = false;
+            moved = true;
+          }
+          if (moved) patience.again();
+          else ok = patience.left();
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&s_qempty[q]));
@@ -727,22 +776,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (done < all) at.next_unit(p);
     }
   } else if (warp >= kQueryWarp) {
-    // ================= queries of the units after the first
+    // ================= the queries of the units after the first (and copies of V)
+    Cursor<R, SPARSE> head = at;
     int done = min(at.u.tiles - at.tile, run_tiles), units = 1;
     at.tile += done;
     if (done < run_tiles) at.next_unit(p);
+    Patience patience;
 #pragma unroll 1
-    while (done < run_tiles) {
+    while (done < run_tiles || (C::kSplit && jv < run_tiles)) {
+      bool moved = false;
+      if (C::kSplit && copy_v(head, follow(&s_jk))) {
+        if (lane == 0) publish(&s_jv, jv);
+        moved = true;
+      }
       const int buf = units & 1;
-      if (units >= 2 && !(ok = warp_wait(smem_addr(&s_qempty[buf]), ((units / 2) & 1) ^ 1u))) break;
-      write_query<D, R, SPARSE>(p, at.u, s_rows, s_q + buf * C::kQ, s_cs[buf], s_lim[buf], s_limits[buf], 0, 1);
-      if (lane == 0) mbar_arrive_many(smem_addr(&s_qfull[buf]), kQueryArrivals);
-      const int nt = min(at.u.tiles - at.tile, run_tiles - done);
-      done += nt;
-      ++units;
-      at.tile += nt;
-      if (done < run_tiles) at.next_unit(p);
+      if (done < run_tiles && (units < 2 || warp_over(smem_addr(&s_qempty[buf]), ((units / 2) & 1) ^ 1u))) {
+        write_query<D, R, SPARSE>(p, at.u, s_rows, s_q + buf * C::kQ, s_cs[buf], s_lim[buf], s_limits[buf], 0, 1);
+        if (lane == 0) mbar_arrive_many(smem_addr(&s_qfull[buf]), kQueryArrivals);
+        const int nt = min(at.u.tiles - at.tile, run_tiles - done);
+        done += nt;
+        ++units;
+        at.tile += nt;
+        if (done < run_tiles) at.next_unit(p);
+        moved = true;
+      }
+      if (moved) patience.again();
+      else if (!(ok = patience.left())) break;
     }
+    if (C::kSplit && !ok) land(s_vfull, jv);
   } else {
     // ================= softmax: thread = token of the tile (in the outputs: dim)
     const int group = warp / 4, quarter = warp % 4, token = 32 * quarter + lane;
