@@ -1539,8 +1539,11 @@ w8a8_status w8a8_fp8_kv_block_means(const void* k_cache, int64_t num_blocks, int
 
 size_t w8a8_fp8_kv_select_blocks_workspace_size(int64_t tokens, int64_t num_kv_heads, int64_t max_blocks) {
   if (tokens < 1 || tokens >= (1LL << 31) || num_kv_heads < 1 || num_kv_heads > 65535 || max_blocks < 1 ||
-      max_blocks > w8a8::kMaxSelectBlocks)
+      max_blocks > w8a8::kMaxSelectBlocks) {
+    fail(W8A8_ERR_INVALID_ARG, "tokens, num_kv_heads or max_blocks out of range");
     return 0;
+  }
+  t_last_error.clear();
   return w8a8::fp8_select_workspace(tokens, num_kv_heads, max_blocks);
 }
 

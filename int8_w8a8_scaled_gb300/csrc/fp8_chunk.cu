@@ -25,7 +25,14 @@
 // the end.  Two threads share a softmax row, 64 tokens each.  The loops are kept
 // short: together they have to fit the instruction cache.
 //
-// MEASURED
+// Measured: 2048 new tokens after 30000, 32 query and 8 KV heads of 128: 1031 us, 1.00
+// PFLOP/s, 52 % of the 1.95 that a bf16 matrix product reaches.  A turn (256 rows, 128
+// tokens) takes about 4700 cycles where the MMAs need 2050: what bounds it is the four
+// warps that make f16 tiles (1100 cycles a quarter, most of it waiting for issue slots
+// beside 16 softmax warps) together with the chain of a slot, softmax (1500) - product
+// with V - next scores.  Before: codes loaded by the warps themselves 2052 us (spilled),
+// three quarters in flight 1328, masks and selects in every quarter 1124.  Two of the
+// four warps for K and two for V: 1098.
 //
 // A unit is one request, KV head and 256 rows; its work is the token tiles up to
 // the last one that its last row sees.  All units' tiles in a row are cut into

