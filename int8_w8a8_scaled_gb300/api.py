@@ -771,8 +771,9 @@ def fp8_kv_rotate_write(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor
     (they add up to rot_dim / 2); one outside cos_sin gives NaN.  k_cache,
     v_cache: [num_blocks, block_size, num_kv_heads, head_dim] float8_e4m3fn (or
     uint8 views).  slots: int64 [tokens] (block * block_size + offset; one
-    outside the cache is skipped).  k_scale, v_scale: float32 [1].  q_out:
-    rotated queries, as q; q itself is fine.  q and q_out may be None."""
+    outside the cache is skipped; no slot twice).  k_scale, v_scale: float32
+    [1].  q_out: rotated queries, as q; q itself is fine.  q and q_out may be
+    None."""
     nb, bs, h, d = _fp8_caches(k_cache, v_cache)
     if k.ndim != 3:
         raise ValueError("k and v must be [tokens, num_kv_heads, head_dim]")
