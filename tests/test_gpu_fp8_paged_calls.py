@@ -164,3 +164,50 @@ def test_steps_of_random_shapes(seed):
                      np.full(got.shape, -9, np.int32))
     assert np.array_equal(got.cpu().numpy(), want)
     assert w8.device_status() == 0
+
+
+def test_blocks_past_four_gigabytes():
+    """The same step over a small cache and over the last blocks of one of 4.6 GB each for K and V: the same bits."""
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("two caches of 4.6 GB")
+    hq, h, d, bs, tokens = 16, 8, 128, 64, 75
+    rng = np.random.default_rng(70)
+    lens, new = np.int32([700, 130]), np.int32([3, 72])
+    small, large = 16, 70000                                 # blocks of 64 KB
+    table = np.full((2, 11), -1, np.int32)
+    table[0], table[1, :3] = rng.permutation(small)[:11], [0, 0, 0]
+    table[1, :3] = np.setdiff1d(np.arange(small), table[0])[:3]
+    start = dev(np.int32([0, 3, 75]))
+    codes = [torch.from_numpy(fp.encode(np.float32(rng.standard_normal((small, bs, h, d)) * 20))).cuda() for _ in range(2)]
+    q, k, v = (torch.from_numpy(np.float32(rng.standard_normal((tokens, n, d)))).bfloat16().cuda() for n in (hq, h, h))
+    angle = rng.uniform(-3, 3, (700, d // 2))
+    cos_sin = dev(np.concatenate([np.cos(angle), np.sin(angle)], 1).astype(np.float32))
+    pos = np.concatenate([np.arange(n - m, n) for n, m in zip(lens, new)]).astype(np.int32)
+    row = np.repeat([0, 1], new)
+    g = torch.full((1,), 0.02, device="cuda")
+
+    def step(blocks):
+        first = blocks - small
+        caches = [torch.zeros(blocks, bs, h, d, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        for cache, part in zip(caches, codes):
+            cache[first:] = part
+        ids = np.where(table >= 0, table + first, -1).astype(np.int32)
+        slots = ids[row, pos // bs].astype(np.int64) * bs + pos % bs
+        means, scales = torch.zeros(blocks, h, d, dtype=torch.int8, device="cuda"), torch.zeros(blocks, h, device="cuda")
+        turned, whole, sparse = (torch.zeros_like(q) for _ in range(3))
+        few = torch.zeros_like(q[:3])
+        sel = torch.zeros(tokens, h, 5, dtype=torch.int32, device="cuda")
+        seq, ids = dev(lens), dev(ids)
+        w8.fp8_kv_rotate_write(q, k, v, cos_sin, dev(pos), *caches, dev(slots), g, g, turned)
+        kw = dict(query_start=start, max_query_len=72)
+        w8.fp8_kv_block_means(caches[0], seq, ids, means, scales, query_start=dev(np.int32([0, 700, 830])), max_query_len=700)
+        w8.fp8_kv_attention(turned, *caches, seq, ids, g, g, whole, **kw)
+        w8.fp8_kv_attention(turned[:3], *caches, seq[:1], ids[:1], g, g, few, query_start=start[:2], max_query_len=3)
+        w8.fp8_kv_select_blocks(turned, means, scales, seq, ids, bs, sel, **kw)
+        w8.fp8_kv_sparse_attention(turned, *caches, seq, ids, sel, g, g, sparse, **kw)
+        assert w8.device_status() == 0
+        return [c[first:].clone() for c in (*caches, means, scales)] + [turned, whole, few, sel, sparse]
+
+    for a, b in zip(step(small), step(large)):
+        assert a.abs().max() > 0 if a.is_floating_point() else (a != 0).any()
+        assert torch.equal(a, b)
