@@ -663,7 +663,9 @@ W8A8_API w8a8_status w8a8_fp8_kv_block_means(const void* k_cache, int64_t num_bl
  *   selected   int32 [tokens, num_kv_heads, budget]: columns of the block
  *              table in rising order, then -1.
  *   workspace  w8a8_fp8_kv_select_blocks_workspace_size() bytes, 16-byte
- *              aligned; holds nothing from one call to the next.
+ *              aligned; holds nothing from one call to the next, and is left
+ *              zero where it was written in its first 65536 bytes, so that other
+ *              calls' counters in the same memory stay zero.
  * first_blocks >= 0, last_blocks >= 1, their sum at most budget;
  * max_blocks <= 49152; num_q_heads / num_kv_heads at most 64. */
 W8A8_API size_t w8a8_fp8_kv_select_blocks_workspace_size(int64_t tokens, int64_t num_kv_heads, int64_t max_blocks);

@@ -920,7 +920,8 @@ def fp8_kv_select_blocks(q: torch.Tensor, means: torch.Tensor, mean_scales: torc
     num_kv_heads, budget], columns of the block table in rising order, then
     -1.  q, seq_lens, block_table, query_start and max_query_len: as for
     fp8_kv_attention; rows of no request are not written.  workspace: a
-    Workspace, or a uint8 tensor of fp8_kv_select_blocks_workspace_size()."""
+    Workspace (the one of the attention calls is fine), or a uint8 tensor of
+    fp8_kv_select_blocks_workspace_size()."""
     nb, hkv, d = _block_means(means, mean_scales)
     shape = q.shape
     if len(shape) != 3 or shape[2] != d:

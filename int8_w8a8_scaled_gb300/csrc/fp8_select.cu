@@ -24,7 +24,9 @@
 // memory, the budget's threshold found by three passes of 11, 11 and 10 bits
 // over histograms (a pass looks only at keys that agree so far), then the
 // columns above the threshold, and the lowest of those at it, written in rising
-// order by ballots.
+// order by ballots.  It leaves zeros where its scores lay in the workspace's first
+// kCounterRegion bytes: other operators keep their arrival counters there and
+// find them in the same workspace afterwards.
 //
 // Means and selection are latency, a chain of lengths, block ids, means and scores; so are
 // the scores of few tokens, and those of several wait for the int8 matrix instruction
@@ -311,13 +313,22 @@ __global__ void __launch_bounds__(kPickThreads) fp8_pick_blocks_kernel(const Fp8
   const int pos = r.len - r.all + token - r.first;
   int* out = a.selected + (static_cast<size_t>(token) * a.c.num_kv_heads + kvh) * a.budget;
   const int n = pos < 0 ? 0 : pos / a.c.block_size + 1;  // blocks up to its own
+  const size_t at_score = (static_cast<size_t>(token - token0) * a.c.num_kv_heads + kvh) * a.c.max_blocks;
+  // the scores of this row that lie where other calls have their counters, once they have been read
+  auto clear = [&] {
+    const size_t region = kCounterRegion / sizeof(float);
+    if (at_score >= region) return;
+    const int end = static_cast<int>(min(region - at_score, static_cast<size_t>(a.c.max_blocks)));
+    for (int c = tid; c < end; c += kPickThreads) a.scores[at_score + c] = 0.f;
+  };
   if (n <= a.budget) {
     for (int i = tid; i < a.budget; i += kPickThreads) out[i] = i < n ? i : -1;
+    clear();
     return;
   }
   const int lo = a.first_blocks, hi = n - a.last_blocks;  // columns [lo, hi) are chosen from
-  const float* src = a.scores + (static_cast<size_t>(token - token0) * a.c.num_kv_heads + kvh) * a.c.max_blocks;
-  for (int c = lo + tid; c < hi; c += kPickThreads) s_key[c] = key_of(__ldg(src + c));
+  const float* src = a.scores + at_score;
+  for (int c = lo + tid; c < hi; c += kPickThreads) s_key[c] = key_of(src[c]);
 
   // ---- the threshold: `want` keys are taken, those above `prefix` and the first
   // at it; bits below `shift` are not fixed yet
@@ -373,6 +384,7 @@ __global__ void __launch_bounds__(kPickThreads) fp8_pick_blocks_kernel(const Fp8
   const int per = ((n + kPickWarps - 1) / kPickWarps + 31) / 32 * 32;
   const int c0 = min(n, warp * per), c1 = min(n, c0 + per);
   __syncthreads();
+  clear();
   // 2: taken, 1: at the threshold, 0: not taken
   auto state = [&](int c) {
     if (c >= c1) return 0;

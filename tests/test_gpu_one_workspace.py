@@ -1,0 +1,52 @@
+"""One Workspace for the operators of a step, one after the other on a stream: the
+arrival counters at its head are zero after each call, and every result is that
+of a call with a workspace of its own."""
+import numpy as np
+import pytest
+import torch
+
+import int8_w8a8_scaled_gb300 as w8
+from oracle import fp8_paged as fp
+from test_gpu_fp8_paged import Step, dev, random_columns
+
+pytestmark = pytest.mark.gpu
+COUNTERS = 65536                                             # bytes at the head of a workspace
+
+
+def select_into(s, selected, workspace, budget_first=1, last=2):
+    rng = np.random.default_rng(7)
+    means, scales = rng.integers(-127, 128, (s.nb, s.h, s.d)).astype(np.int8), (rng.random((s.nb, s.h)) + 0.1).astype(np.float32)
+    w8.fp8_kv_select_blocks(s.q.cuda(), dev(means), dev(scales), dev(s.lens), dev(s.table), s.bs, selected, query_start=dev(s.start),
+                            max_query_len=s.most, first_blocks=budget_first, last_blocks=last, workspace=workspace)
+    return means, scales
+
+
+@pytest.mark.parametrize("lens,new,budget,columns", [
+    ([3000, 900, 1700], [3, 1, 2], 20, 0),                   # scores of a few rows
+    ([500, 40, 0, 16], [300, 5, 0, 1], 4, 0),                # most of the counters' bytes, and rows with fewer blocks than the budget
+    ([60, 40, 900], [60, 40, 300], 6, 40000),                # several slabs of rows of 160 KB
+])
+def test_a_selection_leaves_the_counters_zero(lens, new, budget, columns):
+    s = Step(81, lens, new, 8, 2, 128, 16, extra_rows=2)
+    if columns:
+        s.table = np.concatenate([s.table, np.full((len(lens), columns - s.table.shape[1]), -1, np.int32)], 1)
+    ws = w8.Workspace()
+    selected = torch.full((s.q.shape[0], 2, budget), -9, dtype=torch.int32, device="cuda")
+    means, scales = select_into(s, selected, ws)
+    want = fp.select(s.q.float().numpy(), means, scales, s.lens, s.table, 16, s.start, s.most, 1, 2, budget,
+                     np.full(selected.shape, -9, np.int32))
+    assert np.array_equal(selected.cpu().numpy(), want)
+    assert not ws.buf[:COUNTERS].any()
+
+
+@pytest.mark.parametrize("kind", ["few", "chunk", "sparse"])
+def test_a_selection_and_attention_share_a_workspace(kind):
+    """Attention of units that are cut between CTAs, which meet on the counters."""
+    s = Step(82, [3000, 900, 1700], [60, 1, 80] if kind == "chunk" else [3, 1, 2], 8, 2, 128, 16)
+    ws = w8.Workspace(64 << 20)
+    selected = torch.full((s.q.shape[0], 2, 30), -9, dtype=torch.int32, device="cuda")
+    select_into(s, selected, ws)
+    sel = random_columns(s, 40, s.rng) if kind == "sparse" else None
+    out = s.run(selected=sel, workspace=ws)
+    s.check(out, selected=sel)
+    assert torch.equal(out, s.run(selected=sel))
