@@ -41,7 +41,7 @@ cudaError_t launch_fp8_attention(const Fp8AttnParams& args, const CUtensorMap& m
                                  void* workspace, cudaStream_t stream) {
   Fp8AttnParams p = args;
   p.counters = static_cast<unsigned*>(workspace);
-  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kFp8CounterBytes);
+  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterRegion);
   p.few_rows = kFewRows;
   const long long rows = p.selected ? std::min(p.share, kFewRows) : static_cast<long long>(p.share) * p.c.max_query_len;
   if (rows <= kFewRows) return launch_fp8_rows(p, static_cast<int>(rows), map_k, map_v, num_sms, stream);

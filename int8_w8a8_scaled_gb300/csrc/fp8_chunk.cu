@@ -930,7 +930,7 @@ cudaError_t launch_t(const Fp8AttnParams& p, const CUtensorMap& k, const CUtenso
 }  // namespace
 
 size_t fp8_chunk_workspace(int head_dim, int num_sms) {
-  return kFp8CounterBytes + static_cast<size_t>(std::min(num_sms, kFp8MaxCtas)) * 2 * kUnitRows * (head_dim + 2) * sizeof(float);
+  return kCounterRegion + static_cast<size_t>(std::min(num_sms, kFp8MaxCtas)) * 2 * kUnitRows * (head_dim + 2) * sizeof(float);
 }
 
 cudaError_t read_clear_fp8_chunk_status(int* flags) {

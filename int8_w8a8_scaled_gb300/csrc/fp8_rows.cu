@@ -1208,7 +1208,7 @@ cudaError_t launch_r(const Fp8AttnParams& p, int rows, const CUtensorMap& k, con
 
 size_t fp8_rows_workspace(int rows, int head_dim, int num_sms) {
   const int r = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-  return kFp8CounterBytes + static_cast<size_t>(std::min(num_sms, kFp8MaxCtas)) * 2 * r * (head_dim + 2) * sizeof(float);
+  return kCounterRegion + static_cast<size_t>(std::min(num_sms, kFp8MaxCtas)) * 2 * r * (head_dim + 2) * sizeof(float);
 }
 
 cudaError_t read_clear_fp8_rows_status(int* flags) {

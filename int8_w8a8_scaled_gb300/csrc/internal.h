@@ -10,6 +10,12 @@
 
 namespace w8a8 {
 
+// Arrival counters: a fixed region at the head of a workspace (a matmul has one 32-bit
+// counter per output tile, attention one per CTA), left zero by every call that uses it.
+// Scratch data lives after the region, so that one workspace serves calls of any operator.
+constexpr size_t kCounterSlots = 16384;
+constexpr size_t kCounterRegion = kCounterSlots * sizeof(unsigned);
+
 // Parameters of one scaled-matmul launch.  "P" is the operand on the
 // 128-row MMA side, "Q" the operand on the narrow (block_n) side.  Without
 // swap P = activations [M, K] and Q = weights [N, K]; with swap the roles
@@ -315,8 +321,7 @@ struct Fp8AttnParams {
   unsigned* counters;     // parts of a cut unit that have arrived, left zero
   float* partial;         // [CTAs][2] partial results
 };
-constexpr int kFp8MaxCtas = 1024;
-constexpr size_t kFp8CounterBytes = kFp8MaxCtas * sizeof(unsigned);
+constexpr int kFp8MaxCtas = 1024;  // a counter each: fewer than kCounterSlots
 // Units of at most 32 rows (fp8_rows.cu; `rows`: the most of a request, or a
 // token's heads).  The maps: caches as [rows, num_kv_heads * head_dim] bytes, a
 // box of `box` rows and head_dim bytes, swizzled over a row of the box.
@@ -386,12 +391,6 @@ cudaError_t launch_dequant(const DequantArgs& a, int num_sms, cudaStream_t strea
 
 // Sets the message returned by w8a8_last_error() on this host thread.
 void set_last_error(const char* msg);
-
-// Split-K arrival counters: a fixed region at the head of every matmul
-// workspace (one 32-bit counter per output tile), left zero by every call
-// that uses it.  Scratch data always lives after the region.
-constexpr size_t kCounterSlots = 16384;
-constexpr size_t kCounterRegion = kCounterSlots * sizeof(unsigned);
 
 // Bytes at the head of the workspace whose counters this matmul uses under
 // `cfg` (complete: no automatic fields) on the current device, 0 when it

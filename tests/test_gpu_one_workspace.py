@@ -50,3 +50,12 @@ def test_a_selection_and_attention_share_a_workspace(kind):
     out = s.run(selected=sel, workspace=ws)
     s.check(out, selected=sel)
     assert torch.equal(out, s.run(selected=sel))
+
+
+@pytest.mark.parametrize("kind", ["few", "chunk", "sparse"])
+def test_attention_leaves_the_matmuls_counters_zero(kind):
+    s = Step(83, [3000, 900, 1700], [60, 1, 80] if kind == "chunk" else [3, 1, 2], 8, 2, 128, 16)
+    ws = w8.Workspace(64 << 20)
+    sel = random_columns(s, 40, s.rng) if kind == "sparse" else None
+    s.check(s.run(selected=sel, workspace=ws), selected=sel)
+    assert not ws.buf[:COUNTERS].any()
