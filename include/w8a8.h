@@ -367,7 +367,9 @@ W8A8_API w8a8_status w8a8_requant_shards(const void* q, int q_dtype, int64_t col
  * size is an upper bound on purpose: it assumes chunks of 64 tokens, the
  * smallest the kernel picks, so one size serves every call with the same
  * batch, heads and max_seq_len whatever the GPU (the kernel takes chunks of
- * up to 512 tokens, and then uses an eighth of it).  No
+ * up to 512 tokens, and then uses an eighth of it).  What a call writes into
+ * the workspace's first 65536 bytes it leaves zero again, for the counters that
+ * other calls keep there.  No
  * allocation, no synchronisation; graph-capturable.  Errors: INVALID_ARG
  * (null pointer, sizes, head_dim, G), MISALIGNED (cache base not 16-byte
  * aligned), WORKSPACE (too small), CUDA (launch).  The workspace size is

@@ -677,6 +677,15 @@ __global__ void __launch_bounds__(kHeadDim) fp8kv_attn_combine_kernel(const Attn
       }
     }
     y = l > 0.f ? (o / l) * __ldg(p.v_scale) : 0.f;
+    // Zeros again where the partial results lay over other operators' counters, which are
+    // found in the same workspace afterwards (chunks behind the sequence's end wrote nothing).
+    constexpr size_t kRegion = kCounterRegion / sizeof(float);
+    const size_t first = static_cast<size_t>(part - p.partial);
+    if (first < kRegion) {
+      __syncthreads();  // they have been read
+      const size_t end = min(kRegion - first, static_cast<size_t>(used) * kPartStride);
+      for (size_t i = d; i < end; i += kHeadDim) p.partial[first + i] = 0.f;
+    }
   }
   if (p.out_fp16)
     static_cast<__half*>(p.out)[oi] = __float2half_rn(y);

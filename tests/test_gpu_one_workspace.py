@@ -59,3 +59,22 @@ def test_attention_leaves_the_matmuls_counters_zero(kind):
     sel = random_columns(s, 40, s.rng) if kind == "sparse" else None
     s.check(s.run(selected=sel, workspace=ws), selected=sel)
     assert not ws.buf[:COUNTERS].any()
+
+
+@pytest.mark.parametrize("batch,tokens,paged", [(1, 5000, False), (4, 700, True), (3, 1, False)])
+def test_decode_attention_leaves_the_counters_zero(batch, tokens, paged):
+    gen = torch.Generator(device="cuda").manual_seed(85)
+    hq, h, bs = 8, 2, 16
+    nb = -(-tokens // bs) * batch
+    shape = (nb, bs, h, 128) if paged else (batch, tokens, h, 128)
+    k, v = (torch.randint(0, 126, shape, generator=gen, device="cuda", dtype=torch.uint8) for _ in range(2))
+    table = torch.arange(nb, dtype=torch.int32, device="cuda").view(batch, -1) if paged else None
+    q = torch.randn(batch, hq, 128, generator=gen, device="cuda").bfloat16()
+    lens = torch.tensor([tokens, tokens // 2, 0, 1][:batch], dtype=torch.int32, device="cuda")
+    one = torch.full((1,), 0.02, device="cuda")
+    ws = w8.Workspace(64 << 20)
+    outs = [torch.empty_like(q) for _ in range(2)]
+    for out, workspace in zip(outs, (ws, None)):
+        w8.fp8_kv_decode_attention(q, k, v, lens, one, one, out, block_table=table, workspace=workspace)
+    assert not ws.buf[:COUNTERS].any()
+    assert torch.equal(*outs)
