@@ -178,10 +178,12 @@ W8A8_API w8a8_status w8a8_scaled_dequant(const void* q, int q_dtype, int64_t row
  *           first 64 KiB hold split-K arrival counters that must be
  *           zero-filled before the first use; every call leaves them zero
  *           again and writes its other scratch (split-K partials, the K
- *           halves of CTA-pair tiles, int8 f16 planes) only after them, so one zero-filled buffer serves any sequence of
- *           scaled_mm calls of any shape on one stream.  Use it for nothing
- *           else, and give calls that may overlap on the GPU separate
- *           workspaces.
+ *           halves of CTA-pair tiles, int8 f16 planes) only after them, so
+ *           one zero-filled buffer serves any sequence of scaled_mm calls of
+ *           any shape on one stream, and the attention and selection calls
+ *           between them, which keep to the same rule.  Use it for nothing
+ *           else (the quantiser's is its own), and give calls that may overlap
+ *           on the GPU separate workspaces.
  *  Alignment (the CUTLASS page's "misaligned address" crash turned into a
  *  status): a_q and b_q 16-byte aligned and lda, ldb multiples of 16
  *  (W8A8_ERR_MISALIGNED otherwise).  out needs element alignment only.

@@ -109,12 +109,13 @@ def _stream(stream, device: int) -> int:
 class Workspace:
     """A zero-filled device scratch buffer reused across calls on one stream.
 
-    The matmul's split-K counters must start at zero; the library leaves them
-    at zero after each successful call, so the buffer only needs zeroing once,
-    on the stream that is current where it is made (a larger one that a call
-    needs: on that call's stream).  The first call on another stream waits for
-    the zeroing; what calls on several streams do with the buffer is for their
-    caller to order.
+    The arrival counters at its head (of split-K matmuls and of attention) must
+    start at zero; the library leaves them at zero after each successful call, so
+    the buffer only needs zeroing once, on the stream that is current where it is
+    made (a larger one that a call needs: on that call's stream), and one
+    Workspace serves calls of every operator that takes one.  The first call on
+    another stream waits for the zeroing; what calls on several streams do with
+    the buffer is for their caller to order.
 
     A buffer that a captured call uses is kept as long as the Workspace, so that
     the graph can be replayed after the Workspace has grown.  Make it before the

@@ -82,7 +82,6 @@ constexpr int kSmallRows = 32;
 constexpr float kHeadroom = 2.f;
 constexpr float kNoScore = -1e25f;               // below any product, and finite
 constexpr int kMaxCounters = 1024;               // CTAs that may leave a unit open
-constexpr size_t kCounterBytes = kMaxCounters * sizeof(unsigned);
 
 // CTAs of the few-rows kernel that are resident at once (its registers and
 // shared memory allow two of 8 rows to an SM, one of 16).
@@ -797,7 +796,7 @@ cudaError_t launch_kind(const Kv4AttnParams& p, int num_sms, cudaStream_t stream
 size_t kv4_attention_workspace(int share, long long max_query_len, int head_dim, int num_sms) {
   if (share * max_query_len > kSmallRows) return kv4_prompt_workspace(head_dim, num_sms);
   const int nt = share * max_query_len <= 8 ? 1 : 2;
-  return kCounterBytes + static_cast<size_t>(few_rows_ctas(nt, num_sms)) * 2 * 8 * nt * (head_dim + 4) * sizeof(float);
+  return kCounterRegion + static_cast<size_t>(few_rows_ctas(nt, num_sms)) * 2 * 8 * nt * (head_dim + 4) * sizeof(float);
 }
 
 cudaError_t read_clear_kv4_status(int* flags) {
@@ -816,7 +815,7 @@ cudaError_t read_clear_kv4_status(int* flags) {
 cudaError_t launch_kv4_attention(const Kv4AttnParams& args, int num_sms, void* workspace, cudaStream_t stream) {
   Kv4AttnParams p = args;
   p.counters = static_cast<unsigned*>(workspace);
-  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes);
+  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterRegion);
   p.share = p.num_q_heads / p.num_kv_heads;
   p.per_block = p.block_size / kKv4Tokens;
   p.block_shift = -1;

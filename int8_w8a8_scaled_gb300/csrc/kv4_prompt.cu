@@ -70,7 +70,6 @@ constexpr float kNoScore = -1e25f;
 // 2^-9 at most.  From 2^26 on it would push them out of f16.
 constexpr float kFar = 65536.f;
 constexpr int kMaxCounters = 1024;
-constexpr size_t kCounterBytes = kMaxCounters * sizeof(unsigned);
 constexpr uint32_t kTmemCols = 512;
 
 template <int D>
@@ -931,7 +930,7 @@ cudaError_t launch_t(const Kv4AttnParams& p, int num_sms, cudaStream_t stream) {
 }  // namespace
 
 size_t kv4_prompt_workspace(int head_dim, int num_sms) {
-  return kCounterBytes + static_cast<size_t>(std::min(num_sms, kMaxCounters)) * 2 * kUnitRows * (head_dim + 2) * sizeof(float);
+  return kCounterRegion + static_cast<size_t>(std::min(num_sms, kMaxCounters)) * 2 * kUnitRows * (head_dim + 2) * sizeof(float);
 }
 
 cudaError_t read_clear_kv4_prompt_status(int* flags) {

@@ -8,6 +8,7 @@ import torch
 import int8_w8a8_scaled_gb300 as w8
 from oracle import fp8_paged as fp
 from test_gpu_fp8_paged import Step, dev, random_columns
+from test_gpu_workspaces import attention_problem, matmul_problem
 
 pytestmark = pytest.mark.gpu
 COUNTERS = 65536                                             # bytes at the head of a workspace
@@ -78,3 +79,43 @@ def test_decode_attention_leaves_the_counters_zero(batch, tokens, paged):
         w8.fp8_kv_decode_attention(q, k, v, lens, one, one, out, block_table=table, workspace=workspace)
     assert not ws.buf[:COUNTERS].any()
     assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("new", [1, 3, 60])
+def test_attention_over_the_4_bit_cache_leaves_the_matmuls_counters_zero(new):
+    call, like = attention_problem(new, 84)
+    ws = w8.Workspace(64 << 20)
+    outs = [torch.empty_like(like) for _ in range(2)]
+    call(outs[0], workspace=ws)
+    assert not ws.buf[:COUNTERS].any()
+    call(outs[1])
+    assert torch.equal(*outs)
+
+
+def test_a_step_on_one_workspace():
+    """Matmuls with split K, selection and every attention in turn, three times."""
+    s = Step(86, [3000, 900, 1700], [3, 1, 2], 8, 2, 128, 16)
+    chunk = Step(87, [3000, 900, 1700], [60, 1, 80], 8, 2, 128, 16)
+    sel = random_columns(s, 40, s.rng)
+    matmul, product = matmul_problem(88)
+    kv4, rows = attention_problem(60, 89)
+    selected = [torch.full((s.q.shape[0], 2, 30), -9, dtype=torch.int32, device="cuda") for _ in range(2)]
+    products, fours = ([torch.empty_like(x) for _ in range(2)] for x in (product, rows))
+
+    def step(i, ws):
+        matmul(products[i], workspace=ws)
+        select_into(s, selected[i], ws)
+        a = s.run(selected=sel, workspace=ws)
+        matmul(products[i], workspace=ws)
+        b = chunk.run(workspace=ws)
+        kv4(fours[i], workspace=ws)
+        matmul(products[i], workspace=ws)
+        return a, b, s.run(workspace=ws)
+
+    want = step(0, None)
+    ws = w8.Workspace(128 << 20)
+    for _ in range(3):
+        got = step(1, ws)
+        for a, b in zip((*want, products[0], selected[0], fours[0]), (*got, products[1], selected[1], fours[1])):
+            assert torch.equal(a, b)
+    assert not ws.buf[:COUNTERS].any() and w8.device_status() == 0
