@@ -566,8 +566,9 @@ W8A8_API w8a8_status w8a8_verify_drafts(const void* target_probs, const void* dr
  * token t % block_size of block block_table[b * max_blocks + t / block_size];
  * tokens of a block whose id is outside [0, num_blocks) are skipped.
  * Request b's new tokens are rows query_start[b] .. query_start[b + 1] - 1 of
- * q (int32 [batch + 1], clamped to [0, tokens]; NULL: one token a request,
- * tokens = batch), of which the first max_query_len are looked at; seq_lens
+ * q (int32 [batch + 1], clamped to [0, tokens]; none where the next start is
+ * not above b's; no row of two requests; NULL: one token a request, tokens =
+ * batch), of which the first max_query_len are looked at; seq_lens
  * (int32 [batch], clamped to [0, max_blocks * block_size]) counts them in.
  * Row i of a request's n new tokens stands at position p = seq_lens[b] - n + i
  * and sees the tokens t <= p.  Rows that belong to no request, or lie past

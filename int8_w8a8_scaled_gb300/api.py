@@ -839,7 +839,8 @@ def fp8_kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     views), block_size a multiple of 16, head_dim 64 or 128.  seq_lens: int32
     [batch], lengths with the new tokens.  block_table: int32 [batch,
     max_blocks].  query_start: int32 [batch + 1], the first row of each request
-    in q, with max_query_len the most rows of one (or more; rows past it are
+    in q, which ends in front of the next one's (no rows where that is not
+    above; no row of two requests), with max_query_len the most rows of one (or more; rows past it are
     not written); None: one row a request.  Row i of a request's n sees its
     tokens t <= seq_len - n + i; a row that sees none gives zeros.  sm_scale
     defaults to 1 / sqrt(head_dim).  workspace: a Workspace, or a zero-filled

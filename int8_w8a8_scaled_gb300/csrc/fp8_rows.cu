@@ -262,27 +262,31 @@ struct Cursor {
   int group, groups, tile;  // row group of the unit, groups of the request; next tile
   int token;                // sparse: the row of q
 
-  // Sparse: the request of `token`, looked for from request u.b on (starts rise).
+  // Sparse: the request of `token`, looked for from request `from` on where starts rise;
+  // where they do not (a batch padded by zeros), among all of them, as the selection does.
   __device__ __forceinline__ void find(const Fp8AttnParams& p, int from) {
     const Fp8Paged& c = p.c;
     u.b = u.base = -1;
     u.len = 0;
-    for (int b = from; b < c.batch; ++b) {
+    // (one loop for both: it is inlined where the tiles are counted, and the code of those
+    // loops has to stay in the instruction cache)
+#pragma unroll 1
+    for (int b = falls ? 0 : from; b < c.batch; ++b) {
       const Fp8Request r = fp8_request(c, b);
-      if (token < r.first) break;
-      if (token < r.first + r.all) {
-        if (token - r.first < r.n) {
-          u.b = b;
-          u.len = r.len;
-          u.base = r.len - r.all + token - r.first;
-        }
-        seen = b;
-        return;
-      }
+      const int row = token - r.first;
+      if (row < 0 && !falls) break;
       seen = b;
+      if (row < 0 || row >= (falls ? r.n : r.all)) continue;
+      if (row < r.n) {
+        u.b = b;
+        u.len = r.len;
+        u.base = r.len - r.all + row;
+      }
+      return;
     }
   }
   int seen;                 // sparse: requests in front of this one end before `token`
+  bool falls;               // sparse: some start is below the one in front of it
 
   __device__ __forceinline__ void dense(const Fp8AttnParams& p, int b) {
     const Fp8Request r = fp8_request(p.c, b);
@@ -545,6 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int sparse_tiles = SPARSE ? static_cast<int>((static_cast<long long>(p.budget) * p.c.block_size + kTile - 1) / kTile) : 0;
   const int sparse_groups = SPARSE ? (p.share + R - 1) / R : 0;
   int sparse_seen = 0;
+  bool sparse_falls = false;
   if constexpr (SPARSE) {
     const long long per_token = static_cast<long long>(sparse_tiles) * sparse_groups * (p.c.num_kv_heads / p.side);
     total = per_token * p.c.tokens;
@@ -553,10 +558,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long token = share * nth / per_token;
     if (tid == 0) s_found = 0;
     __syncthreads();
+    bool fall = false;
     if (p.c.query_start && token < p.c.tokens)
-      for (int b = tid; b < p.c.batch; b += kThreads)
-        if (__ldg(p.c.query_start + b) <= token) atomicMax(&s_found, b);
-    __syncthreads();
+      for (int b = tid; b < p.c.batch; b += kThreads) {
+        const int start = __ldg(p.c.query_start + b);
+        if (start <= token) atomicMax(&s_found, b);
+        fall = fall || __ldg(p.c.query_start + b + 1) < start;
+      }
+    sparse_falls = __syncthreads_or(fall);
     sparse_seen = p.c.query_start ? s_found : static_cast<int>(min(token, static_cast<long long>(p.c.batch)));
   }
   tc_fence_before();
@@ -569,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Cursor<R, SPARSE> at;
   at.u.b = -1;
   at.lane = place;
+  at.falls = sparse_falls;
   if (run_tiles > 0) {
     if constexpr (SPARSE) {
       const long long unit = r0 / sparse_tiles;

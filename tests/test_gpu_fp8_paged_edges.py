@@ -1,0 +1,31 @@
+"""The operators over the paged fp8 cache at the edges of what their documentation
+allows (tolerances as in test_gpu_fp8_paged.py)."""
+import numpy as np
+import pytest
+
+from oracle import fp8_paged as fp
+from test_gpu_fp8_paged import Step, random_columns, selection_of
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("lens,start,tokens", [
+    ([500, 300, 0, 0], [0, 1, 2, 0, 0], 2),                  # a batch padded by zeros
+    ([500, 300, 77, 900], [0, 3, 3, 5, 0], 6),               # the last start below the others, a row of nobody
+    ([500, 300, 400], [4, 6, 0, 4], 6),                      # the first request's rows behind the last one's
+    ([90, 300, 400, 200], [-3, 1, 1 << 30, 1 << 30, 3], 4), # clamped starts: 1, 3, 0 and 0 rows
+])
+def test_starts_that_do_not_rise(lens, start, tokens):
+    s = Step(90, lens, [tokens] + [0] * (len(lens) - 1), 8, 2, 128, 16, extra_rows=1)
+    s.start, s.tokens, s.most = np.int32(start), tokens, 4
+    s.q = s.q[:tokens]
+    owners = [t for _, t, _ in fp.requests(s.lens, s.start, tokens, s.most, s.table.shape[1] * s.bs)]
+    assert len(owners) == len(set(owners))                   # no row of two requests
+    s.check(s.run())
+    sel = random_columns(s, 9, s.rng)
+    s.check(s.run(selected=sel), selected=sel)
+    means, scales = s.rng.integers(-127, 128, (s.nb, 2, 128)).astype(np.int8), (s.rng.random((s.nb, 2)) + 0.1).astype(np.float32)
+    before = np.full((tokens, 2, 5), -9, np.int32)
+    want = fp.select(s.q.float().numpy(), means, scales, s.lens, s.table, 16, s.start, s.most, 1, 2, 5, before)
+    assert np.array_equal(selection_of(s, means, scales, 5, 1, 2), want)
+    s.check(s.run(selected=want), selected=want)
