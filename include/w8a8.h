@@ -640,7 +640,8 @@ W8A8_API w8a8_status w8a8_fp8_kv_paged_attention(
 
 /* 8-bit means of the keys of the blocks that got new tokens, columns (L - n) /
  * block_size .. (L - 1) / block_size of each request of L tokens, n of them
- * new.  For each KV head, over the tokens of the block that lie below L:
+ * new: all n, also where max_query_len, by which the launch is sized, is less.
+ * For each KV head, over the tokens of the block that lie below L:
  *   mean = fl(sum of the codes' values) / count,  scale = absmax * fl(1 / 127)
  *   (1 if that is 0),  code = round(mean / scale), half to even,
  * the sum exact (NaN codes count as 0), the quotients and the product correctly
@@ -648,8 +649,8 @@ W8A8_API w8a8_status w8a8_fp8_kv_paged_attention(
  * The means are in units of k_scale, which has no part in their order.
  *   means        int8 [num_blocks, num_kv_heads, head_dim], 16-byte aligned
  *   mean_scales  fp32 [num_blocks, num_kv_heads]
- * Rows of other blocks are left as they are.  No block of two requests in a
- * call may be among the written ones. */
+ * Rows of other blocks are left as they are.  No block may be among the written
+ * ones twice in a call, of two requests or of two columns. */
 W8A8_API w8a8_status w8a8_fp8_kv_block_means(const void* k_cache, int64_t num_blocks, int64_t block_size,
                                              int64_t num_kv_heads, int64_t head_dim,
                                              const int32_t* block_table, int64_t max_blocks,

@@ -886,9 +886,10 @@ def fp8_kv_block_means(k_cache: torch.Tensor, seq_lens: torch.Tensor, block_tabl
     Written: the rows of means (int8 [num_blocks, num_kv_heads, head_dim]) and
     mean_scales (float32 [num_blocks, num_kv_heads]) of the blocks that hold
     the last n of each request's seq_len tokens, over the tokens that it
-    holds; other rows stay.  No block may belong to two requests of the call
-    there.  query_start: int32 [batch + 1], whose differences are the n, at
-    most max_query_len (both as for fp8_kv_attention); None: one each."""
+    holds; other rows stay.  No block may be among them twice, of two requests
+    or two columns.  query_start: int32 [batch + 1], whose differences are the
+    n, None: one each.  max_query_len: the largest n, or more (with less the
+    means are the same, and take longer)."""
     nb, bs, h, d = _fp8_cache(k_cache, "k_cache")
     if _block_means(means, mean_scales) != (nb, h, d):
         raise ValueError("means must be [num_blocks, num_kv_heads, head_dim] of the cache")

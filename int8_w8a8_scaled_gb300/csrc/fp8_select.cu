@@ -61,74 +61,78 @@ __global__ void __launch_bounds__(kMeanThreads) fp8_block_means_kernel(const Fp8
   const int kvh = blockIdx.x % a.c.num_kv_heads, nth = blockIdx.x / a.c.num_kv_heads, b = blockIdx.y;
   const Fp8Request r = fp8_request(a.c, b);
   if (r.n <= 0 || r.len <= 0) return;
-  const int col = max(0, r.len - r.all) / a.c.block_size + nth;
-  const long long t0 = static_cast<long long>(col) * a.c.block_size;
-  if (t0 >= r.len) return;
-  const int block = __ldg(a.c.block_table + static_cast<size_t>(b) * a.c.max_blocks + col);
-  if (block < 0 || block >= a.c.num_blocks) return;
-  const int count = static_cast<int>(min(static_cast<long long>(a.c.block_size), r.len - t0));
   const int tid = threadIdx.x, piece = tid % kPieces;
-  if (tid < D) s_sum[tid] = 0;
-  __syncthreads();
   const size_t row = static_cast<size_t>(a.c.num_kv_heads) * D;
-  const uint8_t* src = static_cast<const uint8_t*>(a.k_cache) + static_cast<size_t>(block) * a.c.block_size * row +
-                       static_cast<size_t>(kvh) * D + 16 * piece;
+  // (one turn, but where a request has more new tokens than max_query_len)
 #pragma unroll 1
-  for (int u0 = 0; u0 < count; u0 += kExact * kTokens) {
-    float sum[16];
+  for (long long col = max(0, r.len - r.all) / a.c.block_size + nth;; col += gridDim.x / a.c.num_kv_heads) {
+    const long long t0 = col * a.c.block_size;
+    if (t0 >= r.len) return;
+    const int block = __ldg(a.c.block_table + static_cast<size_t>(b) * a.c.max_blocks + col);
+    if (block < 0 || block >= a.c.num_blocks) continue;
+    const int count = static_cast<int>(min(static_cast<long long>(a.c.block_size), r.len - t0));
+    if (tid < D) s_sum[tid] = 0;
+    __syncthreads();
+    const uint8_t* src = static_cast<const uint8_t*>(a.k_cache) + static_cast<size_t>(block) * a.c.block_size * row +
+                         static_cast<size_t>(kvh) * D + 16 * piece;
+#pragma unroll 1
+    for (int u0 = 0; u0 < count; u0 += kExact * kTokens) {
+      float sum[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sum[i] = 0.f;
+      for (int i = 0; i < 16; ++i) sum[i] = 0.f;
 #pragma unroll 4
-    for (int u = u0 + tid / kPieces; u < min(count, u0 + kExact * kTokens); u += kTokens) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(src + u * row));
-      const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+      for (int u = u0 + tid / kPieces; u < min(count, u0 + kExact * kTokens); u += kTokens) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(src + u * row));
+        const uint32_t word[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t h[2];
-        const uint32_t clean = fp8_nan_to_zero(word[i]);
-        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-            : "=r"(h[0]), "=r"(h[1])
-            : "r"(clean));
+        for (int i = 0; i < 4; ++i) {
+          uint32_t h[2];
+          const uint32_t clean = fp8_nan_to_zero(word[i]);
+          asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+              "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+              : "=r"(h[0]), "=r"(h[1])
+              : "r"(clean));
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
-          sum[4 * i + 2 * k] += f.x;
-          sum[4 * i + 2 * k + 1] += f.y;
+          for (int k = 0; k < 2; ++k) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+            sum[4 * i + 2 * k] += f.x;
+            sum[4 * i + 2 * k + 1] += f.y;
+          }
         }
       }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        int x = __float2int_rn(sum[i] * 512.f);
+        // lanes with the same piece first
+#pragma unroll
+        for (int off = kPieces; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+        sum[i] = __int_as_float(x);
+      }
+      if (tid % 32 < kPieces) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) atomicAdd(&s_sum[16 * piece + i], __float_as_int(sum[i]));
+      }
     }
+    __syncthreads();
+    float mean = 0.f;
+    if (tid < D) {
+      mean = __fdiv_rn(__int2float_rn(s_sum[tid]) * (1.f / 512.f), static_cast<float>(count));
+      float top = fabsf(mean);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      int x = __float2int_rn(sum[i] * 512.f);
-      // lanes with the same piece first
-#pragma unroll
-      for (int off = kPieces; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-      sum[i] = __int_as_float(x);
+      for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      if (tid % 32 == 0) s_top[tid / 32] = top;
     }
-    if (tid % 32 < kPieces) {
+    __syncthreads();
+    if (tid < D) {
+      float top = s_top[0];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) atomicAdd(&s_sum[16 * piece + i], __float_as_int(sum[i]));
+      for (int i = 1; i < D / 32; ++i) top = fmaxf(top, s_top[i]);
+      const float scale = int8_scale(top);
+      const size_t at = static_cast<size_t>(block) * a.c.num_kv_heads + kvh;
+      a.means[at * D + tid] = static_cast<int8_t>(enc1<1>(__fdiv_rn(mean, scale)));
+      if (tid == 0) a.mean_scales[at] = scale;
     }
   }
-  __syncthreads();
-  float mean = 0.f, scale = 0.f;
-  if (tid < D) {
-    mean = __fdiv_rn(__int2float_rn(s_sum[tid]) * (1.f / 512.f), static_cast<float>(count));
-    float top = fabsf(mean);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    if (tid % 32 == 0) s_top[tid / 32] = top;
-  }
-  __syncthreads();
-  if (tid >= D) return;
-  float top = s_top[0];
-#pragma unroll
-  for (int i = 1; i < D / 32; ++i) top = fmaxf(top, s_top[i]);
-  scale = int8_scale(top);
-  const size_t at = static_cast<size_t>(block) * a.c.num_kv_heads + kvh;
-  a.means[at * D + tid] = static_cast<int8_t>(enc1<1>(__fdiv_rn(mean, scale)));
-  if (tid == 0) a.mean_scales[at] = scale;
 }
 
 // ------------------------------------------------------------------ scores

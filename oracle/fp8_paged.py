@@ -121,11 +121,11 @@ def quantise8(x):
 
 
 def block_means(k_codes, seq_lens, table, query_start, most, means, scales):
-    """Copies of means and scales with the rows of the blocks that got tokens."""
+    """Copies of means and scales with the rows of the blocks that got tokens (`most` has no part in it)."""
     means, scales = means.copy(), scales.copy()
     nb, bs = k_codes.shape[:2]
     rows: dict = {}
-    for b, _, pos in requests(seq_lens, query_start, 1 << 31, most, table.shape[1] * bs):
+    for b, _, pos in requests(seq_lens, query_start, 1 << 31, 1 << 31, table.shape[1] * bs):
         rows.setdefault(b, []).append(pos)
     for b, positions in rows.items():
         length = int(np.clip(seq_lens[b], 0, table.shape[1] * bs))

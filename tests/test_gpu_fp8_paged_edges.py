@@ -3,8 +3,9 @@ allows (tolerances as in test_gpu_fp8_paged.py)."""
 import numpy as np
 import pytest
 
+import int8_w8a8_scaled_gb300 as w8
 from oracle import fp8_paged as fp
-from test_gpu_fp8_paged import Step, random_columns, selection_of
+from test_gpu_fp8_paged import E4M3, Step, dev, random_columns, selection_of
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +30,16 @@ def test_starts_that_do_not_rise(lens, start, tokens):
     want = fp.select(s.q.float().numpy(), means, scales, s.lens, s.table, 16, s.start, s.most, 1, 2, 5, before)
     assert np.array_equal(selection_of(s, means, scales, 5, 1, 2), want)
     s.check(s.run(selected=want), selected=want)
+
+
+@pytest.mark.parametrize("lens,new,most,bs", [
+    ([40], [40], 1, 16), ([700, 64, 63], [200, 64, 1], 3, 64), ([33, 300], [33, 290], 16, 16), ([20], [50], 2, 16),
+])
+def test_block_means_of_more_tokens_than_are_looked_at(lens, new, most, bs):
+    """Every block that got new tokens has new means, whatever max_query_len is."""
+    s = Step(91, lens, new, 2, 2, 64, bs, tail=0x7F)
+    means, scales = s.rng.integers(-127, 128, (s.nb, 2, 64)).astype(np.int8), s.rng.random((s.nb, 2)).astype(np.float32)
+    gm, gs = dev(means), dev(scales)
+    w8.fp8_kv_block_means(dev(s.kc).view(E4M3), dev(s.lens), dev(s.table), gm, gs, query_start=dev(s.start), max_query_len=most)
+    wm, ws = fp.block_means(s.kc, s.lens, s.table, s.start, max(new), means, scales)
+    assert np.array_equal(gm.cpu().numpy(), wm) and np.array_equal(gs.cpu().numpy(), ws)
