@@ -1525,8 +1525,6 @@ w8a8_status w8a8_fp8_kv_block_means(const void* k_cache, int64_t num_blocks, int
   if (st != W8A8_OK) return st;
   if (!aligned(k_cache, 16) || !aligned(means, 16) || !aligned(mean_scales, 4))
     return fail(W8A8_ERR_MISALIGNED, "the cache and the means must be 16-byte aligned, their scales 4-byte");
-  if ((std::min(max_query_len, tokens) / block_size + 2) * num_kv_heads >= (1LL << 31))
-    return fail(W8A8_ERR_UNSUPPORTED, "max_query_len / block_size * num_kv_heads out of range");
   DeviceInfo dev;
   if ((st = device_info(&dev)) != W8A8_OK) return st;
   a.k_cache = k_cache;

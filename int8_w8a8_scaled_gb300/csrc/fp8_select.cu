@@ -443,6 +443,7 @@ cudaError_t launch_scores(const Fp8SelectArgs& a, int token0, cudaStream_t strea
 
 cudaError_t launch_fp8_block_means(const Fp8MeansArgs& a, cudaStream_t stream) {
   const int most = static_cast<int>(std::min<long long>((a.c.max_query_len - 1LL) / a.c.block_size + 2, a.c.max_blocks));
+  // (at most max_blocks * num_kv_heads, which the sizes' limits keep below 2^29)
   const dim3 grid(static_cast<unsigned>(most) * a.c.num_kv_heads, a.c.batch);
   if (a.c.head_dim == 64) return fp8_launch(fp8_block_means_kernel<64>, grid, dim3(kMeanThreads), 0, stream, a);
   return fp8_launch(fp8_block_means_kernel<128>, grid, dim3(kMeanThreads), 0, stream, a);

@@ -2,6 +2,7 @@
 allows (tolerances as in test_gpu_fp8_paged.py)."""
 import numpy as np
 import pytest
+import torch
 
 import int8_w8a8_scaled_gb300 as w8
 from oracle import fp8_paged as fp
@@ -43,3 +44,14 @@ def test_block_means_of_more_tokens_than_are_looked_at(lens, new, most, bs):
     w8.fp8_kv_block_means(dev(s.kc).view(E4M3), dev(s.lens), dev(s.table), gm, gs, query_start=dev(s.start), max_query_len=most)
     wm, ws = fp.block_means(s.kc, s.lens, s.table, s.start, max(new), means, scales)
     assert np.array_equal(gm.cpu().numpy(), wm) and np.array_equal(gs.cpu().numpy(), ws)
+
+
+@pytest.mark.parametrize("most", [64, (1 << 31) - 1])
+def test_block_means_of_many_heads_with_a_generous_limit(most):
+    """max_query_len may be any number above the new tokens."""
+    s = Step(92, [100, 33], [5, 1], 32, 32, 64, 16)
+    means, scales = torch.zeros(s.nb, 32, 64, dtype=torch.int8, device="cuda"), torch.zeros(s.nb, 32, device="cuda")
+    w8.fp8_kv_block_means(dev(s.kc).view(E4M3), dev(s.lens), dev(s.table), means, scales, query_start=dev(s.start), max_query_len=most)
+    zero = np.zeros((s.nb, 32, 64), np.int8), np.zeros((s.nb, 32), np.float32)
+    wm, ws = fp.block_means(s.kc, s.lens, s.table, s.start, 5, *zero)
+    assert np.array_equal(means.cpu().numpy(), wm) and np.array_equal(scales.cpu().numpy(), ws)
