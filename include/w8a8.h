@@ -622,9 +622,9 @@ W8A8_API w8a8_status w8a8_fp8_kv_rotate_write(
  *               its counters zero again.  Calls that may overlap on the GPU
  *               need workspaces of their own.
  * Limits: num_q_heads a multiple of num_kv_heads with a quotient of at most 64;
- * max_blocks * block_size < 2^31 and its product with batch * num_kv_heads <
- * 2^33; batch * max_query_len * num_q_heads < 2^31; batch and head counts <=
- * 65535.  The workspace size is 0 for sizes outside the limits. */
+ * max_blocks * block_size <= 2^31 - 2^24 and its product with batch *
+ * num_kv_heads < 2^33; batch * max_query_len * num_q_heads < 2^31; batch and
+ * head counts <= 65535.  The workspace size is 0 for sizes outside the limits. */
 W8A8_API size_t w8a8_fp8_kv_paged_attention_workspace_size(int64_t batch, int64_t max_query_len,
                                                            int64_t num_q_heads, int64_t num_kv_heads,
                                                            int64_t head_dim);

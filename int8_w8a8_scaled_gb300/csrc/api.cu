@@ -1334,6 +1334,8 @@ w8a8_status fp8_attention_call(const void* q, int q_dtype, int64_t num_q_heads, 
   if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !out) return fail(W8A8_ERR_INVALID_ARG, "null pointer argument");
   if ((q_dtype != W8A8_BF16 && q_dtype != W8A8_FP16) || (out_dtype != W8A8_BF16 && out_dtype != W8A8_FP16))
     return fail(W8A8_ERR_INVALID_ARG, "q and out must be BF16 or FP16");
+  if (static_cast<int64_t>(c.max_blocks) * c.block_size > w8a8::kFp8MostTokens)
+    return fail(W8A8_ERR_UNSUPPORTED, "max_blocks * block_size must be at most 2^31 - 2^24");
   const int64_t tokens = c.tokens, d = c.head_dim;
   if (!strides_ok(tokens, num_q_heads, q_token_stride, q_head_stride) ||
       !strides_ok(tokens, num_q_heads, out_token_stride, out_head_stride) || (tokens > 1 && out_token_stride < d) ||

@@ -66,7 +66,7 @@ constexpr float kNoScore = -1e25f;
 // values, and values at most a ring (8 tiles) ahead of the products, which come after
 // the places have been read.
 constexpr int kPlaces = 32;
-constexpr int kDead = 0x7f000000;             // the position of a token that is not there
+constexpr int kDead = kFp8MostTokens;         // the position of a token that is not there
 constexpr size_t kSmemMost = 227 * 1024;
 
 template <int D, int R>
