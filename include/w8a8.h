@@ -615,7 +615,8 @@ W8A8_API w8a8_status w8a8_fp8_kv_rotate_write(
  * infinity in q[i,h,:] gives NaN in that row.
  *   q, out      [tokens, num_q_heads, head_dim] bf16 / fp16, a head's dims
  *               consecutive, token and head strides in elements; out may not
- *               share memory with q.
+ *               share memory with q (slices of one buffer that lie beside each
+ *               other with the same strides do not).
  *   max_query_len  the largest number of new tokens of a request, or more.
  *   workspace   w8a8_fp8_kv_paged_attention_workspace_size() bytes, 16-byte
  *               aligned, zero-filled before its first use; every call leaves

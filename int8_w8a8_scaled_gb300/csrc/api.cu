@@ -1312,13 +1312,46 @@ w8a8_status fp8_heads(int64_t batch, int64_t max_query_len, int64_t num_q_heads,
   return W8A8_OK;
 }
 
-// A [tokens, heads, head_dim] operand's bytes, from its first to its last element.
-struct Span {
-  uintptr_t begin, end;
-  Span(const void* p, int64_t tokens, int64_t heads, int64_t head_dim, int64_t token_stride, int64_t head_stride)
-      : begin(reinterpret_cast<uintptr_t>(p)),
-        end(begin + 2 * static_cast<uintptr_t>((tokens - 1) * token_stride + (heads - 1) * head_stride + head_dim)) {}
-  bool meets(const Span& o) const { return begin < o.end && o.begin < end; }
+// A [tokens, heads, head_dim] operand of 16-bit elements: where it begins, and its steps
+// and the number of each (tokens, heads), in bytes.  A step of one, or of stride 0, is none.
+struct Operand {
+  int64_t begin, step[2], count[2], dims;
+  Operand(const void* p, int64_t tokens, int64_t heads, int64_t head_dim, int64_t token_stride, int64_t head_stride)
+      : begin(static_cast<int64_t>(reinterpret_cast<uintptr_t>(p))),
+        step{2 * token_stride, 2 * head_stride},
+        count{token_stride ? tokens : 1, head_stride ? heads : 1},
+        dims(2 * head_dim) {}
+  // Bytes from its first to its last element, over the heads of a token (or the tokens of a
+  // head) alone, or all of it.
+  int64_t length(bool outer, bool inner, int first) const {
+    return (outer ? (count[first] - 1) * step[first] : 0) + (inner ? (count[1 - first] - 1) * step[1 - first] : 0) + dims;
+  }
+  // Whether it may share an element with `o`: no where their ranges lie apart, or where both
+  // repeat at the same step and each repeat's ranges lie apart in every period (slices of one
+  // buffer); anything else counts as yes.
+  bool meets(const Operand& o) const {
+    // the outer axis: the one of the larger step
+    const Operand& two = count[0] > 1 && count[1] > 1 ? *this : o;
+    const int first = two.count[0] > 1 && two.count[1] > 1 && two.step[1] > two.step[0] ? 1 : 0;
+    int64_t delta = o.begin - begin;
+    if (apart(delta, length(true, true, first), o.length(true, true, first))) return false;
+    for (int level = 0; level < 2; ++level) {
+      const int axis = level ? 1 - first : first;
+      if (count[axis] == 1 && o.count[axis] == 1) continue;
+      const int64_t s = count[axis] > 1 ? step[axis] : o.step[axis];
+      const int64_t mine = length(false, !level, first), other = o.length(false, !level, first);
+      if ((o.count[axis] > 1 && o.step[axis] != s) || mine > s || other > s) return true;
+      delta = (delta % s + s) % s;  // `o` begins here, and a period before
+      if (apart(delta, mine, other)) {
+        if (apart(delta - s, mine, other)) return false;
+        delta -= s;
+      } else if (!apart(delta - s, mine, other)) {
+        return true;
+      }
+    }
+    return true;
+  }
+  static bool apart(int64_t delta, int64_t mine, int64_t other) { return delta >= mine || -delta >= other; }
 };
 
 // Strides of an operand: not negative, and small enough that offsets fit 62 bits.
@@ -1344,7 +1377,8 @@ w8a8_status fp8_attention_call(const void* q, int q_dtype, int64_t num_q_heads, 
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return fail(W8A8_ERR_MISALIGNED, "the caches must be 16-byte aligned");
   if (!aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(selected, 4) || !aligned(q, 2) || !aligned(out, 2))
     return fail(W8A8_ERR_MISALIGNED, "misaligned q, out, scale or selection pointer");
-  if (Span(q, tokens, num_q_heads, d, q_token_stride, q_head_stride).meets(Span(out, tokens, num_q_heads, d, out_token_stride, out_head_stride)))
+  if (Operand(q, tokens, num_q_heads, d, q_token_stride, q_head_stride)
+          .meets(Operand(out, tokens, num_q_heads, d, out_token_stride, out_head_stride)))
     return fail(W8A8_ERR_INVALID_ARG, "out must not share memory with q");
   if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
     return fail(W8A8_ERR_WORKSPACE, "workspace must be 16-byte aligned and hold %zu bytes", need);
@@ -1430,10 +1464,10 @@ w8a8_status w8a8_fp8_kv_rotate_write(const void* q, const void* k, const void* v
       !aligned(slots, 8) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
     return fail(W8A8_ERR_MISALIGNED, "misaligned q, k, v, cos_sin, positions, slots or scale pointer");
   if (num_q_heads > 0 && !(q == q_out && q_token_stride == q_out_token_stride && q_head_stride == q_out_head_stride)) {
-    const Span o(q_out, tokens, num_q_heads, head_dim, q_out_token_stride, q_out_head_stride);
-    if (o.meets(Span(q, tokens, num_q_heads, head_dim, q_token_stride, q_head_stride)) ||
-        o.meets(Span(k, tokens, num_kv_heads, head_dim, k_token_stride, k_head_stride)) ||
-        o.meets(Span(v, tokens, num_kv_heads, head_dim, v_token_stride, v_head_stride)))
+    const Operand o(q_out, tokens, num_q_heads, head_dim, q_out_token_stride, q_out_head_stride);
+    if (o.meets(Operand(q, tokens, num_q_heads, head_dim, q_token_stride, q_head_stride)) ||
+        o.meets(Operand(k, tokens, num_kv_heads, head_dim, k_token_stride, k_head_stride)) ||
+        o.meets(Operand(v, tokens, num_kv_heads, head_dim, v_token_stride, v_head_stride)))
       return fail(W8A8_ERR_INVALID_ARG, "q_out must be q itself or share no memory with q, k and v");
   }
   w8a8_status st;

@@ -6,7 +6,7 @@ import torch
 
 import int8_w8a8_scaled_gb300 as w8
 from oracle import fp8_paged as fp
-from test_gpu_fp8_paged import E4M3, Step, dev, random_columns, selection_of
+from test_gpu_fp8_paged import E4M3, Step, codes, dev, head_rows, host, random_columns, selection_of
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +55,48 @@ def test_block_means_of_many_heads_with_a_generous_limit(most):
     zero = np.zeros((s.nb, 32, 64), np.int8), np.zeros((s.nb, 32), np.float32)
     wm, ws = fp.block_means(s.kc, s.lens, s.table, s.start, 5, *zero)
     assert np.array_equal(means.cpu().numpy(), wm) and np.array_equal(scales.cpu().numpy(), ws)
+
+
+@pytest.mark.parametrize("layout", ["halves", "heads", "dims", "heads_first"])
+@pytest.mark.parametrize("new", [[3, 2], [70, 1]])
+def test_queries_and_outputs_side_by_side(layout, new):
+    """q and out are slices of one buffer that share none of its elements."""
+    s = Step(93, [300, 200], new, 8, 2, 64, 16)
+    T, H, D = s.q.shape
+    if layout == "halves":
+        buf = torch.full((T, 2 * H, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        q, out = buf[:, :H], buf[:, H:]
+    elif layout == "heads":
+        buf = torch.full((T, 2 * H, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        q, out = buf[:, ::2], buf[:, 1::2]
+    elif layout == "dims":
+        buf = torch.full((T, H, 2 * D), 7.0, dtype=torch.bfloat16, device="cuda")
+        q, out = buf[:, :, :D], buf[:, :, D:]
+    else:
+        buf = torch.full((H, T, 2 * D), 7.0, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+        q, out = buf[:, :, D:], buf[:, :, :D]
+    q.copy_(s.q)
+    w8.fp8_kv_attention(q, dev(s.kc).view(E4M3), dev(s.vc).view(E4M3), dev(s.lens), dev(s.table), dev(np.float32([s.kg])),
+                        dev(np.float32([s.vg])), out, query_start=dev(s.start), max_query_len=s.most, sm_scale=s.sm)
+    s.check(out)
+    assert torch.equal(q.cpu(), s.q)
+
+
+def test_rotated_queries_beside_the_projection():
+    """q_out is a slice of the buffer that q, k and v are slices of."""
+    rng = np.random.default_rng(94)
+    x = head_rows(rng, (19, 12, 64), "bf16")
+    buf = torch.full((19, 20, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    buf[:, :12] = x.cuda()
+    angle = rng.uniform(-3, 3, (50, 32))
+    table = np.concatenate([np.cos(angle), np.sin(angle)], 1).astype(np.float32)
+    pos, slots = rng.integers(0, 50, 19).astype(np.int32), rng.permutation(32)[:19].astype(np.int64)
+    caches = [torch.zeros(2, 16, 2, 64, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    one = torch.ones(1, device="cuda")
+    w8.fp8_kv_rotate_write(buf[:, :8], buf[:, 8:10], buf[:, 10:12], dev(table), dev(pos), *caches, dev(slots), one, one, buf[:, 12:])
+    x = x.float().numpy()
+    assert np.array_equal(host(buf[:, 12:]), host(torch.from_numpy(fp.rotate(x[:, :8], pos, table)).bfloat16()))
+    assert np.array_equal(host(buf[:, :12]), x)
+    zero = np.zeros((2, 16, 2, 64), np.uint8)
+    assert np.array_equal(codes(caches[0]), fp.write(zero, slots, fp.rotate(x[:, 8:10], pos, table), 1.0))
+    assert np.array_equal(codes(caches[1]), fp.write(zero, slots, x[:, 10:], 1.0))
