@@ -587,7 +587,8 @@ W8A8_API w8a8_status w8a8_verify_drafts(const void* target_probs, const void* dr
  *   q, k, v   [tokens, heads, head_dim] bf16 or fp16 (dtype), a head's dims
  *             consecutive, token and head strides in elements.  num_q_heads
  *             may be 0: then q and q_out are not looked at.
- *   q_out     as q; q itself (same pointer and strides) or memory of its own.
+ *   q_out     as q; q itself (same pointer and strides) or memory of its own;
+ *             never that of k or v.
  *   cos_sin   fp32 [max_position, rot_dim]: cosines of the rot_dim / 2 pairs,
  *             then sines.  A position outside it gives NaN for its pairs.
  *   positions int32 [axes, tokens]; axes is 1 to 4.

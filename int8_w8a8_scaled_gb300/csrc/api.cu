@@ -1463,12 +1463,13 @@ w8a8_status w8a8_fp8_kv_rotate_write(const void* q, const void* k, const void* v
   if (!aligned(k, 2) || !aligned(v, 2) || !aligned(q, 2) || !aligned(q_out, 2) || !aligned(cos_sin, 4) || !aligned(positions, 4) ||
       !aligned(slots, 8) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
     return fail(W8A8_ERR_MISALIGNED, "misaligned q, k, v, cos_sin, positions, slots or scale pointer");
-  if (num_q_heads > 0 && !(q == q_out && q_token_stride == q_out_token_stride && q_head_stride == q_out_head_stride)) {
+  if (num_q_heads > 0) {
+    const bool in_place = q == q_out && q_token_stride == q_out_token_stride && q_head_stride == q_out_head_stride;
     const Operand o(q_out, tokens, num_q_heads, head_dim, q_out_token_stride, q_out_head_stride);
-    if (o.meets(Operand(q, tokens, num_q_heads, head_dim, q_token_stride, q_head_stride)) ||
+    if ((!in_place && o.meets(Operand(q, tokens, num_q_heads, head_dim, q_token_stride, q_head_stride))) ||
         o.meets(Operand(k, tokens, num_kv_heads, head_dim, k_token_stride, k_head_stride)) ||
         o.meets(Operand(v, tokens, num_kv_heads, head_dim, v_token_stride, v_head_stride)))
-      return fail(W8A8_ERR_INVALID_ARG, "q_out must be q itself or share no memory with q, k and v");
+      return fail(W8A8_ERR_INVALID_ARG, "q_out must be q itself or share no memory with q, and share none with k and v");
   }
   w8a8_status st;
   DeviceInfo dev;

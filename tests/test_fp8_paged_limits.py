@@ -4,7 +4,8 @@ import ctypes
 
 import pytest
 
-from test_fp8_paged_abi import FAKE, attend
+from int8_w8a8_scaled_gb300 import _lib
+from test_fp8_paged_abi import FAKE, FAKE2, WRITE, attend
 
 INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 4
 
@@ -32,3 +33,13 @@ def test_positions_of_attention(sparse, blocks, size, status):
 def test_queries_and_outputs_in_one_buffer(sparse, apart, token, head, status):
     kw = dict(qt=token, qh=head, ot=token, oh=head, out=ctypes.c_void_p(FAKE.value + 2 * apart))
     assert attend(sparse, **kw) == status
+
+
+@pytest.mark.parametrize("kw", [dict(k=FAKE, v=FAKE2), dict(k=FAKE2, v=FAKE), dict(k=ctypes.c_void_p(FAKE.value + 2 * 1023), v=FAKE2, qt=1280, ot=1280, kt=1280)])
+def test_queries_turned_in_place_over_keys_or_values(kw):
+    """A key of another token or head would be read before or after its memory is a turned query."""
+    a = {**WRITE, "out": FAKE, **kw}
+    assert _lib.load().w8a8_fp8_kv_rotate_write(
+        a["q"], a["k"], a["v"], a["dtype"], a["tokens"], a["hq"], a["h"], a["d"], a["qt"], a["qh"], a["kt"], a["kh"], a["vt"], a["vh"],
+        a["cs"], a["mp"], a["rot"], a["pos"], a["axes"], None, a["inter"], a["kc"], a["vc"], a["nb"], a["bs"], a["slots"], a["ks"],
+        a["vs"], a["out"], a["ot"], a["oh"], None) == INVALID
