@@ -625,8 +625,9 @@ W8A8_API w8a8_status w8a8_fp8_kv_rotate_write(
  *               need workspaces of their own.
  * Limits: num_q_heads a multiple of num_kv_heads with a quotient of at most 64;
  * max_blocks * block_size <= 2^31 - 2^24 and its product with batch *
- * num_kv_heads < 2^33; batch * max_query_len * num_q_heads < 2^31; batch and
- * head counts <= 65535.  The workspace size is 0 for sizes outside the limits. */
+ * num_kv_heads < 2^33; batch * max_query_len * num_q_heads <= 2^31 - 2^24;
+ * batch and head counts <= 65535.  The workspace size is 0 for sizes outside the
+ * limits. */
 W8A8_API size_t w8a8_fp8_kv_paged_attention_workspace_size(int64_t batch, int64_t max_query_len,
                                                            int64_t num_q_heads, int64_t num_kv_heads,
                                                            int64_t head_dim);
@@ -675,7 +676,7 @@ W8A8_API w8a8_status w8a8_fp8_kv_block_means(const void* k_cache, int64_t num_bl
  *              zero where it was written in its first 65536 bytes, so that other
  *              calls' counters in the same memory stay zero.
  * first_blocks >= 0, last_blocks >= 1, their sum at most budget;
- * max_blocks <= 49152; num_q_heads / num_kv_heads at most 64. */
+ * max_blocks <= 49152; heads and rows as for w8a8_fp8_kv_paged_attention. */
 W8A8_API size_t w8a8_fp8_kv_select_blocks_workspace_size(int64_t tokens, int64_t num_kv_heads, int64_t max_blocks);
 
 W8A8_API w8a8_status w8a8_fp8_kv_select_blocks(
@@ -693,7 +694,8 @@ W8A8_API w8a8_status w8a8_fp8_kv_select_blocks(
  * column named twice counts twice.
  *   workspace  w8a8_fp8_kv_sparse_attention_workspace_size() bytes, 16-byte
  *              aligned, zero-filled before its first use and left so.
- * budget * block_size < 2^24; the other limits as above. */
+ * budget * block_size < 2^24, tokens * num_q_heads <= 2^31 - 2^24; the other
+ * limits as above. */
 W8A8_API size_t w8a8_fp8_kv_sparse_attention_workspace_size(int64_t tokens, int64_t num_q_heads,
                                                             int64_t num_kv_heads, int64_t head_dim,
                                                             int64_t budget, int64_t block_size);

@@ -1306,8 +1306,10 @@ w8a8_status fp8_paged(const int32_t* block_table, int64_t max_blocks, const int3
 w8a8_status fp8_heads(int64_t batch, int64_t max_query_len, int64_t num_q_heads, int64_t num_kv_heads) {
   if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0)
     return fail(W8A8_ERR_INVALID_ARG, "num_q_heads must be a multiple of num_kv_heads, both >= 1");
-  if (num_q_heads > 65535 || max_query_len >= (1LL << 31) / num_q_heads || max_query_len * num_q_heads >= (1LL << 31) / batch)
-    return fail(W8A8_ERR_UNSUPPORTED, "batch * max_query_len * num_q_heads must be below 2^31, num_q_heads <= 65535");
+  // (the kernels count rows in steps of up to 256, in 32 bits: not up to the last ones)
+  if (num_q_heads > 65535 || max_query_len > w8a8::kFp8MostRows / num_q_heads ||
+      max_query_len * num_q_heads > w8a8::kFp8MostRows / batch)
+    return fail(W8A8_ERR_UNSUPPORTED, "batch * max_query_len * num_q_heads must be at most 2^31 - 2^24, num_q_heads <= 65535");
   if (num_q_heads / num_kv_heads > 64) return fail(W8A8_ERR_UNSUPPORTED, "num_q_heads / num_kv_heads must be at most 64");
   return W8A8_OK;
 }

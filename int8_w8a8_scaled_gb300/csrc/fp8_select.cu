@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kScoreThreads, 4) fp8_block_scores_kernel(cons
   const int per_pass = tiles > 1 ? kRowTile / 8 / tiles : kRowTile / pad;  // tokens (share <= 64: at least one)
   const int rows_of = tiles > 1 ? 8 * tiles : pad;                         // padded rows of a token
 #pragma unroll 1
-  for (int i = i0; i < i1; i += per_pass) {
+  for (int i = i0; i < i1; i += per_pass) {  // (i1 is at most kFp8MostRows)
     const int n = min(per_pass, i1 - i);
     __syncthreads();
     // a warp quantises its rows, D / 32 values a lane, four rows' loads in flight; zeros for
@@ -455,7 +455,7 @@ size_t fp8_select_workspace(long long tokens, long long num_kv_heads, long long 
 
 cudaError_t launch_fp8_select(const Fp8SelectArgs& args, cudaStream_t stream) {
   Fp8SelectArgs a = args;
-  a.slab = slab_of(a.c.tokens, a.c.num_kv_heads, a.c.max_blocks);
+  const int slab = slab_of(a.c.tokens, a.c.num_kv_heads, a.c.max_blocks);
   const int smem = (a.c.max_blocks + 3) / 4 * 4 * static_cast<int>(sizeof(uint32_t));
   // more threads where there are many columns: 4096 of them (16 tokens, 8 heads) 12.8 us by 1024
   // threads, 16.5 by 256; 300 (32 tokens, 8 heads) 9.0 by 256.  (Ranks in place of the
@@ -466,8 +466,9 @@ cudaError_t launch_fp8_select(const Fp8SelectArgs& args, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(pick, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kMaxSelectBlocks * static_cast<int>(sizeof(uint32_t)));
   if (e != cudaSuccess) return e;
-  for (long long t0 = 0; t0 < a.c.tokens; t0 += a.slab) {
-    const int n = static_cast<int>(std::min<long long>(a.slab, a.c.tokens - t0));
+  for (long long t0 = 0; t0 < a.c.tokens; t0 += slab) {
+    const int n = static_cast<int>(std::min<long long>(slab, a.c.tokens - t0));
+    a.slab = n;  // (the last pass's own: the kernel's token0 + slab never passes the tokens, nor 2^31)
     e = a.c.head_dim == 64 ? launch_scores<64>(a, static_cast<int>(t0), stream) : launch_scores<128>(a, static_cast<int>(t0), stream);
     if (e != cudaSuccess) return e;
     e = fp8_launch(pick, dim3(n, a.c.num_kv_heads), dim3(wide ? 1024 : 256), smem, stream, a, static_cast<int>(t0));

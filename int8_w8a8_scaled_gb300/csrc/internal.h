@@ -324,6 +324,8 @@ struct Fp8AttnParams {
 // max_blocks * block_size of the attention calls is at most this: tokens that are not
 // there have it as their position, which no row sees, and sums with it fit 32 bits.
 constexpr int kFp8MostTokens = 0x7f000000;
+// batch * max_query_len * num_q_heads is at most this: sums of a row and a step fit 32 bits.
+constexpr int64_t kFp8MostRows = 0x7f000000;
 constexpr int kFp8MaxCtas = 1024;  // a counter each: fewer than kCounterSlots
 // Units of at most 32 rows (fp8_rows.cu; `rows`: the most of a request, or a
 // token's heads).  The maps: caches as [rows, num_kv_heads * head_dim] bytes, a

@@ -4,8 +4,9 @@ import ctypes
 
 import pytest
 
+import int8_w8a8_scaled_gb300 as w8
 from int8_w8a8_scaled_gb300 import _lib
-from test_fp8_paged_abi import FAKE, FAKE2, WRITE, attend
+from test_fp8_paged_abi import ATTEND, FAKE, FAKE2, WRITE, attend
 
 INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 4
 
@@ -43,3 +44,20 @@ def test_queries_turned_in_place_over_keys_or_values(kw):
         a["q"], a["k"], a["v"], a["dtype"], a["tokens"], a["hq"], a["h"], a["d"], a["qt"], a["qh"], a["kt"], a["kh"], a["vt"], a["vh"],
         a["cs"], a["mp"], a["rot"], a["pos"], a["axes"], None, a["inter"], a["kc"], a["vc"], a["nb"], a["bs"], a["slots"], a["ks"],
         a["vs"], a["out"], a["ot"], a["oh"], None) == INVALID
+
+
+@pytest.mark.parametrize("most,heads,status", [
+    ((1 << 31) - 1, 1, UNSUPPORTED), ((1 << 31) - 64, 1, UNSUPPORTED), (0x7F000000 + 1, 1, UNSUPPORTED), ((1 << 28) - 1, 8, UNSUPPORTED),
+    (0x7F000000, 1, WORKSPACE), (0x7F000000 // 8, 8, WORKSPACE),
+])
+def test_rows_of_a_request(most, heads, status):
+    """The kernels count a request's rows in 32 bits, a step of rows past the last one."""
+    a = {**ATTEND, "tokens": most, "batch": 1, "most": most, "h": 1, "hq": heads, "qt": 0, "qh": 128}
+    assert _lib.load().w8a8_fp8_kv_select_blocks(
+        a["q"], a["qd"], a["tokens"], a["hq"], a["h"], a["d"], a["qt"], a["qh"], FAKE, FAKE, a["nb"], a["bs"], a["table"], a["mb"],
+        a["lens"], a["start"], 1, a["most"], 0, 1, a["budget"], a["sel"], None, 0, None) == status
+    kw = {x: a[x] for x in ("tokens", "batch", "most", "h", "hq", "qt", "qh")}
+    for sparse in (False, True):
+        assert attend(sparse, **kw, ot=128 * heads, oh=128, out=ctypes.c_void_p(FAKE.value + (1 << 44))) == status
+    assert (w8.fp8_kv_attention_workspace_size(1, most, heads, 1, 128) > 0) == (status == WORKSPACE)
+    assert (w8.fp8_kv_sparse_attention_workspace_size(most, heads, 1, 128, 4, 16) > 0) == (status == WORKSPACE)

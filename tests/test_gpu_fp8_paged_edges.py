@@ -100,3 +100,20 @@ def test_rotated_queries_beside_the_projection():
     zero = np.zeros((2, 16, 2, 64), np.uint8)
     assert np.array_equal(codes(caches[0]), fp.write(zero, slots, fp.rotate(x[:, 8:10], pos, table), 1.0))
     assert np.array_equal(codes(caches[1]), fp.write(zero, slots, x[:, 10:], 1.0))
+
+
+def test_select_blocks_for_the_last_of_two_billion_rows():
+    """Rows of q up to the largest number of them: a pass over the scores may not count past 2^31."""
+    if torch.cuda.mem_get_info()[0] < 48 << 30:
+        pytest.skip("a selection of 17 GB")
+    tokens = (1 << 31) - 1
+    q = torch.ones(1, 1, 64, dtype=torch.bfloat16, device="cuda").expand(tokens, 1, 64)
+    means = torch.zeros(3, 1, 64, dtype=torch.int8, device="cuda")
+    means[:, 0, 0] = torch.tensor([-3, 5, 1], dtype=torch.int8, device="cuda")
+    selected = torch.full((tokens, 1, 2), -9, dtype=torch.int32, device="cuda")
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    ws = torch.zeros(w8.fp8_kv_select_blocks_workspace_size(tokens, 1, 3), dtype=torch.uint8, device="cuda")
+    w8.fp8_kv_select_blocks(q, means, torch.ones(3, 1, device="cuda"), ints(48), ints(0, 1, 2).view(1, 3), 16, selected,
+                            query_start=ints(tokens - 1, tokens), first_blocks=0, last_blocks=1, workspace=ws)
+    assert selected[-1, 0].tolist() == [1, 2]
+    assert (selected[:-1] == -9).all()
