@@ -117,3 +117,57 @@ def test_select_blocks_for_the_last_of_two_billion_rows():
                             query_start=ints(tokens - 1, tokens), first_blocks=0, last_blocks=1, workspace=ws)
     assert selected[-1, 0].tolist() == [1, 2]
     assert (selected[:-1] == -9).all()
+
+
+# ------------------------------------------------------------------ lengths that they are for
+
+
+@pytest.mark.parametrize("lens,new,hq,h,bs,budget,first,last", [
+    ([60000, 33000], [40, 3], 4, 2, 16, 200, 1, 2),          # 3750 and 2063 columns: the wide kernel
+    ([50000], [2100], 2, 1, 16, 64, 2, 3),                   # a prompt chunk of thousands, in several passes and slabs
+    ([40000, 39000, 38000], [1, 1, 1], 16, 2, 16, 2400, 0, 1),
+    ([34000, 100], [1200, 1], 8, 1, 32, 30, 1, 2),           # 1063 columns: the narrow kernel
+])
+def test_select_blocks_of_long_contexts(lens, new, hq, h, bs, budget, first, last):
+    s = Step(95, lens, new, hq, h, 64, bs)
+    means, scales = s.rng.integers(-127, 128, (s.nb, h, 64)).astype(np.int8), (s.rng.random((s.nb, h)) + 0.1).astype(np.float32)
+    before = np.full((s.q.shape[0], h, budget), -9, np.int32)
+    want = fp.select(s.q.float().numpy(), means, scales, s.lens, s.table, bs, s.start, s.most, first, last, budget, before)
+    assert np.array_equal(selection_of(s, means, scales, budget, first, last), want)
+
+
+def test_select_blocks_of_long_contexts_with_ties():
+    s = Step(96, [60000], [70], 2, 1, 64, 16)
+    means, scales = s.rng.integers(-1, 2, (s.nb, 1, 64)).astype(np.int8), np.ones((s.nb, 1), np.float32)
+    s.q = torch.from_numpy(s.rng.integers(-1, 2, s.q.shape).astype(np.float32)).bfloat16()
+    s.q[0] = 0
+    s.table[0, 2000:2100] = -1
+    before = np.full((70, 1, 3000), -9, np.int32)
+    want = fp.select(s.q.float().numpy(), means, scales, s.lens, s.table, 16, s.start, 70, 1, 2, 3000, before)
+    assert np.array_equal(selection_of(s, means, scales, 3000, 1, 2), want)
+
+
+@pytest.mark.parametrize("lens,new,hq,h,d,bs", [
+    ([70000, 50], [1, 1], 4, 1, 64, 16), ([40000], [5], 8, 2, 128, 64), ([50000, 20000], [40, 1], 2, 1, 128, 32), ([30000], [50], 4, 2, 64, 16),
+])
+def test_attention_of_long_contexts(lens, new, hq, h, d, bs):
+    s = Step(97, lens, new, hq, h, d, bs, tail=0x7F)
+    s.check(s.run())
+    sel = random_columns(s, 100, s.rng)
+    s.check(s.run(selected=sel), selected=sel)
+
+
+def test_steps_of_a_long_context():
+    """Means of a whole prompt of tens of thousands of tokens, then selection and sparse attention by them."""
+    s = Step(98, [45000, 20010], [2, 1], 8, 2, 64, 32, tail=0x7F)
+    gm, gs = torch.zeros(s.nb, 2, 64, dtype=torch.int8, device="cuda"), torch.zeros(s.nb, 2, device="cuda")
+    w8.fp8_kv_block_means(dev(s.kc).view(E4M3), dev(s.lens), dev(s.table), gm, gs, query_start=dev(np.int32([0, 45000, 65010])),
+                          max_query_len=45000)
+    zero = np.zeros((s.nb, 2, 64), np.int8), np.zeros((s.nb, 2), np.float32)
+    wm, ws = fp.block_means(s.kc, s.lens, s.table, np.int32([0, 45000, 65010]), 45000, *zero)
+    assert np.array_equal(gm.cpu().numpy(), wm) and np.array_equal(gs.cpu().numpy(), ws)
+    before = np.full((3, 2, 64), -9, np.int32)
+    want = fp.select(s.q.float().numpy(), wm, ws, s.lens, s.table, 32, s.start, 2, 1, 2, 64, before)
+    got = selection_of(s, wm, ws, 64, 1, 2)
+    assert np.array_equal(got, want)
+    s.check(s.run(selected=got), selected=got)
