@@ -619,10 +619,32 @@ W8A8_API w8a8_status w8a8_fp8_kv_rotate_write(
  *               share memory with q (slices of one buffer that lie beside each
  *               other with the same strides do not).
  *   max_query_len  the largest number of new tokens of a request, or more.
+ *               It chooses the kernels.  With R = max_query_len (tokens, if that
+ *               is less) * num_q_heads / num_kv_heads up to 32, all requests run
+ *               in the kernel for few rows, in its form for 8, 16 or 32.  Above,
+ *               requests of at most 8 rows (16, 32 where a token alone has more)
+ *               run there and the others in the kernel for chunks, 128 rows at
+ *               a time.  A limit above the need costs time: 64 single tokens of
+ *               4 heads each over contexts to 8192 take 121 us with 1, 237 with
+ *               8, 121 with 64; 32 requests of up to 5 drafts over contexts to
+ *               4096 take 90 us with 5 to 8, 129 with 64.
  *   workspace   w8a8_fp8_kv_paged_attention_workspace_size() bytes, 16-byte
  *               aligned, zero-filled before its first use; every call leaves
  *               its counters zero again.  Calls that may overlap on the GPU
  *               need workspaces of their own.
+ * Scores, softmax statistics and sums are fp32.  A softmax weight enters the second
+ * product rounded to f16's 11 bits, the sum that divides it does not, which
+ * moves an output by at most 2^-11 of its weighted mean of |V| (half a step is
+ * 2^-8 of a bf16 output, 2^-11 of an fp16 one); weights below 2^-17 of the row's
+ * largest are rounded at 2^-28 of it with few rows, those below 2^-27 at 2^-38
+ * with more.  The query is exact down to 2^-13 of its
+ * row's largest element with few rows, rounded at 2^-24 of it below, and exact down
+ * to 2^-28 with more.  w8a8_fp8_kv_decode_attention carries weights in about 22
+ * bits and the query down to 2^-31.  For single tokens with head_dim 128 and a
+ * quotient of 1, 2, 4 or 8 either call will do (32 query and 8 KV heads):
+ * it was the faster one for many short contexts (128 to 1000 tokens 47 us, this
+ * one 80; 16 to 4096 in blocks of 16: 31 and 34), this one for long ones (64
+ * to 8192 in blocks of 64: 121, the other 131; one of 30000: 22 and 31).
  * Limits: num_q_heads a multiple of num_kv_heads with a quotient of at most 64;
  * max_blocks * block_size <= 2^31 - 2^24 and its product with batch *
  * num_kv_heads < 2^33; batch * max_query_len * num_q_heads <= 2^31 - 2^24;
@@ -646,7 +668,7 @@ W8A8_API w8a8_status w8a8_fp8_kv_paged_attention(
  * new: all n, also where max_query_len, by which the launch is sized, is less.
  * For each KV head, over the tokens of the block that lie below L:
  *   mean = fl(sum of the codes' values) / count,  scale = absmax * fl(1 / 127)
- *   (1 if that is 0),  code = round(mean / scale), half to even,
+ *   (1 if that is 0; a product, where w8a8_scaled_quant's is a quotient),  code = round(mean / scale), half to even,
  * the sum exact (NaN codes count as 0), the quotients and the product correctly
  * rounded fp32.
  * The means are in units of k_scale, which has no part in their order.

@@ -840,12 +840,18 @@ def fp8_kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     [batch], lengths with the new tokens.  block_table: int32 [batch,
     max_blocks].  query_start: int32 [batch + 1], the first row of each request
     in q, which ends in front of the next one's (no rows where that is not
-    above; no row of two requests), with max_query_len the most rows of one (or more; rows past it are
-    not written); None: one row a request.  Row i of a request's n sees its
-    tokens t <= seq_len - n + i; a row that sees none gives zeros.  sm_scale
-    defaults to 1 / sqrt(head_dim).  workspace: a Workspace, or a zero-filled
-    uint8 tensor of fp8_kv_attention_workspace_size(); None: the default one of
-    the stream that the call runs on."""
+    above; no row of two requests), with max_query_len the most rows of one (or
+    more; rows past it are not written, and it chooses the kernels: a limit
+    above the need costs time); None: one row a request.  Row i of a request's n
+    sees its tokens t <= seq_len - n + i; a row that sees none gives zeros.
+    sm_scale defaults to 1 / sqrt(head_dim).  workspace: a Workspace, or a
+    zero-filled uint8 tensor of fp8_kv_attention_workspace_size(); None: the
+    default one of the stream that the call runs on.
+
+    Scores and sums are 32-bit; a softmax weight has 11 bits in the second
+    product.  fp8_kv_decode_attention (single tokens, head_dim 128) carries
+    about 22, and is the faster call for many short contexts.  include/w8a8.h
+    has the figures, and max_query_len's."""
     nb, bs, hkv, d = _fp8_caches(k_cache, v_cache)
     shape = q.shape
     if len(shape) != 3 or shape[2] != d:

@@ -13,7 +13,8 @@
 //     largest element lies in [2^7, 2^8): exact for bf16 and fp16 (4 bits a
 //     part) down to 2^-13 of that element, rounded at 2^-24 of it below;
 //   a weight is f16(2^(s - m + 6)) = a + b 2^-4 + c 2^-8 + d 2^-12, exact (11
-//     bits) for weights above 2^-18 of the largest, rounded at 2^-28 below; the
+//     bits) for weights above 2^-17 of the largest, rounded at 2^-28 below (the last
+//     part's steps are 2^-21, an f16's 2^-21 from 2^-11 on); the
 //     sum that divides is of the weights before that rounding.
 // The maximum m is raised, and O rescaled, only when a score passes it by 2^2.
 //
@@ -35,13 +36,14 @@
 // in the workspace from each of its CTAs, joined by the last to arrive, in their
 // order: results do not depend on timing.
 //
-// Measured (in a graph; cold L2 adds 5 to 10 us): 64 requests up to 8192 tokens, 8 KV
-// heads of 128, 4 query heads each: 114 us, 5.6 TB/s, 83 % of what a copy reaches (128
-// requests: 197 us, 6.1 TB/s); blocks of 16 in place of 64: 134 (four times the copies);
-// heads of 64: 101; 16 / 32 query heads: 163 / 266; one request of 2003 tokens: 18, of
+// Measured (calls in a row in a graph): 64 requests up to 8192 tokens, 8 KV
+// heads of 128, 4 query heads each: 121 us, 5.3 TB/s, 79 % of what a copy reaches (128
+// requests: 214 us, 5.6 TB/s); blocks of 16 in place of 64: 135 (four times the copies);
+// heads of 64: 101; 16 / 32 query heads: 173 / 283; one request of 2003 tokens: 16, of
 // which about 2 us each go to the launch, the first copies, the first tile, the unit's end
-// and the joining.  One MMA warp for both groups: 166 us; K and V fetched together: 166,
-// apart: 136; the query's rows loaded one after another by one warp: 5 us at the start.
+// and the joining.  On the way there: one MMA warp for both groups 166 us; K and V fetched
+// together 166, apart 136; the query's rows loaded one after another by one warp 5 us at
+// the start.
 //
 // Weights of 0 do not cancel a NaN code, so the rows of V that no row of the unit
 // sees are cleared in shared memory before the product, and NaN codes of tokens

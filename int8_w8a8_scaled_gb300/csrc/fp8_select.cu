@@ -30,9 +30,10 @@
 //
 // Means and selection are latency, a chain of lengths, block ids, means and scores; so are
 // the scores of few tokens, and those of several wait for the int8 matrix instruction
-// (44 % of its rate).  32 requests up to 32768 tokens in blocks of 64, 8 KV heads: means
-// 7 us, scores 9, selection 9 (24 in a row); 4 requests of 131071 in blocks of 32, 4
-// tokens and 8 x 8 heads: 5, 17, 13 (32 in a graph).
+// (44 % of its rate).  32 requests up to 32768 tokens in blocks of 64, 8 KV heads: 22 us
+// in a graph, of which the means take 4; 4 requests of 131071 in blocks of 32, 4 tokens
+// and 8 x 8 heads: 36 (under the profiler 6.5, 21 and 15).  Rows of a prompt chunk are not
+// divided over CTAs: 600 tokens after 30000, blocks of 64, 505 us; 2048 tokens 1703.
 #include <algorithm>
 
 #include "fp8_paged.cuh"
@@ -43,7 +44,8 @@ namespace w8a8 {
 namespace {
 
 // The scale of 8-bit codes: absmax times 1/127, both in fp32, 1 for zeros (a
-// product and not a quotient: the codes are of this scale, whatever its last bit).
+// product and not, as the quantiser's int8 scale, a quotient: a last bit apart, and the codes
+// are of this one).
 __device__ __forceinline__ float int8_scale(float top) { return top > 0.f ? __fmul_rn(top, 1.f / 127.f) : 1.f; }
 
 // ------------------------------------------------------------------ means
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(kPickThreads) fp8_pick_blocks_kernel(const Fp8
       if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & ((1u << bits) - 1u)], 1);
     }
     __syncthreads();
-    // from the top: thread tid has bins kBins - 1 - 8 tid and the 7 below
+    // from the top: a thread has kBins / kPickThreads bins, thread 0 the highest ones
     int mine = 0;
 #pragma unroll
     for (int i = 0; i < kBins / kPickThreads; ++i) mine += s_hist[kBins - 1 - (kBins / kPickThreads) * tid - i];
