@@ -660,11 +660,12 @@ __global__ void __launch_bounds__(kHeadDim) fp8kv_attn_combine_kernel(const Attn
   const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
   const int len = seq_len_of(p, b);
   const size_t oi = (static_cast<size_t>(b) * p.num_q_heads + h) * kHeadDim + d;
+  const int nch = (p.max_seq_len + p.chunk - 1) / p.chunk;
+  const size_t first = (static_cast<size_t>(b) * p.num_q_heads + h) * nch * kPartStride;
   float y = 0.f;  // an empty sequence gives zeros
   if (len > 0) {
-    const int nch = (p.max_seq_len + p.chunk - 1) / p.chunk;
     const int used = (len + p.chunk - 1) / p.chunk;
-    const float* part = p.partial + (static_cast<size_t>(b) * p.num_q_heads + h) * nch * kPartStride;
+    const float* part = p.partial + first;
     float mx = -INFINITY;
     for (int c = 0; c < used; ++c) mx = fmaxf(mx, part[c * kPartStride + kHeadDim]);
     float l = 0.f, o = 0.f;
@@ -677,20 +678,19 @@ __global__ void __launch_bounds__(kHeadDim) fp8kv_attn_combine_kernel(const Attn
       }
     }
     y = l > 0.f ? (o / l) * __ldg(p.v_scale) : 0.f;
-    // Zeros again where the partial results lay over other operators' counters, which are
-    // found in the same workspace afterwards (chunks behind the sequence's end wrote nothing).
-    constexpr size_t kRegion = kCounterRegion / sizeof(float);
-    const size_t first = static_cast<size_t>(part - p.partial);
-    if (first < kRegion) {
-      __syncthreads();  // they have been read
-      const size_t end = min(kRegion - first, static_cast<size_t>(used) * kPartStride);
-      for (size_t i = d; i < end; i += kHeadDim) p.partial[first + i] = 0.f;
-    }
   }
   if (p.out_fp16)
     static_cast<__half*>(p.out)[oi] = __float2half_rn(y);
   else
     static_cast<__nv_bfloat16*>(p.out)[oi] = __float2bfloat16_rn(y);
+  // Zeros again where the partial results lay over other operators' counters, which are
+  // found in the same workspace afterwards (chunks behind the sequence's end wrote nothing).
+  constexpr size_t kRegion = kCounterRegion / sizeof(float);
+  if (len > 0 && first < kRegion) {
+    __syncthreads();  // they have been read
+    const size_t end = min(kRegion - first, static_cast<size_t>((len + p.chunk - 1) / p.chunk) * kPartStride);
+    for (size_t i = d; i < end; i += kHeadDim) p.partial[first + i] = 0.f;
+  }
 }
 
 // Launch with programmatic stream serialisation (both attention kernels wait
