@@ -613,7 +613,7 @@ W8A8_API w8a8_status w8a8_fp8_kv_rotate_write(
  * for every query head h, KV head h / (num_q_heads / num_kv_heads), with K and
  * V the codes times k_scale and v_scale.  A row that sees no token gives zeros.
  * What a row does not see has no part in it, NaN codes included; a NaN or an
- * infinity in q[i,h,:] gives NaN in that row.
+ * infinity in q[i,h,:] gives NaN in that row, if it sees a token.
  *   q, out      [tokens, num_q_heads, head_dim] bf16 / fp16, a head's dims
  *               consecutive, token and head strides in elements; out may not
  *               share memory with q (slices of one buffer that lie beside each
@@ -668,7 +668,8 @@ W8A8_API w8a8_status w8a8_fp8_kv_paged_attention(
  * new: all n, also where max_query_len, by which the launch is sized, is less.
  * For each KV head, over the tokens of the block that lie below L:
  *   mean = fl(sum of the codes' values) / count,  scale = absmax * fl(1 / 127)
- *   (1 if that is 0; a product, where w8a8_scaled_quant's is a quotient),  code = round(mean / scale), half to even,
+ *   (1 if that is 0; a product, where w8a8_scaled_quant's is a quotient),
+ *   code = round(mean / scale), half to even,
  * the sum exact (NaN codes count as 0), the quotients and the product correctly
  * rounded fp32.
  * The means are in units of k_scale, which has no part in their order.
@@ -715,9 +716,10 @@ W8A8_API w8a8_status w8a8_fp8_kv_select_blocks(
  * max_blocks) are skipped, those past the token's own block see nothing; a
  * column named twice counts twice.
  *   workspace  w8a8_fp8_kv_sparse_attention_workspace_size() bytes, 16-byte
- *              aligned, zero-filled before its first use and left so.
+ *              aligned, zero-filled before its first use; every call leaves its
+ *              counters zero again.
  * budget * block_size < 2^24, tokens * num_q_heads <= 2^31 - 2^24; the other
- * limits as above. */
+ * limits as above, w8a8_fp8_kv_paged_attention's. */
 W8A8_API size_t w8a8_fp8_kv_sparse_attention_workspace_size(int64_t tokens, int64_t num_q_heads,
                                                             int64_t num_kv_heads, int64_t head_dim,
                                                             int64_t budget, int64_t block_size);

@@ -694,8 +694,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the last unit's NaN marks have been read (who writes this entry again comes four units on)
       if (old.tiles > 0 && tid % kSlotThreads < D) s_nan[(nth - 1) & 3][slot][tid % kSlotThreads] = kDead;
       const int lim = real ? rq.len - rq.all + my / p.share : rq.len - 1;  // the last token seen
-      // (a row that sees nothing has no scores, NaN ones neither)
-      cs = lim >= 0 ? s_cs[pair ? slot : 0][row] : 1.f;
+      // (a row of NaN scores goes by those of its finite query: what it does not see has weight
+      // 0 then, and its sum says at the end whether it saw anything)
+      cs = s_cs[pair ? slot : 0][row];
+      if (!(cs == cs)) cs = 1.f;
       const float room = fminf(kHeadroom / cs, 1e38f);
       m = kNoScore;
       l = 0.f;
@@ -830,7 +832,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++mine;
       }
 
-      // ---- its end
+      // ---- its end: NaN for such a row, if it saw a token (the next unit's scales are written
+      // behind the next barrier)
+      if (l != 0.f && !(s_cs[pair ? slot : 0][row] == s_cs[pair ? slot : 0][row])) l = __int_as_float(0x7fffffff);
       const long long unit = r0 + done - at.tile;
       old.whole = at.tile == 0 && nt == at.tiles;
       old.begun = unit / share == blockIdx.x;

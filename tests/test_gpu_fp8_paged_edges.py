@@ -119,6 +119,30 @@ def test_select_blocks_for_the_last_of_two_billion_rows():
     assert (selected[:-1] == -9).all()
 
 
+@pytest.mark.parametrize("lens,new,hq,h", [([60, 300], [6, 3], 8, 2), ([300, 260], [70, 200], 8, 2), ([26, 100], [1, 1], 48, 1), ([500], [300], 2, 1)])
+@pytest.mark.parametrize("scale", [None, "k", "sm"])
+def test_nan_scores_of_rows_that_see_no_token(lens, new, hq, h, scale):
+    """Zeros, whether the tokens lie in blocks outside the cache or behind the row; NaN where one is seen."""
+    s = Step(99, lens, new, hq, h, 64, 16, tail=0x7F)
+    s.table[0, :(lens[0] - new[0] // 2) // 16] = -1          # the first request's first rows see nothing, or none of its rows
+    if len(lens) > 1:
+        s.table[1, ::2] = s.nb
+    s.q[::3, 0, 3], s.q[1::5, hq - 1, 7] = float("nan"), float("inf")
+    if scale == "k":
+        s.kg = float("nan")
+    elif scale == "sm":
+        s.sm = float("nan")
+    out = s.run()
+    s.check(out)
+    if len(lens) > 1:                                        # all of its tokens gone
+        s.table[1] = -1
+        out = s.run()
+        s.check(out)
+        assert not out[int(s.start[1]):].any()
+    sel = random_columns(s, 9, s.rng)
+    s.check(s.run(selected=sel), selected=sel)
+
+
 # ------------------------------------------------------------------ lengths that they are for
 
 
