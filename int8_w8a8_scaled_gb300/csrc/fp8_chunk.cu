@@ -25,7 +25,7 @@
 // the end.  Two threads share a softmax row, 64 tokens each.  The loops are kept
 // short: together they have to fit the instruction cache.
 //
-// Measured: 2048 new tokens after 30000, 32 query and 8 KV heads of 128: 1031 us, 1.00
+// Measured: 2048 new tokens after 30000, 32 query and 8 KV heads of 128: 1022 us, 1.02
 // PFLOP/s, 52 % of the 1.95 that a bf16 matrix product reaches.  A turn (256 rows, 128
 // tokens) takes about 4700 cycles where the MMAs need 2050: what bounds it is the four
 // warps that make f16 tiles (1100 cycles a quarter, most of it waiting for issue slots
